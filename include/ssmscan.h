@@ -332,6 +332,138 @@ ssm_status ssm_scan_split_plan(const ssm_shapes* shapes, ssm_dtype dtype, int ha
                                int64_t time_segments, int64_t* segments,
                                size_t* workspace_bytes);
 
+/*
+ * ---- The operators around the scan -------------------------------------------
+ *
+ * A layer of a language model built on the scan normalises the residual
+ * stream, projects it, filters the channels with a short causal convolution,
+ * scans them and projects back; the model ends in a softmax cross entropy over
+ * its vocabulary.  The entries below are the steps of that path that are not
+ * plain matrix products.  They follow the conventions above (caller-owned
+ * buffers, nothing allocated, asynchronous, argument errors as a status before
+ * any launch), and their weights, statistics, losses and weight gradients of
+ * conv and norm are fp32 whatever `dtype` is.
+ */
+
+/* Sizes of the short causal convolution. */
+typedef struct {
+  int64_t batch, seqlen, dim; /* >= 1 */
+  int64_t width;              /* taps per channel: 2, 3 or 4 */
+  int64_t x_batch_stride;     /* elements from one batch row of x to the next */
+  int64_t x_step_stride;      /* elements from one step of x to the next */
+  int32_t silu;               /* 1: y = silu(pre), 0: y = pre */
+} ssm_conv_shapes;
+
+/*
+ * ssm_conv_fwd -- the causal convolution of every channel with its own taps:
+ *   pre[b,t,d] = bias[d] + sum_{k < width} weight[d,k] x[b, t - (width-1) + k, d]
+ *   y[b,t,d]   = silu(pre) or pre;   0 for t >= valid_len[b]
+ * where steps before the first are those of state0 (row width-2 is the step
+ * just before step 0), or zeros without it.
+ *   x         : device, dtype `dtype`, [batch, seqlen, dim] with the strides of
+ *               `shapes` (channels contiguous): columns of a wider projection
+ *               can be passed in place.
+ *   weight    : device fp32 [dim, width].  bias: fp32 [dim] or NULL.
+ *   valid_len : device int32 [batch] or NULL; clamped to [0, seqlen] on the
+ *               device.  Steps past it are not read.
+ *   state0    : device, dtype `dtype`, [batch, width-1, dim] or NULL.
+ *   out_y     : device, dtype `dtype`, [batch, seqlen, dim], contiguous.
+ *   out_final : device, dtype `dtype`, [batch, width-1, dim] or NULL: the last
+ *               width-1 valid steps, with which a next call (or ssm_conv_step)
+ *               continues.
+ * Running [0, k) and then [k, L) from the first call's final state gives the
+ * y of one call over [0, L), bit for bit.
+ */
+ssm_status ssm_conv_fwd(const void* x, const float* weight, const float* bias,
+                        const int32_t* valid_len, const void* state0, void* out_y,
+                        void* out_final, const ssm_conv_shapes* shapes, ssm_dtype dtype,
+                        cudaStream_t stream);
+
+/*
+ * ssm_conv_bwd -- every gradient of sum(dy * y) for ssm_conv_fwd on the same
+ * inputs (pre is formed again from x).
+ *   dy      : device, dtype `dtype`, [batch, seqlen, dim], contiguous; not read
+ *             past valid_len.
+ *   dx      : device, dtype `dtype`, [batch, seqlen, dim], contiguous; 0 past
+ *             valid_len.
+ *   dweight : device fp32 [dim, width].  dbias: fp32 [dim] or NULL.
+ *   dstate0 : device, dtype `dtype`, [batch, width-1, dim] or NULL.
+ *   workspace: device memory of at least ssm_conv_bwd_workspace_bytes() bytes,
+ *             16-byte aligned, unused by other work until `stream` passes the call.
+ * Sums are taken in a fixed order: equal inputs give equal bits.
+ */
+ssm_status ssm_conv_bwd(const void* x, const float* weight, const float* bias,
+                        const int32_t* valid_len, const void* state0, const void* dy, void* dx,
+                        float* dweight, float* dbias, void* dstate0, void* workspace,
+                        size_t workspace_bytes, const ssm_conv_shapes* shapes, ssm_dtype dtype,
+                        cudaStream_t stream);
+/* Workspace bytes of ssm_conv_bwd; 0 on invalid shapes. */
+size_t ssm_conv_bwd_workspace_bytes(const ssm_conv_shapes* shapes);
+
+/*
+ * ssm_conv_step -- one step of the convolution on a carried state, in place
+ * (token-by-token generation), with ssm_conv_fwd's arithmetic.
+ *   x     : device, dtype `dtype`, [batch, dim], rows shapes->x_batch_stride
+ *           elements apart.
+ *   state : device, dtype `dtype`, [batch, width-1, dim]; the oldest row leaves,
+ *           x becomes the newest.
+ *   out_y : device, dtype `dtype`, [batch, dim].
+ * shapes->seqlen must be 1; x_step_stride is not used.
+ */
+ssm_status ssm_conv_step(const void* x, const float* weight, const float* bias, void* state,
+                         void* out_y, const ssm_conv_shapes* shapes, ssm_dtype dtype,
+                         cudaStream_t stream);
+
+/* Sizes and types of the norm of the residual stream. */
+typedef struct {
+  int64_t rows;             /* >= 1 */
+  int64_t dim;              /* 1 .. 8192 */
+  int32_t rms;              /* 0: layer norm, 1: root-mean-square norm */
+  float eps;                /* added to the variance; finite and >= 0 */
+  ssm_dtype dtype;          /* of x, y, dy and dx */
+  ssm_dtype residual_dtype; /* of residual, r, dr and dresidual: `dtype`, or SSM_F32 */
+} ssm_norm_shapes;
+
+/*
+ * ssm_norm_fwd -- the addition to the residual stream and the norm of the sum:
+ *   r = x + residual, rounded to residual_dtype (r = x without a residual)
+ *   y = (r - mean(r)) * rstd * weight + bias,  rstd = 1 / sqrt(var(r) + eps)
+ * per row; with rms, mean(r) is taken as 0 (y = r / sqrt(mean(r^2) + eps) ...).
+ *   x, out_y  : device, [rows, dim], dtype.
+ *   residual  : device, [rows, dim], residual_dtype, or NULL (residual_dtype
+ *               must then equal dtype).
+ *   weight    : device fp32 [dim].  bias: fp32 [dim] or NULL.
+ *   out_r     : device, [rows, dim], residual_dtype; required with residual,
+ *               NULL without.  It may be `residual` itself (in place).
+ *   out_stats : device fp32 [2, rows] or NULL: the means (0 with rms), then the
+ *               rstd, for ssm_norm_bwd.
+ */
+ssm_status ssm_norm_fwd(const void* x, const void* residual, const float* weight,
+                        const float* bias, void* out_y, void* out_r, float* out_stats,
+                        const ssm_norm_shapes* shapes, cudaStream_t stream);
+
+/*
+ * ssm_norm_bwd -- every gradient of sum(dy * y) + sum(dr * r) for ssm_norm_fwd.
+ *   r         : what was normalised: out_r, or x without a residual.
+ *   stats     : the forward's out_stats.
+ *   dy        : device, [rows, dim], dtype.
+ *   dr        : device, [rows, dim], residual_dtype, or NULL: the gradient that
+ *               arrives along the residual stream.
+ *   dx        : device, [rows, dim], dtype: the gradient of x.
+ *   dresidual : device, [rows, dim], residual_dtype, or NULL: the same gradient
+ *               as the residual's (with equal types dx serves for both).
+ *   dweight   : device fp32 [dim].  dbias: fp32 [dim] or NULL.
+ *   workspace : at least ssm_norm_bwd_workspace_bytes() bytes, 16-byte aligned,
+ *               unused by other work until `stream` passes the call.
+ * Sums are taken in a fixed order: equal inputs give equal bits.
+ */
+ssm_status ssm_norm_bwd(const void* r, const float* weight, const float* stats, const void* dy,
+                        const void* dr, void* dx, void* dresidual, float* dweight, float* dbias,
+                        void* workspace, size_t workspace_bytes, const ssm_norm_shapes* shapes,
+                        cudaStream_t stream);
+/* Workspace bytes of ssm_norm_bwd; 0 on invalid shapes. */
+size_t ssm_norm_bwd_workspace_bytes(const ssm_norm_shapes* shapes);
+
 /* The tier (and its grid) that ssm_scan_fwd_ex would launch for these
  * arguments, without launching anything.  `has_*` describe which optional
  * tensors the call passes.  Writes the tier to *kernel and the launch grid

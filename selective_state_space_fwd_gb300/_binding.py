@@ -72,6 +72,20 @@ class DeltaPrep(ctypes.Structure):
                 ("clamp", ctypes.c_int32), ("lo", ctypes.c_float), ("hi", ctypes.c_float)]
 
 
+class ConvShapes(ctypes.Structure):
+    """ssm_conv_shapes."""
+    _fields_ = [("batch", ctypes.c_int64), ("seqlen", ctypes.c_int64), ("dim", ctypes.c_int64),
+                ("width", ctypes.c_int64), ("x_batch_stride", ctypes.c_int64),
+                ("x_step_stride", ctypes.c_int64), ("silu", ctypes.c_int32)]
+
+
+class NormShapes(ctypes.Structure):
+    """ssm_norm_shapes."""
+    _fields_ = [("rows", ctypes.c_int64), ("dim", ctypes.c_int64), ("rms", ctypes.c_int32),
+                ("eps", ctypes.c_float), ("dtype", ctypes.c_int32),
+                ("residual_dtype", ctypes.c_int32)]
+
+
 def _prep(dt_bias, delta_softplus, delta_clamp, dim, dev):
     """A DeltaPrep for the keyword arguments, or None when nothing is asked."""
     if dt_bias is None and not delta_softplus and delta_clamp is None:
@@ -140,6 +154,21 @@ def load() -> ctypes.CDLL:
                                         ctypes.POINTER(SZ)]
     lib.ssm_selftest_wait_timeout.restype = I32
     lib.ssm_selftest_wait_timeout.argtypes = [ctypes.c_uint32, P]
+    CP, NP = ctypes.POINTER(ConvShapes), ctypes.POINTER(NormShapes)
+    lib.ssm_conv_fwd.restype = I32
+    lib.ssm_conv_fwd.argtypes = [P] * 7 + [CP, I32, P]
+    lib.ssm_conv_bwd.restype = I32
+    lib.ssm_conv_bwd.argtypes = [P] * 11 + [SZ, CP, I32, P]
+    lib.ssm_conv_bwd_workspace_bytes.restype = SZ
+    lib.ssm_conv_bwd_workspace_bytes.argtypes = [CP]
+    lib.ssm_conv_step.restype = I32
+    lib.ssm_conv_step.argtypes = [P] * 5 + [CP, I32, P]
+    lib.ssm_norm_fwd.restype = I32
+    lib.ssm_norm_fwd.argtypes = [P] * 7 + [NP, P]
+    lib.ssm_norm_bwd.restype = I32
+    lib.ssm_norm_bwd.argtypes = [P] * 10 + [SZ, NP, P]
+    lib.ssm_norm_bwd_workspace_bytes.restype = SZ
+    lib.ssm_norm_bwd_workspace_bytes.argtypes = [NP]
     _lib = lib
     return lib
 

@@ -1,4 +1,5 @@
-"""The selective scan as a differentiable PyTorch function.
+"""The selective scan and the operators around it as differentiable PyTorch
+functions.
 
 ``selective_scan`` runs the library's forward (``scan_fwd``), keeping the
 chunk boundary states the backward replays from, and its backward
@@ -10,6 +11,7 @@ runs in the library's kernels.
 import torch
 
 from ._binding import scan_bwd, scan_fwd
+from .layers import conv_bwd, conv_fwd, norm_bwd, norm_fwd
 
 
 class _SelectiveScan(torch.autograd.Function):
@@ -40,3 +42,52 @@ def selective_scan(x, delta, A, B, C, D=None, z=None, valid_len=None, *, h0=None
     the boundary states kept for the backward: a multiple of 16 lets the
     backward take its tiled kernel."""
     return _SelectiveScan.apply(x, delta, A, B, C, D, z, valid_len, h0, int(chunk_len))
+
+
+class _CausalConv(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, bias, valid_len, state0, silu):
+        ctx.save_for_backward(x, weight, bias, valid_len, state0)
+        ctx.silu = silu
+        return conv_fwd(x, weight, bias, valid_len, state0=state0, silu=silu)
+
+    @staticmethod
+    def backward(ctx, dy):
+        x, weight, bias, valid_len, state0 = ctx.saved_tensors
+        g = conv_bwd(x, weight, bias, valid_len, dy=dy.contiguous(), state0=state0, silu=ctx.silu,
+                     want_dstate0=state0 is not None and ctx.needs_input_grad[4])
+        return g["dx"], g["dweight"], g["dbias"], None, g["dstate0"], None
+
+
+def causal_conv(x, weight, bias=None, valid_len=None, *, state0=None, silu: bool = True):
+    """y = the short causal convolution of x (as ``conv_fwd``), differentiable in
+    x, weight, bias and state0."""
+    return _CausalConv.apply(x, weight, bias, valid_len, state0, bool(silu))
+
+
+class _LayerNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, bias, residual, rms, eps):
+        y, r, stats = norm_fwd(x, weight, bias, residual=residual, rms=rms, eps=eps,
+                               want_stats=True)
+        ctx.save_for_backward(x if r is None else r, weight, stats)
+        ctx.rms, ctx.bias, ctx.x_dtype = rms, bias is not None, x.dtype
+        ctx.set_materialize_grads(False)
+        return y, r
+
+    @staticmethod
+    def backward(ctx, dy, dr):
+        r, weight, stats = ctx.saved_tensors
+        dy = torch.zeros(r.shape, dtype=ctx.x_dtype, device=r.device) if dy is None else dy
+        g = norm_bwd(r, weight, stats=stats, dy=dy.contiguous(),
+                     dr=None if dr is None else dr.contiguous(), rms=ctx.rms, want_dbias=ctx.bias)
+        return (g["dx"], g["dweight"], g["dbias"],
+                g["dresidual"] if ctx.needs_input_grad[3] else None, None, None)
+
+
+def layer_norm(x, weight, bias=None, *, residual=None, rms: bool = False, eps: float = 1e-5):
+    """The norm of x (as ``norm_fwd``), differentiable in x, weight, bias and
+    residual.  Returns y, or ``(y, r)`` with a residual, r = x + residual being
+    the stream that the next layer adds to."""
+    y, r = _LayerNorm.apply(x, weight, bias, residual, bool(rms), float(eps))
+    return y if residual is None else (y, r)

@@ -10,11 +10,16 @@
 #include <new>
 
 #include "ssmscan.h"
+#include "api_util.h"
 #include "ssd.h"
 #include "tiers.h"
 
 namespace {
 
+using ssm::aligned;
+using ssm::current_device_for;
+using ssm::elem_size;
+using ssm::mul_ok;
 using ssm::ScanParams;
 
 constexpr int64_t kBwdMaxChunk = 512;  // longest chunk the backward replays in shared memory
@@ -22,17 +27,6 @@ constexpr uint32_t kSelftestMaxPolls = 1u << 20;  // bound of ssm_selftest_wait_
 
 bool supported_dstate(int64_t n) {
   return n == 1 || n == 2 || n == 4 || n == 8 || n == 16 || n == 32 || n == 64;
-}
-
-size_t elem_size(ssm_dtype t) { return t == SSM_BF16 ? 2 : 4; }
-
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-// a * b without signed overflow, for non-negative operands; false on overflow.
-bool mul_ok(int64_t a, int64_t b, int64_t* out) {
-  if (a != 0 && b > INT64_MAX / a) return false;
-  *out = a * b;
-  return true;
 }
 
 // Shape checks shared by every entry point.  Element counts are kept below
@@ -161,25 +155,6 @@ ssm_status apply_prep(const ssm_delta_prep* prep, P* p) {
   p->delta_lo = prep->lo;
   p->delta_hi = prep->hi;
   return SSM_OK;
-}
-
-// The entry points keep per-device state (the sticky error word of the
-// bounded waits, copy streams, the address of the fixed workspace) and look it
-// up by the calling thread's current device; `stream` must belong to that
-// device, else SSM_ERR_CUDA.  The special handles (0, legacy, per-thread)
-// always do.
-ssm_status current_device_for(cudaStream_t stream, int* dev) {
-  if (cudaGetDevice(dev) != cudaSuccess) return SSM_ERR_CUDA;
-  if (stream == nullptr || stream == cudaStreamLegacy || stream == cudaStreamPerThread)
-    return SSM_OK;
-  // A stream being captured into a CUDA graph is not queried for its device
-  // (the query would invalidate the capture); the calls then only record work.
-  cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
-  if (cudaStreamIsCapturing(stream, &cap) != cudaSuccess) return SSM_ERR_CUDA;
-  if (cap != cudaStreamCaptureStatusNone) return SSM_OK;
-  int sdev = -1;
-  if (cudaStreamGetDevice(stream, &sdev) != cudaSuccess) return SSM_ERR_CUDA;
-  return sdev == *dev ? SSM_OK : SSM_ERR_CUDA;
 }
 
 // Launch the planned tier.

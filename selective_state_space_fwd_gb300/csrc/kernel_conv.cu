@@ -1,0 +1,456 @@
+// kernel_conv.cu -- the short causal convolution in front of the scan: every
+// channel is filtered along time with its own `width` (2 to 4) taps,
+//   pre[t] = bias + sum_k w[k] x[t - (width - 1) + k],   y = silu(pre) or pre,
+// the steps before the first taken from a carried state (zeros without one).
+// Steps past valid_len give y = 0 and are never read.
+//
+// Bound by HBM: each element is read and written once, for `width` fused
+// multiply-adds and one MUFU pair.  A thread holds VEC consecutive channels
+// (16 bytes) with their taps in registers and walks along time with the last
+// width - 1 rows in registers, so a row is loaded once; the loads of U rows
+// are in flight together.  A sequence is cut into chunks of tc steps for
+// parallelism; a chunk re-reads the width - 1 rows before it.
+//
+// The backward, with dpre = dy silu'(pre) (pre formed again from x) and 0 past
+// valid_len:
+//   dx[t] = sum_k w[k] dpre[t + (width - 1) - k],
+//   dw[k] = sum_{b,t} dpre[t] x[t - (width - 1) + k],   dbias = sum_{b,t} dpre[t].
+// The same walk, with the last width values of dpre in registers too and
+// width - 1 steps run past the chunk's end.  dw and dbias are summed per
+// thread, then over the threads of the CTA in a fixed order, then over the
+// CTAs by a second kernel: no atomics, so the sums do not depend on timing.
+#include "common.cuh"
+#include "layers.h"
+#include "vec.cuh"
+
+namespace ssm {
+namespace {
+
+constexpr int kConvThreads = 256;
+constexpr int kSms = 152;
+
+// Steps per chunk: long chunks re-read less; short ones are for inputs that
+// would not give every SM two CTAs.
+int chunk_steps(int64_t batch, int64_t seqlen, int64_t cvs) {
+  for (int tc = 64; tc > 8; tc /= 2)
+    if (batch * ((seqlen + tc - 1) / tc) * cvs >= int64_t(kSms) * 2 * kConvThreads) return tc;
+  return 8;
+}
+
+// Channel groups per CTA (a power of two): a warp along the channels where
+// there are enough of them.
+int lanes_log2(int64_t cvs) { return cvs >= 32 ? 5 : cvs >= 16 ? 4 : 3; }
+
+struct ConvGrid {
+  int tc, lx;
+  int64_t chunks, gx, gy;
+};
+
+ConvGrid conv_grid(int64_t batch, int64_t seqlen, int64_t dim, int vec, int ctas_per_sm) {
+  ConvGrid g;
+  const int64_t cvs = (dim + vec - 1) / vec;
+  g.tc = chunk_steps(batch, seqlen, cvs);
+  g.lx = lanes_log2(cvs);
+  g.chunks = (seqlen + g.tc - 1) / g.tc;
+  const int64_t ty = kConvThreads >> g.lx;
+  g.gx = (cvs + (int64_t(1) << g.lx) - 1) >> g.lx;
+  const int64_t need = (batch * g.chunks + ty - 1) / ty;
+  const int64_t most = (int64_t(kSms) * ctas_per_sm + g.gx - 1) / g.gx;
+  g.gy = need < most ? need : most;
+  return g;
+}
+
+__device__ __forceinline__ int64_t conv_valid(const ConvParams& p, int64_t b) {
+  if (p.valid_len == nullptr) return p.seqlen;
+  const int64_t v = p.valid_len[b];
+  return v < 0 ? 0 : (v > p.seqlen ? p.seqlen : v);
+}
+
+// The row `back` steps before step 0: row width - 1 - back of the state.
+template <typename T, int K, int VEC>
+__device__ __forceinline__ Raw<T, VEC> state_row(const void* state0, int64_t b, int64_t dim,
+                                                 int64_t d0, int row) {
+  Raw<T, VEC> r;
+  if (state0 == nullptr) {
+    raw_zero<T, VEC>(r);
+    return r;
+  }
+  return raw_load<T, VEC>(static_cast<const T*>(state0) + (b * (K - 1) + row) * dim + d0);
+}
+
+template <int K, int VEC>
+__device__ __forceinline__ void load_taps(const float* weight, const float* bias, int64_t d0,
+                                          float (&w)[VEC][K], float (&bv)[VEC]) {
+  if constexpr (VEC > 1) {  // VEC * K consecutive floats, 16-byte aligned (the caller's check)
+    float t[VEC * K];
+#pragma unroll
+    for (int i = 0; i < VEC * K / 4; ++i) {
+      const float4 v = __ldg(reinterpret_cast<const float4*>(weight + d0 * K) + i);
+      t[4 * i] = v.x; t[4 * i + 1] = v.y; t[4 * i + 2] = v.z; t[4 * i + 3] = v.w;
+    }
+#pragma unroll
+    for (int v = 0; v < VEC; ++v)
+#pragma unroll
+      for (int k = 0; k < K; ++k) w[v][k] = t[v * K + k];
+  } else {
+#pragma unroll
+    for (int k = 0; k < K; ++k) w[0][k] = __ldg(weight + d0 * K + k);
+  }
+#pragma unroll
+  for (int v = 0; v < VEC; ++v) bv[v] = bias ? __ldg(bias + d0 + v) : 0.f;
+}
+
+// pre of the row `cur` after the window `win` (oldest row first).
+template <int K, int VEC>
+__device__ __forceinline__ void taps(const float (&w)[VEC][K], const float (&bv)[VEC],
+                                     const float (&win)[K - 1][VEC], const float (&cur)[VEC],
+                                     float (&pre)[VEC]) {
+#pragma unroll
+  for (int v = 0; v < VEC; ++v) {
+    float a = bv[v];
+#pragma unroll
+    for (int k = 0; k < K - 1; ++k) a = fmaf(w[v][k], win[k][v], a);
+    pre[v] = fmaf(w[v][K - 1], cur[v], a);
+  }
+}
+
+template <int K, int VEC>
+__device__ __forceinline__ void push(float (&win)[K - 1][VEC], const float (&cur)[VEC]) {
+#pragma unroll
+  for (int v = 0; v < VEC; ++v) {
+#pragma unroll
+    for (int k = 0; k + 1 < K - 1; ++k) win[k][v] = win[k + 1][v];
+    win[K - 2][v] = cur[v];
+  }
+}
+
+template <typename T, int K, int VEC, int U>
+__global__ void __launch_bounds__(kConvThreads) conv_fwd_kernel(const ConvParams p, int tc, int lx,
+                                                                int64_t chunks) {
+  const int64_t cv = (static_cast<int64_t>(blockIdx.x) << lx) + (threadIdx.x & ((1 << lx) - 1));
+  const int64_t d0 = cv * VEC;
+  if (d0 >= p.dim) return;
+  const int64_t ty = kConvThreads >> lx, items = p.batch * chunks;
+  float w[VEC][K], bv[VEC];
+  load_taps<K, VEC>(p.weight, p.bias, d0, w, bv);
+  for (int64_t it = blockIdx.y * ty + (threadIdx.x >> lx); it < items; it += gridDim.y * ty) {
+    const int64_t b = it / chunks, c = it - b * chunks;
+    const int64_t t0 = c * tc, t1 = t0 + tc < p.seqlen ? t0 + tc : p.seqlen;
+    const int64_t vl = conv_valid(p, b);
+    const int64_t te = t1 < vl ? t1 : vl;  // end of the valid steps of the chunk
+    const T* xb = static_cast<const T*>(p.x) + b * p.x_batch + d0;
+    T* yb = static_cast<T*>(p.y) + b * p.seqlen * p.dim + d0;
+    if (t0 < te) {
+      float win[K - 1][VEC];
+#pragma unroll
+      for (int k = 0; k < K - 1; ++k) {
+        const int64_t t = t0 - (K - 1) + k;
+        const Raw<T, VEC> r = t >= 0 ? raw_load<T, VEC>(xb + t * p.x_step)
+                                     : state_row<T, K, VEC>(p.state0, b, p.dim, d0,
+                                                            static_cast<int>(t) + K - 1);
+        widen<VEC>(r, win[k]);
+      }
+      for (int64_t t = t0; t < te; t += U) {
+        Raw<T, VEC> raw[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          if (t + u < te) raw[u] = raw_load<T, VEC>(xb + (t + u) * p.x_step);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          if (t + u < te) {
+            float cur[VEC], pre[VEC];
+            widen<VEC>(raw[u], cur);
+            taps<K, VEC>(w, bv, win, cur, pre);
+            if (p.silu) {
+#pragma unroll
+              for (int v = 0; v < VEC; ++v) pre[v] = silu(pre[v]);
+            }
+            store_f<T, VEC>(yb + (t + u) * p.dim, pre);
+            push<K, VEC>(win, cur);
+          }
+        }
+      }
+    }
+    Raw<T, VEC> z;
+    raw_zero<T, VEC>(z);
+    for (int64_t t = t0 < te ? te : t0; t < t1; ++t) raw_store<T, VEC>(yb + t * p.dim, z);
+    if (c == 0 && p.out_final != nullptr) {
+      T* fb = static_cast<T*>(p.out_final) + b * (K - 1) * p.dim + d0;
+      Raw<T, VEC> r[K - 1];
+#pragma unroll
+      for (int k = 0; k < K - 1; ++k) {
+        const int64_t t = vl - (K - 1) + k;
+        r[k] = t >= 0 ? raw_load<T, VEC>(xb + t * p.x_step)
+                      : state_row<T, K, VEC>(p.state0, b, p.dim, d0, static_cast<int>(t) + K - 1);
+      }
+#pragma unroll
+      for (int k = 0; k < K - 1; ++k) raw_store<T, VEC>(fb + k * p.dim, r[k]);
+    }
+  }
+}
+
+template <typename T, int K, int VEC, int U>
+__global__ void __launch_bounds__(kConvThreads) conv_bwd_kernel(const ConvBwdParams q, int tc,
+                                                                int lx, int64_t chunks) {
+  const ConvParams& p = q.fwd;
+  const int tx = threadIdx.x & ((1 << lx) - 1);
+  const int64_t cv = (static_cast<int64_t>(blockIdx.x) << lx) + tx;
+  const int64_t d0 = cv * VEC;
+  const bool on = d0 < p.dim;
+  const int ty = kConvThreads >> lx;
+  const int64_t items = on ? p.batch * chunks : 0;
+  float w[VEC][K], bv[VEC], dw[K][VEC], db[VEC];
+#pragma unroll
+  for (int v = 0; v < VEC; ++v) {
+    db[v] = 0.f;
+#pragma unroll
+    for (int k = 0; k < K; ++k) dw[k][v] = 0.f;
+  }
+  if (on) load_taps<K, VEC>(p.weight, p.bias, d0, w, bv);
+  for (int64_t it = static_cast<int64_t>(blockIdx.y) * ty + (threadIdx.x >> lx); it < items;
+       it += static_cast<int64_t>(gridDim.y) * ty) {
+    const int64_t b = it / chunks, c = it - b * chunks;
+    const int64_t t0 = c * tc, t1 = t0 + tc < p.seqlen ? t0 + tc : p.seqlen;
+    const int64_t vl = conv_valid(p, b);
+    const int64_t tl = t1 + K - 1;          // dx[t1 - 1] needs dpre up to step t1 + K - 2
+    const int64_t te = tl < vl ? tl : vl;   // dpre is 0 from valid_len on
+    const T* xb = static_cast<const T*>(p.x) + b * p.x_batch + d0;
+    const T* gb = static_cast<const T*>(q.dy) + b * p.seqlen * p.dim + d0;
+    T* ob = static_cast<T*>(q.dx) + b * p.seqlen * p.dim + d0;
+    T* sb = c == 0 && q.dstate0 ? static_cast<T*>(q.dstate0) + b * (K - 1) * p.dim + d0 : nullptr;
+    float win[K - 1][VEC], dp[K - 1][VEC];
+#pragma unroll
+    for (int k = 0; k < K - 1; ++k) {
+#pragma unroll
+      for (int v = 0; v < VEC; ++v) win[k][v] = dp[k][v] = 0.f;
+      const int64_t t = t0 - (K - 1) + k;
+      if (t0 < te)
+        widen<VEC>(t >= 0 ? raw_load<T, VEC>(xb + t * p.x_step)
+                          : state_row<T, K, VEC>(p.state0, b, p.dim, d0, static_cast<int>(t) + K - 1),
+                   win[k]);
+    }
+    for (int64_t t = t0; t < tl; t += U) {
+      Raw<T, VEC> xr[U], gr[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (t + u < te) {
+          xr[u] = raw_load<T, VEC>(xb + (t + u) * p.x_step);
+          gr[u] = raw_load<T, VEC>(gb + (t + u) * p.dim);
+        }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int64_t tt = t + u;
+        if (tt < tl) {
+          float g[VEC];
+#pragma unroll
+          for (int v = 0; v < VEC; ++v) g[v] = 0.f;
+          if (tt < te) {
+            float cur[VEC];
+            widen<VEC>(xr[u], cur);
+            widen<VEC>(gr[u], g);
+            if (p.silu) {  // silu'(v) = s (1 + v (1 - s)), s = sigmoid(v)
+              float pre[VEC];
+              taps<K, VEC>(w, bv, win, cur, pre);
+#pragma unroll
+              for (int v = 0; v < VEC; ++v) {
+                const float s = __fdividef(1.f, 1.f + ex2(-pre[v] * kLog2e));
+                g[v] *= s * fmaf(pre[v], 1.f - s, 1.f);
+              }
+            }
+            if (tt < t1) {
+#pragma unroll
+              for (int v = 0; v < VEC; ++v) {
+                db[v] += g[v];
+#pragma unroll
+                for (int k = 0; k < K - 1; ++k) dw[k][v] = fmaf(g[v], win[k][v], dw[k][v]);
+                dw[K - 1][v] = fmaf(g[v], cur[v], dw[K - 1][v]);
+              }
+            }
+            push<K, VEC>(win, cur);
+          }
+          // dx of step e = tt - (K - 1): taps K - 1 .. 0 against dpre[e .. tt]
+          float o[VEC];
+#pragma unroll
+          for (int v = 0; v < VEC; ++v) {
+            float a = w[v][0] * g[v];
+#pragma unroll
+            for (int k = 1; k < K; ++k) a = fmaf(w[v][k], dp[K - 1 - k][v], a);
+            o[v] = a;
+          }
+          const int64_t e = tt - (K - 1);
+          if (e >= t0)
+            store_f<T, VEC>(ob + e * p.dim, o);
+          else if (sb != nullptr)
+            store_f<T, VEC>(sb + (e + K - 1) * p.dim, o);
+          push<K, VEC>(dp, g);
+        }
+      }
+    }
+  }
+
+  // sums over the CTA's time slots: quantity k < K is tap k, quantity K the bias
+  __shared__ float red[kConvThreads * VEC];
+  const int cx = 1 << lx, wide = cx * VEC;
+#pragma unroll
+  for (int k = 0; k <= K; ++k) {
+    __syncthreads();
+#pragma unroll
+    for (int v = 0; v < VEC; ++v)
+      red[(threadIdx.x >> lx) * wide + tx * VEC + v] = k < K ? dw[k < K ? k : 0][v] : db[v];
+    __syncthreads();
+    for (int i = threadIdx.x; i < wide; i += kConvThreads) {
+      const int64_t d = (static_cast<int64_t>(blockIdx.x) << lx) * VEC + i;
+      float a = 0.f;
+      for (int j = 0; j < ty; ++j) a += red[j * wide + i];
+      if (d < p.dim) q.partial[(static_cast<int64_t>(blockIdx.y) * (K + 1) + k) * p.dim + d] = a;
+    }
+  }
+}
+
+// dweight[d][k] and dbias[d]: the sum of the CTAs' partial sums.
+__global__ void __launch_bounds__(256) conv_bwd_sum_kernel(const float* partial, float* dweight,
+                                                           float* dbias, int64_t dim, int width,
+                                                           int64_t parts) {
+  __shared__ float red[8][33];
+  const int lane = threadIdx.x & 31, wy = threadIdx.x >> 5;
+  const int64_t d = static_cast<int64_t>(blockIdx.x) * 32 + lane;
+  const int k = blockIdx.y;
+  float a = 0.f;
+  if (d < dim)
+    for (int64_t j = wy; j < parts; j += 8) a += partial[(j * (width + 1) + k) * dim + d];
+  red[wy][lane] = a;
+  __syncthreads();
+  if (wy == 0 && d < dim) {
+    for (int j = 1; j < 8; ++j) a += red[j][lane];
+    if (k < width)
+      dweight[d * width + k] = a;
+    else if (dbias)
+      dbias[d] = a;
+  }
+}
+
+template <typename T, int K, int VEC>
+__global__ void __launch_bounds__(128) conv_step_kernel(const ConvStepParams p, int64_t cvs) {
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
+  if (i >= p.batch * cvs) return;
+  const int64_t b = i / cvs, d0 = (i - b * cvs) * VEC;
+  T* st = static_cast<T*>(p.state) + b * (K - 1) * p.dim + d0;
+  Raw<T, VEC> win[K];
+#pragma unroll
+  for (int k = 0; k < K - 1; ++k) win[k] = raw_load_rw<T, VEC>(st + k * p.dim);
+  win[K - 1] = raw_load<T, VEC>(static_cast<const T*>(p.x) + b * p.x_batch + d0);
+  float w[VEC][K], bv[VEC], f[K - 1][VEC], cur[VEC], pre[VEC];
+  load_taps<K, VEC>(p.weight, p.bias, d0, w, bv);
+#pragma unroll
+  for (int k = 0; k < K - 1; ++k) {
+    widen<VEC>(win[k], f[k]);
+    raw_store<T, VEC>(st + k * p.dim, win[k + 1]);
+  }
+  widen<VEC>(win[K - 1], cur);
+  taps<K, VEC>(w, bv, f, cur, pre);
+  if (p.silu) {
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) pre[v] = silu(pre[v]);
+  }
+  store_f<T, VEC>(static_cast<T*>(p.y) + b * p.dim + d0, pre);
+}
+
+bool fits(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+// Whether rows of `vec` elements can be moved whole: every row of every tensor
+// then starts on an access boundary.
+bool conv_vec_ok(const ConvParams& p, int vec, size_t es) {
+  const size_t a = vec * es;
+  return p.dim % vec == 0 && (p.x_batch * es) % a == 0 && (p.x_step * es) % a == 0 &&
+         fits(p.x, a) && fits(p.y, a) && fits(p.state0, a) && fits(p.out_final, a) &&
+         fits(p.weight, 16);
+}
+
+template <typename T, int K>
+cudaError_t conv_fwd_k(const ConvParams& p, cudaStream_t s) {
+  constexpr int V = 16 / sizeof(T);
+  if (conv_vec_ok(p, V, sizeof(T))) {
+    const ConvGrid g = conv_grid(p.batch, p.seqlen, p.dim, V, 8);
+    conv_fwd_kernel<T, K, V, 4><<<dim3(g.gx, g.gy), kConvThreads, 0, s>>>(p, g.tc, g.lx, g.chunks);
+  } else {
+    const ConvGrid g = conv_grid(p.batch, p.seqlen, p.dim, 1, 8);
+    conv_fwd_kernel<T, K, 1, 8><<<dim3(g.gx, g.gy), kConvThreads, 0, s>>>(p, g.tc, g.lx, g.chunks);
+  }
+  return cudaGetLastError();
+}
+
+constexpr int kBwdVec = 4;       // channels per thread of the vector form
+constexpr int kBwdCtasPerSm = 4;
+
+template <typename T, int K>
+cudaError_t conv_bwd_k(const ConvBwdParams& q, cudaStream_t s) {
+  const ConvParams& p = q.fwd;
+  const size_t a = kBwdVec * sizeof(T);
+  const bool vec = conv_vec_ok(p, kBwdVec, sizeof(T)) && fits(q.dy, a) && fits(q.dx, a) &&
+                   fits(q.dstate0, a);
+  const ConvGrid g = conv_grid(p.batch, p.seqlen, p.dim, vec ? kBwdVec : 1, kBwdCtasPerSm);
+  const dim3 grid(g.gx, g.gy);
+  if (vec)
+    conv_bwd_kernel<T, K, kBwdVec, 4><<<grid, kConvThreads, 0, s>>>(q, g.tc, g.lx, g.chunks);
+  else
+    conv_bwd_kernel<T, K, 1, 8><<<grid, kConvThreads, 0, s>>>(q, g.tc, g.lx, g.chunks);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  conv_bwd_sum_kernel<<<dim3((p.dim + 31) / 32, K + 1), 256, 0, s>>>(q.partial, q.dweight, q.dbias,
+                                                                     p.dim, K, g.gy);
+  return cudaGetLastError();
+}
+
+template <typename T, int K>
+cudaError_t conv_step_k(const ConvStepParams& p, cudaStream_t s) {
+  constexpr int V = 16 / sizeof(T);
+  constexpr int64_t threads = 128;
+  const bool vec = p.dim % V == 0 && (p.x_batch * sizeof(T)) % 16 == 0 && fits(p.x, 16) &&
+                   fits(p.y, 16) && fits(p.state, 16) && fits(p.weight, 16);
+  const int64_t cvs = vec ? p.dim / V : p.dim;
+  const int64_t blocks = (p.batch * cvs + threads - 1) / threads;
+  if (blocks > 0x7FFFFFFF) return cudaErrorInvalidValue;
+  if (vec)
+    conv_step_kernel<T, K, V><<<static_cast<unsigned>(blocks), threads, 0, s>>>(p, cvs);
+  else
+    conv_step_kernel<T, K, 1><<<static_cast<unsigned>(blocks), threads, 0, s>>>(p, cvs);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_conv_fwd(const ConvParams& p, bool bf16, cudaStream_t s) {
+  switch (p.width) {
+    case 2: return bf16 ? conv_fwd_k<__nv_bfloat16, 2>(p, s) : conv_fwd_k<float, 2>(p, s);
+    case 3: return bf16 ? conv_fwd_k<__nv_bfloat16, 3>(p, s) : conv_fwd_k<float, 3>(p, s);
+    case 4: return bf16 ? conv_fwd_k<__nv_bfloat16, 4>(p, s) : conv_fwd_k<float, 4>(p, s);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+// The most partial sums either form of the backward writes.
+int64_t conv_bwd_partials(int64_t batch, int64_t seqlen, int64_t dim) {
+  const int64_t a = conv_grid(batch, seqlen, dim, kBwdVec, kBwdCtasPerSm).gy;
+  const int64_t b = conv_grid(batch, seqlen, dim, 1, kBwdCtasPerSm).gy;
+  return a > b ? a : b;
+}
+
+cudaError_t launch_conv_bwd(const ConvBwdParams& q, bool bf16, cudaStream_t s) {
+  switch (q.fwd.width) {
+    case 2: return bf16 ? conv_bwd_k<__nv_bfloat16, 2>(q, s) : conv_bwd_k<float, 2>(q, s);
+    case 3: return bf16 ? conv_bwd_k<__nv_bfloat16, 3>(q, s) : conv_bwd_k<float, 3>(q, s);
+    case 4: return bf16 ? conv_bwd_k<__nv_bfloat16, 4>(q, s) : conv_bwd_k<float, 4>(q, s);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+cudaError_t launch_conv_step(const ConvStepParams& p, bool bf16, cudaStream_t s) {
+  switch (p.width) {
+    case 2: return bf16 ? conv_step_k<__nv_bfloat16, 2>(p, s) : conv_step_k<float, 2>(p, s);
+    case 3: return bf16 ? conv_step_k<__nv_bfloat16, 3>(p, s) : conv_step_k<float, 3>(p, s);
+    case 4: return bf16 ? conv_step_k<__nv_bfloat16, 4>(p, s) : conv_step_k<float, 4>(p, s);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+}  // namespace ssm

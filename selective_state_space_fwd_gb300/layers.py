@@ -1,0 +1,260 @@
+"""The operators around the scan: short causal convolution and norm of the
+residual stream.
+
+Argument marshalling only, like ``_binding``: dtypes, shapes, devices and
+strides are checked, outputs and workspaces are allocated when the caller
+passes none, and the library's kernels do the work.  Weights, biases,
+statistics and weight gradients are fp32; activations are fp32 or bf16.  Every
+function takes ``stream=`` (a stream or its handle) and runs on the current
+PyTorch stream without it.
+"""
+from __future__ import annotations
+
+import ctypes
+import functools
+
+import torch
+
+from ._binding import ConvShapes, DType, NormShapes, SsmError, _check, load
+
+_CODES = {torch.float32: int(DType.F32), torch.bfloat16: int(DType.BF16)}
+
+
+def _code(dtype) -> int:
+    code = _CODES.get(dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {dtype}")
+    return code
+
+
+def _dense(t, name, shape, dtype, dev):
+    """The contiguous tensor `t`, checked (the common case without the cost of
+    building messages)."""
+    if t.dtype != dtype or t.shape != shape or t.device != dev or not t.is_contiguous():
+        _check(t, name, shape, dtype, dev)
+    return t
+
+
+def _new(out, name, shape, dtype, dev):
+    return (torch.empty(shape, dtype=dtype, device=dev) if out is None
+            else _dense(out, name, shape, dtype, dev))
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _on_stream(f):
+    """The call's tensors are allocated where they are used: with ``stream=``
+    given, the whole call runs with it as PyTorch's current stream, so that no
+    output or workspace takes memory another stream may still be using."""
+    @functools.wraps(f)
+    def call(t, *args, stream=None, **kw):
+        if stream is None:
+            return f(t, *args, **kw)
+        dev = _cuda(t, "the first argument")
+        if not hasattr(stream, "cuda_stream"):
+            stream = (torch.cuda.ExternalStream(int(stream), device=dev) if int(stream)
+                      else torch.cuda.default_stream(dev))
+        if stream.device != dev:
+            raise ValueError(f"stream: on {stream.device}, expected {dev}")
+        with torch.cuda.stream(stream):
+            return f(t, *args, **kw)
+    return call
+
+
+def _call(fn, dev, *args):
+    """fn(*args, the current stream of `dev`) on `dev`, raising SsmError on a bad
+    status."""
+    handle = torch.cuda.current_stream(dev).cuda_stream
+    if torch.cuda.current_device() == dev.index:
+        st = fn(*args, handle)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, handle)
+    if st != 0:
+        raise SsmError(st, fn.__name__)
+
+
+def _cuda(t, name):
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return t.device
+
+
+def _conv_args(x, weight, bias, silu, rank):
+    """Checked (device, dtype code, sizes, ConvShapes) of a convolution whose x
+    has `rank` dimensions, the last of them contiguous."""
+    dev = _cuda(x, "x")
+    code = _code(x.dtype)
+    if x.dim() != rank:
+        raise ValueError(f"x: {x.dim()} dimensions, expected {rank}")
+    if weight.dim() != 2:
+        raise ValueError(f"weight: shape {tuple(weight.shape)}, expected [dim, width]")
+    batch, dim = x.shape[0], x.shape[-1]
+    seqlen = x.shape[1] if rank == 3 else 1
+    width = weight.shape[1]
+    stride = x.stride()
+    if stride[-1] != 1 and dim > 1:
+        raise ValueError("x: the channels must be contiguous")
+    _dense(weight, "weight", (dim, width), torch.float32, dev)
+    if bias is not None:
+        _dense(bias, "bias", (dim,), torch.float32, dev)
+    # the stride of an axis of one element is never used; the row's own length
+    # keeps it from deciding the alignment rule
+    shapes = ConvShapes(batch, seqlen, dim, width, stride[0] if batch > 1 else dim,
+                        stride[1] if rank == 3 and seqlen > 1 else dim, int(bool(silu)))
+    return dev, code, (batch, seqlen, dim, width), shapes
+
+
+@_on_stream
+def conv_fwd(x, weight, bias=None, valid_len=None, *, state0=None, silu: bool = True,
+             want_final: bool = False, out=None, out_final=None):
+    """The short causal convolution of every channel along time.
+
+    x: [batch, L, dim], fp32 or bf16, channels contiguous; rows may be strided
+    (columns of a wider projection).  weight: fp32 [dim, width], width 2 to 4,
+    the last tap on the current step; bias: fp32 [dim]; valid_len: int32
+    [batch], steps past it give 0 and are not read.  state0: like x, [batch,
+    width - 1, dim], the steps before the first (zeros when None).  With
+    ``silu`` the result is silu(pre).  Returns y [batch, L, dim], or
+    ``(y, final)`` with ``want_final``, final [batch, width - 1, dim] being the
+    last valid steps, from which a next call or ``conv_step`` continues."""
+    dev, code, (batch, L, dim, width), shapes = _conv_args(x, weight, bias, silu, 3)
+    if valid_len is not None:
+        _dense(valid_len, "valid_len", (batch,), torch.int32, dev)
+    if state0 is not None:
+        _dense(state0, "state0", (batch, width - 1, dim), x.dtype, dev)
+    y = _new(out, "out", (batch, L, dim), x.dtype, dev)
+    final = None
+    if want_final or out_final is not None:
+        final = _new(out_final, "out_final", (batch, width - 1, dim), x.dtype, dev)
+    _call(load().ssm_conv_fwd, dev, x.data_ptr(), weight.data_ptr(), _addr(bias),
+          _addr(valid_len), _addr(state0), y.data_ptr(), _addr(final), ctypes.byref(shapes), code)
+    return y if final is None else (y, final)
+
+
+@_on_stream
+def conv_bwd(x, weight, bias=None, valid_len=None, *, dy, state0=None, silu: bool = True,
+             want_dbias: bool | None = None, want_dstate0: bool = False, workspace=None) -> dict:
+    """Every gradient of sum(dy * y) for ``conv_fwd`` on the same inputs: a dict
+    of dx (like x, contiguous), dweight and dbias (fp32; dbias None without a
+    bias, or as ``want_dbias`` says) and dstate0 (when wanted).  ``workspace``,
+    a CUDA uint8 tensor, is allocated here when None."""
+    dev, code, (batch, L, dim, width), shapes = _conv_args(x, weight, bias, silu, 3)
+    if valid_len is not None:
+        _dense(valid_len, "valid_len", (batch,), torch.int32, dev)
+    if state0 is not None:
+        _dense(state0, "state0", (batch, width - 1, dim), x.dtype, dev)
+    _dense(dy, "dy", (batch, L, dim), x.dtype, dev)
+    lib = load()
+    ws = _workspace(workspace, lib.ssm_conv_bwd_workspace_bytes(ctypes.byref(shapes)), dev)
+    f32 = dict(dtype=torch.float32, device=dev)
+    g = {"dx": torch.empty((batch, L, dim), dtype=x.dtype, device=dev),
+         "dweight": torch.empty((dim, width), **f32),
+         "dbias": torch.empty((dim,), **f32) if (bias is not None if want_dbias is None
+                                                 else want_dbias) else None,
+         "dstate0": torch.empty((batch, width - 1, dim), dtype=x.dtype, device=dev)
+         if want_dstate0 else None}
+    _call(lib.ssm_conv_bwd, dev, x.data_ptr(), weight.data_ptr(), _addr(bias),
+          _addr(valid_len), _addr(state0), dy.data_ptr(), g["dx"].data_ptr(),
+          g["dweight"].data_ptr(), _addr(g["dbias"]), _addr(g["dstate0"]), ws.data_ptr(),
+          ws.numel(), ctypes.byref(shapes), code)
+    return g
+
+
+@_on_stream
+def conv_step(x, weight, bias=None, *, state, silu: bool = True, out=None):
+    """One step of the convolution on a carried state, in place (decode).
+
+    x: [batch, dim] (rows may be strided); state: like x, [batch, width - 1,
+    dim], the last steps, oldest first (``conv_fwd``'s final state): the oldest
+    leaves and x becomes the newest.  Returns y [batch, dim]."""
+    dev, code, (batch, _, dim, width), shapes = _conv_args(x, weight, bias, silu, 2)
+    _dense(state, "state", (batch, width - 1, dim), x.dtype, dev)
+    y = _new(out, "out", (batch, dim), x.dtype, dev)
+    _call(load().ssm_conv_step, dev, x.data_ptr(), weight.data_ptr(), _addr(bias),
+          state.data_ptr(), y.data_ptr(), ctypes.byref(shapes), code)
+    return y
+
+
+def _workspace(workspace, need, dev):
+    if workspace is None:
+        return torch.empty(need, dtype=torch.uint8, device=dev)
+    if workspace.device != dev or workspace.dtype != torch.uint8 or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous uint8 tensor on x's device")
+    return workspace
+
+
+def _rows(t):
+    return t.numel() // t.shape[-1] if t.dim() and t.shape[-1] else 0
+
+
+@_on_stream
+def norm_fwd(x, weight, bias=None, *, residual=None, rms: bool = False, eps: float = 1e-5,
+             want_stats: bool = False, out=None, out_r=None):
+    """The norm of the residual stream, with the addition that precedes it.
+
+    x: [..., dim], fp32 or bf16, contiguous, dim up to 8192.  With ``residual``
+    (like x, or fp32) the sum r = x + residual, stored in the residual's type,
+    is what is normalised; without it, x is.  weight, bias: fp32 [dim].
+    ``rms`` takes the mean as 0 (root-mean-square norm).  Returns
+    ``(y, r, stats)``: y like x, r the sum (None without a residual; ``out_r``
+    may be ``residual`` itself), stats fp32 [2, rows] with the means and the
+    reciprocal standard deviations (None unless ``want_stats``)."""
+    dev = _cuda(x, "x")
+    code = _code(x.dtype)
+    shape = x.shape
+    dim, rows = shape[-1] if x.dim() else 0, _rows(x)
+    _dense(x, "x", shape, x.dtype, dev)
+    _dense(weight, "weight", (dim,), torch.float32, dev)
+    if bias is not None:
+        _dense(bias, "bias", (dim,), torch.float32, dev)
+    rcode, r = code, None
+    if residual is not None:
+        rcode = _code(residual.dtype)
+        _dense(residual, "residual", shape, residual.dtype, dev)
+        r = _new(out_r, "out_r", shape, residual.dtype, dev)
+    elif out_r is not None:
+        raise ValueError("out_r needs a residual")
+    y = _new(out, "out", shape, x.dtype, dev)
+    stats = torch.empty((2, rows), dtype=torch.float32, device=dev) if want_stats else None
+    shapes = NormShapes(rows, dim, int(bool(rms)), eps, code, rcode)
+    _call(load().ssm_norm_fwd, dev, x.data_ptr(), _addr(residual), weight.data_ptr(),
+          _addr(bias), y.data_ptr(), _addr(r), _addr(stats), ctypes.byref(shapes))
+    return y, r, stats
+
+
+@_on_stream
+def norm_bwd(r, weight, *, stats, dy, dr=None, rms: bool = False, want_dbias: bool = False,
+             workspace=None) -> dict:
+    """Every gradient of sum(dy * y) + sum(dr * r) for ``norm_fwd``.
+
+    r: what was normalised (the forward's r, or x without a residual); stats:
+    the forward's; dy like y; dr like r, the gradient that arrives along the
+    residual stream (None for none).  Returns a dict: dx (dy's type), dresidual
+    (r's type; the same tensor as dx when the types are equal), dweight and
+    dbias (fp32; dbias None unless wanted)."""
+    dev = _cuda(r, "r")
+    code, rcode = _code(dy.dtype), _code(r.dtype)
+    shape = r.shape
+    dim, rows = shape[-1] if r.dim() else 0, _rows(r)
+    _dense(r, "r", shape, r.dtype, dev)
+    _dense(dy, "dy", shape, dy.dtype, dev)
+    _dense(weight, "weight", (dim,), torch.float32, dev)
+    _dense(stats, "stats", (2, rows), torch.float32, dev)
+    if dr is not None:
+        _dense(dr, "dr", shape, r.dtype, dev)
+    lib = load()
+    shapes = NormShapes(rows, dim, int(bool(rms)), 0.0, code, rcode)
+    ws = _workspace(workspace, lib.ssm_norm_bwd_workspace_bytes(ctypes.byref(shapes)), dev)
+    f32 = dict(dtype=torch.float32, device=dev)
+    dx = torch.empty(shape, dtype=dy.dtype, device=dev)
+    dres = torch.empty(shape, dtype=r.dtype, device=dev) if rcode != code else None
+    dweight = torch.empty((dim,), **f32)
+    dbias = torch.empty((dim,), **f32) if want_dbias else None
+    _call(lib.ssm_norm_bwd, dev, r.data_ptr(), weight.data_ptr(), stats.data_ptr(),
+          dy.data_ptr(), _addr(dr), dx.data_ptr(), _addr(dres), dweight.data_ptr(), _addr(dbias),
+          ws.data_ptr(), ws.numel(), ctypes.byref(shapes))
+    return {"dx": dx, "dresidual": dx if dres is None else dres, "dweight": dweight,
+            "dbias": dbias}
