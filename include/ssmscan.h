@@ -464,6 +464,56 @@ ssm_status ssm_norm_bwd(const void* r, const float* weight, const float* stats, 
 /* Workspace bytes of ssm_norm_bwd; 0 on invalid shapes. */
 size_t ssm_norm_bwd_workspace_bytes(const ssm_norm_shapes* shapes);
 
+/* Sizes of the cross entropy. */
+typedef struct {
+  int64_t tokens;       /* 1 .. 2^30 */
+  int64_t vocab;        /* 1 .. 2^30 */
+  int64_t dim;          /* >= 1, a multiple of 8 */
+  int64_t ignore_index; /* targets of this value take no part */
+} ssm_xent_shapes;
+
+/*
+ * ssm_xent_fwd -- softmax cross entropy of every token over the vocabulary,
+ * from the hidden states, without keeping the logits S = h weight^T:
+ *   lse[t] = log sum_v exp(S[t,v]),   loss[t] = lse[t] - S[t, targets[t]]
+ * Ignored tokens get loss 0 and lse 0, and their rows of h are not used.  A
+ * target outside [0, vocab) that is not ignore_index gives a loss of NaN.
+ *   h       : device bf16 [tokens, dim], 16-byte aligned.
+ *   weight  : device bf16 [vocab, dim], 16-byte aligned.
+ *   targets : device int64 [tokens].
+ *   out_loss, out_lse : device fp32 [tokens].
+ *   workspace : at least ssm_xent_workspace_bytes(shapes, 0) bytes, 256-byte
+ *             aligned, unused by other work until `stream` passes the call.
+ * Products take bf16 operands and accumulate in fp32; the softmax is fp32.
+ * dtype must be SSM_BF16 (SSM_ERR_UNSUPPORTED otherwise).  A CTA whose bounded
+ * wait gives up sets the sticky device error word (ssm_check_device_errors).
+ */
+ssm_status ssm_xent_fwd(const void* h, const void* weight, const int64_t* targets, float* out_loss,
+                        float* out_lse, void* workspace, size_t workspace_bytes,
+                        const ssm_xent_shapes* shapes, ssm_dtype dtype, cudaStream_t stream);
+
+/*
+ * ssm_xent_bwd -- the gradients of sum_t dloss[t] loss[t] for ssm_xent_fwd:
+ *   G[t,v] = dloss[t] (exp(S[t,v] - lse[t]) - [v = targets[t]]),
+ *   dh = G weight,   dweight = G^T h,
+ * formed in pieces of the vocabulary (G rounded to bf16 as an operand of the
+ * two products, which accumulate in fp32).
+ *   lse     : the forward's out_lse.   dloss : device fp32 [tokens], not read
+ *             for ignored tokens.
+ *   dh      : device bf16 [tokens, dim], 16-byte aligned; 0 for ignored tokens.
+ *   dweight : device bf16 [vocab, dim], 16-byte aligned.
+ *   workspace : at least ssm_xent_workspace_bytes(shapes, 1) bytes, as above.
+ * An out-of-range target gives NaN gradients.  Sums are taken in a fixed
+ * order: equal inputs give equal bits.
+ */
+ssm_status ssm_xent_bwd(const void* h, const void* weight, const int64_t* targets,
+                        const float* lse, const float* dloss, void* dh, void* dweight,
+                        void* workspace, size_t workspace_bytes, const ssm_xent_shapes* shapes,
+                        ssm_dtype dtype, cudaStream_t stream);
+/* Workspace bytes of ssm_xent_fwd (backward 0) or ssm_xent_bwd (backward 1); 0
+ * on invalid shapes. */
+size_t ssm_xent_workspace_bytes(const ssm_xent_shapes* shapes, int backward);
+
 /* The tier (and its grid) that ssm_scan_fwd_ex would launch for these
  * arguments, without launching anything.  `has_*` describe which optional
  * tensors the call passes.  Writes the tier to *kernel and the launch grid

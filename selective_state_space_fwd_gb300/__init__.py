@@ -11,14 +11,14 @@ from ._binding import (Kernel, SsmError, Status, check_device_errors, chunk_coun
                        scan_fwd_host_static, scan_fwd_split, selftest_wait_timeout, split_plan,
                        ssd_fwd, static_capacity,
                        status_string, version)
-from .layers import conv_bwd, conv_fwd, conv_step, norm_bwd, norm_fwd
-from .autograd import causal_conv, layer_norm, selective_scan
+from .layers import conv_bwd, conv_fwd, conv_step, norm_bwd, norm_fwd, xent_bwd, xent_fwd
+from .autograd import causal_conv, layer_norm, linear_cross_entropy, selective_scan
 
 __all__ = ["Kernel", "SsmError", "Status", "causal_conv", "check_device_errors", "chunk_count",
            "conv_bwd", "conv_fwd", "conv_step", "decode_step", "declared_functions",
-           "host_workspace_bytes", "kernel_name", "layer_norm", "load", "norm_bwd", "norm_fwd",
+           "host_workspace_bytes", "kernel_name", "layer_norm", "linear_cross_entropy", "load", "norm_bwd", "norm_fwd",
            "plan", "scan_bwd", "scan_fwd",
            "scan_fwd_host", "scan_fwd_host_static", "scan_fwd_split", "selftest_wait_timeout",
            "selective_scan", "split_plan", "ssd_fwd",
            "static_capacity",
-           "status_string", "version"]
+           "status_string", "version", "xent_bwd", "xent_fwd"]

@@ -86,6 +86,12 @@ class NormShapes(ctypes.Structure):
                 ("residual_dtype", ctypes.c_int32)]
 
 
+class XentShapes(ctypes.Structure):
+    """ssm_xent_shapes."""
+    _fields_ = [("tokens", ctypes.c_int64), ("vocab", ctypes.c_int64), ("dim", ctypes.c_int64),
+                ("ignore_index", ctypes.c_int64)]
+
+
 def _prep(dt_bias, delta_softplus, delta_clamp, dim, dev):
     """A DeltaPrep for the keyword arguments, or None when nothing is asked."""
     if dt_bias is None and not delta_softplus and delta_clamp is None:
@@ -169,6 +175,13 @@ def load() -> ctypes.CDLL:
     lib.ssm_norm_bwd.argtypes = [P] * 10 + [SZ, NP, P]
     lib.ssm_norm_bwd_workspace_bytes.restype = SZ
     lib.ssm_norm_bwd_workspace_bytes.argtypes = [NP]
+    XP = ctypes.POINTER(XentShapes)
+    lib.ssm_xent_fwd.restype = I32
+    lib.ssm_xent_fwd.argtypes = [P] * 6 + [SZ, XP, I32, P]
+    lib.ssm_xent_bwd.restype = I32
+    lib.ssm_xent_bwd.argtypes = [P] * 8 + [SZ, XP, I32, P]
+    lib.ssm_xent_workspace_bytes.restype = SZ
+    lib.ssm_xent_workspace_bytes.argtypes = [XP, I32]
     _lib = lib
     return lib
 

@@ -11,7 +11,7 @@ runs in the library's kernels.
 import torch
 
 from ._binding import scan_bwd, scan_fwd
-from .layers import conv_bwd, conv_fwd, norm_bwd, norm_fwd
+from .layers import conv_bwd, conv_fwd, norm_bwd, norm_fwd, xent_bwd, xent_fwd
 
 
 class _SelectiveScan(torch.autograd.Function):
@@ -91,3 +91,35 @@ def layer_norm(x, weight, bias=None, *, residual=None, rms: bool = False, eps: f
     the stream that the next layer adds to."""
     y, r = _LayerNorm.apply(x, weight, bias, residual, bool(rms), float(eps))
     return y if residual is None else (y, r)
+
+
+class _CrossEntropy(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, h, weight, targets, ignore_index):
+        loss, lse = xent_fwd(h, weight, targets, ignore_index=ignore_index)
+        ctx.save_for_backward(h, weight, targets, lse)
+        ctx.ignore_index = ignore_index
+        return loss
+
+    @staticmethod
+    def backward(ctx, dloss):
+        h, weight, targets, lse = ctx.saved_tensors
+        g = xent_bwd(h, weight, targets, lse=lse, dloss=dloss.contiguous(),
+                     ignore_index=ctx.ignore_index)
+        return g["dh"], g["dweight"], None, None
+
+
+def linear_cross_entropy(h, weight, targets, *, ignore_index: int = -100, reduction: str = "mean"):
+    """Softmax cross entropy over the vocabulary of the logits h weight^T, which
+    are never kept (as ``xent_fwd``), differentiable in h and weight.  h: bf16
+    [..., dim], targets: int64 [...].  ``reduction``: "mean" over the tokens that
+    are not ignored (0 when all are), "sum", or "none" for the losses like
+    targets."""
+    if reduction not in ("mean", "sum", "none"):
+        raise ValueError(f"reduction: {reduction!r}, expected 'mean', 'sum' or 'none'")
+    loss = _CrossEntropy.apply(h.reshape(-1, h.shape[-1]), weight, targets.reshape(-1),
+                               int(ignore_index))
+    if reduction == "none":
+        return loss.view(targets.shape)
+    total = loss.sum()
+    return total if reduction == "sum" else total / (targets != ignore_index).sum().clamp(min=1)

@@ -7,6 +7,7 @@
 
 #include "api_util.h"
 #include "layers.h"
+#include "ssd.h"
 #include "ssmscan.h"
 
 namespace {
@@ -66,6 +67,26 @@ ssm_status check_norm(const ssm_norm_shapes* s) {
   int64_t n;
   if (!mul_ok(s->rows, s->dim, &n) || n > kMaxElements) return SSM_ERR_SHAPE;
   return SSM_OK;
+}
+
+ssm_status check_xent(const ssm_xent_shapes* s) {
+  if (s == nullptr) return SSM_ERR_NULL;
+  if (s->tokens < 1 || s->vocab < 1 || s->dim < 1) return SSM_ERR_SHAPE;
+  const int64_t lim = int64_t(1) << 30;  // rows are addressed by 32-bit copy coordinates
+  int64_t n;
+  if (s->tokens > lim || s->vocab > lim || s->dim > lim || !mul_ok(s->tokens, s->vocab, &n) ||
+      n > kMaxElements / 16)
+    return SSM_ERR_SHAPE;
+  return s->dim % 8 == 0 ? SSM_OK : SSM_ERR_UNSUPPORTED;  // copies start on 16-byte boundaries
+}
+
+ssm::XentParams xent_params(const void* h, const void* weight, const int64_t* targets,
+                            const ssm_xent_shapes& s, void* workspace) {
+  ssm::XentParams p = {};
+  p.h = h; p.weight = weight; p.targets = targets; p.ignore_index = s.ignore_index;
+  p.shape = {s.tokens, s.vocab, s.dim};
+  p.workspace = workspace;
+  return p;
 }
 
 }  // namespace
@@ -190,6 +211,51 @@ ssm_status ssm_norm_bwd(const void* r, const float* weight, const float* stats, 
   p.rows = s.rows; p.dim = s.dim; p.rms = s.rms;
   return status_of(ssm::launch_norm_bwd(p, s.dtype == SSM_BF16, s.residual_dtype == SSM_BF16,
                                         stream));
+}
+
+size_t ssm_xent_workspace_bytes(const ssm_xent_shapes* shapes, int backward) {
+  if (check_xent(shapes) != SSM_OK) return 0;
+  return ssm::xent_workspace_bytes({shapes->tokens, shapes->vocab, shapes->dim}, backward != 0);
+}
+
+ssm_status ssm_xent_fwd(const void* h, const void* weight, const int64_t* targets, float* out_loss,
+                        float* out_lse, void* workspace, size_t workspace_bytes,
+                        const ssm_xent_shapes* shapes, ssm_dtype dtype, cudaStream_t stream) {
+  ssm_status st = check_xent(shapes);
+  if (st != SSM_OK) return st;
+  if (dtype != SSM_BF16) return SSM_ERR_UNSUPPORTED;
+  if (!h || !weight || !targets || !out_loss || !out_lse || !workspace) return SSM_ERR_NULL;
+  if (!aligned(h, 16) || !aligned(weight, 16) || !aligned(targets, 8) || !aligned(out_loss, 4) ||
+      !aligned(out_lse, 4) || !aligned(workspace, 256))
+    return SSM_ERR_ALIGN;
+  if (workspace_bytes < ssm_xent_workspace_bytes(shapes, 0)) return SSM_ERR_SHAPE;
+  int dev = 0;
+  if ((st = current_device_for(stream, &dev)) != SSM_OK) return st;
+  ssm::XentParams p = xent_params(h, weight, targets, *shapes, workspace);
+  if (!(p.err = ssm::stream::error_word())) return SSM_ERR_CUDA;
+  p.loss = out_loss; p.lse = out_lse;
+  return status_of(ssm::launch_xent_fwd(p, stream));
+}
+
+ssm_status ssm_xent_bwd(const void* h, const void* weight, const int64_t* targets,
+                        const float* lse, const float* dloss, void* dh, void* dweight,
+                        void* workspace, size_t workspace_bytes, const ssm_xent_shapes* shapes,
+                        ssm_dtype dtype, cudaStream_t stream) {
+  ssm_status st = check_xent(shapes);
+  if (st != SSM_OK) return st;
+  if (dtype != SSM_BF16) return SSM_ERR_UNSUPPORTED;
+  if (!h || !weight || !targets || !lse || !dloss || !dh || !dweight || !workspace)
+    return SSM_ERR_NULL;
+  if (!aligned(h, 16) || !aligned(weight, 16) || !aligned(targets, 8) || !aligned(lse, 4) ||
+      !aligned(dloss, 4) || !aligned(dh, 16) || !aligned(dweight, 16) || !aligned(workspace, 256))
+    return SSM_ERR_ALIGN;
+  if (workspace_bytes < ssm_xent_workspace_bytes(shapes, 1)) return SSM_ERR_SHAPE;
+  int dev = 0;
+  if ((st = current_device_for(stream, &dev)) != SSM_OK) return st;
+  ssm::XentParams p = xent_params(h, weight, targets, *shapes, workspace);
+  if (!(p.err = ssm::stream::error_word())) return SSM_ERR_CUDA;
+  p.lse_in = lse; p.dloss = dloss; p.dh = dh; p.dweight = dweight;
+  return status_of(ssm::launch_xent_bwd(p, stream));
 }
 
 }  // extern "C"

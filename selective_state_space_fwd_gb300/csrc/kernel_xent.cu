@@ -1,0 +1,734 @@
+// kernel_xent.cu -- softmax cross entropy over a large vocabulary, from the
+// hidden states and the output embedding, without keeping the logits.
+//
+// With S = h W^T (tokens x vocabulary), per token t with target c:
+//   lse[t]  = log sum_v exp(S[t,v]),   loss[t] = lse[t] - S[t,c]
+//   G[t,v]  = dloss[t] (exp(S[t,v] - lse[t]) - [v = c])
+//   dh = G W,   dW = G^T h.
+// Tokens whose target is ignored take no part: the others' rows of h are
+// gathered first, which also keeps whatever the ignored rows hold (NaN, say)
+// out of dW.
+//
+// The forward multiplies tile by tile; a tile's epilogue reduces each row to
+// the maximum and the sum of exponentials of its 256 columns (and picks the
+// target's logit out), so that only a 64th of the logits' size is written; a
+// second kernel joins the tiles of a row.  The backward forms G again in
+// pieces of the vocabulary: one launch writes a piece of G (bf16; the products
+// take bf16 operands), a second multiplies it with W into dh and with h into
+// dW, both kinds of tile in one launch.  dh is summed over the pieces in fp32.
+// 8 T V D operations with the gradients; the tensor cores bound it.
+//
+// Products: 256 x 256 tiles on pairs of CTAs (umma_pair.cuh), operands by TMA
+// in 64-wide, 128-byte swizzled boxes through a ring of kStages stages, fp32
+// accumulators in tensor memory, two of them so that the epilogue of a tile
+// runs under the products of the next.  Per CTA: warp 0 copies, warp 1 (of the
+// even CTA) issues products, warps 2 to 5 run the epilogue, a thread per row.
+// Clusters are persistent and take tiles in turn.
+#include <cuda.h>
+#include <cuda_bf16.h>
+
+#include "common.cuh"
+#include "layers.h"
+#include "ssd.h"
+#include "tma_map.h"
+#include "umma_pair.cuh"
+
+namespace ssm {
+namespace {
+
+constexpr int kSms = 152;
+constexpr int kClusters = kSms / 2;
+constexpr int kTile = 256;               // rows and columns of a tile of the pair
+constexpr int kHalfTile = 128;           // rows of A, and of B, that a CTA holds
+constexpr int kBk = 64;                  // K per stage
+constexpr int kStages = 6;
+constexpr uint32_t kOperand = kHalfTile * kBk * 2;  // 16 KB: a CTA's A or B of a stage
+constexpr uint32_t kStage = 2 * kOperand;
+constexpr uint32_t kSmem = kStages * kStage + 1024 + 256;  // ring, alignment slack, barriers
+constexpr int kThreads = 192;
+constexpr int kEpilogueWarps = 4;
+constexpr uint64_t kWaitNs = 2000000000ull;  // a wait gives up after 2 s
+constexpr unsigned kErrXentWait = 8u;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr int64_t kPieceBytes = int64_t(512) << 20;  // most bytes of one piece of G
+
+enum Mode { kLse = 0, kGrad = 1, kProducts = 2 };
+
+struct GemmArgs {
+  const int* count;       // rows kept
+  const int* target;      // [rows] column of the target, -1 for none
+  const float* lse;       // [rows], kGrad
+  const float* scale;     // [rows] dloss, kGrad
+  int64_t vocab, dim;
+  int64_t v0;             // first column of the piece
+  int vp;                 // columns of the piece
+  int kv_whole;           // kProducts: stages of a whole piece's columns
+  float2* part;           // kLse: [tiles of columns][part_pitch] maximum (log2 units), sum
+  int64_t part_pitch;
+  float* target_logit;    // kLse: [rows]
+  __nv_bfloat16* g;       // kGrad: the piece of G, [rows][g_pitch]
+  int64_t g_pitch;
+  float* dh;              // kProducts: [splits][rows, whole tiles][dim] partial sums
+  bool add;               // kProducts: add to dh (a later piece) rather than store
+  __nv_bfloat16* dw;      // kProducts: [vocab][dim]
+  unsigned* err;
+};
+
+// Operand maps: kLse and kGrad use a = h and b = W in boxes of 128 rows;
+// kProducts uses a = G (128-row boxes) and b = W (64-row boxes) for dh, at = G
+// and bt = h (64-row boxes) for dW.
+struct Maps {
+  CUtensorMap a, b, at, bt;
+};
+
+__host__ __device__ inline int ceil_div(int64_t a, int64_t b) {
+  return static_cast<int>((a + b - 1) / b);
+}
+
+// The dh tiles' reduction over the vocabulary is split into ranges where there
+// are fewer tiles than clusters.  Every piece takes the split of a whole one
+// (kv stages), so that all pieces add into the same partial sums.
+__host__ __device__ inline int dh_splits(int mt, int nt, int kv) {
+  const int tiles = mt * nt > 0 ? mt * nt : 1;
+  const int s = (kClusters + tiles - 1) / tiles;
+  return s < kv ? s : kv;
+}
+
+// One tile of work: its position, its range of K in stages and its kind.
+struct Unit {
+  int m, n, k0, k1, split;
+  bool dw;
+};
+
+template <int MODE>
+struct Work {
+  int mt, nt, vt, kv, kt, units, ndh, splits;
+  __device__ explicit Work(const GemmArgs& p) {
+    const int rows = *p.count;
+    mt = ceil_div(rows, kTile);
+    vt = ceil_div(p.vp, kTile);
+    nt = MODE == kProducts ? ceil_div(p.dim, kTile) : vt;
+    kv = ceil_div(p.vp, kBk);
+    kt = MODE == kProducts ? ceil_div(rows, kBk) : ceil_div(p.dim, kBk);
+    splits = MODE == kProducts ? dh_splits(mt, nt, p.kv_whole) : 1;
+    ndh = MODE == kProducts ? mt * nt * splits : 0;
+    units = MODE == kProducts ? ndh + vt * nt : mt * nt;
+  }
+  __device__ Unit at(int u) const {
+    Unit r;
+    if (MODE != kProducts) {
+      r.m = u % mt; r.n = u / mt; r.k0 = 0; r.k1 = kt; r.split = 0; r.dw = false;
+    } else if (u < ndh) {
+      r.n = u % nt;
+      const int q = u / nt;
+      r.m = q % mt; r.split = q / mt; r.dw = false;
+      r.k0 = static_cast<int>(static_cast<int64_t>(kv) * r.split / splits);
+      r.k1 = static_cast<int>(static_cast<int64_t>(kv) * (r.split + 1) / splits);
+    } else {
+      r.n = (u - ndh) % nt; r.m = (u - ndh) / nt; r.split = 0; r.dw = true;
+      r.k0 = 0; r.k1 = kt;
+    }
+    return r;
+  }
+};
+
+// K-major operand of 128 rows: K step j (16 elements) is 32 bytes further in
+// the 128-byte rows; 8-row groups 1024 bytes apart.  MN-major operand in two
+// boxes of 64 x 64: K step j is 16 rows further; the boxes are 8192 bytes
+// apart, 8-row groups 1024.
+__device__ __forceinline__ uint64_t desc(uint32_t tile, int j, bool mn) {
+  const uint64_t sw128 = uint64_t(2) << 61;
+  return sw128 | (mn ? umma::smem_desc(tile + j * 2048, 8192, 1024)
+                     : umma::smem_desc(tile + j * 32, 16, 1024));
+}
+
+__device__ __forceinline__ void store32(void* p, const uint32_t* r) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// The epilogue of one thread: row `row` of the tile, whose 256 columns are the
+// TMEM columns from `acc`.
+__device__ __forceinline__ void epilogue_lse(const GemmArgs& p, uint32_t acc, int64_t row, int n,
+                                             int tgt) {
+  const int c0 = n * kTile;
+  const int cols = p.vp - c0 < kTile ? p.vp - c0 : kTile;
+  const int rel = tgt - c0;  // the target's column in this tile, if it is in it
+  float m = -INFINITY, l = 0.f;
+  for (int c = 0; c < cols; c += 32) {
+    uint32_t r[32];
+    __syncwarp();
+    umma::tmem_ld32_async(acc + c, r);
+    umma::tmem_wait_ld(r);
+    float v[32];
+#pragma unroll
+    for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
+    if (c + 32 > cols) {  // columns past the vocabulary
+#pragma unroll
+      for (int j = 0; j < 32; ++j) v[j] = c + j < cols ? v[j] : -INFINITY;
+    }
+    if (static_cast<unsigned>(rel - c) < 32u) {
+      float t = 0.f;
+#pragma unroll
+      for (int j = 0; j < 32; ++j) t = c + j == rel ? v[j] : t;
+      p.target_logit[row] = t;
+    }
+    float top[4] = {v[0], v[1], v[2], v[3]};
+#pragma unroll
+    for (int j = 4; j < 32; ++j) top[j & 3] = fmaxf(top[j & 3], v[j]);
+    const float cm = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * kLog2e;
+    const float nm = fmaxf(m, cm);
+    float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int j = 0; j < 32; ++j) s[j & 3] += ex2(fmaf(v[j], kLog2e, -nm));
+    l = fmaf(l, ex2(m - nm), (s[0] + s[1]) + (s[2] + s[3]));
+    m = nm;
+  }
+  p.part[static_cast<int64_t>(n) * p.part_pitch + row] = make_float2(m, l);
+}
+
+__device__ __forceinline__ void epilogue_grad(const GemmArgs& p, uint32_t acc, int64_t row, int n,
+                                              int tgt, float lse2, float scale) {
+  const int c0 = n * kTile;
+  const int cols = p.vp - c0 < kTile ? p.vp - c0 : kTile;
+  const int64_t t64 = static_cast<int64_t>(tgt) - p.v0 - c0;
+  const int rel = t64 >= 0 && t64 < kTile ? static_cast<int>(t64) : -1;
+  __nv_bfloat16* out = p.g + row * p.g_pitch + c0;
+  for (int c = 0; c < kTile; c += 32) {
+    uint32_t r[32];
+    __syncwarp();
+    umma::tmem_ld32_async(acc + c, r);
+    umma::tmem_wait_ld(r);
+    float v[32];
+#pragma unroll
+    for (int j = 0; j < 32; ++j) v[j] = ex2(fmaf(__uint_as_float(r[j]), kLog2e, -lse2));
+    if (rel >= c && rel < c + 32) {
+#pragma unroll
+      for (int j = 0; j < 32; ++j) v[j] -= c + j == rel ? 1.f : 0.f;
+    }
+#pragma unroll
+    for (int j = 0; j < 32; ++j) v[j] *= scale;
+    if (c + 32 > cols) {  // columns past the vocabulary take no part in dh
+#pragma unroll
+      for (int j = 0; j < 32; ++j) v[j] = c + j < cols ? v[j] : 0.f;
+    }
+    uint32_t w[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) w[j] = pack2(v[2 * j], v[2 * j + 1]);
+    store32(out + c, w);
+    store32(out + c + 16, w + 8);
+  }
+}
+
+__device__ __forceinline__ void epilogue_products(const GemmArgs& p, uint32_t acc, const Unit& u,
+                                                  int row, int mt, bool empty) {
+  const int64_t c0 = static_cast<int64_t>(u.n) * kTile;
+  const int cols = p.dim - c0 < kTile ? static_cast<int>(p.dim - c0) : kTile;
+  const int64_t vrow = p.v0 + static_cast<int64_t>(u.m) * kTile + row;
+  const bool on = !u.dw || vrow < p.v0 + p.vp;
+  float* dh = p.dh + ((static_cast<int64_t>(u.split) * mt + u.m) * kTile + row) * p.dim + c0;
+  __nv_bfloat16* dw = p.dw + vrow * p.dim + c0;
+  for (int c = 0; c < cols; c += 32) {
+    uint32_t r[32];
+    __syncwarp();
+    if (!empty) {
+      umma::tmem_ld32_async(acc + c, r);
+      umma::tmem_wait_ld(r);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 32; ++j) r[j] = 0u;
+    }
+    if (!on) continue;
+#pragma unroll
+    for (int j = 0; j < 32; j += 8) {  // dim is a multiple of 8: groups of 8 are whole
+      if (c + j < cols) {
+        float v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[j + i]);
+        if (u.dw) {
+          *reinterpret_cast<uint4*>(dw + c + j) = make_uint4(pack2(v[0], v[1]), pack2(v[2], v[3]),
+                                                             pack2(v[4], v[5]), pack2(v[6], v[7]));
+        } else {
+          float* o = dh + c + j;
+          if (p.add) {
+            const float4 a = reinterpret_cast<const float4*>(o)[0];
+            const float4 b = reinterpret_cast<const float4*>(o)[1];
+            v[0] += a.x; v[1] += a.y; v[2] += a.z; v[3] += a.w;
+            v[4] += b.x; v[5] += b.y; v[6] += b.z; v[7] += b.w;
+          }
+          uint32_t w[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(v[i]);
+          store32(o, w);
+        }
+      }
+    }
+  }
+}
+
+template <int MODE>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    xent_gemm_kernel(const __grid_constant__ Maps maps, const GemmArgs p) {
+  extern __shared__ unsigned char sm_raw[];
+  const uint32_t base = (umma::smem_u32(sm_raw) + 1023u) & ~1023u;
+  const uint32_t bars = base + kStages * kStage;
+  const auto full = [&](int s) { return bars + 8 * s; };
+  const auto empty = [&](int s) { return bars + 8 * (kStages + s); };
+  const auto acc_full = [&](int b) { return bars + 8 * (2 * kStages + b); };
+  const auto acc_empty = [&](int b) { return bars + 8 * (2 * kStages + 2 + b); };
+  const uint32_t slot = bars + 8 * (2 * kStages + 4);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = pair::cluster_rank();
+  const Work<MODE> work(p);
+  const int first = blockIdx.x >> 1, step = gridDim.x >> 1;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      umma::mbar_init(full(s), 1);
+      umma::mbar_init(empty(s), 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      umma::mbar_init(acc_full(b), 1);
+      umma::mbar_init(acc_empty(b), 2 * kEpilogueWarps);
+    }
+  }
+  if (warp == 1) pair::tmem_alloc(slot, 512);
+  umma::fence_before_sync();
+  __syncthreads();
+  pair::cluster_sync();
+  umma::fence_after_sync();
+  uint32_t tm;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(tm) : "r"(slot) : "memory");
+
+  bool bad = false;
+  if (warp == 0 && lane == 0) {
+    // ---- copies: this CTA's halves of A and B, announced on the even CTA's barrier
+    int s = 0;
+    uint32_t ph = 1;
+    int used = 0;  // stages that hold a copy, at most kStages
+    for (int u = first; u < work.units && !bad; u += step) {
+      const Unit t = work.at(u);
+      const int ma = t.m * kTile + rank * kHalfTile, nb = t.n * kTile + rank * kHalfTile;
+      const int v0 = static_cast<int>(p.v0);
+      for (int k = t.k0; k < t.k1; ++k) {
+        if (!pair::mbar_wait(empty(s), ph, kWaitNs)) {
+          bad = true;
+          break;
+        }
+        const uint32_t a = base + s * kStage, b = a + kOperand;
+        const uint32_t bar = pair::map_to(full(s), 0);
+        if (rank == 0) umma::mbar_expect_tx(full(s), 2 * kStage);
+        if (MODE != kProducts) {
+          pair::tma_load_2d(a, &maps.a, k * kBk, ma, bar);
+          pair::tma_load_2d(b, &maps.b, k * kBk, v0 + nb, bar);
+        } else if (!t.dw) {
+          pair::tma_load_2d(a, &maps.a, k * kBk, ma, bar);
+          pair::tma_load_2d(b, &maps.b, nb, v0 + k * kBk, bar);
+          pair::tma_load_2d(b + kOperand / 2, &maps.b, nb + 64, v0 + k * kBk, bar);
+        } else {
+          pair::tma_load_2d(a, &maps.at, ma, k * kBk, bar);
+          pair::tma_load_2d(a + kOperand / 2, &maps.at, ma + 64, k * kBk, bar);
+          pair::tma_load_2d(b, &maps.bt, nb, k * kBk, bar);
+          pair::tma_load_2d(b + kOperand / 2, &maps.bt, nb + 64, k * kBk, bar);
+        }
+        if (used < kStages) ++used;
+        if (++s == kStages) { s = 0; ph ^= 1; }
+      }
+    }
+    // every copy has landed, and been read, once its stage is free again
+    for (int i = 0; i < used; ++i) {
+      if (--s < 0) { s = kStages - 1; ph ^= 1; }
+    }
+    for (int i = 0; i < used; ++i) {
+      if (!pair::mbar_wait(empty(s), ph ^ 1, kWaitNs)) {
+        bad = true;  // far longer than any copy takes has passed
+        break;
+      }
+      if (++s == kStages) { s = 0; ph ^= 1; }
+    }
+  } else if (warp == 1 && lane == 0 && rank == 0) {
+    // ---- products
+    int s = 0, n = 0;
+    uint32_t ph = 0;
+    for (int u = first; u < work.units && !bad; u += step, ++n) {
+      const Unit t = work.at(u);
+      const int b = n & 1;
+      const bool a_mn = t.dw, b_mn = MODE == kProducts;
+      const uint32_t id = umma::idesc_bf16(kTile, kTile, a_mn, b_mn);
+      if (!pair::mbar_wait(acc_empty(b), ((n >> 1) & 1) ^ 1, kWaitNs)) {
+        bad = true;
+        break;
+      }
+      umma::fence_after_sync();
+      for (int k = t.k0; k < t.k1; ++k) {
+        if (!pair::mbar_wait(full(s), ph, kWaitNs)) {
+          bad = true;
+          break;
+        }
+        umma::fence_after_sync();
+        const uint32_t at = base + s * kStage, bt = at + kOperand;
+#pragma unroll
+        for (int j = 0; j < kBk / 16; ++j)
+          pair::mma_bf16(tm + b * kTile, desc(at, j, a_mn), desc(bt, j, b_mn), id,
+                         k > t.k0 || j > 0);
+        pair::mma_commit(empty(s));
+        if (++s == kStages) { s = 0; ph ^= 1; }
+      }
+      if (!bad) pair::mma_commit(acc_full(b));
+    }
+  } else if (warp >= 2) {
+    // ---- epilogue: warp w reads TMEM lanes 32 (w mod 4) ..
+    const int q = warp & 3;
+    const int row = static_cast<int>(rank) * kHalfTile + q * 32 + lane;
+    int n = 0;
+    for (int u = first; u < work.units && !bad; u += step, ++n) {
+      const Unit t = work.at(u);
+      const int b = n & 1;
+      const int64_t r = static_cast<int64_t>(t.m) * kTile + row;
+      int tgt = -1;
+      float lse2 = 0.f, scale = 0.f;
+      if (MODE != kProducts) tgt = p.target[r];
+      if (MODE == kGrad) {
+        lse2 = p.lse[r] * kLog2e;
+        scale = p.scale[r];
+      }
+      if (!pair::mbar_wait(acc_full(b), (n >> 1) & 1, kWaitNs)) bad = true;
+      if (__any_sync(0xffffffffu, bad)) {
+        bad = true;
+        break;
+      }
+      umma::fence_after_sync();
+      const uint32_t acc = tm + b * kTile + (static_cast<uint32_t>(q * 32) << 16);
+      if (MODE == kLse) epilogue_lse(p, acc, r, t.n, tgt);
+      if (MODE == kGrad) epilogue_grad(p, acc, r, t.n, tgt, lse2, scale);
+      if (MODE == kProducts) epilogue_products(p, acc, t, row, work.mt, t.k1 <= t.k0);
+      umma::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) pair::mbar_arrive(pair::map_to(acc_empty(b), 0));
+    }
+  }
+  if (bad) atomicOr(p.err, kErrXentWait);
+  __syncwarp();
+  umma::fence_before_sync();
+  __syncthreads();
+  pair::cluster_sync();  // the peer's barriers and operands stay until both are done
+  umma::fence_after_sync();
+  if (warp == 1) pair::tmem_dealloc(tm, 512);
+}
+
+// ---- gathering the kept tokens --------------------------------------------------
+constexpr int kGatherTokens = 128;  // tokens per CTA
+
+struct GatherArgs {
+  const __nv_bfloat16* h;
+  const int64_t* targets;
+  int64_t ignore;
+  int64_t tokens, vocab, dim;
+  int* count;
+  int* idx;            // [rows] token of the row, -1 past the kept ones
+  int* target;         // [rows]
+  __nv_bfloat16* rows;  // [rows][dim]
+  // forward: zeroed for ignored tokens
+  float* loss;
+  float* lse_out;
+  // backward: gathered, and dh zeroed for ignored tokens
+  const float* lse;
+  const float* dloss;
+  float* lse_rows;
+  float* scale;
+  __nv_bfloat16* dh;
+};
+
+// Every CTA counts the kept tokens before its own (the targets are a few bytes
+// per token), so one launch places them all, in order.
+__global__ void __launch_bounds__(256) xent_gather_kernel(const GatherArgs p) {
+  __shared__ int before_s, total_s, warp_n[4], src[kGatherTokens], gone[kGatherTokens];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * kGatherTokens;
+  if (tid == 0) before_s = total_s = 0;
+  __syncthreads();
+  int before = 0, total = 0;
+  for (int64_t t = tid; t < p.tokens; t += 256) {
+    const int keep = __ldg(p.targets + t) != p.ignore;
+    total += keep;
+    before += t < t0 ? keep : 0;
+  }
+  for (int m = 16; m >= 1; m /= 2) {
+    before += __shfl_xor_sync(0xffffffffu, before, m);
+    total += __shfl_xor_sync(0xffffffffu, total, m);
+  }
+  if (lane == 0) {
+    atomicAdd(&before_s, before);
+    atomicAdd(&total_s, total);
+  }
+  const int64_t t = t0 + tid;
+  const bool in = tid < kGatherTokens && t < p.tokens;
+  const int64_t tg = in ? __ldg(p.targets + t) : p.ignore;
+  const bool keep = in && tg != p.ignore;
+  const unsigned votes = __ballot_sync(0xffffffffu, keep);
+  if (lane == 0 && warp < 4) warp_n[warp] = __popc(votes);
+  __syncthreads();
+  before = before_s;
+  total = total_s;
+  int rank = __popc(votes & ((1u << lane) - 1)), kept = 0;
+  for (int w = 0; w < 4; ++w) {
+    rank += w < warp ? warp_n[w] : 0;
+    kept += warp_n[w];
+  }
+  const int64_t here = p.tokens - t0 < kGatherTokens ? p.tokens - t0 : kGatherTokens;
+  const int absent = here > 0 ? static_cast<int>(here) - kept : 0;
+  if (in) {
+    if (keep) {
+      const int64_t r = before + rank;
+      src[rank] = static_cast<int>(t);
+      const bool fine = tg >= 0 && tg < p.vocab;
+      p.idx[r] = static_cast<int>(t);
+      p.target[r] = fine ? static_cast<int>(tg) : -1;
+      if (p.scale) {
+        p.lse_rows[r] = p.lse[t];
+        p.scale[r] = fine ? p.dloss[t] : NAN;
+      }
+    } else {
+      gone[tid - rank] = static_cast<int>(t);  // rank kept tokens come before it
+      if (p.loss) {
+        p.loss[t] = 0.f;
+        p.lse_out[t] = 0.f;
+      }
+    }
+  }
+  if (blockIdx.x == 0 && tid == 0) *p.count = total;
+  __syncthreads();
+  const int vec = static_cast<int>(p.dim / 8);
+  for (int64_t i = tid; i < static_cast<int64_t>(kept) * vec; i += 256) {
+    const int r = static_cast<int>(i / vec), c = static_cast<int>(i - static_cast<int64_t>(r) * vec);
+    reinterpret_cast<uint4*>(p.rows + (before + r) * p.dim)[c] =
+        __ldg(reinterpret_cast<const uint4*>(p.h + src[r] * p.dim) + c);
+  }
+  if (p.dh)
+    for (int64_t i = tid; i < static_cast<int64_t>(absent) * vec; i += 256) {
+      const int r = static_cast<int>(i / vec), c = static_cast<int>(i - static_cast<int64_t>(r) * vec);
+      reinterpret_cast<uint4*>(p.dh + gone[r] * p.dim)[c] = make_uint4(0, 0, 0, 0);
+    }
+  // rows past the kept ones, up to a whole tile
+  const int64_t end = (static_cast<int64_t>(total) + kTile - 1) / kTile * kTile;
+  const int64_t z0 = t0 > total ? t0 : total;
+  const int64_t z1 = t0 + kGatherTokens < end ? t0 + kGatherTokens : end;
+  for (int64_t r = z0 + tid; r < z1; r += 256) {
+    p.idx[r] = -1;
+    p.target[r] = -1;
+    if (p.scale) p.lse_rows[r] = p.scale[r] = 0.f;
+  }
+  for (int64_t i = tid; i < (z1 - z0) * vec; i += 256)
+    reinterpret_cast<uint4*>(p.rows + z0 * p.dim)[i] = make_uint4(0, 0, 0, 0);
+}
+
+// ---- joining the tiles of a row --------------------------------------------------
+__global__ void __launch_bounds__(256) xent_join_kernel(const int* count, const int* idx,
+                                                        const int* target, const float2* part,
+                                                        int64_t pitch, int tiles,
+                                                        const float* target_logit, float* loss,
+                                                        float* lse) {
+  __shared__ float2 red[8][32];
+  const int lane = threadIdx.x & 31, wy = threadIdx.x >> 5;
+  const int64_t r = static_cast<int64_t>(blockIdx.x) * 32 + lane;
+  const bool on = r < *count;
+  float m = -INFINITY, l = 0.f;
+  if (on)
+    for (int i = wy; i < tiles; i += 8) {
+      const float2 v = part[i * pitch + r];
+      const float nm = fmaxf(m, v.x);
+      l = l * ex2(m - nm) + v.y * ex2(v.x - nm);
+      m = nm;
+    }
+  red[wy][lane] = make_float2(m, l);
+  __syncthreads();
+  if (wy == 0 && on) {
+    for (int i = 1; i < 8; ++i) {
+      const float2 v = red[i][lane];
+      if (v.x == -INFINITY && v.y == 0.f) continue;  // no tile fell to this warp
+      const float nm = fmaxf(m, v.x);
+      l = l * ex2(m - nm) + v.y * ex2(v.x - nm);
+      m = nm;
+    }
+    const float s = kLn2 * (m + log2f(l));
+    const int t = idx[r];
+    lse[t] = s;
+    loss[t] = target[r] >= 0 ? s - target_logit[r] : NAN;
+  }
+}
+
+// dh of a token: the sum of the splits' partial sums, rounded once.
+__global__ void __launch_bounds__(256) xent_dh_kernel(const int* count, const int* idx,
+                                                      const float* part, int64_t dim, int kv_whole,
+                                                      __nv_bfloat16* dh) {
+  const int rows = *count, mt = ceil_div(rows, kTile);
+  const int splits = dh_splits(mt, ceil_div(dim, kTile), kv_whole);
+  const int vec = static_cast<int>(dim / 8);
+  const int64_t step = static_cast<int64_t>(gridDim.x) * 256, n = static_cast<int64_t>(rows) * vec;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < n; i += step) {
+    const int64_t r = i / vec, c = (i - r * vec) * 8;
+    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    for (int s = 0; s < splits; ++s) {
+      const float4* q =
+          reinterpret_cast<const float4*>(part + (static_cast<int64_t>(s) * mt * kTile + r) * dim + c);
+      const float4 a = q[0], b = q[1];
+      v[0] += a.x; v[1] += a.y; v[2] += a.z; v[3] += a.w;
+      v[4] += b.x; v[5] += b.y; v[6] += b.z; v[7] += b.w;
+    }
+    *reinterpret_cast<uint4*>(dh + idx[r] * dim + c) = make_uint4(
+        pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[4], v[5]), pack2(v[6], v[7]));
+  }
+}
+
+// ---- workspace and launches -------------------------------------------------------
+struct Layout {
+  size_t count, idx, target, target_logit, lse, scale, rows, part, g, dh, total;
+  int64_t tpad, piece, pieces;
+};
+
+Layout layout_of(const XentShape& s, bool backward) {
+  Layout l;
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    const size_t o = off;
+    off += (bytes + 255) / 256 * 256;
+    return o;
+  };
+  l.tpad = (s.tokens + kTile - 1) / kTile * kTile;
+  const int64_t vpad = (s.vocab + kTile - 1) / kTile * kTile;
+  int64_t piece = kPieceBytes / (2 * l.tpad) / kTile * kTile;
+  piece = piece < kTile ? kTile : piece;
+  // equal pieces, in whole tiles
+  l.pieces = (vpad + piece - 1) / piece;
+  l.piece = ((vpad / kTile + l.pieces - 1) / l.pieces) * kTile;
+  l.pieces = (vpad + l.piece - 1) / l.piece;
+  l.count = take(256);
+  l.idx = take(4 * l.tpad);
+  l.target = take(4 * l.tpad);
+  l.rows = take(2 * l.tpad * s.dim);
+  l.target_logit = l.part = l.lse = l.scale = l.g = l.dh = 0;
+  if (!backward) {
+    l.target_logit = take(4 * l.tpad);
+    l.part = take(sizeof(float2) * (vpad / kTile) * l.tpad);
+  } else {
+    l.lse = take(4 * l.tpad);
+    l.scale = take(4 * l.tpad);
+    l.g = take(2 * l.tpad * l.piece);
+    // splits x rows: with fewer tiles than clusters the splits fill the clusters
+    const int64_t nt = (s.dim + kTile - 1) / kTile;
+    l.dh = take(4 * (l.tpad + ((kClusters + nt - 1) / nt) * kTile) * s.dim);
+  }
+  l.total = off;
+  return l;
+}
+
+template <int MODE>
+cudaError_t gemm(const Maps& maps, const GemmArgs& a, cudaStream_t s) {
+  auto* k = xent_gemm_kernel<MODE>;
+  const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             static_cast<int>(kSmem));
+  if (e != cudaSuccess) return e;
+  k<<<2 * kClusters, kThreads, kSmem, s>>>(maps, a);
+  return cudaGetLastError();
+}
+
+GatherArgs gather_args(const XentParams& p, const Layout& l, char* ws) {
+  GatherArgs g = {};
+  g.h = static_cast<const __nv_bfloat16*>(p.h);
+  g.targets = p.targets;
+  g.ignore = p.ignore_index;
+  g.tokens = p.shape.tokens; g.vocab = p.shape.vocab; g.dim = p.shape.dim;
+  g.count = reinterpret_cast<int*>(ws + l.count);
+  g.idx = reinterpret_cast<int*>(ws + l.idx);
+  g.target = reinterpret_cast<int*>(ws + l.target);
+  g.rows = reinterpret_cast<__nv_bfloat16*>(ws + l.rows);
+  return g;
+}
+
+GemmArgs gemm_args(const XentParams& p, const Layout& l, char* ws) {
+  GemmArgs a = {};
+  a.count = reinterpret_cast<int*>(ws + l.count);
+  a.target = reinterpret_cast<int*>(ws + l.target);
+  a.vocab = p.shape.vocab; a.dim = p.shape.dim;
+  a.err = p.err;
+  return a;
+}
+
+}  // namespace
+
+size_t xent_workspace_bytes(const XentShape& s, bool backward) { return layout_of(s, backward).total; }
+
+cudaError_t launch_xent_fwd(const XentParams& p, cudaStream_t s) {
+  const XentShape& z = p.shape;
+  const Layout l = layout_of(z, false);
+  char* ws = static_cast<char*>(p.workspace);
+  GatherArgs g = gather_args(p, l, ws);
+  g.loss = p.loss;
+  g.lse_out = p.lse;
+  Maps maps = {};
+  if (!map_bf16_sw128(&maps.a, g.rows, z.dim, l.tpad, z.dim, kHalfTile) ||
+      !map_bf16_sw128(&maps.b, p.weight, z.dim, z.vocab, z.dim, kHalfTile))
+    return cudaErrorInvalidValue;
+  xent_gather_kernel<<<static_cast<unsigned>(l.tpad / kGatherTokens), 256, 0, s>>>(g);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  GemmArgs a = gemm_args(p, l, ws);
+  a.v0 = 0;
+  a.vp = static_cast<int>(z.vocab);
+  a.part = reinterpret_cast<float2*>(ws + l.part);
+  a.part_pitch = l.tpad;
+  a.target_logit = reinterpret_cast<float*>(ws + l.target_logit);
+  if ((e = gemm<kLse>(maps, a, s)) != cudaSuccess) return e;
+  xent_join_kernel<<<static_cast<unsigned>((z.tokens + 31) / 32), 256, 0, s>>>(
+      a.count, g.idx, a.target, a.part, a.part_pitch, ceil_div(z.vocab, kTile), a.target_logit,
+      p.loss, p.lse);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_xent_bwd(const XentParams& p, cudaStream_t s) {
+  const XentShape& z = p.shape;
+  const Layout l = layout_of(z, true);
+  char* ws = static_cast<char*>(p.workspace);
+  GatherArgs g = gather_args(p, l, ws);
+  g.lse = p.lse_in;
+  g.dloss = p.dloss;
+  g.lse_rows = reinterpret_cast<float*>(ws + l.lse);
+  g.scale = reinterpret_cast<float*>(ws + l.scale);
+  g.dh = static_cast<__nv_bfloat16*>(p.dh);
+  GemmArgs a = gemm_args(p, l, ws);
+  a.lse = g.lse_rows;
+  a.scale = g.scale;
+  a.g = reinterpret_cast<__nv_bfloat16*>(ws + l.g);
+  a.g_pitch = l.piece;
+  a.dh = reinterpret_cast<float*>(ws + l.dh);
+  a.kv_whole = ceil_div(l.piece, kBk);
+  a.dw = static_cast<__nv_bfloat16*>(p.dweight);
+  Maps in = {}, out = {};
+  if (!map_bf16_sw128(&in.a, g.rows, z.dim, l.tpad, z.dim, kHalfTile) ||
+      !map_bf16_sw128(&in.b, p.weight, z.dim, z.vocab, z.dim, kHalfTile) ||
+      !map_bf16_sw128(&out.a, a.g, l.piece, l.tpad, l.piece, kHalfTile) ||
+      !map_bf16_sw128(&out.b, p.weight, z.dim, z.vocab, z.dim, kBk) ||
+      !map_bf16_sw128(&out.at, a.g, l.piece, l.tpad, l.piece, kBk) ||
+      !map_bf16_sw128(&out.bt, g.rows, z.dim, l.tpad, z.dim, kBk))
+    return cudaErrorInvalidValue;
+  xent_gather_kernel<<<static_cast<unsigned>(l.tpad / kGatherTokens), 256, 0, s>>>(g);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  for (int64_t i = 0; i < l.pieces; ++i) {
+    a.v0 = i * l.piece;
+    a.vp = static_cast<int>(z.vocab - a.v0 < l.piece ? z.vocab - a.v0 : l.piece);
+    a.add = i > 0;
+    if ((e = gemm<kGrad>(in, a, s)) != cudaSuccess) return e;
+    if ((e = gemm<kProducts>(out, a, s)) != cudaSuccess) return e;
+  }
+  xent_dh_kernel<<<4 * kSms, 256, 0, s>>>(a.count, g.idx, a.dh, z.dim, a.kv_whole,
+                                          static_cast<__nv_bfloat16*>(p.dh));
+  return cudaGetLastError();
+}
+
+}  // namespace ssm

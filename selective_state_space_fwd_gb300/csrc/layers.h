@@ -83,4 +83,31 @@ cudaError_t launch_norm_fwd(const NormParams& p, bool bf16, bool residual_bf16, 
 int64_t norm_bwd_partials(int64_t rows, int64_t dim);
 cudaError_t launch_norm_bwd(const NormBwdParams& p, bool bf16, bool residual_bf16, cudaStream_t s);
 
+// ---- softmax cross entropy over the vocabulary (kernel_xent.cu) ----------------
+struct XentShape {
+  int64_t tokens, vocab, dim;
+};
+
+struct XentParams {
+  const void* h;            // [tokens, dim] bf16
+  const void* weight;       // [vocab, dim] bf16
+  const int64_t* targets;   // [tokens]
+  int64_t ignore_index;
+  XentShape shape;
+  void* workspace;
+  unsigned int* err;        // sticky error word of the bounded waits
+  // forward
+  float* loss;              // [tokens]
+  float* lse;               // [tokens]
+  // backward
+  const float* lse_in;      // [tokens]
+  const float* dloss;       // [tokens]
+  void* dh;                 // [tokens, dim] bf16
+  void* dweight;            // [vocab, dim] bf16
+};
+
+size_t xent_workspace_bytes(const XentShape& s, bool backward);
+cudaError_t launch_xent_fwd(const XentParams& p, cudaStream_t s);
+cudaError_t launch_xent_bwd(const XentParams& p, cudaStream_t s);
+
 }  // namespace ssm

@@ -1,5 +1,5 @@
-"""The operators around the scan: short causal convolution and norm of the
-residual stream.
+"""The operators around the scan: short causal convolution, norm of the residual
+stream, and softmax cross entropy over the vocabulary.
 
 Argument marshalling only, like ``_binding``: dtypes, shapes, devices and
 strides are checked, outputs and workspaces are allocated when the caller
@@ -15,7 +15,7 @@ import functools
 
 import torch
 
-from ._binding import ConvShapes, DType, NormShapes, SsmError, _check, load
+from ._binding import ConvShapes, DType, NormShapes, SsmError, XentShapes, _check, load
 
 _CODES = {torch.float32: int(DType.F32), torch.bfloat16: int(DType.BF16)}
 
@@ -258,3 +258,57 @@ def norm_bwd(r, weight, *, stats, dy, dr=None, rms: bool = False, want_dbias: bo
           ws.data_ptr(), ws.numel(), ctypes.byref(shapes))
     return {"dx": dx, "dresidual": dx if dres is None else dres, "dweight": dweight,
             "dbias": dbias}
+
+
+def _xent_args(h, weight, targets, ignore_index):
+    """Checked (device, dtype code, sizes, XentShapes) of a cross entropy."""
+    dev = _cuda(h, "h")
+    code = _code(h.dtype)
+    if h.dim() != 2:
+        raise ValueError(f"h: shape {tuple(h.shape)}, expected [tokens, dim]")
+    if weight.dim() != 2:
+        raise ValueError(f"weight: shape {tuple(weight.shape)}, expected [vocab, dim]")
+    tokens, dim = h.shape
+    vocab = weight.shape[0]
+    _dense(h, "h", (tokens, dim), h.dtype, dev)
+    _dense(weight, "weight", (vocab, dim), h.dtype, dev)
+    _dense(targets, "targets", (tokens,), torch.int64, dev)
+    return dev, code, (tokens, vocab, dim), XentShapes(tokens, vocab, dim, int(ignore_index))
+
+
+@_on_stream
+def xent_fwd(h, weight, targets, *, ignore_index: int = -100, workspace=None):
+    """Softmax cross entropy of every token over the vocabulary, from the hidden
+    states, without keeping the logits h weight^T.
+
+    h: bf16 [tokens, dim]; weight: bf16 [vocab, dim] (the output embedding), dim
+    a multiple of 8; targets: int64 [tokens].  Returns ``(loss, lse)``, fp32
+    [tokens]: the losses and the logs of the softmax's denominators, which
+    ``xent_bwd`` needs.  Tokens whose target is ``ignore_index`` get 0 in both
+    and their rows of h are not used; a target outside the vocabulary gives
+    NaN."""
+    dev, code, (tokens, _, _), shapes = _xent_args(h, weight, targets, ignore_index)
+    lib = load()
+    ws = _workspace(workspace, lib.ssm_xent_workspace_bytes(ctypes.byref(shapes), 0), dev)
+    loss = torch.empty((tokens,), dtype=torch.float32, device=dev)
+    lse = torch.empty((tokens,), dtype=torch.float32, device=dev)
+    _call(lib.ssm_xent_fwd, dev, h.data_ptr(), weight.data_ptr(), targets.data_ptr(),
+          loss.data_ptr(), lse.data_ptr(), ws.data_ptr(), ws.numel(), ctypes.byref(shapes), code)
+    return loss, lse
+
+
+@_on_stream
+def xent_bwd(h, weight, targets, *, lse, dloss, ignore_index: int = -100, workspace=None) -> dict:
+    """The gradients of sum(dloss * loss) for ``xent_fwd``: a dict of dh (like h;
+    0 for ignored tokens) and dweight (like weight).  lse: the forward's; dloss:
+    fp32 [tokens]."""
+    dev, code, (tokens, _, _), shapes = _xent_args(h, weight, targets, ignore_index)
+    _dense(lse, "lse", (tokens,), torch.float32, dev)
+    _dense(dloss, "dloss", (tokens,), torch.float32, dev)
+    lib = load()
+    ws = _workspace(workspace, lib.ssm_xent_workspace_bytes(ctypes.byref(shapes), 1), dev)
+    dh, dweight = torch.empty_like(h), torch.empty_like(weight)
+    _call(lib.ssm_xent_bwd, dev, h.data_ptr(), weight.data_ptr(), targets.data_ptr(),
+          lse.data_ptr(), dloss.data_ptr(), dh.data_ptr(), dweight.data_ptr(), ws.data_ptr(),
+          ws.numel(), ctypes.byref(shapes), code)
+    return {"dh": dh, "dweight": dweight}

@@ -9,7 +9,8 @@ from selective_state_space_fwd_gb300 import _binding as Bd
 
 FAKE = 0x10000
 EXPECTED = {"ssm_conv_fwd", "ssm_conv_bwd", "ssm_conv_step", "ssm_conv_bwd_workspace_bytes",
-            "ssm_norm_fwd", "ssm_norm_bwd", "ssm_norm_bwd_workspace_bytes"}
+            "ssm_norm_fwd", "ssm_norm_bwd", "ssm_norm_bwd_workspace_bytes",
+            "ssm_xent_fwd", "ssm_xent_bwd", "ssm_xent_workspace_bytes"}
 
 
 def test_every_operator_is_declared_and_exported(ssmlib):
@@ -102,6 +103,46 @@ def test_norm_argument_errors(ssmlib, kw, status):
     assert _norm(**kw) == status
 
 
+def _xent(fn="fwd", h=FAKE, w=FAKE, t=FAKE, loss=FAKE, lse=FAKE, dloss=FAKE, dw=FAKE, ws=FAKE,
+          nbytes=1 << 60, shapes=(4, 100, 64, -100), dtype=1, no_shapes=False):
+    lib, s = Bd.load(), Bd.XentShapes(*shapes)
+    ref = None if no_shapes else ctypes.byref(s)
+    if fn == "fwd":
+        return lib.ssm_xent_fwd(h, w, t, loss, lse, ws, nbytes, ref, dtype, None)
+    return lib.ssm_xent_bwd(h, w, t, lse, dloss, loss, dw, ws, nbytes, ref, dtype, None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(no_shapes=True), E.ERR_NULL),
+    (dict(h=None), E.ERR_NULL),
+    (dict(w=None), E.ERR_NULL),
+    (dict(t=None), E.ERR_NULL),
+    (dict(lse=None), E.ERR_NULL),
+    (dict(ws=None), E.ERR_NULL),
+    (dict(fn="bwd", dloss=None), E.ERR_NULL),
+    (dict(fn="bwd", dw=None), E.ERR_NULL),
+    (dict(shapes=(0, 100, 64, -100)), E.ERR_SHAPE),
+    (dict(shapes=(4, 0, 64, -100)), E.ERR_SHAPE),
+    (dict(shapes=(4, 100, -8, -100)), E.ERR_SHAPE),
+    (dict(shapes=(1 << 31, 100, 64, -100)), E.ERR_SHAPE),
+    (dict(shapes=(4, 1 << 31, 64, -100)), E.ERR_SHAPE),
+    (dict(shapes=(1 << 30, 1 << 30, 64, -100)), E.ERR_SHAPE),
+    (dict(shapes=(4, 100, 60, -100)), E.ERR_UNSUPPORTED),
+    (dict(dtype=0), E.ERR_UNSUPPORTED),
+    (dict(dtype=9), E.ERR_UNSUPPORTED),
+    (dict(h=FAKE + 8), E.ERR_ALIGN),
+    (dict(w=FAKE + 2), E.ERR_ALIGN),
+    (dict(t=FAKE + 4), E.ERR_ALIGN),
+    (dict(lse=FAKE + 2), E.ERR_ALIGN),
+    (dict(ws=FAKE + 128), E.ERR_ALIGN),
+    (dict(fn="bwd", dw=FAKE + 8), E.ERR_ALIGN),
+    (dict(nbytes=1000), E.ERR_SHAPE),
+    (dict(fn="bwd", nbytes=1000), E.ERR_SHAPE),
+])
+def test_xent_argument_errors(ssmlib, kw, status):
+    assert _xent(**kw) == status
+
+
 def test_workspace_sizes(ssmlib):
     lib = Bd.load()
     conv = Bd.ConvShapes(8, 4096, 1024, 4, 0, 1024, 1)
@@ -110,3 +151,9 @@ def test_workspace_sizes(ssmlib):
     assert lib.ssm_conv_bwd_workspace_bytes(None) == 0
     assert lib.ssm_norm_bwd_workspace_bytes(ctypes.byref(Bd.NormShapes(1, 64, 0, 0.0, 0, 0))) == 512
     assert lib.ssm_norm_bwd_workspace_bytes(ctypes.byref(Bd.NormShapes(0, 64, 0, 0.0, 0, 0))) == 0
+    for tokens, vocab in ((1, 1), (8192, 65536), (100000, 300000)):
+        s = Bd.XentShapes(tokens, vocab, 64, -100)
+        fwd = lib.ssm_xent_workspace_bytes(ctypes.byref(s), 0)
+        bwd = lib.ssm_xent_workspace_bytes(ctypes.byref(s), 1)
+        assert 0 < fwd < 2 ** 31 and 0 < bwd < 2 ** 31  # never the logits' size
+    assert lib.ssm_xent_workspace_bytes(None, 0) == 0
