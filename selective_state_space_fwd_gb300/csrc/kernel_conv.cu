@@ -21,6 +21,7 @@
 // CTAs by a second kernel: no atomics, so the sums do not depend on timing.
 #include "common.cuh"
 #include "layers.h"
+#include "pdl.cuh"
 #include "vec.cuh"
 
 namespace ssm {
@@ -199,6 +200,7 @@ __global__ void __launch_bounds__(kConvThreads) conv_bwd_kernel(const ConvBwdPar
   const bool on = d0 < p.dim;
   const int ty = kConvThreads >> lx;
   const int64_t items = on ? p.batch * chunks : 0;
+  release_next();
   float w[VEC][K], bv[VEC], dw[K][VEC], db[VEC];
 #pragma unroll
   for (int v = 0; v < VEC; ++v) {
@@ -307,25 +309,33 @@ __global__ void __launch_bounds__(kConvThreads) conv_bwd_kernel(const ConvBwdPar
   }
 }
 
-// dweight[d][k] and dbias[d]: the sum of the CTAs' partial sums.
-__global__ void __launch_bounds__(256) conv_bwd_sum_kernel(const float* partial, float* dweight,
-                                                           float* dbias, int64_t dim, int width,
-                                                           int64_t parts) {
-  __shared__ float red[8][33];
+// dweight[d][k] and dbias[d]: the sums of the CTAs' partial sums, 32 warps to 32
+// channels.
+__global__ void __launch_bounds__(1024) conv_bwd_sum_kernel(const float* partial, float* dweight,
+                                                            float* dbias, int64_t dim, int width,
+                                                            int parts) {
+  __shared__ float red[32][33];
   const int lane = threadIdx.x & 31, wy = threadIdx.x >> 5;
   const int64_t d = static_cast<int64_t>(blockIdx.x) * 32 + lane;
   const int k = blockIdx.y;
+  wait_previous();
   float a = 0.f;
-  if (d < dim)
-    for (int64_t j = wy; j < parts; j += 8) a += partial[(j * (width + 1) + k) * dim + d];
-  red[wy][lane] = a;
+  if (d < dim) {
+#pragma unroll 8
+    for (int j = wy; j < parts; j += 32)
+      a += partial[(static_cast<int64_t>(j) * (width + 1) + k) * dim + d];
+  }
+  red[lane][wy] = a;
   __syncthreads();
-  if (wy == 0 && d < dim) {
-    for (int j = 1; j < 8; ++j) a += red[j][lane];
+  float v = red[wy][lane];  // warp wy joins channel wy
+#pragma unroll
+  for (int m = 16; m >= 1; m /= 2) v += __shfl_xor_sync(0xffffffffu, v, m);
+  const int64_t o = static_cast<int64_t>(blockIdx.x) * 32 + wy;
+  if (lane == 0 && o < dim) {
     if (k < width)
-      dweight[d * width + k] = a;
-    else if (dbias)
-      dbias[d] = a;
+      dweight[o * width + k] = v;
+    else
+      dbias[o] = v;
   }
 }
 
@@ -396,9 +406,9 @@ cudaError_t conv_bwd_k(const ConvBwdParams& q, cudaStream_t s) {
     conv_bwd_kernel<T, K, 1, 8><<<grid, kConvThreads, 0, s>>>(q, g.tc, g.lx, g.chunks);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  conv_bwd_sum_kernel<<<dim3((p.dim + 31) / 32, K + 1), 256, 0, s>>>(q.partial, q.dweight, q.dbias,
-                                                                     p.dim, K, g.gy);
-  return cudaGetLastError();
+  return launch_after(conv_bwd_sum_kernel,
+                      dim3(static_cast<unsigned>((p.dim + 31) / 32), q.dbias ? K + 1 : K), 1024, 0, s,
+                      q.partial, q.dweight, q.dbias, p.dim, K, static_cast<int>(g.gy));
 }
 
 template <typename T, int K>

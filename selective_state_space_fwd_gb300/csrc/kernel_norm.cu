@@ -21,6 +21,7 @@
 // second kernel in a fixed order (no atomics).
 #include "common.cuh"
 #include "layers.h"
+#include "pdl.cuh"
 #include "vec.cuh"
 
 namespace ssm {
@@ -150,6 +151,7 @@ __global__ void __launch_bounds__(THREADS) norm_bwd_kernel(const NormBwdParams p
     for (int v = 0; v < VEC; ++v) w[i][v] = dw[i][v] = db[i][v] = 0.f;
     if (c < dim) load_f<float, VEC>(p.weight + c, w[i]);
   }
+  release_next();
   int buf = 0;
   const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
   for (int64_t base = static_cast<int64_t>(blockIdx.x) * groups; base < p.rows; base += step) {
@@ -247,23 +249,26 @@ __global__ void __launch_bounds__(THREADS) norm_bwd_kernel(const NormBwdParams p
   }
 }
 
-// dw and db: the sums of the CTAs' partial sums.
-__global__ void __launch_bounds__(256) norm_bwd_sum_kernel(const float* partial, float* dweight,
-                                                           float* dbias, int64_t dim,
-                                                           int64_t parts) {
-  __shared__ float red[8][33];
+// dw and db: the sums of the CTAs' partial sums, 32 warps to 32 columns.
+__global__ void __launch_bounds__(1024) norm_bwd_sum_kernel(const float* partial, float* dweight,
+                                                            float* dbias, int64_t dim, int parts) {
+  __shared__ float red[32][33];
   const int lane = threadIdx.x & 31, wy = threadIdx.x >> 5;
   const int64_t d = static_cast<int64_t>(blockIdx.x) * 32 + lane;
   const int k = blockIdx.y;
+  wait_previous();
   float a = 0.f;
-  if (d < dim)
-    for (int64_t j = wy; j < parts; j += 8) a += partial[(j * 2 + k) * dim + d];
-  red[wy][lane] = a;
-  __syncthreads();
-  if (wy == 0 && d < dim) {
-    for (int j = 1; j < 8; ++j) a += red[j][lane];
-    (k == 0 ? dweight : dbias)[d] = a;
+  if (d < dim) {
+#pragma unroll 8
+    for (int j = wy; j < parts; j += 32) a += partial[(static_cast<int64_t>(j) * 2 + k) * dim + d];
   }
+  red[lane][wy] = a;
+  __syncthreads();
+  float v = red[wy][lane];  // warp wy joins column wy
+#pragma unroll
+  for (int m = 16; m >= 1; m /= 2) v += __shfl_xor_sync(0xffffffffu, v, m);
+  const int64_t o = static_cast<int64_t>(blockIdx.x) * 32 + wy;
+  if (lane == 0 && o < dim) (k == 0 ? dweight : dbias)[o] = v;
 }
 
 bool fits(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
@@ -323,9 +328,9 @@ cudaError_t norm_bwd_v(const NormBwdParams& p, cudaStream_t s) {
   }
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  norm_bwd_sum_kernel<<<dim3(static_cast<unsigned>((p.dim + 31) / 32), p.dbias ? 2 : 1), 256, 0,
-                        s>>>(p.partial, p.dweight, p.dbias, p.dim, g);
-  return cudaGetLastError();
+  return launch_after(norm_bwd_sum_kernel,
+                      dim3(static_cast<unsigned>((p.dim + 31) / 32), p.dbias ? 2 : 1), 1024, 0, s,
+                      p.partial, p.dweight, p.dbias, p.dim, static_cast<int>(g));
 }
 
 template <typename TX, typename TR>

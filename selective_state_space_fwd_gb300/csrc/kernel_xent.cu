@@ -29,6 +29,7 @@
 
 #include "common.cuh"
 #include "layers.h"
+#include "pdl.cuh"
 #include "ssd.h"
 #include "tma_map.h"
 #include "umma_pair.cuh"
@@ -55,8 +56,10 @@ constexpr int64_t kPieceBytes = int64_t(512) << 20;  // most bytes of one piece 
 enum Mode { kLse = 0, kGrad = 1, kProducts = 2 };
 
 struct GemmArgs {
-  const int* count;       // rows kept
+  const int* count;       // rows kept; null: every token is a row
   const int* target;      // [rows] column of the target, -1 for none
+  const int64_t* targets;  // the tokens' targets, used without `count`
+  int64_t tokens;
   const float* lse;       // [rows], kGrad
   const float* scale;     // [rows] dloss, kGrad
   int64_t vocab, dim;
@@ -74,12 +77,23 @@ struct GemmArgs {
   unsigned* err;
 };
 
-// Operand maps: kLse and kGrad use a = h and b = W in boxes of 128 rows;
-// kProducts uses a = G (128-row boxes) and b = W (64-row boxes) for dh, at = G
-// and bt = h (64-row boxes) for dW.
+// Operand maps: kLse and kGrad use a = the gathered rows of h and b = W in boxes
+// of 128 rows; kProducts uses a = G (128-row boxes) and b = W (64-row boxes) for
+// dh, at = G and bt = the rows of h (64-row boxes) for dW.  h is the same as
+// the rows' map, over h itself: with no token ignored nothing is gathered.
 struct Maps {
-  CUtensorMap a, b, at, bt;
+  CUtensorMap a, b, at, bt, h;
 };
+
+__device__ __forceinline__ int rows_of(const GemmArgs& p) {
+  return p.count ? *p.count : static_cast<int>(p.tokens);
+}
+__device__ __forceinline__ int target_of(const GemmArgs& p, int64_t row) {
+  if (p.count) return p.target[row];
+  if (row >= p.tokens) return -1;
+  const int64_t t = p.targets[row];
+  return t >= 0 && t < p.vocab ? static_cast<int>(t) : -1;
+}
 
 __host__ __device__ inline int ceil_div(int64_t a, int64_t b) {
   return static_cast<int>((a + b - 1) / b);
@@ -104,7 +118,7 @@ template <int MODE>
 struct Work {
   int mt, nt, vt, kv, kt, units, ndh, splits;
   __device__ explicit Work(const GemmArgs& p) {
-    const int rows = *p.count;
+    const int rows = rows_of(p);
     mt = ceil_div(rows, kTile);
     vt = ceil_div(p.vp, kTile);
     nt = MODE == kProducts ? ceil_div(p.dim, kTile) : vt;
@@ -284,7 +298,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const uint32_t slot = bars + 8 * (2 * kStages + 4);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = pair::cluster_rank();
-  const Work<MODE> work(p);
   const int first = blockIdx.x >> 1, step = gridDim.x >> 1;
 
   if (threadIdx.x == 0) {
@@ -304,6 +317,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   umma::fence_after_sync();
   uint32_t tm;
   asm volatile("ld.shared.u32 %0, [%1];" : "=r"(tm) : "r"(slot) : "memory");
+  wait_previous();
+  release_next();
+  const Work<MODE> work(p);
 
   bool bad = false;
   if (warp == 0 && lane == 0) {
@@ -311,6 +327,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     int s = 0;
     uint32_t ph = 1;
     int used = 0;  // stages that hold a copy, at most kStages
+    const bool all = rows_of(p) == p.tokens;
+    const CUtensorMap* ma_map = MODE != kProducts && all ? &maps.h : &maps.a;
+    const CUtensorMap* bt_map = all ? &maps.h : &maps.bt;
     for (int u = first; u < work.units && !bad; u += step) {
       const Unit t = work.at(u);
       const int ma = t.m * kTile + rank * kHalfTile, nb = t.n * kTile + rank * kHalfTile;
@@ -324,7 +343,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const uint32_t bar = pair::map_to(full(s), 0);
         if (rank == 0) umma::mbar_expect_tx(full(s), 2 * kStage);
         if (MODE != kProducts) {
-          pair::tma_load_2d(a, &maps.a, k * kBk, ma, bar);
+          pair::tma_load_2d(a, ma_map, k * kBk, ma, bar);
           pair::tma_load_2d(b, &maps.b, k * kBk, v0 + nb, bar);
         } else if (!t.dw) {
           pair::tma_load_2d(a, &maps.a, k * kBk, ma, bar);
@@ -333,8 +352,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         } else {
           pair::tma_load_2d(a, &maps.at, ma, k * kBk, bar);
           pair::tma_load_2d(a + kOperand / 2, &maps.at, ma + 64, k * kBk, bar);
-          pair::tma_load_2d(b, &maps.bt, nb, k * kBk, bar);
-          pair::tma_load_2d(b + kOperand / 2, &maps.bt, nb + 64, k * kBk, bar);
+          pair::tma_load_2d(b, bt_map, nb, k * kBk, bar);
+          pair::tma_load_2d(b + kOperand / 2, bt_map, nb + 64, k * kBk, bar);
         }
         if (used < kStages) ++used;
         if (++s == kStages) { s = 0; ph ^= 1; }
@@ -392,7 +411,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const int64_t r = static_cast<int64_t>(t.m) * kTile + row;
       int tgt = -1;
       float lse2 = 0.f, scale = 0.f;
-      if (MODE != kProducts) tgt = p.target[r];
+      if (MODE != kProducts) tgt = target_of(p, r);
       if (MODE == kGrad) {
         lse2 = p.lse[r] * kLog2e;
         scale = p.scale[r];
@@ -422,7 +441,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 }
 
 // ---- gathering the kept tokens --------------------------------------------------
-constexpr int kGatherTokens = 128;  // tokens per CTA
+constexpr int kGatherThreads = 256;
+
+// Tokens per CTA: few, for the copy's sake, while there are at most four CTAs
+// per SM (each reads all the targets).
+int gather_tokens(int64_t tokens) {
+  int64_t per = 16;
+  while ((tokens + per - 1) / per > 4 * kSms) per *= 2;
+  return static_cast<int>(per);
+}
 
 struct GatherArgs {
   const __nv_bfloat16* h;
@@ -430,9 +457,10 @@ struct GatherArgs {
   int64_t ignore;
   int64_t tokens, vocab, dim;
   int* count;
-  int* idx;            // [rows] token of the row, -1 past the kept ones
+  int* idx;            // [rows] token of the row
   int* target;         // [rows]
-  __nv_bfloat16* rows;  // [rows][dim]
+  __nv_bfloat16* rows;  // [rows][dim], written only where a token is ignored
+  int per;             // tokens per CTA
   // forward: zeroed for ignored tokens
   float* loss;
   float* lse_out;
@@ -446,14 +474,16 @@ struct GatherArgs {
 
 // Every CTA counts the kept tokens before its own (the targets are a few bytes
 // per token), so one launch places them all, in order.
-__global__ void __launch_bounds__(256) xent_gather_kernel(const GatherArgs p) {
-  __shared__ int before_s, total_s, warp_n[4], src[kGatherTokens], gone[kGatherTokens];
+__global__ void __launch_bounds__(kGatherThreads) xent_gather_kernel(const GatherArgs p) {
+  constexpr int kWarps = kGatherThreads / 32;
+  __shared__ int before_n[kWarps], total_n[kWarps], warp_n[kWarps];
+  __shared__ int src[kGatherThreads], gone[kGatherThreads];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * kGatherTokens;
-  if (tid == 0) before_s = total_s = 0;
-  __syncthreads();
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * p.per;
+  release_next();
   int before = 0, total = 0;
-  for (int64_t t = tid; t < p.tokens; t += 256) {
+#pragma unroll 8
+  for (int64_t t = tid; t < p.tokens; t += kGatherThreads) {
     const int keep = __ldg(p.targets + t) != p.ignore;
     total += keep;
     before += t < t0 ? keep : 0;
@@ -463,124 +493,152 @@ __global__ void __launch_bounds__(256) xent_gather_kernel(const GatherArgs p) {
     total += __shfl_xor_sync(0xffffffffu, total, m);
   }
   if (lane == 0) {
-    atomicAdd(&before_s, before);
-    atomicAdd(&total_s, total);
+    before_n[warp] = before;
+    total_n[warp] = total;
   }
-  const int64_t t = t0 + tid;
-  const bool in = tid < kGatherTokens && t < p.tokens;
-  const int64_t tg = in ? __ldg(p.targets + t) : p.ignore;
-  const bool keep = in && tg != p.ignore;
-  const unsigned votes = __ballot_sync(0xffffffffu, keep);
-  if (lane == 0 && warp < 4) warp_n[warp] = __popc(votes);
   __syncthreads();
-  before = before_s;
-  total = total_s;
-  int rank = __popc(votes & ((1u << lane) - 1)), kept = 0;
-  for (int w = 0; w < 4; ++w) {
-    rank += w < warp ? warp_n[w] : 0;
-    kept += warp_n[w];
+  before = total = 0;
+  for (int w = 0; w < kWarps; ++w) {
+    before += before_n[w];
+    total += total_n[w];
   }
-  const int64_t here = p.tokens - t0 < kGatherTokens ? p.tokens - t0 : kGatherTokens;
-  const int absent = here > 0 ? static_cast<int>(here) - kept : 0;
-  if (in) {
+  const bool all = total == p.tokens;
+  const int vec = static_cast<int>(p.dim / 8);
+  const int64_t t1 = t0 + p.per < p.tokens ? t0 + p.per : p.tokens;
+  for (int64_t c0 = t0; c0 < t1; c0 += kGatherThreads) {
+    const int64_t t = c0 + tid;
+    const bool in = t < t1;
+    const int64_t tg = in ? __ldg(p.targets + t) : p.ignore;
+    const bool keep = in && tg != p.ignore;
+    const unsigned votes = __ballot_sync(0xffffffffu, keep);
+    __syncthreads();  // the lists of the chunk before have been read
+    if (lane == 0) warp_n[warp] = __popc(votes);
+    __syncthreads();
+    int rank = __popc(votes & ((1u << lane) - 1)), kept = 0;
+    for (int w = 0; w < kWarps; ++w) {
+      rank += w < warp ? warp_n[w] : 0;
+      kept += warp_n[w];
+    }
     if (keep) {
       const int64_t r = before + rank;
-      src[rank] = static_cast<int>(t);
       const bool fine = tg >= 0 && tg < p.vocab;
+      src[rank] = static_cast<int>(t);
       p.idx[r] = static_cast<int>(t);
       p.target[r] = fine ? static_cast<int>(tg) : -1;
       if (p.scale) {
         p.lse_rows[r] = p.lse[t];
         p.scale[r] = fine ? p.dloss[t] : NAN;
       }
-    } else {
-      gone[tid - rank] = static_cast<int>(t);  // rank kept tokens come before it
+    } else if (in) {
+      gone[tid - rank] = static_cast<int>(t);  // `rank` kept tokens come before it
       if (p.loss) {
         p.loss[t] = 0.f;
         p.lse_out[t] = 0.f;
       }
     }
+    if (!all) {
+      __syncthreads();
+      const int n = kept * vec;
+#pragma unroll 4
+      for (int i = tid; i < n; i += kGatherThreads) {
+        const int r = i / vec, c = i - r * vec;
+        reinterpret_cast<uint4*>(p.rows + (static_cast<int64_t>(before) + r) * p.dim)[c] =
+            __ldg(reinterpret_cast<const uint4*>(p.h + src[r] * p.dim) + c);
+      }
+      const int absent = p.dh ? (static_cast<int>(t1 - c0 < kGatherThreads ? t1 - c0 : kGatherThreads) - kept) * vec : 0;
+      for (int i = tid; i < absent; i += kGatherThreads) {
+        const int r = i / vec, c = i - r * vec;
+        reinterpret_cast<uint4*>(p.dh + gone[r] * p.dim)[c] = make_uint4(0, 0, 0, 0);
+      }
+    }
+    before += kept;
   }
   if (blockIdx.x == 0 && tid == 0) *p.count = total;
-  __syncthreads();
-  const int vec = static_cast<int>(p.dim / 8);
-  for (int64_t i = tid; i < static_cast<int64_t>(kept) * vec; i += 256) {
-    const int r = static_cast<int>(i / vec), c = static_cast<int>(i - static_cast<int64_t>(r) * vec);
-    reinterpret_cast<uint4*>(p.rows + (before + r) * p.dim)[c] =
-        __ldg(reinterpret_cast<const uint4*>(p.h + src[r] * p.dim) + c);
-  }
-  if (p.dh)
-    for (int64_t i = tid; i < static_cast<int64_t>(absent) * vec; i += 256) {
-      const int r = static_cast<int>(i / vec), c = static_cast<int>(i - static_cast<int64_t>(r) * vec);
-      reinterpret_cast<uint4*>(p.dh + gone[r] * p.dim)[c] = make_uint4(0, 0, 0, 0);
-    }
-  // rows past the kept ones, up to a whole tile
+  // rows past the kept ones, up to a whole tile: shared out among the CTAs
   const int64_t end = (static_cast<int64_t>(total) + kTile - 1) / kTile * kTile;
-  const int64_t z0 = t0 > total ? t0 : total;
-  const int64_t z1 = t0 + kGatherTokens < end ? t0 + kGatherTokens : end;
-  for (int64_t r = z0 + tid; r < z1; r += 256) {
-    p.idx[r] = -1;
-    p.target[r] = -1;
-    if (p.scale) p.lse_rows[r] = p.scale[r] = 0.f;
+  for (int64_t r = total + blockIdx.x; r < end; r += gridDim.x) {
+    if (tid == 0) {
+      p.target[r] = -1;
+      if (p.scale) p.lse_rows[r] = p.scale[r] = 0.f;
+    }
+    if (!all)
+      for (int c = tid; c < vec; c += kGatherThreads)
+        reinterpret_cast<uint4*>(p.rows + r * p.dim)[c] = make_uint4(0, 0, 0, 0);
   }
-  for (int64_t i = tid; i < (z1 - z0) * vec; i += 256)
-    reinterpret_cast<uint4*>(p.rows + z0 * p.dim)[i] = make_uint4(0, 0, 0, 0);
 }
 
 // ---- joining the tiles of a row --------------------------------------------------
-__global__ void __launch_bounds__(256) xent_join_kernel(const int* count, const int* idx,
-                                                        const int* target, const float2* part,
-                                                        int64_t pitch, int tiles,
-                                                        const float* target_logit, float* loss,
-                                                        float* lse) {
-  __shared__ float2 red[8][32];
+// Merges (maximum, sum) pairs of a softmax's denominator.
+__device__ __forceinline__ void merge(float& m, float& l, const float2 v) {
+  const float nm = fmaxf(m, v.x);
+  if (nm == -INFINITY && l == 0.f && v.y == 0.f) return;  // nothing on either side
+  l = l * ex2(m - nm) + v.y * ex2(v.x - nm);
+  m = nm;
+}
+
+// A warp row per 32 tokens, 32 of them sharing the tiles.
+__global__ void __launch_bounds__(1024) xent_join_kernel(const GemmArgs p, int64_t ignore,
+                                                         const int* idx, int tiles, float* loss,
+                                                         float* lse) {
+  __shared__ float2 red[32][33];
   const int lane = threadIdx.x & 31, wy = threadIdx.x >> 5;
   const int64_t r = static_cast<int64_t>(blockIdx.x) * 32 + lane;
-  const bool on = r < *count;
+  wait_previous();
+  const bool on = r < rows_of(p);
   float m = -INFINITY, l = 0.f;
-  if (on)
-    for (int i = wy; i < tiles; i += 8) {
-      const float2 v = part[i * pitch + r];
-      const float nm = fmaxf(m, v.x);
-      l = l * ex2(m - nm) + v.y * ex2(v.x - nm);
-      m = nm;
+  if (on) {
+    const float2* q = p.part + r;
+    for (int i = wy; i < tiles; i += 128) {
+      float2 v[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        v[j] = i + 32 * j < tiles ? q[(i + 32 * j) * p.part_pitch] : make_float2(-INFINITY, 0.f);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) merge(m, l, v[j]);
     }
-  red[wy][lane] = make_float2(m, l);
+  }
+  red[lane][wy] = make_float2(m, l);
   __syncthreads();
-  if (wy == 0 && on) {
-    for (int i = 1; i < 8; ++i) {
-      const float2 v = red[i][lane];
-      if (v.x == -INFINITY && v.y == 0.f) continue;  // no tile fell to this warp
-      const float nm = fmaxf(m, v.x);
-      l = l * ex2(m - nm) + v.y * ex2(v.x - nm);
-      m = nm;
-    }
+  // warp wy joins token wy's 32 pairs
+  const float2 v = red[wy][lane];
+  m = v.x;
+  l = v.y;
+#pragma unroll
+  for (int o = 16; o >= 1; o /= 2) {
+    const float2 w = make_float2(__shfl_xor_sync(0xffffffffu, m, o), __shfl_xor_sync(0xffffffffu, l, o));
+    merge(m, l, w);
+  }
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * 32 + wy;
+  if (lane == 0 && row < rows_of(p)) {
+    const int64_t t = idx ? idx[row] : row;
+    const bool none = !p.count && p.targets[t] == ignore;
     const float s = kLn2 * (m + log2f(l));
-    const int t = idx[r];
-    lse[t] = s;
-    loss[t] = target[r] >= 0 ? s - target_logit[r] : NAN;
+    lse[t] = none ? 0.f : s;
+    loss[t] = none ? 0.f : target_of(p, row) >= 0 ? s - p.target_logit[row] : NAN;
   }
 }
 
 // dh of a token: the sum of the splits' partial sums, rounded once.
-__global__ void __launch_bounds__(256) xent_dh_kernel(const int* count, const int* idx,
-                                                      const float* part, int64_t dim, int kv_whole,
+__global__ void __launch_bounds__(256) xent_dh_kernel(const GemmArgs p, const int* idx,
                                                       __nv_bfloat16* dh) {
-  const int rows = *count, mt = ceil_div(rows, kTile);
-  const int splits = dh_splits(mt, ceil_div(dim, kTile), kv_whole);
-  const int vec = static_cast<int>(dim / 8);
+  wait_previous();
+  const int rows = rows_of(p), mt = ceil_div(rows, kTile);
+  const int splits = dh_splits(mt, ceil_div(p.dim, kTile), p.kv_whole);
+  const int vec = static_cast<int>(p.dim / 8);
   const int64_t step = static_cast<int64_t>(gridDim.x) * 256, n = static_cast<int64_t>(rows) * vec;
+  const int64_t plane = static_cast<int64_t>(mt) * kTile * p.dim;
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < n; i += step) {
     const int64_t r = i / vec, c = (i - r * vec) * 8;
+    const float* q = p.dh + r * p.dim + c;
     float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
     for (int s = 0; s < splits; ++s) {
-      const float4* q =
-          reinterpret_cast<const float4*>(part + (static_cast<int64_t>(s) * mt * kTile + r) * dim + c);
-      const float4 a = q[0], b = q[1];
+      const float4 a = reinterpret_cast<const float4*>(q + s * plane)[0];
+      const float4 b = reinterpret_cast<const float4*>(q + s * plane)[1];
       v[0] += a.x; v[1] += a.y; v[2] += a.z; v[3] += a.w;
       v[4] += b.x; v[5] += b.y; v[6] += b.z; v[7] += b.w;
     }
-    *reinterpret_cast<uint4*>(dh + idx[r] * dim + c) = make_uint4(
+    *reinterpret_cast<uint4*>(dh + idx[r] * p.dim + c) = make_uint4(
         pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[4], v[5]), pack2(v[6], v[7]));
   }
 }
@@ -633,7 +691,12 @@ cudaError_t gemm(const Maps& maps, const GemmArgs& a, cudaStream_t s) {
   const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              static_cast<int>(kSmem));
   if (e != cudaSuccess) return e;
-  k<<<2 * kClusters, kThreads, kSmem, s>>>(maps, a);
+  return launch_after(k, 2 * kClusters, kThreads, kSmem, s, maps, a);
+}
+
+cudaError_t gather(const GatherArgs& g, cudaStream_t s) {
+  const int64_t ctas = (g.tokens + g.per - 1) / g.per;
+  xent_gather_kernel<<<static_cast<unsigned>(ctas), kGatherThreads, 0, s>>>(g);
   return cudaGetLastError();
 }
 
@@ -647,6 +710,7 @@ GatherArgs gather_args(const XentParams& p, const Layout& l, char* ws) {
   g.idx = reinterpret_cast<int*>(ws + l.idx);
   g.target = reinterpret_cast<int*>(ws + l.target);
   g.rows = reinterpret_cast<__nv_bfloat16*>(ws + l.rows);
+  g.per = gather_tokens(p.shape.tokens);
   return g;
 }
 
@@ -654,6 +718,8 @@ GemmArgs gemm_args(const XentParams& p, const Layout& l, char* ws) {
   GemmArgs a = {};
   a.count = reinterpret_cast<int*>(ws + l.count);
   a.target = reinterpret_cast<int*>(ws + l.target);
+  a.targets = p.targets;
+  a.tokens = p.shape.tokens;
   a.vocab = p.shape.vocab; a.dim = p.shape.dim;
   a.err = p.err;
   return a;
@@ -667,27 +733,33 @@ cudaError_t launch_xent_fwd(const XentParams& p, cudaStream_t s) {
   const XentShape& z = p.shape;
   const Layout l = layout_of(z, false);
   char* ws = static_cast<char*>(p.workspace);
-  GatherArgs g = gather_args(p, l, ws);
-  g.loss = p.loss;
-  g.lse_out = p.lse;
-  Maps maps = {};
-  if (!map_bf16_sw128(&maps.a, g.rows, z.dim, l.tpad, z.dim, kHalfTile) ||
-      !map_bf16_sw128(&maps.b, p.weight, z.dim, z.vocab, z.dim, kHalfTile))
-    return cudaErrorInvalidValue;
-  xent_gather_kernel<<<static_cast<unsigned>(l.tpad / kGatherTokens), 256, 0, s>>>(g);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
   GemmArgs a = gemm_args(p, l, ws);
   a.v0 = 0;
   a.vp = static_cast<int>(z.vocab);
   a.part = reinterpret_cast<float2*>(ws + l.part);
   a.part_pitch = l.tpad;
   a.target_logit = reinterpret_cast<float*>(ws + l.target_logit);
+  GatherArgs g = gather_args(p, l, ws);
+  g.loss = p.loss;
+  g.lse_out = p.lse;
+  Maps maps = {};
+  if (!map_bf16_sw128(&maps.h, p.h, z.dim, z.tokens, z.dim, kHalfTile) ||
+      !map_bf16_sw128(&maps.b, p.weight, z.dim, z.vocab, z.dim, kHalfTile))
+    return cudaErrorInvalidValue;
+  cudaError_t e;
+  // leaving ignored tokens out saves nothing while all of them fit one row of tiles
+  const bool direct = z.tokens <= kTile;
+  if (direct) {
+    a.count = nullptr;
+  } else {
+    if (!map_bf16_sw128(&maps.a, g.rows, z.dim, l.tpad, z.dim, kHalfTile))
+      return cudaErrorInvalidValue;
+    if ((e = gather(g, s)) != cudaSuccess) return e;
+  }
   if ((e = gemm<kLse>(maps, a, s)) != cudaSuccess) return e;
-  xent_join_kernel<<<static_cast<unsigned>((z.tokens + 31) / 32), 256, 0, s>>>(
-      a.count, g.idx, a.target, a.part, a.part_pitch, ceil_div(z.vocab, kTile), a.target_logit,
-      p.loss, p.lse);
-  return cudaGetLastError();
+  return launch_after(xent_join_kernel, static_cast<unsigned>((z.tokens + 31) / 32), 1024, 0, s, a,
+                      p.ignore_index, direct ? nullptr : g.idx, ceil_div(z.vocab, kTile), p.loss,
+                      p.lse);
 }
 
 cudaError_t launch_xent_bwd(const XentParams& p, cudaStream_t s) {
@@ -710,14 +782,15 @@ cudaError_t launch_xent_bwd(const XentParams& p, cudaStream_t s) {
   a.dw = static_cast<__nv_bfloat16*>(p.dweight);
   Maps in = {}, out = {};
   if (!map_bf16_sw128(&in.a, g.rows, z.dim, l.tpad, z.dim, kHalfTile) ||
+      !map_bf16_sw128(&in.h, p.h, z.dim, z.tokens, z.dim, kHalfTile) ||
       !map_bf16_sw128(&in.b, p.weight, z.dim, z.vocab, z.dim, kHalfTile) ||
       !map_bf16_sw128(&out.a, a.g, l.piece, l.tpad, l.piece, kHalfTile) ||
       !map_bf16_sw128(&out.b, p.weight, z.dim, z.vocab, z.dim, kBk) ||
       !map_bf16_sw128(&out.at, a.g, l.piece, l.tpad, l.piece, kBk) ||
-      !map_bf16_sw128(&out.bt, g.rows, z.dim, l.tpad, z.dim, kBk))
+      !map_bf16_sw128(&out.bt, g.rows, z.dim, l.tpad, z.dim, kBk) ||
+      !map_bf16_sw128(&out.h, p.h, z.dim, z.tokens, z.dim, kBk))
     return cudaErrorInvalidValue;
-  xent_gather_kernel<<<static_cast<unsigned>(l.tpad / kGatherTokens), 256, 0, s>>>(g);
-  cudaError_t e = cudaGetLastError();
+  cudaError_t e = gather(g, s);
   if (e != cudaSuccess) return e;
   for (int64_t i = 0; i < l.pieces; ++i) {
     a.v0 = i * l.piece;
@@ -726,9 +799,8 @@ cudaError_t launch_xent_bwd(const XentParams& p, cudaStream_t s) {
     if ((e = gemm<kGrad>(in, a, s)) != cudaSuccess) return e;
     if ((e = gemm<kProducts>(out, a, s)) != cudaSuccess) return e;
   }
-  xent_dh_kernel<<<4 * kSms, 256, 0, s>>>(a.count, g.idx, a.dh, z.dim, a.kv_whole,
-                                          static_cast<__nv_bfloat16*>(p.dh));
-  return cudaGetLastError();
+  return launch_after(xent_dh_kernel, 4 * kSms, 256, 0, s, a, g.idx,
+                      static_cast<__nv_bfloat16*>(p.dh));
 }
 
 }  // namespace ssm

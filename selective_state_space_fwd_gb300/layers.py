@@ -19,6 +19,11 @@ from ._binding import ConvShapes, DType, NormShapes, SsmError, XentShapes, _chec
 
 _CODES = {torch.float32: int(DType.F32), torch.bfloat16: int(DType.BF16)}
 
+# the current stream's handle by device index: a tenth of the cost of building
+# a Stream object, which is a good part of a short call
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
 
 def _code(dtype) -> int:
     code = _CODES.get(dtype)
@@ -66,7 +71,7 @@ def _on_stream(f):
 def _call(fn, dev, *args):
     """fn(*args, the current stream of `dev`) on `dev`, raising SsmError on a bad
     status."""
-    handle = torch.cuda.current_stream(dev).cuda_stream
+    handle = _raw_stream(dev.index)
     if torch.cuda.current_device() == dev.index:
         st = fn(*args, handle)
     else:
@@ -77,7 +82,7 @@ def _call(fn, dev, *args):
 
 
 def _cuda(t, name):
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     return t.device
 
@@ -87,14 +92,17 @@ def _conv_args(x, weight, bias, silu, rank):
     has `rank` dimensions, the last of them contiguous."""
     dev = _cuda(x, "x")
     code = _code(x.dtype)
-    if x.dim() != rank:
-        raise ValueError(f"x: {x.dim()} dimensions, expected {rank}")
+    size, stride = x.shape, x.stride()
+    if len(size) != rank:
+        raise ValueError(f"x: {len(size)} dimensions, expected {rank}")
     if weight.dim() != 2:
         raise ValueError(f"weight: shape {tuple(weight.shape)}, expected [dim, width]")
-    batch, dim = x.shape[0], x.shape[-1]
-    seqlen = x.shape[1] if rank == 3 else 1
     width = weight.shape[1]
-    stride = x.stride()
+    if rank == 3:
+        batch, seqlen, dim = size
+        step = stride[1] if seqlen > 1 else dim
+    else:
+        (batch, dim), seqlen, step = size, 1, size[1]
     if stride[-1] != 1 and dim > 1:
         raise ValueError("x: the channels must be contiguous")
     _dense(weight, "weight", (dim, width), torch.float32, dev)
@@ -102,9 +110,8 @@ def _conv_args(x, weight, bias, silu, rank):
         _dense(bias, "bias", (dim,), torch.float32, dev)
     # the stride of an axis of one element is never used; the row's own length
     # keeps it from deciding the alignment rule
-    shapes = ConvShapes(batch, seqlen, dim, width, stride[0] if batch > 1 else dim,
-                        stride[1] if rank == 3 and seqlen > 1 else dim, int(bool(silu)))
-    return dev, code, (batch, seqlen, dim, width), shapes
+    return dev, code, (batch, seqlen, dim, width), ConvShapes(
+        batch, seqlen, dim, width, stride[0] if batch > 1 else dim, step, 1 if silu else 0)
 
 
 @_on_stream
