@@ -20,6 +20,7 @@
 // thread, then over the threads of the CTA in a fixed order, then over the
 // CTAs by a second kernel: no atomics, so the sums do not depend on timing.
 #include "common.cuh"
+#include "f32x2.cuh"
 #include "layers.h"
 #include "pdl.cuh"
 #include "vec.cuh"
@@ -30,12 +31,33 @@ namespace {
 constexpr int kConvThreads = 256;
 constexpr int kSms = 152;
 
-// Steps per chunk: long chunks re-read less; short ones are for inputs that
-// would not give every SM two CTAs.
-int chunk_steps(int64_t batch, int64_t seqlen, int64_t cvs) {
-  for (int tc = 64; tc > 8; tc /= 2)
-    if (batch * ((seqlen + tc - 1) / tc) * cvs >= int64_t(kSms) * 2 * kConvThreads) return tc;
-  return 8;
+// Rows in flight per thread, channels per thread and resident CTAs per SM
+// (their registers are the bound: the taps, the window and the rows in flight).
+// Measured on 8 x 4096 x 1024, width 4: forward fp32 48.5 us with 4 channels and
+// 2 CTAs, 57.6 us with 2 and 3; bf16 30.3 us with 4 channels and 3 CTAs, 32.5 us
+// with 8 and 2.  Backward (forward included, fp32): 130 us with 2 channels and 8
+// rows in flight, 139 us with 4 rows, 146 us with 4 channels and 2 rows.
+constexpr int U = 8;
+constexpr int kFwdVec = 4;
+template <typename T> constexpr int fwd_ctas() { return sizeof(T) == 2 ? 3 : 2; }
+template <typename T> constexpr int bwd_vec() { return 8 / sizeof(T); }
+constexpr int kBwdCtas = 2;
+
+// Steps per chunk.  A thread's time is its number of chunks times their length
+// and the `halo` steps a chunk adds; short chunks spread the work evenly, long
+// ones add less.
+int chunk_steps(int64_t batch, int64_t seqlen, int64_t cvs, int ctas_per_sm, int halo) {
+  const int64_t slots = int64_t(kSms) * ctas_per_sm * kConvThreads;
+  int best = 64;
+  int64_t least = INT64_MAX;
+  for (int tc : {64, 48, 32, 24, 16, 8}) {
+    const int64_t per = (batch * ((seqlen + tc - 1) / tc) * cvs + slots - 1) / slots;
+    if (per * (tc + halo) < least) {
+      least = per * (tc + halo);
+      best = tc;
+    }
+  }
+  return best;
 }
 
 // Channel groups per CTA (a power of two): a warp along the channels where
@@ -47,10 +69,10 @@ struct ConvGrid {
   int64_t chunks, gx, gy;
 };
 
-ConvGrid conv_grid(int64_t batch, int64_t seqlen, int64_t dim, int vec, int ctas_per_sm) {
+ConvGrid conv_grid(int64_t batch, int64_t seqlen, int64_t dim, int vec, int ctas_per_sm, int halo) {
   ConvGrid g;
   const int64_t cvs = (dim + vec - 1) / vec;
-  g.tc = chunk_steps(batch, seqlen, cvs);
+  g.tc = chunk_steps(batch, seqlen, cvs, ctas_per_sm, halo);
   g.lx = lanes_log2(cvs);
   g.chunks = (seqlen + g.tc - 1) / g.tc;
   const int64_t ty = kConvThreads >> g.lx;
@@ -81,21 +103,26 @@ __device__ __forceinline__ Raw<T, VEC> state_row(const void* state0, int64_t b, 
 
 template <int K, int VEC>
 __device__ __forceinline__ void load_taps(const float* weight, const float* bias, int64_t d0,
-                                          float (&w)[VEC][K], float (&bv)[VEC]) {
+                                          float (&w)[K][VEC], float (&bv)[VEC]) {
   if constexpr (VEC > 1) {  // VEC * K consecutive floats, 16-byte aligned (the caller's check)
     float t[VEC * K];
+    if constexpr (VEC * K % 4 == 0) {
 #pragma unroll
-    for (int i = 0; i < VEC * K / 4; ++i) {
-      const float4 v = __ldg(reinterpret_cast<const float4*>(weight + d0 * K) + i);
-      t[4 * i] = v.x; t[4 * i + 1] = v.y; t[4 * i + 2] = v.z; t[4 * i + 3] = v.w;
+      for (int i = 0; i < VEC * K / 4; ++i) {
+        const float4 v = __ldg(reinterpret_cast<const float4*>(weight + d0 * K) + i);
+        t[4 * i] = v.x; t[4 * i + 1] = v.y; t[4 * i + 2] = v.z; t[4 * i + 3] = v.w;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < VEC * K; ++i) t[i] = __ldg(weight + d0 * K + i);
     }
 #pragma unroll
     for (int v = 0; v < VEC; ++v)
 #pragma unroll
-      for (int k = 0; k < K; ++k) w[v][k] = t[v * K + k];
+      for (int k = 0; k < K; ++k) w[k][v] = t[v * K + k];
   } else {
 #pragma unroll
-    for (int k = 0; k < K; ++k) w[0][k] = __ldg(weight + d0 * K + k);
+    for (int k = 0; k < K; ++k) w[k][0] = __ldg(weight + d0 * K + k);
   }
 #pragma unroll
   for (int v = 0; v < VEC; ++v) bv[v] = bias ? __ldg(bias + d0 + v) : 0.f;
@@ -103,16 +130,36 @@ __device__ __forceinline__ void load_taps(const float* weight, const float* bias
 
 // pre of the row `cur` after the window `win` (oldest row first).
 template <int K, int VEC>
-__device__ __forceinline__ void taps(const float (&w)[VEC][K], const float (&bv)[VEC],
+__device__ __forceinline__ void taps(const float (&w)[K][VEC], const float (&bv)[VEC],
                                      const float (&win)[K - 1][VEC], const float (&cur)[VEC],
                                      float (&pre)[VEC]) {
+  vfma<VEC>(pre, w[0], win[0], bv);
 #pragma unroll
-  for (int v = 0; v < VEC; ++v) {
-    float a = bv[v];
+  for (int k = 1; k < K - 1; ++k) vfma<VEC>(pre, w[k], win[k], pre);
+  vfma<VEC>(pre, w[K - 1], cur, pre);
+}
+
+// 1 / v with the MUFU unit (PTX rcp.approx.ftz.f32: within 1 ulp; 0 for
+// infinities, which a sigmoid's denominator may be).
+__device__ __forceinline__ float rcp(float v) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+
+// s = sigmoid(v) = 1 / (1 + e^-v).
+template <int VEC>
+__device__ __forceinline__ void sigmoid(const float (&v)[VEC], float (&s)[VEC]) {
+  float one[VEC];
+  vscale<VEC>(s, v, -kLog2e);
 #pragma unroll
-    for (int k = 0; k < K - 1; ++k) a = fmaf(w[v][k], win[k][v], a);
-    pre[v] = fmaf(w[v][K - 1], cur[v], a);
+  for (int i = 0; i < VEC; ++i) {
+    s[i] = ex2(s[i]);
+    one[i] = 1.f;
   }
+  vadd<VEC>(s, s, one);
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) s[i] = rcp(s[i]);
 }
 
 template <int K, int VEC>
@@ -125,74 +172,78 @@ __device__ __forceinline__ void push(float (&win)[K - 1][VEC], const float (&cur
   }
 }
 
-template <typename T, int K, int VEC, int U>
-__global__ void __launch_bounds__(kConvThreads) conv_fwd_kernel(const ConvParams p, int tc, int lx,
-                                                                int64_t chunks) {
+template <typename T, int K, int VEC>
+__global__ void __launch_bounds__(kConvThreads, fwd_ctas<T>())
+    conv_fwd_kernel(const ConvParams p, int tc, int lx, int64_t chunks) {
   const int64_t cv = (static_cast<int64_t>(blockIdx.x) << lx) + (threadIdx.x & ((1 << lx) - 1));
   const int64_t d0 = cv * VEC;
   if (d0 >= p.dim) return;
   const int64_t ty = kConvThreads >> lx, items = p.batch * chunks;
-  float w[VEC][K], bv[VEC];
+  float w[K][VEC], bv[VEC];
   load_taps<K, VEC>(p.weight, p.bias, d0, w, bv);
   for (int64_t it = blockIdx.y * ty + (threadIdx.x >> lx); it < items; it += gridDim.y * ty) {
     const int64_t b = it / chunks, c = it - b * chunks;
-    const int64_t t0 = c * tc, t1 = t0 + tc < p.seqlen ? t0 + tc : p.seqlen;
+    const int64_t t0 = c * tc;
     const int64_t vl = conv_valid(p, b);
-    const int64_t te = t1 < vl ? t1 : vl;  // end of the valid steps of the chunk
+    const int n = static_cast<int>(p.seqlen - t0 < tc ? p.seqlen - t0 : tc);  // steps of the chunk
+    const int nv = static_cast<int>(vl - t0 < 0 ? 0 : vl - t0 < n ? vl - t0 : n);  // valid ones
     const T* xb = static_cast<const T*>(p.x) + b * p.x_batch + d0;
-    T* yb = static_cast<T*>(p.y) + b * p.seqlen * p.dim + d0;
-    if (t0 < te) {
+    T* y = static_cast<T*>(p.y) + (b * p.seqlen + t0) * p.dim + d0;
+    if (nv > 0) {
+      const T* x = xb + t0 * p.x_step;
       float win[K - 1][VEC];
 #pragma unroll
-      for (int k = 0; k < K - 1; ++k) {
-        const int64_t t = t0 - (K - 1) + k;
-        const Raw<T, VEC> r = t >= 0 ? raw_load<T, VEC>(xb + t * p.x_step)
-                                     : state_row<T, K, VEC>(p.state0, b, p.dim, d0,
-                                                            static_cast<int>(t) + K - 1);
-        widen<VEC>(r, win[k]);
-      }
-      for (int64_t t = t0; t < te; t += U) {
+      for (int k = 0; k < K - 1; ++k)
+        widen<VEC>(t0 > 0 ? raw_load<T, VEC>(x - (K - 1 - k) * p.x_step)
+                          : state_row<T, K, VEC>(p.state0, b, p.dim, d0, k),
+                   win[k]);
+      auto emit = [&](const Raw<T, VEC>& raw) {
+        float cur[VEC], pre[VEC];
+        widen<VEC>(raw, cur);
+        taps<K, VEC>(w, bv, win, cur, pre);
+        if (p.silu) {
+          float sg[VEC];
+          sigmoid<VEC>(pre, sg);
+          vmul<VEC>(pre, pre, sg);
+        }
+        store_f<T, VEC>(y, pre);
+        y += p.dim;
+        push<K, VEC>(win, cur);
+      };
+      int i = 0;
+      for (; i + U <= nv; i += U) {  // U rows in flight
         Raw<T, VEC> raw[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-          if (t + u < te) raw[u] = raw_load<T, VEC>(xb + (t + u) * p.x_step);
-#pragma unroll
         for (int u = 0; u < U; ++u) {
-          if (t + u < te) {
-            float cur[VEC], pre[VEC];
-            widen<VEC>(raw[u], cur);
-            taps<K, VEC>(w, bv, win, cur, pre);
-            if (p.silu) {
-#pragma unroll
-              for (int v = 0; v < VEC; ++v) pre[v] = silu(pre[v]);
-            }
-            store_f<T, VEC>(yb + (t + u) * p.dim, pre);
-            push<K, VEC>(win, cur);
-          }
+          raw[u] = raw_load<T, VEC>(x);
+          x += p.x_step;
         }
+#pragma unroll
+        for (int u = 0; u < U; ++u) emit(raw[u]);
       }
+#pragma unroll 1
+      for (; i < nv; ++i, x += p.x_step) emit(raw_load<T, VEC>(x));
     }
     Raw<T, VEC> z;
     raw_zero<T, VEC>(z);
-    for (int64_t t = t0 < te ? te : t0; t < t1; ++t) raw_store<T, VEC>(yb + t * p.dim, z);
+    for (int i = nv; i < n; ++i, y += p.dim) raw_store<T, VEC>(y, z);
     if (c == 0 && p.out_final != nullptr) {
       T* fb = static_cast<T*>(p.out_final) + b * (K - 1) * p.dim + d0;
-      Raw<T, VEC> r[K - 1];
 #pragma unroll
       for (int k = 0; k < K - 1; ++k) {
         const int64_t t = vl - (K - 1) + k;
-        r[k] = t >= 0 ? raw_load<T, VEC>(xb + t * p.x_step)
-                      : state_row<T, K, VEC>(p.state0, b, p.dim, d0, static_cast<int>(t) + K - 1);
+        raw_store<T, VEC>(fb + k * p.dim,
+                          t >= 0 ? raw_load<T, VEC>(xb + t * p.x_step)
+                                 : state_row<T, K, VEC>(p.state0, b, p.dim, d0,
+                                                        static_cast<int>(t) + K - 1));
       }
-#pragma unroll
-      for (int k = 0; k < K - 1; ++k) raw_store<T, VEC>(fb + k * p.dim, r[k]);
     }
   }
 }
 
-template <typename T, int K, int VEC, int U>
-__global__ void __launch_bounds__(kConvThreads) conv_bwd_kernel(const ConvBwdParams q, int tc,
-                                                                int lx, int64_t chunks) {
+template <typename T, int K, int VEC>
+__global__ void __launch_bounds__(kConvThreads, kBwdCtas)
+    conv_bwd_kernel(const ConvBwdParams q, int tc, int lx, int64_t chunks) {
   const ConvParams& p = q.fwd;
   const int tx = threadIdx.x & ((1 << lx) - 1);
   const int64_t cv = (static_cast<int64_t>(blockIdx.x) << lx) + tx;
@@ -201,7 +252,7 @@ __global__ void __launch_bounds__(kConvThreads) conv_bwd_kernel(const ConvBwdPar
   const int ty = kConvThreads >> lx;
   const int64_t items = on ? p.batch * chunks : 0;
   release_next();
-  float w[VEC][K], bv[VEC], dw[K][VEC], db[VEC];
+  float w[K][VEC], bv[VEC], dw[K][VEC], db[VEC];
 #pragma unroll
   for (int v = 0; v < VEC; ++v) {
     db[v] = 0.f;
@@ -212,82 +263,85 @@ __global__ void __launch_bounds__(kConvThreads) conv_bwd_kernel(const ConvBwdPar
   for (int64_t it = static_cast<int64_t>(blockIdx.y) * ty + (threadIdx.x >> lx); it < items;
        it += static_cast<int64_t>(gridDim.y) * ty) {
     const int64_t b = it / chunks, c = it - b * chunks;
-    const int64_t t0 = c * tc, t1 = t0 + tc < p.seqlen ? t0 + tc : p.seqlen;
+    const int64_t t0 = c * tc;
     const int64_t vl = conv_valid(p, b);
-    const int64_t tl = t1 + K - 1;          // dx[t1 - 1] needs dpre up to step t1 + K - 2
-    const int64_t te = tl < vl ? tl : vl;   // dpre is 0 from valid_len on
-    const T* xb = static_cast<const T*>(p.x) + b * p.x_batch + d0;
-    const T* gb = static_cast<const T*>(q.dy) + b * p.seqlen * p.dim + d0;
-    T* ob = static_cast<T*>(q.dx) + b * p.seqlen * p.dim + d0;
-    T* sb = c == 0 && q.dstate0 ? static_cast<T*>(q.dstate0) + b * (K - 1) * p.dim + d0 : nullptr;
+    const int n = static_cast<int>(p.seqlen - t0 < tc ? p.seqlen - t0 : tc);  // steps of the chunk
+    // steps from the chunk's first that have a dpre; dx[n - 1] needs dpre up to n + K - 2
+    const int nl = static_cast<int>(vl - t0 < 0 ? 0 : vl - t0 < n + K - 1 ? vl - t0 : n + K - 1);
+    const T* x = static_cast<const T*>(p.x) + b * p.x_batch + t0 * p.x_step + d0;
+    const T* gy = static_cast<const T*>(q.dy) + (b * p.seqlen + t0) * p.dim + d0;
+    // dx of step i - (K - 1), written at step i
+    T* o = static_cast<T*>(q.dx) + (b * p.seqlen + t0 - (K - 1)) * p.dim + d0;
     float win[K - 1][VEC], dp[K - 1][VEC];
 #pragma unroll
     for (int k = 0; k < K - 1; ++k) {
 #pragma unroll
       for (int v = 0; v < VEC; ++v) win[k][v] = dp[k][v] = 0.f;
-      const int64_t t = t0 - (K - 1) + k;
-      if (t0 < te)
-        widen<VEC>(t >= 0 ? raw_load<T, VEC>(xb + t * p.x_step)
-                          : state_row<T, K, VEC>(p.state0, b, p.dim, d0, static_cast<int>(t) + K - 1),
+      if (nl > 0)
+        widen<VEC>(t0 > 0 ? raw_load<T, VEC>(x - (K - 1 - k) * p.x_step)
+                          : state_row<T, K, VEC>(p.state0, b, p.dim, d0, k),
                    win[k]);
     }
-    for (int64_t t = t0; t < tl; t += U) {
+    // dx from the window of dpre and the step's own
+    auto emit = [&](int i, const float(&g)[VEC]) {
+      float a[VEC];
+      vmul<VEC>(a, w[0], g);
+#pragma unroll
+      for (int k = 1; k < K; ++k) vfma<VEC>(a, w[k], dp[K - 1 - k], a);
+      if (i >= K - 1)
+        store_f<T, VEC>(o, a);
+      else if (c == 0 && q.dstate0)
+        store_f<T, VEC>(static_cast<T*>(q.dstate0) + (b * (K - 1) + i) * p.dim + d0, a);
+      o += p.dim;
+      push<K, VEC>(dp, g);
+    };
+    auto step = [&](int i, const Raw<T, VEC>& xr, const Raw<T, VEC>& gr) {
+      float cur[VEC], g[VEC];
+      widen<VEC>(xr, cur);
+      widen<VEC>(gr, g);
+      if (p.silu) {  // silu'(v) = s (1 + v (1 - s)), s = sigmoid(v)
+        float pre[VEC], sg[VEC], t[VEC], one[VEC];
+        taps<K, VEC>(w, bv, win, cur, pre);
+        sigmoid<VEC>(pre, sg);
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) {
+          t[v] = 1.f - sg[v];
+          one[v] = 1.f;
+        }
+        vfma<VEC>(t, pre, t, one);
+        vmul<VEC>(t, t, sg);
+        vmul<VEC>(g, g, t);
+      }
+      if (i < n) {
+        vadd<VEC>(db, db, g);
+#pragma unroll
+        for (int k = 0; k < K - 1; ++k) vfma<VEC>(dw[k], g, win[k], dw[k]);
+        vfma<VEC>(dw[K - 1], g, cur, dw[K - 1]);
+      }
+      emit(i, g);
+      push<K, VEC>(win, cur);
+    };
+    int i = 0;
+    for (; i + U <= nl; i += U) {  // U rows of x and of dy in flight
       Raw<T, VEC> xr[U], gr[U];
 #pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (t + u < te) {
-          xr[u] = raw_load<T, VEC>(xb + (t + u) * p.x_step);
-          gr[u] = raw_load<T, VEC>(gb + (t + u) * p.dim);
-        }
-#pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int64_t tt = t + u;
-        if (tt < tl) {
-          float g[VEC];
-#pragma unroll
-          for (int v = 0; v < VEC; ++v) g[v] = 0.f;
-          if (tt < te) {
-            float cur[VEC];
-            widen<VEC>(xr[u], cur);
-            widen<VEC>(gr[u], g);
-            if (p.silu) {  // silu'(v) = s (1 + v (1 - s)), s = sigmoid(v)
-              float pre[VEC];
-              taps<K, VEC>(w, bv, win, cur, pre);
-#pragma unroll
-              for (int v = 0; v < VEC; ++v) {
-                const float s = __fdividef(1.f, 1.f + ex2(-pre[v] * kLog2e));
-                g[v] *= s * fmaf(pre[v], 1.f - s, 1.f);
-              }
-            }
-            if (tt < t1) {
-#pragma unroll
-              for (int v = 0; v < VEC; ++v) {
-                db[v] += g[v];
-#pragma unroll
-                for (int k = 0; k < K - 1; ++k) dw[k][v] = fmaf(g[v], win[k][v], dw[k][v]);
-                dw[K - 1][v] = fmaf(g[v], cur[v], dw[K - 1][v]);
-              }
-            }
-            push<K, VEC>(win, cur);
-          }
-          // dx of step e = tt - (K - 1): taps K - 1 .. 0 against dpre[e .. tt]
-          float o[VEC];
-#pragma unroll
-          for (int v = 0; v < VEC; ++v) {
-            float a = w[v][0] * g[v];
-#pragma unroll
-            for (int k = 1; k < K; ++k) a = fmaf(w[v][k], dp[K - 1 - k][v], a);
-            o[v] = a;
-          }
-          const int64_t e = tt - (K - 1);
-          if (e >= t0)
-            store_f<T, VEC>(ob + e * p.dim, o);
-          else if (sb != nullptr)
-            store_f<T, VEC>(sb + (e + K - 1) * p.dim, o);
-          push<K, VEC>(dp, g);
-        }
+        xr[u] = raw_load<T, VEC>(x);
+        gr[u] = raw_load<T, VEC>(gy);
+        x += p.x_step;
+        gy += p.dim;
       }
+#pragma unroll
+      for (int u = 0; u < U; ++u) step(i + u, xr[u], gr[u]);
     }
+#pragma unroll 1
+    for (; i < nl; ++i, x += p.x_step, gy += p.dim)
+      step(i, raw_load<T, VEC>(x), raw_load<T, VEC>(gy));
+    float none[VEC];
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) none[v] = 0.f;
+#pragma unroll 1
+    for (; i < n + K - 1; ++i) emit(i, none);
   }
 
   // sums over the CTA's time slots: quantity k < K is tap k, quantity K the bias
@@ -349,7 +403,7 @@ __global__ void __launch_bounds__(128) conv_step_kernel(const ConvStepParams p, 
 #pragma unroll
   for (int k = 0; k < K - 1; ++k) win[k] = raw_load_rw<T, VEC>(st + k * p.dim);
   win[K - 1] = raw_load<T, VEC>(static_cast<const T*>(p.x) + b * p.x_batch + d0);
-  float w[VEC][K], bv[VEC], f[K - 1][VEC], cur[VEC], pre[VEC];
+  float w[K][VEC], bv[VEC], f[K - 1][VEC], cur[VEC], pre[VEC];
   load_taps<K, VEC>(p.weight, p.bias, d0, w, bv);
 #pragma unroll
   for (int k = 0; k < K - 1; ++k) {
@@ -359,8 +413,9 @@ __global__ void __launch_bounds__(128) conv_step_kernel(const ConvStepParams p, 
   widen<VEC>(win[K - 1], cur);
   taps<K, VEC>(w, bv, f, cur, pre);
   if (p.silu) {
-#pragma unroll
-    for (int v = 0; v < VEC; ++v) pre[v] = silu(pre[v]);
+    float sg[VEC];
+    sigmoid<VEC>(pre, sg);
+    vmul<VEC>(pre, pre, sg);
   }
   store_f<T, VEC>(static_cast<T*>(p.y) + b * p.dim + d0, pre);
 }
@@ -378,32 +433,28 @@ bool conv_vec_ok(const ConvParams& p, int vec, size_t es) {
 
 template <typename T, int K>
 cudaError_t conv_fwd_k(const ConvParams& p, cudaStream_t s) {
-  constexpr int V = 16 / sizeof(T);
-  if (conv_vec_ok(p, V, sizeof(T))) {
-    const ConvGrid g = conv_grid(p.batch, p.seqlen, p.dim, V, 8);
-    conv_fwd_kernel<T, K, V, 4><<<dim3(g.gx, g.gy), kConvThreads, 0, s>>>(p, g.tc, g.lx, g.chunks);
-  } else {
-    const ConvGrid g = conv_grid(p.batch, p.seqlen, p.dim, 1, 8);
-    conv_fwd_kernel<T, K, 1, 8><<<dim3(g.gx, g.gy), kConvThreads, 0, s>>>(p, g.tc, g.lx, g.chunks);
-  }
+  const bool vec = conv_vec_ok(p, kFwdVec, sizeof(T));
+  const ConvGrid g = conv_grid(p.batch, p.seqlen, p.dim, vec ? kFwdVec : 1, fwd_ctas<T>(), 2);
+  const dim3 grid(g.gx, g.gy);
+  if (vec)
+    conv_fwd_kernel<T, K, kFwdVec><<<grid, kConvThreads, 0, s>>>(p, g.tc, g.lx, g.chunks);
+  else
+    conv_fwd_kernel<T, K, 1><<<grid, kConvThreads, 0, s>>>(p, g.tc, g.lx, g.chunks);
   return cudaGetLastError();
 }
-
-constexpr int kBwdVec = 4;       // channels per thread of the vector form
-constexpr int kBwdCtasPerSm = 4;
 
 template <typename T, int K>
 cudaError_t conv_bwd_k(const ConvBwdParams& q, cudaStream_t s) {
   const ConvParams& p = q.fwd;
-  const size_t a = kBwdVec * sizeof(T);
-  const bool vec = conv_vec_ok(p, kBwdVec, sizeof(T)) && fits(q.dy, a) && fits(q.dx, a) &&
-                   fits(q.dstate0, a);
-  const ConvGrid g = conv_grid(p.batch, p.seqlen, p.dim, vec ? kBwdVec : 1, kBwdCtasPerSm);
+  constexpr int V = bwd_vec<T>();
+  const bool vec = conv_vec_ok(p, V, sizeof(T)) && fits(q.dy, 8) && fits(q.dx, 8) &&
+                   fits(q.dstate0, 8);
+  const ConvGrid g = conv_grid(p.batch, p.seqlen, p.dim, vec ? V : 1, kBwdCtas, 4);
   const dim3 grid(g.gx, g.gy);
   if (vec)
-    conv_bwd_kernel<T, K, kBwdVec, 4><<<grid, kConvThreads, 0, s>>>(q, g.tc, g.lx, g.chunks);
+    conv_bwd_kernel<T, K, V><<<grid, kConvThreads, 0, s>>>(q, g.tc, g.lx, g.chunks);
   else
-    conv_bwd_kernel<T, K, 1, 8><<<grid, kConvThreads, 0, s>>>(q, g.tc, g.lx, g.chunks);
+    conv_bwd_kernel<T, K, 1><<<grid, kConvThreads, 0, s>>>(q, g.tc, g.lx, g.chunks);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   return launch_after(conv_bwd_sum_kernel,
@@ -438,11 +489,14 @@ cudaError_t launch_conv_fwd(const ConvParams& p, bool bf16, cudaStream_t s) {
   }
 }
 
-// The most partial sums either form of the backward writes.
+// The most partial sums any form of the backward writes.
 int64_t conv_bwd_partials(int64_t batch, int64_t seqlen, int64_t dim) {
-  const int64_t a = conv_grid(batch, seqlen, dim, kBwdVec, kBwdCtasPerSm).gy;
-  const int64_t b = conv_grid(batch, seqlen, dim, 1, kBwdCtasPerSm).gy;
-  return a > b ? a : b;
+  int64_t most = 0;
+  for (int vec : {bwd_vec<float>(), bwd_vec<__nv_bfloat16>(), 1}) {
+    const int64_t n = conv_grid(batch, seqlen, dim, vec, kBwdCtas, 4).gy;
+    most = n > most ? n : most;
+  }
+  return most;
 }
 
 cudaError_t launch_conv_bwd(const ConvBwdParams& q, bool bf16, cudaStream_t s) {

@@ -28,13 +28,23 @@ namespace ssm {
 namespace {
 
 constexpr int kSms = 152;
+constexpr int kBwdPer = 8;  // backward: elements of a row per thread, up to 512 threads; then twice as many
+constexpr int kBwdWarpsPerSm = 20;  // backward: what the registers are shared out for
+__host__ __device__ constexpr int bwd_ctas_per_sm(int threads) {
+  return kBwdWarpsPerSm * 32 / threads;
+}
 
-// Sum of v over the tpr threads of the row (tpr >= 32: whole warps; the warp
-// sums meet in `red`, one slot per warp).  Every thread of the CTA takes part.
-__device__ __forceinline__ float row_sum(float v, int wpr, float* red) {
+// Sum of v over the tpr threads of the row (a part of a warp, or whole warps,
+// whose sums meet in `red`, one slot per warp).  Every thread of the CTA takes
+// part.
+__device__ __forceinline__ float row_sum(float v, int tpr, float* red) {
 #pragma unroll
-  for (int m = 16; m >= 1; m /= 2) v += __shfl_xor_sync(0xffffffffu, v, m);
-  if (wpr == 1) return v;
+  for (int m = 16; m >= 1; m /= 2) {
+    const float o = __shfl_xor_sync(0xffffffffu, v, m);
+    v += m < tpr ? o : 0.f;
+  }
+  if (tpr <= 32) return v;
+  const int wpr = tpr >> 5;
   const int warp = threadIdx.x >> 5;
   if ((threadIdx.x & 31) == 0) red[warp] = v;
   __syncthreads();
@@ -44,158 +54,195 @@ __device__ __forceinline__ float row_sum(float v, int wpr, float* red) {
   return a;
 }
 
+// Group i of a thread's columns starts at column (i tpr + lane) VEC.  Loads past
+// the row's end are made at its last group instead, and their values dropped,
+// so that no load waits on a branch.
+template <int VEC>
+__device__ __forceinline__ int clamped(int c, int dim) {
+  return c < dim ? c : dim - VEC;
+}
+
 template <typename TX, typename TR, int VEC, int NV>
-__global__ void __launch_bounds__(1024) norm_fwd_kernel(const NormParams p, int tpr) {
+__global__ void __launch_bounds__(VEC * NV == 8 ? 1024 : 512)
+    norm_fwd_kernel(const NormParams p, int tpr) {
   __shared__ float red[2][32];
-  const int wpr = tpr >> 5;
   const int64_t row = static_cast<int64_t>(blockIdx.x) * (blockDim.x / tpr) + threadIdx.x / tpr;
   const int lane = threadIdx.x & (tpr - 1);
   const bool on = row < p.rows;
   const int dim = static_cast<int>(p.dim);
-  const int64_t at = row * p.dim;
+  const int64_t at = (on ? row : p.rows - 1) * p.dim;  // groups without a row write nothing
+  const TX* x = static_cast<const TX*>(p.x) + at;
   float f[NV][VEC];
-  if (on) {
-    Raw<TX, VEC> xr[NV];
+  Raw<TX, VEC> xr[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+    xr[i] = raw_load<TX, VEC>(x + clamped<VEC>((i * tpr + lane) * VEC, dim));
+  if (p.residual) {
+    const TR* res = static_cast<const TR*>(p.residual) + at;
+    TR* out = static_cast<TR*>(p.r) + at;
     Raw<TR, VEC> rr[NV];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = (i * tpr + lane) * VEC;
-      if (c < dim) {
-        xr[i] = raw_load<TX, VEC>(static_cast<const TX*>(p.x) + at + c);
-        if (p.residual) rr[i] = raw_load_rw<TR, VEC>(static_cast<const TR*>(p.residual) + at + c);
-      }
-    }
+    for (int i = 0; i < NV; ++i)
+      rr[i] = raw_load_rw<TR, VEC>(res + clamped<VEC>((i * tpr + lane) * VEC, dim));
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = (i * tpr + lane) * VEC;
-      if (c < dim) {
-        widen<VEC>(xr[i], f[i]);
-        if (p.residual) {
-          float g[VEC];
-          widen<VEC>(rr[i], g);
+      float g[VEC];
+      widen<VEC>(xr[i], f[i]);
+      widen<VEC>(rr[i], g);
 #pragma unroll
-          for (int v = 0; v < VEC; ++v) f[i][v] += g[v];
-          Raw<TR, VEC> o;
-          narrow<VEC>(f[i], o);
-          raw_store<TR, VEC>(static_cast<TR*>(p.r) + at + c, o);
-          widen<VEC>(o, f[i]);  // as stored
-        }
-      } else {
-#pragma unroll
-        for (int v = 0; v < VEC; ++v) f[i][v] = 0.f;
-      }
+      for (int v = 0; v < VEC; ++v) f[i][v] += g[v];
+      Raw<TR, VEC> o;
+      narrow<VEC>(f[i], o);
+      if (on && c < dim) raw_store<TR, VEC>(out + c, o);
+      widen<VEC>(o, f[i]);  // as stored
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-      for (int v = 0; v < VEC; ++v) f[i][v] = 0.f;
+    for (int i = 0; i < NV; ++i) widen<VEC>(xr[i], f[i]);
   }
   const float inv = 1.f / static_cast<float>(dim);
   float mean = 0.f;
   if (!p.rms) {
     float a = 0.f;
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
+    for (int i = 0; i < NV; ++i) {
+      const bool in = (i * tpr + lane) * VEC < dim;
 #pragma unroll
-      for (int v = 0; v < VEC; ++v) a += f[i][v];
-    mean = row_sum(a, wpr, red[0]) * inv;
+      for (int v = 0; v < VEC; ++v) a += in ? f[i][v] : 0.f;
+    }
+    mean = row_sum(a, tpr, red[0]) * inv;
   }
   float q = 0.f;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    if ((i * tpr + lane) * VEC < dim) {
+    const bool in = (i * tpr + lane) * VEC < dim;
 #pragma unroll
-      for (int v = 0; v < VEC; ++v) {
-        f[i][v] -= mean;
-        q = fmaf(f[i][v], f[i][v], q);
-      }
+    for (int v = 0; v < VEC; ++v) {
+      f[i][v] -= mean;
+      q = fmaf(in ? f[i][v] : 0.f, f[i][v], q);
     }
   }
-  const float rstd = rsqrtf(row_sum(q, wpr, red[1]) * inv + p.eps);
+  const float rstd = rsqrtf(row_sum(q, tpr, red[1]) * inv + p.eps);
   if (!on) return;
   if (p.stats && lane == 0) {
     p.stats[row] = mean;
     p.stats[p.rows + row] = rstd;
   }
+  TX* y = static_cast<TX*>(p.y) + at;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    float w[VEC];
+    load_f<float, VEC>(p.weight + clamped<VEC>((i * tpr + lane) * VEC, dim), w);
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) f[i][v] *= rstd * w[v];
+  }
+  if (p.bias) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      float b[VEC];
+      load_f<float, VEC>(p.bias + clamped<VEC>((i * tpr + lane) * VEC, dim), b);
+#pragma unroll
+      for (int v = 0; v < VEC; ++v) f[i][v] += b[v];
+    }
+  }
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int c = (i * tpr + lane) * VEC;
-    if (c < dim) {
-      float w[VEC], b[VEC];
-      load_f<float, VEC>(p.weight + c, w);
-      if (p.bias) load_f<float, VEC>(p.bias + c, b);
-#pragma unroll
-      for (int v = 0; v < VEC; ++v) {
-        f[i][v] *= rstd * w[v];
-        if (p.bias) f[i][v] += b[v];
-      }
-      store_f<TX, VEC>(static_cast<TX*>(p.y) + at + c, f[i]);
-    }
+    if (c < dim) store_f<TX, VEC>(y + c, f[i]);
   }
 }
 
+// A row's operands of one thread, as loaded.
+template <typename TX, typename TR, int VEC, int NV>
+struct RowRaw {
+  Raw<TR, VEC> r[NV], dr[NV];
+  Raw<TX, VEC> dy[NV];
+  float mean, rstd;
+};
+
+// The loads of the next row are in flight while a row is reduced and written.
 template <typename TX, typename TR, int VEC, int NV, int THREADS>
-__global__ void __launch_bounds__(THREADS) norm_bwd_kernel(const NormBwdParams p, int tpr) {
+__global__ void __launch_bounds__(THREADS, bwd_ctas_per_sm(THREADS))
+    norm_bwd_kernel(const NormBwdParams p, int tpr) {
   __shared__ float2 red[2][32];
   __shared__ float acc[THREADS * VEC];
   const int wpr = tpr >> 5, groups = THREADS / tpr;
   const int group = threadIdx.x / tpr, lane = threadIdx.x & (tpr - 1);
   const int dim = static_cast<int>(p.dim);
   const float inv = 1.f / static_cast<float>(dim);
-  float w[NV][VEC], dw[NV][VEC], db[NV][VEC];
+  const bool has_dr = p.dr != nullptr;
+  constexpr bool kHoldW = NV * VEC == kBwdPer;  // wider rows read the weight again per row
+  float w[kHoldW ? NV : 1][VEC], dw[NV][VEC], db[NV][VEC];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int c = (i * tpr + lane) * VEC;
+    if constexpr (kHoldW)
+      load_f<float, VEC>(p.weight + clamped<VEC>((i * tpr + lane) * VEC, dim), w[i]);
 #pragma unroll
-    for (int v = 0; v < VEC; ++v) w[i][v] = dw[i][v] = db[i][v] = 0.f;
-    if (c < dim) load_f<float, VEC>(p.weight + c, w[i]);
+    for (int v = 0; v < VEC; ++v) dw[i][v] = db[i][v] = 0.f;
   }
   release_next();
+  const auto load = [&](RowRaw<TX, TR, VEC, NV>& x, int64_t row) {
+    if (row >= p.rows) return;
+    const int64_t at = row * p.dim;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int64_t o = at + clamped<VEC>((i * tpr + lane) * VEC, dim);
+      x.r[i] = raw_load<TR, VEC>(static_cast<const TR*>(p.r) + o);
+      x.dy[i] = raw_load<TX, VEC>(static_cast<const TX*>(p.dy) + o);
+    }
+    if (has_dr) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        x.dr[i] = raw_load<TR, VEC>(static_cast<const TR*>(p.dr) + at +
+                                    clamped<VEC>((i * tpr + lane) * VEC, dim));
+    }
+    x.mean = p.rms ? 0.f : __ldg(p.stats + row);
+    x.rstd = __ldg(p.stats + p.rows + row);
+  };
   int buf = 0;
   const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
+  RowRaw<TX, TR, VEC, NV> next = {};
+  load(next, static_cast<int64_t>(blockIdx.x) * groups + group);
   for (int64_t base = static_cast<int64_t>(blockIdx.x) * groups; base < p.rows; base += step) {
     const int64_t row = base + group;
     const bool on = row < p.rows;
     const int64_t at = row * p.dim;
+    const float mean = next.mean, rstd = next.rstd;
     float xh[NV][VEC], g[NV][VEC];
-    Raw<TR, VEC> rr[NV], er[NV];
-    Raw<TX, VEC> gr[NV];
-    float mean = 0.f, rstd = 0.f;
-    if (on) {
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int c = (i * tpr + lane) * VEC;
-        if (c < dim) {
-          rr[i] = raw_load<TR, VEC>(static_cast<const TR*>(p.r) + at + c);
-          gr[i] = raw_load<TX, VEC>(static_cast<const TX*>(p.dy) + at + c);
-          if (p.dr) er[i] = raw_load<TR, VEC>(static_cast<const TR*>(p.dr) + at + c);
-        }
-      }
-      mean = p.rms ? 0.f : __ldg(p.stats + row);
-      rstd = __ldg(p.stats + p.rows + row);
-    }
+    Raw<TR, VEC> er[NV];
     float2 a = make_float2(0.f, 0.f);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      if (on && (i * tpr + lane) * VEC < dim) {
-        widen<VEC>(rr[i], xh[i]);
-        widen<VEC>(gr[i], g[i]);
+      const bool in = on && (i * tpr + lane) * VEC < dim;
+      widen<VEC>(next.r[i], xh[i]);
+      widen<VEC>(next.dy[i], g[i]);
+      er[i] = next.dr[i];
+      float wi[VEC];
+      if constexpr (kHoldW) {
 #pragma unroll
-        for (int v = 0; v < VEC; ++v) {
-          xh[i][v] = (xh[i][v] - mean) * rstd;
-          db[i][v] += g[i][v];
-          dw[i][v] = fmaf(g[i][v], xh[i][v], dw[i][v]);
-          g[i][v] *= w[i][v];
-          a.x += g[i][v];
-          a.y = fmaf(g[i][v], xh[i][v], a.y);
-        }
+        for (int v = 0; v < VEC; ++v) wi[v] = w[i][v];
+      } else {
+        load_f<float, VEC>(p.weight + clamped<VEC>((i * tpr + lane) * VEC, dim), wi);
+      }
+#pragma unroll
+      for (int v = 0; v < VEC; ++v) {
+        xh[i][v] = in ? (xh[i][v] - mean) * rstd : 0.f;
+        g[i][v] = in ? g[i][v] : 0.f;
+        db[i][v] += g[i][v];
+        dw[i][v] = fmaf(g[i][v], xh[i][v], dw[i][v]);
+        g[i][v] *= wi[v];
+        a.x += g[i][v];
+        a.y = fmaf(g[i][v], xh[i][v], a.y);
       }
     }
+    load(next, row + step);
 #pragma unroll
     for (int m = 16; m >= 1; m /= 2) {
-      a.x += __shfl_xor_sync(0xffffffffu, a.x, m);
-      a.y += __shfl_xor_sync(0xffffffffu, a.y, m);
+      const float ox = __shfl_xor_sync(0xffffffffu, a.x, m);
+      const float oy = __shfl_xor_sync(0xffffffffu, a.y, m);
+      a.x += m < tpr ? ox : 0.f;
+      a.y += m < tpr ? oy : 0.f;
     }
     if (wpr > 1) {  // two buffers: a row's sums are read before the buffer's next writes
       const int warp = threadIdx.x >> 5;
@@ -210,22 +257,19 @@ __global__ void __launch_bounds__(THREADS) norm_bwd_kernel(const NormBwdParams p
       buf ^= 1;
     }
     const float mg = p.rms ? 0.f : a.x * inv, mx = a.y * inv;
-    if (on) {
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int c = (i * tpr + lane) * VEC;
-        if (c < dim) {
-          float o[VEC], e[VEC];
+    for (int i = 0; i < NV; ++i) {
+      const int c = (i * tpr + lane) * VEC;
+      float o[VEC], e[VEC];
+      widen<VEC>(er[i], e);
 #pragma unroll
-          for (int v = 0; v < VEC; ++v) o[v] = rstd * (g[i][v] - mg - xh[i][v] * mx);
-          if (p.dr) {
-            widen<VEC>(er[i], e);
-#pragma unroll
-            for (int v = 0; v < VEC; ++v) o[v] += e[v];
-          }
-          if (p.dx) store_f<TX, VEC>(static_cast<TX*>(p.dx) + at + c, o);
-          if (p.dresidual) store_f<TR, VEC>(static_cast<TR*>(p.dresidual) + at + c, o);
-        }
+      for (int v = 0; v < VEC; ++v) {
+        o[v] = rstd * (g[i][v] - mg - xh[i][v] * mx);
+        o[v] = has_dr ? o[v] + e[v] : o[v];
+      }
+      if (on && c < dim) {
+        store_f<TX, VEC>(static_cast<TX*>(p.dx) + at + c, o);
+        if (p.dresidual) store_f<TR, VEC>(static_cast<TR*>(p.dresidual) + at + c, o);
       }
     }
   }
@@ -273,9 +317,9 @@ __global__ void __launch_bounds__(1024) norm_bwd_sum_kernel(const float* partial
 
 bool fits(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
-// Threads per row, whole warps: at most `per` elements of the row per thread.
+// Threads per row, a power of two: at most `per` elements of the row per thread.
 int threads_per_row(int64_t dim, int per) {
-  int t = 32;
+  int t = 8;
   while (int64_t(t) * per < dim) t *= 2;
   return t;
 }
@@ -305,27 +349,31 @@ cudaError_t norm_fwd_t(const NormParams& p, cudaStream_t s) {
   return vec ? norm_fwd_v<TX, TR, V>(p, s) : norm_fwd_v<TX, TR, 1>(p, s);
 }
 
-constexpr int kBwdPer = 8;       // elements of a row per thread: 1024 threads hold kNormMaxDim
-constexpr int kBwdThreads = 256; // threads per CTA, for rows of up to that many threads
-constexpr int kBwdCtasPerSm = 4;
+int bwd_threads(int64_t dim) {
+  const int t = threads_per_row(dim, kBwdPer);
+  return t < 512 ? t : 512;
+}
 
 int64_t bwd_ctas(int64_t rows, int tpr) {
-  const int threads = tpr > kBwdThreads ? tpr : kBwdThreads;
+  const int threads = tpr > 128 ? tpr : 128;
   const int64_t groups = threads / tpr, need = (rows + groups - 1) / groups;
-  const int64_t most = int64_t(kSms) * kBwdCtasPerSm * kBwdThreads / threads;
+  const int64_t most = int64_t(kSms) * bwd_ctas_per_sm(threads);
   return need < most ? need : most;
 }
 
 template <typename TX, typename TR, int VEC>
 cudaError_t norm_bwd_v(const NormBwdParams& p, cudaStream_t s) {
   constexpr int NV = kBwdPer / VEC;
-  const int tpr = threads_per_row(p.dim, kBwdPer);
+  const int tpr = bwd_threads(p.dim);
   const unsigned g = static_cast<unsigned>(bwd_ctas(p.rows, tpr));
-  switch (tpr) {
-    case 512: norm_bwd_kernel<TX, TR, VEC, NV, 512><<<g, 512, 0, s>>>(p, tpr); break;
-    case 1024: norm_bwd_kernel<TX, TR, VEC, NV, 1024><<<g, 1024, 0, s>>>(p, tpr); break;
-    default: norm_bwd_kernel<TX, TR, VEC, NV, kBwdThreads><<<g, kBwdThreads, 0, s>>>(p, tpr);
-  }
+  if (p.dim > kBwdPer * 512)
+    norm_bwd_kernel<TX, TR, VEC, 2 * NV, 512><<<g, 512, 0, s>>>(p, tpr);
+  else if (tpr == 512)
+    norm_bwd_kernel<TX, TR, VEC, NV, 512><<<g, 512, 0, s>>>(p, tpr);
+  else if (tpr == 256)
+    norm_bwd_kernel<TX, TR, VEC, NV, 256><<<g, 256, 0, s>>>(p, tpr);
+  else
+    norm_bwd_kernel<TX, TR, VEC, NV, 128><<<g, 128, 0, s>>>(p, tpr);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   return launch_after(norm_bwd_sum_kernel,
@@ -351,7 +399,7 @@ cudaError_t launch_norm_fwd(const NormParams& p, bool bf16, bool residual_bf16, 
 }
 
 int64_t norm_bwd_partials(int64_t rows, int64_t dim) {
-  return bwd_ctas(rows, threads_per_row(dim, kBwdPer));
+  return bwd_ctas(rows, bwd_threads(dim));
 }
 
 cudaError_t launch_norm_bwd(const NormBwdParams& p, bool bf16, bool residual_bf16,
