@@ -45,7 +45,11 @@ constexpr int kBk = 64;                  // K per stage
 constexpr int kStages = 6;
 constexpr uint32_t kOperand = kHalfTile * kBk * 2;  // 16 KB: a CTA's A or B of a stage
 constexpr uint32_t kStage = 2 * kOperand;
-constexpr uint32_t kSmem = kStages * kStage + 1024 + 256;  // ring, alignment slack, barriers
+constexpr uint32_t kBox = 32 * 128;      // 4 KB: a warp's 32 rows of 128 bytes on their way out
+constexpr uint32_t kOut = kStages * kStage;  // two boxes per epilogue warp
+constexpr uint32_t kBars = kOut + 4 * 2 * kBox;
+constexpr uint32_t kSmem = kBars + 256 + 1024;  // ring, boxes, barriers, alignment slack
+static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
 constexpr int kThreads = 192;
 constexpr int kEpilogueWarps = 4;
 constexpr uint64_t kWaitNs = 2000000000ull;  // a wait gives up after 2 s
@@ -69,11 +73,8 @@ struct GemmArgs {
   float2* part;           // kLse: [tiles of columns][part_pitch] maximum (log2 units), sum
   int64_t part_pitch;
   float* target_logit;    // kLse: [rows]
-  __nv_bfloat16* g;       // kGrad: the piece of G, [rows][g_pitch]
-  int64_t g_pitch;
   float* dh;              // kProducts: [splits][rows, whole tiles][dim] partial sums
   bool add;               // kProducts: add to dh (a later piece) rather than store
-  __nv_bfloat16* dw;      // kProducts: [vocab][dim]
   unsigned* err;
 };
 
@@ -81,8 +82,10 @@ struct GemmArgs {
 // of 128 rows; kProducts uses a = G (128-row boxes) and b = W (64-row boxes) for
 // dh, at = G and bt = the rows of h (64-row boxes) for dW.  h is the same as
 // the rows' map, over h itself: with no token ignored nothing is gathered.
+// Results leave in boxes of 32 rows: g = the piece of G (kGrad), dw and dh
+// (kProducts).
 struct Maps {
-  CUtensorMap a, b, at, bt, h;
+  CUtensorMap a, b, at, bt, h, g, dw, dh;
 };
 
 __device__ __forceinline__ int rows_of(const GemmArgs& p) {
@@ -104,7 +107,8 @@ __host__ __device__ inline int ceil_div(int64_t a, int64_t b) {
 // (kv stages), so that all pieces add into the same partial sums.
 __host__ __device__ inline int dh_splits(int mt, int nt, int kv) {
   const int tiles = mt * nt > 0 ? mt * nt : 1;
-  const int s = (kClusters + tiles - 1) / tiles;
+  int s = kClusters / tiles;
+  if (s < 1) s = 1;
   return s < kv ? s : kv;
 }
 
@@ -114,10 +118,16 @@ struct Unit {
   bool dw;
 };
 
+// The units of one cluster, in order: its dh tiles, then its dW tiles.  Tiles are
+// dealt out in turn; where the dh tiles do not come out even, the clusters with
+// one fewer take the dW tiles that make up for it first.
 template <int MODE>
 struct Work {
-  int mt, nt, vt, kv, kt, units, ndh, splits;
-  __device__ explicit Work(const GemmArgs& p) {
+  int mt, nt, vt, kv, kt, splits;
+  int ndh, ndw;              // units of either kind (kLse and kGrad: all are "dh")
+  int cluster, clusters;
+  int heavy, light, ahead;   // clusters with a dh unit more, without, dW units these take first
+  __device__ Work(const GemmArgs& p, int c, int n) : cluster(c), clusters(n) {
     const int rows = rows_of(p);
     mt = ceil_div(rows, kTile);
     vt = ceil_div(p.vp, kTile);
@@ -125,24 +135,42 @@ struct Work {
     kv = ceil_div(p.vp, kBk);
     kt = MODE == kProducts ? ceil_div(rows, kBk) : ceil_div(p.dim, kBk);
     splits = MODE == kProducts ? dh_splits(mt, nt, p.kv_whole) : 1;
-    ndh = MODE == kProducts ? mt * nt * splits : 0;
-    units = MODE == kProducts ? ndh + vt * nt : mt * nt;
-  }
-  __device__ Unit at(int u) const {
-    Unit r;
-    if (MODE != kProducts) {
-      r.m = u % mt; r.n = u / mt; r.k0 = 0; r.k1 = kt; r.split = 0; r.dw = false;
-    } else if (u < ndh) {
-      r.n = u % nt;
-      const int q = u / nt;
-      r.m = q % mt; r.split = q / mt; r.dw = false;
-      r.k0 = static_cast<int>(static_cast<int64_t>(kv) * r.split / splits);
-      r.k1 = static_cast<int>(static_cast<int64_t>(kv) * (r.split + 1) / splits);
-    } else {
-      r.n = (u - ndh) % nt; r.m = (u - ndh) / nt; r.split = 0; r.dw = true;
-      r.k0 = 0; r.k1 = kt;
+    ndh = mt * nt * splits;
+    ndw = MODE == kProducts ? vt * nt : 0;
+    heavy = ndh % clusters;
+    light = clusters - heavy;
+    ahead = 0;
+    if (MODE == kProducts && heavy > 0 && kt > 0) {
+      ahead = kv / splits / kt;
+      if (ahead > ndw / light) ahead = ndw / light;
     }
-    return r;
+  }
+  // The cluster's i-th unit; false past its last.
+  __device__ bool at(int i, Unit* r) const {
+    const int u = cluster + i * clusters;
+    if (u < ndh) {
+      r->split = 0; r->dw = false; r->k0 = 0; r->k1 = kt;
+      if (MODE != kProducts) {
+        r->m = u % mt; r->n = u / mt;
+        return true;
+      }
+      const int q = u / nt;
+      r->n = u % nt; r->m = q % mt; r->split = q / mt;
+      r->k0 = static_cast<int>(static_cast<int64_t>(kv) * r->split / splits);
+      r->k1 = static_cast<int>(static_cast<int64_t>(kv) * (r->split + 1) / splits);
+      return true;
+    }
+    if (MODE != kProducts) return false;
+    int j = i - (ndh / clusters + (cluster < heavy ? 1 : 0)), w;
+    if (cluster >= heavy && j < ahead) {
+      w = cluster - heavy + j * light;
+    } else {
+      if (cluster >= heavy) j -= ahead;
+      w = ahead * light + cluster + j * clusters;
+    }
+    if (w >= ndw) return false;
+    r->n = w % nt; r->m = w / nt; r->split = 0; r->dw = true; r->k0 = 0; r->k1 = kt;
+    return true;
   }
 };
 
@@ -156,11 +184,47 @@ __device__ __forceinline__ uint64_t desc(uint32_t tile, int j, bool mn) {
                      : umma::smem_desc(tile + j * 32, 16, 1024));
 }
 
-__device__ __forceinline__ void store32(void* p, const uint32_t* r) {
-  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(r[0]), "r"(r[1]),
-               "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-               : "memory");
-}
+// A box of 32 rows x 128 bytes in shared memory, a row per lane, leaves by one
+// copy (or one elementwise addition) of the warp.  Two boxes alternate: a box is
+// written again once the copy before the last has read it.
+struct OutBox {
+  uint32_t base;
+  int n;
+  __device__ __forceinline__ void open() {
+    if ((threadIdx.x & 31) == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+    __syncwarp();
+  }
+  __device__ __forceinline__ void put(int chunk, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    const int lane = threadIdx.x & 31;
+    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(
+                     base + (n & 1) * kBox + lane * 128 + ((chunk ^ (lane & 7)) << 4)),
+                 "r"(a), "r"(b), "r"(c), "r"(d)
+                 : "memory");
+  }
+  __device__ __forceinline__ void send(const CUtensorMap* map, int x, int y, bool add) {
+    umma::fence_smem_to_async();
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) {
+      const uint32_t box = base + (n & 1) * kBox;
+      if (add)
+        asm volatile(
+            "cp.reduce.async.bulk.tensor.2d.global.shared::cta.add.bulk_group [%0, {%1, %2}], [%3];"
+            ::"l"(map), "r"(x), "r"(y), "r"(box)
+            : "memory");
+      else
+        asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];"
+                     ::"l"(map), "r"(x), "r"(y), "r"(box)
+                     : "memory");
+      asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+    }
+    ++n;
+  }
+  __device__ __forceinline__ void drain() {
+    if ((threadIdx.x & 31) == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    __syncwarp();
+  }
+};
+
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);
@@ -206,82 +270,88 @@ __device__ __forceinline__ void epilogue_lse(const GemmArgs& p, uint32_t acc, in
   p.part[static_cast<int64_t>(n) * p.part_pitch + row] = make_float2(m, l);
 }
 
-__device__ __forceinline__ void epilogue_grad(const GemmArgs& p, uint32_t acc, int64_t row, int n,
-                                              int tgt, float lse2, float scale) {
+__device__ __forceinline__ void epilogue_grad(const GemmArgs& p, const Maps& maps, OutBox& out,
+                                              uint32_t acc, int row0, int n, int tgt, float lse2,
+                                              float scale) {
   const int c0 = n * kTile;
   const int cols = p.vp - c0 < kTile ? p.vp - c0 : kTile;
   const int64_t t64 = static_cast<int64_t>(tgt) - p.v0 - c0;
   const int rel = t64 >= 0 && t64 < kTile ? static_cast<int>(t64) : -1;
-  __nv_bfloat16* out = p.g + row * p.g_pitch + c0;
-  for (int c = 0; c < kTile; c += 32) {
-    uint32_t r[32];
+  for (int c = 0; c < kTile; c += 64) {
+    uint32_t r[2][32];
     __syncwarp();
-    umma::tmem_ld32_async(acc + c, r);
-    umma::tmem_wait_ld(r);
-    float v[32];
+    umma::tmem_ld32_async(acc + c, r[0]);
+    umma::tmem_ld32_async(acc + c + 32, r[1]);
+    out.open();
+    umma::tmem_wait_ld(r[0]);
+    umma::tmem_wait_ld(r[1]);
 #pragma unroll
-    for (int j = 0; j < 32; ++j) v[j] = ex2(fmaf(__uint_as_float(r[j]), kLog2e, -lse2));
-    if (rel >= c && rel < c + 32) {
+    for (int h = 0; h < 2; ++h) {
+      const int b = c + 32 * h;
+      float v[32];
 #pragma unroll
-      for (int j = 0; j < 32; ++j) v[j] -= c + j == rel ? 1.f : 0.f;
+      for (int j = 0; j < 32; ++j) v[j] = ex2(fmaf(__uint_as_float(r[h][j]), kLog2e, -lse2));
+      if (static_cast<unsigned>(rel - b) < 32u) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] -= b + j == rel ? 1.f : 0.f;
+      }
+#pragma unroll
+      for (int j = 0; j < 32; ++j) v[j] *= scale;
+      if (b + 32 > cols) {  // columns past the vocabulary take no part in dh
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] = b + j < cols ? v[j] : 0.f;
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        out.put(4 * h + k, pack2(v[8 * k], v[8 * k + 1]), pack2(v[8 * k + 2], v[8 * k + 3]),
+                pack2(v[8 * k + 4], v[8 * k + 5]), pack2(v[8 * k + 6], v[8 * k + 7]));
     }
-#pragma unroll
-    for (int j = 0; j < 32; ++j) v[j] *= scale;
-    if (c + 32 > cols) {  // columns past the vocabulary take no part in dh
-#pragma unroll
-      for (int j = 0; j < 32; ++j) v[j] = c + j < cols ? v[j] : 0.f;
-    }
-    uint32_t w[16];
-#pragma unroll
-    for (int j = 0; j < 16; ++j) w[j] = pack2(v[2 * j], v[2 * j + 1]);
-    store32(out + c, w);
-    store32(out + c + 16, w + 8);
+    out.send(&maps.g, c0 + c, row0, false);
   }
 }
 
-__device__ __forceinline__ void epilogue_products(const GemmArgs& p, uint32_t acc, const Unit& u,
-                                                  int row, int mt, bool empty) {
-  const int64_t c0 = static_cast<int64_t>(u.n) * kTile;
+// `row`: the warp's first row in the tile.
+__device__ __forceinline__ void epilogue_products(const GemmArgs& p, const Maps& maps, OutBox& out,
+                                                  uint32_t acc, const Unit& u, int row, int mt,
+                                                  bool empty) {
+  const int c0 = u.n * kTile;
   const int cols = p.dim - c0 < kTile ? static_cast<int>(p.dim - c0) : kTile;
-  const int64_t vrow = p.v0 + static_cast<int64_t>(u.m) * kTile + row;
-  const bool on = !u.dw || vrow < p.v0 + p.vp;
-  float* dh = p.dh + ((static_cast<int64_t>(u.split) * mt + u.m) * kTile + row) * p.dim + c0;
-  __nv_bfloat16* dw = p.dw + vrow * p.dim + c0;
-  for (int c = 0; c < cols; c += 32) {
-    uint32_t r[32];
+  const int64_t y = u.dw ? p.v0 + static_cast<int64_t>(u.m) * kTile + row
+                         : (static_cast<int64_t>(u.split) * mt + u.m) * kTile + row;
+  if (u.dw ? y >= p.vocab : empty && p.add) return;  // nothing to write, or to add
+  const int width = u.dw ? 64 : 32;
+  for (int c = 0; c < cols; c += width) {
+    uint32_t r[2][32];
     __syncwarp();
-    if (!empty) {
-      umma::tmem_ld32_async(acc + c, r);
-      umma::tmem_wait_ld(r);
-    } else {
 #pragma unroll
-      for (int j = 0; j < 32; ++j) r[j] = 0u;
-    }
-    if (!on) continue;
+    for (int h = 0; h < 2; ++h) {
+      if (empty) {
 #pragma unroll
-    for (int j = 0; j < 32; j += 8) {  // dim is a multiple of 8: groups of 8 are whole
-      if (c + j < cols) {
-        float v[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[j + i]);
-        if (u.dw) {
-          *reinterpret_cast<uint4*>(dw + c + j) = make_uint4(pack2(v[0], v[1]), pack2(v[2], v[3]),
-                                                             pack2(v[4], v[5]), pack2(v[6], v[7]));
-        } else {
-          float* o = dh + c + j;
-          if (p.add) {
-            const float4 a = reinterpret_cast<const float4*>(o)[0];
-            const float4 b = reinterpret_cast<const float4*>(o)[1];
-            v[0] += a.x; v[1] += a.y; v[2] += a.z; v[3] += a.w;
-            v[4] += b.x; v[5] += b.y; v[6] += b.z; v[7] += b.w;
-          }
-          uint32_t w[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(v[i]);
-          store32(o, w);
-        }
+        for (int j = 0; j < 32; ++j) r[h][j] = 0u;
+      } else if (h == 0 || u.dw) {
+        umma::tmem_ld32_async(acc + c + 32 * h, r[h]);
       }
     }
+    out.open();
+    umma::tmem_wait_ld(r[0]);
+    umma::tmem_wait_ld(r[1]);
+    if (u.dw) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          uint32_t w[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            w[i] = pack2(__uint_as_float(r[h][8 * k + 2 * i]), __uint_as_float(r[h][8 * k + 2 * i + 1]));
+          out.put(4 * h + k, w[0], w[1], w[2], w[3]);
+        }
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        out.put(k, r[0][4 * k], r[0][4 * k + 1], r[0][4 * k + 2], r[0][4 * k + 3]);
+    }
+    out.send(u.dw ? &maps.dw : &maps.dh, c0 + c, static_cast<int>(y), !u.dw && p.add);
   }
 }
 
@@ -290,7 +360,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     xent_gemm_kernel(const __grid_constant__ Maps maps, const GemmArgs p) {
   extern __shared__ unsigned char sm_raw[];
   const uint32_t base = (umma::smem_u32(sm_raw) + 1023u) & ~1023u;
-  const uint32_t bars = base + kStages * kStage;
+  const uint32_t bars = base + kBars;
   const auto full = [&](int s) { return bars + 8 * s; };
   const auto empty = [&](int s) { return bars + 8 * (kStages + s); };
   const auto acc_full = [&](int b) { return bars + 8 * (2 * kStages + b); };
@@ -298,7 +368,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const uint32_t slot = bars + 8 * (2 * kStages + 4);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = pair::cluster_rank();
-  const int first = blockIdx.x >> 1, step = gridDim.x >> 1;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
@@ -319,7 +388,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   asm volatile("ld.shared.u32 %0, [%1];" : "=r"(tm) : "r"(slot) : "memory");
   wait_previous();
   release_next();
-  const Work<MODE> work(p);
+  const Work<MODE> work(p, blockIdx.x >> 1, gridDim.x >> 1);
 
   bool bad = false;
   if (warp == 0 && lane == 0) {
@@ -330,8 +399,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const bool all = rows_of(p) == p.tokens;
     const CUtensorMap* ma_map = MODE != kProducts && all ? &maps.h : &maps.a;
     const CUtensorMap* bt_map = all ? &maps.h : &maps.bt;
-    for (int u = first; u < work.units && !bad; u += step) {
-      const Unit t = work.at(u);
+    Unit t;
+    for (int i = 0; !bad && work.at(i, &t); ++i) {
       const int ma = t.m * kTile + rank * kHalfTile, nb = t.n * kTile + rank * kHalfTile;
       const int v0 = static_cast<int>(p.v0);
       for (int k = t.k0; k < t.k1; ++k) {
@@ -374,8 +443,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // ---- products
     int s = 0, n = 0;
     uint32_t ph = 0;
-    for (int u = first; u < work.units && !bad; u += step, ++n) {
-      const Unit t = work.at(u);
+    Unit t;
+    for (; !bad && work.at(n, &t); ++n) {
       const int b = n & 1;
       const bool a_mn = t.dw, b_mn = MODE == kProducts;
       const uint32_t id = umma::idesc_bf16(kTile, kTile, a_mn, b_mn);
@@ -404,9 +473,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // ---- epilogue: warp w reads TMEM lanes 32 (w mod 4) ..
     const int q = warp & 3;
     const int row = static_cast<int>(rank) * kHalfTile + q * 32 + lane;
-    int n = 0;
-    for (int u = first; u < work.units && !bad; u += step, ++n) {
-      const Unit t = work.at(u);
+    OutBox out = {base + kOut + (warp - 2) * 2 * kBox, 0};
+    Unit t;
+    for (int n = 0; !bad && work.at(n, &t); ++n) {
       const int b = n & 1;
       const int64_t r = static_cast<int64_t>(t.m) * kTile + row;
       int tgt = -1;
@@ -424,12 +493,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       umma::fence_after_sync();
       const uint32_t acc = tm + b * kTile + (static_cast<uint32_t>(q * 32) << 16);
       if (MODE == kLse) epilogue_lse(p, acc, r, t.n, tgt);
-      if (MODE == kGrad) epilogue_grad(p, acc, r, t.n, tgt, lse2, scale);
-      if (MODE == kProducts) epilogue_products(p, acc, t, row, work.mt, t.k1 <= t.k0);
+      if (MODE == kGrad)
+        epilogue_grad(p, maps, out, acc, static_cast<int>(r) - lane, t.n, tgt, lse2, scale);
+      if (MODE == kProducts)
+        epilogue_products(p, maps, out, acc, t, row - lane, work.mt, t.k1 <= t.k0);
+      __syncwarp();
       umma::fence_before_sync();
       __syncwarp();
       if (lane == 0) pair::mbar_arrive(pair::map_to(acc_empty(b), 0));
     }
+    out.drain();
   }
   if (bad) atomicOr(p.err, kErrXentWait);
   __syncwarp();
@@ -646,7 +719,7 @@ __global__ void __launch_bounds__(256) xent_dh_kernel(const GemmArgs p, const in
 // ---- workspace and launches -------------------------------------------------------
 struct Layout {
   size_t count, idx, target, target_logit, lse, scale, rows, part, g, dh, total;
-  int64_t tpad, piece, pieces;
+  int64_t tpad, piece, pieces, dh_rows;
 };
 
 Layout layout_of(const XentShape& s, bool backward) {
@@ -670,6 +743,7 @@ Layout layout_of(const XentShape& s, bool backward) {
   l.target = take(4 * l.tpad);
   l.rows = take(2 * l.tpad * s.dim);
   l.target_logit = l.part = l.lse = l.scale = l.g = l.dh = 0;
+  l.dh_rows = 0;
   if (!backward) {
     l.target_logit = take(4 * l.tpad);
     l.part = take(sizeof(float2) * (vpad / kTile) * l.tpad);
@@ -679,7 +753,8 @@ Layout layout_of(const XentShape& s, bool backward) {
     l.g = take(2 * l.tpad * l.piece);
     // splits x rows: with fewer tiles than clusters the splits fill the clusters
     const int64_t nt = (s.dim + kTile - 1) / kTile;
-    l.dh = take(4 * (l.tpad + ((kClusters + nt - 1) / nt) * kTile) * s.dim);
+    l.dh_rows = l.tpad + ((kClusters + nt - 1) / nt) * kTile;
+    l.dh = take(4 * l.dh_rows * s.dim);
   }
   l.total = off;
   return l;
@@ -775,18 +850,19 @@ cudaError_t launch_xent_bwd(const XentParams& p, cudaStream_t s) {
   GemmArgs a = gemm_args(p, l, ws);
   a.lse = g.lse_rows;
   a.scale = g.scale;
-  a.g = reinterpret_cast<__nv_bfloat16*>(ws + l.g);
-  a.g_pitch = l.piece;
+  void* piece = ws + l.g;
   a.dh = reinterpret_cast<float*>(ws + l.dh);
   a.kv_whole = ceil_div(l.piece, kBk);
-  a.dw = static_cast<__nv_bfloat16*>(p.dweight);
   Maps in = {}, out = {};
   if (!map_bf16_sw128(&in.a, g.rows, z.dim, l.tpad, z.dim, kHalfTile) ||
       !map_bf16_sw128(&in.h, p.h, z.dim, z.tokens, z.dim, kHalfTile) ||
       !map_bf16_sw128(&in.b, p.weight, z.dim, z.vocab, z.dim, kHalfTile) ||
-      !map_bf16_sw128(&out.a, a.g, l.piece, l.tpad, l.piece, kHalfTile) ||
+      !map_bf16_sw128(&in.g, piece, l.piece, l.tpad, l.piece, 32) ||
+      !map_bf16_sw128(&out.dw, p.dweight, z.dim, z.vocab, z.dim, 32) ||
+      !map_f32_sw128(&out.dh, a.dh, z.dim, l.dh_rows, z.dim, 32) ||
+      !map_bf16_sw128(&out.a, piece, l.piece, l.tpad, l.piece, kHalfTile) ||
       !map_bf16_sw128(&out.b, p.weight, z.dim, z.vocab, z.dim, kBk) ||
-      !map_bf16_sw128(&out.at, a.g, l.piece, l.tpad, l.piece, kBk) ||
+      !map_bf16_sw128(&out.at, piece, l.piece, l.tpad, l.piece, kBk) ||
       !map_bf16_sw128(&out.bt, g.rows, z.dim, l.tpad, z.dim, kBk) ||
       !map_bf16_sw128(&out.h, p.h, z.dim, z.tokens, z.dim, kBk))
     return cudaErrorInvalidValue;

@@ -11,7 +11,6 @@ PyTorch stream without it.
 from __future__ import annotations
 
 import ctypes
-import functools
 
 import torch
 
@@ -45,27 +44,29 @@ def _new(out, name, shape, dtype, dev):
             else _dense(out, name, shape, dtype, dev))
 
 
+def _like(out, name, t, shape, dev):
+    """`out`, checked, or a new contiguous tensor of t's type."""
+    if out is not None:
+        return _dense(out, name, shape, t.dtype, dev)
+    return torch.empty_like(t) if t.is_contiguous() else torch.empty(shape, dtype=t.dtype, device=dev)
+
+
 def _addr(t):
     return None if t is None else t.data_ptr()
 
 
-def _on_stream(f):
-    """The call's tensors are allocated where they are used: with ``stream=``
-    given, the whole call runs with it as PyTorch's current stream, so that no
-    output or workspace takes memory another stream may still be using."""
-    @functools.wraps(f)
-    def call(t, *args, stream=None, **kw):
-        if stream is None:
-            return f(t, *args, **kw)
-        dev = _cuda(t, "the first argument")
-        if not hasattr(stream, "cuda_stream"):
-            stream = (torch.cuda.ExternalStream(int(stream), device=dev) if int(stream)
-                      else torch.cuda.default_stream(dev))
-        if stream.device != dev:
-            raise ValueError(f"stream: on {stream.device}, expected {dev}")
-        with torch.cuda.stream(stream):
-            return f(t, *args, **kw)
-    return call
+def _on_stream(stream, f, t, *args, **kw):
+    """f(t, *args, **kw) with `stream` (or its handle) as PyTorch's current
+    stream: the call's outputs and workspaces are then allocated where they are
+    used, and take no memory that another stream may still be using."""
+    dev = _cuda(t, "the first argument")
+    if not hasattr(stream, "cuda_stream"):
+        stream = (torch.cuda.ExternalStream(int(stream), device=dev) if int(stream)
+                  else torch.cuda.default_stream(dev))
+    if stream.device != dev:
+        raise ValueError(f"stream: on {stream.device}, expected {dev}")
+    with torch.cuda.stream(stream):
+        return f(t, *args, **kw)
 
 
 def _call(fn, dev, *args):
@@ -114,9 +115,8 @@ def _conv_args(x, weight, bias, silu, rank):
         batch, seqlen, dim, width, stride[0] if batch > 1 else dim, step, 1 if silu else 0)
 
 
-@_on_stream
 def conv_fwd(x, weight, bias=None, valid_len=None, *, state0=None, silu: bool = True,
-             want_final: bool = False, out=None, out_final=None):
+             want_final: bool = False, out=None, out_final=None, stream=None):
     """The short causal convolution of every channel along time.
 
     x: [batch, L, dim], fp32 or bf16, channels contiguous; rows may be strided
@@ -127,12 +127,15 @@ def conv_fwd(x, weight, bias=None, valid_len=None, *, state0=None, silu: bool = 
     ``silu`` the result is silu(pre).  Returns y [batch, L, dim], or
     ``(y, final)`` with ``want_final``, final [batch, width - 1, dim] being the
     last valid steps, from which a next call or ``conv_step`` continues."""
+    if stream is not None:
+        return _on_stream(stream, conv_fwd, x, weight, bias, valid_len, state0=state0, silu=silu,
+                          want_final=want_final, out=out, out_final=out_final)
     dev, code, (batch, L, dim, width), shapes = _conv_args(x, weight, bias, silu, 3)
     if valid_len is not None:
         _dense(valid_len, "valid_len", (batch,), torch.int32, dev)
     if state0 is not None:
         _dense(state0, "state0", (batch, width - 1, dim), x.dtype, dev)
-    y = _new(out, "out", (batch, L, dim), x.dtype, dev)
+    y = _like(out, "out", x, (batch, L, dim), dev)
     final = None
     if want_final or out_final is not None:
         final = _new(out_final, "out_final", (batch, width - 1, dim), x.dtype, dev)
@@ -141,13 +144,17 @@ def conv_fwd(x, weight, bias=None, valid_len=None, *, state0=None, silu: bool = 
     return y if final is None else (y, final)
 
 
-@_on_stream
 def conv_bwd(x, weight, bias=None, valid_len=None, *, dy, state0=None, silu: bool = True,
-             want_dbias: bool | None = None, want_dstate0: bool = False, workspace=None) -> dict:
+             want_dbias: bool | None = None, want_dstate0: bool = False, workspace=None,
+             stream=None) -> dict:
     """Every gradient of sum(dy * y) for ``conv_fwd`` on the same inputs: a dict
     of dx (like x, contiguous), dweight and dbias (fp32; dbias None without a
     bias, or as ``want_dbias`` says) and dstate0 (when wanted).  ``workspace``,
     a CUDA uint8 tensor, is allocated here when None."""
+    if stream is not None:
+        return _on_stream(stream, conv_bwd, x, weight, bias, valid_len, dy=dy, state0=state0,
+                          silu=silu, want_dbias=want_dbias, want_dstate0=want_dstate0,
+                          workspace=workspace)
     dev, code, (batch, L, dim, width), shapes = _conv_args(x, weight, bias, silu, 3)
     if valid_len is not None:
         _dense(valid_len, "valid_len", (batch,), torch.int32, dev)
@@ -170,16 +177,17 @@ def conv_bwd(x, weight, bias=None, valid_len=None, *, dy, state0=None, silu: boo
     return g
 
 
-@_on_stream
-def conv_step(x, weight, bias=None, *, state, silu: bool = True, out=None):
+def conv_step(x, weight, bias=None, *, state, silu: bool = True, out=None, stream=None):
     """One step of the convolution on a carried state, in place (decode).
 
     x: [batch, dim] (rows may be strided); state: like x, [batch, width - 1,
     dim], the last steps, oldest first (``conv_fwd``'s final state): the oldest
     leaves and x becomes the newest.  Returns y [batch, dim]."""
+    if stream is not None:
+        return _on_stream(stream, conv_step, x, weight, bias, state=state, silu=silu, out=out)
     dev, code, (batch, _, dim, width), shapes = _conv_args(x, weight, bias, silu, 2)
     _dense(state, "state", (batch, width - 1, dim), x.dtype, dev)
-    y = _new(out, "out", (batch, dim), x.dtype, dev)
+    y = _like(out, "out", x, (batch, dim), dev)
     _call(load().ssm_conv_step, dev, x.data_ptr(), weight.data_ptr(), _addr(bias),
           state.data_ptr(), y.data_ptr(), ctypes.byref(shapes), code)
     return y
@@ -197,9 +205,8 @@ def _rows(t):
     return t.numel() // t.shape[-1] if t.dim() and t.shape[-1] else 0
 
 
-@_on_stream
 def norm_fwd(x, weight, bias=None, *, residual=None, rms: bool = False, eps: float = 1e-5,
-             want_stats: bool = False, out=None, out_r=None):
+             want_stats: bool = False, out=None, out_r=None, stream=None):
     """The norm of the residual stream, with the addition that precedes it.
 
     x: [..., dim], fp32 or bf16, contiguous, dim up to 8192.  With ``residual``
@@ -209,6 +216,9 @@ def norm_fwd(x, weight, bias=None, *, residual=None, rms: bool = False, eps: flo
     ``(y, r, stats)``: y like x, r the sum (None without a residual; ``out_r``
     may be ``residual`` itself), stats fp32 [2, rows] with the means and the
     reciprocal standard deviations (None unless ``want_stats``)."""
+    if stream is not None:
+        return _on_stream(stream, norm_fwd, x, weight, bias, residual=residual, rms=rms, eps=eps,
+                          want_stats=want_stats, out=out, out_r=out_r)
     dev = _cuda(x, "x")
     code = _code(x.dtype)
     shape = x.shape
@@ -221,10 +231,10 @@ def norm_fwd(x, weight, bias=None, *, residual=None, rms: bool = False, eps: flo
     if residual is not None:
         rcode = _code(residual.dtype)
         _dense(residual, "residual", shape, residual.dtype, dev)
-        r = _new(out_r, "out_r", shape, residual.dtype, dev)
+        r = _like(out_r, "out_r", residual, shape, dev)
     elif out_r is not None:
         raise ValueError("out_r needs a residual")
-    y = _new(out, "out", shape, x.dtype, dev)
+    y = _like(out, "out", x, shape, dev)
     stats = torch.empty((2, rows), dtype=torch.float32, device=dev) if want_stats else None
     shapes = NormShapes(rows, dim, int(bool(rms)), eps, code, rcode)
     _call(load().ssm_norm_fwd, dev, x.data_ptr(), _addr(residual), weight.data_ptr(),
@@ -232,9 +242,8 @@ def norm_fwd(x, weight, bias=None, *, residual=None, rms: bool = False, eps: flo
     return y, r, stats
 
 
-@_on_stream
 def norm_bwd(r, weight, *, stats, dy, dr=None, rms: bool = False, want_dbias: bool = False,
-             workspace=None) -> dict:
+             workspace=None, stream=None) -> dict:
     """Every gradient of sum(dy * y) + sum(dr * r) for ``norm_fwd``.
 
     r: what was normalised (the forward's r, or x without a residual); stats:
@@ -242,6 +251,9 @@ def norm_bwd(r, weight, *, stats, dy, dr=None, rms: bool = False, want_dbias: bo
     residual stream (None for none).  Returns a dict: dx (dy's type), dresidual
     (r's type; the same tensor as dx when the types are equal), dweight and
     dbias (fp32; dbias None unless wanted)."""
+    if stream is not None:
+        return _on_stream(stream, norm_bwd, r, weight, stats=stats, dy=dy, dr=dr, rms=rms,
+                          want_dbias=want_dbias, workspace=workspace)
     dev = _cuda(r, "r")
     code, rcode = _code(dy.dtype), _code(r.dtype)
     shape = r.shape
@@ -283,8 +295,7 @@ def _xent_args(h, weight, targets, ignore_index):
     return dev, code, (tokens, vocab, dim), XentShapes(tokens, vocab, dim, int(ignore_index))
 
 
-@_on_stream
-def xent_fwd(h, weight, targets, *, ignore_index: int = -100, workspace=None):
+def xent_fwd(h, weight, targets, *, ignore_index: int = -100, workspace=None, stream=None):
     """Softmax cross entropy of every token over the vocabulary, from the hidden
     states, without keeping the logits h weight^T.
 
@@ -294,6 +305,9 @@ def xent_fwd(h, weight, targets, *, ignore_index: int = -100, workspace=None):
     ``xent_bwd`` needs.  Tokens whose target is ``ignore_index`` get 0 in both
     and their rows of h are not used; a target outside the vocabulary gives
     NaN."""
+    if stream is not None:
+        return _on_stream(stream, xent_fwd, h, weight, targets, ignore_index=ignore_index,
+                          workspace=workspace)
     dev, code, (tokens, _, _), shapes = _xent_args(h, weight, targets, ignore_index)
     lib = load()
     ws = _workspace(workspace, lib.ssm_xent_workspace_bytes(ctypes.byref(shapes), 0), dev)
@@ -304,11 +318,14 @@ def xent_fwd(h, weight, targets, *, ignore_index: int = -100, workspace=None):
     return loss, lse
 
 
-@_on_stream
-def xent_bwd(h, weight, targets, *, lse, dloss, ignore_index: int = -100, workspace=None) -> dict:
+def xent_bwd(h, weight, targets, *, lse, dloss, ignore_index: int = -100, workspace=None,
+             stream=None) -> dict:
     """The gradients of sum(dloss * loss) for ``xent_fwd``: a dict of dh (like h;
     0 for ignored tokens) and dweight (like weight).  lse: the forward's; dloss:
     fp32 [tokens]."""
+    if stream is not None:
+        return _on_stream(stream, xent_bwd, h, weight, targets, lse=lse, dloss=dloss,
+                          ignore_index=ignore_index, workspace=workspace)
     dev, code, (tokens, _, _), shapes = _xent_args(h, weight, targets, ignore_index)
     _dense(lse, "lse", (tokens,), torch.float32, dev)
     _dense(dloss, "dloss", (tokens,), torch.float32, dev)
