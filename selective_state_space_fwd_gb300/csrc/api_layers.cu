@@ -106,14 +106,17 @@ ssm_status ssm_conv_fwd(const void* x, const float* weight, const float* bias,
     return SSM_ERR_ALIGN;
   int dev = 0;
   if ((st = current_device_for(stream, &dev)) != SSM_OK) return st;
+  unsigned* err = ssm::stream::error_word();
+  if (!err) return SSM_ERR_CUDA;
   return status_of(ssm::launch_conv_fwd(
       conv_params(x, weight, bias, valid_len, state0, out_y, out_final, *shapes),
-      dtype == SSM_BF16, stream));
+      dtype == SSM_BF16, err, stream));
 }
 
 size_t ssm_conv_bwd_workspace_bytes(const ssm_conv_shapes* shapes) {
   if (check_conv(shapes, SSM_F32) != SSM_OK) return 0;
-  const int64_t parts = ssm::conv_bwd_partials(shapes->batch, shapes->seqlen, shapes->dim);
+  const int64_t parts = ssm::conv_bwd_partials(shapes->batch, shapes->seqlen, shapes->dim,
+                                                static_cast<int>(shapes->width));
   return static_cast<size_t>(parts) * (shapes->width + 1) * shapes->dim * sizeof(float);
 }
 
@@ -137,7 +140,9 @@ ssm_status ssm_conv_bwd(const void* x, const float* weight, const float* bias,
   q.fwd = conv_params(x, weight, bias, valid_len, state0, nullptr, nullptr, *shapes);
   q.dy = dy; q.dx = dx; q.dstate0 = dstate0; q.dweight = dweight; q.dbias = dbias;
   q.partial = static_cast<float*>(workspace);
-  return status_of(ssm::launch_conv_bwd(q, dtype == SSM_BF16, stream));
+  unsigned* err = ssm::stream::error_word();
+  if (!err) return SSM_ERR_CUDA;
+  return status_of(ssm::launch_conv_bwd(q, dtype == SSM_BF16, err, stream));
 }
 
 ssm_status ssm_conv_step(const void* x, const float* weight, const float* bias, void* state,

@@ -19,11 +19,8 @@
 // width - 1 steps run past the chunk's end.  dw and dbias are summed per
 // thread, then over the threads of the CTA in a fixed order, then over the
 // CTAs by a second kernel: no atomics, so the sums do not depend on timing.
-#include "common.cuh"
-#include "f32x2.cuh"
-#include "layers.h"
+#include "conv.cuh"
 #include "pdl.cuh"
-#include "vec.cuh"
 
 namespace ssm {
 namespace {
@@ -31,27 +28,18 @@ namespace {
 constexpr int kConvThreads = 256;
 constexpr int kSms = 152;
 
-// Rows in flight per thread, channels per thread and resident CTAs per SM
-// (their registers are the bound: the taps, the window and the rows in flight).
-// Measured on 8 x 4096 x 1024, width 4: forward fp32 48.5 us with 4 channels and
-// 2 CTAs, 57.6 us with 2 and 3; bf16 30.3 us with 4 channels and 3 CTAs, 32.5 us
-// with 8 and 2.  Backward (forward included, fp32): 130 us with 2 channels and 8
-// rows in flight, 139 us with 4 rows, 146 us with 4 channels and 2 rows.
-constexpr int U = 8;
-constexpr int kFwdVec = 4;
-template <typename T> constexpr int fwd_ctas() { return sizeof(T) == 2 ? 3 : 2; }
-template <typename T> constexpr int bwd_vec() { return 8 / sizeof(T); }
-constexpr int kBwdCtas = 2;
+constexpr int U = 8;         // rows in flight per thread
+constexpr int kFwdCtas = 3, kBwdCtas = 2;  // resident CTAs per SM
 
 // Steps per chunk.  A thread's time is its number of chunks times their length
 // and the `halo` steps a chunk adds; short chunks spread the work evenly, long
 // ones add less.
-int chunk_steps(int64_t batch, int64_t seqlen, int64_t cvs, int ctas_per_sm, int halo) {
+int chunk_steps(int64_t batch, int64_t seqlen, int64_t dim, int ctas_per_sm, int halo) {
   const int64_t slots = int64_t(kSms) * ctas_per_sm * kConvThreads;
   int best = 64;
   int64_t least = INT64_MAX;
   for (int tc : {64, 48, 32, 24, 16, 8}) {
-    const int64_t per = (batch * ((seqlen + tc - 1) / tc) * cvs + slots - 1) / slots;
+    const int64_t per = (batch * ((seqlen + tc - 1) / tc) * dim + slots - 1) / slots;
     if (per * (tc + halo) < least) {
       least = per * (tc + halo);
       best = tc;
@@ -60,120 +48,30 @@ int chunk_steps(int64_t batch, int64_t seqlen, int64_t cvs, int ctas_per_sm, int
   return best;
 }
 
-// Channel groups per CTA (a power of two): a warp along the channels where
+// Channels per CTA (a power of two): a warp along the channels where
 // there are enough of them.
-int lanes_log2(int64_t cvs) { return cvs >= 32 ? 5 : cvs >= 16 ? 4 : 3; }
+int lanes_log2(int64_t dim) { return dim >= 32 ? 5 : dim >= 16 ? 4 : 3; }
 
 struct ConvGrid {
   int tc, lx;
   int64_t chunks, gx, gy;
 };
 
-ConvGrid conv_grid(int64_t batch, int64_t seqlen, int64_t dim, int vec, int ctas_per_sm, int halo) {
+ConvGrid conv_grid(int64_t batch, int64_t seqlen, int64_t dim, int ctas_per_sm, int halo) {
   ConvGrid g;
-  const int64_t cvs = (dim + vec - 1) / vec;
-  g.tc = chunk_steps(batch, seqlen, cvs, ctas_per_sm, halo);
-  g.lx = lanes_log2(cvs);
+  g.tc = chunk_steps(batch, seqlen, dim, ctas_per_sm, halo);
+  g.lx = lanes_log2(dim);
   g.chunks = (seqlen + g.tc - 1) / g.tc;
   const int64_t ty = kConvThreads >> g.lx;
-  g.gx = (cvs + (int64_t(1) << g.lx) - 1) >> g.lx;
+  g.gx = (dim + (int64_t(1) << g.lx) - 1) >> g.lx;
   const int64_t need = (batch * g.chunks + ty - 1) / ty;
   const int64_t most = (int64_t(kSms) * ctas_per_sm + g.gx - 1) / g.gx;
   g.gy = need < most ? need : most;
   return g;
 }
 
-__device__ __forceinline__ int64_t conv_valid(const ConvParams& p, int64_t b) {
-  if (p.valid_len == nullptr) return p.seqlen;
-  const int64_t v = p.valid_len[b];
-  return v < 0 ? 0 : (v > p.seqlen ? p.seqlen : v);
-}
-
-// The row `back` steps before step 0: row width - 1 - back of the state.
 template <typename T, int K, int VEC>
-__device__ __forceinline__ Raw<T, VEC> state_row(const void* state0, int64_t b, int64_t dim,
-                                                 int64_t d0, int row) {
-  Raw<T, VEC> r;
-  if (state0 == nullptr) {
-    raw_zero<T, VEC>(r);
-    return r;
-  }
-  return raw_load<T, VEC>(static_cast<const T*>(state0) + (b * (K - 1) + row) * dim + d0);
-}
-
-template <int K, int VEC>
-__device__ __forceinline__ void load_taps(const float* weight, const float* bias, int64_t d0,
-                                          float (&w)[K][VEC], float (&bv)[VEC]) {
-  if constexpr (VEC > 1) {  // VEC * K consecutive floats, 16-byte aligned (the caller's check)
-    float t[VEC * K];
-    if constexpr (VEC * K % 4 == 0) {
-#pragma unroll
-      for (int i = 0; i < VEC * K / 4; ++i) {
-        const float4 v = __ldg(reinterpret_cast<const float4*>(weight + d0 * K) + i);
-        t[4 * i] = v.x; t[4 * i + 1] = v.y; t[4 * i + 2] = v.z; t[4 * i + 3] = v.w;
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < VEC * K; ++i) t[i] = __ldg(weight + d0 * K + i);
-    }
-#pragma unroll
-    for (int v = 0; v < VEC; ++v)
-#pragma unroll
-      for (int k = 0; k < K; ++k) w[k][v] = t[v * K + k];
-  } else {
-#pragma unroll
-    for (int k = 0; k < K; ++k) w[k][0] = __ldg(weight + d0 * K + k);
-  }
-#pragma unroll
-  for (int v = 0; v < VEC; ++v) bv[v] = bias ? __ldg(bias + d0 + v) : 0.f;
-}
-
-// pre of the row `cur` after the window `win` (oldest row first).
-template <int K, int VEC>
-__device__ __forceinline__ void taps(const float (&w)[K][VEC], const float (&bv)[VEC],
-                                     const float (&win)[K - 1][VEC], const float (&cur)[VEC],
-                                     float (&pre)[VEC]) {
-  vfma<VEC>(pre, w[0], win[0], bv);
-#pragma unroll
-  for (int k = 1; k < K - 1; ++k) vfma<VEC>(pre, w[k], win[k], pre);
-  vfma<VEC>(pre, w[K - 1], cur, pre);
-}
-
-// 1 / v with the MUFU unit (PTX rcp.approx.ftz.f32: within 1 ulp; 0 for
-// infinities, which a sigmoid's denominator may be).
-__device__ __forceinline__ float rcp(float v) {
-  float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
-  return r;
-}
-
-// s = sigmoid(v) = 1 / (1 + e^-v).
-template <int VEC>
-__device__ __forceinline__ void sigmoid(const float (&v)[VEC], float (&s)[VEC]) {
-  float one[VEC];
-  vscale<VEC>(s, v, -kLog2e);
-#pragma unroll
-  for (int i = 0; i < VEC; ++i) {
-    s[i] = ex2(s[i]);
-    one[i] = 1.f;
-  }
-  vadd<VEC>(s, s, one);
-#pragma unroll
-  for (int i = 0; i < VEC; ++i) s[i] = rcp(s[i]);
-}
-
-template <int K, int VEC>
-__device__ __forceinline__ void push(float (&win)[K - 1][VEC], const float (&cur)[VEC]) {
-#pragma unroll
-  for (int v = 0; v < VEC; ++v) {
-#pragma unroll
-    for (int k = 0; k + 1 < K - 1; ++k) win[k][v] = win[k + 1][v];
-    win[K - 2][v] = cur[v];
-  }
-}
-
-template <typename T, int K, int VEC>
-__global__ void __launch_bounds__(kConvThreads, fwd_ctas<T>())
+__global__ void __launch_bounds__(kConvThreads, kFwdCtas)
     conv_fwd_kernel(const ConvParams p, int tc, int lx, int64_t chunks) {
   const int64_t cv = (static_cast<int64_t>(blockIdx.x) << lx) + (threadIdx.x & ((1 << lx) - 1));
   const int64_t d0 = cv * VEC;
@@ -201,11 +99,7 @@ __global__ void __launch_bounds__(kConvThreads, fwd_ctas<T>())
         float cur[VEC], pre[VEC];
         widen<VEC>(raw, cur);
         taps<K, VEC>(w, bv, win, cur, pre);
-        if (p.silu) {
-          float sg[VEC];
-          sigmoid<VEC>(pre, sg);
-          vmul<VEC>(pre, pre, sg);
-        }
+        if (p.silu) apply_silu<VEC>(pre);
         store_f<T, VEC>(y, pre);
         y += p.dim;
         push<K, VEC>(win, cur);
@@ -285,9 +179,7 @@ __global__ void __launch_bounds__(kConvThreads, kBwdCtas)
     // dx from the window of dpre and the step's own
     auto emit = [&](int i, const float(&g)[VEC]) {
       float a[VEC];
-      vmul<VEC>(a, w[0], g);
-#pragma unroll
-      for (int k = 1; k < K; ++k) vfma<VEC>(a, w[k], dp[K - 1 - k], a);
+      dx_taps<K, VEC>(w, dp, g, a);
       if (i >= K - 1)
         store_f<T, VEC>(o, a);
       else if (c == 0 && q.dstate0)
@@ -299,25 +191,12 @@ __global__ void __launch_bounds__(kConvThreads, kBwdCtas)
       float cur[VEC], g[VEC];
       widen<VEC>(xr, cur);
       widen<VEC>(gr, g);
-      if (p.silu) {  // silu'(v) = s (1 + v (1 - s)), s = sigmoid(v)
-        float pre[VEC], sg[VEC], t[VEC], one[VEC];
+      if (p.silu) {
+        float pre[VEC];
         taps<K, VEC>(w, bv, win, cur, pre);
-        sigmoid<VEC>(pre, sg);
-#pragma unroll
-        for (int v = 0; v < VEC; ++v) {
-          t[v] = 1.f - sg[v];
-          one[v] = 1.f;
-        }
-        vfma<VEC>(t, pre, t, one);
-        vmul<VEC>(t, t, sg);
-        vmul<VEC>(g, g, t);
+        apply_dsilu<VEC>(pre, g);
       }
-      if (i < n) {
-        vadd<VEC>(db, db, g);
-#pragma unroll
-        for (int k = 0; k < K - 1; ++k) vfma<VEC>(dw[k], g, win[k], dw[k]);
-        vfma<VEC>(dw[K - 1], g, cur, dw[K - 1]);
-      }
+      if (i < n) add_dw<K, VEC>(dw, db, g, win, cur);
       emit(i, g);
       push<K, VEC>(win, cur);
     };
@@ -412,54 +291,28 @@ __global__ void __launch_bounds__(128) conv_step_kernel(const ConvStepParams p, 
   }
   widen<VEC>(win[K - 1], cur);
   taps<K, VEC>(w, bv, f, cur, pre);
-  if (p.silu) {
-    float sg[VEC];
-    sigmoid<VEC>(pre, sg);
-    vmul<VEC>(pre, pre, sg);
-  }
+  if (p.silu) apply_silu<VEC>(pre);
   store_f<T, VEC>(static_cast<T*>(p.y) + b * p.dim + d0, pre);
 }
 
 bool fits(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
-// Whether rows of `vec` elements can be moved whole: every row of every tensor
-// then starts on an access boundary.
-bool conv_vec_ok(const ConvParams& p, int vec, size_t es) {
-  const size_t a = vec * es;
-  return p.dim % vec == 0 && (p.x_batch * es) % a == 0 && (p.x_step * es) % a == 0 &&
-         fits(p.x, a) && fits(p.y, a) && fits(p.state0, a) && fits(p.out_final, a) &&
-         fits(p.weight, 16);
-}
-
 template <typename T, int K>
 cudaError_t conv_fwd_k(const ConvParams& p, cudaStream_t s) {
-  const bool vec = conv_vec_ok(p, kFwdVec, sizeof(T));
-  const ConvGrid g = conv_grid(p.batch, p.seqlen, p.dim, vec ? kFwdVec : 1, fwd_ctas<T>(), 2);
-  const dim3 grid(g.gx, g.gy);
-  if (vec)
-    conv_fwd_kernel<T, K, kFwdVec><<<grid, kConvThreads, 0, s>>>(p, g.tc, g.lx, g.chunks);
-  else
-    conv_fwd_kernel<T, K, 1><<<grid, kConvThreads, 0, s>>>(p, g.tc, g.lx, g.chunks);
+  const ConvGrid g = conv_grid(p.batch, p.seqlen, p.dim, kFwdCtas, 2);
+  conv_fwd_kernel<T, K, 1>
+      <<<dim3(g.gx, g.gy), kConvThreads, 0, s>>>(p, g.tc, g.lx, g.chunks);
   return cudaGetLastError();
 }
 
 template <typename T, int K>
-cudaError_t conv_bwd_k(const ConvBwdParams& q, cudaStream_t s) {
+cudaError_t conv_bwd_k(const ConvBwdParams& q, int* parts, cudaStream_t s) {
   const ConvParams& p = q.fwd;
-  constexpr int V = bwd_vec<T>();
-  const bool vec = conv_vec_ok(p, V, sizeof(T)) && fits(q.dy, 8) && fits(q.dx, 8) &&
-                   fits(q.dstate0, 8);
-  const ConvGrid g = conv_grid(p.batch, p.seqlen, p.dim, vec ? V : 1, kBwdCtas, 4);
-  const dim3 grid(g.gx, g.gy);
-  if (vec)
-    conv_bwd_kernel<T, K, V><<<grid, kConvThreads, 0, s>>>(q, g.tc, g.lx, g.chunks);
-  else
-    conv_bwd_kernel<T, K, 1><<<grid, kConvThreads, 0, s>>>(q, g.tc, g.lx, g.chunks);
-  const cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  return launch_after(conv_bwd_sum_kernel,
-                      dim3(static_cast<unsigned>((p.dim + 31) / 32), q.dbias ? K + 1 : K), 1024, 0, s,
-                      q.partial, q.dweight, q.dbias, p.dim, K, static_cast<int>(g.gy));
+  const ConvGrid g = conv_grid(p.batch, p.seqlen, p.dim, kBwdCtas, 4);
+  conv_bwd_kernel<T, K, 1>
+      <<<dim3(g.gx, g.gy), kConvThreads, 0, s>>>(q, g.tc, g.lx, g.chunks);
+  *parts = static_cast<int>(g.gy);
+  return cudaGetLastError();
 }
 
 template <typename T, int K>
@@ -480,7 +333,8 @@ cudaError_t conv_step_k(const ConvStepParams& p, cudaStream_t s) {
 
 }  // namespace
 
-cudaError_t launch_conv_fwd(const ConvParams& p, bool bf16, cudaStream_t s) {
+cudaError_t launch_conv_fwd(const ConvParams& p, bool bf16, unsigned* err, cudaStream_t s) {
+  if (conv_tma_ok(p, bf16)) return launch_conv_fwd_tma(p, bf16, err, s);
   switch (p.width) {
     case 2: return bf16 ? conv_fwd_k<__nv_bfloat16, 2>(p, s) : conv_fwd_k<float, 2>(p, s);
     case 3: return bf16 ? conv_fwd_k<__nv_bfloat16, 3>(p, s) : conv_fwd_k<float, 3>(p, s);
@@ -490,22 +344,30 @@ cudaError_t launch_conv_fwd(const ConvParams& p, bool bf16, cudaStream_t s) {
 }
 
 // The most partial sums any form of the backward writes.
-int64_t conv_bwd_partials(int64_t batch, int64_t seqlen, int64_t dim) {
-  int64_t most = 0;
-  for (int vec : {bwd_vec<float>(), bwd_vec<__nv_bfloat16>(), 1}) {
-    const int64_t n = conv_grid(batch, seqlen, dim, vec, kBwdCtas, 4).gy;
-    most = n > most ? n : most;
-  }
-  return most;
+int64_t conv_bwd_partials(int64_t batch, int64_t seqlen, int64_t dim, int width) {
+  const int64_t a = conv_grid(batch, seqlen, dim, kBwdCtas, 4).gy;
+  const int64_t b = conv_bwd_tma_partials(batch, seqlen, dim, width);
+  return a > b ? a : b;
 }
 
-cudaError_t launch_conv_bwd(const ConvBwdParams& q, bool bf16, cudaStream_t s) {
-  switch (q.fwd.width) {
-    case 2: return bf16 ? conv_bwd_k<__nv_bfloat16, 2>(q, s) : conv_bwd_k<float, 2>(q, s);
-    case 3: return bf16 ? conv_bwd_k<__nv_bfloat16, 3>(q, s) : conv_bwd_k<float, 3>(q, s);
-    case 4: return bf16 ? conv_bwd_k<__nv_bfloat16, 4>(q, s) : conv_bwd_k<float, 4>(q, s);
-    default: return cudaErrorInvalidValue;
+cudaError_t launch_conv_bwd(const ConvBwdParams& q, bool bf16, unsigned* err, cudaStream_t s) {
+  const int width = q.fwd.width;
+  int parts = 0;
+  cudaError_t e = cudaErrorInvalidValue;
+  if (conv_bwd_tma_ok(q, bf16)) {
+    e = launch_conv_bwd_tma(q, bf16, err, &parts, s);
+  } else {
+    switch (width) {
+      case 2: e = bf16 ? conv_bwd_k<__nv_bfloat16, 2>(q, &parts, s) : conv_bwd_k<float, 2>(q, &parts, s); break;
+      case 3: e = bf16 ? conv_bwd_k<__nv_bfloat16, 3>(q, &parts, s) : conv_bwd_k<float, 3>(q, &parts, s); break;
+      case 4: e = bf16 ? conv_bwd_k<__nv_bfloat16, 4>(q, &parts, s) : conv_bwd_k<float, 4>(q, &parts, s); break;
+      default: break;
+    }
   }
+  if (e != cudaSuccess) return e;
+  return launch_after(conv_bwd_sum_kernel,
+                      dim3(static_cast<unsigned>((q.fwd.dim + 31) / 32), q.dbias ? width + 1 : width),
+                      1024, 0, s, q.partial, q.dweight, q.dbias, q.fwd.dim, width, parts);
 }
 
 cudaError_t launch_conv_step(const ConvStepParams& p, bool bf16, cudaStream_t s) {

@@ -44,9 +44,18 @@ struct ConvStepParams {
 };
 
 inline bool conv_supported_width(int64_t k) { return k >= 2 && k <= 4; }
-cudaError_t launch_conv_fwd(const ConvParams& p, bool bf16, cudaStream_t s);
-int64_t conv_bwd_partials(int64_t batch, int64_t seqlen, int64_t dim);
-cudaError_t launch_conv_bwd(const ConvBwdParams& p, bool bf16, cudaStream_t s);
+// `err`: the sticky error word of the bounded waits.
+cudaError_t launch_conv_fwd(const ConvParams& p, bool bf16, unsigned* err, cudaStream_t s);
+int64_t conv_bwd_partials(int64_t batch, int64_t seqlen, int64_t dim, int width);
+cudaError_t launch_conv_bwd(const ConvBwdParams& p, bool bf16, unsigned* err, cudaStream_t s);
+// The forms whose rows are staged by TMA (kernel_conv_tma.cu), and whether a
+// call's tensors allow it.
+bool conv_tma_ok(const ConvParams& p, bool bf16);
+bool conv_bwd_tma_ok(const ConvBwdParams& p, bool bf16);
+int64_t conv_bwd_tma_partials(int64_t batch, int64_t seqlen, int64_t dim, int width);
+cudaError_t launch_conv_fwd_tma(const ConvParams& p, bool bf16, unsigned* err, cudaStream_t s);
+cudaError_t launch_conv_bwd_tma(const ConvBwdParams& p, bool bf16, unsigned* err, int* parts,
+                                cudaStream_t s);
 cudaError_t launch_conv_step(const ConvStepParams& p, bool bf16, cudaStream_t s);
 
 // ---- norm of the residual stream (kernel_norm.cu) ----------------------------
