@@ -93,7 +93,12 @@ CASES = [
     (300, 20000, 64, 0.1, 2.0),      # dh split along the vocabulary
     (1000, 3001, 768, 0.5, 2.0),
     (700, 5000, 1000, 0.2, 30.0),    # peaked: most probabilities underflow
+    (16, 129, 136, 0.2, 2.0),        # up to 32 tokens the forward streams the vocabulary
+    (17, 30001, 72, 0.0, 2.0),
+    (32, 700, 136, 0.0, 30.0),
+    (33, 20000, 64, 0.3, 2.0),
     (64, 33000, 2048, 0.0, 2.0),
+    (65, 700, 64, 0.0, 2.0),
     (8000, 70001, 64, 0.1, 2.0),     # several pieces of the vocabulary
 ]
 
@@ -173,30 +178,32 @@ def test_another_ignore_index():
     assert torch.equal(a["loss"][kept], b["loss"]) and torch.equal(a["dweight"], b["dweight"])
 
 
-def test_targets_outside_the_vocabulary_give_nan():
-    t = make(100, 300, 64)
+@pytest.mark.parametrize("T", [100, 12, 40])
+def test_targets_outside_the_vocabulary_give_nan(T):
+    t = make(T, 300, 64)
     want = run(t)
     for bad in (300, -1, 2 ** 40, -2 ** 40):
         u = dict(t, targets=t["targets"].clone())
         u["targets"][5] = bad
         got = run(u)
         assert got["loss"][5].isnan() and got["dh"][5].isnan().all()
-        keep = torch.arange(100, device="cuda") != 5
+        keep = torch.arange(T, device="cuda") != 5
         assert torch.equal(got["loss"][keep], want["loss"][keep])
         assert torch.equal(got["dh"][keep], want["dh"][keep])
         assert got["dweight"].isnan().all()
     S.check_device_errors()
 
 
-def test_nan_rows_stay_apart():
+@pytest.mark.parametrize("T", [100, 12, 40])
+def test_nan_rows_stay_apart(T):
     """A token whose hidden state is NaN has a NaN loss; the others' values and dh
     do not change."""
-    t = make(100, 300, 64)
+    t = make(T, 300, 64)
     want = run(t)
     u = dict(t, h=t["h"].clone())
     u["h"][9, 3] = float("nan")
     got = run(u)
-    keep = torch.arange(100, device="cuda") != 9
+    keep = torch.arange(T, device="cuda") != 9
     assert got["loss"][9].isnan()
     assert torch.equal(got["loss"][keep], want["loss"][keep])
     assert torch.equal(got["dh"][keep], want["dh"][keep])
