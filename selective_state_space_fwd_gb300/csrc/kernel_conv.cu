@@ -240,7 +240,13 @@ __global__ void __launch_bounds__(kConvThreads, kBwdCtas)
       const int64_t d = (static_cast<int64_t>(blockIdx.x) << lx) * VEC + i;
       float a = 0.f;
       for (int j = 0; j < ty; ++j) a += red[j * wide + i];
-      if (d < p.dim) q.partial[(static_cast<int64_t>(blockIdx.y) * (K + 1) + k) * p.dim + d] = a;
+      if (d >= p.dim) continue;
+      if (gridDim.y > 1)
+        q.partial[(static_cast<int64_t>(blockIdx.y) * (K + 1) + k) * p.dim + d] = a;
+      else if (k < K)  // the channels' only CTA: its sums are the result
+        q.dweight[d * K + k] = a;
+      else if (q.dbias)
+        q.dbias[d] = a;
     }
   }
 }
@@ -387,7 +393,7 @@ cudaError_t launch_conv_bwd(const ConvBwdParams& q, bool bf16, unsigned* err, cu
       default: break;
     }
   }
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || parts == 1) return e;
   return launch_after(conv_bwd_sum_kernel,
                       dim3(static_cast<unsigned>((q.fwd.dim + 31) / 32), q.dbias ? width + 1 : width),
                       1024, 0, s, q.partial, q.dweight, q.dbias, q.fwd.dim, width, parts);

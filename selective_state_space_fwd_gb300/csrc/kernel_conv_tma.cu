@@ -393,16 +393,22 @@ __global__ void __launch_bounds__(kWarps * 32, kBwdCtas)
 #pragma unroll
     for (int j = 0; j < kWarps; ++j) a += red[(j * (K + 1) + k) * kWide + c];
     const int64_t d = ring.x + c;
-    if (d < p.dim)
+    if (d >= p.dim) continue;
+    if (gridDim.x > q.slabs)
       bp.partial[(static_cast<int64_t>(blockIdx.x / q.slabs) * (K + 1) + k) * p.dim + d] = a;
+    else if (k < K)  // the slab's only CTA: its sums are the result
+      bp.dweight[d * K + k] = a;
+    else if (bp.dbias)
+      bp.dbias[d] = a;
   }
 }
 
 // Pieces of whole boxes, with `halo` steps around them: the longest piece for
 // which the slowest warp has least to do.  Only the first piece of a sequence
 // may reach into the state, so a piece has at least width - 1 steps.  `rows`:
-// CTAs per slab.
-Pieces make_pieces(const ConvParams& p, int vec, int ctas, int halo, int* rows) {
+// CTAs per slab.  With `alone`, work that a slab's four warps finish in a piece
+// of up to four boxes each goes to one CTA, whose sums need no second kernel.
+Pieces make_pieces(const ConvParams& p, int vec, int ctas, int halo, bool alone, int* rows) {
   Pieces q;
   q.slabs = static_cast<int>((p.dim + 32 * vec - 1) / (32 * vec));
   const int64_t most = int64_t(kSms) * ctas / q.slabs > 0 ? int64_t(kSms) * ctas / q.slabs : 1;
@@ -416,6 +422,13 @@ Pieces make_pieces(const ConvParams& p, int vec, int ctas, int halo, int* rows) 
     if (cost < least) {
       least = cost;
       q.tc = tc;
+    }
+  }
+  for (int n = 1; alone && n <= 4; ++n) {
+    const int tc = n * kRows - halo;
+    if (tc >= p.width - 1 && p.batch * ((p.seqlen + tc - 1) / tc) <= kWarps) {
+      q.tc = tc;
+      break;
     }
   }
   q.segs = static_cast<int>((p.seqlen + q.tc - 1) / q.tc);
@@ -448,7 +461,7 @@ bool fits(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a
 template <typename T, int K>
 cudaError_t fwd_k(const ConvParams& p, unsigned* err, cudaStream_t s) {
   int rows;
-  const Pieces q = make_pieces(p, 8 / sizeof(T), kFwdCtas, K - 1, &rows);
+  const Pieces q = make_pieces(p, 8 / sizeof(T), kFwdCtas, K - 1, false, &rows);
   CUtensorMap mx;
   if (!conv_map(&mx, sizeof(T) == 2, p.x, p, p.x_batch, p.x_step)) return cudaErrorInvalidValue;
   conv_fwd_tma_kernel<T, K><<<q.slabs * rows, kWarps * 32, kFwdSmem, s>>>(mx, p, q, err);
@@ -459,7 +472,7 @@ template <typename T, int K>
 cudaError_t bwd_k(const ConvBwdParams& b, unsigned* err, int* parts, cudaStream_t s) {
   const ConvParams& p = b.fwd;
   int rows;
-  const Pieces q = make_pieces(p, 8 / sizeof(T), kBwdCtas, 2 * (K - 1), &rows);
+  const Pieces q = make_pieces(p, 8 / sizeof(T), kBwdCtas, 2 * (K - 1), true, &rows);
   CUtensorMap mx, mg;
   if (!conv_map(&mx, sizeof(T) == 2, p.x, p, p.x_batch, p.x_step) ||
       !conv_map(&mg, sizeof(T) == 2, b.dy, p, p.seqlen * p.dim, p.dim))
@@ -494,7 +507,7 @@ int64_t conv_bwd_tma_partials(int64_t batch, int64_t seqlen, int64_t dim, int wi
   int most = 0;
   for (int vec : {2, 4}) {
     int rows;
-    make_pieces(p, vec, kBwdCtas, 2 * (width - 1), &rows);
+    make_pieces(p, vec, kBwdCtas, 2 * (width - 1), true, &rows);
     most = rows > most ? rows : most;
   }
   return most;

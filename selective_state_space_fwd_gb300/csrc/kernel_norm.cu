@@ -287,7 +287,13 @@ __global__ void __launch_bounds__(THREADS, bwd_ctas_per_sm(THREADS))
         const int c = i * wide + j;
         float s = 0.f;
         for (int u = 0; u < groups; ++u) s += acc[u * wide + j];
-        if (c < dim) p.partial[(static_cast<int64_t>(blockIdx.x) * 2 + k) * p.dim + c] = s;
+        if (c >= dim) continue;
+        if (gridDim.x > 1)
+          p.partial[(static_cast<int64_t>(blockIdx.x) * 2 + k) * p.dim + c] = s;
+        else if (k == 0)  // the only CTA: its sums are the result
+          p.dweight[c] = s;
+        else if (p.dbias)
+          p.dbias[c] = s;
       }
     }
   }
@@ -357,6 +363,7 @@ int bwd_threads(int64_t dim) {
 int64_t bwd_ctas(int64_t rows, int tpr) {
   const int threads = tpr > 128 ? tpr : 128;
   const int64_t groups = threads / tpr, need = (rows + groups - 1) / groups;
+  if (need <= 4) return 1;  // a few rows in turn cost less than a second kernel for the sums
   const int64_t most = int64_t(kSms) * bwd_ctas_per_sm(threads);
   return need < most ? need : most;
 }
@@ -375,7 +382,7 @@ cudaError_t norm_bwd_v(const NormBwdParams& p, cudaStream_t s) {
   else
     norm_bwd_kernel<TX, TR, VEC, NV, 128><<<g, 128, 0, s>>>(p, tpr);
   const cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || g == 1) return e;
   return launch_after(norm_bwd_sum_kernel,
                       dim3(static_cast<unsigned>((p.dim + 31) / 32), p.dbias ? 2 : 1), 1024, 0, s,
                       p.partial, p.dweight, p.dbias, p.dim, static_cast<int>(g));
