@@ -19,6 +19,8 @@
 // keeps CTAs resident and walks rows, so that every thread sums dw and db of
 // its own columns in registers; the CTAs' sums are written once and added by a
 // second kernel in a fixed order (no atomics).
+#include <type_traits>
+
 #include "common.cuh"
 #include "layers.h"
 #include "pdl.cuh"
@@ -54,39 +56,106 @@ __device__ __forceinline__ float row_sum(float v, int tpr, float* red) {
   return a;
 }
 
-// Group i of a thread's columns starts at column (i tpr + lane) VEC.  Loads past
-// the row's end are made at its last group instead, and their values dropped,
-// so that no load waits on a branch.
-template <int VEC>
-__device__ __forceinline__ int clamped(int c, int dim) {
-  return c < dim ? c : dim - VEC;
-}
+// A thread's columns: NV groups of VEC, group i from column (i tpr + lane) VEC.
+// Rows whose length is not a multiple of VEC start off the access boundary; with
+// SHIFT their groups start `shift` columns earlier, on it, and reach into the
+// rows before and after, whose elements are read (but past the tensor's end) and
+// dropped.  shift = row dim mod VEC, as tensors start on a boundary.
+template <int VEC, bool SHIFT>
+struct Cols {
+  int dim, shift;
+  bool last;  // the tensor ends within a group of the row's end: nothing is read past it
+  __device__ __forceinline__ Cols(int dim_, int64_t row, int64_t rows) : dim(dim_), shift(0) {
+    if (SHIFT) shift = static_cast<int>(row % VEC) * (dim % VEC) % VEC;
+    set_row(row, rows);
+  }
+  // Another row of the same shift.
+  __device__ __forceinline__ void set_row(int64_t row, int64_t rows) {
+    last = SHIFT && (rows - 1 - row) * dim < VEC;
+  }
+  __device__ __forceinline__ int at(int group) const { return group * VEC - shift; }
+  __device__ __forceinline__ bool whole(int c) const {
+    return SHIFT ? c >= 0 && c + VEC <= dim : c < dim;
+  }
+  // f(v, whether column c + v is the row's), for the elements of a group: no
+  // comparisons per element in the groups inside the row.
+  template <typename F>
+  __device__ __forceinline__ void each(int c, F&& f) const {
+    if (whole(c)) {
+#pragma unroll
+      for (int v = 0; v < VEC; ++v) f(v, std::true_type());
+    } else {
+#pragma unroll
+      for (int v = 0; v < VEC; ++v) f(v, SHIFT && c + v >= 0 && c + v < dim);
+    }
+  }
+  // Loads of groups past the row's end are made at its last group instead, and
+  // their values dropped, so that no load waits on a branch.
+  template <typename T, bool RW = false>
+  __device__ __forceinline__ Raw<T, VEC> load(const T* row, int c) const {
+    const int end = SHIFT ? (dim + shift - 1) / VEC * VEC - shift : dim - VEC;
+    c = c < dim ? c : end;
+    if constexpr (SHIFT) {
+      if (last && c + VEC > dim) {
+        Raw<T, VEC> r;
+        float f[VEC];
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) f[v] = c + v < dim ? static_cast<float>(row[c + v]) : 0.f;
+        narrow<VEC>(f, r);
+        return r;
+      }
+    }
+    if constexpr (RW) return raw_load_rw<T, VEC>(row + c);
+    else return raw_load<T, VEC>(row + c);
+  }
+  // The weight's (or bias's) values of a group; they start on a boundary only
+  // without a shift.
+  __device__ __forceinline__ void load_w(const float* w, int c, float (&f)[VEC]) const {
+    if constexpr (SHIFT) {
+      each(c, [&](int v, auto in) { f[v] = in ? __ldg(w + (c + v)) : 0.f; });
+    } else {
+      load_f<float, VEC>(w + (c < dim ? c : dim - VEC), f);
+    }
+  }
+  template <typename T>
+  __device__ __forceinline__ void store(T* row, int c, const float (&f)[VEC]) const {
+    if (whole(c)) {
+      store_f<T, VEC>(row + c, f);
+    } else if constexpr (SHIFT) {
+#pragma unroll
+      for (int v = 0; v < VEC; ++v) {
+        const float one[1] = {f[v]};
+        if (c + v >= 0 && c + v < dim) store_f<T, 1>(row + c + v, one);
+      }
+    }
+  }
+};
 
-template <typename TX, typename TR, int VEC, int NV>
+template <typename TX, typename TR, int VEC, int NV, bool SHIFT>
 __global__ void __launch_bounds__(VEC * NV == 8 ? 1024 : 512)
     norm_fwd_kernel(const NormParams p, int tpr) {
   __shared__ float red[2][32];
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * (blockDim.x / tpr) + threadIdx.x / tpr;
+  int64_t row = static_cast<int64_t>(blockIdx.x) * (blockDim.x / tpr) + threadIdx.x / tpr;
   const int lane = threadIdx.x & (tpr - 1);
   const bool on = row < p.rows;
+  row = on ? row : p.rows - 1;  // groups without a row write nothing
   const int dim = static_cast<int>(p.dim);
-  const int64_t at = (on ? row : p.rows - 1) * p.dim;  // groups without a row write nothing
+  const int64_t at = row * p.dim;
+  const Cols<VEC, SHIFT> cols(dim, row, p.rows);
   const TX* x = static_cast<const TX*>(p.x) + at;
   float f[NV][VEC];
   Raw<TX, VEC> xr[NV];
 #pragma unroll
-  for (int i = 0; i < NV; ++i)
-    xr[i] = raw_load<TX, VEC>(x + clamped<VEC>((i * tpr + lane) * VEC, dim));
+  for (int i = 0; i < NV; ++i) xr[i] = cols.load(x, cols.at(i * tpr + lane));
   if (p.residual) {
     const TR* res = static_cast<const TR*>(p.residual) + at;
     TR* out = static_cast<TR*>(p.r) + at;
     Raw<TR, VEC> rr[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i)
-      rr[i] = raw_load_rw<TR, VEC>(res + clamped<VEC>((i * tpr + lane) * VEC, dim));
+      rr[i] = cols.template load<TR, true>(res, cols.at(i * tpr + lane));
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = (i * tpr + lane) * VEC;
       float g[VEC];
       widen<VEC>(xr[i], f[i]);
       widen<VEC>(rr[i], g);
@@ -94,8 +163,8 @@ __global__ void __launch_bounds__(VEC * NV == 8 ? 1024 : 512)
       for (int v = 0; v < VEC; ++v) f[i][v] += g[v];
       Raw<TR, VEC> o;
       narrow<VEC>(f[i], o);
-      if (on && c < dim) raw_store<TR, VEC>(out + c, o);
       widen<VEC>(o, f[i]);  // as stored
+      if (on) cols.store(out, cols.at(i * tpr + lane), f[i]);
     }
   } else {
 #pragma unroll
@@ -107,21 +176,19 @@ __global__ void __launch_bounds__(VEC * NV == 8 ? 1024 : 512)
     float a = 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const bool in = (i * tpr + lane) * VEC < dim;
-#pragma unroll
-      for (int v = 0; v < VEC; ++v) a += in ? f[i][v] : 0.f;
+      const int c = cols.at(i * tpr + lane);
+      cols.each(c, [&](int v, auto in) { a += in ? f[i][v] : 0.f; });
     }
     mean = row_sum(a, tpr, red[0]) * inv;
   }
   float q = 0.f;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const bool in = (i * tpr + lane) * VEC < dim;
-#pragma unroll
-    for (int v = 0; v < VEC; ++v) {
+    const int c = cols.at(i * tpr + lane);
+    cols.each(c, [&](int v, auto in) {
       f[i][v] -= mean;
       q = fmaf(in ? f[i][v] : 0.f, f[i][v], q);
-    }
+    });
   }
   const float rstd = rsqrtf(row_sum(q, tpr, red[1]) * inv + p.eps);
   if (!on) return;
@@ -133,7 +200,7 @@ __global__ void __launch_bounds__(VEC * NV == 8 ? 1024 : 512)
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     float w[VEC];
-    load_f<float, VEC>(p.weight + clamped<VEC>((i * tpr + lane) * VEC, dim), w);
+    cols.load_w(p.weight, cols.at(i * tpr + lane), w);
 #pragma unroll
     for (int v = 0; v < VEC; ++v) f[i][v] *= rstd * w[v];
   }
@@ -141,16 +208,13 @@ __global__ void __launch_bounds__(VEC * NV == 8 ? 1024 : 512)
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       float b[VEC];
-      load_f<float, VEC>(p.bias + clamped<VEC>((i * tpr + lane) * VEC, dim), b);
+      cols.load_w(p.bias, cols.at(i * tpr + lane), b);
 #pragma unroll
       for (int v = 0; v < VEC; ++v) f[i][v] += b[v];
     }
   }
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int c = (i * tpr + lane) * VEC;
-    if (c < dim) store_f<TX, VEC>(y + c, f[i]);
-  }
+  for (int i = 0; i < NV; ++i) cols.store(y, cols.at(i * tpr + lane), f[i]);
 }
 
 // A row's operands of one thread, as loaded.
@@ -162,11 +226,13 @@ struct RowRaw {
 };
 
 // The loads of the next row are in flight while a row is reduced and written.
-template <typename TX, typename TR, int VEC, int NV, int THREADS>
+// With SHIFT a group of threads takes rows of one shift only (the launch makes
+// the rows' stride a multiple of VEC), so that its columns stay its own.
+template <typename TX, typename TR, int VEC, int NV, int THREADS, bool SHIFT>
 __global__ void __launch_bounds__(THREADS, bwd_ctas_per_sm(THREADS))
     norm_bwd_kernel(const NormBwdParams p, int tpr) {
   __shared__ float2 red[2][32];
-  __shared__ float acc[THREADS * VEC];
+  __shared__ float acc[THREADS * VEC * NV];
   const int wpr = tpr >> 5, groups = THREADS / tpr;
   const int group = threadIdx.x / tpr, lane = threadIdx.x & (tpr - 1);
   const int dim = static_cast<int>(p.dim);
@@ -174,10 +240,11 @@ __global__ void __launch_bounds__(THREADS, bwd_ctas_per_sm(THREADS))
   const bool has_dr = p.dr != nullptr;
   constexpr bool kHoldW = NV * VEC == kBwdPer;  // wider rows read the weight again per row
   float w[kHoldW ? NV : 1][VEC], dw[NV][VEC], db[NV][VEC];
+  const int64_t row0 = static_cast<int64_t>(blockIdx.x) * groups + group;
+  const Cols<VEC, SHIFT> own(dim, row0, p.rows);  // the shift of the group's rows
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    if constexpr (kHoldW)
-      load_f<float, VEC>(p.weight + clamped<VEC>((i * tpr + lane) * VEC, dim), w[i]);
+    if constexpr (kHoldW) own.load_w(p.weight, own.at(i * tpr + lane), w[i]);
 #pragma unroll
     for (int v = 0; v < VEC; ++v) dw[i][v] = db[i][v] = 0.f;
   }
@@ -185,17 +252,18 @@ __global__ void __launch_bounds__(THREADS, bwd_ctas_per_sm(THREADS))
   const auto load = [&](RowRaw<TX, TR, VEC, NV>& x, int64_t row) {
     if (row >= p.rows) return;
     const int64_t at = row * p.dim;
+    Cols<VEC, SHIFT> cols = own;
+    cols.set_row(row, p.rows);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int64_t o = at + clamped<VEC>((i * tpr + lane) * VEC, dim);
-      x.r[i] = raw_load<TR, VEC>(static_cast<const TR*>(p.r) + o);
-      x.dy[i] = raw_load<TX, VEC>(static_cast<const TX*>(p.dy) + o);
+      const int c = cols.at(i * tpr + lane);
+      x.r[i] = cols.load(static_cast<const TR*>(p.r) + at, c);
+      x.dy[i] = cols.load(static_cast<const TX*>(p.dy) + at, c);
     }
     if (has_dr) {
 #pragma unroll
       for (int i = 0; i < NV; ++i)
-        x.dr[i] = raw_load<TR, VEC>(static_cast<const TR*>(p.dr) + at +
-                                    clamped<VEC>((i * tpr + lane) * VEC, dim));
+        x.dr[i] = cols.load(static_cast<const TR*>(p.dr) + at, cols.at(i * tpr + lane));
     }
     x.mean = p.rms ? 0.f : __ldg(p.stats + row);
     x.rstd = __ldg(p.stats + p.rows + row);
@@ -203,7 +271,7 @@ __global__ void __launch_bounds__(THREADS, bwd_ctas_per_sm(THREADS))
   int buf = 0;
   const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
   RowRaw<TX, TR, VEC, NV> next = {};
-  load(next, static_cast<int64_t>(blockIdx.x) * groups + group);
+  load(next, row0);
   for (int64_t base = static_cast<int64_t>(blockIdx.x) * groups; base < p.rows; base += step) {
     const int64_t row = base + group;
     const bool on = row < p.rows;
@@ -214,7 +282,7 @@ __global__ void __launch_bounds__(THREADS, bwd_ctas_per_sm(THREADS))
     float2 a = make_float2(0.f, 0.f);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const bool in = on && (i * tpr + lane) * VEC < dim;
+      const int c = own.at(i * tpr + lane);
       widen<VEC>(next.r[i], xh[i]);
       widen<VEC>(next.dy[i], g[i]);
       er[i] = next.dr[i];
@@ -223,17 +291,18 @@ __global__ void __launch_bounds__(THREADS, bwd_ctas_per_sm(THREADS))
 #pragma unroll
         for (int v = 0; v < VEC; ++v) wi[v] = w[i][v];
       } else {
-        load_f<float, VEC>(p.weight + clamped<VEC>((i * tpr + lane) * VEC, dim), wi);
+        own.load_w(p.weight, c, wi);
       }
-#pragma unroll
-      for (int v = 0; v < VEC; ++v) {
-        xh[i][v] = in ? (xh[i][v] - mean) * rstd : 0.f;
-        g[i][v] = in ? g[i][v] : 0.f;
-        db[i][v] += g[i][v];
-        dw[i][v] = fmaf(g[i][v], xh[i][v], dw[i][v]);
-        g[i][v] *= wi[v];
-        a.x += g[i][v];
-        a.y = fmaf(g[i][v], xh[i][v], a.y);
+      if (on) {
+        own.each(c, [&](int v, auto in) {
+          xh[i][v] = in ? (xh[i][v] - mean) * rstd : 0.f;
+          g[i][v] = in ? g[i][v] : 0.f;
+          db[i][v] += g[i][v];
+          dw[i][v] = fmaf(g[i][v], xh[i][v], dw[i][v]);
+          g[i][v] *= wi[v];
+          a.x += g[i][v];
+          a.y = fmaf(g[i][v], xh[i][v], a.y);
+        });
       }
     }
     load(next, row + step);
@@ -259,7 +328,7 @@ __global__ void __launch_bounds__(THREADS, bwd_ctas_per_sm(THREADS))
     const float mg = p.rms ? 0.f : a.x * inv, mx = a.y * inv;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = (i * tpr + lane) * VEC;
+      const int c = own.at(i * tpr + lane);
       float o[VEC], e[VEC];
       widen<VEC>(er[i], e);
 #pragma unroll
@@ -267,34 +336,35 @@ __global__ void __launch_bounds__(THREADS, bwd_ctas_per_sm(THREADS))
         o[v] = rstd * (g[i][v] - mg - xh[i][v] * mx);
         o[v] = has_dr ? o[v] + e[v] : o[v];
       }
-      if (on && c < dim) {
-        store_f<TX, VEC>(static_cast<TX*>(p.dx) + at + c, o);
-        if (p.dresidual) store_f<TR, VEC>(static_cast<TR*>(p.dresidual) + at + c, o);
+      if (on) {
+        own.store(static_cast<TX*>(p.dx) + at, c, o);
+        if (p.dresidual) own.store(static_cast<TR*>(p.dresidual) + at, c, o);
       }
     }
   }
   // the row groups' sums, added in the order of the groups
+  const int span = tpr * VEC * NV;
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
+    __syncthreads();
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      __syncthreads();
+    for (int i = 0; i < NV; ++i)
 #pragma unroll
-      for (int v = 0; v < VEC; ++v) acc[threadIdx.x * VEC + v] = k == 0 ? dw[i][v] : db[i][v];
-      __syncthreads();
-      const int wide = tpr * VEC;
-      for (int j = threadIdx.x; j < wide; j += THREADS) {
-        const int c = i * wide + j;
-        float s = 0.f;
-        for (int u = 0; u < groups; ++u) s += acc[u * wide + j];
-        if (c >= dim) continue;
-        if (gridDim.x > 1)
-          p.partial[(static_cast<int64_t>(blockIdx.x) * 2 + k) * p.dim + c] = s;
-        else if (k == 0)  // the only CTA: its sums are the result
-          p.dweight[c] = s;
-        else if (p.dbias)
-          p.dbias[c] = s;
+      for (int v = 0; v < VEC; ++v)
+        acc[group * span + (i * tpr + lane) * VEC + v] = k == 0 ? dw[i][v] : db[i][v];
+    __syncthreads();
+    for (int c = threadIdx.x; c < dim; c += THREADS) {
+      float s = 0.f;
+      for (int u = 0; u < groups; ++u) {
+        const Cols<VEC, SHIFT> theirs(dim, row0 - group + u, p.rows);
+        s += acc[u * span + c + theirs.shift];
       }
+      if (gridDim.x > 1)
+        p.partial[(static_cast<int64_t>(blockIdx.x) * 2 + k) * p.dim + c] = s;
+      else if (k == 0)  // the only CTA: its sums are the result
+        p.dweight[c] = s;
+      else if (p.dbias)
+        p.dbias[c] = s;
     }
   }
 }
@@ -332,31 +402,47 @@ int threads_per_row(int64_t dim, int per) {
 
 // Rows are held 8 elements per thread where there are few of them (a row's
 // latency counts), else 16 (fewer threads to synchronise per row).
-template <typename TX, typename TR, int VEC>
+// Columns that a row's groups span.
+int64_t span_of(int64_t dim, int vec, bool shift) { return shift ? dim + vec - 1 : dim; }
+
+template <typename TX, typename TR, int VEC, bool SHIFT>
 cudaError_t norm_fwd_v(const NormParams& p, cudaStream_t s) {
   const int per = p.rows < 4 * kSms ? 8 : 16;
-  const int tpr = threads_per_row(p.dim, per);
+  const int tpr = threads_per_row(span_of(p.dim, VEC, SHIFT), per);
   const int threads = tpr > 128 ? tpr : 128;
   const int64_t rpb = threads / tpr, blocks = (p.rows + rpb - 1) / rpb;
   if (blocks > 0x7FFFFFFF) return cudaErrorInvalidValue;
   const unsigned g = static_cast<unsigned>(blocks);
   if (per == 8)
-    norm_fwd_kernel<TX, TR, VEC, 8 / VEC><<<g, threads, 0, s>>>(p, tpr);
+    norm_fwd_kernel<TX, TR, VEC, 8 / VEC, SHIFT><<<g, threads, 0, s>>>(p, tpr);
   else
-    norm_fwd_kernel<TX, TR, VEC, 16 / VEC><<<g, threads, 0, s>>>(p, tpr);
+    norm_fwd_kernel<TX, TR, VEC, 16 / VEC, SHIFT><<<g, threads, 0, s>>>(p, tpr);
   return cudaGetLastError();
+}
+
+// How a call's rows are accessed: in whole groups, in shifted groups (rows that
+// do not start on a boundary, tensors that do), or element by element.
+enum class Access { kWhole, kShift, kSingle };
+Access access_of(int64_t dim, int vec, bool aligned) {
+  if (!aligned) return Access::kSingle;
+  if (dim % vec == 0) return Access::kWhole;
+  return span_of(dim, vec, true) <= kNormMaxDim ? Access::kShift : Access::kSingle;
 }
 
 template <typename TX, typename TR>
 cudaError_t norm_fwd_t(const NormParams& p, cudaStream_t s) {
   constexpr int V = 16 / sizeof(TX);
-  const bool vec = p.dim % V == 0 && fits(p.x, 16) && fits(p.y, 16) && fits(p.residual, 16) &&
-                   fits(p.r, 16) && fits(p.weight, 16) && fits(p.bias, 16);
-  return vec ? norm_fwd_v<TX, TR, V>(p, s) : norm_fwd_v<TX, TR, 1>(p, s);
+  const bool aligned = fits(p.x, 16) && fits(p.y, 16) && fits(p.residual, 16) && fits(p.r, 16) &&
+                       fits(p.weight, 16) && fits(p.bias, 16);
+  switch (access_of(p.dim, V, aligned)) {
+    case Access::kWhole: return norm_fwd_v<TX, TR, V, false>(p, s);
+    case Access::kShift: return norm_fwd_v<TX, TR, V, true>(p, s);
+    default: return norm_fwd_v<TX, TR, 1, false>(p, s);
+  }
 }
 
-int bwd_threads(int64_t dim) {
-  const int t = threads_per_row(dim, kBwdPer);
+int bwd_threads(int64_t span) {
+  const int t = threads_per_row(span, kBwdPer);
   return t < 512 ? t : 512;
 }
 
@@ -368,19 +454,21 @@ int64_t bwd_ctas(int64_t rows, int tpr) {
   return need < most ? need : most;
 }
 
-template <typename TX, typename TR, int VEC>
+template <typename TX, typename TR, int VEC, bool SHIFT>
 cudaError_t norm_bwd_v(const NormBwdParams& p, cudaStream_t s) {
   constexpr int NV = kBwdPer / VEC;
-  const int tpr = bwd_threads(p.dim);
-  const unsigned g = static_cast<unsigned>(bwd_ctas(p.rows, tpr));
-  if (p.dim > kBwdPer * 512)
-    norm_bwd_kernel<TX, TR, VEC, 2 * NV, 512><<<g, 512, 0, s>>>(p, tpr);
+  const int64_t span = span_of(p.dim, VEC, SHIFT);
+  const int tpr = bwd_threads(span);
+  unsigned g = static_cast<unsigned>(bwd_ctas(p.rows, tpr));
+  if (SHIFT) g = (g + VEC - 1) / VEC * VEC;  // the rows' stride a multiple of VEC
+  if (span > kBwdPer * 512)
+    norm_bwd_kernel<TX, TR, VEC, 2 * NV, 512, SHIFT><<<g, 512, 0, s>>>(p, tpr);
   else if (tpr == 512)
-    norm_bwd_kernel<TX, TR, VEC, NV, 512><<<g, 512, 0, s>>>(p, tpr);
+    norm_bwd_kernel<TX, TR, VEC, NV, 512, SHIFT><<<g, 512, 0, s>>>(p, tpr);
   else if (tpr == 256)
-    norm_bwd_kernel<TX, TR, VEC, NV, 256><<<g, 256, 0, s>>>(p, tpr);
+    norm_bwd_kernel<TX, TR, VEC, NV, 256, SHIFT><<<g, 256, 0, s>>>(p, tpr);
   else
-    norm_bwd_kernel<TX, TR, VEC, NV, 128><<<g, 128, 0, s>>>(p, tpr);
+    norm_bwd_kernel<TX, TR, VEC, NV, 128, SHIFT><<<g, 128, 0, s>>>(p, tpr);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || g == 1) return e;
   return launch_after(norm_bwd_sum_kernel,
@@ -391,9 +479,13 @@ cudaError_t norm_bwd_v(const NormBwdParams& p, cudaStream_t s) {
 template <typename TX, typename TR>
 cudaError_t norm_bwd_t(const NormBwdParams& p, cudaStream_t s) {
   constexpr int V = 16 / sizeof(TX);
-  const bool vec = p.dim % V == 0 && fits(p.r, 16) && fits(p.dy, 16) && fits(p.dr, 16) &&
-                   fits(p.dx, 16) && fits(p.dresidual, 16) && fits(p.weight, 16);
-  return vec ? norm_bwd_v<TX, TR, V>(p, s) : norm_bwd_v<TX, TR, 1>(p, s);
+  const bool aligned = fits(p.r, 16) && fits(p.dy, 16) && fits(p.dr, 16) && fits(p.dx, 16) &&
+                       fits(p.dresidual, 16) && fits(p.weight, 16);
+  switch (access_of(p.dim, V, aligned)) {
+    case Access::kWhole: return norm_bwd_v<TX, TR, V, false>(p, s);
+    case Access::kShift: return norm_bwd_v<TX, TR, V, true>(p, s);
+    default: return norm_bwd_v<TX, TR, 1, false>(p, s);
+  }
 }
 
 }  // namespace
@@ -405,8 +497,13 @@ cudaError_t launch_norm_fwd(const NormParams& p, bool bf16, bool residual_bf16, 
                        : norm_fwd_t<__nv_bfloat16, float>(p, s);
 }
 
+// The most CTAs any form of the backward launches.
 int64_t norm_bwd_partials(int64_t rows, int64_t dim) {
-  return bwd_ctas(rows, bwd_threads(dim));
+  const int64_t a = bwd_ctas(rows, bwd_threads(dim));
+  const int64_t b = (bwd_ctas(rows, bwd_threads(span_of(dim, 8, true))) + 7) / 8 * 8;
+  const int64_t c = (bwd_ctas(rows, bwd_threads(span_of(dim, 4, true))) + 3) / 4 * 4;
+  const int64_t m = a > b ? a : b;
+  return m > c ? m : c;
 }
 
 cudaError_t launch_norm_bwd(const NormBwdParams& p, bool bf16, bool residual_bf16,

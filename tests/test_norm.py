@@ -77,6 +77,14 @@ CASES = [
     ("bf16", 1300, 8191, "bf16", True, False),
     ("bf16", 1300, 8192, "f32", False, True),
     ("bf16", 40000, 33, "bf16", False, True),
+    # rows that start off a 16-byte boundary
+    ("bf16", 650, 1001, "f32", False, True),
+    ("bf16", 7, 3, "bf16", False, True),
+    ("bf16", 9, 1, "f32", True, False),
+    ("f32", 21, 2, "f32", False, True),
+    ("f32", 611, 8189, None, False, True),
+    ("bf16", 2000, 1030, None, True, False),
+    ("bf16", 333, 4500, "bf16", False, True),
 ]
 
 
@@ -124,6 +132,30 @@ def test_forward_and_backward_match_the_formulas(dtype, rows, dim, residual, rms
         assert_close(g["dbias"], dy.sum(0), n * np.abs(dy).sum(0), "dbias")
     else:
         assert g["dbias"] is None
+
+
+@pytest.mark.parametrize("dim", [96, 97])
+def test_tensors_off_a_boundary(dim):
+    """Contiguous tensors that start off a 16-byte boundary give what aligned
+    copies of them give, up to the order of the sums."""
+    t = make("bf16", 40, dim, "bf16")
+
+    def moved(v):
+        buf = torch.empty(v.numel() + 1, dtype=v.dtype, device="cuda")
+        buf[1:] = v.reshape(-1)
+        return buf[1:].view(v.shape)
+
+    y, r, stats = S.norm_fwd(t["x"], t["w"], t["b"], residual=t["res"], want_stats=True)
+    y2, r2, stats2 = S.norm_fwd(moved(t["x"]), moved(t["w"]), moved(t["b"]),
+                                residual=moved(t["res"]), want_stats=True)
+    assert torch.equal(r, r2)
+    assert torch.allclose(y.float(), y2.float(), rtol=2 ** -7, atol=2 ** -14)
+    g = S.norm_bwd(r, t["w"], stats=stats, dy=t["dy"], dr=t["dr"], want_dbias=True)
+    g2 = S.norm_bwd(moved(r), moved(t["w"]), stats=stats, dy=moved(t["dy"]), dr=moved(t["dr"]),
+                    want_dbias=True)
+    assert torch.allclose(g["dx"].float(), g2["dx"].float(), rtol=2 ** -7, atol=2 ** -12)
+    for k in ("dweight", "dbias"):
+        assert torch.allclose(g[k], g2[k], rtol=1e-4, atol=1e-4)
 
 
 @pytest.mark.parametrize("rms", [False, True])
