@@ -15,7 +15,7 @@
 // residual stream; dr_total is the gradient of x and of the residual.
 //
 // Bound by HBM: every tensor is moved once.  A row is held in registers by
-// `tpr` threads (a power of two), NV groups of VEC elements each.  The backward
+// `tpr` threads, NV groups of VEC elements each.  The backward
 // keeps CTAs resident and walks rows, so that every thread sums dw and db of
 // its own columns in registers; the CTAs' sums are written once and added by a
 // second kernel in a fixed order (no atomics).
@@ -30,7 +30,7 @@ namespace ssm {
 namespace {
 
 constexpr int kSms = 152;
-constexpr int kBwdPer = 8;  // backward: elements of a row per thread, up to 512 threads; then twice as many
+constexpr int kBwdPer = 8;  // backward: elements of a row per thread, up to 512 threads
 constexpr int kBwdWarpsPerSm = 20;  // backward: what the registers are shared out for
 __host__ __device__ constexpr int bwd_ctas_per_sm(int threads) {
   return kBwdWarpsPerSm * 32 / threads;
@@ -50,7 +50,7 @@ __device__ __forceinline__ float row_sum(float v, int tpr, float* red) {
   const int warp = threadIdx.x >> 5;
   if ((threadIdx.x & 31) == 0) red[warp] = v;
   __syncthreads();
-  const int first = warp & ~(wpr - 1);
+  const int first = warp / wpr * wpr;
   float a = 0.f;
   for (int i = 0; i < wpr; ++i) a += red[first + i];
   return a;
@@ -135,8 +135,8 @@ template <typename TX, typename TR, int VEC, int NV, bool SHIFT>
 __global__ void __launch_bounds__(VEC * NV == 8 ? 1024 : 512)
     norm_fwd_kernel(const NormParams p, int tpr) {
   __shared__ float red[2][32];
-  int64_t row = static_cast<int64_t>(blockIdx.x) * (blockDim.x / tpr) + threadIdx.x / tpr;
-  const int lane = threadIdx.x & (tpr - 1);
+  const int group = threadIdx.x / tpr, lane = threadIdx.x - group * tpr;
+  int64_t row = static_cast<int64_t>(blockIdx.x) * (blockDim.x / tpr) + group;
   const bool on = row < p.rows;
   row = on ? row : p.rows - 1;  // groups without a row write nothing
   const int dim = static_cast<int>(p.dim);
@@ -233,8 +233,8 @@ __global__ void __launch_bounds__(THREADS, bwd_ctas_per_sm(THREADS))
     norm_bwd_kernel(const NormBwdParams p, int tpr) {
   __shared__ float2 red[2][32];
   __shared__ float acc[THREADS * VEC * NV];
-  const int wpr = tpr >> 5, groups = THREADS / tpr;
-  const int group = threadIdx.x / tpr, lane = threadIdx.x & (tpr - 1);
+  const int wpr = tpr >> 5, groups = blockDim.x / tpr;
+  const int group = threadIdx.x / tpr, lane = threadIdx.x - group * tpr;
   const int dim = static_cast<int>(p.dim);
   const float inv = 1.f / static_cast<float>(dim);
   const bool has_dr = p.dr != nullptr;
@@ -317,7 +317,7 @@ __global__ void __launch_bounds__(THREADS, bwd_ctas_per_sm(THREADS))
       const int warp = threadIdx.x >> 5;
       if ((threadIdx.x & 31) == 0) red[buf][warp] = a;
       __syncthreads();
-      const int first = warp & ~(wpr - 1);
+      const int first = group * wpr;
       a = make_float2(0.f, 0.f);
       for (int i = 0; i < wpr; ++i) {
         a.x += red[buf][first + i].x;
@@ -353,7 +353,7 @@ __global__ void __launch_bounds__(THREADS, bwd_ctas_per_sm(THREADS))
       for (int v = 0; v < VEC; ++v)
         acc[group * span + (i * tpr + lane) * VEC + v] = k == 0 ? dw[i][v] : db[i][v];
     __syncthreads();
-    for (int c = threadIdx.x; c < dim; c += THREADS) {
+    for (int c = threadIdx.x; c < dim; c += blockDim.x) {
       float s = 0.f;
       for (int u = 0; u < groups; ++u) {
         const Cols<VEC, SHIFT> theirs(dim, row0 - group + u, p.rows);
@@ -393,23 +393,27 @@ __global__ void __launch_bounds__(1024) norm_bwd_sum_kernel(const float* partial
 
 bool fits(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
-// Threads per row, a power of two: at most `per` elements of the row per thread.
+// Threads per row: at most `per` elements of the row per thread.  Parts of a warp
+// and pairs of warps share CTAs of 128 threads; wider rows take a CTA of their
+// own of as many warps as they need.
 int threads_per_row(int64_t dim, int per) {
   int t = 8;
-  while (int64_t(t) * per < dim) t *= 2;
+  while (int64_t(t) * per < dim && t < 64) t *= 2;
+  if (int64_t(t) * per < dim) t = static_cast<int>((dim + 32 * per - 1) / (32 * per)) * 32;
   return t;
 }
+int cta_threads(int tpr) { return tpr > 64 ? tpr : 128; }
 
-// Rows are held 8 elements per thread where there are few of them (a row's
-// latency counts), else 16 (fewer threads to synchronise per row).
 // Columns that a row's groups span.
 int64_t span_of(int64_t dim, int vec, bool shift) { return shift ? dim + vec - 1 : dim; }
 
+// Rows are held 8 elements per thread where there are few of them (a row's
+// latency counts), else 16 (fewer threads to synchronise per row).
 template <typename TX, typename TR, int VEC, bool SHIFT>
 cudaError_t norm_fwd_v(const NormParams& p, cudaStream_t s) {
   const int per = p.rows < 4 * kSms ? 8 : 16;
   const int tpr = threads_per_row(span_of(p.dim, VEC, SHIFT), per);
-  const int threads = tpr > 128 ? tpr : 128;
+  const int threads = cta_threads(tpr);
   const int64_t rpb = threads / tpr, blocks = (p.rows + rpb - 1) / rpb;
   if (blocks > 0x7FFFFFFF) return cudaErrorInvalidValue;
   const unsigned g = static_cast<unsigned>(blocks);
@@ -441,16 +445,25 @@ cudaError_t norm_fwd_t(const NormParams& p, cudaStream_t s) {
   }
 }
 
+// The backward's rows: kBwdPer elements per thread up to 512 threads, else twice
+// as many.
 int bwd_threads(int64_t span) {
-  const int t = threads_per_row(span, kBwdPer);
-  return t < 512 ? t : 512;
+  return threads_per_row(span, span <= kBwdPer * 512 ? kBwdPer : 2 * kBwdPer);
 }
 
-int64_t bwd_ctas(int64_t rows, int tpr) {
-  const int threads = tpr > 128 ? tpr : 128;
-  const int64_t groups = threads / tpr, need = (rows + groups - 1) / groups;
+// The bound on a CTA's threads that its kernel is compiled for.
+int bwd_bound(int64_t span, int tpr) {
+  if (span > kBwdPer * 512) return 512;
+  for (int t : {128, 192, 256, 320})
+    if (cta_threads(tpr) <= t) return t;
+  return 512;
+}
+
+int64_t bwd_ctas(int64_t rows, int64_t span) {
+  const int tpr = bwd_threads(span);
+  const int64_t groups = cta_threads(tpr) / tpr, need = (rows + groups - 1) / groups;
   if (need <= 4) return 1;  // a few rows in turn cost less than a second kernel for the sums
-  const int64_t most = int64_t(kSms) * bwd_ctas_per_sm(threads);
+  const int64_t most = int64_t(kSms) * bwd_ctas_per_sm(bwd_bound(span, tpr));
   return need < most ? need : most;
 }
 
@@ -458,17 +471,20 @@ template <typename TX, typename TR, int VEC, bool SHIFT>
 cudaError_t norm_bwd_v(const NormBwdParams& p, cudaStream_t s) {
   constexpr int NV = kBwdPer / VEC;
   const int64_t span = span_of(p.dim, VEC, SHIFT);
-  const int tpr = bwd_threads(span);
-  unsigned g = static_cast<unsigned>(bwd_ctas(p.rows, tpr));
+  const int tpr = bwd_threads(span), threads = cta_threads(tpr);
+  unsigned g = static_cast<unsigned>(bwd_ctas(p.rows, span));
   if (SHIFT) g = (g + VEC - 1) / VEC * VEC;  // the rows' stride a multiple of VEC
-  if (span > kBwdPer * 512)
-    norm_bwd_kernel<TX, TR, VEC, 2 * NV, 512, SHIFT><<<g, 512, 0, s>>>(p, tpr);
-  else if (tpr == 512)
-    norm_bwd_kernel<TX, TR, VEC, NV, 512, SHIFT><<<g, 512, 0, s>>>(p, tpr);
-  else if (tpr == 256)
-    norm_bwd_kernel<TX, TR, VEC, NV, 256, SHIFT><<<g, 256, 0, s>>>(p, tpr);
-  else
-    norm_bwd_kernel<TX, TR, VEC, NV, 128, SHIFT><<<g, 128, 0, s>>>(p, tpr);
+  if (span > kBwdPer * 512) {
+    norm_bwd_kernel<TX, TR, VEC, 2 * NV, 512, SHIFT><<<g, threads, 0, s>>>(p, tpr);
+  } else {
+    switch (bwd_bound(span, tpr)) {
+      case 128: norm_bwd_kernel<TX, TR, VEC, NV, 128, SHIFT><<<g, threads, 0, s>>>(p, tpr); break;
+      case 192: norm_bwd_kernel<TX, TR, VEC, NV, 192, SHIFT><<<g, threads, 0, s>>>(p, tpr); break;
+      case 256: norm_bwd_kernel<TX, TR, VEC, NV, 256, SHIFT><<<g, threads, 0, s>>>(p, tpr); break;
+      case 320: norm_bwd_kernel<TX, TR, VEC, NV, 320, SHIFT><<<g, threads, 0, s>>>(p, tpr); break;
+      default: norm_bwd_kernel<TX, TR, VEC, NV, 512, SHIFT><<<g, threads, 0, s>>>(p, tpr);
+    }
+  }
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || g == 1) return e;
   return launch_after(norm_bwd_sum_kernel,
@@ -499,9 +515,9 @@ cudaError_t launch_norm_fwd(const NormParams& p, bool bf16, bool residual_bf16, 
 
 // The most CTAs any form of the backward launches.
 int64_t norm_bwd_partials(int64_t rows, int64_t dim) {
-  const int64_t a = bwd_ctas(rows, bwd_threads(dim));
-  const int64_t b = (bwd_ctas(rows, bwd_threads(span_of(dim, 8, true))) + 7) / 8 * 8;
-  const int64_t c = (bwd_ctas(rows, bwd_threads(span_of(dim, 4, true))) + 3) / 4 * 4;
+  const int64_t a = bwd_ctas(rows, dim);
+  const int64_t b = (bwd_ctas(rows, span_of(dim, 8, true)) + 7) / 8 * 8;
+  const int64_t c = (bwd_ctas(rows, span_of(dim, 4, true)) + 3) / 4 * 4;
   const int64_t m = a > b ? a : b;
   return m > c ? m : c;
 }
