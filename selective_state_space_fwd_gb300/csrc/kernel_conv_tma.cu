@@ -404,17 +404,20 @@ __global__ void __launch_bounds__(kWarps * 32, kBwdCtas)
 }
 
 // Pieces of whole boxes, with `halo` steps around them: the longest piece for
-// which the slowest warp has least to do.  Only the first piece of a sequence
+// which the slowest warp has least to do, and up to 8 boxes with valid lengths
+// (`masked`), so that a warp has several pieces, live and masked ones (bf16 32 x
+// 2048 x 1536: 60.5 us against 64.2 us with up to 16).  Only the first piece of a sequence
 // may reach into the state, so a piece has at least width - 1 steps.  `rows`:
 // CTAs per slab.  With `alone`, work that a slab's four warps finish in a piece
 // of up to four boxes each goes to one CTA, whose sums need no second kernel.
-Pieces make_pieces(const ConvParams& p, int vec, int ctas, int halo, bool alone, int* rows) {
+Pieces make_pieces(const ConvParams& p, int vec, int ctas, int halo, bool masked, bool alone,
+                   int* rows) {
   Pieces q;
   q.slabs = static_cast<int>((p.dim + 32 * vec - 1) / (32 * vec));
   const int64_t most = int64_t(kSms) * ctas / q.slabs > 0 ? int64_t(kSms) * ctas / q.slabs : 1;
   int64_t least = INT64_MAX;
   q.tc = 0;
-  for (int n = 16; n >= 1; --n) {
+  for (int n = masked ? 8 : 16; n >= 1; --n) {
     const int tc = n * kRows - halo;
     if (tc < p.width - 1) break;
     const int64_t items = p.batch * ((p.seqlen + tc - 1) / tc);
@@ -461,7 +464,7 @@ bool fits(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a
 template <typename T, int K>
 cudaError_t fwd_k(const ConvParams& p, unsigned* err, cudaStream_t s) {
   int rows;
-  const Pieces q = make_pieces(p, 8 / sizeof(T), kFwdCtas, K - 1, false, &rows);
+  const Pieces q = make_pieces(p, 8 / sizeof(T), kFwdCtas, K - 1, p.valid_len != nullptr, false, &rows);
   CUtensorMap mx;
   if (!conv_map(&mx, sizeof(T) == 2, p.x, p, p.x_batch, p.x_step)) return cudaErrorInvalidValue;
   conv_fwd_tma_kernel<T, K><<<q.slabs * rows, kWarps * 32, kFwdSmem, s>>>(mx, p, q, err);
@@ -472,7 +475,8 @@ template <typename T, int K>
 cudaError_t bwd_k(const ConvBwdParams& b, unsigned* err, int* parts, cudaStream_t s) {
   const ConvParams& p = b.fwd;
   int rows;
-  const Pieces q = make_pieces(p, 8 / sizeof(T), kBwdCtas, 2 * (K - 1), true, &rows);
+  const Pieces q = make_pieces(p, 8 / sizeof(T), kBwdCtas, 2 * (K - 1), p.valid_len != nullptr,
+                               true, &rows);
   CUtensorMap mx, mg;
   if (!conv_map(&mx, sizeof(T) == 2, p.x, p, p.x_batch, p.x_step) ||
       !conv_map(&mg, sizeof(T) == 2, b.dy, p, p.seqlen * p.dim, p.dim))
@@ -505,11 +509,12 @@ int64_t conv_bwd_tma_partials(int64_t batch, int64_t seqlen, int64_t dim, int wi
   ConvParams p = {};
   p.batch = batch; p.seqlen = seqlen; p.dim = dim; p.width = width;
   int most = 0;
-  for (int vec : {2, 4}) {
-    int rows;
-    make_pieces(p, vec, kBwdCtas, 2 * (width - 1), true, &rows);
-    most = rows > most ? rows : most;
-  }
+  for (int vec : {2, 4})
+    for (bool masked : {false, true}) {
+      int rows;
+      make_pieces(p, vec, kBwdCtas, 2 * (width - 1), masked, true, &rows);
+      most = rows > most ? rows : most;
+    }
   return most;
 }
 

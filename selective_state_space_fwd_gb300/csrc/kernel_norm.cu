@@ -515,11 +515,13 @@ cudaError_t launch_norm_fwd(const NormParams& p, bool bf16, bool residual_bf16, 
 
 // The most CTAs any form of the backward launches.
 int64_t norm_bwd_partials(int64_t rows, int64_t dim) {
-  const int64_t a = bwd_ctas(rows, dim);
-  const int64_t b = (bwd_ctas(rows, span_of(dim, 8, true)) + 7) / 8 * 8;
-  const int64_t c = (bwd_ctas(rows, span_of(dim, 4, true)) + 3) / 4 * 4;
-  const int64_t m = a > b ? a : b;
-  return m > c ? m : c;
+  int64_t most = bwd_ctas(rows, dim);
+  for (int vec : {4, 8}) {
+    if (dim % vec == 0) continue;
+    const int64_t n = (bwd_ctas(rows, span_of(dim, vec, true)) + vec - 1) / vec * vec;
+    most = n > most ? n : most;
+  }
+  return most;
 }
 
 cudaError_t launch_norm_bwd(const NormBwdParams& p, bool bf16, bool residual_bf16,

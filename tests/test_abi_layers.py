@@ -157,3 +157,19 @@ def test_workspace_sizes(ssmlib):
         bwd = lib.ssm_xent_workspace_bytes(ctypes.byref(s), 1)
         assert 0 < fwd < 2 ** 31 and 0 < bwd < 2 ** 31  # never the logits' size
     assert lib.ssm_xent_workspace_bytes(None, 0) == 0
+
+
+def test_workspaces_cover_every_row_count(ssmlib):
+    """The norm's workspace grows with its rows and never shrinks below what two
+    rows per column take; the convolution's holds at least one partial sum."""
+    lib = Bd.load()
+    for dim in (1, 7, 64, 513, 1536, 8191, 8192):
+        last = 0
+        for rows in (1, 4, 5, 100, 5000, 1 << 20):
+            n = lib.ssm_norm_bwd_workspace_bytes(ctypes.byref(Bd.NormShapes(rows, dim, 0, 0.0, 1, 1)))
+            assert n % (8 * dim) == 0 and n >= last > -1
+            last = n
+    for batch, L, dim, width in ((1, 1, 1, 2), (3, 7, 33, 3), (32, 2048, 1536, 4)):
+        s = Bd.ConvShapes(batch, L, dim, width, L * dim, dim, 1)
+        n = lib.ssm_conv_bwd_workspace_bytes(ctypes.byref(s))
+        assert n >= 4 * (width + 1) * dim and n % (4 * (width + 1) * dim) == 0
