@@ -11,17 +11,38 @@ PyTorch stream without it.
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import torch
 
 from ._binding import ConvShapes, DType, NormShapes, SsmError, XentShapes, _check, load
 
-_CODES = {torch.float32: int(DType.F32), torch.bfloat16: int(DType.BF16)}
+_F32 = torch.float32
+_CODES = {_F32: int(DType.F32), torch.bfloat16: int(DType.BF16)}
 
-# the current stream's handle by device index: a tenth of the cost of building
-# a Stream object, which is a good part of a short call
+# The current stream's handle by device index, and the current device: a tenth of
+# the cost of torch.cuda.current_stream and current_device, which are a good part
+# of a short call.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
+_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
+# The sizes as the library takes them: equal sizes share one structure, which
+# the library only reads.
+@functools.lru_cache(maxsize=512)
+def _conv_sizes(*sizes):
+    return ctypes.byref(ConvShapes(*sizes))
+
+
+@functools.lru_cache(maxsize=512)
+def _norm_sizes(*sizes):
+    return ctypes.byref(NormShapes(*sizes))
+
+
+@functools.lru_cache(maxsize=512)
+def _xent_sizes(*sizes):
+    return ctypes.byref(XentShapes(*sizes))
 
 
 def _code(dtype) -> int:
@@ -34,7 +55,7 @@ def _code(dtype) -> int:
 def _dense(t, name, shape, dtype, dev):
     """The contiguous tensor `t`, checked (the common case without the cost of
     building messages)."""
-    if t.dtype != dtype or t.shape != shape or t.device != dev or not t.is_contiguous():
+    if t.dtype is not dtype or t.shape != shape or t.device != dev or not t.is_contiguous():
         _check(t, name, shape, dtype, dev)
     return t
 
@@ -72,8 +93,9 @@ def _on_stream(stream, f, t, *args, **kw):
 def _call(fn, dev, *args):
     """fn(*args, the current stream of `dev`) on `dev`, raising SsmError on a bad
     status."""
-    handle = _raw_stream(dev.index)
-    if torch.cuda.current_device() == dev.index:
+    index = dev.index
+    handle = _raw_stream(index)
+    if _device() == index:
         st = fn(*args, handle)
     else:
         with torch.cuda.device(dev):
@@ -89,8 +111,8 @@ def _cuda(t, name):
 
 
 def _conv_args(x, weight, bias, silu, rank):
-    """Checked (device, dtype code, sizes, ConvShapes) of a convolution whose x
-    has `rank` dimensions, the last of them contiguous."""
+    """Checked (device, dtype code, batch, seqlen, dim, width, ConvShapes) of a
+    convolution whose x has `rank` dimensions, the last of them contiguous."""
     dev = _cuda(x, "x")
     code = _code(x.dtype)
     size, stride = x.shape, x.stride()
@@ -103,15 +125,16 @@ def _conv_args(x, weight, bias, silu, rank):
         batch, seqlen, dim = size
         step = stride[1] if seqlen > 1 else dim
     else:
-        (batch, dim), seqlen, step = size, 1, size[1]
+        batch, dim = size
+        seqlen, step = 1, dim
     if stride[-1] != 1 and dim > 1:
         raise ValueError("x: the channels must be contiguous")
-    _dense(weight, "weight", (dim, width), torch.float32, dev)
+    _dense(weight, "weight", (dim, width), _F32, dev)
     if bias is not None:
-        _dense(bias, "bias", (dim,), torch.float32, dev)
+        _dense(bias, "bias", (dim,), _F32, dev)
     # the stride of an axis of one element is never used; the row's own length
     # keeps it from deciding the alignment rule
-    return dev, code, (batch, seqlen, dim, width), ConvShapes(
+    return dev, code, batch, seqlen, dim, width, _conv_sizes(
         batch, seqlen, dim, width, stride[0] if batch > 1 else dim, step, 1 if silu else 0)
 
 
@@ -130,7 +153,7 @@ def conv_fwd(x, weight, bias=None, valid_len=None, *, state0=None, silu: bool = 
     if stream is not None:
         return _on_stream(stream, conv_fwd, x, weight, bias, valid_len, state0=state0, silu=silu,
                           want_final=want_final, out=out, out_final=out_final)
-    dev, code, (batch, L, dim, width), shapes = _conv_args(x, weight, bias, silu, 3)
+    dev, code, batch, L, dim, width, sizes = _conv_args(x, weight, bias, silu, 3)
     if valid_len is not None:
         _dense(valid_len, "valid_len", (batch,), torch.int32, dev)
     if state0 is not None:
@@ -140,7 +163,7 @@ def conv_fwd(x, weight, bias=None, valid_len=None, *, state0=None, silu: bool = 
     if want_final or out_final is not None:
         final = _new(out_final, "out_final", (batch, width - 1, dim), x.dtype, dev)
     _call(load().ssm_conv_fwd, dev, x.data_ptr(), weight.data_ptr(), _addr(bias),
-          _addr(valid_len), _addr(state0), y.data_ptr(), _addr(final), ctypes.byref(shapes), code)
+          _addr(valid_len), _addr(state0), y.data_ptr(), _addr(final), sizes, code)
     return y if final is None else (y, final)
 
 
@@ -155,14 +178,14 @@ def conv_bwd(x, weight, bias=None, valid_len=None, *, dy, state0=None, silu: boo
         return _on_stream(stream, conv_bwd, x, weight, bias, valid_len, dy=dy, state0=state0,
                           silu=silu, want_dbias=want_dbias, want_dstate0=want_dstate0,
                           workspace=workspace)
-    dev, code, (batch, L, dim, width), shapes = _conv_args(x, weight, bias, silu, 3)
+    dev, code, batch, L, dim, width, sizes = _conv_args(x, weight, bias, silu, 3)
     if valid_len is not None:
         _dense(valid_len, "valid_len", (batch,), torch.int32, dev)
     if state0 is not None:
         _dense(state0, "state0", (batch, width - 1, dim), x.dtype, dev)
     _dense(dy, "dy", (batch, L, dim), x.dtype, dev)
     lib = load()
-    ws = _workspace(workspace, lib.ssm_conv_bwd_workspace_bytes(ctypes.byref(shapes)), dev)
+    ws = _workspace(workspace, lib.ssm_conv_bwd_workspace_bytes(sizes), dev)
     f32 = dict(dtype=torch.float32, device=dev)
     g = {"dx": torch.empty((batch, L, dim), dtype=x.dtype, device=dev),
          "dweight": torch.empty((dim, width), **f32),
@@ -173,7 +196,7 @@ def conv_bwd(x, weight, bias=None, valid_len=None, *, dy, state0=None, silu: boo
     _call(lib.ssm_conv_bwd, dev, x.data_ptr(), weight.data_ptr(), _addr(bias),
           _addr(valid_len), _addr(state0), dy.data_ptr(), g["dx"].data_ptr(),
           g["dweight"].data_ptr(), _addr(g["dbias"]), _addr(g["dstate0"]), ws.data_ptr(),
-          ws.numel(), ctypes.byref(shapes), code)
+          ws.numel(), sizes, code)
     return g
 
 
@@ -185,11 +208,11 @@ def conv_step(x, weight, bias=None, *, state, silu: bool = True, out=None, strea
     leaves and x becomes the newest.  Returns y [batch, dim]."""
     if stream is not None:
         return _on_stream(stream, conv_step, x, weight, bias, state=state, silu=silu, out=out)
-    dev, code, (batch, _, dim, width), shapes = _conv_args(x, weight, bias, silu, 2)
+    dev, code, batch, _, dim, width, sizes = _conv_args(x, weight, bias, silu, 2)
     _dense(state, "state", (batch, width - 1, dim), x.dtype, dev)
     y = _like(out, "out", x, (batch, dim), dev)
     _call(load().ssm_conv_step, dev, x.data_ptr(), weight.data_ptr(), _addr(bias),
-          state.data_ptr(), y.data_ptr(), ctypes.byref(shapes), code)
+          state.data_ptr(), y.data_ptr(), sizes, code)
     return y
 
 
@@ -201,8 +224,8 @@ def _workspace(workspace, need, dev):
     return workspace
 
 
-def _rows(t):
-    return t.numel() // t.shape[-1] if t.dim() and t.shape[-1] else 0
+def _rows(t, dim):
+    return t.numel() // dim if dim else 0
 
 
 def norm_fwd(x, weight, bias=None, *, residual=None, rms: bool = False, eps: float = 1e-5,
@@ -222,11 +245,13 @@ def norm_fwd(x, weight, bias=None, *, residual=None, rms: bool = False, eps: flo
     dev = _cuda(x, "x")
     code = _code(x.dtype)
     shape = x.shape
-    dim, rows = shape[-1] if x.dim() else 0, _rows(x)
-    _dense(x, "x", shape, x.dtype, dev)
-    _dense(weight, "weight", (dim,), torch.float32, dev)
+    dim = shape[-1] if shape else 0
+    rows = _rows(x, dim)
+    if not x.is_contiguous():
+        raise ValueError("x: must be contiguous")
+    _dense(weight, "weight", (dim,), _F32, dev)
     if bias is not None:
-        _dense(bias, "bias", (dim,), torch.float32, dev)
+        _dense(bias, "bias", (dim,), _F32, dev)
     rcode, r = code, None
     if residual is not None:
         rcode = _code(residual.dtype)
@@ -236,9 +261,9 @@ def norm_fwd(x, weight, bias=None, *, residual=None, rms: bool = False, eps: flo
         raise ValueError("out_r needs a residual")
     y = _like(out, "out", x, shape, dev)
     stats = torch.empty((2, rows), dtype=torch.float32, device=dev) if want_stats else None
-    shapes = NormShapes(rows, dim, int(bool(rms)), eps, code, rcode)
+    sizes = _norm_sizes(rows, dim, 1 if rms else 0, eps, code, rcode)
     _call(load().ssm_norm_fwd, dev, x.data_ptr(), _addr(residual), weight.data_ptr(),
-          _addr(bias), y.data_ptr(), _addr(r), _addr(stats), ctypes.byref(shapes))
+          _addr(bias), y.data_ptr(), _addr(r), _addr(stats), sizes)
     return y, r, stats
 
 
@@ -257,16 +282,18 @@ def norm_bwd(r, weight, *, stats, dy, dr=None, rms: bool = False, want_dbias: bo
     dev = _cuda(r, "r")
     code, rcode = _code(dy.dtype), _code(r.dtype)
     shape = r.shape
-    dim, rows = shape[-1] if r.dim() else 0, _rows(r)
-    _dense(r, "r", shape, r.dtype, dev)
+    dim = shape[-1] if shape else 0
+    rows = _rows(r, dim)
+    if not r.is_contiguous():
+        raise ValueError("r: must be contiguous")
     _dense(dy, "dy", shape, dy.dtype, dev)
-    _dense(weight, "weight", (dim,), torch.float32, dev)
-    _dense(stats, "stats", (2, rows), torch.float32, dev)
+    _dense(weight, "weight", (dim,), _F32, dev)
+    _dense(stats, "stats", (2, rows), _F32, dev)
     if dr is not None:
         _dense(dr, "dr", shape, r.dtype, dev)
     lib = load()
-    shapes = NormShapes(rows, dim, int(bool(rms)), 0.0, code, rcode)
-    ws = _workspace(workspace, lib.ssm_norm_bwd_workspace_bytes(ctypes.byref(shapes)), dev)
+    sizes = _norm_sizes(rows, dim, 1 if rms else 0, 0.0, code, rcode)
+    ws = _workspace(workspace, lib.ssm_norm_bwd_workspace_bytes(sizes), dev)
     f32 = dict(dtype=torch.float32, device=dev)
     dx = torch.empty(shape, dtype=dy.dtype, device=dev)
     dres = torch.empty(shape, dtype=r.dtype, device=dev) if rcode != code else None
@@ -274,13 +301,13 @@ def norm_bwd(r, weight, *, stats, dy, dr=None, rms: bool = False, want_dbias: bo
     dbias = torch.empty((dim,), **f32) if want_dbias else None
     _call(lib.ssm_norm_bwd, dev, r.data_ptr(), weight.data_ptr(), stats.data_ptr(),
           dy.data_ptr(), _addr(dr), dx.data_ptr(), _addr(dres), dweight.data_ptr(), _addr(dbias),
-          ws.data_ptr(), ws.numel(), ctypes.byref(shapes))
+          ws.data_ptr(), ws.numel(), sizes)
     return {"dx": dx, "dresidual": dx if dres is None else dres, "dweight": dweight,
             "dbias": dbias}
 
 
 def _xent_args(h, weight, targets, ignore_index):
-    """Checked (device, dtype code, sizes, XentShapes) of a cross entropy."""
+    """Checked (device, dtype code, tokens, XentShapes) of a cross entropy."""
     dev = _cuda(h, "h")
     code = _code(h.dtype)
     if h.dim() != 2:
@@ -292,7 +319,7 @@ def _xent_args(h, weight, targets, ignore_index):
     _dense(h, "h", (tokens, dim), h.dtype, dev)
     _dense(weight, "weight", (vocab, dim), h.dtype, dev)
     _dense(targets, "targets", (tokens,), torch.int64, dev)
-    return dev, code, (tokens, vocab, dim), XentShapes(tokens, vocab, dim, int(ignore_index))
+    return dev, code, tokens, _xent_sizes(tokens, vocab, dim, int(ignore_index))
 
 
 def xent_fwd(h, weight, targets, *, ignore_index: int = -100, workspace=None, stream=None):
@@ -308,13 +335,13 @@ def xent_fwd(h, weight, targets, *, ignore_index: int = -100, workspace=None, st
     if stream is not None:
         return _on_stream(stream, xent_fwd, h, weight, targets, ignore_index=ignore_index,
                           workspace=workspace)
-    dev, code, (tokens, _, _), shapes = _xent_args(h, weight, targets, ignore_index)
+    dev, code, tokens, sizes = _xent_args(h, weight, targets, ignore_index)
     lib = load()
-    ws = _workspace(workspace, lib.ssm_xent_workspace_bytes(ctypes.byref(shapes), 0), dev)
+    ws = _workspace(workspace, lib.ssm_xent_workspace_bytes(sizes, 0), dev)
     loss = torch.empty((tokens,), dtype=torch.float32, device=dev)
     lse = torch.empty((tokens,), dtype=torch.float32, device=dev)
     _call(lib.ssm_xent_fwd, dev, h.data_ptr(), weight.data_ptr(), targets.data_ptr(),
-          loss.data_ptr(), lse.data_ptr(), ws.data_ptr(), ws.numel(), ctypes.byref(shapes), code)
+          loss.data_ptr(), lse.data_ptr(), ws.data_ptr(), ws.numel(), sizes, code)
     return loss, lse
 
 
@@ -326,13 +353,13 @@ def xent_bwd(h, weight, targets, *, lse, dloss, ignore_index: int = -100, worksp
     if stream is not None:
         return _on_stream(stream, xent_bwd, h, weight, targets, lse=lse, dloss=dloss,
                           ignore_index=ignore_index, workspace=workspace)
-    dev, code, (tokens, _, _), shapes = _xent_args(h, weight, targets, ignore_index)
-    _dense(lse, "lse", (tokens,), torch.float32, dev)
-    _dense(dloss, "dloss", (tokens,), torch.float32, dev)
+    dev, code, tokens, sizes = _xent_args(h, weight, targets, ignore_index)
+    _dense(lse, "lse", (tokens,), _F32, dev)
+    _dense(dloss, "dloss", (tokens,), _F32, dev)
     lib = load()
-    ws = _workspace(workspace, lib.ssm_xent_workspace_bytes(ctypes.byref(shapes), 1), dev)
+    ws = _workspace(workspace, lib.ssm_xent_workspace_bytes(sizes, 1), dev)
     dh, dweight = torch.empty_like(h), torch.empty_like(weight)
     _call(lib.ssm_xent_bwd, dev, h.data_ptr(), weight.data_ptr(), targets.data_ptr(),
           lse.data_ptr(), dloss.data_ptr(), dh.data_ptr(), dweight.data_ptr(), ws.data_ptr(),
-          ws.numel(), ctypes.byref(shapes), code)
+          ws.numel(), sizes, code)
     return {"dh": dh, "dweight": dweight}
