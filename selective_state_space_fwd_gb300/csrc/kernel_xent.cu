@@ -130,12 +130,12 @@ struct Unit {
 // one fewer take the dW tiles that make up for it first.
 template <int MODE>
 struct Work {
-  int mt, nt, vt, kv, kt, splits;
+  int rows, mt, nt, vt, kv, kt, splits;
   int ndh, ndw;              // units of either kind (kLse and kGrad: all are "dh")
   int cluster, clusters;
   int heavy, light, ahead;   // clusters with a dh unit more, without, dW units these take first
   __device__ Work(const GemmArgs& p, int c, int n) : cluster(c), clusters(n) {
-    const int rows = rows_of(p);
+    rows = rows_of(p);
     mt = ceil_div(rows, kTile);
     vt = ceil_div(p.vp, kTile);
     nt = MODE == kProducts ? ceil_div(p.dim, kTile) : vt;
@@ -319,13 +319,14 @@ __device__ __forceinline__ void epilogue_grad(const GemmArgs& p, const Maps& map
 
 // `row`: the warp's first row in the tile.
 __device__ __forceinline__ void epilogue_products(const GemmArgs& p, const Maps& maps, OutBox& out,
-                                                  uint32_t acc, const Unit& u, int row, int mt,
-                                                  bool empty) {
+                                                  uint32_t acc, const Unit& u, int row, int rows,
+                                                  int mt, bool empty) {
   const int c0 = u.n * kTile;
   const int cols = p.dim - c0 < kTile ? static_cast<int>(p.dim - c0) : kTile;
   const int64_t y = u.dw ? p.v0 + static_cast<int64_t>(u.m) * kTile + row
                          : (static_cast<int64_t>(u.split) * mt + u.m) * kTile + row;
-  if (u.dw ? y >= p.vocab : empty && p.add) return;  // nothing to write, or to add
+  // nothing to write, or to add
+  if (u.dw ? y >= p.vocab : u.m * kTile + row >= rows || (empty && p.add)) return;
   const int width = u.dw ? 64 : 32;
   for (int c = 0; c < cols; c += width) {
     uint32_t r[2][32];
@@ -500,10 +501,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       umma::fence_after_sync();
       const uint32_t acc = tm + b * kTile + (static_cast<uint32_t>(q * 32) << 16);
       if (MODE == kLse) epilogue_lse(p, acc, r, t.n, tgt);
-      if (MODE == kGrad)
+      // rows of G past the last kept one are read up to a whole stage of dW's products
+      if (MODE == kGrad && r - lane < (work.rows + kBk - 1) / kBk * kBk)
         epilogue_grad(p, maps, out, acc, static_cast<int>(r) - lane, t.n, tgt, lse2, scale);
       if (MODE == kProducts)
-        epilogue_products(p, maps, out, acc, t, row - lane, work.mt, t.k1 <= t.k0);
+        epilogue_products(p, maps, out, acc, t, row - lane, work.rows, work.mt, t.k1 <= t.k0);
       __syncwarp();
       umma::fence_before_sync();
       __syncwarp();
@@ -899,22 +901,20 @@ __global__ void __launch_bounds__(256) xent_dh_kernel(const GemmArgs p, const in
   wait_previous();
   const int rows = rows_of(p), mt = ceil_div(rows, kTile);
   const int splits = dh_splits(mt, ceil_div(p.dim, kTile), p.kv_whole);
-  const int vec = static_cast<int>(p.dim / 8);
+  const int vec = static_cast<int>(p.dim / 4);
   const int64_t step = static_cast<int64_t>(gridDim.x) * 256, n = static_cast<int64_t>(rows) * vec;
   const int64_t plane = static_cast<int64_t>(mt) * kTile * p.dim;
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < n; i += step) {
-    const int64_t r = i / vec, c = (i - r * vec) * 8;
+    const int64_t r = i / vec, c = (i - r * vec) * 4;
     const float* q = p.dh + r * p.dim + c;
-    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
     for (int s = 0; s < splits; ++s) {
-      const float4 a = reinterpret_cast<const float4*>(q + s * plane)[0];
-      const float4 b = reinterpret_cast<const float4*>(q + s * plane)[1];
-      v[0] += a.x; v[1] += a.y; v[2] += a.z; v[3] += a.w;
-      v[4] += b.x; v[5] += b.y; v[6] += b.z; v[7] += b.w;
+      const float4 a = *reinterpret_cast<const float4*>(q + s * plane);
+      v.x += a.x; v.y += a.y; v.z += a.z; v.w += a.w;
     }
-    *reinterpret_cast<uint4*>(dh + idx[r] * p.dim + c) = make_uint4(
-        pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[4], v[5]), pack2(v[6], v[7]));
+    *reinterpret_cast<uint2*>(dh + idx[r] * p.dim + c) =
+        make_uint2(pack2(v.x, v.y), pack2(v.z, v.w));
   }
 }
 

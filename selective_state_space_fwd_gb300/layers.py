@@ -186,11 +186,10 @@ def conv_bwd(x, weight, bias=None, valid_len=None, *, dy, state0=None, silu: boo
     _dense(dy, "dy", (batch, L, dim), x.dtype, dev)
     lib = load()
     ws = _workspace(workspace, lib.ssm_conv_bwd_workspace_bytes(sizes), dev)
-    f32 = dict(dtype=torch.float32, device=dev)
-    g = {"dx": torch.empty((batch, L, dim), dtype=x.dtype, device=dev),
-         "dweight": torch.empty((dim, width), **f32),
-         "dbias": torch.empty((dim,), **f32) if (bias is not None if want_dbias is None
-                                                 else want_dbias) else None,
+    if want_dbias is None:
+        want_dbias = bias is not None
+    g = {"dx": torch.empty_like(dy), "dweight": torch.empty_like(weight),
+         "dbias": torch.empty((dim,), dtype=_F32, device=dev) if want_dbias else None,
          "dstate0": torch.empty((batch, width - 1, dim), dtype=x.dtype, device=dev)
          if want_dstate0 else None}
     _call(lib.ssm_conv_bwd, dev, x.data_ptr(), weight.data_ptr(), _addr(bias),
@@ -260,7 +259,7 @@ def norm_fwd(x, weight, bias=None, *, residual=None, rms: bool = False, eps: flo
     elif out_r is not None:
         raise ValueError("out_r needs a residual")
     y = _like(out, "out", x, shape, dev)
-    stats = torch.empty((2, rows), dtype=torch.float32, device=dev) if want_stats else None
+    stats = torch.empty((2, rows), dtype=_F32, device=dev) if want_stats else None
     sizes = _norm_sizes(rows, dim, 1 if rms else 0, eps, code, rcode)
     _call(load().ssm_norm_fwd, dev, x.data_ptr(), _addr(residual), weight.data_ptr(),
           _addr(bias), y.data_ptr(), _addr(r), _addr(stats), sizes)
@@ -294,11 +293,10 @@ def norm_bwd(r, weight, *, stats, dy, dr=None, rms: bool = False, want_dbias: bo
     lib = load()
     sizes = _norm_sizes(rows, dim, 1 if rms else 0, 0.0, code, rcode)
     ws = _workspace(workspace, lib.ssm_norm_bwd_workspace_bytes(sizes), dev)
-    f32 = dict(dtype=torch.float32, device=dev)
-    dx = torch.empty(shape, dtype=dy.dtype, device=dev)
-    dres = torch.empty(shape, dtype=r.dtype, device=dev) if rcode != code else None
-    dweight = torch.empty((dim,), **f32)
-    dbias = torch.empty((dim,), **f32) if want_dbias else None
+    dx = torch.empty_like(dy)
+    dres = torch.empty_like(r) if rcode != code else None
+    dweight = torch.empty_like(weight)
+    dbias = torch.empty_like(weight) if want_dbias else None
     _call(lib.ssm_norm_bwd, dev, r.data_ptr(), weight.data_ptr(), stats.data_ptr(),
           dy.data_ptr(), _addr(dr), dx.data_ptr(), _addr(dres), dweight.data_ptr(), _addr(dbias),
           ws.data_ptr(), ws.numel(), sizes)
@@ -338,8 +336,8 @@ def xent_fwd(h, weight, targets, *, ignore_index: int = -100, workspace=None, st
     dev, code, tokens, sizes = _xent_args(h, weight, targets, ignore_index)
     lib = load()
     ws = _workspace(workspace, lib.ssm_xent_workspace_bytes(sizes, 0), dev)
-    loss = torch.empty((tokens,), dtype=torch.float32, device=dev)
-    lse = torch.empty((tokens,), dtype=torch.float32, device=dev)
+    loss = torch.empty((tokens,), dtype=_F32, device=dev)
+    lse = torch.empty((tokens,), dtype=_F32, device=dev)
     _call(lib.ssm_xent_fwd, dev, h.data_ptr(), weight.data_ptr(), targets.data_ptr(),
           loss.data_ptr(), lse.data_ptr(), ws.data_ptr(), ws.numel(), sizes, code)
     return loss, lse
