@@ -95,6 +95,11 @@ struct Maps {
   CUtensorMap a, b, at, bt, h, g, dw, dh;
 };
 
+// Whether the products read h itself: no token is ignored, and there is a whole
+// tile of them.
+__device__ __forceinline__ bool rows_in_place(int64_t rows, int64_t tokens) {
+  return rows == tokens && tokens >= kTile;
+}
 __device__ __forceinline__ int rows_of(const GemmArgs& p) {
   return p.count ? *p.count : static_cast<int>(p.tokens);
 }
@@ -404,7 +409,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     int s = 0;
     uint32_t ph = 1;
     int used = 0;  // stages that hold a copy, at most kStages
-    const bool all = rows_of(p) == p.tokens;
+    const bool all = p.count == nullptr || rows_in_place(rows_of(p), p.tokens);
     const CUtensorMap* ma_map = MODE != kProducts && all ? &maps.h : &maps.a;
     const CUtensorMap* bt_map = all ? &maps.h : &maps.bt;
     Unit t;
@@ -787,7 +792,7 @@ __global__ void __launch_bounds__(kGatherThreads) xent_gather_kernel(const Gathe
     before += before_n[w];
     total += total_n[w];
   }
-  const bool all = total == p.tokens;
+  const bool all = rows_in_place(total, p.tokens);
   const int vec = static_cast<int>(p.dim / 8);
   const int64_t t1 = t0 + p.per < p.tokens ? t0 + p.per : p.tokens;
   for (int64_t c0 = t0; c0 < t1; c0 += kGatherThreads) {
@@ -839,16 +844,20 @@ __global__ void __launch_bounds__(kGatherThreads) xent_gather_kernel(const Gathe
     before += kept;
   }
   if (blockIdx.x == 0 && tid == 0) *p.count = total;
-  // rows past the kept ones, up to a whole tile: shared out among the CTAs
+  // past the kept rows: no target up to a whole tile, and zeros up to a whole
+  // stage of the products that sum over rows
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * kGatherThreads + tid;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kGatherThreads;
   const int64_t end = (static_cast<int64_t>(total) + kTile - 1) / kTile * kTile;
-  for (int64_t r = total + blockIdx.x; r < end; r += gridDim.x) {
-    if (tid == 0) {
-      p.target[r] = -1;
-      if (p.scale) p.lse_rows[r] = p.scale[r] = 0.f;
-    }
-    if (!all)
-      for (int c = tid; c < vec; c += kGatherThreads)
-        reinterpret_cast<uint4*>(p.rows + r * p.dim)[c] = make_uint4(0, 0, 0, 0);
+  for (int64_t r = total + first; r < end; r += step) {
+    p.target[r] = -1;
+    if (p.scale) p.lse_rows[r] = p.scale[r] = 0.f;
+  }
+  if (!all) {
+    const int64_t zeros = ((static_cast<int64_t>(total) + kBk - 1) / kBk * kBk - total) * vec;
+    for (int64_t i = first; i < zeros; i += step)
+      reinterpret_cast<uint4*>(p.rows + static_cast<int64_t>(total) * p.dim)[i] =
+          make_uint4(0, 0, 0, 0);
   }
 }
 
