@@ -18,6 +18,12 @@
 // dW, both kinds of tile in one launch.  dh is summed over the pieces in fp32.
 // 8 T V D operations with the gradients; the tensor cores bound it.
 //
+// Where all tokens have the same dloss (a mean), G is formed without it and the
+// results are multiplied by it in fp32: rounded into G it would be off by up to
+// 2^-8 in the same direction for every token, as p - 1 at the target is nearly
+// -1.  What rounding takes from a token's G at the target is kept in fp32 and
+// put back into its dh.
+//
 // Products: 256 x 256 tiles on pairs of CTAs (umma_pair.cuh), operands by TMA
 // in 64-wide, 128-byte swizzled boxes through a ring of kStages stages, fp32
 // accumulators in tensor memory, two of them so that the epilogue of a tile
@@ -64,15 +70,24 @@ constexpr unsigned kErrXentWait = 8u;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int64_t kPieceBytes = int64_t(512) << 20;  // most bytes of one piece of G
 
+// The dloss that all kept tokens share, or 1 with `shared` 0.
+struct Common {
+  int shared;
+  float dloss;
+};
+
 enum Mode { kLse = 0, kGrad = 1, kProducts = 2 };
 
 struct GemmArgs {
   const int* count;       // rows kept; null: every token is a row
+  const Common* common;   // the tokens' dloss, if it is one
   const int* target;      // [rows] column of the target, -1 for none
   const int64_t* targets;  // the tokens' targets, used without `count`
   int64_t tokens;
   const float* lse;       // [rows], kGrad
   const float* scale;     // [rows] dloss, kGrad
+  float* lost;            // [rows] what rounding took from G at the target (kGrad writes it)
+  const __nv_bfloat16* weight;  // [vocab][dim]
   int64_t vocab, dim;
   int64_t v0;             // first column of the piece
   int vp;                 // columns of the piece
@@ -283,8 +298,9 @@ __device__ __forceinline__ void epilogue_lse(const GemmArgs& p, uint32_t acc, in
 }
 
 __device__ __forceinline__ void epilogue_grad(const GemmArgs& p, const Maps& maps, OutBox& out,
-                                              uint32_t acc, int row0, int n, int tgt, float lse2,
-                                              float scale) {
+                                              uint32_t acc, int64_t row, int n, int tgt,
+                                              float lse2, float scale) {
+  const int row0 = static_cast<int>(row) - static_cast<int>(threadIdx.x & 31);
   const int c0 = n * kTile;
   const int cols = p.vp - c0 < kTile ? p.vp - c0 : kTile;
   const int64_t t64 = static_cast<int64_t>(tgt) - p.v0 - c0;
@@ -304,8 +320,13 @@ __device__ __forceinline__ void epilogue_grad(const GemmArgs& p, const Maps& map
 #pragma unroll
       for (int j = 0; j < 32; ++j) v[j] = ex2(fmaf(__uint_as_float(r[h][j]), kLog2e, -lse2));
       if (static_cast<unsigned>(rel - b) < 32u) {
+        float at = 0.f;
 #pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] -= b + j == rel ? 1.f : 0.f;
+        for (int j = 0; j < 32; ++j) {
+          v[j] -= b + j == rel ? 1.f : 0.f;
+          at = b + j == rel ? v[j] * scale : at;
+        }
+        p.lost[row] = at - __bfloat162float(__float2bfloat16_rn(at));
       }
 #pragma unroll
       for (int j = 0; j < 32; ++j) v[j] *= scale;
@@ -325,7 +346,7 @@ __device__ __forceinline__ void epilogue_grad(const GemmArgs& p, const Maps& map
 // `row`: the warp's first row in the tile.
 __device__ __forceinline__ void epilogue_products(const GemmArgs& p, const Maps& maps, OutBox& out,
                                                   uint32_t acc, const Unit& u, int row, int rows,
-                                                  int mt, bool empty) {
+                                                  int mt, bool empty, float common) {
   const int c0 = u.n * kTile;
   const int cols = p.dim - c0 < kTile ? static_cast<int>(p.dim - c0) : kTile;
   const int64_t y = u.dw ? p.v0 + static_cast<int64_t>(u.m) * kTile + row
@@ -356,7 +377,8 @@ __device__ __forceinline__ void epilogue_products(const GemmArgs& p, const Maps&
           uint32_t w[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            w[i] = pack2(__uint_as_float(r[h][8 * k + 2 * i]), __uint_as_float(r[h][8 * k + 2 * i + 1]));
+            w[i] = pack2(__uint_as_float(r[h][8 * k + 2 * i]) * common,
+                         __uint_as_float(r[h][8 * k + 2 * i + 1]) * common);
           out.put(4 * h + k, w[0], w[1], w[2], w[3]);
         }
     } else {
@@ -487,6 +509,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int q = warp & 3;
     const int row = static_cast<int>(rank) * kHalfTile + q * 32 + lane;
     OutBox out = {base + kOut + (warp - 2) * 2 * kBox, 0};
+    const float common = MODE == kProducts ? p.common->dloss : 1.f;
     Unit t;
     for (int n = 0; !bad && work.at(n, &t); ++n) {
       const int b = n & 1;
@@ -496,7 +519,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (MODE != kProducts) tgt = target_of(p, r);
       if (MODE == kGrad) {
         lse2 = p.lse[r] * kLog2e;
-        scale = p.scale[r];
+        scale = p.common->shared ? (r < work.rows ? 1.f : 0.f) : p.scale[r];
       }
       if (!pair::mbar_wait(acc_full(b), (n >> 1) & 1, kWaitNs)) bad = true;
       if (__any_sync(0xffffffffu, bad)) {
@@ -508,9 +531,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (MODE == kLse) epilogue_lse(p, acc, r, t.n, tgt);
       // rows of G past the last kept one are read up to a whole stage of dW's products
       if (MODE == kGrad && r - lane < (work.rows + kBk - 1) / kBk * kBk)
-        epilogue_grad(p, maps, out, acc, static_cast<int>(r) - lane, t.n, tgt, lse2, scale);
+        epilogue_grad(p, maps, out, acc, r, t.n, tgt, lse2, scale);
       if (MODE == kProducts)
-        epilogue_products(p, maps, out, acc, t, row - lane, work.rows, work.mt, t.k1 <= t.k0);
+        epilogue_products(p, maps, out, acc, t, row - lane, work.rows, work.mt, t.k1 <= t.k0,
+                          common);
       __syncwarp();
       umma::fence_before_sync();
       __syncwarp();
@@ -759,6 +783,7 @@ struct GatherArgs {
   const float* dloss;
   float* lse_rows;
   float* scale;
+  Common* common;
   __nv_bfloat16* dh;
 };
 
@@ -767,24 +792,37 @@ struct GatherArgs {
 __global__ void __launch_bounds__(kGatherThreads) xent_gather_kernel(const GatherArgs p) {
   constexpr int kWarps = kGatherThreads / 32;
   __shared__ int before_n[kWarps], total_n[kWarps], warp_n[kWarps];
+  __shared__ unsigned low_n[kWarps], high_n[kWarps];
   __shared__ int src[kGatherThreads], gone[kGatherThreads];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * p.per;
   release_next();
   int before = 0, total = 0;
+  unsigned low = 0xffffffffu, high = 0u;  // of the bits of the kept tokens' dloss
 #pragma unroll 8
   for (int64_t t = tid; t < p.tokens; t += kGatherThreads) {
-    const int keep = __ldg(p.targets + t) != p.ignore;
+    const int64_t tg = __ldg(p.targets + t);
+    const int keep = tg != p.ignore;
     total += keep;
     before += t < t0 ? keep : 0;
+    if (p.scale && blockIdx.x == 0 && keep) {
+      // a target outside the vocabulary counts as a dloss of its own
+      const unsigned bits = tg >= 0 && tg < p.vocab ? __float_as_uint(__ldg(p.dloss + t)) : ~0u;
+      low = bits < low ? bits : low;
+      high = bits > high ? bits : high;
+    }
   }
   for (int m = 16; m >= 1; m /= 2) {
     before += __shfl_xor_sync(0xffffffffu, before, m);
     total += __shfl_xor_sync(0xffffffffu, total, m);
   }
+  low = __reduce_min_sync(0xffffffffu, low);
+  high = __reduce_max_sync(0xffffffffu, high);
   if (lane == 0) {
     before_n[warp] = before;
     total_n[warp] = total;
+    low_n[warp] = low;
+    high_n[warp] = high;
   }
   __syncthreads();
   before = total = 0;
@@ -843,7 +881,18 @@ __global__ void __launch_bounds__(kGatherThreads) xent_gather_kernel(const Gathe
     }
     before += kept;
   }
-  if (blockIdx.x == 0 && tid == 0) *p.count = total;
+  if (blockIdx.x == 0 && tid == 0) {
+    *p.count = total;
+    if (p.common) {
+      for (int w = 0; w < kWarps; ++w) {
+        low = low_n[w] < low ? low_n[w] : low;
+        high = high_n[w] > high ? high_n[w] : high;
+      }
+      const bool shared = low == high && low != ~0u;
+      p.common->shared = shared;
+      p.common->dloss = shared ? __uint_as_float(low) : 1.f;
+    }
+  }
   // past the kept rows: no target up to a whole tile, and zeros up to a whole
   // stage of the products that sum over rows
   const int64_t first = static_cast<int64_t>(blockIdx.x) * kGatherThreads + tid;
@@ -904,7 +953,8 @@ __global__ void __launch_bounds__(1024) xent_join_kernel(const GemmArgs p, int64
   }
 }
 
-// dh of a token: the sum of the splits' partial sums, rounded once.
+// dh of a token: the sum of the splits' partial sums and of what rounding took
+// from G at the target, rounded once.
 __global__ void __launch_bounds__(256) xent_dh_kernel(const GemmArgs p, const int* idx,
                                                       __nv_bfloat16* dh) {
   wait_previous();
@@ -913,6 +963,7 @@ __global__ void __launch_bounds__(256) xent_dh_kernel(const GemmArgs p, const in
   const int vec = static_cast<int>(p.dim / 4);
   const int64_t step = static_cast<int64_t>(gridDim.x) * 256, n = static_cast<int64_t>(rows) * vec;
   const int64_t plane = static_cast<int64_t>(mt) * kTile * p.dim;
+  const float common = p.common->dloss;
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < n; i += step) {
     const int64_t r = i / vec, c = (i - r * vec) * 4;
     const float* q = p.dh + r * p.dim + c;
@@ -922,14 +973,22 @@ __global__ void __launch_bounds__(256) xent_dh_kernel(const GemmArgs p, const in
       const float4 a = *reinterpret_cast<const float4*>(q + s * plane);
       v.x += a.x; v.y += a.y; v.z += a.z; v.w += a.w;
     }
+    if (const int t = p.target[r]; t >= 0) {
+      const uint2 w = __ldg(reinterpret_cast<const uint2*>(p.weight + t * p.dim + c));
+      const float lost = p.lost[r];
+      v.x = fmaf(lost, __uint_as_float(w.x << 16), v.x);
+      v.y = fmaf(lost, __uint_as_float(w.x & 0xffff0000u), v.y);
+      v.z = fmaf(lost, __uint_as_float(w.y << 16), v.z);
+      v.w = fmaf(lost, __uint_as_float(w.y & 0xffff0000u), v.w);
+    }
     *reinterpret_cast<uint2*>(dh + idx[r] * p.dim + c) =
-        make_uint2(pack2(v.x, v.y), pack2(v.z, v.w));
+        make_uint2(pack2(v.x * common, v.y * common), pack2(v.z * common, v.w * common));
   }
 }
 
 // ---- workspace and launches -------------------------------------------------------
 struct Layout {
-  size_t count, idx, target, target_logit, lse, scale, rows, part, g, dh, total;
+  size_t count, idx, target, target_logit, lse, scale, lost, rows, part, g, dh, total;
   int64_t tpad, piece, pieces, dh_rows;
 };
 
@@ -953,7 +1012,7 @@ Layout layout_of(const XentShape& s, bool backward) {
   l.idx = take(4 * l.tpad);
   l.target = take(4 * l.tpad);
   l.rows = take(2 * l.tpad * s.dim);
-  l.target_logit = l.part = l.lse = l.scale = l.g = l.dh = 0;
+  l.target_logit = l.part = l.lse = l.scale = l.lost = l.g = l.dh = 0;
   l.dh_rows = 0;
   if (!backward) {
     l.target_logit = take(4 * l.tpad);
@@ -963,6 +1022,7 @@ Layout layout_of(const XentShape& s, bool backward) {
   } else {
     l.lse = take(4 * l.tpad);
     l.scale = take(4 * l.tpad);
+    l.lost = take(4 * l.tpad);
     l.g = take(2 * l.tpad * l.piece);
     // splits x rows: with fewer tiles than clusters the splits fill the clusters
     const int64_t nt = (s.dim + kTile - 1) / kTile;
@@ -1079,10 +1139,14 @@ cudaError_t launch_xent_bwd(const XentParams& p, cudaStream_t s) {
   g.dloss = p.dloss;
   g.lse_rows = reinterpret_cast<float*>(ws + l.lse);
   g.scale = reinterpret_cast<float*>(ws + l.scale);
+  g.common = reinterpret_cast<Common*>(ws + l.count + 64);  // `count` holds 256 bytes
   g.dh = static_cast<__nv_bfloat16*>(p.dh);
   GemmArgs a = gemm_args(p, l, ws);
   a.lse = g.lse_rows;
   a.scale = g.scale;
+  a.common = g.common;
+  a.lost = reinterpret_cast<float*>(ws + l.lost);
+  a.weight = static_cast<const __nv_bfloat16*>(p.weight);
   void* piece = ws + l.g;
   a.dh = reinterpret_cast<float*>(ws + l.dh);
   a.kv_whole = ceil_div(l.piece, kBk);

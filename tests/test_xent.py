@@ -297,3 +297,21 @@ def test_refusals():
         with pytest.raises(S.SsmError) as e:
             call()
         assert e.value.status == status
+
+
+@pytest.mark.parametrize("T,scale", [(1, 1.0), (24, 1 / 24), (40, 3.7e-3), (300, 1 / 300), (24, 0.0)])
+def test_a_shared_loss_weight_is_not_rounded(T, scale):
+    """With one dloss for all tokens (a mean) the gradients are within their own
+    rounding and that of the probabilities: no common factor is lost.  The bound
+    is that of `reference` without the rounding of G at the target, p - 1, but for
+    the 2^-9 that it loses when p is not small."""
+    t = make(T, 3001, 256, 0.2 if T > 1 else 0.0, seed=T)
+    t["dloss"] = torch.full((T,), scale, device="cuda")
+    ref = reference(t)
+    got = run(t)
+    for name in ("dh", "dweight"):
+        assert_close(got[name], ref, name)
+        norm = ref[name].norm()
+        off = (got[name].double() - ref[name]).norm()
+        # outputs round by at most 2^-8, 2^-9 on average over a tensor
+        assert off <= 2.0 ** -9 * 1.25 * norm, (name, float(off / norm))
