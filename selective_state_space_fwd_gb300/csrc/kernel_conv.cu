@@ -73,9 +73,10 @@ ConvGrid conv_grid(int64_t batch, int64_t seqlen, int64_t dim, int ctas_per_sm, 
   return g;
 }
 
-template <typename T, int K, int VEC>
+template <typename T, int K>
 __global__ void __launch_bounds__(kConvThreads, kFwdCtas)
     conv_fwd_kernel(const ConvParams p, int tc, int lx, int64_t chunks) {
+  constexpr int VEC = 1;
   const int64_t cv = (static_cast<int64_t>(blockIdx.x) << lx) + (threadIdx.x & ((1 << lx) - 1));
   const int64_t d0 = cv * VEC;
   if (d0 >= p.dim) return;
@@ -138,9 +139,10 @@ __global__ void __launch_bounds__(kConvThreads, kFwdCtas)
   }
 }
 
-template <typename T, int K, int VEC>
+template <typename T, int K>
 __global__ void __launch_bounds__(kConvThreads, kBwdCtas)
     conv_bwd_kernel(const ConvBwdParams q, int tc, int lx, int64_t chunks) {
+  constexpr int VEC = 1;
   const ConvParams& p = q.fwd;
   const int tx = threadIdx.x & ((1 << lx) - 1);
   const int64_t cv = (static_cast<int64_t>(blockIdx.x) << lx) + tx;
@@ -320,8 +322,7 @@ bool fits(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a
 template <typename T, int K>
 cudaError_t conv_fwd_k(const ConvParams& p, cudaStream_t s) {
   const ConvGrid g = conv_grid(p.batch, p.seqlen, p.dim, kFwdCtas, 2);
-  conv_fwd_kernel<T, K, 1>
-      <<<dim3(g.gx, g.gy), kConvThreads, 0, s>>>(p, g.tc, g.lx, g.chunks);
+  conv_fwd_kernel<T, K><<<dim3(g.gx, g.gy), kConvThreads, 0, s>>>(p, g.tc, g.lx, g.chunks);
   return cudaGetLastError();
 }
 
@@ -329,8 +330,7 @@ template <typename T, int K>
 cudaError_t conv_bwd_k(const ConvBwdParams& q, int* parts, cudaStream_t s) {
   const ConvParams& p = q.fwd;
   const ConvGrid g = conv_grid(p.batch, p.seqlen, p.dim, kBwdCtas, 4);
-  conv_bwd_kernel<T, K, 1>
-      <<<dim3(g.gx, g.gy), kConvThreads, 0, s>>>(q, g.tc, g.lx, g.chunks);
+  conv_bwd_kernel<T, K><<<dim3(g.gx, g.gy), kConvThreads, 0, s>>>(q, g.tc, g.lx, g.chunks);
   *parts = static_cast<int>(g.gy);
   return cudaGetLastError();
 }

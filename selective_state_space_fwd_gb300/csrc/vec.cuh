@@ -11,7 +11,7 @@ namespace ssm {
 template <typename T, int VEC> struct Raw {
   static constexpr int kWords = VEC * static_cast<int>(sizeof(T)) / 4;
   static_assert(kWords * 4 == VEC * static_cast<int>(sizeof(T)), "whole 32-bit words");
-  static_assert(kWords <= 2 || kWords % 4 == 0, "accesses of 4, 8 or 16 bytes");
+  static_assert(kWords <= 2 || kWords % 4 == 0, "accesses of up to 16 bytes");
   uint32_t w[kWords];
 };
 template <> struct Raw<float, 1> { float w; };
@@ -27,14 +27,12 @@ __device__ __forceinline__ void raw_zero(Raw<T, VEC>& r) {
   }
 }
 
-// p is aligned to the access (VEC elements, up to 16 bytes).
+// p is aligned to the access: 8 or 16 bytes when VEC > 1.
 template <typename T, int VEC>
 __device__ __forceinline__ Raw<T, VEC> raw_load(const T* p) {
   Raw<T, VEC> r;
   if constexpr (VEC == 1) {
     r.w = __ldg(p);
-  } else if constexpr (Raw<T, VEC>::kWords == 1) {
-    r.w[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
   } else if constexpr (Raw<T, VEC>::kWords == 2) {
     const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
     r.w[0] = v.x; r.w[1] = v.y;
@@ -55,8 +53,6 @@ __device__ __forceinline__ Raw<T, VEC> raw_load_rw(const T* p) {
   Raw<T, VEC> r;
   if constexpr (VEC == 1) {
     r.w = *p;
-  } else if constexpr (Raw<T, VEC>::kWords == 1) {
-    r.w[0] = *reinterpret_cast<const uint32_t*>(p);
   } else if constexpr (Raw<T, VEC>::kWords == 2) {
     const uint2 v = *reinterpret_cast<const uint2*>(p);
     r.w[0] = v.x; r.w[1] = v.y;
@@ -74,8 +70,6 @@ template <typename T, int VEC>
 __device__ __forceinline__ void raw_store(T* p, const Raw<T, VEC>& r) {
   if constexpr (VEC == 1) {
     *p = r.w;
-  } else if constexpr (Raw<T, VEC>::kWords == 1) {
-    *reinterpret_cast<uint32_t*>(p) = r.w[0];
   } else if constexpr (Raw<T, VEC>::kWords == 2) {
     *reinterpret_cast<uint2*>(p) = make_uint2(r.w[0], r.w[1]);
   } else {

@@ -28,8 +28,8 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
 _device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
-# The sizes as the library takes them: equal sizes share one structure, which
-# the library only reads.
+# The sizes as the library takes them: equal sizes share one structure, which the
+# library only reads, and the workspace bytes that follow from them.
 @functools.lru_cache(maxsize=512)
 def _conv_sizes(*sizes):
     return ctypes.byref(ConvShapes(*sizes))
@@ -43,6 +43,21 @@ def _norm_sizes(*sizes):
 @functools.lru_cache(maxsize=512)
 def _xent_sizes(*sizes):
     return ctypes.byref(XentShapes(*sizes))
+
+
+@functools.lru_cache(maxsize=512)
+def _conv_workspace(sizes):
+    return load().ssm_conv_bwd_workspace_bytes(sizes)
+
+
+@functools.lru_cache(maxsize=512)
+def _norm_workspace(sizes):
+    return load().ssm_norm_bwd_workspace_bytes(sizes)
+
+
+@functools.lru_cache(maxsize=512)
+def _xent_workspace(sizes, backward):
+    return load().ssm_xent_workspace_bytes(sizes, backward)
 
 
 def _code(dtype) -> int:
@@ -185,7 +200,7 @@ def conv_bwd(x, weight, bias=None, valid_len=None, *, dy, state0=None, silu: boo
         _dense(state0, "state0", (batch, width - 1, dim), x.dtype, dev)
     _dense(dy, "dy", (batch, L, dim), x.dtype, dev)
     lib = load()
-    ws = _workspace(workspace, lib.ssm_conv_bwd_workspace_bytes(sizes), dev)
+    ws = _workspace(workspace, _conv_workspace(sizes), dev)
     if want_dbias is None:
         want_dbias = bias is not None
     g = {"dx": torch.empty_like(dy), "dweight": torch.empty_like(weight),
@@ -292,7 +307,7 @@ def norm_bwd(r, weight, *, stats, dy, dr=None, rms: bool = False, want_dbias: bo
         _dense(dr, "dr", shape, r.dtype, dev)
     lib = load()
     sizes = _norm_sizes(rows, dim, 1 if rms else 0, 0.0, code, rcode)
-    ws = _workspace(workspace, lib.ssm_norm_bwd_workspace_bytes(sizes), dev)
+    ws = _workspace(workspace, _norm_workspace(sizes), dev)
     dx = torch.empty_like(dy)
     dres = torch.empty_like(r) if rcode != code else None
     dweight = torch.empty_like(weight)
@@ -335,7 +350,7 @@ def xent_fwd(h, weight, targets, *, ignore_index: int = -100, workspace=None, st
                           workspace=workspace)
     dev, code, tokens, sizes = _xent_args(h, weight, targets, ignore_index)
     lib = load()
-    ws = _workspace(workspace, lib.ssm_xent_workspace_bytes(sizes, 0), dev)
+    ws = _workspace(workspace, _xent_workspace(sizes, 0), dev)
     loss = torch.empty((tokens,), dtype=_F32, device=dev)
     lse = torch.empty((tokens,), dtype=_F32, device=dev)
     _call(lib.ssm_xent_fwd, dev, h.data_ptr(), weight.data_ptr(), targets.data_ptr(),
@@ -355,7 +370,7 @@ def xent_bwd(h, weight, targets, *, lse, dloss, ignore_index: int = -100, worksp
     _dense(lse, "lse", (tokens,), _F32, dev)
     _dense(dloss, "dloss", (tokens,), _F32, dev)
     lib = load()
-    ws = _workspace(workspace, lib.ssm_xent_workspace_bytes(sizes, 1), dev)
+    ws = _workspace(workspace, _xent_workspace(sizes, 1), dev)
     dh, dweight = torch.empty_like(h), torch.empty_like(weight)
     _call(lib.ssm_xent_bwd, dev, h.data_ptr(), weight.data_ptr(), targets.data_ptr(),
           lse.data_ptr(), dloss.data_ptr(), dh.data_ptr(), dweight.data_ptr(), ws.data_ptr(),
