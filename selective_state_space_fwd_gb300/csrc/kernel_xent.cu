@@ -510,6 +510,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int row = static_cast<int>(rank) * kHalfTile + q * 32 + lane;
     OutBox out = {base + kOut + (warp - 2) * 2 * kBox, 0};
     const float common = MODE == kProducts ? p.common->dloss : 1.f;
+    const bool shared = MODE == kGrad && p.common->shared;
     Unit t;
     for (int n = 0; !bad && work.at(n, &t); ++n) {
       const int b = n & 1;
@@ -519,7 +520,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (MODE != kProducts) tgt = target_of(p, r);
       if (MODE == kGrad) {
         lse2 = p.lse[r] * kLog2e;
-        scale = p.common->shared ? (r < work.rows ? 1.f : 0.f) : p.scale[r];
+        scale = shared ? (r < work.rows ? 1.f : 0.f) : p.scale[r];
       }
       if (!pair::mbar_wait(acc_full(b), (n >> 1) & 1, kWaitNs)) bad = true;
       if (__any_sync(0xffffffffu, bad)) {
@@ -798,18 +799,23 @@ __global__ void __launch_bounds__(kGatherThreads) xent_gather_kernel(const Gathe
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * p.per;
   release_next();
   int before = 0, total = 0;
-  unsigned low = 0xffffffffu, high = 0u;  // of the bits of the kept tokens' dloss
 #pragma unroll 8
   for (int64_t t = tid; t < p.tokens; t += kGatherThreads) {
-    const int64_t tg = __ldg(p.targets + t);
-    const int keep = tg != p.ignore;
+    const int keep = __ldg(p.targets + t) != p.ignore;
     total += keep;
     before += t < t0 ? keep : 0;
-    if (p.scale && blockIdx.x == 0 && keep) {
+  }
+  unsigned low = 0xffffffffu, high = 0u;  // of the bits of the kept tokens' dloss
+  if (p.common && blockIdx.x == 0) {
+#pragma unroll 8
+    for (int64_t t = tid; t < p.tokens; t += kGatherThreads) {
+      const int64_t tg = __ldg(p.targets + t);
+      const unsigned dloss = __float_as_uint(__ldg(p.dloss + t));
       // a target outside the vocabulary counts as a dloss of its own
-      const unsigned bits = tg >= 0 && tg < p.vocab ? __float_as_uint(__ldg(p.dloss + t)) : ~0u;
-      low = bits < low ? bits : low;
-      high = bits > high ? bits : high;
+      const unsigned bits = tg >= 0 && tg < p.vocab ? dloss : 0xffffffffu;
+      const bool keep = tg != p.ignore;
+      low = keep && bits < low ? bits : low;
+      high = keep && bits > high ? bits : high;
     }
   }
   for (int m = 16; m >= 1; m /= 2) {
