@@ -32,7 +32,7 @@
 // Clusters are persistent and take tiles in turn.
 //
 // Measured on GB300: values of 4096 tokens x 50257 x 1536 in 323 us, 1.96
-// PFLOP/s; with gradients, 8192 x 65536 x 2048 in 5.06 ms, 1.74 PFLOP/s (the
+// PFLOP/s; with gradients, 8192 x 65536 x 2048 in 5.02 ms, 1.75 PFLOP/s (the
 // power limit: a cuBLAS loop sustains 1.74), 1000 tokens, half of them ignored, x
 // 32001 x 768 in 113 us, 0.87 PFLOP/s (short launches: fill, drain and uneven
 // last tiles).  Eight epilogue warps instead of four, and 4 or 5 stages instead
