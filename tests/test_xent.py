@@ -315,3 +315,87 @@ def test_a_shared_loss_weight_is_not_rounded(T, scale):
         off = (got[name].double() - ref[name]).norm()
         # outputs round by at most 2^-8, 2^-9 on average over a tensor
         assert off <= 2.0 ** -9 * 1.25 * norm, (name, float(off / norm))
+
+
+@pytest.mark.parametrize("T", [8, 40])
+def test_a_vocabulary_past_32_bits(T):
+    """More than 2^31 elements in the weight and its gradient.  All of its rows
+    but the last 300 are zero, so the exact values need those alone.  To the
+    bounds at the top comes the sum of as many equal exponentials: at most 512
+    additions one after the other (256 columns, then the tiles' sums), 2^-24
+    of the sum each."""
+    D, n = 2048, 300
+    V = 2 ** 31 // D + n
+    t = make(T, n, D, seed=5)
+    w = torch.zeros(V, D, dtype=torch.bfloat16, device="cuda")
+    w[-n:] = t["w"]
+    t["targets"] += V - n
+    t["targets"][0] = 0
+    got = run(dict(t, w=w))
+    S.check_device_errors()
+    h, wt, g = t["h"].double(), t["w"].double(), t["dloss"].double()
+    s = h @ wt.T
+    e = D * 2.0 ** -23 * (h.abs() @ wt.abs().T).amax(1)
+    long = 512 * 2.0 ** -24
+    lse = torch.log(torch.exp(s).sum(1) + (V - n))
+    at = (t["targets"] - (V - n)).clamp_min(0)[:, None]
+    logit = torch.where(t["targets"] == 0, 0.0, s.gather(1, at)[:, 0])
+    small = 2.0 ** -20 * (1 + lse.abs() + logit.abs()) + long
+    for name, ref, bound in (("lse", lse, e + small), ("loss", lse - logit, 2 * e + small)):
+        assert ((got[name].double() - ref).abs() <= bound).all(), name
+    off_p = (2 * e + long + 2.0 ** -20)[:, None]
+
+    def grads(p, hit):
+        G = p * g[:, None]
+        eG = G.abs() * off_p
+        G = G - hit * g[:, None]
+        return G, eG + 2.0 ** -8 * (G.abs() + eG)
+
+    zero = torch.zeros(T, 2, dtype=torch.double, device="cuda")  # the vocabulary's first row, another zero one
+    zero[0, 0] = 1.0
+    tail = torch.zeros_like(s).scatter_(1, at, (t["targets"] > 0).double()[:, None])
+    Gz, eGz = grads(torch.exp(-lse)[:, None].expand(T, 2), zero)
+    Gt, eGt = grads(torch.exp(s - lse[:, None]), tail)
+
+    def check(got, G, eG, a, terms, name):
+        ref = G @ a
+        bound = eG @ a.abs() + terms * 2.0 ** -23 * (G.abs() @ a.abs())
+        bound = bound + 2.0 ** -8 * (ref.abs() + bound)
+        off = (got.double() - ref).abs() - bound
+        assert (off <= 0).all(), f"{name}: {off.max().item():.3e} over its bound"
+
+    check(got["dh"], Gt, eGt, wt, V, "dh")
+    check(got["dweight"][-n:], Gt.T, eGt.T, h, T, "dweight")
+    check(got["dweight"][:1], Gz[:, :1].T, eGz[:, :1].T, h, T, "dweight, first row")
+    same = got["dweight"][1:2]
+    check(same, Gz[:, 1:].T, eGz[:, 1:].T, h, T, "dweight, a zero row")
+    assert (got["dweight"][1:-n] == same).all()
+
+
+@pytest.mark.parametrize("ignored", [False, True])
+def test_tokens_past_32_bits(ignored):
+    """More than 2^31 elements in h and its gradient; all rows of h but the last
+    ones are zero, and where `ignored` out of the loss."""
+    D, V, n = 2048, 512, 70
+    T = 2 ** 31 // D + n
+    small = make(n + 30, V, D, seed=6)
+    small["h"][:30] = 0
+    small["dloss"][:] = 2.0 ** -10
+    if ignored:
+        small["targets"][:30] = IGNORE
+    g = torch.Generator(device="cuda").manual_seed(7)
+    t = {"h": torch.zeros(T, D, dtype=torch.bfloat16, device="cuda"), "w": small["w"],
+         "targets": torch.full((T,), IGNORE, device="cuda") if ignored else
+                    torch.randint(0, V, (T,), generator=g, device="cuda"),
+         "dloss": torch.full((T,), 2.0 ** -10, device="cuda")}
+    t["h"][-n:] = small["h"][-n:]
+    sample = torch.cat([torch.arange(30, device="cuda"), torch.arange(T - n, T, device="cuda")])
+    t["targets"][sample] = small["targets"]
+    ref = reference(small)
+    got = run(t)
+    S.check_device_errors()
+    for name in ("loss", "lse", "dh"):
+        assert_close(got[name][sample], ref, name)
+    assert_close(got["dweight"], ref, "dweight")
+    if ignored:
+        assert (got["dh"][:-n] == 0).all() and (got["loss"][:-n] == 0).all()
