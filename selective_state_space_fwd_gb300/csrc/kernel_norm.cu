@@ -193,8 +193,9 @@ __global__ void __launch_bounds__(VEC * NV == 8 ? 1024 : 512)
   for (int i = 0; i < NV; ++i) {
     const int c = cols.at(i * tpr + lane);
     cols.each(c, [&](int v, auto in) {
-      f[i][v] -= mean;
-      q = fmaf(in ? f[i][v] : 0.f, f[i][v], q);
+      // a dropped element may be another row's NaN: neither factor is taken from it
+      f[i][v] = in ? f[i][v] - mean : 0.f;
+      q = fmaf(f[i][v], f[i][v], q);
     });
   }
   const float rstd = rsqrtf(row_sum(q, tpr, red[1]) * inv + p.eps);
