@@ -299,7 +299,7 @@ __device__ __forceinline__ void epilogue_lse(const GemmArgs& p, uint32_t acc, in
 
 __device__ __forceinline__ void epilogue_grad(const GemmArgs& p, const Maps& maps, OutBox& out,
                                               uint32_t acc, int64_t row, int n, int tgt,
-                                              float lse2, float scale) {
+                                              float lse2, float scale, bool kept) {
   const int row0 = static_cast<int>(row) - static_cast<int>(threadIdx.x & 31);
   const int c0 = n * kTile;
   const int cols = p.vp - c0 < kTile ? p.vp - c0 : kTile;
@@ -330,6 +330,10 @@ __device__ __forceinline__ void epilogue_grad(const GemmArgs& p, const Maps& map
       }
 #pragma unroll
       for (int j = 0; j < 32; ++j) v[j] *= scale;
+      if (!kept) {  // zeros, whatever the products of no token's row gave (0 inf = NaN)
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] = 0.f;
+      }
       if (b + 32 > cols) {  // columns past the vocabulary take no part in dh
 #pragma unroll
         for (int j = 0; j < 32; ++j) v[j] = b + j < cols ? v[j] : 0.f;
@@ -520,7 +524,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (MODE != kProducts) tgt = target_of(p, r);
       if (MODE == kGrad) {
         lse2 = p.lse[r] * kLog2e;
-        scale = shared ? (r < work.rows ? 1.f : 0.f) : p.scale[r];
+        scale = shared ? 1.f : p.scale[r];
       }
       if (!pair::mbar_wait(acc_full(b), (n >> 1) & 1, kWaitNs)) bad = true;
       if (__any_sync(0xffffffffu, bad)) {
@@ -532,7 +536,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (MODE == kLse) epilogue_lse(p, acc, r, t.n, tgt);
       // rows of G past the last kept one are read up to a whole stage of dW's products
       if (MODE == kGrad && r - lane < (work.rows + kBk - 1) / kBk * kBk)
-        epilogue_grad(p, maps, out, acc, r, t.n, tgt, lse2, scale);
+        epilogue_grad(p, maps, out, acc, r, t.n, tgt, lse2, scale, r < work.rows);
       if (MODE == kProducts)
         epilogue_products(p, maps, out, acc, t, row - lane, work.rows, work.mt, t.k1 <= t.k0,
                           common);
