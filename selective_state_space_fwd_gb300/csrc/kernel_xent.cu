@@ -41,6 +41,7 @@
 #include <cuda_bf16.h>
 
 #include "common.cuh"
+#include "f32x2.cuh"
 #include "layers.h"
 #include "pdl.cuh"
 #include "ssd.h"
@@ -67,7 +68,6 @@ constexpr int kThreads = 192;
 constexpr int kEpilogueWarps = 4;
 constexpr uint64_t kWaitNs = 2000000000ull;  // a wait gives up after 2 s
 constexpr unsigned kErrXentWait = 8u;
-constexpr float kLn2 = 0.6931471805599453f;
 constexpr int64_t kPieceBytes = int64_t(512) << 20;  // most bytes of one piece of G
 
 // The dloss that all kept tokens share, or 1 with `shared` 0.
@@ -92,7 +92,7 @@ struct GemmArgs {
   int64_t v0;             // first column of the piece
   int vp;                 // columns of the piece
   int kv_whole;           // kProducts: stages of a whole piece's columns
-  float2* part;           // kLse: [tiles of columns][part_pitch] maximum (log2 units), sum
+  float2* part;           // kLse: [tiles of columns][part_pitch] maximum, sum of exp(logit - maximum)
   int64_t part_pitch;
   float* target_logit;    // kLse: [rows]
   float* dh;              // kProducts: [splits][rows, whole tiles][dim] partial sums
@@ -257,6 +257,28 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
+// Softmax statistics are kept in the logits' own units, so that a maximum is a
+// logit, not the rounding of one, and exp(v - max) is taken of the rounded
+// difference: never above 1, and 0 for a logit that a mask has put far below the
+// others, or at -infinity.  (exp2(v log2(e) - max') with a fused product and a
+// rounded max' is infinite where max' is off by more than 128: for logits past
+// 10^9.)
+
+// What exponents are taken from: the maximum, or 0 while all there is is
+// -infinity, whose exponentials are then 0.
+__device__ __forceinline__ float origin(float m) { return m == -INFINITY ? 0.f : m; }
+
+// v = exp(v - from).
+__device__ __forceinline__ void exponentials(float (&v)[32], float from) {
+  float a[32];
+#pragma unroll
+  for (int j = 0; j < 32; ++j) a[j] = -from;
+  vadd<32>(v, v, a);
+  vscale<32>(v, v, kLog2e);
+#pragma unroll
+  for (int j = 0; j < 32; ++j) v[j] = ex2(v[j]);
+}
+
 // The epilogue of one thread: row `row` of the tile, whose 256 columns are the
 // TMEM columns from `acc`.
 __device__ __forceinline__ void epilogue_lse(const GemmArgs& p, uint32_t acc, int64_t row, int n,
@@ -286,12 +308,13 @@ __device__ __forceinline__ void epilogue_lse(const GemmArgs& p, uint32_t acc, in
     float top[4] = {v[0], v[1], v[2], v[3]};
 #pragma unroll
     for (int j = 4; j < 32; ++j) top[j & 3] = fmaxf(top[j & 3], v[j]);
-    const float cm = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * kLog2e;
-    const float nm = fmaxf(m, cm);
+    const float nm = fmaxf(m, fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])));
+    const float from = origin(nm);
+    exponentials(v, from);
     float s[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int j = 0; j < 32; ++j) s[j & 3] += ex2(fmaf(v[j], kLog2e, -nm));
-    l = fmaf(l, ex2(m - nm), (s[0] + s[1]) + (s[2] + s[3]));
+    for (int j = 0; j < 32; ++j) s[j & 3] += v[j];
+    l = fmaf(l, ex2((m - from) * kLog2e), (s[0] + s[1]) + (s[2] + s[3]));
     m = nm;
   }
   p.part[static_cast<int64_t>(n) * p.part_pitch + row] = make_float2(m, l);
@@ -593,8 +616,8 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
 // Merges (maximum, sum) pairs of a softmax's denominator.
 __device__ __forceinline__ void merge(float& m, float& l, const float2 v) {
   const float nm = fmaxf(m, v.x);
-  if (nm == -INFINITY && l == 0.f && v.y == 0.f) return;  // nothing on either side
-  l = l * ex2(m - nm) + v.y * ex2(v.x - nm);
+  const float from = origin(nm);
+  l = l * ex2((m - from) * kLog2e) + v.y * ex2((v.x - from) * kLog2e);
   m = nm;
 }
 
@@ -721,10 +744,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float x = __uint_as_float(r[j]);
           if (in && tgt_s[c + j] == v) p.target_logit[c + j] = x;
           // one exponential: of the distance between the maximum so far and x
-          const float s = x * kLog2e, d = s - m[c + j], e = ex2(-fabsf(d));
-          if (in && s != -INFINITY) {
+          const float d = x - m[c + j], e = ex2(-fabsf(d) * kLog2e);
+          if (in && x != -INFINITY) {
             l[c + j] = d > 0.f ? fmaf(l[c + j], e, 1.f) : l[c + j] + e;
-            m[c + j] = fmaxf(m[c + j], s);
+            m[c + j] = fmaxf(m[c + j], x);
           }
         }
       }
@@ -957,7 +980,7 @@ __global__ void __launch_bounds__(1024) xent_join_kernel(const GemmArgs p, int64
   if (lane == 0 && row < rows_of(p)) {
     const int64_t t = idx ? idx[row] : row;
     const bool none = !p.count && p.targets[t] == ignore;
-    const float s = kLn2 * (m + log2f(l));
+    const float s = m + logf(l);
     lse[t] = none ? 0.f : s;
     loss[t] = none ? 0.f : target_of(p, row) >= 0 ? s - p.target_logit[row] : NAN;
   }

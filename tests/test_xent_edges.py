@@ -50,3 +50,44 @@ def test_an_infinite_weight_leaves_the_gradient_finite(T, value):
         assert_close(got["dh"][:, first:], ref, "dh")
         assert_close(got["dweight"][left], ref, "dweight")
         assert (got["dweight"][7] == 0).all()
+
+
+def spans(V):
+    """Masked stretches: the first columns of the vocabulary, a whole tile of 256, a
+    stretch that starts or ends inside a tile, the vocabulary's end, all but one."""
+    return {"first 32": [(0, 32)], "first tile": [(0, 256)], "first 40": [(0, 40)],
+            "middle": [(256, 300), (512, 800)], "end": [(V - 70, V)],
+            "all but one": [(0, 600), (601, V)], "every second": [(i, i + 1) for i in range(0, V, 2)]}
+
+
+def masked(T, V, D, stretches, value, seed):
+    t = make(T, V, D, seed=seed)
+    t["h"][:, 0] = 1.0
+    t["w"][:, 0] = 0.0
+    out = torch.zeros(V, dtype=torch.bool, device="cuda")
+    for a, b in stretches:
+        out[a:b] = True
+    t["w"][out, 0] = value
+    left = torch.nonzero(~out)[:, 0]
+    t["targets"] = left[t["targets"] % left.numel()]
+    place = torch.cumsum((~out).long(), 0) - 1
+    small = dict(t, w=t["w"][left].contiguous(), targets=place[t["targets"]])
+    return t, out, left, small
+
+
+@pytest.mark.parametrize("value", [-math.inf, LOWEST, -1e30, -1e10, -9e9])
+@pytest.mark.parametrize("where", list(spans(1000)))
+@pytest.mark.parametrize("T", [12, 40, 300])
+def test_masked_vocabulary(T, where, value):
+    V, D = 1000, 64
+    t, out, left, small = masked(T, V, D, spans(V)[where], value, seed=T)
+    ref = reference(small)
+    got = run(t)
+    for name in ("loss", "lse"):
+        assert_close(got[name], ref, name)
+    # an infinite weight makes dh of its own feature 0 * inf; the others stand
+    first = 1 if math.isinf(value) else 0
+    ref["dh"], ref["dh_bound"] = ref["dh"][:, first:], ref["dh_bound"][:, first:]
+    assert_close(got["dh"][:, first:], ref, "dh")
+    assert_close(got["dweight"][left], ref, "dweight")
+    assert (got["dweight"][out] == 0).all()
