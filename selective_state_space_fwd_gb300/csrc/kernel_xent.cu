@@ -980,9 +980,11 @@ __global__ void __launch_bounds__(1024) xent_join_kernel(const GemmArgs p, int64
   if (lane == 0 && row < rows_of(p)) {
     const int64_t t = idx ? idx[row] : row;
     const bool none = !p.count && p.targets[t] == ignore;
-    const float s = m + logf(l);
-    lse[t] = none ? 0.f : s;
-    loss[t] = none ? 0.f : target_of(p, row) >= 0 ? s - p.target_logit[row] : NAN;
+    const float s = logf(l);  // l >= 1: the maximum's own term
+    lse[t] = none ? 0.f : m + s;
+    // of the difference to the maximum: a certain token's loss, far below an ulp of
+    // lse, keeps its digits and is never negative
+    loss[t] = none ? 0.f : target_of(p, row) >= 0 ? s + (m - p.target_logit[row]) : NAN;
   }
 }
 

@@ -91,3 +91,53 @@ def test_masked_vocabulary(T, where, value):
     assert_close(got["dh"][:, first:], ref, "dh")
     assert_close(got["dweight"][left], ref, "dweight")
     assert (got["dweight"][out] == 0).all()
+
+
+def exact_logits(T, V, top, seed, D=64):
+    """Logits that are exact in fp32 whatever the order of the sums: one feature is 1
+    and all others 0, so that S[t, v] = weight[v, 0].  The targets' entry is at `top`,
+    the others 16 to 40 below."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    h = torch.zeros(T, D, dtype=torch.bfloat16, device="cuda")
+    h[:, 0] = 1.0
+    w = torch.zeros(V, D, dtype=torch.bfloat16, device="cuda")
+    w[:, 0] = top - 16 - torch.randint(0, 4, (V,), generator=g, device="cuda") * 8
+    target = int(torch.randint(0, V, (1,), generator=g, device="cuda"))
+    w[target, 0] = top
+    assert (w[:, 0] % 8 == 0).all()  # no entry was rounded: bf16 steps by 8 up to 2048
+    return {"h": h, "w": w, "targets": torch.full((T,), target, device="cuda"),
+            "dloss": torch.randn(T, generator=g, device="cuda")}
+
+
+@pytest.mark.parametrize("top", [0.0, 40.0, -1024.0, 1024.0])
+@pytest.mark.parametrize("T,V", [(3, 1000), (40, 1000), (300, 700), (20, 1), (50, 1)])
+def test_a_certain_tokens_loss_keeps_its_digits(T, V, top):
+    """Losses of 1e-5 under an lse of up to 1024: never negative, and within the
+    rounding of the sum of exponentials, not of lse.  The sum is 1 and less than
+    2^-9; each of its additions is off by at most 2^-24 and at most 64 follow one
+    another (1000 columns in steps of 32 and the joins), each exponential by 2^-20
+    of itself."""
+    t = exact_logits(T, V, top, seed=V + T)
+    loss, lse = S.xent_fwd(t["h"], t["w"], t["targets"])
+    s = t["w"][:, 0].double()
+    # log sum exp(s - top) without the top entry's 1, which log1p takes apart
+    rest = torch.exp(s - top).sum() - 1.0
+    want = torch.log1p(rest)
+    assert (loss >= 0).all()
+    assert ((loss.double() - want).abs() <= 64 * 2.0 ** -24 + 2.0 ** -20 * want).all()
+    assert ((lse.double() - (top + want)).abs() <= 64 * 2.0 ** -24 + 2.0 ** -22 * abs(top)).all()
+
+
+@pytest.mark.parametrize("T", [3, 40, 300])
+@pytest.mark.parametrize("level", [LOWEST, -1e30, -1e10, 1e10, 1e30])
+def test_a_vocabulary_that_is_masked_as_a_whole(T, level):
+    """All logits equal, at the mask's value: the loss is the vocabulary's logarithm,
+    not the difference of two numbers of the mask's size."""
+    V = 1000
+    t = make(T, V, 64, seed=T)
+    t["h"][:, 1:] = 0
+    t["h"][:, 0] = 1.0
+    t["w"][:, 0] = level
+    loss, lse = S.xent_fwd(t["h"], t["w"], t["targets"])
+    assert ((loss.double() - math.log(V)).abs() <= 2.0 ** -18).all()
+    assert (lse == t["w"][0, 0].float()).all()
