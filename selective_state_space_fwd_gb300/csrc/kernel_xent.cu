@@ -322,7 +322,7 @@ __device__ __forceinline__ void epilogue_lse(const GemmArgs& p, uint32_t acc, in
 
 __device__ __forceinline__ void epilogue_grad(const GemmArgs& p, const Maps& maps, OutBox& out,
                                               uint32_t acc, int64_t row, int n, int tgt,
-                                              float lse2, float scale, bool kept) {
+                                              float lse, float scale, bool kept) {
   const int row0 = static_cast<int>(row) - static_cast<int>(threadIdx.x & 31);
   const int c0 = n * kTile;
   const int cols = p.vp - c0 < kTile ? p.vp - c0 : kTile;
@@ -341,7 +341,8 @@ __device__ __forceinline__ void epilogue_grad(const GemmArgs& p, const Maps& map
       const int b = c + 32 * h;
       float v[32];
 #pragma unroll
-      for (int j = 0; j < 32; ++j) v[j] = ex2(fmaf(__uint_as_float(r[h][j]), kLog2e, -lse2));
+      for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[h][j]);
+      exponentials(v, lse);
       if (static_cast<unsigned>(rel - b) < 32u) {
         float at = 0.f;
 #pragma unroll
@@ -543,10 +544,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const int b = n & 1;
       const int64_t r = static_cast<int64_t>(t.m) * kTile + row;
       int tgt = -1;
-      float lse2 = 0.f, scale = 0.f;
+      float lse = 0.f, scale = 0.f;
       if (MODE != kProducts) tgt = target_of(p, r);
       if (MODE == kGrad) {
-        lse2 = p.lse[r] * kLog2e;
+        lse = p.lse[r];
         scale = shared ? 1.f : p.scale[r];
       }
       if (!pair::mbar_wait(acc_full(b), (n >> 1) & 1, kWaitNs)) bad = true;
@@ -559,7 +560,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (MODE == kLse) epilogue_lse(p, acc, r, t.n, tgt);
       // rows of G past the last kept one are read up to a whole stage of dW's products
       if (MODE == kGrad && r - lane < (work.rows + kBk - 1) / kBk * kBk)
-        epilogue_grad(p, maps, out, acc, r, t.n, tgt, lse2, scale, r < work.rows);
+        epilogue_grad(p, maps, out, acc, r, t.n, tgt, lse, scale, r < work.rows);
       if (MODE == kProducts)
         epilogue_products(p, maps, out, acc, t, row - lane, work.rows, work.mt, t.k1 <= t.k0,
                           common);

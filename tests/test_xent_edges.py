@@ -141,3 +141,34 @@ def test_a_vocabulary_that_is_masked_as_a_whole(T, level):
     loss, lse = S.xent_fwd(t["h"], t["w"], t["targets"])
     assert ((loss.double() - math.log(V)).abs() <= 2.0 ** -18).all()
     assert (lse == t["w"][0, 0].float()).all()
+
+
+@pytest.mark.parametrize("T", [3, 40, 300])
+@pytest.mark.parametrize("level", [-1e30, -1e10, -3.3e9, 3.3e9, 1e10, 1e30])
+def test_gradients_of_logits_far_from_0(T, level):
+    """G is dloss (exp(S - lse) - onehot) of the lse that the forward returned: with
+    one entry at `level` and the others, at twice the distance from 0 below it, of
+    probability 0, dweight is -dloss h at the targets and dloss h at that entry."""
+    V, D = 600, 64
+    t = make(T, V, D, seed=T)
+    t["h"][:, 1:] = 0
+    t["h"][:, 0] = 1.0
+    t["w"][:, 1:] = 0
+    t["w"][:, 0] = 2 * level if level < 0 else -level
+    t["w"][77, 0] = level
+    t["targets"][t["targets"] == 77] = 78
+    for dloss in (t["dloss"], torch.full_like(t["dloss"], 0.25)):
+        got = run(dict(t, dloss=dloss))
+        assert (got["lse"] == t["w"][77, 0].float()).all()
+        at = torch.zeros(V, dtype=torch.double, device="cuda")
+        at.index_add_(0, t["targets"], -dloss.double())
+        at[77] = dloss.double().sum()
+        size = torch.zeros_like(at).index_add_(0, t["targets"], dloss.double().abs())
+        size[77] = dloss.double().abs().sum()
+        # bf16 G, at most 2^-8 of each term, and the result's own rounding
+        assert ((got["dweight"][:, 0].double() - at).abs() <= 2 * 2.0 ** -8 * size).all()
+        assert (got["dweight"][:, 1:] == 0).all()
+        # dh of feature 0: dloss (w[77] - w[target]), each term rounded in G
+        want = dloss.double() * (t["w"][77, 0].double() - t["w"][t["targets"], 0].double())
+        size = dloss.double().abs() * (abs(t["w"][77, 0].double()) + t["w"][t["targets"], 0].double().abs())
+        assert ((got["dh"][:, 0].double() - want).abs() <= 2 * 2.0 ** -8 * size).all()
