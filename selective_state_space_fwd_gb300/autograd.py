@@ -6,12 +6,47 @@ chunk boundary states the backward replays from, and its backward
 (``scan_bwd``) when autograd asks for gradients: the recompute scheme of [P1]
 s3.4 (only the chunk states are stored between the two passes).  This module
 only passes tensors between PyTorch and the C ABI; every step of both passes
-runs in the library's kernels.
+runs in the library's kernels.  The gradients themselves have no derivatives:
+differentiating them again (after create_graph=True) raises a RuntimeError.
 """
+import functools
+
 import torch
 
 from ._binding import scan_bwd, scan_fwd
 from .layers import conv_bwd, conv_fwd, norm_bwd, norm_fwd, xent_bwd, xent_fwd
+
+
+class _Final(torch.autograd.Function):
+    """Passes gradients on, tied to the tensors they were computed from, and refuses
+    to be differentiated."""
+
+    @staticmethod
+    def forward(ctx, name, count, *tensors):
+        ctx.name = name
+        return tuple(None if t is None else t.detach() for t in tensors[count:])
+
+    @staticmethod
+    def backward(ctx, *grads):
+        raise RuntimeError(f"{ctx.name}: its gradients cannot be differentiated again")
+
+
+def _once(name):
+    """Marks the backward of the function that users call `name`.  With
+    create_graph=True its results depend on the incoming gradients and on what the
+    forward saved, which PyTorch cannot see inside a kernel: without the mark a
+    second derivative would take them for constants, silently."""
+    def mark(backward):
+        @functools.wraps(backward)
+        def marked(ctx, *grads):
+            with torch.no_grad():
+                out = backward(ctx, *grads)
+            if not torch.is_grad_enabled():
+                return out
+            tied = [t for t in (*grads, *ctx.saved_tensors) if t is not None and t.requires_grad]
+            return _Final.apply(name, len(tied), *tied, *out) if tied else out
+        return marked
+    return mark
 
 
 class _SelectiveScan(torch.autograd.Function):
@@ -23,6 +58,7 @@ class _SelectiveScan(torch.autograd.Function):
         return y
 
     @staticmethod
+    @_once("selective_scan")
     def backward(ctx, dy):
         x, delta, A, B, C, D, z, valid_len, h0, states = ctx.saved_tensors
         want_dh0 = h0 is not None and ctx.needs_input_grad[8]
@@ -52,6 +88,7 @@ class _CausalConv(torch.autograd.Function):
         return conv_fwd(x, weight, bias, valid_len, state0=state0, silu=silu)
 
     @staticmethod
+    @_once("causal_conv")
     def backward(ctx, dy):
         x, weight, bias, valid_len, state0 = ctx.saved_tensors
         g = conv_bwd(x, weight, bias, valid_len, dy=dy.contiguous(), state0=state0, silu=ctx.silu,
@@ -76,6 +113,7 @@ class _LayerNorm(torch.autograd.Function):
         return y, r
 
     @staticmethod
+    @_once("layer_norm")
     def backward(ctx, dy, dr):
         r, weight, stats = ctx.saved_tensors
         dy = torch.zeros(r.shape, dtype=ctx.x_dtype, device=r.device) if dy is None else dy
@@ -102,6 +140,7 @@ class _CrossEntropy(torch.autograd.Function):
         return loss
 
     @staticmethod
+    @_once("linear_cross_entropy")
     def backward(ctx, dloss):
         h, weight, targets, lse = ctx.saved_tensors
         g = xent_bwd(h, weight, targets, lse=lse, dloss=dloss.contiguous(),
