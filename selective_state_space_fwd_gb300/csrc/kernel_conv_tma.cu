@@ -1,6 +1,6 @@
 // kernel_conv_tma.cu -- the short causal convolution (conv.cuh has the
 // formulas) with its rows staged by TMA, for tensors whose rows start on 16-byte
-// boundaries.
+// boundaries and whose strides a tensor map takes (axes_of).
 //
 // Work split: a warp owns a slab of 256 bytes of channels (8 bytes per lane) and
 // walks pieces of sequences, a piece after another: boxes of kRows steps x 256
@@ -48,6 +48,7 @@ struct Pieces {
   int segs;         // pieces per batch row
   int slabs;        // slabs of channels
   int64_t items;    // pieces of a slab: batch x segs
+  bool time_last;   // x's map has the axes (channel, batch, time), not (channel, time, batch)
 };
 
 // One piece of one batch row.
@@ -104,11 +105,14 @@ struct Ring {
       const int s = filled % STAGES;
       const uint32_t bar = bars + 8 * s;
       umma::mbar_expect_tx(bar, NT * kBoxBytes);
+      const int t = static_cast<int>(piece.t0) - (K - 1) + box * kRows;
+      const int b = static_cast<int>(piece.b);
 #pragma unroll
-      for (int i = 0; i < NT; ++i)
-        umma::tma_load_3d(base + (s * NT + i) * kBoxBytes, map[i], x,
-                          static_cast<int>(piece.t0) - (K - 1) + box * kRows,
-                          static_cast<int>(piece.b), bar);
+      for (int i = 0; i < NT; ++i) {
+        const bool swap = i == 0 && q.time_last;
+        umma::tma_load_3d(base + (s * NT + i) * kBoxBytes, map[i], x, swap ? b : t, swap ? t : b,
+                          bar);
+      }
     }
     ++box;
     ++filled;
@@ -417,7 +421,7 @@ __global__ void __launch_bounds__(kWarps * 32, kBwdCtas)
 // of up to four boxes each goes to one CTA, whose sums need no second kernel.
 Pieces make_pieces(const ConvParams& p, int vec, int ctas, int halo, bool masked, bool alone,
                    int* rows) {
-  Pieces q;
+  Pieces q = {};
   q.slabs = static_cast<int>((p.dim + 32 * vec - 1) / (32 * vec));
   const int64_t most = int64_t(kSms) * ctas / q.slabs > 0 ? int64_t(kSms) * ctas / q.slabs : 1;
   int64_t least = INT64_MAX;
@@ -446,17 +450,45 @@ Pieces make_pieces(const ConvParams& p, int vec, int ctas, int halo, bool masked
   return q;
 }
 
-// A [batch, seqlen, dim] tensor copied in boxes of kRows steps x 256 bytes.
-bool conv_map(CUtensorMap* m, bool bf16, const void* base, const ConvParams& p, int64_t batch_stride,
-              int64_t step_stride) {
+// A [batch, seqlen, dim] tensor's axes in the order in which a tensor map takes
+// them: every stride a multiple of the one before, and the first no less than a
+// row of channels.  An axis of one element goes last, whatever its stride.
+struct Axes {
+  bool ok, time_last;
+  int64_t inner, outer;  // strides in elements
+};
+
+Axes axes_of(const ConvParams& p, int64_t batch_stride, int64_t step_stride) {
+  Axes a;
+  if (p.batch == 1) {
+    a.time_last = false;
+    a.inner = p.seqlen > 1 ? step_stride : p.dim;
+    a.outer = a.inner * p.seqlen;
+  } else if (p.seqlen == 1) {
+    a.time_last = true;
+    a.inner = batch_stride;
+    a.outer = batch_stride * p.batch;
+  } else {
+    a.time_last = batch_stride < step_stride;
+    a.inner = a.time_last ? batch_stride : step_stride;
+    a.outer = a.time_last ? step_stride : batch_stride;
+  }
+  a.ok = a.inner >= p.dim && a.outer % a.inner == 0;
+  return a;
+}
+
+// The same, copied in boxes of kRows steps x 256 bytes.
+bool conv_map(CUtensorMap* m, bool bf16, const void* base, const ConvParams& p, const Axes& a) {
   const EncodeTiledFn fn = encode_tiled();
   if (!fn) return false;
   const unsigned size = bf16 ? 2 : 4;
-  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(p.dim), static_cast<cuuint64_t>(p.seqlen),
-                              static_cast<cuuint64_t>(p.batch)};
-  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(step_stride) * size,
-                                 static_cast<cuuint64_t>(batch_stride) * size};
-  const cuuint32_t box[3] = {kRowBytes / size, kRows, 1};
+  const cuuint64_t time = static_cast<cuuint64_t>(p.seqlen), batch = static_cast<cuuint64_t>(p.batch);
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(p.dim), a.time_last ? batch : time,
+                              a.time_last ? time : batch};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(a.inner) * size,
+                                 static_cast<cuuint64_t>(a.outer) * size};
+  const cuuint32_t rows = kRows;
+  const cuuint32_t box[3] = {kRowBytes / size, a.time_last ? 1 : rows, a.time_last ? rows : 1};
   const cuuint32_t estr[3] = {1, 1, 1};
   return fn(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3,
             const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
@@ -469,9 +501,11 @@ bool fits(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a
 template <typename T, int K>
 cudaError_t fwd_k(const ConvParams& p, unsigned* err, cudaStream_t s) {
   int rows;
-  const Pieces q = make_pieces(p, 8 / sizeof(T), kFwdCtas, K - 1, p.valid_len != nullptr, false, &rows);
+  Pieces q = make_pieces(p, 8 / sizeof(T), kFwdCtas, K - 1, p.valid_len != nullptr, false, &rows);
+  const Axes ax = axes_of(p, p.x_batch, p.x_step);
+  q.time_last = ax.time_last;
   CUtensorMap mx;
-  if (!conv_map(&mx, sizeof(T) == 2, p.x, p, p.x_batch, p.x_step)) return cudaErrorInvalidValue;
+  if (!conv_map(&mx, sizeof(T) == 2, p.x, p, ax)) return cudaErrorInvalidValue;
   conv_fwd_tma_kernel<T, K><<<q.slabs * rows, kWarps * 32, kFwdSmem, s>>>(mx, p, q, err);
   return cudaGetLastError();
 }
@@ -480,11 +514,13 @@ template <typename T, int K>
 cudaError_t bwd_k(const ConvBwdParams& b, unsigned* err, int* parts, cudaStream_t s) {
   const ConvParams& p = b.fwd;
   int rows;
-  const Pieces q = make_pieces(p, 8 / sizeof(T), kBwdCtas, 2 * (K - 1), p.valid_len != nullptr,
-                               true, &rows);
+  Pieces q = make_pieces(p, 8 / sizeof(T), kBwdCtas, 2 * (K - 1), p.valid_len != nullptr, true,
+                         &rows);
+  const Axes ax = axes_of(p, p.x_batch, p.x_step);
+  q.time_last = ax.time_last;
+  const Axes ag = {true, false, p.dim, p.seqlen * p.dim};
   CUtensorMap mx, mg;
-  if (!conv_map(&mx, sizeof(T) == 2, p.x, p, p.x_batch, p.x_step) ||
-      !conv_map(&mg, sizeof(T) == 2, b.dy, p, p.seqlen * p.dim, p.dim))
+  if (!conv_map(&mx, sizeof(T) == 2, p.x, p, ax) || !conv_map(&mg, sizeof(T) == 2, b.dy, p, ag))
     return cudaErrorInvalidValue;
   auto* k = conv_bwd_tma_kernel<T, K>;
   const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -500,8 +536,8 @@ cudaError_t bwd_k(const ConvBwdParams& b, unsigned* err, int* parts, cudaStream_
 bool conv_tma_ok(const ConvParams& p, bool bf16) {
   const int64_t es = bf16 ? 2 : 4;
   const int64_t lim = int64_t(1) << 30, stride = int64_t(1) << 38;
-  return (p.dim * es) % 16 == 0 && (p.x_step * es) % 16 == 0 && (p.x_batch * es) % 16 == 0 &&
-         p.x_step > 0 && p.x_batch > 0 && p.x_step < stride && p.x_batch < stride &&
+  const Axes a = axes_of(p, p.x_batch, p.x_step);
+  return a.ok && (p.dim * es) % 16 == 0 && (a.inner * es) % 16 == 0 && a.outer < stride &&
          p.dim <= lim && p.seqlen <= lim && p.batch <= lim && p.seqlen * p.dim < stride &&
          fits(p.x, 16) && fits(p.weight, 16) && fits(p.y, 8) && fits(p.state0, 8) &&
          fits(p.out_final, 8);
