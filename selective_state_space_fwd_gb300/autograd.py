@@ -151,11 +151,13 @@ class _CrossEntropy(torch.autograd.Function):
 def linear_cross_entropy(h, weight, targets, *, ignore_index: int = -100, reduction: str = "mean"):
     """Softmax cross entropy over the vocabulary of the logits h weight^T, which
     are never kept (as ``xent_fwd``), differentiable in h and weight.  h: bf16
-    [..., dim], targets: int64 [...].  ``reduction``: "mean" over the tokens that
+    [..., dim], targets: int64 [...] or flat, [tokens].  ``reduction``: "mean" over the tokens that
     are not ignored (0 when all are), "sum", or "none" for the losses like
     targets."""
     if reduction not in ("mean", "sum", "none"):
         raise ValueError(f"reduction: {reduction!r}, expected 'mean', 'sum' or 'none'")
+    if targets.dim() != 1 and targets.shape != h.shape[:-1]:
+        raise ValueError(f"targets: shape {tuple(targets.shape)}, expected {tuple(h.shape[:-1])}")
     loss = _CrossEntropy.apply(h.reshape(-1, h.shape[-1]), weight, targets.reshape(-1),
                                int(ignore_index))
     if reduction == "none":

@@ -172,3 +172,17 @@ def test_gradients_of_logits_far_from_0(T, level):
         want = dloss.double() * (t["w"][77, 0].double() - t["w"][t["targets"], 0].double())
         size = dloss.double().abs() * (abs(t["w"][77, 0].double()) + t["w"][t["targets"], 0].double().abs())
         assert ((got["dh"][:, 0].double() - want).abs() <= 2 * 2.0 ** -8 * size).all()
+
+
+def test_targets_in_another_order_of_axes_are_refused():
+    """Targets [length, batch] for h [batch, length, dim] have the right number of
+    elements in the wrong places."""
+    t = make(60, 200, 64)
+    h, targets = t["h"].view(3, 20, 64), t["targets"].view(3, 20)
+    want = S.linear_cross_entropy(h, t["w"], targets)
+    assert torch.equal(S.linear_cross_entropy(h, t["w"], t["targets"]), want)  # flat, in order
+    for wrong in (targets.T, targets.reshape(20, 3), targets[:, :10], targets[None]):
+        with pytest.raises(ValueError):
+            S.linear_cross_entropy(h, t["w"], wrong)
+    with pytest.raises(ValueError):
+        S.linear_cross_entropy(h, t["w"], t["targets"][:59])
