@@ -67,3 +67,20 @@ def test_layouts_of_x(name, B, L, D, batch, step, masked, dtype):
         step_y = S.conv_step(t["x"][:, 0], t["w"], t["b"], state=state)
         if not masked:
             assert torch.equal(step_y, y[:, 0]) and torch.equal(state, final)
+
+
+@pytest.mark.parametrize("dtype,B,D", [("bf16", 1021, 2048), ("bf16", 1022, 2048), ("bf16", 1023, 2048),
+                                       ("bf16", 1024, 2048), ("f32", 1023, 1024), ("f32", 1024, 1024),
+                                       ("bf16", 700, 2048), ("f32", 513, 1000)])
+@pytest.mark.parametrize("K", [2, 3, 4])
+def test_steps_of_large_batches(dtype, B, D, K):
+    """Single steps whose threads hold one batch row or four, with remainders of one
+    to three rows: the bits of conv_fwd from the same state."""
+    t = make(dtype, B, 1, D, K, bias=K != 3, carry=True, seed=K)
+    for silu in (True, False):
+        want, final = S.conv_fwd(t["x"], t["w"], t["b"], state0=t["state0"], silu=silu, want_final=True)
+        guard = torch.full((3, K - 1, D), 7.0, dtype=t["state0"].dtype, device="cuda")
+        held = torch.cat([t["state0"], guard])
+        y = S.conv_step(t["x"][:, 0], t["w"], t["b"], state=held[:B], silu=silu)
+        assert torch.equal(y, want[:, 0]) and torch.equal(held[:B], final)
+        assert (held[B:] == 7).all()  # nothing is written past the last row

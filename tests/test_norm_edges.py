@@ -5,6 +5,7 @@ import torch
 
 import selective_state_space_fwd_gb300 as S
 from test_norm import make
+from test_norm import test_forward_and_backward_match_the_formulas as formulas
 
 pytestmark = pytest.mark.gpu
 
@@ -55,3 +56,27 @@ def test_a_row_of_nan_or_infinities_stays_apart(dtype, dim, stream, rms):
             for k, v in want.items():
                 if v is not None:
                     assert torch.equal(got[k][keep], v[keep]), (k, rows, bad)
+
+
+@pytest.mark.parametrize("rows", [5, 900])
+@pytest.mark.parametrize("dim", [1300, 1700, 2561, 3000, 4089, 4096])
+@pytest.mark.parametrize("dtype,residual", [("f32", "f32"), ("bf16", "bf16"), ("bf16", "f32")])
+def test_wide_rows_match_the_formulas(dtype, residual, dim, rows):
+    """Row lengths that take the backward's CTAs of 161 to 512 threads with 8 columns
+    each."""
+    formulas(dtype, rows, dim, residual, rms=dim % 2 == 1, bias=True)
+
+
+@pytest.mark.parametrize("dtype,residual", [("f32", "f32"), ("bf16", "bf16"), ("bf16", "f32")])
+@pytest.mark.parametrize("dim", [1, 3, 97, 1001, 1537, 4089, 8189])
+def test_in_place_stream_off_a_boundary(dtype, residual, dim):
+    """The stream updated in place where groups of columns reach into the rows before
+    and after, which other threads are writing."""
+    rows = 3001 if dim < 2000 else 1200
+    t = make(dtype, rows, dim, residual)
+    y, r, stats = S.norm_fwd(t["x"], t["w"], t["b"], residual=t["res"], want_stats=True)
+    for _ in range(5):
+        res = t["res"].clone()
+        y2, r2, stats2 = S.norm_fwd(t["x"], t["w"], t["b"], residual=res, out_r=res, want_stats=True)
+        assert r2.data_ptr() == res.data_ptr()
+        assert torch.equal(r2, r) and torch.equal(y2, y) and torch.equal(stats2, stats)

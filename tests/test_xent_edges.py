@@ -12,7 +12,7 @@ import pytest
 import torch
 
 import selective_state_space_fwd_gb300 as S
-from test_xent import assert_close, make, reference, run
+from test_xent import IGNORE, assert_close, make, reference, run
 
 pytestmark = pytest.mark.gpu
 
@@ -186,3 +186,36 @@ def test_targets_in_another_order_of_axes_are_refused():
             S.linear_cross_entropy(h, t["w"], wrong)
     with pytest.raises(ValueError):
         S.linear_cross_entropy(h, t["w"], t["targets"][:59])
+
+
+@pytest.mark.parametrize("shared", [False, True])
+def test_seams_of_the_vocabulary(shared):
+    """Several pieces of the vocabulary, with nearly all of each token's probability on
+    one column beside a seam: the first and last columns of pieces, tiles and the
+    vocabulary.  A column lost or doubled there is an error of the size of dh
+    itself."""
+    T, V, D = 8000, 70001, 64
+    rows = (T + 255) // 256 * 256
+    most = (512 << 20) // (2 * rows) // 256                   # tiles of 256 columns in a piece of 512 MiB
+    tiles = (V + 255) // 256
+    pieces = -(-tiles // most)
+    step = -(-tiles // pieces) * 256
+    assert pieces > 2
+    at = [0, 255, 256, V - 1, V // 64 * 64 - 1] + [c + d for c in range(step, V, step) for d in (-1, 0)]
+    at = torch.tensor(sorted(set(at)), device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(11)
+    w = (torch.randint(0, 2, (V, D), generator=g, device="cuda") * 2 - 1).to(torch.bfloat16)
+    column = at[torch.arange(T, device="cuda") % len(at)]
+    t = {"h": w[column] * 0.5, "w": w, "targets": torch.randint(0, V, (T,), generator=g, device="cuda"),
+         "dloss": torch.full((T,), 1.0 / T, device="cuda") if shared else
+                  torch.randn(T, generator=g, device="cuda")}
+    t["targets"] = torch.where(t["targets"] == column, (column + 1000) % V, t["targets"])
+    t["targets"][5::50] = IGNORE
+    ref, got = reference(t), run(t)
+    for name in ("loss", "lse", "dh", "dweight"):
+        assert_close(got[name], ref, name)
+    if shared:
+        for name in ("dh", "dweight"):
+            off = (got[name].double() - ref[name]).norm()
+            # outputs round by at most 2^-8, 2^-9 on average over a tensor
+            assert off <= 2.0 ** -9 * 1.25 * ref[name].norm(), name
