@@ -77,9 +77,8 @@ ConvGrid conv_grid(int64_t batch, int64_t seqlen, int64_t dim, int ctas_per_sm, 
 template <typename T, int K>
 __global__ void __launch_bounds__(kConvThreads, kFwdCtas)
     conv_fwd_kernel(const ConvParams p, int tc, int lx, int64_t chunks) {
-  constexpr int VEC = 1;
-  const int64_t cv = (static_cast<int64_t>(blockIdx.x) << lx) + (threadIdx.x & ((1 << lx) - 1));
-  const int64_t d0 = cv * VEC;
+  constexpr int VEC = 1;  // channels per thread
+  const int64_t d0 = (static_cast<int64_t>(blockIdx.x) << lx) + (threadIdx.x & ((1 << lx) - 1));
   if (d0 >= p.dim) return;
   const int64_t ty = kConvThreads >> lx, items = p.batch * chunks;
   float w[K][VEC], bv[VEC];
@@ -143,22 +142,17 @@ __global__ void __launch_bounds__(kConvThreads, kFwdCtas)
 template <typename T, int K>
 __global__ void __launch_bounds__(kConvThreads, kBwdCtas)
     conv_bwd_kernel(const ConvBwdParams q, int tc, int lx, int64_t chunks) {
-  constexpr int VEC = 1;
+  constexpr int VEC = 1;  // channels per thread
   const ConvParams& p = q.fwd;
   const int tx = threadIdx.x & ((1 << lx) - 1);
-  const int64_t cv = (static_cast<int64_t>(blockIdx.x) << lx) + tx;
-  const int64_t d0 = cv * VEC;
+  const int64_t d0 = (static_cast<int64_t>(blockIdx.x) << lx) + tx;
   const bool on = d0 < p.dim;
   const int ty = kConvThreads >> lx;
   const int64_t items = on ? p.batch * chunks : 0;
   release_next();
-  float w[K][VEC], bv[VEC], dw[K][VEC], db[VEC];
+  float w[K][VEC], bv[VEC], dw[K][VEC], db[VEC] = {0.f};
 #pragma unroll
-  for (int v = 0; v < VEC; ++v) {
-    db[v] = 0.f;
-#pragma unroll
-    for (int k = 0; k < K; ++k) dw[k][v] = 0.f;
-  }
+  for (int k = 0; k < K; ++k) dw[k][0] = 0.f;
   if (on) load_taps<K, VEC>(p.weight, p.bias, d0, w, bv);
   for (int64_t it = static_cast<int64_t>(blockIdx.y) * ty + (threadIdx.x >> lx); it < items;
        it += static_cast<int64_t>(gridDim.y) * ty) {
@@ -175,8 +169,7 @@ __global__ void __launch_bounds__(kConvThreads, kBwdCtas)
     float win[K - 1][VEC], dp[K - 1][VEC];
 #pragma unroll
     for (int k = 0; k < K - 1; ++k) {
-#pragma unroll
-      for (int v = 0; v < VEC; ++v) win[k][v] = dp[k][v] = 0.f;
+      win[k][0] = dp[k][0] = 0.f;
       if (nl > 0)
         widen<VEC>(t0 > 0 ? raw_load<T, VEC>(x - (K - 1 - k) * p.x_step)
                           : state_row<T, K, VEC>(p.state0, b, p.dim, d0, k),
@@ -222,25 +215,21 @@ __global__ void __launch_bounds__(kConvThreads, kBwdCtas)
 #pragma unroll 1
     for (; i < nl; ++i, x += p.x_step, gy += p.dim)
       step(i, raw_load<T, VEC>(x), raw_load<T, VEC>(gy));
-    float none[VEC];
-#pragma unroll
-    for (int v = 0; v < VEC; ++v) none[v] = 0.f;
+    const float none[VEC] = {0.f};
 #pragma unroll 1
     for (; i < n + K - 1; ++i) emit(i, none);
   }
 
   // sums over the CTA's time slots: quantity k < K is tap k, quantity K the bias
-  __shared__ float red[kConvThreads * VEC];
-  const int cx = 1 << lx, wide = cx * VEC;
+  __shared__ float red[kConvThreads];
+  const int wide = 1 << lx;
 #pragma unroll
   for (int k = 0; k <= K; ++k) {
     __syncthreads();
-#pragma unroll
-    for (int v = 0; v < VEC; ++v)
-      red[(threadIdx.x >> lx) * wide + tx * VEC + v] = k < K ? dw[k < K ? k : 0][v] : db[v];
+    red[threadIdx.x] = k < K ? dw[k < K ? k : 0][0] : db[0];
     __syncthreads();
     for (int i = threadIdx.x; i < wide; i += kConvThreads) {
-      const int64_t d = (static_cast<int64_t>(blockIdx.x) << lx) * VEC + i;
+      const int64_t d = (static_cast<int64_t>(blockIdx.x) << lx) + i;
       float a = 0.f;
       for (int j = 0; j < ty; ++j) a += red[j * wide + i];
       if (d >= p.dim) continue;
