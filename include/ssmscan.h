@@ -365,7 +365,8 @@ typedef struct {
  *               can be passed in place.
  *   weight    : device fp32 [dim, width].  bias: fp32 [dim] or NULL.
  *   valid_len : device int32 [batch] or NULL; clamped to [0, seqlen] on the
- *               device.  Steps past it are not read.
+ *               device.  What x holds past it has no effect (whole boxes of
+ *               steps may be copied: the memory has to be there).
  *   state0    : device, dtype `dtype`, [batch, width-1, dim] or NULL.
  *   out_y     : device, dtype `dtype`, [batch, seqlen, dim], contiguous.
  *   out_final : device, dtype `dtype`, [batch, width-1, dim] or NULL: the last
@@ -382,8 +383,8 @@ ssm_status ssm_conv_fwd(const void* x, const float* weight, const float* bias,
 /*
  * ssm_conv_bwd -- every gradient of sum(dy * y) for ssm_conv_fwd on the same
  * inputs (pre is formed again from x).
- *   dy      : device, dtype `dtype`, [batch, seqlen, dim], contiguous; not read
- *             past valid_len.
+ *   dy      : device, dtype `dtype`, [batch, seqlen, dim], contiguous; what it
+ *             holds past valid_len has no effect.
  *   dx      : device, dtype `dtype`, [batch, seqlen, dim], contiguous; 0 past
  *             valid_len.
  *   dweight : device fp32 [dim, width].  dbias: fp32 [dim] or NULL.
@@ -498,8 +499,8 @@ ssm_status ssm_xent_fwd(const void* h, const void* weight, const int64_t* target
  *   dh = G weight,   dweight = G^T h,
  * formed in pieces of the vocabulary (G rounded to bf16 as an operand of the
  * two products, which accumulate in fp32).
- *   lse     : the forward's out_lse.   dloss : device fp32 [tokens], not read
- *             for ignored tokens.
+ *   lse     : the forward's out_lse.   dloss : device fp32 [tokens], without
+ *             effect for ignored tokens.
  *   dh      : device bf16 [tokens, dim], 16-byte aligned; 0 for ignored tokens.
  *   dweight : device bf16 [vocab, dim], 16-byte aligned.
  *   workspace : at least ssm_xent_workspace_bytes(shapes, 1) bytes, as above.

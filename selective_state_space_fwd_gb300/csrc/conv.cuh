@@ -15,7 +15,7 @@ __device__ __forceinline__ int64_t conv_valid(const ConvParams& p, int64_t b) {
   return v < 0 ? 0 : (v > p.seqlen ? p.seqlen : v);
 }
 
-// The row `back` steps before step 0: row width - 1 - back of the state.
+// Row `row` of the carried state: the step width - 1 - row before step 0.
 template <typename T, int K, int VEC>
 __device__ __forceinline__ Raw<T, VEC> state_row(const void* state0, int64_t b, int64_t dim,
                                                  int64_t d0, int row) {

@@ -2,7 +2,7 @@
 // channel is filtered along time with its own `width` (2 to 4) taps,
 //   pre[t] = bias + sum_k w[k] x[t - (width - 1) + k],   y = silu(pre) or pre,
 // the steps before the first taken from a carried state (zeros without one).
-// Steps past valid_len give y = 0 and are never read.
+// Steps past valid_len give y = 0, whatever x holds there.
 //
 // Bound by HBM: each element is read and written once, for `width` fused
 // multiply-adds and one MUFU pair.  A thread holds VEC channels with their taps

@@ -79,7 +79,7 @@ struct NormBwdParams {
   const float* stats;    // [2, rows]
   const void* dy;        // [rows, dim], I/O type
   const void* dr;        // nullable, [rows, dim], residual type
-  void* dx;              // nullable, [rows, dim], I/O type
+  void* dx;              // [rows, dim], I/O type
   void* dresidual;       // nullable, [rows, dim], residual type
   float* dweight;        // [dim]
   float* dbias;          // nullable, [dim]

@@ -160,7 +160,7 @@ def conv_fwd(x, weight, bias=None, valid_len=None, *, state0=None, silu: bool = 
     x: [batch, L, dim], fp32 or bf16, channels contiguous; rows may be strided
     (columns of a wider projection).  weight: fp32 [dim, width], width 2 to 4,
     the last tap on the current step; bias: fp32 [dim]; valid_len: int32
-    [batch], steps past it give 0 and are not read.  state0: like x, [batch,
+    [batch], steps past it give 0 whatever x holds there.  state0: like x, [batch,
     width - 1, dim], the steps before the first (zeros when None).  With
     ``silu`` the result is silu(pre).  Returns y [batch, L, dim], or
     ``(y, final)`` with ``want_final``, final [batch, width - 1, dim] being the
