@@ -614,12 +614,28 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
       : "memory");
 }
 
-// Merges (maximum, sum) pairs of a softmax's denominator.
-__device__ __forceinline__ void merge(float& m, float& l, const float2 v) {
-  const float nm = fmaxf(m, v.x);
-  const float from = origin(nm);
-  l = l * ex2((m - from) * kLog2e) + v.y * ex2((v.x - from) * kLog2e);
-  m = nm;
+// (maximum, sum) pairs of a softmax's denominator joined with (m, l): the maximum
+// of all first, then the sums, each scaled to it once.
+template <int N>
+__device__ __forceinline__ void join(float& m, float& l, const float2 (&v)[N]) {
+  float top = m;
+#pragma unroll
+  for (int i = 0; i < N; ++i) top = fmaxf(top, v[i].x);
+  const float from = origin(top);
+  l *= ex2((m - from) * kLog2e);
+#pragma unroll
+  for (int i = 0; i < N; ++i) l = fmaf(v[i].y, ex2((v[i].x - from) * kLog2e), l);
+  m = top;
+}
+// The pairs of a warp's lanes, joined in every lane.
+__device__ __forceinline__ void join_lanes(float& m, float& l) {
+  float top = m;
+#pragma unroll
+  for (int o = 16; o >= 1; o /= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  l *= ex2((m - origin(top)) * kLog2e);
+#pragma unroll
+  for (int o = 16; o >= 1; o /= 2) l += __shfl_xor_sync(0xffffffffu, l, o);
+  m = top;
 }
 
 template <int N>
@@ -764,14 +780,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("bar.sync 1, 128;" ::: "memory");
     for (int j = q; j < N; j += 4) {
       float a = -INFINITY, z = 0.f;
+      float2 v[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) merge(a, z, pairs[j * 128 + i * 32 + lane]);
-#pragma unroll
-      for (int o = 16; o >= 1; o /= 2) {
-        const float2 w = make_float2(__shfl_xor_sync(0xffffffffu, a, o),
-                                     __shfl_xor_sync(0xffffffffu, z, o));
-        merge(a, z, w);
-      }
+      for (int i = 0; i < 4; ++i) v[i] = pairs[j * 128 + i * 32 + lane];
+      join(a, z, v);
+      join_lanes(a, z);
       if (lane == 0) p.part[static_cast<int64_t>(blockIdx.x) * p.part_pitch + j] = make_float2(a, z);
     }
   }
@@ -962,8 +975,7 @@ __global__ void __launch_bounds__(1024) xent_join_kernel(const GemmArgs p, int64
 #pragma unroll
       for (int j = 0; j < 4; ++j)
         v[j] = i + 32 * j < tiles ? q[(i + 32 * j) * p.part_pitch] : make_float2(-INFINITY, 0.f);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) merge(m, l, v[j]);
+      join(m, l, v);
     }
   }
   red[lane][wy] = make_float2(m, l);
@@ -972,11 +984,7 @@ __global__ void __launch_bounds__(1024) xent_join_kernel(const GemmArgs p, int64
   const float2 v = red[wy][lane];
   m = v.x;
   l = v.y;
-#pragma unroll
-  for (int o = 16; o >= 1; o /= 2) {
-    const float2 w = make_float2(__shfl_xor_sync(0xffffffffu, m, o), __shfl_xor_sync(0xffffffffu, l, o));
-    merge(m, l, w);
-  }
+  join_lanes(m, l);
   const int64_t row = static_cast<int64_t>(blockIdx.x) * 32 + wy;
   if (lane == 0 && row < rows_of(p)) {
     const int64_t t = idx ? idx[row] : row;
