@@ -192,11 +192,21 @@ __global__ void __launch_bounds__(VEC * NV == 8 ? 1024 : 512)
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int c = cols.at(i * tpr + lane);
-    cols.each(c, [&](int v, auto in) {
-      // a dropped element may be another row's NaN: neither factor is taken from it
-      f[i][v] = in ? f[i][v] - mean : 0.f;
-      q = fmaf(f[i][v], f[i][v], q);
-    });
+    if constexpr (SHIFT) {
+      cols.each(c, [&](int v, auto in) {
+        f[i][v] -= mean;
+        const float own = in ? f[i][v] : 0.f;  // what is dropped may be another row's NaN
+        q = fmaf(own, own, q);
+      });
+    } else {  // a group is the row's, or dropped, as a whole
+      float s = q;
+#pragma unroll
+      for (int v = 0; v < VEC; ++v) {
+        f[i][v] -= mean;
+        s = fmaf(f[i][v], f[i][v], s);
+      }
+      q = c < dim ? s : q;
+    }
   }
   const float rstd = rsqrtf(row_sum(q, tpr, red[1]) * inv + p.eps);
   if (!on) return;

@@ -80,3 +80,19 @@ def test_in_place_stream_off_a_boundary(dtype, residual, dim):
         y2, r2, stats2 = S.norm_fwd(t["x"], t["w"], t["b"], residual=res, out_r=res, want_stats=True)
         assert r2.data_ptr() == res.data_ptr()
         assert torch.equal(r2, r) and torch.equal(y2, y) and torch.equal(stats2, stats)
+
+
+@pytest.mark.parametrize("rows", [5, 700])
+@pytest.mark.parametrize("dtype,dim", [("bf16", 1000), ("bf16", 1001), ("bf16", 96), ("f32", 1500), ("f32", 1537)])
+@pytest.mark.parametrize("column", [0, 50, -1])
+def test_an_infinity_in_a_root_mean_square_row(dtype, dim, column, rows):
+    """The mean square is infinite and its reciprocal root 0: the row's finite columns
+    are 0 wherever the infinity stands, also in the last group of columns, which
+    threads past the row's end hold too."""
+    t = make(dtype, rows, dim, None, bias=False)
+    t["x"][1, column] = float("inf")
+    y, _, stats = S.norm_fwd(t["x"], t["w"], rms=True, want_stats=True)
+    assert stats[1, 1] == 0
+    rest = torch.ones(dim, dtype=torch.bool, device="cuda")
+    rest[column] = False
+    assert (y[1, rest] == 0).all() and y[1, column].isnan()
