@@ -37,7 +37,6 @@
 #include "common.cuh"
 #include "device_errors.h"
 #include "ssd.h"
-#include "tma_map.h"
 #include "umma.cuh"
 
 namespace ssm {
@@ -519,10 +518,38 @@ __global__ void __launch_bounds__(2 * kThreads, SsdCfg<NS>::kMinBlocks)
   if (warp == 0) umma::tmem_dealloc(tm, K::kTmemCols);
 }
 
-// A bf16 [rows, inner] tensor in boxes of 64 elements x one block of rows (one
-// part of a tile).
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode() {
+  static EncodeTiledFn fn = nullptr;
+  static bool tried = false;
+  if (!tried) {
+    tried = true;
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault,
+                                         &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<EncodeTiledFn>(f);
+  }
+  return fn;
+}
+
+// 2-D map over a bf16 [rows, inner] tensor with a box of 64 elements x 128
+// rows, 128-byte swizzled (one part of a tile).  Rows past the end read as zeros.
 bool tile_map(CUtensorMap* m, const void* base, int64_t inner, int64_t rows) {
-  return map_bf16_sw128(m, base, inner, rows, inner, Q);
+  EncodeTiledFn fn = encode();
+  if (!fn) return false;
+  cuuint64_t dims[2] = {cuuint64_t(inner), cuuint64_t(rows)};
+  cuuint64_t strides[1] = {cuuint64_t(inner * 2)};
+  cuuint32_t box[2] = {64, cuuint32_t(Q)};
+  cuuint32_t estr[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box,
+            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <int NS, bool GATE>

@@ -6,7 +6,6 @@
 
 #include "stream_core.cuh"
 #include "tiers.h"
-#include "tma_map.h"
 
 namespace ssm {
 
@@ -46,12 +45,32 @@ __global__ void wait_timeout_selftest_kernel(unsigned polls, unsigned int* err) 
 // Dynamic shared memory a STREAM CTA may use (the opt-in limit of sm_103).
 int max_dynamic_smem() { return 227 * 1024; }
 
-bool tma_encode_available() { return encode_tiled() != nullptr; }
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_fn() {
+  static EncodeTiledFn fn = nullptr;
+  static bool tried = false;
+  if (!tried) {
+    tried = true;
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault,
+                                         &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<EncodeTiledFn>(f);
+  }
+  return fn;
+}
+
+bool tma_encode_available() { return encode_fn() != nullptr; }
 
 // 3-D map over a [batch, seqlen, inner] tensor with a box of {box_inner, box_t, 1}.
 bool make_map(CUtensorMap* m, const void* base, bool bf16, int64_t inner, int64_t L, int64_t batch,
               int box_inner, int box_t) {
-  const EncodeTiledFn fn = encode_tiled();
+  EncodeTiledFn fn = encode_fn();
   if (!fn || base == nullptr) return false;
   const int es = bf16 ? 2 : 4;
   cuuint64_t dims[3] = {cuuint64_t(inner), cuuint64_t(L), cuuint64_t(batch)};
@@ -221,7 +240,7 @@ bool stream_eligible(const ScanParams& p, bool bf16, StreamShape sh) {
                         reinterpret_cast<uintptr_t>(p.h0) |
                         reinterpret_cast<uintptr_t>(p.h_final);
   if (mis % 16 != 0) return false;
-  if (encode_tiled() == nullptr) return false;
+  if (encode_fn() == nullptr) return false;
   return stream_grid(p, sh) <= INT32_MAX;
 }
 
