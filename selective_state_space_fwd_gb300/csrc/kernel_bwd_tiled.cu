@@ -573,7 +573,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
   }
   if (!good) {
-    if (lane == 0) atomicOr(err, kErrWait);
+    if (lane == 0) atomicOr(err, stream::kErrWait);
     if (tid == 0) {
       // let the copies already issued land before the CTA's memory is released
       for (int64_t i = it; i < issued; ++i)

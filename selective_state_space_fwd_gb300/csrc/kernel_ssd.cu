@@ -35,7 +35,6 @@
 #include <cuda_bf16.h>
 
 #include "common.cuh"
-#include "device_errors.h"
 #include "ssd.h"
 #include "umma.cuh"
 
@@ -45,6 +44,8 @@ namespace {
 constexpr int Q = kSsdChunk, P = kSsdHeadDim;
 constexpr int kThreads = 128;  // rows of a block; the CTA has two threads per row
 constexpr unsigned kSsdWaitLimit = 1u << 24;  // try_wait polls before a wait gives up
+constexpr unsigned kErrSsdWait = 2u;
+constexpr unsigned kErrSsdAlign = 4u;  // shared memory not 1024-byte aligned: nothing computed
 
 // Two tile layouts.  The tiles that arrive by TMA (C, B, x) are 128-byte
 // swizzled: 64 bf16 of each of the 128 rows per 16 KB part, row r at r * 128,

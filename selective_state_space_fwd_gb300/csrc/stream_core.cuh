@@ -38,7 +38,6 @@
 #include <type_traits>
 
 #include "common.cuh"
-#include "device_errors.h"
 #include "tiers.h"
 
 namespace ssm {
@@ -46,6 +45,7 @@ namespace stream {
 
 typedef unsigned long long u64;
 constexpr unsigned kWaitLimit = 1u << 24;  // try_wait polls before a wait gives up
+constexpr unsigned kErrWait = 1u;
 
 // ---- paired fp32: two channels per instruction ---------------------------------
 __device__ __forceinline__ u64 pk2(float lo, float hi) {

@@ -55,6 +55,8 @@ using stream::pk2;
 using stream::u64;
 using stream::upk2;
 
+constexpr unsigned kErrWaitTm = 8u;  // sticky error bit of this tier's bounded waits
+
 template <int N_, int G_, int R_, int W_, typename IO_, bool GATE_>
 struct Cfg {
   static constexpr int N = N_, G = G_, R = R_, W = W_;
