@@ -39,10 +39,10 @@ def _once(name):
     def mark(backward):
         @functools.wraps(backward)
         def marked(ctx, *grads):
+            if not torch.is_grad_enabled():
+                return backward(ctx, *grads)
             with torch.no_grad():
                 out = backward(ctx, *grads)
-            if not torch.is_grad_enabled():
-                return out
             tied = [t for t in (*grads, *ctx.saved_tensors) if t is not None and t.requires_grad]
             return _Final.apply(name, len(tied), *tied, *out) if tied else out
         return marked
