@@ -32,7 +32,6 @@ constexpr int kWarps = 4;           // warps per CTA
 constexpr uint32_t kRowBytes = 256;  // of a slab
 constexpr uint32_t kBoxBytes = kRows * kRowBytes;
 constexpr uint64_t kWaitNs = 2000000000ull;
-constexpr unsigned kErrConvWait = 16u;
 
 // Stages per warp and CTAs per SM.  Measured on bf16 8 x 4096 x 1024 (forward)
 // and 8 x 2048 x 2048 (training step): boxes of 16 steps 23.7 and 64.5 us, of 8

@@ -67,7 +67,6 @@ static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
 constexpr int kThreads = 192;
 constexpr int kEpilogueWarps = 4;
 constexpr uint64_t kWaitNs = 2000000000ull;  // a wait gives up after 2 s
-constexpr unsigned kErrXentWait = 8u;
 constexpr int64_t kPieceBytes = int64_t(512) << 20;  // most bytes of one piece of G
 
 // The dloss that all kept tokens share, or 1 with `shared` 0.

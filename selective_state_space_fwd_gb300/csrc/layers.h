@@ -8,6 +8,12 @@
 
 namespace ssm {
 
+// Bits of the sticky device error word that the bounded waits of these operators
+// set, one each.  The scan's kernels have 1 (STREAM and the tiled backward), 2 and 4
+// (SSD form) and 8 (STREAM-TM).
+constexpr unsigned kErrConvWait = 16u;
+constexpr unsigned kErrXentWait = 32u;
+
 // ---- short causal convolution (kernel_conv.cu) ------------------------------
 struct ConvParams {
   const void* x;             // [batch, seqlen, dim], channels contiguous
