@@ -11,9 +11,10 @@
 // the sequence arrive as zeros.  tc makes the steps of a piece whole boxes.
 //
 // Bound by HBM.  Measured on GB300, width 4 with silu: fp32 8 x 4096 x 1024
-// forward 46.5 us, 5.8 TB/s, forward and backward 119 us, 5.6 TB/s (one launch
-// alone, ncu: 40.0 and 62.0 us, 6.7 and 6.5 TB/s); bf16 8 x 4096 x 1024 forward
-// 23.6 us, 5.7 TB/s; bf16 prompts 32 x 2048 x 1536 with valid lengths 60 us.
+// forward 47.1 us, 5.7 TB/s, forward and backward 120 us, 5.6 TB/s, with x
+// time-major 119 us (one launch alone, ncu: 40.0 and 62.0 us, 6.7 and 6.5 TB/s);
+// bf16 8 x 4096 x 1024 forward 23.4 us, 5.7 TB/s; bf16 prompts 32 x 2048 x 1536
+// with valid lengths 61 us.
 #include <cuda.h>
 
 #include <type_traits>

@@ -22,7 +22,8 @@
 // results are multiplied by it in fp32: rounded into G it would be off by up to
 // 2^-8 in the same direction for every token, as p - 1 at the target is nearly
 // -1.  What rounding takes from a token's G at the target is kept in fp32 and
-// put back into its dh.
+// put back into its dh.  With a dloss per token dW keeps the rounding of G, which
+// falls either way: 2.4e-3 off in all, against 1.7e-3 for its own rounding alone.
 //
 // Products: 256 x 256 tiles on pairs of CTAs (umma_pair.cuh), operands by TMA
 // in 64-wide, 128-byte swizzled boxes through a ring of kStages stages, fp32
@@ -31,11 +32,11 @@
 // even CTA) issues products, warps 2 to 5 run the epilogue, a thread per row.
 // Clusters are persistent and take tiles in turn.
 //
-// Measured on GB300: values of 4096 tokens x 50257 x 1536 in 323 us, 1.96
-// PFLOP/s; with gradients, 8192 x 65536 x 2048 in 5.02 ms, 1.75 PFLOP/s (the
-// power limit: a cuBLAS loop sustains 1.74), 1000 tokens, half of them ignored, x
-// 32001 x 768 in 113 us, 0.87 PFLOP/s (short launches: fill, drain and uneven
-// last tiles).  Eight epilogue warps instead of four, and 4 or 5 stages instead
+// Measured on GB300: values of 4096 tokens x 50257 x 1536 in 350 to 379 us in a
+// loop, 1.71 PFLOP/s, 323 us in a short run; with gradients, 8192 x 65536 x 2048
+// in 5.17 ms, 1.70 PFLOP/s (the power limit: a cuBLAS loop sustains 1.75), 1000
+// tokens, half of them ignored, x 32001 x 768 in 112 us, 0.88 PFLOP/s (short
+// launches: fill, drain and uneven last tiles).  Eight epilogue warps instead of four, and 4 or 5 stages instead
 // of 6, measured no better on these.
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -67,7 +68,9 @@ static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
 constexpr int kThreads = 192;
 constexpr int kEpilogueWarps = 4;
 constexpr uint64_t kWaitNs = 2000000000ull;  // a wait gives up after 2 s
-constexpr int64_t kPieceBytes = int64_t(512) << 20;  // most bytes of one piece of G
+// Most bytes of one piece of G, which has at least one tile of columns (from 2^20
+// tokens on the larger).
+constexpr int64_t kPieceBytes = int64_t(512) << 20;
 
 // The dloss that all kept tokens share, or 1 with `shared` 0.
 struct Common {
@@ -585,9 +588,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 // rows, the B operand, so that nearly all bytes in flight are W's.  Thread r of
 // the epilogue holds row r of a tile and keeps a running (maximum, sum) per
 // token over the CTA's tiles; the threads' pairs are joined once, at the end.
-// With a vocabulary of 32768 x 1024 (67 MB, 9.9 us of HBM): 1 token 19.5 us, 32
-// tokens 21.0 us; the 256 x 256 tiles take 25.8 us for 1 token and 20.5 us for 65,
-// against 25.3 us here with N = 64.
+// With a vocabulary of 32768 x 1024 (67 MB, 9.9 us of HBM): 1 token 19.8 us, 32
+// tokens 20.8 us.  The 256 x 256 tiles take 25.8 us for 1 token, 20.4 us for 33 and
+// 19.3 us for 64, which took 25.3 us here with N = 64.
 constexpr int kFewMost = 32;
 
 template <int N>
