@@ -33,7 +33,7 @@
 // Clusters are persistent and take tiles in turn.
 //
 // Measured on GB300: values of 4096 tokens x 50257 x 1536 in 350 to 379 us in a
-// loop, 1.71 PFLOP/s, 323 us in a short run; with gradients, 8192 x 65536 x 2048
+// loop, 1.71 PFLOP/s, 326 in a short run; with gradients, 8192 x 65536 x 2048
 // in 5.17 ms, 1.70 PFLOP/s (the power limit: a cuBLAS loop sustains 1.75), 1000
 // tokens, half of them ignored, x 32001 x 768 in 112 us, 0.88 PFLOP/s (short
 // launches: fill, drain and uneven last tiles).  Eight epilogue warps instead of four, and 4 or 5 stages instead
