@@ -515,6 +515,80 @@ ssm_status ssm_xent_bwd(const void* h, const void* weight, const int64_t* target
  * on invalid shapes. */
 size_t ssm_xent_workspace_bytes(const ssm_xent_shapes* shapes, int backward);
 
+/* Sizes and strides of the gated linear recurrence.  Strides are in elements;
+ * channels are contiguous.  The stride of an axis of one element is not used. */
+typedef struct {
+  int64_t batch;             /* >= 1 */
+  int64_t seqlen;            /* >= 1 */
+  int64_t dim;               /* >= 1 */
+  int64_t gate_batch_stride; /* of gate, between batch rows; >= 0 */
+  int64_t gate_step_stride;  /* of gate, between steps; >= 0 */
+  int64_t value_batch_stride;
+  int64_t value_step_stride;
+} ssm_recur_shapes;
+
+/*
+ * ssm_recur_fwd -- the gated linear recurrence of every channel along time:
+ *   b[t] = (1 - floor) sigmoid(-gate[t]),  a[t] = 1 - b[t]
+ *        (a[t] = floor + (1 - floor) sigmoid(gate[t])),
+ *   h[t] = a[t] h[t-1] + b[t] value[t],    y[t] = h[t] rounded to dtype.
+ *   gate, value : device, dtype `dtype`, [batch, seqlen, dim], strided as
+ *                 `shapes` says (halves of the columns of one projection, say).
+ *   floor       : device fp32 [dim] or NULL (0): the least decay of a channel, in
+ *                 [0, 1].
+ *   valid_len   : device int32 [batch] or NULL; clamped to [0, seqlen].  Steps past
+ *                 it give y = 0 and leave the state, whatever gate and value hold.
+ *   state0      : device fp32 [batch, dim] or NULL (zeros): h before the first step.
+ *   out_y       : device, dtype `dtype`, [batch, seqlen, dim], contiguous.
+ *   out_final   : device fp32 [batch, dim] or NULL: h after the last valid step.
+ *   out_states  : device fp32 [batch, ssm_recur_chunks(shapes), dim] or NULL: h
+ *                 before every chunk of steps, for ssm_recur_bwd.
+ * The state is fp32.  At most 2^31 - 1 (batch row, 32 channels) pairs.
+ */
+ssm_status ssm_recur_fwd(const void* gate, const void* value, const float* floor,
+                         const int32_t* valid_len, const float* state0, void* out_y,
+                         float* out_final, float* out_states, const ssm_recur_shapes* shapes,
+                         ssm_dtype dtype, cudaStream_t stream);
+
+/*
+ * ssm_recur_bwd -- every gradient of sum(dy * y) + sum(dfinal * final) for
+ * ssm_recur_fwd on the same inputs (the states inside a chunk are formed again).
+ *   states  : the forward's out_states.
+ *   dy      : device, dtype `dtype`, [batch, seqlen, dim], contiguous; what it
+ *             holds past valid_len has no effect.
+ *   dfinal  : device fp32 [batch, dim] or NULL (zeros).
+ *   dgate, dvalue : device, dtype `dtype`, [batch, seqlen, dim], contiguous; 0 past
+ *             valid_len.
+ *   dfloor  : device fp32 [dim] or NULL.   dstate0: fp32 [batch, dim] or NULL.
+ *   workspace: with dfloor, device memory of at least
+ *             ssm_recur_bwd_workspace_bytes() bytes, 16-byte aligned, unused by
+ *             other work until `stream` passes the call; NULL without.
+ * Sums are taken in a fixed order: equal inputs give equal bits.
+ */
+ssm_status ssm_recur_bwd(const void* gate, const void* value, const float* floor,
+                         const int32_t* valid_len, const float* states, const void* dy,
+                         const float* dfinal, void* dgate, void* dvalue, float* dfloor,
+                         float* dstate0, void* workspace, size_t workspace_bytes,
+                         const ssm_recur_shapes* shapes, ssm_dtype dtype, cudaStream_t stream);
+/* Workspace bytes of ssm_recur_bwd with dfloor; 0 on invalid shapes. */
+size_t ssm_recur_bwd_workspace_bytes(const ssm_recur_shapes* shapes);
+/* Chunks of steps whose entering states the backward needs, ceil(seqlen / 64); 0
+ * on invalid shapes. */
+int64_t ssm_recur_chunks(const ssm_recur_shapes* shapes);
+
+/*
+ * ssm_recur_step -- one step of the recurrence on a carried state, in place
+ * (token-by-token generation).
+ *   gate, value : device, dtype `dtype`, [batch, dim], rows gate_batch_stride and
+ *                 value_batch_stride elements apart.
+ *   state : device fp32 [batch, dim]: h, advanced by the step.
+ *   out_y : device, dtype `dtype`, [batch, dim].
+ * shapes->seqlen must be 1; the step strides are not used.
+ */
+ssm_status ssm_recur_step(const void* gate, const void* value, const float* floor, float* state,
+                          void* out_y, const ssm_recur_shapes* shapes, ssm_dtype dtype,
+                          cudaStream_t stream);
+
 /* The tier (and its grid) that ssm_scan_fwd_ex would launch for these
  * arguments, without launching anything.  `has_*` describe which optional
  * tensors the call passes.  Writes the tier to *kernel and the launch grid

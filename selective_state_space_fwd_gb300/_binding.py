@@ -92,6 +92,13 @@ class XentShapes(ctypes.Structure):
                 ("ignore_index", ctypes.c_int64)]
 
 
+class RecurShapes(ctypes.Structure):
+    """ssm_recur_shapes."""
+    _fields_ = [("batch", ctypes.c_int64), ("seqlen", ctypes.c_int64), ("dim", ctypes.c_int64),
+                ("gate_batch_stride", ctypes.c_int64), ("gate_step_stride", ctypes.c_int64),
+                ("value_batch_stride", ctypes.c_int64), ("value_step_stride", ctypes.c_int64)]
+
+
 def _prep(dt_bias, delta_softplus, delta_clamp, dim, dev):
     """A DeltaPrep for the keyword arguments, or None when nothing is asked."""
     if dt_bias is None and not delta_softplus and delta_clamp is None:
@@ -182,6 +189,17 @@ def load() -> ctypes.CDLL:
     lib.ssm_xent_bwd.argtypes = [P] * 8 + [SZ, XP, I32, P]
     lib.ssm_xent_workspace_bytes.restype = SZ
     lib.ssm_xent_workspace_bytes.argtypes = [XP, I32]
+    RP = ctypes.POINTER(RecurShapes)
+    lib.ssm_recur_fwd.restype = I32
+    lib.ssm_recur_fwd.argtypes = [P] * 8 + [RP, I32, P]
+    lib.ssm_recur_bwd.restype = I32
+    lib.ssm_recur_bwd.argtypes = [P] * 12 + [SZ, RP, I32, P]
+    lib.ssm_recur_bwd_workspace_bytes.restype = SZ
+    lib.ssm_recur_bwd_workspace_bytes.argtypes = [RP]
+    lib.ssm_recur_chunks.restype = I64
+    lib.ssm_recur_chunks.argtypes = [RP]
+    lib.ssm_recur_step.restype = I32
+    lib.ssm_recur_step.argtypes = [P] * 5 + [RP, I32, P]
     _lib = lib
     return lib
 

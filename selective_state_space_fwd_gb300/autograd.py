@@ -14,7 +14,8 @@ import functools
 import torch
 
 from ._binding import scan_bwd, scan_fwd
-from .layers import conv_bwd, conv_fwd, norm_bwd, norm_fwd, xent_bwd, xent_fwd
+from .layers import (conv_bwd, conv_fwd, norm_bwd, norm_fwd, recur_bwd, recur_fwd, xent_bwd,
+                     xent_fwd)
 
 
 class _Final(torch.autograd.Function):
@@ -164,3 +165,33 @@ def linear_cross_entropy(h, weight, targets, *, ignore_index: int = -100, reduct
         return loss.view(targets.shape)
     total = loss.sum()
     return total if reduction == "sum" else total / (targets != ignore_index).sum().clamp(min=1)
+
+
+class _GatedRecurrence(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, gate, value, floor, valid_len, state0):
+        y, final, states = recur_fwd(gate, value, floor, valid_len, state0=state0, want_final=True,
+                                     want_states=True)
+        ctx.save_for_backward(gate, value, floor, valid_len, states)
+        ctx.set_materialize_grads(False)
+        return y, final
+
+    @staticmethod
+    @_once("gated_recurrence")
+    def backward(ctx, dy, dfinal):
+        gate, value, floor, valid_len, states = ctx.saved_tensors
+        if dy is None:
+            dy = torch.zeros(gate.shape, dtype=gate.dtype, device=gate.device)
+        g = recur_bwd(gate, value, floor, valid_len, states=states, dy=dy.contiguous(),
+                      dfinal=None if dfinal is None else dfinal.contiguous(),
+                      want_dstate0=ctx.needs_input_grad[4])
+        return g["dgate"], g["dvalue"], g["dfloor"], None, g["dstate0"]
+
+
+def gated_recurrence(gate, value, floor=None, valid_len=None, *, state0=None,
+                     want_final: bool = False):
+    """y = the gated linear recurrence of value (as ``recur_fwd``), differentiable
+    in gate, value, floor and state0.  Returns y, or ``(y, final)`` with
+    ``want_final``, final being differentiable too."""
+    y, final = _GatedRecurrence.apply(gate, value, floor, valid_len, state0)
+    return (y, final) if want_final else y

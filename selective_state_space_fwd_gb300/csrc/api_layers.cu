@@ -80,6 +80,38 @@ ssm_status check_xent(const ssm_xent_shapes* s) {
   return s->dim % 8 == 0 ? SSM_OK : SSM_ERR_UNSUPPORTED;  // copies start on 16-byte boundaries
 }
 
+// A tensor read with these strides: its span stays addressable.
+bool span_ok(int64_t batch, int64_t batch_stride, int64_t seqlen, int64_t step_stride) {
+  int64_t b, t;
+  return batch_stride >= 0 && step_stride >= 0 && mul_ok(batch, batch_stride, &b) &&
+         mul_ok(seqlen, step_stride, &t) && b <= kMaxElements && t <= kMaxElements;
+}
+
+ssm_status check_recur(const ssm_recur_shapes* s, ssm_dtype dtype) {
+  if (s == nullptr) return SSM_ERR_NULL;
+  if (!known(dtype)) return SSM_ERR_UNSUPPORTED;
+  if (s->batch < 1 || s->seqlen < 1 || s->dim < 1) return SSM_ERR_SHAPE;
+  int64_t n, units;
+  if (!mul_ok(s->batch, s->seqlen, &n) || !mul_ok(n, s->dim, &n) || n > kMaxElements)
+    return SSM_ERR_SHAPE;
+  // the grid: a CTA per (batch row, 32 channels)
+  if (!mul_ok(s->batch, s->dim / 32 + 1, &units) || units > INT32_MAX) return SSM_ERR_SHAPE;
+  if (!span_ok(s->batch, s->gate_batch_stride, s->seqlen, s->gate_step_stride) ||
+      !span_ok(s->batch, s->value_batch_stride, s->seqlen, s->value_step_stride))
+    return SSM_ERR_SHAPE;
+  return SSM_OK;
+}
+
+ssm::RecurParams recur_params(const void* gate, const void* value, const float* floor,
+                              const int32_t* valid_len, const ssm_recur_shapes& s) {
+  ssm::RecurParams p = {};
+  p.gate = gate; p.value = value; p.floor = floor; p.valid_len = valid_len;
+  p.gate_batch = s.gate_batch_stride; p.gate_step = s.gate_step_stride;
+  p.value_batch = s.value_batch_stride; p.value_step = s.value_step_stride;
+  p.batch = s.batch; p.seqlen = s.seqlen; p.dim = s.dim;
+  return p;
+}
+
 ssm::XentParams xent_params(const void* h, const void* weight, const int64_t* targets,
                             const ssm_xent_shapes& s, void* workspace) {
   ssm::XentParams p = {};
@@ -261,6 +293,79 @@ ssm_status ssm_xent_bwd(const void* h, const void* weight, const int64_t* target
   if (!(p.err = ssm::stream::error_word())) return SSM_ERR_CUDA;
   p.lse_in = lse; p.dloss = dloss; p.dh = dh; p.dweight = dweight;
   return status_of(ssm::launch_xent_bwd(p, stream));
+}
+
+ssm_status ssm_recur_fwd(const void* gate, const void* value, const float* floor,
+                         const int32_t* valid_len, const float* state0, void* out_y,
+                         float* out_final, float* out_states, const ssm_recur_shapes* shapes,
+                         ssm_dtype dtype, cudaStream_t stream) {
+  ssm_status st = check_recur(shapes, dtype);
+  if (st != SSM_OK) return st;
+  if (!gate || !value || !out_y) return SSM_ERR_NULL;
+  const size_t es = elem_size(dtype);
+  if (!aligned(gate, es) || !aligned(value, es) || !aligned(floor, 4) || !aligned(valid_len, 4) ||
+      !aligned(state0, 4) || !aligned(out_y, es) || !aligned(out_final, 4) ||
+      !aligned(out_states, 4))
+    return SSM_ERR_ALIGN;
+  int dev = 0;
+  if ((st = current_device_for(stream, &dev)) != SSM_OK) return st;
+  ssm::RecurParams p = recur_params(gate, value, floor, valid_len, *shapes);
+  p.state0 = state0; p.y = out_y; p.out_final = out_final; p.states = out_states;
+  return status_of(ssm::launch_recur_fwd(p, dtype == SSM_BF16, stream));
+}
+
+size_t ssm_recur_bwd_workspace_bytes(const ssm_recur_shapes* shapes) {
+  if (check_recur(shapes, SSM_F32) != SSM_OK) return 0;
+  return static_cast<size_t>(ssm::recur_bwd_partials(shapes->batch, shapes->seqlen)) *
+         shapes->dim * sizeof(float);
+}
+
+int64_t ssm_recur_chunks(const ssm_recur_shapes* shapes) {
+  if (check_recur(shapes, SSM_F32) != SSM_OK) return 0;
+  return (shapes->seqlen + ssm::kRecurChunk - 1) / ssm::kRecurChunk;
+}
+
+ssm_status ssm_recur_bwd(const void* gate, const void* value, const float* floor,
+                         const int32_t* valid_len, const float* states, const void* dy,
+                         const float* dfinal, void* dgate, void* dvalue, float* dfloor,
+                         float* dstate0, void* workspace, size_t workspace_bytes,
+                         const ssm_recur_shapes* shapes, ssm_dtype dtype, cudaStream_t stream) {
+  ssm_status st = check_recur(shapes, dtype);
+  if (st != SSM_OK) return st;
+  if (!gate || !value || !states || !dy || !dgate || !dvalue || (dfloor && !workspace))
+    return SSM_ERR_NULL;
+  const size_t es = elem_size(dtype);
+  if (!aligned(gate, es) || !aligned(value, es) || !aligned(floor, 4) || !aligned(valid_len, 4) ||
+      !aligned(states, 4) || !aligned(dy, es) || !aligned(dfinal, 4) || !aligned(dgate, es) ||
+      !aligned(dvalue, es) || !aligned(dfloor, 4) || !aligned(dstate0, 4) ||
+      !aligned(workspace, 16))
+    return SSM_ERR_ALIGN;
+  if (dfloor && workspace_bytes < ssm_recur_bwd_workspace_bytes(shapes)) return SSM_ERR_SHAPE;
+  int dev = 0;
+  if ((st = current_device_for(stream, &dev)) != SSM_OK) return st;
+  ssm::RecurBwdParams q;
+  q.fwd = recur_params(gate, value, floor, valid_len, *shapes);
+  q.states = states; q.dy = dy; q.dfinal = dfinal; q.dgate = dgate; q.dvalue = dvalue;
+  q.dfloor = dfloor; q.dstate0 = dstate0; q.partial = static_cast<float*>(workspace);
+  return status_of(ssm::launch_recur_bwd(q, dtype == SSM_BF16, stream));
+}
+
+ssm_status ssm_recur_step(const void* gate, const void* value, const float* floor, float* state,
+                          void* out_y, const ssm_recur_shapes* shapes, ssm_dtype dtype,
+                          cudaStream_t stream) {
+  ssm_status st = check_recur(shapes, dtype);
+  if (st != SSM_OK) return st;
+  if (shapes->seqlen != 1) return SSM_ERR_SHAPE;
+  if (!gate || !value || !state || !out_y) return SSM_ERR_NULL;
+  const size_t es = elem_size(dtype);
+  if (!aligned(gate, es) || !aligned(value, es) || !aligned(floor, 4) || !aligned(state, 4) ||
+      !aligned(out_y, es))
+    return SSM_ERR_ALIGN;
+  int dev = 0;
+  if ((st = current_device_for(stream, &dev)) != SSM_OK) return st;
+  ssm::RecurParams p = recur_params(gate, value, floor, nullptr, *shapes);
+  p.y = out_y; p.out_final = state;
+  return status_of(ssm::launch_recur_step(p, dtype == SSM_BF16, stream));
 }
 
 }  // extern "C"

@@ -1,0 +1,566 @@
+// kernel_recur.cu -- the gated linear recurrence along time (formulas in
+// recur.cuh): prompts with valid lengths and a carried state, every gradient,
+// single steps in place.
+//
+// Work split: a CTA owns 32 x VEC channels (128 bytes of a row) of one batch row
+// and walks its time in tiles of kTile steps.  Each of its warps folds kSteps
+// consecutive steps of the tile, lane by lane, into the stretch's map (C, e); the
+// maps meet in shared memory, every thread composes those before its own with
+// the carried state, and the warp's outputs follow from the state that enters it.
+// The next tile's rows are loaded while a tile is folded.  With fewer CTAs than
+// the GPU holds, a cluster of R of them shares the time of its channels, each
+// taking every R-th tile: the tiles' maps then go to all of the cluster's shared
+// memories, one barrier of the cluster per round.  No step is read twice, and no
+// CTA waits for one that might not run.
+//
+// Backward, from the last tile to the first, with l_t = dL/dh_t:
+//   l_t = dy_t + a_{t+1} l_{t+1},   dv = b l,   dg = l (h_{t-1} - v) b sigmoid(g),
+//   dfloor = sum l (h_{t-1} - v) sigmoid(-g).
+// What enters a tile from its past is the state that the forward kept there (one
+// per kTile steps); the states inside are formed again.  The same maps carry
+// m = a l backwards: m -> e' + m - C m, with the same C.  dfloor is summed per
+// thread, over the warps and, by a second kernel, over the CTAs, in a fixed order.
+#include "pdl.cuh"
+#include "recur.cuh"
+#include "umma_pair.cuh"
+#include "vec.cuh"
+
+namespace ssm {
+namespace {
+
+using recur::Cell;
+using recur::through;
+
+constexpr int kSms = 152;
+constexpr int kWarps = 8;
+constexpr int kSteps = 8;                  // per warp and tile
+constexpr int kTile = kWarps * kSteps;     // steps of a tile, and between kept states
+static_assert(kTile == kRecurChunk, "the states that the backward starts from");
+constexpr int kThreads = kWarps * 32;
+constexpr int kMaxCluster = 16;
+
+// Where a thread stands.
+template <int VEC>
+struct Place {
+  int warp, lane;
+  uint32_t rank, size;   // in the cluster
+  int64_t b, d;          // batch row, first channel
+  bool on;               // d < dim
+  __device__ __forceinline__ Place(int64_t dim, uint32_t r) : size(r) {
+    warp = threadIdx.x >> 5;
+    lane = threadIdx.x & 31;
+    const int64_t groups = (dim + 32 * VEC - 1) / (32 * VEC);
+    const int64_t unit = blockIdx.x / r;
+    rank = blockIdx.x - static_cast<unsigned>(unit) * r;
+    b = unit / groups;
+    d = (unit - b * groups) * (32 * VEC) + lane * VEC;
+    on = d < dim;
+  }
+};
+
+// kSteps rows of a strided tensor from step t0 on, 0 past step `end` and past the
+// last channel.
+template <typename T, int VEC>
+__device__ __forceinline__ void load_rows(typename Cell<T, VEC>::Word (&w)[kSteps], const T* row,
+                                          int64_t step, int64_t t0, int64_t end, bool on) {
+  using Word = typename Cell<T, VEC>::Word;
+  const T* q = row + t0 * step;
+  if (t0 + kSteps <= end) {
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s)
+      w[s] = on ? __ldg(reinterpret_cast<const Word*>(q + s * step)) : Word(0);
+  } else {
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s)
+      w[s] = on && t0 + s < end ? __ldg(reinterpret_cast<const Word*>(q + s * step)) : Word(0);
+  }
+}
+
+// kSteps rows of a contiguous [.., dim] tensor, up to step `end`.
+template <typename T, int VEC>
+__device__ __forceinline__ void store_rows(const typename Cell<T, VEC>::Word (&w)[kSteps], T* row,
+                                           int64_t dim, int64_t t0, int64_t end, bool on) {
+  using Word = typename Cell<T, VEC>::Word;
+  T* q = row + t0 * dim;
+  if (!on) return;
+  if (t0 + kSteps <= end) {
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) *reinterpret_cast<Word*>(q + s * dim) = w[s];
+  } else {
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s)
+      if (t0 + s < end) *reinterpret_cast<Word*>(q + s * dim) = w[s];
+  }
+}
+
+// The maps of the tiles that the cluster's CTAs hold in a round, sent to all of
+// them; `slots` alternates so that one barrier per round is enough.
+template <int N>
+__device__ __forceinline__ void share(float (*slots)[32][N], const Place<N / 2>& at,
+                                      const float (&v)[N]) {
+  if (at.warp == 0) {
+    const uint32_t mine = umma::smem_u32(&slots[at.rank][at.lane][0]);
+    for (uint32_t r = 0; r < at.size; ++r) {
+      const uint32_t to = pair::map_to(mine, r);
+#pragma unroll
+      for (int i = 0; i < N; i += 2)
+        asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(to + 4 * i), "f"(v[i]),
+                     "f"(v[i + 1])
+                     : "memory");
+    }
+  }
+  pair::cluster_sync();
+}
+
+template <typename T, int VEC>
+__global__ void __launch_bounds__(kThreads, 2) recur_fwd_kernel(const RecurParams p, uint32_t size) {
+  using Word = typename Cell<T, VEC>::Word;
+  constexpr int N = 2 * VEC;  // floats of a map: (C, e) per channel
+  __shared__ __align__(16) float maps[2][kWarps][32][N];
+  __shared__ __align__(16) float tiles_s[2][kMaxCluster][32][N];
+  const Place<VEC> at(p.dim, size);
+  const int64_t len = recur::valid_of(p.valid_len, at.b, p.seqlen);
+  const int64_t tiles = (p.seqlen + kTile - 1) / kTile, live = (len + kTile - 1) / kTile;
+  const int64_t rounds = (live + size - 1) / size;
+  const int64_t d = at.on ? at.d : 0;
+  const T* gate = static_cast<const T*>(p.gate) + at.b * p.gate_batch + d;
+  const T* value = static_cast<const T*>(p.value) + at.b * p.value_batch + d;
+  T* y = static_cast<T*>(p.y) + at.b * p.seqlen * p.dim + d;
+  float* states = p.states ? p.states + at.b * tiles * p.dim + d : nullptr;
+  const int inside = at.warp * kSteps;
+
+  float keep[VEC], x[VEC];  // x: the state that enters the round
+#pragma unroll
+  for (int v = 0; v < VEC; ++v) {
+    keep[v] = p.floor ? 1.f - __ldg(p.floor + d + v) : 1.f;
+    x[v] = p.state0 ? __ldg(p.state0 + at.b * p.dim + d + v) : 0.f;
+  }
+  Word gw[kSteps], vw[kSteps];
+  int64_t t0 = static_cast<int64_t>(at.rank) * kTile + inside;
+  load_rows<T, VEC>(gw, gate, p.gate_step, t0, len, at.on);
+  load_rows<T, VEC>(vw, value, p.value_step, t0, len, at.on);
+  if (size > 1) pair::cluster_sync();  // all of the cluster has started
+  for (int64_t i = 0; i < rounds; ++i, t0 += static_cast<int64_t>(size) * kTile) {
+    // the outputs from a state of 0, and C up to each step
+    float h[kSteps][VEC], c[kSteps][VEC];
+    float hl[VEC], cl[VEC];
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) hl[v] = cl[v] = 0.f;
+    const int64_t left = len - t0;
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) {
+      float g[VEC], u[VEC];
+      Cell<T, VEC>::get(gw[s], g);
+      Cell<T, VEC>::get(vw[s], u);
+#pragma unroll
+      for (int v = 0; v < VEC; ++v) {
+        float b = keep[v] * recur::opening(g[v]);
+        b = s < left ? b : 0.f;
+        hl[v] = fmaf(b, u[v] - hl[v], hl[v]);
+        cl[v] = fmaf(b, 1.f - cl[v], cl[v]);
+        h[s][v] = hl[v];
+        c[s][v] = cl[v];
+      }
+    }
+    const int64_t next = t0 + static_cast<int64_t>(size) * kTile;
+    load_rows<T, VEC>(gw, gate, p.gate_step, next, len, at.on);
+    load_rows<T, VEC>(vw, value, p.value_step, next, len, at.on);
+    const int k = i & 1;
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) {
+      maps[k][at.warp][at.lane][2 * v] = cl[v];
+      maps[k][at.warp][at.lane][2 * v + 1] = hl[v];
+    }
+    __syncthreads();
+    float xt[VEC];  // the state that enters this CTA's tile
+    if (size > 1) {
+      float all[N];
+#pragma unroll
+      for (int v = 0; v < N; ++v) all[v] = 0.f;
+      if (at.warp == 0) {
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w)
+#pragma unroll
+          for (int v = 0; v < VEC; ++v) {
+            const float cw = maps[k][w][at.lane][2 * v], ew = maps[k][w][at.lane][2 * v + 1];
+            all[2 * v + 1] = through(all[2 * v + 1], cw, ew);
+            all[2 * v] = fmaf(cw, 1.f - all[2 * v], all[2 * v]);
+          }
+      }
+      share<N>(tiles_s[k], at, all);
+      for (uint32_t r = 0; r < size; ++r)
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) {
+          if (r == at.rank) xt[v] = x[v];
+          x[v] = through(x[v], tiles_s[k][r][at.lane][2 * v], tiles_s[k][r][at.lane][2 * v + 1]);
+        }
+    } else {
+#pragma unroll
+      for (int v = 0; v < VEC; ++v) xt[v] = x[v];
+    }
+    float in[VEC], out[VEC];
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) in[v] = out[v] = xt[v];
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w)
+#pragma unroll
+      for (int v = 0; v < VEC; ++v) {
+        if (w == at.warp) in[v] = out[v];
+        out[v] = through(out[v], maps[k][w][at.lane][2 * v], maps[k][w][at.lane][2 * v + 1]);
+      }
+    if (size == 1) {
+#pragma unroll
+      for (int v = 0; v < VEC; ++v) x[v] = out[v];
+    }
+    if (states && at.warp == 0 && at.on && t0 < p.seqlen) {
+#pragma unroll
+      for (int v = 0; v < VEC; ++v) states[t0 / kTile * p.dim + v] = xt[v];
+    }
+    Word yw[kSteps];
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) {
+      float f[VEC];
+#pragma unroll
+      for (int v = 0; v < VEC; ++v) {
+        f[v] = through(in[v], c[s][v], h[s][v]);
+        f[v] = s < left ? f[v] : 0.f;
+      }
+      yw[s] = Cell<T, VEC>::put(f);
+    }
+    store_rows<T, VEC>(yw, y, p.dim, t0, p.seqlen, at.on);
+  }
+  // x is the last valid step's state
+  if (p.out_final && at.rank == 0 && at.warp == 0 && at.on) {
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) p.out_final[at.b * p.dim + d + v] = x[v];
+  }
+  // past the valid steps: tiles that no round has covered
+  Word zero[kSteps];
+#pragma unroll
+  for (int s = 0; s < kSteps; ++s) zero[s] = Word(0);
+  for (; t0 - inside < p.seqlen; t0 += static_cast<int64_t>(size) * kTile) {
+    store_rows<T, VEC>(zero, y, p.dim, t0, p.seqlen, at.on);
+    if (states && at.warp == 0 && at.on) {
+#pragma unroll
+      for (int v = 0; v < VEC; ++v) states[t0 / kTile * p.dim + v] = x[v];
+    }
+  }
+}
+
+template <typename T, int VEC>
+__global__ void __launch_bounds__(kThreads, 2)
+    recur_bwd_kernel(const RecurBwdParams q, uint32_t size) {
+  using Word = typename Cell<T, VEC>::Word;
+  constexpr int N = 2 * VEC;
+  const RecurParams& p = q.fwd;
+  __shared__ __align__(16) float past[2][kWarps][32][N];         // (C, e) of the states
+  __shared__ __align__(16) float coming[2][kWarps][32][VEC];     // e' of m
+  __shared__ __align__(16) float tiles_s[2][kMaxCluster][32][N];  // (C, e') of the tiles
+  const Place<VEC> at(p.dim, size);
+  const int64_t len = recur::valid_of(p.valid_len, at.b, p.seqlen);
+  const int64_t tiles = (p.seqlen + kTile - 1) / kTile, live = (len + kTile - 1) / kTile;
+  const int64_t rounds = (live + size - 1) / size;
+  const int64_t d = at.on ? at.d : 0;
+  const T* gate = static_cast<const T*>(p.gate) + at.b * p.gate_batch + d;
+  const T* value = static_cast<const T*>(p.value) + at.b * p.value_batch + d;
+  const int64_t base = at.b * p.seqlen * p.dim + d;
+  const T* dy = static_cast<const T*>(q.dy) + base;
+  T* dgate = static_cast<T*>(q.dgate) + base;
+  T* dvalue = static_cast<T*>(q.dvalue) + base;
+  const float* states = q.states + at.b * tiles * p.dim + d;
+  const int inside = at.warp * kSteps;
+
+  float keep[VEC], m[VEC], dfloor[VEC];  // m: a l of the step after the round's last
+#pragma unroll
+  for (int v = 0; v < VEC; ++v) {
+    keep[v] = p.floor ? 1.f - __ldg(p.floor + d + v) : 1.f;
+    m[v] = q.dfinal ? __ldg(q.dfinal + at.b * p.dim + d + v) : 0.f;
+    dfloor[v] = 0.f;
+  }
+  if (size > 1) pair::cluster_sync();  // all of the cluster has started
+  for (int64_t i = 0; i < rounds; ++i) {
+    const int64_t tile = live - 1 - i * size - at.rank;  // negative: none is left
+    const int64_t t0 = tile * kTile + inside;
+    const int64_t end = tile < 0 ? t0 : len;
+    const int64_t left = end - t0;
+    Word gw[kSteps], vw[kSteps], yw[kSteps];
+    load_rows<T, VEC>(gw, gate, p.gate_step, t0, end, at.on);
+    load_rows<T, VEC>(vw, value, p.value_step, t0, end, at.on);
+    load_rows<T, VEC>(yw, dy, p.dim, t0, end, at.on);
+    float h[VEC];
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) h[v] = tile < 0 ? 0.f : __ldg(states + tile * p.dim + v);
+    float open[kSteps][VEC], hold[kSteps][VEC], u[kSteps][VEC], l[kSteps][VEC];
+    float cl[VEC], hl[VEC], ml[VEC];
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) cl[v] = hl[v] = ml[v] = 0.f;
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) {
+      float g[VEC];
+      Cell<T, VEC>::get(gw[s], g);
+      Cell<T, VEC>::get(vw[s], u[s]);
+      Cell<T, VEC>::get(yw[s], l[s]);
+#pragma unroll
+      for (int v = 0; v < VEC; ++v) {
+        const float o = recur::opening(g[v], hold[s][v]);
+        open[s][v] = s < left ? o : 0.f;
+        const float b = keep[v] * open[s][v];
+        hl[v] = fmaf(b, u[s][v] - hl[v], hl[v]);
+        cl[v] = fmaf(b, 1.f - cl[v], cl[v]);
+      }
+    }
+#pragma unroll
+    for (int s = kSteps - 1; s >= 0; --s)
+#pragma unroll
+      for (int v = 0; v < VEC; ++v) {
+        const float lam = l[s][v] + ml[v];
+        ml[v] = fmaf(-(keep[v] * open[s][v]), lam, lam);
+      }
+    const int k = i & 1;
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) {
+      past[k][at.warp][at.lane][2 * v] = cl[v];
+      past[k][at.warp][at.lane][2 * v + 1] = hl[v];
+      coming[k][at.warp][at.lane][v] = ml[v];
+    }
+    __syncthreads();
+    float mt[VEC];  // what enters the tile from the steps after it
+    if (size > 1) {
+      float all[N];
+#pragma unroll
+      for (int v = 0; v < N; ++v) all[v] = 0.f;
+      if (at.warp == 0) {
+#pragma unroll
+        for (int w = kWarps - 1; w >= 0; --w)
+#pragma unroll
+          for (int v = 0; v < VEC; ++v) {
+            const float cw = past[k][w][at.lane][2 * v];
+            all[2 * v + 1] = through(all[2 * v + 1], cw, coming[k][w][at.lane][v]);
+            all[2 * v] = fmaf(cw, 1.f - all[2 * v], all[2 * v]);
+          }
+      }
+      share<N>(tiles_s[k], at, all);
+      for (uint32_t r = 0; r < size; ++r)
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) {
+          if (r == at.rank) mt[v] = m[v];
+          m[v] = through(m[v], tiles_s[k][r][at.lane][2 * v], tiles_s[k][r][at.lane][2 * v + 1]);
+        }
+    } else {
+#pragma unroll
+      for (int v = 0; v < VEC; ++v) mt[v] = m[v];
+    }
+    float mi[VEC];
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w)
+#pragma unroll
+      for (int v = 0; v < VEC; ++v)
+        if (w < at.warp)
+          h[v] = through(h[v], past[k][w][at.lane][2 * v], past[k][w][at.lane][2 * v + 1]);
+#pragma unroll
+    for (int w = kWarps - 1; w >= 0; --w)
+#pragma unroll
+      for (int v = 0; v < VEC; ++v) {
+        if (w == at.warp) mi[v] = mt[v];
+        mt[v] = through(mt[v], past[k][w][at.lane][2 * v], coming[k][w][at.lane][v]);
+      }
+    if (size == 1) {
+#pragma unroll
+      for (int v = 0; v < VEC; ++v) m[v] = mt[v];
+    }
+    // the distance of the state before a step to its value, in the value's place
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+      for (int v = 0; v < VEC; ++v) {
+        u[s][v] = h[v] - u[s][v];
+        h[v] = fmaf(-(keep[v] * open[s][v]), u[s][v], h[v]);
+      }
+    float some[VEC];
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) some[v] = 0.f;
+#pragma unroll
+    for (int s = kSteps - 1; s >= 0; --s) {
+      float dv[VEC], dg[VEC];
+#pragma unroll
+      for (int v = 0; v < VEC; ++v) {
+        const float b = keep[v] * open[s][v], lam = l[s][v] + mi[v];
+        mi[v] = fmaf(-b, lam, lam);
+        dv[v] = b * lam;
+        const float w = lam * u[s][v];
+        dg[v] = w * (b * hold[s][v]);
+        some[v] = fmaf(w, open[s][v], some[v]);
+      }
+      if (s >= left) {
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) dv[v] = dg[v] = 0.f;
+      }
+      vw[s] = Cell<T, VEC>::put(dv);
+      gw[s] = Cell<T, VEC>::put(dg);
+    }
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) dfloor[v] += some[v];
+    const int64_t stop = tile < 0 ? t0 : p.seqlen;
+    store_rows<T, VEC>(vw, dvalue, p.dim, t0, stop, at.on);
+    store_rows<T, VEC>(gw, dgate, p.dim, t0, stop, at.on);
+  }
+  if (q.dstate0 && at.rank == 0 && at.warp == 0 && at.on) {
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) q.dstate0[at.b * p.dim + d + v] = m[v];
+  }
+  Word zero[kSteps];
+#pragma unroll
+  for (int s = 0; s < kSteps; ++s) zero[s] = Word(0);
+  for (int64_t tile = live + at.rank; tile < tiles; tile += size) {
+    store_rows<T, VEC>(zero, dvalue, p.dim, tile * kTile + inside, p.seqlen, at.on);
+    store_rows<T, VEC>(zero, dgate, p.dim, tile * kTile + inside, p.seqlen, at.on);
+  }
+  if (q.dfloor) {
+    __syncthreads();
+    float* sums = &past[0][0][0][0];  // [warp][lane][VEC]
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) sums[(at.warp * 32 + at.lane) * VEC + v] = dfloor[v];
+    __syncthreads();
+    if (at.warp == 0 && at.on) {
+#pragma unroll
+      for (int v = 0; v < VEC; ++v) {
+        float t = 0.f;
+        for (int w = 0; w < kWarps; ++w) t += sums[(w * 32 + at.lane) * VEC + v];
+        q.partial[(at.b * size + at.rank) * p.dim + d + v] = t;
+      }
+    }
+  }
+}
+
+// dfloor: the sum of `rows` partial sums per channel; 8 threads share a channel.
+__global__ void __launch_bounds__(256) recur_floor_kernel(const float* partial, int64_t rows,
+                                                          int64_t dim, float* dfloor) {
+  __shared__ float part[8][33];
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const int64_t d = static_cast<int64_t>(blockIdx.x) * 32 + lane;
+  wait_previous();
+  float t = 0.f;
+  if (d < dim) {
+#pragma unroll 8
+    for (int64_t r = w; r < rows; r += 8) t += partial[r * dim + d];
+  }
+  part[w][lane] = t;
+  __syncthreads();
+  if (w == 0 && d < dim) {
+#pragma unroll
+    for (int i = 1; i < 8; ++i) t += part[i][lane];
+    dfloor[d] = t;
+  }
+}
+
+template <typename T, int VEC>
+__global__ void __launch_bounds__(256) recur_step_kernel(const RecurParams p) {
+  const int64_t vecs = p.dim / VEC;
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  const int64_t b = i / vecs, d = (i - b * vecs) * VEC;
+  if (b >= p.batch) return;
+  float g[VEC], u[VEC], h[VEC], f[VEC];
+  load_f<T, VEC>(static_cast<const T*>(p.gate) + b * p.gate_batch + d, g);
+  load_f<T, VEC>(static_cast<const T*>(p.value) + b * p.value_batch + d, u);
+  widen<VEC>(raw_load_rw<float, VEC>(p.out_final + b * p.dim + d), h);
+  if (p.floor) {
+    load_f<float, VEC>(p.floor + d, f);
+  } else {
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) f[v] = 0.f;
+  }
+#pragma unroll
+  for (int v = 0; v < VEC; ++v) h[v] = fmaf((1.f - f[v]) * recur::opening(g[v]), u[v] - h[v], h[v]);
+  store_f<float, VEC>(p.out_final + b * p.dim + d, h);
+  store_f<T, VEC>(static_cast<T*>(p.y) + b * p.dim + d, h);
+}
+
+// Whether rows of 2 bf16 channels can be read in one access.
+bool pairs(const RecurParams& p) {
+  return p.dim % 2 == 0 && p.gate_batch % 2 == 0 && p.gate_step % 2 == 0 &&
+         p.value_batch % 2 == 0 && p.value_step % 2 == 0 &&
+         (reinterpret_cast<uintptr_t>(p.gate) | reinterpret_cast<uintptr_t>(p.value) |
+          reinterpret_cast<uintptr_t>(p.y)) % 4 == 0;
+}
+
+template <typename... P, typename... A>
+cudaError_t launch_cluster(void (*kernel)(P...), int64_t units, int size, cudaStream_t s,
+                           A... args) {
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = size;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(units * size));
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = s;
+  cfg.attrs = &attr;
+  cfg.numAttrs = size > 1 ? 1 : 0;
+  if (size > 8) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+}
+
+}  // namespace
+
+// CTAs that share the time of a channel group: a power of two, while the grid
+// stays within two CTAs per SM and every CTA has tiles of its own.
+static int recur_cluster(int64_t batch, int64_t seqlen, int64_t units) {
+  const int64_t tiles = (seqlen + kTile - 1) / kTile;
+  int r = 1;
+  while (r < kMaxCluster && 2 * r * units <= 2 * kSms && 2 * r <= tiles) r *= 2;
+  return r;
+}
+
+int64_t recur_bwd_partials(int64_t batch, int64_t seqlen) { return batch * kMaxCluster; }
+
+cudaError_t launch_recur_fwd(const RecurParams& p, bool bf16, cudaStream_t s) {
+  const bool two = bf16 && pairs(p);
+  const int64_t lanes = two ? 64 : 32;
+  const int64_t units = p.batch * ((p.dim + lanes - 1) / lanes);
+  const int r = recur_cluster(p.batch, p.seqlen, units);
+  if (!bf16) return launch_cluster(recur_fwd_kernel<float, 1>, units, r, s, p, r);
+  return two ? launch_cluster(recur_fwd_kernel<__nv_bfloat16, 2>, units, r, s, p, r)
+             : launch_cluster(recur_fwd_kernel<__nv_bfloat16, 1>, units, r, s, p, r);
+}
+
+cudaError_t launch_recur_bwd(const RecurBwdParams& q, bool bf16, cudaStream_t s) {
+  RecurParams p = q.fwd;
+  const bool two = bf16 && pairs(p) &&
+                   (reinterpret_cast<uintptr_t>(q.dy) | reinterpret_cast<uintptr_t>(q.dgate) |
+                    reinterpret_cast<uintptr_t>(q.dvalue)) % 4 == 0;
+  const int64_t lanes = two ? 64 : 32;
+  const int64_t units = p.batch * ((p.dim + lanes - 1) / lanes);
+  const int r = recur_cluster(p.batch, p.seqlen, units);
+  cudaError_t e;
+  if (!bf16)
+    e = launch_cluster(recur_bwd_kernel<float, 1>, units, r, s, q, r);
+  else
+    e = two ? launch_cluster(recur_bwd_kernel<__nv_bfloat16, 2>, units, r, s, q, r)
+            : launch_cluster(recur_bwd_kernel<__nv_bfloat16, 1>, units, r, s, q, r);
+  if (e != cudaSuccess || !q.dfloor) return e;
+  return launch_after(recur_floor_kernel, static_cast<unsigned>((p.dim + 31) / 32), 256, 0, s,
+                      q.partial, p.batch * r, p.dim, q.dfloor);
+}
+
+cudaError_t launch_recur_step(const RecurParams& p, bool bf16, cudaStream_t s) {
+  const auto wide = [&](int vec, size_t bytes) {
+    return p.dim % vec == 0 && p.gate_batch % vec == 0 && p.value_batch % vec == 0 &&
+           (reinterpret_cast<uintptr_t>(p.gate) | reinterpret_cast<uintptr_t>(p.value) |
+            reinterpret_cast<uintptr_t>(p.y)) % bytes == 0 &&
+           (reinterpret_cast<uintptr_t>(p.out_final) | reinterpret_cast<uintptr_t>(p.floor)) % 16 == 0;
+  };
+  const auto go = [&](auto* kernel, int vec) {
+    const int64_t n = p.batch * (p.dim / vec);
+    kernel<<<static_cast<unsigned>((n + 255) / 256), 256, 0, s>>>(p);
+    return cudaGetLastError();
+  };
+  if (!bf16) return wide(4, 16) ? go(recur_step_kernel<float, 4>, 4) : go(recur_step_kernel<float, 1>, 1);
+  return wide(8, 16) ? go(recur_step_kernel<__nv_bfloat16, 8>, 8)
+                     : go(recur_step_kernel<__nv_bfloat16, 1>, 1);
+}
+
+}  // namespace ssm

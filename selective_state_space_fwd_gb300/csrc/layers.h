@@ -1,6 +1,6 @@
 // layers.h -- parameters and launchers of the operators around the scan: the
-// short causal convolution, the norm of the residual stream and the softmax
-// cross entropy over the vocabulary.
+// short causal convolution, the norm of the residual stream, the softmax cross
+// entropy over the vocabulary and the gated linear recurrence.
 #pragma once
 #include <cuda_runtime.h>
 #include <stddef.h>
@@ -124,5 +124,38 @@ struct XentParams {
 size_t xent_workspace_bytes(const XentShape& s, bool backward);
 cudaError_t launch_xent_fwd(const XentParams& p, cudaStream_t s);
 cudaError_t launch_xent_bwd(const XentParams& p, cudaStream_t s);
+
+// ---- gated linear recurrence (kernel_recur.cu) ----------------------------------
+constexpr int kRecurChunk = 64;  // steps between the states kept for the backward
+struct RecurParams {
+  const void* gate;                  // [batch, seqlen, dim], channels contiguous
+  const void* value;
+  int64_t gate_batch, gate_step;     // strides in elements
+  int64_t value_batch, value_step;
+  const float* floor;                // nullable, [dim]
+  const int32_t* valid_len;          // nullable, [batch]
+  const float* state0;               // nullable, [batch, dim]
+  void* y;                           // [batch, seqlen, dim]
+  float* out_final;                  // nullable, [batch, dim]; the step: the state, in place
+  float* states;                     // nullable, [batch, chunks, dim]: entering each chunk
+  int64_t batch, seqlen, dim;
+};
+
+struct RecurBwdParams {
+  RecurParams fwd;        // state0, y, out_final, states unused
+  const float* states;    // [batch, chunks, dim]
+  const void* dy;         // [batch, seqlen, dim]
+  const float* dfinal;    // nullable, [batch, dim]
+  void* dgate;            // [batch, seqlen, dim]
+  void* dvalue;           // [batch, seqlen, dim]
+  float* dfloor;          // nullable, [dim]
+  float* dstate0;         // nullable, [batch, dim]
+  float* partial;         // workspace: [recur_bwd_partials, dim]
+};
+
+int64_t recur_bwd_partials(int64_t batch, int64_t seqlen);
+cudaError_t launch_recur_fwd(const RecurParams& p, bool bf16, cudaStream_t s);
+cudaError_t launch_recur_bwd(const RecurBwdParams& p, bool bf16, cudaStream_t s);
+cudaError_t launch_recur_step(const RecurParams& p, bool bf16, cudaStream_t s);
 
 }  // namespace ssm

@@ -1,5 +1,6 @@
 """The operators around the scan: short causal convolution, norm of the residual
-stream, and softmax cross entropy over the vocabulary.
+stream, softmax cross entropy over the vocabulary, and the gated linear
+recurrence.
 
 Argument marshalling only, like ``_binding``: dtypes, shapes, devices and
 strides are checked, outputs and workspaces are allocated when the caller
@@ -15,7 +16,8 @@ import functools
 
 import torch
 
-from ._binding import ConvShapes, DType, NormShapes, SsmError, XentShapes, _check, load
+from ._binding import (ConvShapes, DType, NormShapes, RecurShapes, SsmError, XentShapes, _check,
+                       load)
 
 _F32 = torch.float32
 _CODES = {_F32: int(DType.F32), torch.bfloat16: int(DType.BF16)}
@@ -46,6 +48,11 @@ def _xent_sizes(*sizes):
 
 
 @functools.lru_cache(maxsize=512)
+def _recur_sizes(*sizes):
+    return ctypes.byref(RecurShapes(*sizes))
+
+
+@functools.lru_cache(maxsize=512)
 def _conv_workspace(sizes):
     return load().ssm_conv_bwd_workspace_bytes(sizes)
 
@@ -58,6 +65,11 @@ def _norm_workspace(sizes):
 @functools.lru_cache(maxsize=512)
 def _xent_workspace(sizes, backward):
     return load().ssm_xent_workspace_bytes(sizes, backward)
+
+
+@functools.lru_cache(maxsize=512)
+def _recur_workspace(sizes):
+    return load().ssm_recur_bwd_workspace_bytes(sizes)
 
 
 def _code(dtype) -> int:
@@ -376,3 +388,116 @@ def xent_bwd(h, weight, targets, *, lse, dloss, ignore_index: int = -100, worksp
           lse.data_ptr(), dloss.data_ptr(), dh.data_ptr(), dweight.data_ptr(), ws.data_ptr(),
           ws.numel(), sizes, code)
     return {"dh": dh, "dweight": dweight}
+
+
+def _recur_args(gate, value, floor, rank):
+    """Checked (device, dtype code, batch, seqlen, dim, RecurShapes) of a
+    recurrence whose gate and value have `rank` dimensions, the last of them
+    contiguous."""
+    dev = _cuda(gate, "gate")
+    code = _code(gate.dtype)
+    size = gate.shape
+    if len(size) != rank:
+        raise ValueError(f"gate: {len(size)} dimensions, expected {rank}")
+    if value.dtype is not gate.dtype:
+        raise TypeError(f"value: dtype {value.dtype}, expected {gate.dtype}")
+    if value.shape != size or value.device != dev:
+        raise ValueError(f"value: shape {tuple(value.shape)} on {value.device}, "
+                         f"expected {tuple(size)} on {dev}")
+    batch, dim = size[0], size[-1]
+    seqlen = size[1] if rank == 3 else 1
+    strides = []
+    for name, t in (("gate", gate), ("value", value)):
+        stride = t.stride()
+        if stride[-1] != 1 and dim > 1:
+            raise ValueError(f"{name}: the channels must be contiguous")
+        # the stride of an axis of one element is never used; the row's own length
+        # keeps it from deciding the alignment rule
+        strides += [stride[0] if batch > 1 else dim, stride[1] if seqlen > 1 else dim]
+    if floor is not None:
+        _dense(floor, "floor", (dim,), _F32, dev)
+    return dev, code, batch, seqlen, dim, _recur_sizes(batch, seqlen, dim, *strides)
+
+
+def recur_fwd(gate, value, floor=None, valid_len=None, *, state0=None, want_final: bool = False,
+              want_states: bool = False, out=None, out_final=None, stream=None):
+    """The gated linear recurrence of every channel along time,
+
+        h[t] = a[t] h[t-1] + (1 - a[t]) value[t],
+        a[t] = floor + (1 - floor) sigmoid(gate[t]).
+
+    gate, value: [batch, L, dim], fp32 or bf16, channels contiguous; rows may be
+    strided (halves of the columns of one projection).  floor: fp32 [dim], in
+    [0, 1], 0 when None; valid_len: int32 [batch], steps past it give 0 and leave
+    the state, whatever gate and value hold there.  state0: fp32 [batch, dim], h
+    before the first step (zeros when None).  Returns ``(y, final, states)``: y
+    [batch, L, dim] like gate, h of every step; final fp32 [batch, dim], from
+    which a next call or ``recur_step`` continues (None unless ``want_final``);
+    states fp32 [batch, chunks, dim], which ``recur_bwd`` needs (None unless
+    ``want_states``)."""
+    if stream is not None:
+        return _on_stream(stream, recur_fwd, gate, value, floor, valid_len, state0=state0,
+                          want_final=want_final, want_states=want_states, out=out,
+                          out_final=out_final)
+    dev, code, batch, L, dim, sizes = _recur_args(gate, value, floor, 3)
+    if valid_len is not None:
+        _dense(valid_len, "valid_len", (batch,), torch.int32, dev)
+    if state0 is not None:
+        _dense(state0, "state0", (batch, dim), _F32, dev)
+    lib = load()
+    y = _like(out, "out", gate, (batch, L, dim), dev)
+    final = states = None
+    if want_final or out_final is not None:
+        final = _new(out_final, "out_final", (batch, dim), _F32, dev)
+    if want_states:
+        states = torch.empty((batch, lib.ssm_recur_chunks(sizes), dim), dtype=_F32, device=dev)
+    _call(lib.ssm_recur_fwd, dev, gate.data_ptr(), value.data_ptr(), _addr(floor),
+          _addr(valid_len), _addr(state0), y.data_ptr(), _addr(final), _addr(states), sizes, code)
+    return y, final, states
+
+
+def recur_bwd(gate, value, floor=None, valid_len=None, *, states, dy, dfinal=None,
+              want_dstate0: bool = False, workspace=None, stream=None) -> dict:
+    """Every gradient of sum(dy * y) + sum(dfinal * final) for ``recur_fwd`` on
+    the same inputs: a dict of dgate and dvalue (like gate, contiguous), dfloor
+    (fp32; None without a floor) and dstate0 (fp32, when wanted).  states: the
+    forward's; dfinal: fp32 [batch, dim] or None.  ``workspace``, a CUDA uint8
+    tensor, is only used with a floor and is allocated here when None."""
+    if stream is not None:
+        return _on_stream(stream, recur_bwd, gate, value, floor, valid_len, states=states, dy=dy,
+                          dfinal=dfinal, want_dstate0=want_dstate0, workspace=workspace)
+    dev, code, batch, L, dim, sizes = _recur_args(gate, value, floor, 3)
+    lib = load()
+    if valid_len is not None:
+        _dense(valid_len, "valid_len", (batch,), torch.int32, dev)
+    _dense(states, "states", (batch, lib.ssm_recur_chunks(sizes), dim), _F32, dev)
+    _dense(dy, "dy", (batch, L, dim), gate.dtype, dev)
+    if dfinal is not None:
+        _dense(dfinal, "dfinal", (batch, dim), _F32, dev)
+    g = {"dgate": torch.empty_like(dy), "dvalue": torch.empty_like(dy), "dfloor": None,
+         "dstate0": torch.empty((batch, dim), dtype=_F32, device=dev) if want_dstate0 else None}
+    ws = None
+    if floor is not None:
+        g["dfloor"] = torch.empty_like(floor)
+        ws = _workspace(workspace, _recur_workspace(sizes), dev)
+    _call(lib.ssm_recur_bwd, dev, gate.data_ptr(), value.data_ptr(), _addr(floor),
+          _addr(valid_len), states.data_ptr(), dy.data_ptr(), _addr(dfinal),
+          g["dgate"].data_ptr(), g["dvalue"].data_ptr(), _addr(g["dfloor"]), _addr(g["dstate0"]),
+          _addr(ws), 0 if ws is None else ws.numel(), sizes, code)
+    return g
+
+
+def recur_step(gate, value, floor=None, *, state, out=None, stream=None):
+    """One step of the recurrence on a carried state, in place (decode).
+
+    gate, value: [batch, dim] (rows may be strided); state: fp32 [batch, dim], h
+    (``recur_fwd``'s final state), advanced by the step.  Returns y [batch, dim]
+    like gate."""
+    if stream is not None:
+        return _on_stream(stream, recur_step, gate, value, floor, state=state, out=out)
+    dev, code, batch, _, dim, sizes = _recur_args(gate, value, floor, 2)
+    _dense(state, "state", (batch, dim), _F32, dev)
+    y = _like(out, "out", gate, (batch, dim), dev)
+    _call(load().ssm_recur_step, dev, gate.data_ptr(), value.data_ptr(), _addr(floor),
+          state.data_ptr(), y.data_ptr(), sizes, code)
+    return y
