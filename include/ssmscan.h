@@ -589,6 +589,46 @@ ssm_status ssm_recur_step(const void* gate, const void* value, const float* floo
                           void* out_y, const ssm_recur_shapes* shapes, ssm_dtype dtype,
                           cudaStream_t stream);
 
+/* Sizes and types of the embedding lookup. */
+typedef struct {
+  int64_t tokens;       /* 1 .. 2^30 */
+  int64_t vocab;        /* 1 .. 2^30 */
+  int64_t dim;          /* >= 1 */
+  int64_t ignore_index; /* ids of this value take no part */
+  float scale;          /* of the looked up rows; finite */
+  ssm_dtype dtype;      /* of weight and dweight */
+  ssm_dtype io_dtype;   /* of y and dy: `dtype`, or SSM_F32 */
+} ssm_embed_shapes;
+
+/*
+ * ssm_embed_fwd -- y[t] = scale weight[ids[t]], rounded to io_dtype once.  An
+ * id of ignore_index gives a row of zeros, any other id outside [0, vocab) one
+ * of NaN.
+ *   ids    : device int64 [tokens].
+ *   weight : device, [vocab, dim], dtype.   out_y : device, [tokens, dim], io_dtype.
+ */
+ssm_status ssm_embed_fwd(const int64_t* ids, const void* weight, void* out_y,
+                         const ssm_embed_shapes* shapes, cudaStream_t stream);
+
+/*
+ * ssm_embed_bwd -- the gradient of sum(dy * y) in the weight:
+ *   dweight[v] = scale sum_{t: ids[t] = v} dy[t],
+ * summed in fp32 in an order fixed by the ids (equal inputs give equal bits) and
+ * rounded to dtype once.  ids of ignore_index, and ids outside [0, vocab), take no
+ * part, whatever their rows of dy hold.
+ *   dy        : device, [tokens, dim], io_dtype.
+ *   dweight   : device, [vocab, dim], dtype.  With `add` 0 it is written as a
+ *               whole; with `add` 1 the sums are added to what it holds, and rows
+ *               that no id names are neither read nor written.
+ *   workspace : at least ssm_embed_bwd_workspace_bytes() bytes, 256-byte aligned,
+ *               unused by other work until `stream` passes the call.
+ */
+ssm_status ssm_embed_bwd(const int64_t* ids, const void* dy, void* dweight, int add,
+                         void* workspace, size_t workspace_bytes, const ssm_embed_shapes* shapes,
+                         cudaStream_t stream);
+/* Workspace bytes of ssm_embed_bwd; 0 on invalid shapes. */
+size_t ssm_embed_bwd_workspace_bytes(const ssm_embed_shapes* shapes);
+
 /* The tier (and its grid) that ssm_scan_fwd_ex would launch for these
  * arguments, without launching anything.  `has_*` describe which optional
  * tensors the call passes.  Writes the tier to *kernel and the launch grid

@@ -99,6 +99,13 @@ class RecurShapes(ctypes.Structure):
                 ("value_batch_stride", ctypes.c_int64), ("value_step_stride", ctypes.c_int64)]
 
 
+class EmbedShapes(ctypes.Structure):
+    """ssm_embed_shapes."""
+    _fields_ = [("tokens", ctypes.c_int64), ("vocab", ctypes.c_int64), ("dim", ctypes.c_int64),
+                ("ignore_index", ctypes.c_int64), ("scale", ctypes.c_float),
+                ("dtype", ctypes.c_int32), ("io_dtype", ctypes.c_int32)]
+
+
 def _prep(dt_bias, delta_softplus, delta_clamp, dim, dev):
     """A DeltaPrep for the keyword arguments, or None when nothing is asked."""
     if dt_bias is None and not delta_softplus and delta_clamp is None:
@@ -200,6 +207,13 @@ def load() -> ctypes.CDLL:
     lib.ssm_recur_chunks.argtypes = [RP]
     lib.ssm_recur_step.restype = I32
     lib.ssm_recur_step.argtypes = [P] * 5 + [RP, I32, P]
+    EP = ctypes.POINTER(EmbedShapes)
+    lib.ssm_embed_fwd.restype = I32
+    lib.ssm_embed_fwd.argtypes = [P] * 3 + [EP, P]
+    lib.ssm_embed_bwd.restype = I32
+    lib.ssm_embed_bwd.argtypes = [P] * 3 + [I32, P, SZ, EP, P]
+    lib.ssm_embed_bwd_workspace_bytes.restype = SZ
+    lib.ssm_embed_bwd_workspace_bytes.argtypes = [EP]
     _lib = lib
     return lib
 

@@ -14,8 +14,8 @@ import functools
 import torch
 
 from ._binding import scan_bwd, scan_fwd
-from .layers import (conv_bwd, conv_fwd, norm_bwd, norm_fwd, recur_bwd, recur_fwd, xent_bwd,
-                     xent_fwd)
+from .layers import (conv_bwd, conv_fwd, embed_bwd, embed_fwd, norm_bwd, norm_fwd, recur_bwd,
+                     recur_fwd, xent_bwd, xent_fwd)
 
 
 class _Final(torch.autograd.Function):
@@ -195,3 +195,25 @@ def gated_recurrence(gate, value, floor=None, valid_len=None, *, state0=None,
     ``want_final``, final being differentiable too."""
     y, final = _GatedRecurrence.apply(gate, value, floor, valid_len, state0)
     return (y, final) if want_final else y
+
+
+class _Embedding(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, ids, weight, scale, ignore_index, dtype):
+        ctx.save_for_backward(ids)
+        ctx.vocab, ctx.dtype = weight.shape[0], weight.dtype
+        ctx.scale, ctx.ignore_index = scale, ignore_index
+        return embed_fwd(ids, weight, scale=scale, ignore_index=ignore_index, dtype=dtype)
+
+    @staticmethod
+    @_once("embedding")
+    def backward(ctx, dy):
+        (ids,) = ctx.saved_tensors
+        g = embed_bwd(ids, dy.contiguous(), vocab=ctx.vocab, scale=ctx.scale,
+                      ignore_index=ctx.ignore_index, dtype=ctx.dtype)
+        return None, g, None, None, None
+
+
+def embedding(ids, weight, *, scale: float = 1.0, ignore_index: int = -100, dtype=None):
+    """y = scale weight[ids] (as ``embed_fwd``), differentiable in weight."""
+    return _Embedding.apply(ids, weight, float(scale), int(ignore_index), dtype)

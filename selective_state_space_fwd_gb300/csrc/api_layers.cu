@@ -112,6 +112,21 @@ ssm::RecurParams recur_params(const void* gate, const void* value, const float* 
   return p;
 }
 
+ssm_status check_embed(const ssm_embed_shapes* s) {
+  if (s == nullptr) return SSM_ERR_NULL;
+  if (!known(s->dtype) || !known(s->io_dtype)) return SSM_ERR_UNSUPPORTED;
+  if (s->tokens < 1 || s->vocab < 1 || s->dim < 1) return SSM_ERR_SHAPE;
+  if (!isfinite(s->scale)) return SSM_ERR_SHAPE;
+  if (s->io_dtype != s->dtype && s->io_dtype != SSM_F32) return SSM_ERR_UNSUPPORTED;
+  const int64_t lim = int64_t(1) << 30;  // ids and tokens are kept in 32 bits
+  int64_t n;
+  if (s->tokens > lim || s->vocab > lim || !mul_ok(s->vocab, s->dim, &n) || n > kMaxElements)
+    return SSM_ERR_SHAPE;
+  // the grid of the sums: a warp per 8 tokens and 128 columns at most
+  if (!mul_ok(s->tokens / 8 + 1, s->dim / 128 + 1, &n) || n > INT32_MAX) return SSM_ERR_SHAPE;
+  return SSM_OK;
+}
+
 ssm::XentParams xent_params(const void* h, const void* weight, const int64_t* targets,
                             const ssm_xent_shapes& s, void* workspace) {
   ssm::XentParams p = {};
@@ -366,6 +381,50 @@ ssm_status ssm_recur_step(const void* gate, const void* value, const float* floo
   ssm::RecurParams p = recur_params(gate, value, floor, nullptr, *shapes);
   p.y = out_y; p.out_final = state;
   return status_of(ssm::launch_recur_step(p, dtype == SSM_BF16, stream));
+}
+
+ssm_status ssm_embed_fwd(const int64_t* ids, const void* weight, void* out_y,
+                         const ssm_embed_shapes* shapes, cudaStream_t stream) {
+  ssm_status st = check_embed(shapes);
+  if (st != SSM_OK) return st;
+  const ssm_embed_shapes& s = *shapes;
+  if (!ids || !weight || !out_y) return SSM_ERR_NULL;
+  if (!aligned(ids, 8) || !aligned(weight, elem_size(s.dtype)) ||
+      !aligned(out_y, elem_size(s.io_dtype)))
+    return SSM_ERR_ALIGN;
+  int dev = 0;
+  if ((st = current_device_for(stream, &dev)) != SSM_OK) return st;
+  ssm::EmbedParams p;
+  p.ids = ids; p.weight = weight; p.y = out_y;
+  p.tokens = s.tokens; p.vocab = s.vocab; p.dim = s.dim;
+  p.ignore = s.ignore_index; p.scale = s.scale;
+  return status_of(ssm::launch_embed_fwd(p, s.dtype == SSM_BF16, s.io_dtype == SSM_BF16, stream));
+}
+
+size_t ssm_embed_bwd_workspace_bytes(const ssm_embed_shapes* shapes) {
+  if (check_embed(shapes) != SSM_OK) return 0;
+  return ssm::embed_bwd_workspace_bytes(shapes->tokens, shapes->dim);
+}
+
+ssm_status ssm_embed_bwd(const int64_t* ids, const void* dy, void* dweight, int add,
+                         void* workspace, size_t workspace_bytes, const ssm_embed_shapes* shapes,
+                         cudaStream_t stream) {
+  ssm_status st = check_embed(shapes);
+  if (st != SSM_OK) return st;
+  const ssm_embed_shapes& s = *shapes;
+  if (add != 0 && add != 1) return SSM_ERR_UNSUPPORTED;
+  if (!ids || !dy || !dweight || !workspace) return SSM_ERR_NULL;
+  if (!aligned(ids, 8) || !aligned(dy, elem_size(s.io_dtype)) ||
+      !aligned(dweight, elem_size(s.dtype)) || !aligned(workspace, 256))
+    return SSM_ERR_ALIGN;
+  if (workspace_bytes < ssm_embed_bwd_workspace_bytes(shapes)) return SSM_ERR_SHAPE;
+  int dev = 0;
+  if ((st = current_device_for(stream, &dev)) != SSM_OK) return st;
+  ssm::EmbedBwdParams p;
+  p.ids = ids; p.dy = dy; p.dweight = dweight; p.add = add != 0;
+  p.tokens = s.tokens; p.vocab = s.vocab; p.dim = s.dim;
+  p.ignore = s.ignore_index; p.scale = s.scale; p.workspace = workspace;
+  return status_of(ssm::launch_embed_bwd(p, s.dtype == SSM_BF16, s.io_dtype == SSM_BF16, stream));
 }
 
 }  // extern "C"

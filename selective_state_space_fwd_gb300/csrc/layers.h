@@ -1,6 +1,6 @@
 // layers.h -- parameters and launchers of the operators around the scan: the
 // short causal convolution, the norm of the residual stream, the softmax cross
-// entropy over the vocabulary and the gated linear recurrence.
+// entropy over the vocabulary, the gated linear recurrence and the embedding lookup.
 #pragma once
 #include <cuda_runtime.h>
 #include <stddef.h>
@@ -157,5 +157,28 @@ int64_t recur_bwd_partials(int64_t batch, int64_t seqlen);
 cudaError_t launch_recur_fwd(const RecurParams& p, bool bf16, cudaStream_t s);
 cudaError_t launch_recur_bwd(const RecurBwdParams& p, bool bf16, cudaStream_t s);
 cudaError_t launch_recur_step(const RecurParams& p, bool bf16, cudaStream_t s);
+
+// ---- embedding lookup (kernel_embed.cu) --------------------------------------------
+struct EmbedParams {
+  const int64_t* ids;    // [tokens]
+  const void* weight;    // [vocab, dim], weight type
+  void* y;               // [tokens, dim], I/O type
+  int64_t tokens, vocab, dim, ignore;
+  float scale;
+};
+
+struct EmbedBwdParams {
+  const int64_t* ids;    // [tokens]
+  const void* dy;        // [tokens, dim], I/O type
+  void* dweight;         // [vocab, dim], weight type
+  bool add;              // onto what dweight holds
+  int64_t tokens, vocab, dim, ignore;
+  float scale;
+  void* workspace;
+};
+
+size_t embed_bwd_workspace_bytes(int64_t tokens, int64_t dim);
+cudaError_t launch_embed_fwd(const EmbedParams& p, bool bf16, bool io_bf16, cudaStream_t s);
+cudaError_t launch_embed_bwd(const EmbedBwdParams& p, bool bf16, bool io_bf16, cudaStream_t s);
 
 }  // namespace ssm

@@ -1,6 +1,6 @@
 """The operators around the scan: short causal convolution, norm of the residual
-stream, softmax cross entropy over the vocabulary, and the gated linear
-recurrence.
+stream, softmax cross entropy over the vocabulary, the gated linear recurrence,
+and the embedding lookup.
 
 Argument marshalling only, like ``_binding``: dtypes, shapes, devices and
 strides are checked, outputs and workspaces are allocated when the caller
@@ -16,8 +16,8 @@ import functools
 
 import torch
 
-from ._binding import (ConvShapes, DType, NormShapes, RecurShapes, SsmError, XentShapes, _check,
-                       load)
+from ._binding import (ConvShapes, DType, EmbedShapes, NormShapes, RecurShapes, SsmError,
+                       XentShapes, _check, load)
 
 _F32 = torch.float32
 _CODES = {_F32: int(DType.F32), torch.bfloat16: int(DType.BF16)}
@@ -53,6 +53,11 @@ def _recur_sizes(*sizes):
 
 
 @functools.lru_cache(maxsize=512)
+def _embed_sizes(*sizes):
+    return ctypes.byref(EmbedShapes(*sizes))
+
+
+@functools.lru_cache(maxsize=512)
 def _conv_workspace(sizes):
     return load().ssm_conv_bwd_workspace_bytes(sizes)
 
@@ -70,6 +75,11 @@ def _xent_workspace(sizes, backward):
 @functools.lru_cache(maxsize=512)
 def _recur_workspace(sizes):
     return load().ssm_recur_bwd_workspace_bytes(sizes)
+
+
+@functools.lru_cache(maxsize=512)
+def _embed_workspace(sizes):
+    return load().ssm_embed_bwd_workspace_bytes(sizes)
 
 
 def _code(dtype) -> int:
@@ -501,3 +511,71 @@ def recur_step(gate, value, floor=None, *, state, out=None, stream=None):
     _call(load().ssm_recur_step, dev, gate.data_ptr(), value.data_ptr(), _addr(floor),
           state.data_ptr(), y.data_ptr(), sizes, code)
     return y
+
+
+def embed_fwd(ids, weight, *, scale: float = 1.0, ignore_index: int = -100, dtype=None, out=None,
+              stream=None):
+    """The embedding lookup y = scale weight[ids].
+
+    ids: int64 [...], contiguous; weight: [vocab, dim], fp32 or bf16.  Returns y
+    [..., dim] in the weight's type, or in fp32 with ``dtype`` (a residual stream
+    kept in 32 bits); it is rounded once.  Tokens of ``ignore_index`` (padding) get
+    rows of zeros, any other id outside the vocabulary a row of NaN."""
+    if stream is not None:
+        return _on_stream(stream, embed_fwd, ids, weight, scale=scale, ignore_index=ignore_index,
+                          dtype=dtype, out=out)
+    dev = _cuda(ids, "ids")
+    if weight.dim() != 2:
+        raise ValueError(f"weight: shape {tuple(weight.shape)}, expected [vocab, dim]")
+    code = _code(weight.dtype)
+    vocab, dim = weight.shape
+    shape = ids.shape
+    _dense(ids, "ids", shape, torch.int64, dev)
+    _dense(weight, "weight", (vocab, dim), weight.dtype, dev)
+    dtype = weight.dtype if dtype is None else dtype
+    y = _new(out, "out", (*shape, dim), dtype, dev)
+    _call(load().ssm_embed_fwd, dev, ids.data_ptr(), weight.data_ptr(), y.data_ptr(),
+          _embed_sizes(ids.numel(), vocab, dim, int(ignore_index), float(scale), code,
+                       _code(dtype)))
+    return y
+
+
+def embed_bwd(ids, dy, *, vocab: int | None = None, scale: float = 1.0, ignore_index: int = -100,
+              dtype=None, add_to=None, workspace=None, stream=None):
+    """The gradient of sum(dy * y) in the weight of ``embed_fwd``, summed in fp32
+    in an order that the ids fix and rounded once.
+
+    dy: [..., dim] for ids [...].  Returns dweight [vocab, dim] in ``dtype`` (dy's
+    when None; dy may be fp32 for a bf16 weight).  With ``add_to``, [vocab, dim],
+    the sums are added to it instead (the gradient of a tied output embedding,
+    say) and it is returned; rows that no token names stay as they are.  Tokens of
+    ``ignore_index``, and ids outside the vocabulary, take no part."""
+    if stream is not None:
+        return _on_stream(stream, embed_bwd, ids, dy, vocab=vocab, scale=scale,
+                          ignore_index=ignore_index, dtype=dtype, add_to=add_to,
+                          workspace=workspace)
+    dev = _cuda(ids, "ids")
+    shape = ids.shape
+    _dense(ids, "ids", shape, torch.int64, dev)
+    if dy.dim() < 1:
+        raise ValueError("dy: no dimensions, expected [..., dim]")
+    dim = dy.shape[-1]
+    io = _code(dy.dtype)
+    _dense(dy, "dy", (*shape, dim), dy.dtype, dev)
+    if add_to is not None:
+        if dtype is not None and dtype != add_to.dtype:
+            raise TypeError(f"dtype: {dtype}, but add_to is {add_to.dtype}")
+        if vocab is not None and add_to.shape[:1] != (vocab,):
+            raise ValueError(f"vocab: {vocab}, but add_to is {tuple(add_to.shape)}")
+        vocab = add_to.shape[0] if add_to.dim() else 0
+        dweight = _dense(add_to, "add_to", (vocab, dim), add_to.dtype, dev)
+    else:
+        if vocab is None:
+            raise ValueError("vocab: needed without add_to")
+        dweight = torch.empty((vocab, dim), dtype=dy.dtype if dtype is None else dtype, device=dev)
+    sizes = _embed_sizes(ids.numel(), vocab, dim, int(ignore_index), float(scale),
+                         _code(dweight.dtype), io)
+    ws = _workspace(workspace, _embed_workspace(sizes), dev)
+    _call(load().ssm_embed_bwd, dev, ids.data_ptr(), dy.data_ptr(), dweight.data_ptr(),
+          0 if add_to is None else 1, ws.data_ptr(), ws.numel(), sizes)
+    return dweight
