@@ -515,6 +515,63 @@ ssm_status ssm_xent_bwd(const void* h, const void* weight, const int64_t* target
  * on invalid shapes. */
 size_t ssm_xent_workspace_bytes(const ssm_xent_shapes* shapes, int backward);
 
+/* Sizes of the distillation. */
+typedef struct {
+  int64_t tokens;          /* 1 .. 2^30 */
+  int64_t vocab;           /* 1 .. 2^30 */
+  int64_t dim;             /* >= 1, a multiple of 8 */
+  int64_t top;             /* the teacher's entries per token, 1 .. 1024 */
+  int64_t ignore_index;    /* entries whose id has this value take no part */
+  float temperature;       /* of both softmaxes; finite and > 0 */
+  ssm_dtype teacher_dtype; /* of the teacher's logits */
+} ssm_distill_shapes;
+
+/*
+ * ssm_distill_fwd -- the divergence of a student from a teacher of whom only the
+ * top logits are known, from the student's hidden states and without keeping its
+ * logits S = h weight^T.  With the teacher's entries (ids[t,k], logits[t,k]) and
+ * T the temperature:
+ *   q[t,:] = softmax_k(logits[t,:] / T)   over the entries that take part,
+ *   lse[t] = log sum_v exp(S[t,v] / T),
+ *   loss[t] = sum_k q[t,k] (log q[t,k] - (S[t, ids[t,k]] / T - lse[t])).
+ * Entries with an id of ignore_index or a logit of -infinity take no part; an id
+ * that comes twice counts twice.  Tokens with no entry left get loss 0 and lse 0,
+ * and their rows of h are not used.  Any other id outside [0, vocab) gives its
+ * token a loss of NaN.
+ *   h       : device bf16 [tokens, dim], 16-byte aligned.
+ *   weight  : device bf16 [vocab, dim], 16-byte aligned.
+ *   ids     : device int64 [tokens, top].
+ *   logits  : device, [tokens, top], teacher_dtype.
+ *   out_loss, out_lse : device fp32 [tokens].
+ *   workspace : at least ssm_distill_workspace_bytes(shapes, 0) bytes, 256-byte
+ *             aligned, unused by other work until `stream` passes the call.
+ * Arithmetic, dtype (of h and weight) and errors as in ssm_xent_fwd.
+ */
+ssm_status ssm_distill_fwd(const void* h, const void* weight, const int64_t* ids,
+                           const void* logits, float* out_loss, float* out_lse, void* workspace,
+                           size_t workspace_bytes, const ssm_distill_shapes* shapes,
+                           ssm_dtype dtype, cudaStream_t stream);
+
+/*
+ * ssm_distill_bwd -- the gradients of sum_t dloss[t] loss[t] for ssm_distill_fwd
+ * in the student (the teacher has none):
+ *   G[t,v] = dloss[t] / T (exp(S[t,v] / T - lse[t]) - sum_{k: ids[t,k] = v} q[t,k]),
+ *   dh = G weight,   dweight = G^T h,
+ * formed as in ssm_xent_bwd, whose notes hold.
+ *   lse     : the forward's out_lse.   dloss : device fp32 [tokens], without
+ *             effect for tokens with no entry.
+ *   dh      : device bf16 [tokens, dim], 16-byte aligned; 0 for those tokens.
+ *   dweight : device bf16 [vocab, dim], 16-byte aligned.
+ *   workspace : at least ssm_distill_workspace_bytes(shapes, 1) bytes, as above.
+ */
+ssm_status ssm_distill_bwd(const void* h, const void* weight, const int64_t* ids,
+                           const void* logits, const float* lse, const float* dloss, void* dh,
+                           void* dweight, void* workspace, size_t workspace_bytes,
+                           const ssm_distill_shapes* shapes, ssm_dtype dtype, cudaStream_t stream);
+/* Workspace bytes of ssm_distill_fwd (backward 0) or ssm_distill_bwd (backward
+ * 1); 0 on invalid shapes. */
+size_t ssm_distill_workspace_bytes(const ssm_distill_shapes* shapes, int backward);
+
 /* Sizes and strides of the gated linear recurrence.  Strides are in elements;
  * channels are contiguous.  The stride of an axis of one element is not used. */
 typedef struct {

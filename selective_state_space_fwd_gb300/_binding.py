@@ -92,6 +92,13 @@ class XentShapes(ctypes.Structure):
                 ("ignore_index", ctypes.c_int64)]
 
 
+class DistillShapes(ctypes.Structure):
+    """ssm_distill_shapes."""
+    _fields_ = [("tokens", ctypes.c_int64), ("vocab", ctypes.c_int64), ("dim", ctypes.c_int64),
+                ("top", ctypes.c_int64), ("ignore_index", ctypes.c_int64),
+                ("temperature", ctypes.c_float), ("teacher_dtype", ctypes.c_int32)]
+
+
 class RecurShapes(ctypes.Structure):
     """ssm_recur_shapes."""
     _fields_ = [("batch", ctypes.c_int64), ("seqlen", ctypes.c_int64), ("dim", ctypes.c_int64),
@@ -196,6 +203,13 @@ def load() -> ctypes.CDLL:
     lib.ssm_xent_bwd.argtypes = [P] * 8 + [SZ, XP, I32, P]
     lib.ssm_xent_workspace_bytes.restype = SZ
     lib.ssm_xent_workspace_bytes.argtypes = [XP, I32]
+    LP = ctypes.POINTER(DistillShapes)
+    lib.ssm_distill_fwd.restype = I32
+    lib.ssm_distill_fwd.argtypes = [P] * 7 + [SZ, LP, I32, P]
+    lib.ssm_distill_bwd.restype = I32
+    lib.ssm_distill_bwd.argtypes = [P] * 9 + [SZ, LP, I32, P]
+    lib.ssm_distill_workspace_bytes.restype = SZ
+    lib.ssm_distill_workspace_bytes.argtypes = [LP, I32]
     RP = ctypes.POINTER(RecurShapes)
     lib.ssm_recur_fwd.restype = I32
     lib.ssm_recur_fwd.argtypes = [P] * 8 + [RP, I32, P]

@@ -14,8 +14,8 @@ import functools
 import torch
 
 from ._binding import scan_bwd, scan_fwd
-from .layers import (conv_bwd, conv_fwd, embed_bwd, embed_fwd, norm_bwd, norm_fwd, recur_bwd,
-                     recur_fwd, xent_bwd, xent_fwd)
+from .layers import (conv_bwd, conv_fwd, distill_bwd, distill_fwd, embed_bwd, embed_fwd, norm_bwd,
+                     norm_fwd, recur_bwd, recur_fwd, xent_bwd, xent_fwd)
 
 
 class _Final(torch.autograd.Function):
@@ -165,6 +165,51 @@ def linear_cross_entropy(h, weight, targets, *, ignore_index: int = -100, reduct
         return loss.view(targets.shape)
     total = loss.sum()
     return total if reduction == "sum" else total / (targets != ignore_index).sum().clamp(min=1)
+
+
+class _Distillation(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, h, weight, ids, logits, temperature, ignore_index):
+        loss, lse = distill_fwd(h, weight, ids, logits, temperature=temperature,
+                                ignore_index=ignore_index)
+        ctx.save_for_backward(h, weight, ids, logits, lse)
+        ctx.temperature, ctx.ignore_index = temperature, ignore_index
+        return loss
+
+    @staticmethod
+    @_once("linear_distillation")
+    def backward(ctx, dloss):
+        h, weight, ids, logits, lse = ctx.saved_tensors
+        g = distill_bwd(h, weight, ids, logits, lse=lse, dloss=dloss.contiguous(),
+                        temperature=ctx.temperature, ignore_index=ctx.ignore_index)
+        return g["dh"], g["dweight"], None, None, None, None
+
+
+def linear_distillation(h, weight, ids, logits, *, temperature: float = 1.0,
+                        ignore_index: int = -100, reduction: str = "mean"):
+    """The divergence of a student, whose logits are h weight^T, from a teacher's top
+    logits (as ``distill_fwd``), differentiable in h and weight; the teacher gets no
+    gradient.  h: bf16 [..., dim]; ids, logits: [..., top].  ``reduction``: "mean"
+    over the tokens that have entries (0 when none has), "sum", or "none" for the
+    losses, [...].  High temperatures T make gradients about T^2 times smaller; multiply by the
+    square to keep their size."""
+    if reduction not in ("mean", "sum", "none"):
+        raise ValueError(f"reduction: {reduction!r}, expected 'mean', 'sum' or 'none'")
+    for name, t in (("ids", ids), ("logits", logits)):
+        if t.shape[:-1] != h.shape[:-1]:
+            raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {(*h.shape[:-1], 'top')}")
+    if logits.requires_grad:
+        raise ValueError("logits: the teacher gets no gradient; pass logits.detach()")
+    loss = _Distillation.apply(h.reshape(-1, h.shape[-1]), weight, ids.reshape(-1, ids.shape[-1]),
+                               logits.reshape(-1, logits.shape[-1]), float(temperature),
+                               int(ignore_index))
+    if reduction == "none":
+        return loss.view(h.shape[:-1])
+    total = loss.sum()
+    if reduction == "sum":
+        return total
+    kept = ((ids != ignore_index) & (logits != -float("inf"))).any(-1).sum()
+    return total / kept.clamp(min=1)
 
 
 class _GatedRecurrence(torch.autograd.Function):

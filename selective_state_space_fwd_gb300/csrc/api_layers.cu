@@ -136,6 +136,29 @@ ssm::XentParams xent_params(const void* h, const void* weight, const int64_t* ta
   return p;
 }
 
+ssm_status check_distill(const ssm_distill_shapes* s) {
+  if (s == nullptr) return SSM_ERR_NULL;
+  const ssm_xent_shapes x = {s->tokens, s->vocab, s->dim, 0};
+  const ssm_status st = check_xent(&x);
+  if (st != SSM_OK) return st;
+  if (!known(s->teacher_dtype)) return SSM_ERR_UNSUPPORTED;
+  if (s->top < 1 || !(s->temperature > 0.f) || isinf(s->temperature) ||
+      isinf(1.f / s->temperature))
+    return SSM_ERR_SHAPE;
+  return s->top <= ssm::kDistillMaxTop ? SSM_OK : SSM_ERR_UNSUPPORTED;
+}
+
+ssm::DistillParams distill_params(const void* h, const void* weight, const int64_t* ids,
+                                  const void* logits, const ssm_distill_shapes& s,
+                                  void* workspace) {
+  ssm::DistillParams d = {};
+  d.xent = xent_params(h, weight, nullptr, {s.tokens, s.vocab, s.dim, 0}, workspace);
+  d.ids = ids; d.logits = logits; d.logits_bf16 = s.teacher_dtype == SSM_BF16;
+  d.top = static_cast<int>(s.top); d.ignore_index = s.ignore_index;
+  d.temperature = s.temperature;
+  return d;
+}
+
 }  // namespace
 
 extern "C" {
@@ -308,6 +331,55 @@ ssm_status ssm_xent_bwd(const void* h, const void* weight, const int64_t* target
   if (!(p.err = ssm::stream::error_word())) return SSM_ERR_CUDA;
   p.lse_in = lse; p.dloss = dloss; p.dh = dh; p.dweight = dweight;
   return status_of(ssm::launch_xent_bwd(p, stream));
+}
+
+size_t ssm_distill_workspace_bytes(const ssm_distill_shapes* shapes, int backward) {
+  if (check_distill(shapes) != SSM_OK) return 0;
+  return ssm::distill_workspace_bytes({shapes->tokens, shapes->vocab, shapes->dim},
+                                      static_cast<int>(shapes->top), backward != 0);
+}
+
+ssm_status ssm_distill_fwd(const void* h, const void* weight, const int64_t* ids,
+                           const void* logits, float* out_loss, float* out_lse, void* workspace,
+                           size_t workspace_bytes, const ssm_distill_shapes* shapes,
+                           ssm_dtype dtype, cudaStream_t stream) {
+  ssm_status st = check_distill(shapes);
+  if (st != SSM_OK) return st;
+  if (dtype != SSM_BF16) return SSM_ERR_UNSUPPORTED;
+  if (!h || !weight || !ids || !logits || !out_loss || !out_lse || !workspace) return SSM_ERR_NULL;
+  if (!aligned(h, 16) || !aligned(weight, 16) || !aligned(ids, 8) ||
+      !aligned(logits, elem_size(shapes->teacher_dtype)) || !aligned(out_loss, 4) ||
+      !aligned(out_lse, 4) || !aligned(workspace, 256))
+    return SSM_ERR_ALIGN;
+  if (workspace_bytes < ssm_distill_workspace_bytes(shapes, 0)) return SSM_ERR_SHAPE;
+  int dev = 0;
+  if ((st = current_device_for(stream, &dev)) != SSM_OK) return st;
+  ssm::DistillParams d = distill_params(h, weight, ids, logits, *shapes, workspace);
+  if (!(d.xent.err = ssm::stream::error_word())) return SSM_ERR_CUDA;
+  d.xent.loss = out_loss; d.xent.lse = out_lse;
+  return status_of(ssm::launch_distill_fwd(d, stream));
+}
+
+ssm_status ssm_distill_bwd(const void* h, const void* weight, const int64_t* ids,
+                           const void* logits, const float* lse, const float* dloss, void* dh,
+                           void* dweight, void* workspace, size_t workspace_bytes,
+                           const ssm_distill_shapes* shapes, ssm_dtype dtype, cudaStream_t stream) {
+  ssm_status st = check_distill(shapes);
+  if (st != SSM_OK) return st;
+  if (dtype != SSM_BF16) return SSM_ERR_UNSUPPORTED;
+  if (!h || !weight || !ids || !logits || !lse || !dloss || !dh || !dweight || !workspace)
+    return SSM_ERR_NULL;
+  if (!aligned(h, 16) || !aligned(weight, 16) || !aligned(ids, 8) ||
+      !aligned(logits, elem_size(shapes->teacher_dtype)) || !aligned(lse, 4) ||
+      !aligned(dloss, 4) || !aligned(dh, 16) || !aligned(dweight, 16) || !aligned(workspace, 256))
+    return SSM_ERR_ALIGN;
+  if (workspace_bytes < ssm_distill_workspace_bytes(shapes, 1)) return SSM_ERR_SHAPE;
+  int dev = 0;
+  if ((st = current_device_for(stream, &dev)) != SSM_OK) return st;
+  ssm::DistillParams d = distill_params(h, weight, ids, logits, *shapes, workspace);
+  if (!(d.xent.err = ssm::stream::error_word())) return SSM_ERR_CUDA;
+  d.xent.lse_in = lse; d.xent.dloss = dloss; d.xent.dh = dh; d.xent.dweight = dweight;
+  return status_of(ssm::launch_distill_bwd(d, stream));
 }
 
 ssm_status ssm_recur_fwd(const void* gate, const void* value, const float* floor,

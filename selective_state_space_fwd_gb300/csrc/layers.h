@@ -1,6 +1,7 @@
 // layers.h -- parameters and launchers of the operators around the scan: the
 // short causal convolution, the norm of the residual stream, the softmax cross
-// entropy over the vocabulary, the gated linear recurrence and the embedding lookup.
+// entropy over the vocabulary, the distillation from a teacher's top logits, the
+// gated linear recurrence and the embedding lookup.
 #pragma once
 #include <cuda_runtime.h>
 #include <stddef.h>
@@ -124,6 +125,22 @@ struct XentParams {
 size_t xent_workspace_bytes(const XentShape& s, bool backward);
 cudaError_t launch_xent_fwd(const XentParams& p, cudaStream_t s);
 cudaError_t launch_xent_bwd(const XentParams& p, cudaStream_t s);
+
+// ---- distillation from a teacher's top logits (kernel_distill.cu) ----------------
+constexpr int kDistillMaxTop = 1024;  // a token's entries are sorted in shared memory
+struct DistillParams {
+  XentParams xent;           // targets and ignore_index unused
+  const int64_t* ids;        // [tokens, top]
+  const void* logits;        // [tokens, top], fp32 or bf16
+  bool logits_bf16;
+  int top;
+  int64_t ignore_index;
+  float temperature;
+};
+
+size_t distill_workspace_bytes(const XentShape& s, int top, bool backward);
+cudaError_t launch_distill_fwd(const DistillParams& p, cudaStream_t s);
+cudaError_t launch_distill_bwd(const DistillParams& p, cudaStream_t s);
 
 // ---- gated linear recurrence (kernel_recur.cu) ----------------------------------
 constexpr int kRecurChunk = 64;  // steps between the states kept for the backward

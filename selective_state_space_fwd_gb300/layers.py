@@ -1,6 +1,6 @@
 """The operators around the scan: short causal convolution, norm of the residual
-stream, softmax cross entropy over the vocabulary, the gated linear recurrence,
-and the embedding lookup.
+stream, softmax cross entropy over the vocabulary, distillation from a teacher's top
+logits, the gated linear recurrence, and the embedding lookup.
 
 Argument marshalling only, like ``_binding``: dtypes, shapes, devices and
 strides are checked, outputs and workspaces are allocated when the caller
@@ -16,8 +16,8 @@ import functools
 
 import torch
 
-from ._binding import (ConvShapes, DType, EmbedShapes, NormShapes, RecurShapes, SsmError,
-                       XentShapes, _check, load)
+from ._binding import (ConvShapes, DistillShapes, DType, EmbedShapes, NormShapes, RecurShapes,
+                       SsmError, XentShapes, _check, load)
 
 _F32 = torch.float32
 _CODES = {_F32: int(DType.F32), torch.bfloat16: int(DType.BF16)}
@@ -48,6 +48,11 @@ def _xent_sizes(*sizes):
 
 
 @functools.lru_cache(maxsize=512)
+def _distill_sizes(*sizes):
+    return ctypes.byref(DistillShapes(*sizes))
+
+
+@functools.lru_cache(maxsize=512)
 def _recur_sizes(*sizes):
     return ctypes.byref(RecurShapes(*sizes))
 
@@ -70,6 +75,11 @@ def _norm_workspace(sizes):
 @functools.lru_cache(maxsize=512)
 def _xent_workspace(sizes, backward):
     return load().ssm_xent_workspace_bytes(sizes, backward)
+
+
+@functools.lru_cache(maxsize=512)
+def _distill_workspace(sizes, backward):
+    return load().ssm_distill_workspace_bytes(sizes, backward)
 
 
 @functools.lru_cache(maxsize=512)
@@ -397,6 +407,78 @@ def xent_bwd(h, weight, targets, *, lse, dloss, ignore_index: int = -100, worksp
     _call(lib.ssm_xent_bwd, dev, h.data_ptr(), weight.data_ptr(), targets.data_ptr(),
           lse.data_ptr(), dloss.data_ptr(), dh.data_ptr(), dweight.data_ptr(), ws.data_ptr(),
           ws.numel(), sizes, code)
+    return {"dh": dh, "dweight": dweight}
+
+
+def _distill_args(h, weight, ids, logits, temperature, ignore_index):
+    """Checked (device, dtype code, tokens, DistillShapes) of a distillation."""
+    dev = _cuda(h, "h")
+    code = _code(h.dtype)
+    if h.dim() != 2:
+        raise ValueError(f"h: shape {tuple(h.shape)}, expected [tokens, dim]")
+    if weight.dim() != 2:
+        raise ValueError(f"weight: shape {tuple(weight.shape)}, expected [vocab, dim]")
+    if ids.dim() != 2:
+        raise ValueError(f"ids: shape {tuple(ids.shape)}, expected [tokens, top]")
+    tokens, dim = h.shape
+    vocab, top = weight.shape[0], ids.shape[1]
+    _dense(h, "h", (tokens, dim), h.dtype, dev)
+    _dense(weight, "weight", (vocab, dim), h.dtype, dev)
+    _dense(ids, "ids", (tokens, top), torch.int64, dev)
+    teacher = _code(logits.dtype)
+    _dense(logits, "logits", (tokens, top), logits.dtype, dev)
+    return dev, code, tokens, _distill_sizes(tokens, vocab, dim, top, int(ignore_index),
+                                             float(temperature), teacher)
+
+
+def distill_fwd(h, weight, ids, logits, *, temperature: float = 1.0, ignore_index: int = -100,
+                workspace=None, stream=None):
+    """The divergence of a student's next-token distribution from a teacher's, of
+    which the top logits are known, without keeping the student's logits
+    h weight^T:
+
+        loss = sum_k q_k (log q_k - log p[ids_k]),
+        q = softmax(logits / temperature) over the token's entries,
+        p = softmax(h weight^T / temperature) over the vocabulary.
+
+    h: bf16 [tokens, dim]; weight: bf16 [vocab, dim], dim a multiple of 8; ids:
+    int64 [tokens, top] and logits: fp32 or bf16 [tokens, top], the teacher's
+    entries in any order, top up to 1024.  Entries of ``ignore_index``, or with a
+    logit of -infinity, take no part; an id that comes twice counts twice.  Returns
+    ``(loss, lse)``, fp32 [tokens]; lse, the log of p's denominator, is what
+    ``distill_bwd`` needs.  Tokens without entries get 0 in both and their rows of
+    h are not used; any other id outside the vocabulary gives NaN."""
+    if stream is not None:
+        return _on_stream(stream, distill_fwd, h, weight, ids, logits, temperature=temperature,
+                          ignore_index=ignore_index, workspace=workspace)
+    dev, code, tokens, sizes = _distill_args(h, weight, ids, logits, temperature, ignore_index)
+    lib = load()
+    ws = _workspace(workspace, _distill_workspace(sizes, 0), dev)
+    loss = torch.empty((tokens,), dtype=_F32, device=dev)
+    lse = torch.empty((tokens,), dtype=_F32, device=dev)
+    _call(lib.ssm_distill_fwd, dev, h.data_ptr(), weight.data_ptr(), ids.data_ptr(),
+          logits.data_ptr(), loss.data_ptr(), lse.data_ptr(), ws.data_ptr(), ws.numel(), sizes,
+          code)
+    return loss, lse
+
+
+def distill_bwd(h, weight, ids, logits, *, lse, dloss, temperature: float = 1.0,
+                ignore_index: int = -100, workspace=None, stream=None) -> dict:
+    """The gradients of sum(dloss * loss) for ``distill_fwd`` in the student: a dict
+    of dh (like h; 0 for tokens without entries) and dweight (like weight).  lse:
+    the forward's; dloss: fp32 [tokens]."""
+    if stream is not None:
+        return _on_stream(stream, distill_bwd, h, weight, ids, logits, lse=lse, dloss=dloss,
+                          temperature=temperature, ignore_index=ignore_index, workspace=workspace)
+    dev, code, tokens, sizes = _distill_args(h, weight, ids, logits, temperature, ignore_index)
+    _dense(lse, "lse", (tokens,), _F32, dev)
+    _dense(dloss, "dloss", (tokens,), _F32, dev)
+    lib = load()
+    ws = _workspace(workspace, _distill_workspace(sizes, 1), dev)
+    dh, dweight = torch.empty_like(h), torch.empty_like(weight)
+    _call(lib.ssm_distill_bwd, dev, h.data_ptr(), weight.data_ptr(), ids.data_ptr(),
+          logits.data_ptr(), lse.data_ptr(), dloss.data_ptr(), dh.data_ptr(), dweight.data_ptr(),
+          ws.data_ptr(), ws.numel(), sizes, code)
     return {"dh": dh, "dweight": dweight}
 
 
