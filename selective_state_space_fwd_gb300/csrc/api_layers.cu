@@ -398,7 +398,9 @@ ssm_status ssm_recur_fwd(const void* gate, const void* value, const float* floor
   if ((st = current_device_for(stream, &dev)) != SSM_OK) return st;
   ssm::RecurParams p = recur_params(gate, value, floor, valid_len, *shapes);
   p.state0 = state0; p.y = out_y; p.out_final = out_final; p.states = out_states;
-  return status_of(ssm::launch_recur_fwd(p, dtype == SSM_BF16, stream));
+  unsigned* err = ssm::stream::error_word();
+  if (!err) return SSM_ERR_CUDA;
+  return status_of(ssm::launch_recur_fwd(p, dtype == SSM_BF16, err, stream));
 }
 
 size_t ssm_recur_bwd_workspace_bytes(const ssm_recur_shapes* shapes) {
@@ -434,7 +436,9 @@ ssm_status ssm_recur_bwd(const void* gate, const void* value, const float* floor
   q.fwd = recur_params(gate, value, floor, valid_len, *shapes);
   q.states = states; q.dy = dy; q.dfinal = dfinal; q.dgate = dgate; q.dvalue = dvalue;
   q.dfloor = dfloor; q.dstate0 = dstate0; q.partial = static_cast<float*>(workspace);
-  return status_of(ssm::launch_recur_bwd(q, dtype == SSM_BF16, stream));
+  unsigned* err = ssm::stream::error_word();
+  if (!err) return SSM_ERR_CUDA;
+  return status_of(ssm::launch_recur_bwd(q, dtype == SSM_BF16, err, stream));
 }
 
 ssm_status ssm_recur_step(const void* gate, const void* value, const float* floor, float* state,

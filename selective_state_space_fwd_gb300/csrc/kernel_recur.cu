@@ -4,7 +4,7 @@
 //
 // Work split: a CTA owns 32 x VEC channels (128 bytes of a row) of one batch row
 // and walks its time in tiles of kTile steps.  Each of its warps folds kSteps
-// consecutive steps of the tile, lane by lane, into the stretch's map (C, e); the
+// consecutive steps of the tile, lane by lane, into the stretch's map; the
 // maps meet in shared memory, every thread composes those before its own with
 // the carried state, and the warp's outputs follow from the state that enters it.
 // The next tile's rows are loaded while a tile is folded.  With fewer CTAs than
@@ -18,7 +18,7 @@
 //   dfloor = sum l (h_{t-1} - v) sigmoid(-g).
 // What enters a tile from its past is the state that the forward kept there (one
 // per kTile steps); the states inside are formed again.  The same maps carry
-// m = a l backwards: m -> e' + m - C m, with the same C.  dfloor is summed per
+// m = a l backwards: m -> e' + P m, with the same P.  dfloor is summed per
 // thread, over the warps and, by a second kernel, over the CTAs, in a fixed order.
 #include "pdl.cuh"
 #include "recur.cuh"
@@ -29,7 +29,6 @@ namespace ssm {
 namespace {
 
 using recur::Cell;
-using recur::through;
 
 constexpr int kSms = 152;
 constexpr int kWarps = 8;
@@ -115,7 +114,7 @@ __device__ __forceinline__ void share(float (*slots)[32][N], const Place<N / 2>&
 template <typename T, int VEC>
 __global__ void __launch_bounds__(kThreads, 2) recur_fwd_kernel(const RecurParams p, uint32_t size) {
   using Word = typename Cell<T, VEC>::Word;
-  constexpr int N = 2 * VEC;  // floats of a map: (C, e) per channel
+  constexpr int N = 2 * VEC;  // floats of a map: (P, e) per channel
   __shared__ __align__(16) float maps[2][kWarps][32][N];
   __shared__ __align__(16) float tiles_s[2][kMaxCluster][32][N];
   const Place<VEC> at(p.dim, size);
@@ -141,25 +140,25 @@ __global__ void __launch_bounds__(kThreads, 2) recur_fwd_kernel(const RecurParam
   load_rows<T, VEC>(vw, value, p.value_step, t0, len, at.on);
   if (size > 1) pair::cluster_sync();  // all of the cluster has started
   for (int64_t i = 0; i < rounds; ++i, t0 += static_cast<int64_t>(size) * kTile) {
-    // the outputs from a state of 0, and C up to each step
-    float h[kSteps][VEC], c[kSteps][VEC];
-    float hl[VEC], cl[VEC];
+    float b[kSteps][VEC], u[kSteps][VEC];
+    float hl[VEC], pl[VEC];
 #pragma unroll
-    for (int v = 0; v < VEC; ++v) hl[v] = cl[v] = 0.f;
+    for (int v = 0; v < VEC; ++v) {
+      hl[v] = 0.f;
+      pl[v] = 1.f;
+    }
     const int64_t left = len - t0;
 #pragma unroll
     for (int s = 0; s < kSteps; ++s) {
-      float g[VEC], u[VEC];
+      float g[VEC];
       Cell<T, VEC>::get(gw[s], g);
-      Cell<T, VEC>::get(vw[s], u);
+      Cell<T, VEC>::get(vw[s], u[s]);
 #pragma unroll
       for (int v = 0; v < VEC; ++v) {
-        float b = keep[v] * recur::opening(g[v]);
-        b = s < left ? b : 0.f;
-        hl[v] = fmaf(b, u[v] - hl[v], hl[v]);
-        cl[v] = fmaf(b, 1.f - cl[v], cl[v]);
-        h[s][v] = hl[v];
-        c[s][v] = cl[v];
+        const float o = keep[v] * recur::opening(g[v]);
+        b[s][v] = s < left ? o : 0.f;
+        hl[v] = fmaf(b[s][v], u[s][v] - hl[v], hl[v]);
+        pl[v] = fmaf(-b[s][v], pl[v], pl[v]);
       }
     }
     const int64_t next = t0 + static_cast<int64_t>(size) * kTile;
@@ -168,7 +167,7 @@ __global__ void __launch_bounds__(kThreads, 2) recur_fwd_kernel(const RecurParam
     const int k = i & 1;
 #pragma unroll
     for (int v = 0; v < VEC; ++v) {
-      maps[k][at.warp][at.lane][2 * v] = cl[v];
+      maps[k][at.warp][at.lane][2 * v] = pl[v];
       maps[k][at.warp][at.lane][2 * v + 1] = hl[v];
     }
     __syncthreads();
@@ -176,15 +175,15 @@ __global__ void __launch_bounds__(kThreads, 2) recur_fwd_kernel(const RecurParam
     if (size > 1) {
       float all[N];
 #pragma unroll
-      for (int v = 0; v < N; ++v) all[v] = 0.f;
+      for (int v = 0; v < N; ++v) all[v] = v & 1 ? 0.f : 1.f;
       if (at.warp == 0) {
 #pragma unroll
         for (int w = 0; w < kWarps; ++w)
 #pragma unroll
           for (int v = 0; v < VEC; ++v) {
-            const float cw = maps[k][w][at.lane][2 * v], ew = maps[k][w][at.lane][2 * v + 1];
-            all[2 * v + 1] = through(all[2 * v + 1], cw, ew);
-            all[2 * v] = fmaf(cw, 1.f - all[2 * v], all[2 * v]);
+            const float pw = maps[k][w][at.lane][2 * v];
+            all[2 * v] *= pw;
+            all[2 * v + 1] = fmaf(pw, all[2 * v + 1], maps[k][w][at.lane][2 * v + 1]);
           }
       }
       share<N>(tiles_s[k], at, all);
@@ -192,7 +191,7 @@ __global__ void __launch_bounds__(kThreads, 2) recur_fwd_kernel(const RecurParam
 #pragma unroll
         for (int v = 0; v < VEC; ++v) {
           if (r == at.rank) xt[v] = x[v];
-          x[v] = through(x[v], tiles_s[k][r][at.lane][2 * v], tiles_s[k][r][at.lane][2 * v + 1]);
+          x[v] = fmaf(tiles_s[k][r][at.lane][2 * v], x[v], tiles_s[k][r][at.lane][2 * v + 1]);
         }
     } else {
 #pragma unroll
@@ -206,7 +205,7 @@ __global__ void __launch_bounds__(kThreads, 2) recur_fwd_kernel(const RecurParam
 #pragma unroll
       for (int v = 0; v < VEC; ++v) {
         if (w == at.warp) in[v] = out[v];
-        out[v] = through(out[v], maps[k][w][at.lane][2 * v], maps[k][w][at.lane][2 * v + 1]);
+        out[v] = fmaf(maps[k][w][at.lane][2 * v], out[v], maps[k][w][at.lane][2 * v + 1]);
       }
     if (size == 1) {
 #pragma unroll
@@ -222,8 +221,8 @@ __global__ void __launch_bounds__(kThreads, 2) recur_fwd_kernel(const RecurParam
       float f[VEC];
 #pragma unroll
       for (int v = 0; v < VEC; ++v) {
-        f[v] = through(in[v], c[s][v], h[s][v]);
-        f[v] = s < left ? f[v] : 0.f;
+        in[v] = fmaf(b[s][v], u[s][v] - in[v], in[v]);
+        f[v] = s < left ? in[v] : 0.f;
       }
       yw[s] = Cell<T, VEC>::put(f);
     }
@@ -253,9 +252,9 @@ __global__ void __launch_bounds__(kThreads, 2)
   using Word = typename Cell<T, VEC>::Word;
   constexpr int N = 2 * VEC;
   const RecurParams& p = q.fwd;
-  __shared__ __align__(16) float past[2][kWarps][32][N];         // (C, e) of the states
+  __shared__ __align__(16) float past[2][kWarps][32][N];         // (P, e) of the states
   __shared__ __align__(16) float coming[2][kWarps][32][VEC];     // e' of m
-  __shared__ __align__(16) float tiles_s[2][kMaxCluster][32][N];  // (C, e') of the tiles
+  __shared__ __align__(16) float tiles_s[2][kMaxCluster][32][N];  // (P, e') of the tiles
   const Place<VEC> at(p.dim, size);
   const int64_t len = recur::valid_of(p.valid_len, at.b, p.seqlen);
   const int64_t tiles = (p.seqlen + kTile - 1) / kTile, live = (len + kTile - 1) / kTile;
@@ -291,9 +290,12 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
     for (int v = 0; v < VEC; ++v) h[v] = tile < 0 ? 0.f : __ldg(states + tile * p.dim + v);
     float open[kSteps][VEC], hold[kSteps][VEC], u[kSteps][VEC], l[kSteps][VEC];
-    float cl[VEC], hl[VEC], ml[VEC];
+    float pl[VEC], hl[VEC], ml[VEC];
 #pragma unroll
-    for (int v = 0; v < VEC; ++v) cl[v] = hl[v] = ml[v] = 0.f;
+    for (int v = 0; v < VEC; ++v) {
+      hl[v] = ml[v] = 0.f;
+      pl[v] = 1.f;
+    }
 #pragma unroll
     for (int s = 0; s < kSteps; ++s) {
       float g[VEC];
@@ -306,7 +308,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         open[s][v] = s < left ? o : 0.f;
         const float b = keep[v] * open[s][v];
         hl[v] = fmaf(b, u[s][v] - hl[v], hl[v]);
-        cl[v] = fmaf(b, 1.f - cl[v], cl[v]);
+        pl[v] = fmaf(-b, pl[v], pl[v]);
       }
     }
 #pragma unroll
@@ -319,7 +321,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int k = i & 1;
 #pragma unroll
     for (int v = 0; v < VEC; ++v) {
-      past[k][at.warp][at.lane][2 * v] = cl[v];
+      past[k][at.warp][at.lane][2 * v] = pl[v];
       past[k][at.warp][at.lane][2 * v + 1] = hl[v];
       coming[k][at.warp][at.lane][v] = ml[v];
     }
@@ -328,15 +330,15 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (size > 1) {
       float all[N];
 #pragma unroll
-      for (int v = 0; v < N; ++v) all[v] = 0.f;
+      for (int v = 0; v < N; ++v) all[v] = v & 1 ? 0.f : 1.f;
       if (at.warp == 0) {
 #pragma unroll
         for (int w = kWarps - 1; w >= 0; --w)
 #pragma unroll
           for (int v = 0; v < VEC; ++v) {
-            const float cw = past[k][w][at.lane][2 * v];
-            all[2 * v + 1] = through(all[2 * v + 1], cw, coming[k][w][at.lane][v]);
-            all[2 * v] = fmaf(cw, 1.f - all[2 * v], all[2 * v]);
+            const float pw = past[k][w][at.lane][2 * v];
+            all[2 * v] *= pw;
+            all[2 * v + 1] = fmaf(pw, all[2 * v + 1], coming[k][w][at.lane][v]);
           }
       }
       share<N>(tiles_s[k], at, all);
@@ -344,7 +346,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
         for (int v = 0; v < VEC; ++v) {
           if (r == at.rank) mt[v] = m[v];
-          m[v] = through(m[v], tiles_s[k][r][at.lane][2 * v], tiles_s[k][r][at.lane][2 * v + 1]);
+          m[v] = fmaf(tiles_s[k][r][at.lane][2 * v], m[v], tiles_s[k][r][at.lane][2 * v + 1]);
         }
     } else {
 #pragma unroll
@@ -356,13 +358,13 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
       for (int v = 0; v < VEC; ++v)
         if (w < at.warp)
-          h[v] = through(h[v], past[k][w][at.lane][2 * v], past[k][w][at.lane][2 * v + 1]);
+          h[v] = fmaf(past[k][w][at.lane][2 * v], h[v], past[k][w][at.lane][2 * v + 1]);
 #pragma unroll
     for (int w = kWarps - 1; w >= 0; --w)
 #pragma unroll
       for (int v = 0; v < VEC; ++v) {
         if (w == at.warp) mi[v] = mt[v];
-        mt[v] = through(mt[v], past[k][w][at.lane][2 * v], coming[k][w][at.lane][v]);
+        mt[v] = fmaf(past[k][w][at.lane][2 * v], mt[v], coming[k][w][at.lane][v]);
       }
     if (size == 1) {
 #pragma unroll
@@ -517,7 +519,8 @@ static int recur_cluster(int64_t batch, int64_t seqlen, int64_t units) {
 
 int64_t recur_bwd_partials(int64_t batch, int64_t seqlen) { return batch * kMaxCluster; }
 
-cudaError_t launch_recur_fwd(const RecurParams& p, bool bf16, cudaStream_t s) {
+cudaError_t launch_recur_fwd(const RecurParams& p, bool bf16, unsigned* err, cudaStream_t s) {
+  if (recur_tma_ok(p, bf16)) return launch_recur_fwd_tma(p, bf16, err, s);
   const bool two = bf16 && pairs(p);
   const int64_t lanes = two ? 64 : 32;
   const int64_t units = p.batch * ((p.dim + lanes - 1) / lanes);
@@ -527,16 +530,18 @@ cudaError_t launch_recur_fwd(const RecurParams& p, bool bf16, cudaStream_t s) {
              : launch_cluster(recur_fwd_kernel<__nv_bfloat16, 1>, units, r, s, p, r);
 }
 
-cudaError_t launch_recur_bwd(const RecurBwdParams& q, bool bf16, cudaStream_t s) {
-  RecurParams p = q.fwd;
+cudaError_t launch_recur_bwd(const RecurBwdParams& q, bool bf16, unsigned* err, cudaStream_t s) {
+  const RecurParams& p = q.fwd;
   const bool two = bf16 && pairs(p) &&
                    (reinterpret_cast<uintptr_t>(q.dy) | reinterpret_cast<uintptr_t>(q.dgate) |
                     reinterpret_cast<uintptr_t>(q.dvalue)) % 4 == 0;
   const int64_t lanes = two ? 64 : 32;
   const int64_t units = p.batch * ((p.dim + lanes - 1) / lanes);
-  const int r = recur_cluster(p.batch, p.seqlen, units);
+  int r = recur_cluster(p.batch, p.seqlen, units);
   cudaError_t e;
-  if (!bf16)
+  if (recur_bwd_tma_ok(q, bf16))
+    e = launch_recur_bwd_tma(q, bf16, err, &r, s);
+  else if (!bf16)
     e = launch_cluster(recur_bwd_kernel<float, 1>, units, r, s, q, r);
   else
     e = two ? launch_cluster(recur_bwd_kernel<__nv_bfloat16, 2>, units, r, s, q, r)

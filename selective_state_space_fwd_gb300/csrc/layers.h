@@ -14,6 +14,7 @@ namespace ssm {
 // (SSD form) and 8 (STREAM-TM).
 constexpr unsigned kErrConvWait = 16u;
 constexpr unsigned kErrXentWait = 32u;
+constexpr unsigned kErrRecurWait = 64u;
 
 // ---- short causal convolution (kernel_conv.cu) ------------------------------
 struct ConvParams {
@@ -171,8 +172,16 @@ struct RecurBwdParams {
 };
 
 int64_t recur_bwd_partials(int64_t batch, int64_t seqlen);
-cudaError_t launch_recur_fwd(const RecurParams& p, bool bf16, cudaStream_t s);
-cudaError_t launch_recur_bwd(const RecurBwdParams& p, bool bf16, cudaStream_t s);
+// `err`: the sticky error word of the bounded waits.
+cudaError_t launch_recur_fwd(const RecurParams& p, bool bf16, unsigned* err, cudaStream_t s);
+cudaError_t launch_recur_bwd(const RecurBwdParams& p, bool bf16, unsigned* err, cudaStream_t s);
+// The forms whose rows are staged by TMA (kernel_recur_tma.cu), and whether a
+// call's tensors allow it.
+bool recur_tma_ok(const RecurParams& p, bool bf16);
+bool recur_bwd_tma_ok(const RecurBwdParams& p, bool bf16);
+cudaError_t launch_recur_fwd_tma(const RecurParams& p, bool bf16, unsigned* err, cudaStream_t s);
+cudaError_t launch_recur_bwd_tma(const RecurBwdParams& p, bool bf16, unsigned* err, int* parts,
+                                 cudaStream_t s);
 cudaError_t launch_recur_step(const RecurParams& p, bool bf16, cudaStream_t s);
 
 // ---- embedding lookup (kernel_embed.cu) --------------------------------------------

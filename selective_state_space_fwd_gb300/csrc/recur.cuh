@@ -2,11 +2,11 @@
 //
 // Per channel, with the gate g and the value v of a step,
 //   b = (1 - floor) sigmoid(-g),   a = 1 - b,   h <- a h + b v = h + b (v - h).
-// A stretch of steps maps the state that enters it to the one that leaves:
-//   h -> h + (e - C h),   C = 1 - prod a,   e the state it leaves from h = 0.
-// C, not the product, is what is kept: where a channel remembers for thousands of
-// steps every b is far below 1, and a rounded a, or a product of them, would lose
-// most of b's digits, in the same direction at every step.
+// A stretch of steps maps the state that enters it to the one that leaves,
+//   h -> P h + e,   P = prod a,   e the state it leaves from h = 0.
+// P is formed as P <- P - b P, not from a rounded a, and the state as h + b (v - h):
+// each rounds once per step, at the size of what it is, so that neither small b
+// (long memories) nor b near 1 (a reset) costs digits.
 #pragma once
 #include "common.cuh"
 #include "layers.h"
@@ -51,21 +51,35 @@ __device__ __forceinline__ float rcp(float x) {
 }
 // sigmoid(-g): 0 for a gate of +infinity, 1 for -infinity, NaN for NaN.
 __device__ __forceinline__ float opening(float g) { return rcp(1.f + ex2(g * kLog2e)); }
-// The same, and hold = sigmoid(g), both with full relative precision: where e^g
-// has left fp32's range (its product with 0 would be NaN) it is 1.
+// e^g where it still has a reciprocal (its product with a reciprocal of 0 would be
+// NaN at infinity); NaN is left to the reciprocal.
+__device__ __forceinline__ float within(float e) { return fminf(e, 8.5e37f); }
+// The same, and hold = sigmoid(g), both with full relative precision.
 __device__ __forceinline__ float opening(float g, float& hold) {
   const float e = ex2(g * kLog2e), r = rcp(1.f + e);
-  hold = e > 1e30f ? 1.f : e * r;
+  hold = within(e) * r;
   return r;
 }
-
-// The state that leaves a stretch (c, e) which x enters.
-__device__ __forceinline__ float through(float x, float c, float e) { return e + fmaf(-c, x, x); }
 
 __device__ __forceinline__ int64_t valid_of(const int32_t* valid_len, int64_t b, int64_t seqlen) {
   if (!valid_len) return seqlen;
   const int64_t v = valid_len[b];
   return v < 0 ? 0 : v > seqlen ? seqlen : v;
+}
+
+// Rows of a batch with valid lengths go to the CTAs longest first (CTAs start in
+// index order, so that the short ones fill the end): the row of rank r among up to
+// 32, a lane per row, ties by index.  All lanes of the warp call it.
+__device__ __forceinline__ int64_t by_length(const int32_t* valid_len, int64_t batch,
+                                             int64_t seqlen, int64_t r) {
+  const int lane = threadIdx.x & 31, n = static_cast<int>(batch);
+  const int64_t len = lane < n ? valid_of(valid_len, lane, seqlen) : -1;
+  int rank = 0;
+  for (int j = 0; j < n; ++j) {
+    const int64_t other = __shfl_sync(0xffffffffu, len, j);
+    rank += other > len || (other == len && j < lane);
+  }
+  return __ffs(__ballot_sync(0xffffffffu, lane < n && rank == r)) - 1;
 }
 
 }  // namespace recur

@@ -274,10 +274,12 @@ def test_layouts(name, B, L, D, batch, step, which, dtype):
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_tensors_off_a_boundary(dtype):
-    """Tensors that start one element into a buffer."""
+    """Tensors that start one element into a buffer: another kernel takes them, which
+    splits time otherwise, so that its results are the definition's within the same
+    bounds, not the same bits."""
     B, L, D = 2, 90, 64
     t = make(dtype, B, L, D, carry=True, seed=6)
-    want = run(t)
+    want = reference(t)
 
     def shifted(v):
         buf = torch.empty(v.numel() + 1, dtype=v.dtype, device="cuda")
@@ -285,10 +287,11 @@ def test_tensors_off_a_boundary(dtype):
 
     out = shifted(torch.zeros_like(t["gate"]))
     y, _, states = S.recur_fwd(shifted(t["gate"]), shifted(t["value"]), state0=shifted(t["state0"]), out=out, want_states=True)
-    assert y is out and torch.equal(y, want["y"]) and torch.equal(states, want["states"])
+    assert y is out
+    assert_close(y, want, "y")
     g = S.recur_bwd(t["gate"], t["value"], states=shifted(states), dy=shifted(t["dy"]), dfinal=t["dfinal"], want_dstate0=True)
     for k in ("dgate", "dvalue", "dstate0"):
-        assert torch.equal(g[k], want[k]), k
+        assert_close(g[k], want, k)
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
