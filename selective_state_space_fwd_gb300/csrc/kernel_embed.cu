@@ -4,11 +4,9 @@
 // The lookup is a copy of rows, bound by HBM.
 //
 // The gradient adds the rows of equal tokens in the order of the tokens, without
-// atomics, so that equal inputs give equal bits.  Three launches:
+// atomics, so that equal inputs give equal bits:
 // 1. The tokens are sorted by id, stably (least significant digits first, kDigits
-//    values at a time), by one cluster of kSortCtas CTAs whose counts meet in
-//    shared memory; the other clusters of the same launch fill dW with zeros, which
-//    takes longer wherever dW is more than a few MB.
+//    values at a time), by one CTA or one cluster whose counts meet in shared memory.
 // 2. The sorted tokens are cut into windows.  A warp takes a window for a slab of
 //    columns, adds the rows of each run of equal ids in fp32 and writes the runs
 //    that lie in the window.  A run that another window shares leaves a partial
@@ -19,6 +17,7 @@
 #include <cuda_bf16.h>
 
 #include "common.cuh"
+#include "f32x2.cuh"
 #include "layers.h"
 #include "pdl.cuh"
 #include "umma_pair.cuh"
@@ -65,22 +64,19 @@ __global__ void __launch_bounds__(kLookThreads) embed_fwd_kernel(const EmbedPara
 }
 
 // ---- sorting the tokens, and zeros ------------------------------------------------
-constexpr int kSortCtas = 8;
+constexpr int kSortCtas = 16;                          // at most
 constexpr int kSortThreads = 1024, kSortWarps = kSortThreads / 32;
 constexpr int kDigitBits = 9, kDigits = 1 << kDigitBits;
 constexpr int kRounds = 8;                             // keys per thread and tile
 constexpr int kSortTile = kSortThreads * kRounds;
-constexpr uint32_t kSortSmem = (kSortWarps + 2) * kDigits * 4;
+static_assert(kSortTile <= 65536, "places within a tile are kept in 16 bits");
 
 struct SortArgs {
   const int64_t* ids;
   int64_t tokens, vocab, ignore;
   uint2 *even, *odd;     // (id, token): what even and odd passes write
-  int passes, bits;    // digits and their width
-  uint4* zeros;        // the part of dW that is filled in 16-byte stores
-  int64_t nzeros;
-  char* edge[2];       // what lies before and after it
-  int nedge[2];
+  int passes, bits;      // digits and their width
+  uint32_t ctas;         // of the cluster
 };
 
 __device__ __forceinline__ uint32_t read_remote(uint32_t addr, uint32_t rank) {
@@ -122,20 +118,26 @@ struct Keys {
   __device__ __forceinline__ uint32_t peers(int r, uint32_t digit) const {
     return __match_any_sync(0xffffffffu, is(r) ? digit : kDigits);
   }
-  // Ranks the keys; whist[warp] is left with the number of each digit.
-  __device__ __forceinline__ void rank(uint32_t (*whist)[kDigits], int shift, uint32_t mask) {
+  // Ranks the keys; counts[warp] is left with the number of each digit.
+  __device__ __forceinline__ void rank(uint16_t (*counts)[kDigits], int shift, uint32_t mask) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    for (int i = threadIdx.x; i < kSortWarps * kDigits; i += kSortThreads) whist[0][i] = 0;
-    __syncthreads();
+    uint4* clear = reinterpret_cast<uint4*>(counts[warp]);
+#pragma unroll
+    for (int i = 0; i < kDigits / 8; i += 32) clear[i + lane] = make_uint4(0, 0, 0, 0);
+    __syncwarp();
+    uint32_t same[kRounds];  // first, so that the rounds' searches overlap
+#pragma unroll
+    for (int r = 0; r < kRounds; ++r)
+      same[r] = r < rounds ? peers(r, (key[r].x >> shift) & mask) : 0;
 #pragma unroll
     for (int r = 0; r < kRounds; ++r) {
       place[r] = 0;
       if (r < rounds) {
-        const uint32_t digit = (key[r].x >> shift) & mask, same = peers(r, digit);
-        const uint32_t before = __popc(same & ((1u << lane) - 1)), seen = whist[warp][digit];
+        const uint32_t digit = (key[r].x >> shift) & mask;
+        const uint32_t before = __popc(same[r] & ((1u << lane) - 1)), seen = counts[warp][digit];
         place[r] = seen + before;
         __syncwarp();
-        if (is(r) && before == 0) whist[warp][digit] = seen + __popc(same);
+        if (is(r) && before == 0) counts[warp][digit] = static_cast<uint16_t>(seen + __popc(same[r]));
         __syncwarp();
       }
     }
@@ -143,26 +145,13 @@ struct Keys {
   }
 };
 
-__global__ void __cluster_dims__(kSortCtas, 1, 1) __launch_bounds__(kSortThreads, 1)
-    embed_sort_kernel(const SortArgs p) {
+__global__ void __launch_bounds__(kSortThreads, 1) embed_sort_kernel(const SortArgs p) {
+  __shared__ __align__(16) uint16_t counts[kSortWarps][kDigits];
+  __shared__ uint32_t hist[kDigits], base[kDigits], sums[kSortWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   release_next();
-  if (blockIdx.x >= kSortCtas) {
-    const int64_t first = static_cast<int64_t>(blockIdx.x - kSortCtas) * kSortThreads + tid;
-    const int64_t step = static_cast<int64_t>(gridDim.x - kSortCtas) * kSortThreads;
-#pragma unroll 4
-    for (int64_t i = first; i < p.nzeros; i += step) p.zeros[i] = make_uint4(0, 0, 0, 0);
-    if (first < p.nedge[0]) p.edge[0][first] = 0;
-    if (first < p.nedge[1]) p.edge[1][first] = 0;
-    return;
-  }
-  extern __shared__ __align__(16) uint32_t sort_mem[];
-  uint32_t(*whist)[kDigits] = reinterpret_cast<uint32_t(*)[kDigits]>(sort_mem);
-  uint32_t* hist = sort_mem + kSortWarps * kDigits;
-  uint32_t* base = hist + kDigits;
-  __shared__ uint32_t sums[kSortWarps];
   const uint32_t rank = pair::cluster_rank();
-  const int64_t per = (p.tokens + 32 * kSortCtas - 1) / (32 * kSortCtas) * 32;
+  const int64_t per = (p.tokens + 32 * p.ctas - 1) / (32 * p.ctas) * 32;
   const int64_t k0 = rank * per < p.tokens ? rank * per : p.tokens;
   const int64_t k1 = k0 + per < p.tokens ? k0 + per : p.tokens;
   const bool one = k1 - k0 <= kSortTile;  // the keys stay in registers between count and move
@@ -173,18 +162,22 @@ __global__ void __cluster_dims__(kSortCtas, 1, 1) __launch_bounds__(kSortThreads
     uint2* to = pass & 1 ? p.odd : p.even;
     const int shift = pass * p.bits;
     const uint32_t mask = (1u << p.bits) - 1;
-    if (tid < kDigits) hist[tid] = 0;
-    __syncthreads();
     if (one) {
       if (pass > 0) k.load(p, pass, k0, k1);
-      k.rank(whist, shift, mask);
+      k.rank(counts, shift, mask);
       if (tid < kDigits) {
         uint32_t n = 0;
-#pragma unroll 8
-        for (int w = 0; w < kSortWarps; ++w) n += whist[w][tid];
+#pragma unroll
+        for (int w = 0; w < kSortWarps; ++w) {
+          const uint32_t c = counts[w][tid];
+          counts[w][tid] = static_cast<uint16_t>(n);  // those of the warps before
+          n += c;
+        }
         hist[tid] = n;
       }
     } else {
+      if (tid < kDigits) hist[tid] = 0;
+      __syncthreads();
       for (int64_t t0 = k0; t0 < k1; t0 += kSortTile) {
         k.load(p, pass, t0, k1);
 #pragma unroll
@@ -202,7 +195,7 @@ __global__ void __cluster_dims__(kSortCtas, 1, 1) __launch_bounds__(kSortThreads
       const uint32_t at = umma::smem_u32(hist + tid);
 #pragma unroll
       for (uint32_t q = 0; q < kSortCtas; ++q) {
-        const uint32_t n = read_remote(at, q);
+        const uint32_t n = q < p.ctas ? read_remote(at, q) : 0;
         total += n;
         below += q < rank ? n : 0;
       }
@@ -220,26 +213,31 @@ __global__ void __cluster_dims__(kSortCtas, 1, 1) __launch_bounds__(kSortThreads
       for (int w = 0; w < warp; ++w) start += sums[w];
       base[tid] = start;
     }
+    __syncthreads();
     for (int64_t t0 = k0; t0 < k1; t0 += kSortTile) {
+      uint32_t n = 0;
       if (!one) {
         k.load(p, pass, t0, k1);
-        k.rank(whist, shift, mask);
-      }
-      if (tid < kDigits) {
-        uint32_t at = base[tid];
-#pragma unroll 8
-        for (int w = 0; w < kSortWarps; ++w) {
-          const uint32_t n = whist[w][tid];
-          whist[w][tid] = at;
-          at += n;
-        }
-        base[tid] = at;
-      }
-      __syncthreads();
+        k.rank(counts, shift, mask);
+        if (tid < kDigits) {
 #pragma unroll
-      for (int r = 0; r < kRounds; ++r)
-        if (k.is(r)) to[whist[warp][(k.key[r].x >> shift) & mask] + k.place[r]] = k.key[r];
+          for (int w = 0; w < kSortWarps; ++w) {
+            const uint32_t c = counts[w][tid];
+            counts[w][tid] = static_cast<uint16_t>(n);
+            n += c;
+          }
+        }
+        __syncthreads();
+      }
+#pragma unroll
+      for (int r = 0; r < kRounds; ++r) {
+        if (!k.is(r)) continue;
+        const uint32_t digit = (k.key[r].x >> shift) & mask;
+        to[base[digit] + counts[warp][digit] + k.place[r]] = k.key[r];
+      }
       __syncthreads();
+      if (!one && tid < kDigits) base[tid] += n;
+      if (!one) __syncthreads();
     }
     pair::cluster_sync();
   }
@@ -253,11 +251,14 @@ struct SumArgs {
   const void* dy;
   void* dweight;
   float* part;          // [windows][2][dim]: head, tail
-  int64_t tokens, vocab, dim, windows;
-  int window;           // tokens per window
+  int64_t tokens, vocab, dim;
+  int64_t windows;      // of the CTAs
+  int window;           // tokens per warp
   int slabs;
   float scale;
-  bool add;
+  const int64_t* ids;   // for the rows that no token names
+  int64_t ignore;
+  int fills;            // CTAs that fill those with zeros
 };
 
 // A lane's columns of a slab: G groups of VEC, a warp's width apart.
@@ -266,19 +267,85 @@ template <int VEC> struct Slab {
   static constexpr int kWidth = 32 * VEC * kGroups;
 };
 
+// The first place from `i` on, below n, whose bit is `set`; n if there is none.
+__device__ __forceinline__ int next_bit(const uint32_t* bits, int i, int n, bool set) {
+  while (i < n) {
+    const uint32_t w = (set ? bits[i / 32] : ~bits[i / 32]) >> (i % 32);
+    if (w) {
+      i += __ffs(w) - 1;
+      break;
+    }
+    i = (i / 32 + 1) * 32;
+  }
+  return i < n ? i : n;
+}
+
+// Zeros over the rows of dW that no token names, kFillRows at a time: those that one
+// does are marked first, from all of the ids.  None of this needs the sort.
+constexpr int kFillRows = 16384;
+template <typename W>
+__device__ __forceinline__ void fill_rows(const SumArgs& p, uint32_t (&named)[kFillRows / 32]) {
+  const int64_t v0 = p.vocab * blockIdx.x / p.fills, v1 = p.vocab * (blockIdx.x + 1) / p.fills;
+  constexpr int kPer = 16 / sizeof(W);
+  for (int64_t r0 = v0; r0 < v1; r0 += kFillRows) {
+    const int n = v1 - r0 < kFillRows ? static_cast<int>(v1 - r0) : kFillRows;
+    for (int i = threadIdx.x; i < (n + 31) / 32; i += kSumThreads) named[i] = 0;
+    __syncthreads();
+#pragma unroll 8
+    for (int64_t t = threadIdx.x; t < p.tokens; t += kSumThreads) {
+      const int64_t id = __ldg(p.ids + t);
+      const int64_t r = id - r0;
+      if (r >= 0 && r < n && id != p.ignore) atomicOr(named + r / 32, 1u << (r % 32));
+    }
+    __syncthreads();
+    // stretches of rows without a mark
+    for (int a = 0, end; (a = next_bit(named, a, n, false)) < n; a = end) {
+      end = next_bit(named, a, n, true);
+      W* begin = static_cast<W*>(p.dweight) + (r0 + a) * p.dim;
+      const int64_t size = (end - a) * p.dim;
+      // from a boundary of 128 bytes on: stores across it leave parts of sectors
+      int64_t head = (128 - reinterpret_cast<uintptr_t>(begin) % 128) % 128 / sizeof(W);
+      head = head < size ? head : size;
+      const int64_t body = (size - head) / kPer, tail = head + body * kPer;
+      uint4* q = reinterpret_cast<uint4*>(begin + head);
+#pragma unroll 8
+      for (int64_t i = threadIdx.x; i < body; i += kSumThreads) q[i] = make_uint4(0, 0, 0, 0);
+      if (threadIdx.x < head) begin[threadIdx.x] = W(0.f);
+      if (tail + threadIdx.x < size) begin[tail + threadIdx.x] = W(0.f);
+    }
+    __syncthreads();
+  }
+}
+
+// A lane's columns of dW's row as it is, for `add`.
 template <typename W, int VEC, int G>
+__device__ __forceinline__ void there(const SumArgs& p, int64_t id, int64_t c0, Raw<W, VEC> (&r)[G]) {
+  const W* row = static_cast<const W*>(p.dweight) + id * p.dim;
+#pragma unroll
+  for (int g = 0; g < G; ++g) {
+    const int64_t c = c0 + g * 32 * VEC;
+    if (c < p.dim) r[g] = raw_load_rw<W, VEC>(row + c);
+    else raw_zero(r[g]);
+  }
+}
+
+template <typename W, int VEC, int G, bool ADD>
 __device__ __forceinline__ void write_row(const SumArgs& p, int64_t id, int64_t c0,
-                                          const float (&acc)[G][VEC]) {
+                                          const float (&acc)[G][VEC], const Raw<W, VEC> (&old)[G]) {
   W* row = static_cast<W*>(p.dweight) + id * p.dim;
 #pragma unroll
   for (int g = 0; g < G; ++g) {
     const int64_t c = c0 + g * 32 * VEC;
     if (c >= p.dim) continue;
-    float f[VEC];
-    if (p.add) widen<VEC>(raw_load_rw<W, VEC>(row + c), f);
+    float f[VEC], by[VEC];
 #pragma unroll
-    for (int v = 0; v < VEC; ++v)
-      f[v] = p.add ? fmaf(acc[g][v], p.scale, f[v]) : acc[g][v] * p.scale;
+    for (int v = 0; v < VEC; ++v) by[v] = p.scale;
+    if (ADD) {
+      widen<VEC>(old[g], f);
+      vfma<VEC>(f, acc[g], by, f);
+    } else {
+      vmul<VEC>(f, acc[g], by);
+    }
     store_f<W, VEC>(row + c, f);
   }
 }
@@ -293,17 +360,33 @@ __device__ __forceinline__ void write_part(const SumArgs& p, int64_t slot, int64
   }
 }
 
-template <typename W, typename O, int VEC>
+// A CTA's warps take consecutive windows of one slab.  What a run leaves in a warp, its
+// head where it began in an earlier window and its tail where it goes on, meets in
+// shared memory; only what leaves the CTA's windows is joined by the next kernel.
+constexpr int kSumWarps = kSumThreads / 32;
+template <typename W, typename O, int VEC, bool ADD>
 __global__ void __launch_bounds__(kSumThreads) embed_sum_kernel(const SumArgs p) {
   constexpr int G = Slab<VEC>::kGroups;
   constexpr int kAhead = 8;
-  const int lane = threadIdx.x & 31;
-  wait_previous();
+  constexpr int kParts = 2 * kSumWarps * 32 * G * VEC;
+  __shared__ __align__(16) union {
+    float part[kSumWarps][2][G * VEC][32];
+    uint32_t named[kFillRows / 32];
+  } sm;
+  static_assert(sizeof(float) * kParts == sizeof(sm.part), "one float per lane and column");
+  __shared__ uint32_t tail_id[kSumWarps];
+  __shared__ unsigned char has_tail[kSumWarps], whole[kSumWarps];
   release_next();
-  const int64_t u = static_cast<int64_t>(blockIdx.x) * (kSumThreads / 32) + (threadIdx.x >> 5);
-  const int64_t w = u / p.slabs;
-  if (w >= p.windows) return;
-  const int64_t c0 = (u - w * p.slabs) * Slab<VEC>::kWidth + lane * VEC;
+  if (!ADD && static_cast<int>(blockIdx.x) < p.fills) {
+    fill_rows<W>(p, sm.named);
+    wait_previous();
+    return;
+  }
+  wait_previous();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t unit = static_cast<int64_t>(blockIdx.x) - (ADD ? 0 : p.fills);
+  const int64_t set = unit / p.slabs, w = set * kSumWarps + warp;
+  const int64_t c0 = (unit - set * p.slabs) * Slab<VEC>::kWidth + lane * VEC;
   const int64_t i0 = w * p.window;
   const int64_t i1 = i0 + p.window < p.tokens ? i0 + p.window : p.tokens;
   const O* dy = static_cast<const O*>(p.dy);
@@ -312,7 +395,15 @@ __global__ void __launch_bounds__(kSumThreads) embed_sum_kernel(const SumArgs p)
   for (int g = 0; g < G; ++g)
 #pragma unroll
     for (int v = 0; v < VEC; ++v) acc[g][v] = 0.f;
-  bool head = i0 > 0 && __ldg(p.sorted + i0 - 1).x == __ldg(p.sorted + i0).x;
+  const auto keep = [&](int which) {
+#pragma unroll
+    for (int g = 0; g < G; ++g)
+#pragma unroll
+      for (int v = 0; v < VEC; ++v) sm.part[warp][which][g * VEC + v][lane] = acc[g][v];
+  };
+  const bool begun = i0 > 0 && i0 < i1 && __ldg(p.sorted + i0 - 1).x == __ldg(p.sorted + i0).x;
+  bool head = begun, goes = false;  // the run in hand began before; the last one goes on
+  uint32_t last_id = 0xffffffffu;
   for (int64_t j = i0; j < i1; j += 32) {
     const int n = i1 - j < 32 ? static_cast<int>(i1 - j) : 32;
     uint2 k = make_uint2(0xffffffffu, 0);
@@ -321,9 +412,10 @@ __global__ void __launch_bounds__(kSumThreads) embed_sum_kernel(const SumArgs p)
     uint32_t after = __shfl_down_sync(0xffffffffu, k.x, 1);
     if (lane == n - 1) after = j + n < p.tokens ? __ldg(p.sorted + j + n).x : 0xffffffffu;
     const unsigned ends = __ballot_sync(0xffffffffu, lane < n && after != k.x);
-    if (__shfl_sync(0xffffffffu, k.x, 0) >= p.vocab) return;  // from here on none is kept
+    if (__shfl_sync(0xffffffffu, k.x, 0) >= p.vocab) break;  // from here on none is kept
     for (int s = 0; s < n; s += kAhead) {
       Raw<O, VEC> r[kAhead][G];
+      Raw<W, VEC> old[ADD ? kAhead : 1][G];
 #pragma unroll
       for (int a = 0; a < kAhead; ++a) {
         const int src = s + a < n ? s + a : 0;
@@ -336,6 +428,8 @@ __global__ void __launch_bounds__(kSumThreads) embed_sum_kernel(const SumArgs p)
           if (in && c < p.dim) r[a][g] = raw_load<O, VEC>(dy + row * p.dim + c);
           else raw_zero(r[a][g]);
         }
+        // a row of dW that a run ends at, before its sum is known
+        if (ADD && in && ((ends >> src) & 1)) there<W, VEC, G>(p, id, c0, old[a]);
       }
 #pragma unroll
       for (int a = 0; a < kAhead; ++a) {
@@ -344,17 +438,19 @@ __global__ void __launch_bounds__(kSumThreads) embed_sum_kernel(const SumArgs p)
         for (int g = 0; g < G; ++g) {
           float f[VEC];
           widen<VEC>(r[a][g], f);
-#pragma unroll
-          for (int v = 0; v < VEC; ++v) acc[g][v] += f[v];
+          vadd<VEC>(acc[g], acc[g], f);
         }
         const bool end = (ends >> (s + a)) & 1, last = j + s + a + 1 == i1;
         if (end || last) {
           const uint32_t id = __shfl_sync(0xffffffffu, k.x, s + a);
           if (id < p.vocab) {
-            if (head) write_part<VEC, G>(p, 2 * w, c0, acc);
-            else if (end) write_row<W, VEC, G>(p, id, c0, acc);
-            else write_part<VEC, G>(p, 2 * w + 1, c0, acc);
+            if (head) keep(0);
+            else if (end) write_row<W, VEC, G, ADD>(p, id, c0, acc, old[ADD ? a : 0]);
+            else keep(1);
+            goes = !end;
+            last_id = id;
           }
+          if (!end) break;
           head = false;
 #pragma unroll
           for (int g = 0; g < G; ++g)
@@ -364,24 +460,66 @@ __global__ void __launch_bounds__(kSumThreads) embed_sum_kernel(const SumArgs p)
       }
     }
   }
+  if (lane == 0) {
+    has_tail[warp] = goes && !head;
+    whole[warp] = goes && head;  // one run, from before the window to after it
+    tail_id[warp] = last_id;
+  }
+  __syncthreads();
+  const auto add = [&](int of) {
+#pragma unroll
+    for (int g = 0; g < G; ++g)
+#pragma unroll
+      for (int v = 0; v < VEC; ++v) acc[g][v] += sm.part[of][0][g * VEC + v][lane];
+  };
+  const auto take = [&](int which) {
+#pragma unroll
+    for (int g = 0; g < G; ++g)
+#pragma unroll
+      for (int v = 0; v < VEC; ++v) acc[g][v] = sm.part[warp][which][g * VEC + v][lane];
+  };
+  if (warp == 0 && begun) {  // a run from before the CTA's windows
+    take(0);
+    for (int of = 0; of + 1 < kSumWarps && whole[of]; ++of) add(of + 1);
+    write_part<VEC, G>(p, 2 * set, c0, acc);
+  }
+  if (has_tail[warp]) {  // a run that began here: the heads that follow are its own
+    const uint32_t id = tail_id[warp];
+    take(1);
+    int of = warp + 1;
+    bool open = true;
+    for (; of < kSumWarps && open; ++of) {
+      add(of);
+      open = whole[of];
+    }
+    if (open) {
+      write_part<VEC, G>(p, 2 * set + 1, c0, acc);
+    } else {
+      Raw<W, VEC> old[G];
+      if (ADD) there<W, VEC, G>(p, id, c0, old);
+      write_row<W, VEC, G, ADD>(p, id, c0, acc, old);
+    }
+  }
 }
 
-template <typename W, int VEC>
+template <typename W, int VEC, bool ADD>
 __global__ void __launch_bounds__(kSumThreads) embed_join_kernel(const SumArgs p) {
   constexpr int G = Slab<VEC>::kGroups;
   const int lane = threadIdx.x & 31;
   wait_previous();
   const int64_t u = static_cast<int64_t>(blockIdx.x) * (kSumThreads / 32) + (threadIdx.x >> 5);
-  const int64_t w = u / p.slabs;
+  const int64_t w = u / p.slabs, width = static_cast<int64_t>(p.window) * kSumWarps;
   if (w + 1 >= p.windows) return;
-  const int64_t i1 = (w + 1) * p.window;
+  const int64_t i1 = (w + 1) * width;
   const uint32_t id = __ldg(p.sorted + i1 - 1).x;
   // the window's last run began in it and goes on
   if (id >= p.vocab || __ldg(p.sorted + i1).x != id) return;
-  const int64_t i0 = w * p.window;
+  const int64_t i0 = w * width;
   if (i0 > 0 && __ldg(p.sorted + i0).x == id && __ldg(p.sorted + i0 - 1).x == id) return;
   const int64_t c0 = (u - w * p.slabs) * Slab<VEC>::kWidth + lane * VEC;
   float acc[G][VEC];
+  Raw<W, VEC> old[G];
+  if (ADD) there<W, VEC, G>(p, id, c0, old);
 #pragma unroll
   for (int g = 0; g < G; ++g) {
     const int64_t c = c0 + g * 32 * VEC;
@@ -389,7 +527,7 @@ __global__ void __launch_bounds__(kSumThreads) embed_join_kernel(const SumArgs p
   }
   for (int64_t j = w + 1;;) {
     const int64_t mine = j + lane;
-    const bool goes = mine < p.windows && __ldg(p.sorted + mine * p.window).x == id;
+    const bool goes = mine < p.windows && __ldg(p.sorted + mine * width).x == id;
     const unsigned stop = ~__ballot_sync(0xffffffffu, goes);
     const int n = stop ? __ffs(stop) - 1 : 32;
 #pragma unroll 8
@@ -407,7 +545,7 @@ __global__ void __launch_bounds__(kSumThreads) embed_join_kernel(const SumArgs p
     j += n;
     if (n < 32) break;
   }
-  write_row<W, VEC, G>(p, id, c0, acc);
+  write_row<W, VEC, G, ADD>(p, id, c0, acc, old);
 }
 
 // ---- sizes and launches -------------------------------------------------------------
@@ -417,13 +555,14 @@ struct Layout {
   int window;
 };
 
-// Tokens per window: as many as leave about 16 warps per SM, each over 256 columns.
-Layout layout_of(int64_t tokens, int64_t dim) {
+// Tokens per warp: the most, up to 32, that leave 16 warps per SM (long windows
+// leave fewer partial sums).
+Layout layout_of(int64_t tokens, int64_t dim, int width) {
   Layout l;
-  const int64_t slabs = (dim + 255) / 256;
+  const int64_t slabs = (dim + width - 1) / width;
   l.window = 8;
-  while (l.window < 128 && (tokens / (2 * l.window)) * slabs >= 16 * kSms) l.window *= 2;
-  l.windows = (tokens + l.window - 1) / l.window;
+  while (l.window < 32 && tokens / (2 * l.window) * slabs >= 16 * kSms) l.window *= 2;
+  l.windows = (tokens + l.window * kSumWarps - 1) / (l.window * kSumWarps);
   size_t off = 0;
   const auto take = [&](size_t bytes) {
     const size_t o = off;
@@ -450,21 +589,45 @@ cudaError_t look(const EmbedParams& p, cudaStream_t s) {
   return cudaGetLastError();
 }
 
-template <typename W, typename O, int VEC>
-cudaError_t sum(const SumArgs& a, cudaStream_t s) {
-  SumArgs b = a;
-  b.slabs = static_cast<int>((a.dim + Slab<VEC>::kWidth - 1) / Slab<VEC>::kWidth);
-  const int64_t ctas = (a.windows * b.slabs + kSumThreads / 32 - 1) / (kSumThreads / 32);
-  if (ctas > INT32_MAX) return cudaErrorInvalidValue;
-  const cudaError_t e =
-      launch_after(embed_sum_kernel<W, O, VEC>, static_cast<unsigned>(ctas), kSumThreads, 0, s, b);
+template <typename W, typename O, int VEC, bool ADD>
+cudaError_t sum(SumArgs a, cudaStream_t s) {
+  a.slabs = static_cast<int>((a.dim + Slab<VEC>::kWidth - 1) / Slab<VEC>::kWidth);
+  const int64_t units = a.windows * a.slabs;
+  const cudaError_t e = launch_after(embed_sum_kernel<W, O, VEC, ADD>,
+                                     static_cast<unsigned>(units + (ADD ? 0 : a.fills)), kSumThreads, 0, s, a);
   if (e != cudaSuccess) return e;
-  return launch_after(embed_join_kernel<W, VEC>, static_cast<unsigned>(ctas), kSumThreads, 0, s, b);
+  const int64_t ctas = (units + kSumWarps - 1) / kSumWarps;
+  return launch_after(embed_join_kernel<W, VEC, ADD>, static_cast<unsigned>(ctas), kSumThreads, 0, s, a);
+}
+
+cudaError_t sort(const SortArgs& a, cudaStream_t s) {
+  cudaError_t e =
+      cudaFuncSetAttribute(embed_sort_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = a.ctas;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(a.ctas);
+  cfg.blockDim = dim3(kSortThreads);
+  cfg.stream = s;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, embed_sort_kernel, a);
 }
 
 }  // namespace
 
-size_t embed_bwd_workspace_bytes(int64_t tokens, int64_t dim) { return layout_of(tokens, dim).total; }
+// The slabs' width depends on the tensors' alignment; the workspace holds for both.
+size_t embed_bwd_workspace_bytes(int64_t tokens, int64_t dim) {
+  size_t most = 0;
+  for (int width : {Slab<1>::kWidth, Slab<4>::kWidth, Slab<8>::kWidth}) {
+    const size_t n = layout_of(tokens, dim, width).total;
+    most = n > most ? n : most;
+  }
+  return most;
+}
 
 cudaError_t launch_embed_fwd(const EmbedParams& p, bool bf16, bool io_bf16, cudaStream_t s) {
   using bf = __nv_bfloat16;
@@ -478,7 +641,10 @@ cudaError_t launch_embed_fwd(const EmbedParams& p, bool bf16, bool io_bf16, cuda
 
 cudaError_t launch_embed_bwd(const EmbedBwdParams& p, bool bf16, bool io_bf16, cudaStream_t s) {
   using bf = __nv_bfloat16;
-  const Layout l = layout_of(p.tokens, p.dim);
+  const int most = bf16 ? 8 : 4;
+  const bool wide = rows_of(p.dweight, p.dim, bf16 ? 2 : 4, most) &&
+                    rows_of(p.dy, p.dim, io_bf16 ? 2 : 4, most);
+  const Layout l = layout_of(p.tokens, p.dim, !wide ? Slab<1>::kWidth : bf16 ? Slab<8>::kWidth : Slab<4>::kWidth);
   char* ws = static_cast<char*>(p.workspace);
   SortArgs a = {};
   a.ids = p.ids;
@@ -489,40 +655,34 @@ cudaError_t launch_embed_bwd(const EmbedBwdParams& p, bool bf16, bool io_bf16, c
   while ((p.vocab >> bits) > 0) ++bits;  // ids, and `vocab` for the tokens that are left out
   a.passes = (bits + kDigitBits - 1) / kDigitBits;
   a.bits = (bits + a.passes - 1) / a.passes;
-  int fill = 0;
-  if (!p.add) {
-    char* begin = static_cast<char*>(p.dweight);
-    const size_t bytes = static_cast<size_t>(p.vocab) * p.dim * (bf16 ? 2 : 4);
-    size_t before = (16 - reinterpret_cast<uintptr_t>(begin) % 16) % 16;
-    if (before > bytes) before = bytes;
-    a.zeros = reinterpret_cast<uint4*>(begin + before);
-    a.nzeros = static_cast<int64_t>((bytes - before) / 16);
-    a.edge[0] = begin;
-    a.nedge[0] = static_cast<int>(before);
-    a.edge[1] = begin + before + a.nzeros * 16;
-    a.nedge[1] = static_cast<int>(bytes - before - a.nzeros * 16);
-    const int64_t need = (a.nzeros / kSortThreads + 1 + kSortCtas - 1) / kSortCtas;
-    const int64_t most = kSms / kSortCtas - 1;
-    fill = static_cast<int>(need < most ? need : most) * kSortCtas;
-  }
-  cudaError_t e = cudaFuncSetAttribute(embed_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(kSortSmem));
+  a.ctas = 1;  // as many as give each thread a token
+  while (a.ctas < kSortCtas && a.ctas * kSortThreads < p.tokens) a.ctas *= 2;
+  const cudaError_t e = sort(a, s);
   if (e != cudaSuccess) return e;
-  embed_sort_kernel<<<kSortCtas + fill, kSortThreads, kSortSmem, s>>>(a);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
   SumArgs b = {};
   b.sorted = a.passes & 1 ? a.even : a.odd;
   b.dy = p.dy; b.dweight = p.dweight;
   b.part = reinterpret_cast<float*>(ws + l.part);
   b.tokens = p.tokens; b.vocab = p.vocab; b.dim = p.dim;
   b.windows = l.windows; b.window = l.window;
-  b.scale = p.scale; b.add = p.add;
-  const auto wide = [&](int vec) {
-    return rows_of(p.dweight, p.dim, bf16 ? 2 : 4, vec) && rows_of(p.dy, p.dim, io_bf16 ? 2 : 4, vec);
-  };
-  if (!bf16) return wide(4) ? sum<float, float, 4>(b, s) : sum<float, float, 1>(b, s);
-  if (io_bf16) return wide(8) ? sum<bf, bf, 8>(b, s) : sum<bf, bf, 1>(b, s);
-  return wide(8) ? sum<bf, float, 8>(b, s) : sum<bf, float, 1>(b, s);
+  b.scale = p.scale;
+  b.ids = p.ids; b.ignore = p.ignore;
+  // CTAs to fill: of 32 KB each at least, and of twice what reading the ids costs
+  // them, but one per SM
+  const int64_t bytes = p.vocab * p.dim * (bf16 ? 2 : 4);
+  int64_t fills = bytes / (16 * p.tokens + 32768) + 1;
+  fills = fills < kSms ? (bytes / 32768 < kSms ? bytes / 32768 + 1 : kSms) : fills;
+  fills = fills < 3 * kSms ? fills : 3 * kSms;
+  b.fills = static_cast<int>(fills < p.vocab ? fills : p.vocab);
+  const auto pick = [&](auto* onto, auto* fresh) { return p.add ? onto(b, s) : fresh(b, s); };
+  if (!bf16)
+    return wide ? pick(sum<float, float, 4, true>, sum<float, float, 4, false>)
+                : pick(sum<float, float, 1, true>, sum<float, float, 1, false>);
+  if (io_bf16)
+    return wide ? pick(sum<bf, bf, 8, true>, sum<bf, bf, 8, false>)
+                : pick(sum<bf, bf, 1, true>, sum<bf, bf, 1, false>);
+  return wide ? pick(sum<bf, float, 8, true>, sum<bf, float, 8, false>)
+              : pick(sum<bf, float, 1, true>, sum<bf, float, 1, false>);
 }
 
 }  // namespace ssm
