@@ -43,12 +43,21 @@ struct Common {
   float dloss;
 };
 
-// Values and G against one target per token (kLse, kGrad) or against a few entries
-// with probabilities (kSoftLse, kSoftGrad); the products.
-enum Mode { kLse = 0, kGrad = 1, kProducts = 2, kSoftLse = 3, kSoftGrad = 4 };
+// Values, G and the products against one target per token (kLse, kGrad, kProducts) or
+// against a few entries with probabilities.
+enum Mode { kLse = 0, kGrad = 1, kProducts = 2, kSoftLse = 3, kSoftGrad = 4, kSoftProducts = 5 };
 constexpr bool is_lse(int mode) { return mode == kLse || mode == kSoftLse; }
 constexpr bool is_grad(int mode) { return mode == kGrad || mode == kSoftGrad; }
-constexpr bool is_soft(int mode) { return mode == kSoftLse || mode == kSoftGrad; }
+constexpr bool is_products(int mode) { return mode == kProducts || mode == kSoftProducts; }
+constexpr bool is_soft(int mode) { return mode >= kSoftLse; }
+
+// Against entries no part of G is nearly exact in bf16 as p - 1 at a target is.  Up to
+// kHalfTile tokens leave half of the one row of tiles empty: there G's lower half is
+// kept, what rounding took from a row of G rounded in turn, kHalfTile rows further.  The
+// products take both halves, dh's at no cost, dW's over twice as many (few) rows, and the
+// gradients are off by little but their own rounding.  With more tokens dh and dW are
+// off by 1.8e-3 to 2.0e-3 and 2.2e-3 to 2.4e-3 of themselves, of which that is 1.7e-3.
+__device__ __forceinline__ bool two_halves(int rows) { return rows <= kHalfTile; }
 
 struct GemmArgs {
   const int* count;       // rows kept; null: every token is a row
@@ -177,16 +186,17 @@ struct Work {
     rows = rows_of(p);
     mt = ceil_div(rows, kTile);
     vt = ceil_div(p.vp, kTile);
-    nt = MODE == kProducts ? ceil_div(p.dim, kTile) : vt;
+    nt = is_products(MODE) ? ceil_div(p.dim, kTile) : vt;
     kv = ceil_div(p.vp, kBk);
-    kt = MODE == kProducts ? ceil_div(rows, kBk) : ceil_div(p.dim, kBk);
-    splits = MODE == kProducts ? dh_splits(mt, nt, p.kv_whole) : 1;
+    kt = is_products(MODE) ? ceil_div(rows, kBk) : ceil_div(p.dim, kBk);
+    if (MODE == kSoftProducts && two_halves(rows)) kt *= 2;
+    splits = is_products(MODE) ? dh_splits(mt, nt, p.kv_whole) : 1;
     ndh = mt * nt * splits;
-    ndw = MODE == kProducts ? vt * nt : 0;
+    ndw = is_products(MODE) ? vt * nt : 0;
     heavy = ndh % clusters;
     light = clusters - heavy;
     ahead = 0;
-    if (MODE == kProducts && heavy > 0 && kt > 0) {
+    if (is_products(MODE) && heavy > 0 && kt > 0) {
       ahead = kv / splits / kt;
       if (ahead > ndw / light) ahead = ndw / light;
     }
@@ -196,7 +206,7 @@ struct Work {
     const int u = cluster + i * clusters;
     if (u < ndh) {
       r->split = 0; r->dw = false; r->k0 = 0; r->k1 = kt;
-      if (MODE != kProducts) {
+      if (!is_products(MODE)) {
         r->m = u % mt; r->n = u / mt;
         return true;
       }
@@ -206,7 +216,7 @@ struct Work {
       r->k1 = static_cast<int>(static_cast<int64_t>(kv) * (r->split + 1) / splits);
       return true;
     }
-    if (MODE != kProducts) return false;
+    if (!is_products(MODE)) return false;
     int j = i - (ndh / clusters + (cluster < heavy ? 1 : 0)), w;
     if (cluster >= heavy && j < ahead) {
       w = cluster - heavy + j * light;
@@ -357,7 +367,8 @@ __device__ __forceinline__ void epilogue_lse(const GemmArgs& p, uint32_t acc, in
 template <bool SOFT>
 __device__ __forceinline__ void epilogue_grad(const GemmArgs& p, const Maps& maps, OutBox& out,
                                               uint32_t acc, int64_t row, int n, int tgt,
-                                              float lse, float scale, bool kept, Cursor& cur) {
+                                              float lse, float scale, bool kept, bool low,
+                                              Cursor& cur) {
   const int row0 = static_cast<int>(row) - static_cast<int>(threadIdx.x & 31);
   const int c0 = n * kTile;
   const int cols = p.vp - c0 < kTile ? p.vp - c0 : kTile;
@@ -371,6 +382,7 @@ __device__ __forceinline__ void epilogue_grad(const GemmArgs& p, const Maps& map
     out.open();
     umma::tmem_wait_ld(r[0]);
     umma::tmem_wait_ld(r[1]);
+    uint32_t lower[SOFT ? 2 : 1][16];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int b = c + 32 * h;
@@ -415,8 +427,26 @@ __device__ __forceinline__ void epilogue_grad(const GemmArgs& p, const Maps& map
       for (int k = 0; k < 4; ++k)
         out.put(4 * h + k, pack2(v[8 * k], v[8 * k + 1]), pack2(v[8 * k + 2], v[8 * k + 3]),
                 pack2(v[8 * k + 4], v[8 * k + 5]), pack2(v[8 * k + 6], v[8 * k + 7]));
+      if constexpr (SOFT) {
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          const uint32_t w = pack2(v[2 * k], v[2 * k + 1]);
+          lower[h][k] = pack2(v[2 * k] - __uint_as_float(w << 16),
+                              v[2 * k + 1] - __uint_as_float(w & 0xffff0000u));
+        }
+      }
     }
     out.send(&maps.g, c0 + c, row0, false);
+    if (SOFT && low) {
+      out.open();
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          out.put(4 * h + k, lower[SOFT ? h : 0][4 * k], lower[SOFT ? h : 0][4 * k + 1],
+                  lower[SOFT ? h : 0][4 * k + 2], lower[SOFT ? h : 0][4 * k + 3]);
+      out.send(&maps.g, c0 + c, row0 + kHalfTile, false);
+    }
   }
 }
 
@@ -509,7 +539,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     uint32_t ph = 1;
     int used = 0;  // stages that hold a copy, at most kStages
     const bool all = p.count == nullptr || rows_in_place(rows_of(p), p.tokens);
-    const CUtensorMap* ma_map = MODE != kProducts && all ? &maps.h : &maps.a;
+    const CUtensorMap* ma_map = !is_products(MODE) && all ? &maps.h : &maps.a;
     const CUtensorMap* bt_map = all ? &maps.h : &maps.bt;
     Unit t;
     for (int i = 0; !bad && work.at(i, &t); ++i) {
@@ -523,7 +553,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const uint32_t a = base + s * kStage, b = a + kOperand;
         const uint32_t bar = pair::map_to(full(s), 0);
         if (rank == 0) umma::mbar_expect_tx(full(s), 2 * kStage);
-        if (MODE != kProducts) {
+        if (!is_products(MODE)) {
           pair::tma_load_2d(a, ma_map, k * kBk, ma, bar);
           pair::tma_load_2d(b, &maps.b, k * kBk, v0 + nb, bar);
         } else if (!t.dw) {
@@ -531,10 +561,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           pair::tma_load_2d(b, &maps.b, nb, v0 + k * kBk, bar);
           pair::tma_load_2d(b + kOperand / 2, &maps.b, nb + 64, v0 + k * kBk, bar);
         } else {
-          pair::tma_load_2d(a, &maps.at, ma, k * kBk, bar);
-          pair::tma_load_2d(a + kOperand / 2, &maps.at, ma + 64, k * kBk, bar);
-          pair::tma_load_2d(b, bt_map, nb, k * kBk, bar);
-          pair::tma_load_2d(b + kOperand / 2, bt_map, nb + 64, k * kBk, bar);
+          int g = k * kBk, r = g;  // rows of G, and of h
+          if (MODE == kSoftProducts && two_halves(work.rows) && k >= work.kt / 2) {
+            r -= work.kt / 2 * kBk;
+            g = kHalfTile + r;
+          }
+          pair::tma_load_2d(a, &maps.at, ma, g, bar);
+          pair::tma_load_2d(a + kOperand / 2, &maps.at, ma + 64, g, bar);
+          pair::tma_load_2d(b, bt_map, nb, r, bar);
+          pair::tma_load_2d(b + kOperand / 2, bt_map, nb + 64, r, bar);
         }
         if (used < kStages) ++used;
         if (++s == kStages) { s = 0; ph ^= 1; }
@@ -558,7 +593,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     Unit t;
     for (; !bad && work.at(n, &t); ++n) {
       const int b = n & 1;
-      const bool a_mn = t.dw, b_mn = MODE == kProducts;
+      const bool a_mn = t.dw, b_mn = is_products(MODE);
       const uint32_t id = umma::idesc_bf16(kTile, kTile, a_mn, b_mn);
       if (!pair::mbar_wait(acc_empty(b), ((n >> 1) & 1) ^ 1, kWaitNs)) {
         bad = true;
@@ -586,7 +621,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int q = warp & 3;
     const int row = static_cast<int>(rank) * kHalfTile + q * 32 + lane;
     OutBox out = {base + kOut + (warp - 2) * 2 * kBox, 0};
-    const float common = MODE == kProducts ? p.common->dloss * p.gain : 1.f;
+    const float common = is_products(MODE) ? p.common->dloss * p.gain : 1.f;
     const bool shared = is_grad(MODE) && p.common->shared;
     Unit t;
     for (int n = 0; !bad && work.at(n, &t); ++n) {
@@ -594,7 +629,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const int64_t r = static_cast<int64_t>(t.m) * kTile + row;
       int tgt = -1;
       float lse = 0.f, scale = 0.f;
-      if (MODE != kProducts) tgt = target_of(p, r);
+      if (!is_products(MODE)) tgt = target_of(p, r);
       if (is_grad(MODE)) {
         lse = p.lse[r];
         scale = shared ? 1.f : p.scale[r];
@@ -612,10 +647,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (is_lse(MODE)) epilogue_lse<is_soft(MODE)>(p, acc, r, t.n, tgt, cur);
       // rows of G past the last kept one are read up to a whole stage of dW's products
       if (is_grad(MODE) && r - lane < (work.rows + kBk - 1) / kBk * kBk)
-        epilogue_grad<is_soft(MODE)>(p, maps, out, acc, r, t.n, tgt, lse, scale, r < work.rows, cur);
-      if (MODE == kProducts)
-        epilogue_products(p, maps, out, acc, t, row - lane, work.rows, work.mt, t.k1 <= t.k0,
-                          common);
+        epilogue_grad<is_soft(MODE)>(p, maps, out, acc, r, t.n, tgt, lse, scale, r < work.rows,
+                                     is_soft(MODE) && two_halves(work.rows), cur);
+      if (is_products(MODE))
+        epilogue_products(p, maps, out, acc, t, row - lane,
+                          MODE == kSoftProducts && two_halves(work.rows) ? kHalfTile + work.rows : work.rows,
+                          work.mt, t.k1 <= t.k0, common);
       __syncwarp();
       umma::fence_before_sync();
       __syncwarp();
@@ -820,6 +857,7 @@ __global__ void __launch_bounds__(kGatherThreads) xent_gather_kernel(const Gathe
 
 // dh of a token: the sum of the splits' partial sums and of what rounding took
 // from G at the target, rounded once.
+template <bool SOFT>
 __global__ void __launch_bounds__(256) xent_dh_kernel(const GemmArgs p, const int* idx,
                                                       __nv_bfloat16* dh) {
   wait_previous();
@@ -838,7 +876,15 @@ __global__ void __launch_bounds__(256) xent_dh_kernel(const GemmArgs p, const in
       const float4 a = *reinterpret_cast<const float4*>(q + s * plane);
       v.x += a.x; v.y += a.y; v.z += a.z; v.w += a.w;
     }
-    if (const int t = p.target[r]; t >= 0) {
+    const bool low = SOFT && two_halves(rows);
+    if (low) {  // the lower half's
+#pragma unroll 8
+      for (int s = 0; s < splits; ++s) {
+        const float4 a = *reinterpret_cast<const float4*>(q + s * plane + kHalfTile * p.dim);
+        v.x += a.x; v.y += a.y; v.z += a.z; v.w += a.w;
+      }
+    }
+    if (const int t = p.target[r]; t >= 0 && !low) {
       const uint2 w = __ldg(reinterpret_cast<const uint2*>(p.weight + t * p.dim + c));
       const float lost = p.lost[r];
       v.x = fmaf(lost, __uint_as_float(w.x << 16), v.x);
@@ -978,9 +1024,9 @@ cudaError_t backward(const XentParams& p, GatherArgs g, GemmArgs a, const Layout
     a.vp = static_cast<int>(z.vocab - a.v0 < l.piece ? z.vocab - a.v0 : l.piece);
     a.add = i > 0;
     if ((e = gemm<GRAD>(in, a, s)) != cudaSuccess) return e;
-    if ((e = gemm<kProducts>(out, a, s)) != cudaSuccess) return e;
+    if ((e = gemm<is_soft(GRAD) ? kSoftProducts : kProducts>(out, a, s)) != cudaSuccess) return e;
   }
-  return launch_after(xent_dh_kernel, 4 * kSms, 256, 0, s, a, g.idx,
+  return launch_after(xent_dh_kernel<is_soft(GRAD)>, 4 * kSms, 256, 0, s, a, g.idx,
                       static_cast<__nv_bfloat16*>(p.dh));
 }
 

@@ -145,12 +145,13 @@ def test_one_entry_is_the_cross_entropy():
     t = make(300, 4000, 128, 1, ignored=0.2)
     loss, lse = S.xent_fwd(t["h"], t["w"], t["ids"][:, 0])
     got = run(t)
-    assert torch.equal(got["lse"], lse)
+    # two results within the bounds of the same definition
     ref = reference(t)
+    assert ((got["lse"] - lse).double().abs() <= 2 * ref["lse_bound"]).all()
     assert ((got["loss"] - loss).double().abs() <= 2 * ref["loss_bound"]).all()
     g = S.xent_bwd(t["h"], t["w"], t["ids"][:, 0], lse=lse, dloss=t["dloss"])
     for k in ("dh", "dweight"):
-        assert torch.allclose(g[k].float(), got[k].float(), rtol=2 ** -7, atol=1e-6), k
+        assert ((g[k].double() - got[k].double()).abs() <= 2 * ref[k + "_bound"]).all(), k
 
 
 def test_a_student_that_agrees():
@@ -457,3 +458,28 @@ def test_refusals():
         with pytest.raises(S.SsmError) as e:
             call()
         assert e.value.status == status
+
+
+@pytest.mark.parametrize("T,K", [(1, 1), (1, 3), (24, 2), (128, 4), (100, 64)])
+@pytest.mark.parametrize("shared", [True, False])
+def test_gradients_of_few_tokens_keep_their_digits(T, K, shared):
+    """Up to 128 tokens G is kept in two halves of 8 bits each, off by 2^-16: dh and
+    dweight are off by their own rounding (at most 2^-8, 2^-9 on average over a
+    tensor) and a little."""
+    t = make(T, 3001, 256, K, seed=T + K, ragged=K > 2)
+    if shared:
+        t["dloss"] = torch.full((T,), 1.0 / T, device="cuda")
+    ref, got = reference(t), run(t)
+    for name in ("dh", "dweight"):
+        assert_close(got[name], ref, name)
+        off = (got[name].double() - ref[name]).norm()
+        assert off <= 2.0 ** -9 * 1.25 * ref[name].norm(), (name, float(off / ref[name].norm()))
+
+
+@pytest.mark.parametrize("T,ignored", [(127, 0.0), (128, 0.0), (129, 0.0), (300, 0.6)])
+def test_around_half_a_tile_of_tokens(T, ignored):
+    """The count of tokens with entries decides, also where others are left out."""
+    t = make(T, 700, 136, 12, ignored=ignored, seed=T)
+    ref, got = reference(t), run(t)
+    for name in NAMES:
+        assert_close(got[name], ref, name)
