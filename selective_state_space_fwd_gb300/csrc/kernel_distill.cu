@@ -48,6 +48,7 @@ __global__ void __launch_bounds__(kPrepWarps * 32) distill_prep_kernel(const Pre
   extern __shared__ uint2 prep_mem[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t t = static_cast<int64_t>(blockIdx.x) * kPrepWarps + warp;
+  release_next();
   if (t >= p.tokens) return;
   uint2* list = prep_mem + warp * p.padded;
   float top = -INFINITY, best = 0.f;
@@ -257,7 +258,7 @@ cudaError_t launch_distill_fwd(const DistillParams& d, cudaStream_t s) {
   // leaving tokens out saves nothing while all of them fit one row of tiles
   if (z.tokens <= kTile)
     a.count = nullptr;
-  else if ((e = gather(g, s)) != cudaSuccess)
+  else if ((e = gather(g, true, s)) != cudaSuccess)
     return e;
   if ((e = gemm<kSoftLse>(maps, a, s)) != cudaSuccess) return e;
   return launch_after(distill_join_kernel, static_cast<unsigned>((z.tokens + 31) / 32), 1024, 0, s,

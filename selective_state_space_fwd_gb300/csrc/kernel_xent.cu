@@ -323,7 +323,7 @@ cudaError_t launch_xent_fwd(const XentParams& p, cudaStream_t s) {
     if (!direct) {
       if (!map_bf16_sw128(&maps.a, g.rows, z.dim, l.tpad, z.dim, kHalfTile))
         return cudaErrorInvalidValue;
-      if ((e = gather(g, s)) != cudaSuccess) return e;
+      if ((e = gather(g, false, s)) != cudaSuccess) return e;
     }
     e = gemm<kLse>(maps, a, s);
   }

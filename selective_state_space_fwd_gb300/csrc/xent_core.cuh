@@ -736,6 +736,7 @@ __global__ void __launch_bounds__(kGatherThreads) xent_gather_kernel(const Gathe
   __shared__ int src[kGatherThreads], gone[kGatherThreads];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * p.per;
+  wait_previous();  // of the kernel that made the targets, where one did
   release_next();
   int before = 0, total = 0;
 #pragma unroll 8
@@ -953,8 +954,10 @@ cudaError_t gemm(const Maps& maps, const GemmArgs& a, cudaStream_t s) {
   return launch_after(k, 2 * kClusters, kThreads, kSmem, s, maps, a);
 }
 
-cudaError_t gather(const GatherArgs& g, cudaStream_t s) {
+cudaError_t gather(const GatherArgs& g, bool after, cudaStream_t s) {
   const int64_t ctas = (g.tokens + g.per - 1) / g.per;
+  if (after)
+    return launch_after(xent_gather_kernel, static_cast<unsigned>(ctas), kGatherThreads, 0, s, g);
   xent_gather_kernel<<<static_cast<unsigned>(ctas), kGatherThreads, 0, s>>>(g);
   return cudaGetLastError();
 }
@@ -1017,7 +1020,7 @@ cudaError_t backward(const XentParams& p, GatherArgs g, GemmArgs a, const Layout
       !map_bf16_sw128(&out.bt, g.rows, z.dim, l.tpad, z.dim, kBk) ||
       !map_bf16_sw128(&out.h, p.h, z.dim, z.tokens, z.dim, kBk))
     return cudaErrorInvalidValue;
-  cudaError_t e = gather(g, s);
+  cudaError_t e = gather(g, is_soft(GRAD), s);
   if (e != cudaSuccess) return e;
   for (int64_t i = 0; i < l.pieces; ++i) {
     a.v0 = i * l.piece;

@@ -487,28 +487,36 @@ def _recur_args(gate, value, floor, rank):
     recurrence whose gate and value have `rank` dimensions, the last of them
     contiguous."""
     dev = _cuda(gate, "gate")
-    code = _code(gate.dtype)
-    size = gate.shape
+    dtype, size = gate.dtype, gate.shape
+    code = _code(dtype)
     if len(size) != rank:
         raise ValueError(f"gate: {len(size)} dimensions, expected {rank}")
-    if value.dtype is not gate.dtype:
-        raise TypeError(f"value: dtype {value.dtype}, expected {gate.dtype}")
+    if value.dtype is not dtype:
+        raise TypeError(f"value: dtype {value.dtype}, expected {dtype}")
     if value.shape != size or value.device != dev:
         raise ValueError(f"value: shape {tuple(value.shape)} on {value.device}, "
                          f"expected {tuple(size)} on {dev}")
-    batch, dim = size[0], size[-1]
-    seqlen = size[1] if rank == 3 else 1
-    strides = []
-    for name, t in (("gate", gate), ("value", value)):
-        stride = t.stride()
-        if stride[-1] != 1 and dim > 1:
-            raise ValueError(f"{name}: the channels must be contiguous")
-        # the stride of an axis of one element is never used; the row's own length
-        # keeps it from deciding the alignment rule
-        strides += [stride[0] if batch > 1 else dim, stride[1] if seqlen > 1 else dim]
+    gs, vs = gate.stride(), value.stride()
+    if rank == 3:
+        batch, seqlen, dim = size
+        if seqlen > 1:
+            g_step, v_step = gs[1], vs[1]
+        else:
+            g_step = v_step = dim
+    else:
+        batch, dim = size
+        seqlen, g_step, v_step = 1, dim, dim
+    if dim > 1 and (gs[-1] != 1 or vs[-1] != 1):
+        raise ValueError("gate and value: the channels must be contiguous")
     if floor is not None:
         _dense(floor, "floor", (dim,), _F32, dev)
-    return dev, code, batch, seqlen, dim, _recur_sizes(batch, seqlen, dim, *strides)
+    # the stride of an axis of one element is never used; the row's own length
+    # keeps it from deciding the alignment rule
+    if batch > 1:
+        sizes = _recur_sizes(batch, seqlen, dim, gs[0], g_step, vs[0], v_step)
+    else:
+        sizes = _recur_sizes(batch, seqlen, dim, dim, g_step, dim, v_step)
+    return dev, code, batch, seqlen, dim, sizes
 
 
 def recur_fwd(gate, value, floor=None, valid_len=None, *, state0=None, want_final: bool = False,
