@@ -1,7 +1,7 @@
 """A small language model of selective-scan layers, trained and generating with
-the library's operators.
+the library's operators, and a student of gated recurrences that learns from it.
 
-    python examples/lm.py [--steps 200]
+    python examples/lm.py [--steps 300] [--student 300]
 
 Each layer adds to a residual stream kept in fp32:
 
@@ -14,6 +14,13 @@ and the model ends in linear_cross_entropy against the embedding, whose logits
 are never kept.  Generation runs the prompt once (conv_fwd and scan_fwd return
 their states) and then single tokens (norm_fwd, conv_step, decode_step), which
 reproduce the prompt pass.
+
+The student's layers mix along time with the gated linear recurrence alone:
+
+    g, v, z = projections of y
+    h = out_proj(gated_recurrence(g, v, floor) * silu(z))
+
+and it is trained by linear_distillation on the teacher's top logits.
 """
 import argparse
 import os
@@ -81,24 +88,71 @@ class Layer(torch.nn.Module):
         return h @ self.out_w.T, stream
 
 
+class GatedLayer(torch.nn.Module):
+    """A layer of the student: the gated linear recurrence and an output gate."""
+
+    def __init__(self, dim: int, inner: int):
+        super().__init__()
+        self.inner = inner
+
+        def weight(rows, cols):
+            return torch.nn.Parameter((torch.randn(rows, cols) / cols ** 0.5).to(BF16))
+
+        self.norm_w = torch.nn.Parameter(torch.ones(dim))
+        self.in_w = weight(3 * inner, dim)                       # gate, value, output gate
+        self.floor_logit = torch.nn.Parameter(torch.linspace(-4, 2, inner))
+        self.out_w = weight(dim, inner)
+
+    def forward(self, h, stream):
+        y, stream = S.layer_norm(h, self.norm_w, residual=stream, rms=True)
+        g, v, z = (y @ self.in_w.T).split(self.inner, dim=-1)    # read in place, strided
+        u = S.gated_recurrence(g, v, torch.sigmoid(self.floor_logit))
+        return (u * F.silu(z)) @ self.out_w.T, stream
+
+    def prompt(self, h, stream):
+        """As forward, keeping the state to generate from."""
+        y, stream, _ = S.norm_fwd(h, self.norm_w, residual=stream, rms=True)
+        g, v, z = (y @ self.in_w.T).split(self.inner, dim=-1)
+        u, state, _ = S.recur_fwd(g, v, torch.sigmoid(self.floor_logit), want_final=True)
+        return (u * F.silu(z)) @ self.out_w.T, stream, state
+
+    def step(self, h, stream, state):
+        """One token per sequence; the state and the stream are updated in place."""
+        y, stream, _ = S.norm_fwd(h, self.norm_w, residual=stream, rms=True, out_r=stream)
+        g, v, z = (y @ self.in_w.T).split(self.inner, dim=-1)
+        u = S.recur_step(g, v, torch.sigmoid(self.floor_logit), state=state)
+        return (u * F.silu(z)) @ self.out_w.T, stream
+
+
 class Model(torch.nn.Module):
-    def __init__(self, vocab=1000, dim=128, layers=2, inner=256, dstate=16, width=4):
+    def __init__(self, vocab=1000, dim=128, layers=2, inner=256, dstate=16, width=4, gated=False):
         super().__init__()
         self.embed = torch.nn.Parameter((torch.randn(vocab, dim) * 0.05).to(BF16))
-        self.layers = torch.nn.ModuleList(Layer(dim, inner, dstate, width) for _ in range(layers))
+        self.layers = torch.nn.ModuleList(
+            GatedLayer(dim, inner) if gated else Layer(dim, inner, dstate, width)
+            for _ in range(layers))
         self.norm_w = torch.nn.Parameter(torch.ones(dim))
 
     def start(self, tokens):
-        h = F.embedding(tokens, self.embed)
+        h = S.embedding(tokens, self.embed)
         return h, torch.zeros(h.shape, dtype=torch.float32, device=h.device)
 
-    def loss(self, tokens, targets):
-        """The mean cross entropy of targets (-100: no target) after tokens."""
+    def hidden(self, tokens):
+        """The last hidden state of every token, which the losses start from."""
         h, stream = self.start(tokens)
         for layer in self.layers:
             h, stream = layer(h, stream)
         y, _ = S.layer_norm(h, self.norm_w, residual=stream, rms=True)
-        return S.linear_cross_entropy(y, self.embed, targets)
+        return y
+
+    def loss(self, tokens, targets):
+        """The mean cross entropy of targets (-100: no target) after tokens."""
+        return S.linear_cross_entropy(self.hidden(tokens), self.embed, targets)
+
+    def distill_loss(self, tokens, ids, logits, temperature=1.0):
+        """The mean divergence from a teacher's top logits after tokens."""
+        return S.linear_distillation(self.hidden(tokens), self.embed, ids, logits,
+                                     temperature=temperature)
 
     def head(self, h, stream):
         y, _, _ = S.norm_fwd(h, self.norm_w, residual=stream, rms=True)
@@ -159,15 +213,41 @@ def train(model, steps, rows=8, length=96, lr=3e-3, seed=0, report=None):
     return [v.item() for v in losses]
 
 
+def teach(teacher, student, steps, top=8, temperature=2.0, rows=8, length=96, lr=3e-3, seed=1,
+          report=None):
+    """Trains the student on the teacher's `top` logits alone."""
+    device = teacher.embed.device
+    rng = torch.Generator().manual_seed(seed)
+    opt = torch.optim.AdamW(student.parameters(), lr=lr, weight_decay=0.0)
+    losses = []
+    for i in range(steps):
+        tokens, targets = batch(rng, rows, length, teacher.embed.shape[0], device)
+        logits, ids = teacher.prompt(tokens)[0].topk(top, dim=-1)
+        ids[targets < 0] = -100                                  # no context yet to learn from
+        loss = student.distill_loss(tokens, ids, logits, temperature) * temperature ** 2
+        opt.zero_grad()
+        loss.backward()
+        opt.step()
+        losses.append(loss.detach())
+        if report and (i + 1) % report == 0:
+            print(f"student, step {i + 1}: divergence {loss.item():.3f}")
+    S.check_device_errors()
+    return [v.item() for v in losses]
+
+
 def main():
     ap = argparse.ArgumentParser(description=__doc__.splitlines()[0])
     ap.add_argument("--steps", type=int, default=300)
+    ap.add_argument("--student", type=int, default=300, help="steps of the student's training")
     a = ap.parse_args()
     torch.manual_seed(0)
     model = Model(vocab=200).cuda()
     train(model, a.steps, report=50)
     prompt = torch.tensor([[10, 12, 14, 16, 18, 20], [50, 51, 52, 53, 54, 55]], device="cuda")
     print("prompt", prompt.tolist(), "->", model.generate(prompt, 6).tolist())
+    student = Model(vocab=200, dim=96, inner=192, gated=True).cuda()
+    teach(model, student, a.student, report=50)
+    print("student:", student.generate(prompt, 6).tolist())
 
 
 if __name__ == "__main__":

@@ -260,5 +260,6 @@ class _Embedding(torch.autograd.Function):
 
 
 def embedding(ids, weight, *, scale: float = 1.0, ignore_index: int = -100, dtype=None):
-    """y = scale weight[ids] (as ``embed_fwd``), differentiable in weight."""
-    return _Embedding.apply(ids, weight, float(scale), int(ignore_index), dtype)
+    """y = scale weight[ids] (as ``embed_fwd``; ids may be strided), differentiable in
+    weight."""
+    return _Embedding.apply(ids.contiguous(), weight, float(scale), int(ignore_index), dtype)

@@ -16,6 +16,8 @@
 // once, and per window two rows of fp32.
 #include <cuda_bf16.h>
 
+#include <atomic>
+
 #include "common.cuh"
 #include "f32x2.cuh"
 #include "layers.h"
@@ -600,10 +602,14 @@ cudaError_t sum(SumArgs a, cudaStream_t s) {
   return launch_after(embed_join_kernel<W, VEC, ADD>, static_cast<unsigned>(ctas), kSumThreads, 0, s, a);
 }
 
-cudaError_t sort(const SortArgs& a, cudaStream_t s) {
+// Sorts with one thread per token, but in at most kSortCtas CTAs (8 where the GPU has
+// no room for a larger cluster).
+cudaError_t sort(SortArgs& a, cudaStream_t s) {
   cudaError_t e =
       cudaFuncSetAttribute(embed_sort_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e != cudaSuccess) return e;
+  a.ctas = 1;
+  while (a.ctas < kSortCtas && a.ctas * kSortThreads < a.tokens) a.ctas *= 2;
   cudaLaunchAttribute attr = {};
   attr.id = cudaLaunchAttributeClusterDimension;
   attr.val.clusterDim.x = a.ctas;
@@ -614,6 +620,20 @@ cudaError_t sort(const SortArgs& a, cudaStream_t s) {
   cfg.stream = s;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
+  static std::atomic<int> whole{-1};  // clusters of kSortCtas that the GPU holds
+  int n = whole.load(std::memory_order_relaxed);
+  if (a.ctas == kSortCtas && n < 0) {
+    if (cudaOccupancyMaxActiveClusters(&n, embed_sort_kernel, &cfg) != cudaSuccess) {
+      cudaGetLastError();
+      n = 0;
+    }
+    whole.store(n, std::memory_order_relaxed);
+  }
+  if (a.ctas == kSortCtas && n < 1) {
+    a.ctas = kSortCtas / 2;
+    attr.val.clusterDim.x = a.ctas;
+    cfg.gridDim = dim3(a.ctas);
+  }
   return cudaLaunchKernelEx(&cfg, embed_sort_kernel, a);
 }
 
@@ -655,8 +675,6 @@ cudaError_t launch_embed_bwd(const EmbedBwdParams& p, bool bf16, bool io_bf16, c
   while ((p.vocab >> bits) > 0) ++bits;  // ids, and `vocab` for the tokens that are left out
   a.passes = (bits + kDigitBits - 1) / kDigitBits;
   a.bits = (bits + a.passes - 1) / a.passes;
-  a.ctas = 1;  // as many as give each thread a token
-  while (a.ctas < kSortCtas && a.ctas * kSortThreads < p.tokens) a.ctas *= 2;
   const cudaError_t e = sort(a, s);
   if (e != cudaSuccess) return e;
   SumArgs b = {};

@@ -431,6 +431,7 @@ __global__ void __launch_bounds__(W * 32)
       if (tile_of(i) < live) ring.drain(i);
     atomicOr(a.err, kErrRecurWait);
   }
+  if (CLUSTER) pair::cluster_sync();  // no map is on its way to a CTA that has ended
 }
 
 // ---- backward -----------------------------------------------------------------
@@ -661,6 +662,7 @@ __global__ void __launch_bounds__(W * 32)
       if (tile_of(i) >= 0) ring.drain(i);
     atomicOr(a.err, kErrRecurWait);
   }
+  if (CLUSTER) pair::cluster_sync();  // no map is on its way to a CTA that has ended
 }
 
 // The axes in the order of their strides, as a tensor map wants them: each stride

@@ -236,6 +236,8 @@ def test_autograd(dtype, io):
     assert torch.equal(y.view(60, 64), S.embed_fwd(t["ids"], t["w"], scale=8.0, dtype=io))
     (y * t["dy"].view(3, 20, 64)).sum().backward()
     assert w.grad.dtype is dtype
+    wide = torch.stack([t["ids"], t["ids"]], 1)[:, 0]  # strided
+    assert torch.equal(S.embedding(wide, w), S.embed_fwd(t["ids"], t["w"]))
     assert torch.equal(w.grad, S.embed_bwd(t["ids"], t["dy"], vocab=90, scale=8.0, dtype=dtype))
     (g,) = torch.autograd.grad((S.embedding(t["ids"], w) ** 2).sum(), w, create_graph=True)
     with pytest.raises(RuntimeError, match="differentiated again"):
