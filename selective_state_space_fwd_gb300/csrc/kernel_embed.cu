@@ -6,7 +6,8 @@
 // The gradient adds the rows of equal tokens in the order of the tokens, without
 // atomics, so that equal inputs give equal bits:
 // 1. The tokens are sorted by id, stably (least significant digits first, kDigits
-//    values at a time), by one CTA or one cluster whose counts meet in shared memory.
+//    values at a time), by one cluster whose counts meet in shared memory; few tokens
+//    are placed by counting instead.  dW is filled with zeros meanwhile.
 // 2. The sorted tokens are cut into windows.  A warp takes a window for a slab of
 //    columns, adds the rows of each run of equal ids in fp32 and writes the runs
 //    that lie in the window.  A run that another window shares leaves a partial
@@ -69,7 +70,7 @@ __global__ void __launch_bounds__(kLookThreads) embed_fwd_kernel(const EmbedPara
 constexpr int kSortCtas = 16;                          // at most
 constexpr int kSortThreads = 1024, kSortWarps = kSortThreads / 32;
 constexpr int kDigitBits = 9, kDigits = 1 << kDigitBits;
-constexpr int kRounds = 8;                             // keys per thread and tile
+constexpr int kRounds = 4;                             // keys per thread and tile
 constexpr int kSortTile = kSortThreads * kRounds;
 static_assert(kSortTile <= 65536, "places within a tile are kept in 16 bits");
 
@@ -245,6 +246,78 @@ __global__ void __launch_bounds__(kSortThreads, 1) embed_sort_kernel(const SortA
   }
 }
 
+// Few tokens are placed by counting, all SMs at once and without passes: a CTA takes
+// kRankTokens of them, one per lane, and its warps share the tokens that each is
+// compared with.  T^2 comparisons: 8192 tokens 5 us, where the passes' latencies alone
+// are 12 us.
+constexpr int kRankMost = 8192, kRankTokens = 32, kRankWarps = 16;
+__global__ void __launch_bounds__(kRankWarps * 32) embed_rank_kernel(const SortArgs p) {
+  __shared__ __align__(16) uint32_t ids[kRankMost];
+  __shared__ uint32_t part[kRankWarps][kRankTokens];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int n = static_cast<int>(p.tokens), i0 = blockIdx.x * kRankTokens, i = i0 + lane;
+  release_next();
+#pragma unroll 8
+  for (int t = threadIdx.x; t < n; t += kRankWarps * 32) {
+    const int64_t id = __ldg(p.ids + t);
+    const bool kept = id >= 0 && id < p.vocab && id != p.ignore;
+    ids[t] = static_cast<uint32_t>(kept ? id : p.vocab);
+  }
+  const int pad = (n + 3) / 4 * 4;
+  if (threadIdx.x < pad - n) ids[n + threadIdx.x] = 0x7fffffffu;  // before nothing
+  __syncthreads();
+  const uint32_t mine = i < n ? ids[i] : 0;
+  // those of an equal id count where they come before: the CTA's own tokens one by one,
+  // the others in groups of four
+  uint32_t count = 0;
+  const auto groups = [&](int from, int to, uint32_t below) {
+#pragma unroll 4
+    for (int j = from + warp * 4; j < to; j += kRankWarps * 4) {
+      const uint4 k = *reinterpret_cast<const uint4*>(ids + j);
+      // k < below: the difference's sign, as neither reaches 2^31
+      count += ((k.x - below) >> 31) + ((k.y - below) >> 31);
+      count += ((k.z - below) >> 31) + ((k.w - below) >> 31);
+    }
+  };
+  groups(0, i0, mine + 1);
+  groups(i0 + kRankTokens, pad, mine);
+  if (warp == 0) {
+    const int own = n - i0 < kRankTokens ? n - i0 : kRankTokens;
+    for (int j = 0; j < own; ++j) {
+      const uint32_t k = ids[i0 + j];
+      count += k < mine || (k == mine && j < lane);
+    }
+  }
+  part[warp][lane] = count;
+  __syncthreads();
+  if (warp == 0 && i < n) {
+    uint32_t place = 0;
+#pragma unroll
+    for (int w = 0; w < kRankWarps; ++w) place += part[w][lane];
+    p.even[place] = make_uint2(mine, static_cast<uint32_t>(i));
+  }
+}
+
+// Zeros over `bytes` bytes at `begin`.  It runs beside the sort, which it does not
+// depend on, but ends after it, so that what follows has both.  (Filling only the rows
+// without tokens, beside the sums, gained nothing: the sums' few dependent loads wait
+// behind its stores.)
+constexpr int kFillThreads = 256;
+__global__ void __launch_bounds__(kFillThreads) embed_fill_kernel(char* begin, int64_t bytes) {
+  release_next();
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * kFillThreads + threadIdx.x;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kFillThreads;
+  int64_t before = (16 - reinterpret_cast<uintptr_t>(begin) % 16) % 16;
+  if (before > bytes) before = bytes;
+  const int64_t n = (bytes - before) / 16, after = bytes - before - 16 * n;
+  uint4* body = reinterpret_cast<uint4*>(begin + before);
+#pragma unroll 8
+  for (int64_t i = first; i < n; i += step) body[i] = make_uint4(0, 0, 0, 0);
+  if (first < before) begin[first] = 0;
+  if (first < after) begin[before + 16 * n + first] = 0;
+  wait_previous();
+}
+
 // ---- sums -------------------------------------------------------------------------
 constexpr int kSumThreads = 128;
 
@@ -258,66 +331,13 @@ struct SumArgs {
   int window;           // tokens per warp
   int slabs;
   float scale;
-  const int64_t* ids;   // for the rows that no token names
-  int64_t ignore;
-  int fills;            // CTAs that fill those with zeros
 };
 
 // A lane's columns of a slab: G groups of VEC, a warp's width apart.
 template <int VEC> struct Slab {
-  static constexpr int kGroups = VEC == 1 ? 4 : 1;
+  static constexpr int kGroups = VEC == 1 ? 2 : 1;
   static constexpr int kWidth = 32 * VEC * kGroups;
 };
-
-// The first place from `i` on, below n, whose bit is `set`; n if there is none.
-__device__ __forceinline__ int next_bit(const uint32_t* bits, int i, int n, bool set) {
-  while (i < n) {
-    const uint32_t w = (set ? bits[i / 32] : ~bits[i / 32]) >> (i % 32);
-    if (w) {
-      i += __ffs(w) - 1;
-      break;
-    }
-    i = (i / 32 + 1) * 32;
-  }
-  return i < n ? i : n;
-}
-
-// Zeros over the rows of dW that no token names, kFillRows at a time: those that one
-// does are marked first, from all of the ids.  None of this needs the sort.
-constexpr int kFillRows = 16384;
-template <typename W>
-__device__ __forceinline__ void fill_rows(const SumArgs& p, uint32_t (&named)[kFillRows / 32]) {
-  const int64_t v0 = p.vocab * blockIdx.x / p.fills, v1 = p.vocab * (blockIdx.x + 1) / p.fills;
-  constexpr int kPer = 16 / sizeof(W);
-  for (int64_t r0 = v0; r0 < v1; r0 += kFillRows) {
-    const int n = v1 - r0 < kFillRows ? static_cast<int>(v1 - r0) : kFillRows;
-    for (int i = threadIdx.x; i < (n + 31) / 32; i += kSumThreads) named[i] = 0;
-    __syncthreads();
-#pragma unroll 8
-    for (int64_t t = threadIdx.x; t < p.tokens; t += kSumThreads) {
-      const int64_t id = __ldg(p.ids + t);
-      const int64_t r = id - r0;
-      if (r >= 0 && r < n && id != p.ignore) atomicOr(named + r / 32, 1u << (r % 32));
-    }
-    __syncthreads();
-    // stretches of rows without a mark
-    for (int a = 0, end; (a = next_bit(named, a, n, false)) < n; a = end) {
-      end = next_bit(named, a, n, true);
-      W* begin = static_cast<W*>(p.dweight) + (r0 + a) * p.dim;
-      const int64_t size = (end - a) * p.dim;
-      // from a boundary of 128 bytes on: stores across it leave parts of sectors
-      int64_t head = (128 - reinterpret_cast<uintptr_t>(begin) % 128) % 128 / sizeof(W);
-      head = head < size ? head : size;
-      const int64_t body = (size - head) / kPer, tail = head + body * kPer;
-      uint4* q = reinterpret_cast<uint4*>(begin + head);
-#pragma unroll 8
-      for (int64_t i = threadIdx.x; i < body; i += kSumThreads) q[i] = make_uint4(0, 0, 0, 0);
-      if (threadIdx.x < head) begin[threadIdx.x] = W(0.f);
-      if (tail + threadIdx.x < size) begin[tail + threadIdx.x] = W(0.f);
-    }
-    __syncthreads();
-  }
-}
 
 // A lane's columns of dW's row as it is, for `add`.
 template <typename W, int VEC, int G>
@@ -369,24 +389,14 @@ constexpr int kSumWarps = kSumThreads / 32;
 template <typename W, typename O, int VEC, bool ADD>
 __global__ void __launch_bounds__(kSumThreads) embed_sum_kernel(const SumArgs p) {
   constexpr int G = Slab<VEC>::kGroups;
-  constexpr int kAhead = 8;
-  constexpr int kParts = 2 * kSumWarps * 32 * G * VEC;
-  __shared__ __align__(16) union {
-    float part[kSumWarps][2][G * VEC][32];
-    uint32_t named[kFillRows / 32];
-  } sm;
-  static_assert(sizeof(float) * kParts == sizeof(sm.part), "one float per lane and column");
+  constexpr int kAhead = 4;
+  __shared__ float part[kSumWarps][2][G * VEC][32];
   __shared__ uint32_t tail_id[kSumWarps];
   __shared__ unsigned char has_tail[kSumWarps], whole[kSumWarps];
   release_next();
-  if (!ADD && static_cast<int>(blockIdx.x) < p.fills) {
-    fill_rows<W>(p, sm.named);
-    wait_previous();
-    return;
-  }
   wait_previous();
+  const int64_t unit = blockIdx.x;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t unit = static_cast<int64_t>(blockIdx.x) - (ADD ? 0 : p.fills);
   const int64_t set = unit / p.slabs, w = set * kSumWarps + warp;
   const int64_t c0 = (unit - set * p.slabs) * Slab<VEC>::kWidth + lane * VEC;
   const int64_t i0 = w * p.window;
@@ -401,7 +411,7 @@ __global__ void __launch_bounds__(kSumThreads) embed_sum_kernel(const SumArgs p)
 #pragma unroll
     for (int g = 0; g < G; ++g)
 #pragma unroll
-      for (int v = 0; v < VEC; ++v) sm.part[warp][which][g * VEC + v][lane] = acc[g][v];
+      for (int v = 0; v < VEC; ++v) part[warp][which][g * VEC + v][lane] = acc[g][v];
   };
   const bool begun = i0 > 0 && i0 < i1 && __ldg(p.sorted + i0 - 1).x == __ldg(p.sorted + i0).x;
   bool head = begun, goes = false;  // the run in hand began before; the last one goes on
@@ -472,13 +482,13 @@ __global__ void __launch_bounds__(kSumThreads) embed_sum_kernel(const SumArgs p)
 #pragma unroll
     for (int g = 0; g < G; ++g)
 #pragma unroll
-      for (int v = 0; v < VEC; ++v) acc[g][v] += sm.part[of][0][g * VEC + v][lane];
+      for (int v = 0; v < VEC; ++v) acc[g][v] += part[of][0][g * VEC + v][lane];
   };
   const auto take = [&](int which) {
 #pragma unroll
     for (int g = 0; g < G; ++g)
 #pragma unroll
-      for (int v = 0; v < VEC; ++v) acc[g][v] = sm.part[warp][which][g * VEC + v][lane];
+      for (int v = 0; v < VEC; ++v) acc[g][v] = part[warp][which][g * VEC + v][lane];
   };
   if (warp == 0 && begun) {  // a run from before the CTA's windows
     take(0);
@@ -596,7 +606,7 @@ cudaError_t sum(SumArgs a, cudaStream_t s) {
   a.slabs = static_cast<int>((a.dim + Slab<VEC>::kWidth - 1) / Slab<VEC>::kWidth);
   const int64_t units = a.windows * a.slabs;
   const cudaError_t e = launch_after(embed_sum_kernel<W, O, VEC, ADD>,
-                                     static_cast<unsigned>(units + (ADD ? 0 : a.fills)), kSumThreads, 0, s, a);
+                                     static_cast<unsigned>(units), kSumThreads, 0, s, a);
   if (e != cudaSuccess) return e;
   const int64_t ctas = (units + kSumWarps - 1) / kSumWarps;
   return launch_after(embed_join_kernel<W, VEC, ADD>, static_cast<unsigned>(ctas), kSumThreads, 0, s, a);
@@ -675,8 +685,23 @@ cudaError_t launch_embed_bwd(const EmbedBwdParams& p, bool bf16, bool io_bf16, c
   while ((p.vocab >> bits) > 0) ++bits;  // ids, and `vocab` for the tokens that are left out
   a.passes = (bits + kDigitBits - 1) / kDigitBits;
   a.bits = (bits + a.passes - 1) / a.passes;
-  const cudaError_t e = sort(a, s);
+  cudaError_t e;
+  if (p.tokens <= kRankMost) {
+    a.passes = 1;
+    const int64_t ctas = (p.tokens + kRankTokens - 1) / kRankTokens;
+    embed_rank_kernel<<<static_cast<unsigned>(ctas), kRankWarps * 32, 0, s>>>(a);
+    e = cudaGetLastError();
+  } else {
+    e = sort(a, s);
+  }
   if (e != cudaSuccess) return e;
+  if (!p.add) {
+    const int64_t bytes = p.vocab * p.dim * (bf16 ? 2 : 4);
+    const int64_t need = bytes / (16 * kFillThreads) + 1, most = int64_t(kSms) * 8;
+    e = launch_after(embed_fill_kernel, static_cast<unsigned>(need < most ? need : most),
+                     kFillThreads, 0, s, static_cast<char*>(p.dweight), bytes);
+    if (e != cudaSuccess) return e;
+  }
   SumArgs b = {};
   b.sorted = a.passes & 1 ? a.even : a.odd;
   b.dy = p.dy; b.dweight = p.dweight;
@@ -684,14 +709,6 @@ cudaError_t launch_embed_bwd(const EmbedBwdParams& p, bool bf16, bool io_bf16, c
   b.tokens = p.tokens; b.vocab = p.vocab; b.dim = p.dim;
   b.windows = l.windows; b.window = l.window;
   b.scale = p.scale;
-  b.ids = p.ids; b.ignore = p.ignore;
-  // CTAs to fill: of 32 KB each at least, and of twice what reading the ids costs
-  // them, but one per SM
-  const int64_t bytes = p.vocab * p.dim * (bf16 ? 2 : 4);
-  int64_t fills = bytes / (16 * p.tokens + 32768) + 1;
-  fills = fills < kSms ? (bytes / 32768 < kSms ? bytes / 32768 + 1 : kSms) : fills;
-  fills = fills < 3 * kSms ? fills : 3 * kSms;
-  b.fills = static_cast<int>(fills < p.vocab ? fills : p.vocab);
   const auto pick = [&](auto* onto, auto* fresh) { return p.add ? onto(b, s) : fresh(b, s); };
   if (!bf16)
     return wide ? pick(sum<float, float, 4, true>, sum<float, float, 4, false>)
