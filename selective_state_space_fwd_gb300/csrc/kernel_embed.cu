@@ -12,7 +12,7 @@
 //    columns, adds the rows of each run of equal ids in fp32 and writes the runs
 //    that lie in the window.  A run that another window shares leaves a partial
 //    sum: `head` where it began before the window, `tail` where it began in it.
-// 3. A warp per window and slab adds a tail and the heads that follow, in order.
+// 3. A CTA per window and slab adds a tail and the heads that follow, in order.
 // A frequent token is thus summed by many warps; reads and writes are dy once, dW
 // once, and per window two rows of fp32.
 #include <cuda_bf16.h>
@@ -514,48 +514,63 @@ __global__ void __launch_bounds__(kSumThreads) embed_sum_kernel(const SumArgs p)
   }
 }
 
+// A CTA takes the run that its windows' last tokens began, for one slab; its warps
+// share the heads.
 template <typename W, int VEC, bool ADD>
 __global__ void __launch_bounds__(kSumThreads) embed_join_kernel(const SumArgs p) {
   constexpr int G = Slab<VEC>::kGroups;
-  const int lane = threadIdx.x & 31;
+  __shared__ float part[kSumWarps][G * VEC][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   wait_previous();
-  const int64_t u = static_cast<int64_t>(blockIdx.x) * (kSumThreads / 32) + (threadIdx.x >> 5);
-  const int64_t w = u / p.slabs, width = static_cast<int64_t>(p.window) * kSumWarps;
-  if (w + 1 >= p.windows) return;
-  const int64_t i1 = (w + 1) * width;
-  const uint32_t id = __ldg(p.sorted + i1 - 1).x;
-  // the window's last run began in it and goes on
-  if (id >= p.vocab || __ldg(p.sorted + i1).x != id) return;
-  const int64_t i0 = w * width;
-  if (i0 > 0 && __ldg(p.sorted + i0).x == id && __ldg(p.sorted + i0 - 1).x == id) return;
-  const int64_t c0 = (u - w * p.slabs) * Slab<VEC>::kWidth + lane * VEC;
+  const int64_t set = blockIdx.x / p.slabs, width = static_cast<int64_t>(p.window) * kSumWarps;
+  const int64_t i0 = set * width, i1 = i0 + width;
+  if (set + 1 >= p.windows) return;
+  const uint32_t id = __ldg(p.sorted + i1 - 1).x, next = __ldg(p.sorted + i1).x;
+  const uint32_t first = __ldg(p.sorted + i0).x, before = i0 > 0 ? __ldg(p.sorted + i0 - 1).x : ~id;
+  // the last run goes on, and began in these windows
+  if (id >= p.vocab || next != id || (first == id && before == id)) return;
+  const int64_t c0 = (blockIdx.x - set * p.slabs) * Slab<VEC>::kWidth + lane * VEC;
+  int64_t n = 0;  // heads
+  for (unsigned stop = 0; !stop;) {
+    const int64_t j = set + 1 + n + lane;
+    stop = ~__ballot_sync(0xffffffffu, j < p.windows && __ldg(p.sorted + j * width).x == id);
+    n += stop ? __ffs(stop) - 1 : 32;
+  }
+  const int64_t share = (n + kSumWarps - 1) / kSumWarps;
+  const int64_t h0 = warp * share, h1 = h0 + share < n ? h0 + share : n;
   float acc[G][VEC];
+#pragma unroll
+  for (int g = 0; g < G; ++g)
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) acc[g][v] = 0.f;
+  const auto add = [&](int64_t slot) {
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      const int64_t c = c0 + g * 32 * VEC;
+      if (c >= p.dim) continue;
+      float f[VEC];
+      load_f<float, VEC>(p.part + slot * p.dim + c, f);
+      vadd<VEC>(acc[g], acc[g], f);
+    }
+  };
+  if (warp == 0) add(2 * set + 1);  // the tail
+#pragma unroll 4
+  for (int64_t h = h0; h < h1; ++h) add(2 * (set + 1 + h));
+  if (warp > 0) {
+#pragma unroll
+    for (int g = 0; g < G; ++g)
+#pragma unroll
+      for (int v = 0; v < VEC; ++v) part[warp][g * VEC + v][lane] = acc[g][v];
+  }
+  __syncthreads();
+  if (warp > 0) return;
   Raw<W, VEC> old[G];
   if (ADD) there<W, VEC, G>(p, id, c0, old);
+  for (int w = 1; w < kSumWarps; ++w) {
 #pragma unroll
-  for (int g = 0; g < G; ++g) {
-    const int64_t c = c0 + g * 32 * VEC;
-    if (c < p.dim) load_f<float, VEC>(p.part + (2 * w + 1) * p.dim + c, acc[g]);
-  }
-  for (int64_t j = w + 1;;) {
-    const int64_t mine = j + lane;
-    const bool goes = mine < p.windows && __ldg(p.sorted + mine * width).x == id;
-    const unsigned stop = ~__ballot_sync(0xffffffffu, goes);
-    const int n = stop ? __ffs(stop) - 1 : 32;
-#pragma unroll 8
-    for (int i = 0; i < n; ++i) {
+    for (int g = 0; g < G; ++g)
 #pragma unroll
-      for (int g = 0; g < G; ++g) {
-        const int64_t c = c0 + g * 32 * VEC;
-        if (c >= p.dim) continue;
-        float f[VEC];
-        load_f<float, VEC>(p.part + 2 * (j + i) * p.dim + c, f);
-#pragma unroll
-        for (int v = 0; v < VEC; ++v) acc[g][v] += f[v];
-      }
-    }
-    j += n;
-    if (n < 32) break;
+      for (int v = 0; v < VEC; ++v) acc[g][v] += part[w][g * VEC + v][lane];
   }
   write_row<W, VEC, G, ADD>(p, id, c0, acc, old);
 }
@@ -608,8 +623,7 @@ cudaError_t sum(SumArgs a, cudaStream_t s) {
   const cudaError_t e = launch_after(embed_sum_kernel<W, O, VEC, ADD>,
                                      static_cast<unsigned>(units), kSumThreads, 0, s, a);
   if (e != cudaSuccess) return e;
-  const int64_t ctas = (units + kSumWarps - 1) / kSumWarps;
-  return launch_after(embed_join_kernel<W, VEC, ADD>, static_cast<unsigned>(ctas), kSumThreads, 0, s, a);
+  return launch_after(embed_join_kernel<W, VEC, ADD>, static_cast<unsigned>(units), kSumThreads, 0, s, a);
 }
 
 // Sorts with one thread per token, but in at most kSortCtas CTAs (8 where the GPU has
