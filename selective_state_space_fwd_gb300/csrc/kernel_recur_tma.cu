@@ -150,8 +150,8 @@ __device__ __forceinline__ void boxes_free() {
   __syncwarp();
 }
 
-// The maps of a round's tiles meet in every CTA of the cluster: warp 0 of each sends
-// its tile's to all (itself too), and the bytes arrive on the receiver's mbarrier, so
+// The maps of a round's tiles meet in every CTA of the cluster: each sends its tile's to
+// all (itself too), the warps to some CTAs each, and the bytes arrive on the receiver's mbarrier, so
 // that no CTA waits for more than the maps.  A CTA sends round i + 1 before it reads
 // round i (it folds the next tile meanwhile), but after it has read round i - 1, for
 // which all had sent theirs, after reading round i - 3: four buffers are enough.
@@ -164,13 +164,13 @@ struct Exchange {
     if (threadIdx.x == 0)
       for (int k = 0; k < kBuffers; ++k) umma::mbar_init(bars + 8 * k, 1);
   }
-  __device__ __forceinline__ void send(int i, const Map<V>& m) const {  // warp 0
+  template <int W>  // the warps below `size` call it
+  __device__ __forceinline__ void send(int i, const Map<V>& m) const {
     const int lane = threadIdx.x & 31, k = i % kBuffers;
     const uint32_t bar = bars + 8 * k;
-    if (lane == 0) umma::mbar_expect_tx(bar, size * 32 * sizeof(Map<V>));
-    __syncwarp();
+    if (threadIdx.x == 0) umma::mbar_expect_tx(bar, size * 32 * sizeof(Map<V>));
     const uint32_t mine = umma::smem_u32(&slots[k * size + rank][lane]);
-    for (uint32_t r = 0; r < size; ++r) {
+    for (uint32_t r = threadIdx.x / 32; r < size; r += W) {
       const uint32_t to = pair::map_to(mine, r), on = pair::map_to(bar, r);
       if constexpr (V == 1)
         asm volatile(
@@ -347,11 +347,11 @@ __global__ void __launch_bounds__(W * 32)
     __syncthreads();
     if (threadIdx.x == 0) load(i + kSlots, ring.at);
     ring.next();
-    if (CLUSTER && warp == 0) {
+    if (CLUSTER && warp < size) {
       Map<V> all = Map<V>::none();
 #pragma unroll
       for (int w = 0; w < W; ++w) all.then(maps[i % 3][w][lane]);
-      cluster.send(i, all);
+      cluster.template send<W>(i, all);
     }
   };
   Steps<V> now, next;
@@ -557,11 +557,11 @@ __global__ void __launch_bounds__(W * 32)
     };
     float mi[V];
     if (CLUSTER) {
-      if (warp == 0) {
+      if (warp < size) {
         Map<V> all = Map<V>::none();
 #pragma unroll
         for (int w = W - 1; w >= 0; --w) all.then(back(w));
-        cluster.send(i, all);
+        cluster.template send<W>(i, all);
       }
       if (!bad && !cluster.wait(i)) bad = true;
       cluster.pass(i, m, mi);
