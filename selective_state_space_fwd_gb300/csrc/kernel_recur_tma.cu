@@ -263,8 +263,9 @@ template <int V> struct Steps { float g[kSteps][V], u[kSteps][V]; };
 template <typename T, int V>
 __device__ __forceinline__ Map<V> fold(Steps<V>& t, uint32_t at, uint32_t far, int left,
                                        const float (&keep)[V]) {
+  if (left <= 0) return Map<V>::none();
   if (left < kSteps) {  // closed gates past the valid steps
-    for (int s = left < 0 ? 0 : left; s < kSteps; ++s) {
+    for (int s = left; s < kSteps; ++s) {
       sts(at + s * kRow, closed<T>());
       sts(at + far + s * kRow, 0u);
     }
@@ -383,12 +384,14 @@ __global__ void __launch_bounds__(W * 32)
         for (int v = 0; v < V; ++v) states[t0 / kRecurChunk * p.dim + v] = in[v];
       }
       boxes_free();
+      if (left > 0) {
 #pragma unroll
-      for (int s = 0; s < kSteps; ++s) {
-        float o[V];
-        minus<V>(o, in, now.u[s]);
-        vfma<V>(in, now.g[s], o, in);
-        sts(out + s * kRow + lane * 4, pack(in));
+        for (int s = 0; s < kSteps; ++s) {
+          float o[V];
+          minus<V>(o, in, now.u[s]);
+          vfma<V>(in, now.g[s], o, in);
+          sts(out + s * kRow + lane * 4, pack(in));
+        }
       }
       if (left < kSteps) {
         for (int s = left < 0 ? 0 : left; s < kSteps; ++s) sts(out + s * kRow + lane * 4, 0u);
@@ -496,8 +499,8 @@ __global__ void __launch_bounds__(W * 32)
     for (int v = 0; v < V; ++v)
       h[v] = here ? __ldg(states + static_cast<int64_t>(tile) * (kTile / kRecurChunk) * p.dim + v) : 0.f;
     if (here && !bad && !ring.wait()) bad = true;
-    if (left < kSteps) {
-      for (int s = left < 0 ? 0 : left; s < kSteps; ++s) {
+    if (left > 0 && left < kSteps) {
+      for (int s = left; s < kSteps; ++s) {
         sts(row + s * kRow, closed<T>());
         sts(row + W * kBox + s * kRow, 0u);
         sts(row + 2 * W * kBox + s * kRow, 0u);
@@ -509,35 +512,37 @@ __global__ void __launch_bounds__(W * 32)
     float ml[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) ml[v] = 0.f;
+    if (left > 0) {
 #pragma unroll
-    for (int s = 0; s < kSteps; ++s) {
-      float e[V], o[V], w[V], bs[V];
-      unpack(lds(row + s * kRow), e);
-      unpack(lds(row + W * kBox + s * kRow), u[s]);
-      unpack(lds(row + 2 * W * kBox + s * kRow), l[s]);
-      vscale<V>(e, e, kLog2e);
+      for (int s = 0; s < kSteps; ++s) {
+        float e[V], o[V], w[V], bs[V];
+        unpack(lds(row + s * kRow), e);
+        unpack(lds(row + W * kBox + s * kRow), u[s]);
+        unpack(lds(row + 2 * W * kBox + s * kRow), l[s]);
+        vscale<V>(e, e, kLog2e);
 #pragma unroll
-      for (int v = 0; v < V; ++v) e[v] = ex2(e[v]);
+        for (int v = 0; v < V; ++v) e[v] = ex2(e[v]);
 #pragma unroll
-      for (int v = 0; v < V; ++v) o[v] = 1.f;
-      vadd<V>(o, e, o);
+        for (int v = 0; v < V; ++v) o[v] = 1.f;
+        vadd<V>(o, e, o);
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        open[s][v] = rcp(o[v]);
-        e[v] = recur::within(e[v]);
+        for (int v = 0; v < V; ++v) {
+          open[s][v] = rcp(o[v]);
+          e[v] = recur::within(e[v]);
+        }
+        vmul<V>(hold[s], e, open[s]);
+        vmul<V>(bs, keep, open[s]);  // -b
+        minus<V>(w, map.e, u[s]);
+        vfma<V>(map.e, bs, w, map.e);
+        vfma<V>(map.p, bs, map.p, map.p);
       }
-      vmul<V>(hold[s], e, open[s]);
-      vmul<V>(bs, keep, open[s]);  // -b
-      minus<V>(w, map.e, u[s]);
-      vfma<V>(map.e, bs, w, map.e);
-      vfma<V>(map.p, bs, map.p, map.p);
-    }
 #pragma unroll
-    for (int s = kSteps - 1; s >= 0; --s) {
-      float lam[V], bs[V];
-      minus<V>(lam, ml, l[s]);
-      vmul<V>(bs, keep, open[s]);
-      vfma<V>(ml, bs, lam, lam);
+      for (int s = kSteps - 1; s >= 0; --s) {
+        float lam[V], bs[V];
+        minus<V>(lam, ml, l[s]);
+        vmul<V>(bs, keep, open[s]);
+        vfma<V>(ml, bs, lam, lam);
+      }
     }
     const int k = i & 1;
     past[k][warp][lane] = map;
@@ -581,34 +586,36 @@ __global__ void __launch_bounds__(W * 32)
 #pragma unroll
     for (int w = 0; w < W - 1; ++w)
       if (w < warp) past[k][w][lane].through(h);
-    // the distance of the value to the state before a step, in the value's place
-#pragma unroll
-    for (int s = 0; s < kSteps; ++s) {
-      float bs[V];
-      vmul<V>(bs, keep, open[s]);
-      minus<V>(u[s], h, u[s]);
-      vfma<V>(h, bs, u[s], h);
-    }
     boxes_free();
-    float some[V];
+    if (left > 0) {
+      // the distance of the value to the state before a step, in the value's place
 #pragma unroll
-    for (int v = 0; v < V; ++v) some[v] = 0.f;
+      for (int s = 0; s < kSteps; ++s) {
+        float bs[V];
+        vmul<V>(bs, keep, open[s]);
+        minus<V>(u[s], h, u[s]);
+        vfma<V>(h, bs, u[s], h);
+      }
+      float some[V];
 #pragma unroll
-    for (int s = kSteps - 1; s >= 0; --s) {
-      float bs[V], lam[V], o[V];
-      vmul<V>(bs, keep, open[s]);
-      minus<V>(lam, mi, l[s]);
-      vfma<V>(mi, bs, lam, lam);
-      vmul<V>(o, bs, lam);
-      sts(out + s * kRow + lane * 4, pack(o));
-      vmul<V>(lam, lam, u[s]);
-      vfma<V>(some, lam, open[s], some);
-      vmul<V>(bs, bs, hold[s]);
-      vmul<V>(o, lam, bs);
-      sts(out + kBox + s * kRow + lane * 4, pack(o));
+      for (int v = 0; v < V; ++v) some[v] = 0.f;
+#pragma unroll
+      for (int s = kSteps - 1; s >= 0; --s) {
+        float bs[V], lam[V], o[V];
+        vmul<V>(bs, keep, open[s]);
+        minus<V>(lam, mi, l[s]);
+        vfma<V>(mi, bs, lam, lam);
+        vmul<V>(o, bs, lam);
+        sts(out + s * kRow + lane * 4, pack(o));
+        vmul<V>(lam, lam, u[s]);
+        vfma<V>(some, lam, open[s], some);
+        vmul<V>(bs, bs, hold[s]);
+        vmul<V>(o, lam, bs);
+        sts(out + kBox + s * kRow + lane * 4, pack(o));
+      }
+#pragma unroll
+      for (int v = 0; v < V; ++v) dfloor[v] -= some[v];
     }
-#pragma unroll
-    for (int v = 0; v < V; ++v) dfloor[v] -= some[v];
     if (left < kSteps) {
       for (int s = left < 0 ? 0 : left; s < kSteps; ++s) {
         sts(out + s * kRow + lane * 4, 0u);
@@ -779,9 +786,10 @@ cudaError_t go(const RecurParams& p, bool bf16, int size, cudaStream_t s, const 
 // Warps per CTA.  Forward: 8 (fp32 8 x 4096 x 1024 62 us, with 4 68 us; bf16 40 and
 // 55 us).  Backward: 8 with two channels per lane and 4 otherwise (bf16 59 and 73 us,
 // fp32 106 and 101 us), but 4 in clusters (bf16 2 x 32768 x 2048 235 and 271 us).
-template <typename T>
+// Short sequences take as few warps as hold them (bf16 1024 x 16 x 768 with 8 and 8:
+// 100 and 249 us).
+template <typename T, int W>
 cudaError_t fwd(const RecurParams& p, unsigned* err, cudaStream_t s) {
-  constexpr int W = 8;
   constexpr bool bf16 = sizeof(T) == 2;
   using M = FwdMem<T, W>;
   const Axes g = axes_of(p, p.gate_batch, p.gate_step), v = axes_of(p, p.value_batch, p.value_step);
@@ -789,13 +797,22 @@ cudaError_t fwd(const RecurParams& p, unsigned* err, cudaStream_t s) {
   if (!map_of(&mg, bf16, p.gate, p, g, W * kSteps) || !map_of(&mv, bf16, p.value, p, v, W * kSteps) ||
       !map_of(&my, bf16, p.y, p, dense(p), kSteps))
     return cudaErrorInvalidValue;
-  constexpr auto shared = recur_fwd_tma_kernel<T, W, true>, alone = recur_fwd_tma_kernel<T, W, false>;
-  const cudaError_t e = allow<shared, M>(kMaxCluster);
-  if (e != cudaSuccess) return e;
-  const int size = cluster_of<shared, M, W>(p, units_of(p, bf16));
-  const TmaArgs a = {static_cast<uint32_t>(size), g.time_last, v.time_last, err};
-  return size > 1 ? go<shared, M, W>(p, bf16, size, s, mg, mv, my, p, a)
-                  : go<alone, M, W>(p, bf16, 1, s, mg, mv, my, p, a);
+  TmaArgs a = {1, g.time_last, v.time_last, err};
+  if constexpr (W == 8) {
+    constexpr auto shared = recur_fwd_tma_kernel<T, W, true>;
+    const cudaError_t e = allow<shared, M>(kMaxCluster);
+    if (e != cudaSuccess) return e;
+    const int size = cluster_of<shared, M, W>(p, units_of(p, bf16));
+    a.size = static_cast<uint32_t>(size);
+    if (size > 1) return go<shared, M, W>(p, bf16, size, s, mg, mv, my, p, a);
+  }
+  return go<recur_fwd_tma_kernel<T, W, false>, M, W>(p, bf16, 1, s, mg, mv, my, p, a);
+}
+
+template <typename T>
+cudaError_t fwd_any(const RecurParams& p, unsigned* err, cudaStream_t s) {
+  if (p.seqlen <= kSteps) return fwd<T, 1>(p, err, s);
+  return p.seqlen <= 4 * kSteps ? fwd<T, 4>(p, err, s) : fwd<T, 8>(p, err, s);
 }
 
 template <typename T, int W, bool CLUSTER>
@@ -817,6 +834,9 @@ cudaError_t bwd(const RecurBwdParams& q, int size, unsigned* err, cudaStream_t s
 template <typename T>
 cudaError_t bwd_any(const RecurBwdParams& q, unsigned* err, int* size, cudaStream_t s) {
   constexpr bool bf16 = sizeof(T) == 2;
+  *size = 1;
+  if (q.fwd.seqlen <= kSteps) return bwd<T, 1, false>(q, 1, err, s);
+  if (q.fwd.seqlen <= 4 * kSteps) return bwd<T, 4, false>(q, 1, err, s);
   const int64_t units = units_of(q.fwd, bf16);
   constexpr auto shared = recur_bwd_tma_kernel<T, 4, true>;
   const cudaError_t e = allow<shared, BwdMem<T, 4>>(kMaxCluster);
@@ -844,7 +864,7 @@ bool recur_bwd_tma_ok(const RecurBwdParams& q, bool bf16) {
 }
 
 cudaError_t launch_recur_fwd_tma(const RecurParams& p, bool bf16, unsigned* err, cudaStream_t s) {
-  return bf16 ? fwd<__nv_bfloat16>(p, err, s) : fwd<float>(p, err, s);
+  return bf16 ? fwd_any<__nv_bfloat16>(p, err, s) : fwd_any<float>(p, err, s);
 }
 
 cudaError_t launch_recur_bwd_tma(const RecurBwdParams& q, bool bf16, unsigned* err, int* parts,

@@ -92,6 +92,13 @@ CASES = [
     (40000, 3000, 2048, "zipf", 0.0),
     (66000, 700, 72, "one", 0.0),
     (300, 50, 6000, "zipf", 0.0),
+    (8191, 300, 64, "zipf", 0.1),    # up to 8192 tokens are placed by counting
+    (8192, 300, 72, "one", 0.0),
+    (8193, 511, 64, "any", 0.1),     # sorted by one digit, two, three
+    (9000, 512, 40, "zipf", 0.1),
+    (9000, 300000, 24, "any", 0.1),
+    (16385, 262144, 8, "any", 0.0),
+    (131073, 3, 8, "zipf", 0.5),
 ]
 
 
@@ -196,6 +203,23 @@ def test_the_same_every_time_and_with_dirty_workspaces():
     for fill in (0, 255):  # 255: NaN in every type
         ws = torch.full((1 << 27,), fill, dtype=torch.uint8, device="cuda")
         assert torch.equal(S.embed_bwd(t["ids"], t["dy"], vocab=900, workspace=ws), a)
+
+
+def test_two_streams_at_once():
+    """Calls on two streams, each with a workspace of its own, interleaved."""
+    ts = [make(20000, 3000, 256, seed=s) for s in (1, 2)]
+    want = [S.embed_bwd(t["ids"], t["dy"], vocab=3000) for t in ts]
+    streams = [torch.cuda.Stream() for _ in ts]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(5):
+        for i, (t, s) in enumerate(zip(ts, streams)):
+            with torch.cuda.stream(s):
+                got[i].append(S.embed_bwd(t["ids"], t["dy"], vocab=3000))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for g in got[i]:
+            assert torch.equal(g, want[i])
 
 
 def test_shapes_of_ids():

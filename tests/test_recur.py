@@ -150,6 +150,12 @@ CASES = [
     (1, 1100, 256, [77]),
     (24, 70, 1000, None),            # more CTAs than the GPU holds
     (40, 130, 512, [3 * i for i in range(40)]),
+    (300, 16, 72, None),             # short sequences: one warp per CTA
+    (70, 17, 72, [i % 18 for i in range(70)]),
+    (30, 61, 40, None),
+    (1, 3000, 32, [0]),              # a cluster with nothing, or one step, to do
+    (1, 3000, 32, [1]),
+    (33, 40, 64, [i for i in range(33)]),  # more rows than are sorted by their lengths
 ]
 
 
@@ -226,6 +232,33 @@ def test_masked_steps_take_no_part(dtype, B, L, D):
     empty = [i for i in range(B) if valid[i] == 0]
     assert torch.equal(clean["final"][empty], t["state0"][empty])
     assert torch.equal(clean["dstate0"][empty], t["dfinal"][empty])
+
+
+@pytest.mark.parametrize("D", [32, 33])
+def test_many_short_rows(D):
+    """More batch rows than a grid's second axis could hold."""
+    t = make("f32", 70000, 3, D, seed=14)
+    ref, got = reference(t), run(t)
+    for name in NAMES:
+        assert_close(got[name], ref, name)
+
+
+def test_two_streams_at_once():
+    """Calls on two streams, each with clusters and workspaces of its own, interleaved."""
+    ts = [make("bf16", 1, 4000, 64, carry=True, floor=True, seed=s) for s in (1, 2)]
+    want = [run(t) for t in ts]
+    streams = [torch.cuda.Stream() for _ in ts]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(5):
+        for i, (t, s) in enumerate(zip(ts, streams)):
+            with torch.cuda.stream(s):
+                got[i].append(run(t))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for g in got[i]:
+            for k in g:
+                assert torch.equal(g[k], want[i][k]), k
 
 
 def test_lengths_outside_the_sequence_are_clamped():
