@@ -522,7 +522,7 @@ typedef struct {
   int64_t dim;             /* >= 1, a multiple of 8 */
   int64_t top;             /* the teacher's entries per token, 1 .. 1024 */
   int64_t ignore_index;    /* entries whose id has this value take no part */
-  float temperature;       /* of both softmaxes; finite and > 0 */
+  float temperature;       /* of both softmaxes; finite, > 0 and not subnormal */
   ssm_dtype teacher_dtype; /* of the teacher's logits */
 } ssm_distill_shapes;
 
@@ -598,6 +598,7 @@ typedef struct {
  *   state0      : device fp32 [batch, dim] or NULL (zeros): h before the first step.
  *   out_y       : device, dtype `dtype`, [batch, seqlen, dim], contiguous.
  *   out_final   : device fp32 [batch, dim] or NULL: h after the last valid step.
+ *                 It may be `state0` itself (a state carried in place).
  *   out_states  : device fp32 [batch, ssm_recur_chunks(shapes), dim] or NULL: h
  *                 before every chunk of steps, for ssm_recur_bwd.
  * The state is fp32.  At most 2^31 - 1 (batch row, 32 channels) pairs.

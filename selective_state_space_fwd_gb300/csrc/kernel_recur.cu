@@ -141,7 +141,8 @@ __global__ void __launch_bounds__(kThreads, 2) recur_fwd_kernel(const RecurParam
 #pragma unroll
   for (int v = 0; v < VEC; ++v) {
     keep[v] = p.floor ? 1.f - __ldg(p.floor + d + v) : 1.f;
-    x[v] = p.state0 ? __ldg(p.state0 + at.b * p.dim + d + v) : 0.f;
+    // before the first barrier, and not as a constant: out_final may be the same memory
+    x[v] = p.state0 ? p.state0[at.b * p.dim + d + v] : 0.f;
   }
   Word gw[kSteps], vw[kSteps];
   int64_t t0 = static_cast<int64_t>(at.rank) * kTile + inside;

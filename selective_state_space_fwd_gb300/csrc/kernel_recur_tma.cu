@@ -346,7 +346,8 @@ __global__ void __launch_bounds__(W * 32)
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     keep[v] = p.floor ? __ldg(p.floor + at.d + v) - 1.f : -1.f;
-    x[v] = p.state0 ? __ldg(p.state0 + at.b * p.dim + at.d + v) : 0.f;
+    // before the first barrier, and not as a constant: out_final may be the same memory
+    x[v] = p.state0 ? p.state0[at.b * p.dim + at.d + v] : 0.f;
   }
   float* states = p.states
       ? p.states + at.b * ((p.seqlen + kRecurChunk - 1) / kRecurChunk) * p.dim + at.d

@@ -532,7 +532,8 @@ def recur_fwd(gate, value, floor=None, valid_len=None, *, state0=None, want_fina
     the state, whatever gate and value hold there.  state0: fp32 [batch, dim], h
     before the first step (zeros when None).  Returns ``(y, final, states)``: y
     [batch, L, dim] like gate, h of every step; final fp32 [batch, dim], from
-    which a next call or ``recur_step`` continues (None unless ``want_final``);
+    which a next call or ``recur_step`` continues (None unless ``want_final`` or
+    ``out_final``, which may be ``state0`` itself: a state carried in place);
     states fp32 [batch, chunks, dim], which ``recur_bwd`` needs (None unless
     ``want_states``)."""
     if stream is not None:

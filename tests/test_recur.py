@@ -360,6 +360,22 @@ def test_prompt_then_steps(dtype):
     assert_close(final, ref, "final")
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("B, L, D, valid", [
+    (2, 1, 64, None), (3, 40, 96, [40, 0, 1]), (1, 5000, 64, None), (2, 3000, 33, [2999, 0]), (40, 300, 256, None),
+])
+def test_a_state_is_carried_in_place(dtype, B, L, D, valid):
+    """state0 and out_final in the same memory: the bits of two tensors."""
+    t = make(dtype, B, L, D, floor=True, valid=valid, carry=True, seed=11)
+    a = (t["gate"], t["value"], t["floor"], t["valid"])
+    y, final, states = S.recur_fwd(*a, state0=t["state0"], want_final=True, want_states=True)
+    for _ in range(3):
+        carried = t["state0"].clone()
+        y1, same, states1 = S.recur_fwd(*a, state0=carried, out_final=carried, want_states=True)
+        assert same.data_ptr() == carried.data_ptr()
+        assert torch.equal(y1, y) and torch.equal(carried, final) and torch.equal(states1, states)
+
+
 def test_gradients_match_central_differences():
     """Against differences of the 64-bit definition (step 2^-10: truncation of order
     2^-20 of the third derivatives, each at most the sums of the absolute values
