@@ -2,6 +2,7 @@
 // include/ssmscan.h): argument validation and launch.  Every argument error is
 // found here, before anything is enqueued, and is returned as an ssm_status.
 #include <cuda_runtime.h>
+#include <float.h>
 #include <math.h>
 #include <stdint.h>
 
@@ -142,9 +143,8 @@ ssm_status check_distill(const ssm_distill_shapes* s) {
   const ssm_status st = check_xent(&x);
   if (st != SSM_OK) return st;
   if (!known(s->teacher_dtype)) return SSM_ERR_UNSUPPORTED;
-  if (s->top < 1 || !(s->temperature > 0.f) || isinf(s->temperature) ||
-      isinf(1.f / s->temperature))
-    return SSM_ERR_SHAPE;
+  // a subnormal one has no reciprocal, or none that log2(e) can scale
+  if (s->top < 1 || !(s->temperature >= FLT_MIN) || isinf(s->temperature)) return SSM_ERR_SHAPE;
   return s->top <= ssm::kDistillMaxTop ? SSM_OK : SSM_ERR_UNSUPPORTED;
 }
 

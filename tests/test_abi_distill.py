@@ -48,6 +48,7 @@ def _distill(fn="fwd", h=FAKE, w=FAKE, ids=FAKE, logits=FAKE, loss=FAKE, lse=FAK
     (dict(shapes=(4, 100, 64, 8, -100, float("nan"), 0)), E.ERR_SHAPE),
     (dict(shapes=(4, 100, 64, 8, -100, float("inf"), 0)), E.ERR_SHAPE),
     (dict(shapes=(4, 100, 64, 8, -100, 1e-40, 0)), E.ERR_SHAPE),
+    (dict(shapes=(4, 100, 64, 8, -100, 3e-39, 0)), E.ERR_SHAPE),  # 1/T is finite, log2(e)/T is not
     (dict(shapes=(4, 100, 60, 8, -100, 1.0, 0)), E.ERR_UNSUPPORTED),
     (dict(shapes=(4, 100, 64, 1025, -100, 1.0, 0)), E.ERR_UNSUPPORTED),
     (dict(shapes=(4, 100, 64, 8, -100, 1.0, 2)), E.ERR_UNSUPPORTED),
