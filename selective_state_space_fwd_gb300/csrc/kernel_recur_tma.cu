@@ -18,10 +18,10 @@
 //
 // Measured on GB300, forward and backward: fp32 8 x 4096 x 1024 62 and 101 us (6.4 and
 // 6.6 TB/s), bf16 39 and 59 us (5.2 and 5.7), both bound by HBM; bf16 2 x 32768 x 2048
-// in clusters of 4 137 and 235 us (5.9 and 5.7); bf16 prompts 32 x 2048 x 1536 with
+// in clusters of 4 132 and 233 us (6.1 and 5.8); bf16 prompts 32 x 2048 x 1536 with
 // valid lengths 68 us forward (in index order of the rows 74); fp32 1 x 65536 x 256 in
-// clusters of 16, 128 CTAs in all, 58 and 107 us (3.5 and 3.1 TB/s): a round of a
-// cluster takes 1.8 us, the latency of its dependent steps at two warps per scheduler.
+// clusters of 16, 128 CTAs in all, 49 and 107 us (4.1 and 3.1 TB/s): a round of a
+// cluster takes 1.5 us (backward 1.7), the latency of its dependent steps.
 // With the cluster's own barrier in place of the exchange these last took 106 and 219
 // us, and with all of a round's latency in the open 92 us forward.
 #include <cuda.h>
@@ -81,6 +81,18 @@ __device__ __forceinline__ void minus(float (&d)[V], const float (&a)[V], const 
   for (int v = 0; v < V; ++v) m[v] = -1.f;
   vfma<V>(d, b, m, a);
 }
+// Waits for a phase of an mbarrier that this CTA alone arrives on; false after kWaitNs.
+__device__ __forceinline__ bool wait_here(uint32_t bar, uint32_t parity) {
+  uint64_t t0 = 0;
+  for (;;) {
+    if (umma::mbar_wait(bar, parity, 64)) return true;
+    uint64_t t;
+    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+    if (t0 == 0) t0 = t;
+    else if (t - t0 > kWaitNs) return false;
+  }
+}
+
 // A lane's 2 V floats in shared memory: (P, e) of its channels.
 template <int V> struct alignas(8 * V) Map {
   float p[V], e[V];
@@ -166,8 +178,8 @@ __device__ __forceinline__ void boxes_free() {
 }
 
 // The maps of a round's tiles meet in every CTA of the cluster: each sends its tile's to
-// all (itself too), the warps to some CTAs each, and the bytes arrive on the receiver's mbarrier, so
-// that no CTA waits for more than the maps.  A CTA sends round i + 1 before it reads
+// all (itself too), and the bytes arrive on the receiver's mbarrier, so that no CTA
+// waits for more than the maps.  A CTA sends round i + 1 before it reads
 // round i (it folds the next tile meanwhile), but after it has read round i - 1, for
 // which all had sent theirs, after reading round i - 3: four buffers are enough.
 constexpr int kBuffers = 4;
@@ -179,13 +191,13 @@ struct Exchange {
     if (threadIdx.x == 0)
       for (int k = 0; k < kBuffers; ++k) umma::mbar_init(bars + 8 * k, 1);
   }
-  template <int W>  // the warps below `size` call it
-  __device__ __forceinline__ void send(int i, const Map<V>& m) const {
+  // To the CTAs from `first` on, a `step` apart; 0 is among one warp's.
+  __device__ __forceinline__ void send(int i, const Map<V>& m, uint32_t first, uint32_t step) const {
     const int lane = threadIdx.x & 31, k = i % kBuffers;
     const uint32_t bar = bars + 8 * k;
-    if (threadIdx.x == 0) umma::mbar_expect_tx(bar, size * 32 * sizeof(Map<V>));
+    if (first == 0 && lane == 0) umma::mbar_expect_tx(bar, size * 32 * sizeof(Map<V>));
     const uint32_t mine = umma::smem_u32(&slots[k * size + rank][lane]);
-    for (uint32_t r = threadIdx.x / 32; r < size; r += W) {
+    for (uint32_t r = first; r < size; r += step) {
       const uint32_t to = pair::map_to(mine, r), on = pair::map_to(bar, r);
       if constexpr (V == 1)
         asm volatile(
@@ -225,6 +237,40 @@ struct Exchange {
   }
 };
 
+// What the warps of a CTA and the two beside them that deal with the cluster hand
+// over: every warp's map of a round, by `full`, and the state that enters the CTA's
+// tile, by `known`.  Two barriers of each are enough: a warp gives the map of round i + 2
+// after it has taken the state of round i, which both helpers' parts in round i precede.
+template <int V>
+struct Handover {
+  uint32_t bars;
+  float (*state)[32][V];  // [2][32]
+  __device__ __forceinline__ void init(int warps) const {
+    if (threadIdx.x == 0)
+      for (int k = 0; k < 2; ++k) {
+        umma::mbar_init(bars + 8 * k, warps);
+        umma::mbar_init(bars + 16 + 8 * k, 1);
+      }
+  }
+  __device__ __forceinline__ void arrive(uint32_t bar) const {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) umma::mbar_arrive(bar);
+  }
+  __device__ __forceinline__ void map_given(int i) const { arrive(bars + 8 * (i & 1)); }
+  __device__ __forceinline__ bool maps(int i) const { return wait_here(bars + 8 * (i & 1), (i >> 1) & 1); }
+  __device__ __forceinline__ void publish(int i, const float (&x)[V]) const {
+#pragma unroll
+    for (int v = 0; v < V; ++v) state[i & 1][threadIdx.x & 31][v] = x[v];
+    arrive(bars + 16 + 8 * (i & 1));
+  }
+  __device__ __forceinline__ bool take(int i, float (&x)[V]) const {
+    const bool ok = wait_here(bars + 16 + 8 * (i & 1), (i >> 1) & 1);
+#pragma unroll
+    for (int v = 0; v < V; ++v) x[v] = state[i & 1][threadIdx.x & 31][v];
+    return ok;
+  }
+};
+
 // Where a CTA stands.
 template <typename T>
 struct Place {
@@ -256,11 +302,12 @@ template <typename T, int W, int NT, int NO, int MAPS>
 struct Mem {
   static constexpr int V = Of<T>::kVec;
   static constexpr uint32_t kBars = 0, kShared = 8 * kSlots;  // the cluster's barriers
-  static constexpr uint32_t kMaps = 128;
+  static constexpr uint32_t kHand = kShared + 8 * kBuffers, kState = 128;  // the helpers'
+  static constexpr uint32_t kMaps = kState + 2 * 32 * V * sizeof(float);
   static constexpr uint32_t kOut = kMaps + MAPS;
   static constexpr uint32_t kIn = kOut + NO * W * kBox;
   static constexpr uint32_t kTiles = kIn + kSlots * NT * W * kBox;
-  static_assert(kShared + 8 * kBuffers <= kMaps && MAPS % 128 == 0, "layout");
+  static_assert(kHand + 32 <= kState && MAPS % 128 == 0, "layout");
   static uint32_t bytes(int size) {
     const uint32_t tile = 32 * static_cast<uint32_t>(sizeof(Map<V>));
     return kTiles + (size > 1 ? kBuffers * size * tile : 0) + 128;
@@ -268,8 +315,9 @@ struct Mem {
 };
 
 // ---- forward ------------------------------------------------------------------
+constexpr int kFwdMaps = 4;  // rounds whose warps' maps are kept
 template <typename T, int W>
-using FwdMem = Mem<T, W, 2, 1, 3 * W * 32 * sizeof(Map<Of<T>::kVec>)>;
+using FwdMem = Mem<T, W, 2, 1, kFwdMaps * W * 32 * sizeof(Map<Of<T>::kVec>)>;
 
 // A warp's steps of a tile: -b (so that no factor is negated) and the values.
 template <int V> struct Steps { float g[kSteps][V], u[kSteps][V]; };
@@ -310,10 +358,16 @@ __device__ __forceinline__ Map<V> fold(Steps<V>& t, uint32_t at, uint32_t far, i
 }
 
 // CLUSTER: a cluster shares the time.  With one channel per lane the next round's tile
-// is folded while the maps of this one travel; with two that takes registers that
-// other CTAs hide the way with.
+// is folded while the maps of this one travel, and two warps beside the others take the
+// exchange: one loads tiles and sends the CTA's map, one takes the maps of all and hands
+// the state that enters on (fp32 1 x 65536 x 256: 49 us, with the exchange in all warps
+// 59 us).  With two channels that takes registers that other CTAs hide the way with
+// (bf16 2 x 32768 x 2048 141 us with the two warps, 132 us without).
+template <typename T, bool CLUSTER>
+constexpr int kHelpers = CLUSTER && Of<T>::kVec == 1 ? 2 : 0;
+
 template <typename T, int W, bool CLUSTER>
-__global__ void __launch_bounds__(W * 32)
+__global__ void __launch_bounds__((W + kHelpers<T, CLUSTER>) * 32, W == 8 ? 2 : 4)
     recur_fwd_tma_kernel(const __grid_constant__ CUtensorMap mg, const __grid_constant__ CUtensorMap mv,
                          const __grid_constant__ CUtensorMap my, const RecurParams p, const TmaArgs a) {
   using M = FwdMem<T, W>;
@@ -323,12 +377,13 @@ __global__ void __launch_bounds__(W * 32)
   unsigned char* mem = raw + pad;
   const uint32_t base = raw_at + pad;
   Map<V>(*maps)[W][32] = reinterpret_cast<Map<V>(*)[W][32]>(mem + M::kMaps);
-  constexpr bool kAhead = CLUSTER && V == 1;
+  constexpr bool kAhead = kHelpers<T, CLUSTER> > 0;
   Ring<W, 2> ring = {base + M::kIn, base + M::kBars, 0, 0};
   const Place<T> at(p, CLUSTER ? a.size : 1);
   const int warp = at.warp, lane = at.lane, len = at.len, size = static_cast<int>(at.size);
   const Exchange<V> cluster = {reinterpret_cast<Map<V>(*)[32]>(mem + M::kTiles),
                                base + M::kShared, at.rank, at.size};
+  const Handover<V> hand = {base + M::kHand, reinterpret_cast<float(*)[32][V]>(mem + M::kState)};
   const int live = (len + kTile - 1) / kTile, rounds = (live + size - 1) / size;
   const CUtensorMap* const in_map[2] = {&mg, &mv};
   const bool last[2] = {a.gate_last, a.value_last};
@@ -339,6 +394,7 @@ __global__ void __launch_bounds__(W * 32)
   };
   ring.init();
   if (CLUSTER) cluster.init();
+  if (kAhead) hand.init(W);
   __syncthreads();
   if (threadIdx.x == 0)
     for (int i = 0; i < kSlots; ++i) load(i, i);
@@ -347,7 +403,7 @@ __global__ void __launch_bounds__(W * 32)
   for (int v = 0; v < V; ++v) {
     keep[v] = p.floor ? __ldg(p.floor + at.d + v) - 1.f : -1.f;
     // before the first barrier, and not as a constant: out_final may be the same memory
-    x[v] = p.state0 ? p.state0[at.b * p.dim + at.d + v] : 0.f;
+    x[v] = p.state0 && (!kAhead || warp > W) ? p.state0[at.b * p.dim + at.d + v] : 0.f;
   }
   float* states = p.states
       ? p.states + at.b * ((p.seqlen + kRecurChunk - 1) / kRecurChunk) * p.dim + at.d
@@ -356,98 +412,131 @@ __global__ void __launch_bounds__(W * 32)
   bool bad = false;
   if (CLUSTER) pair::cluster_sync();  // all of the cluster has started, its barriers too
 
+  // past the valid steps: tiles that no round has covered
+  const int64_t rest = static_cast<int64_t>(tile_of(rounds)) * kTile;
+  const auto ends = [&]() {  // one warp per CTA; x: what leaves the valid steps
+    if (!at.on) return;
+    if (p.out_final && at.rank == 0) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) p.out_final[at.b * p.dim + at.d + v] = x[v];
+    }
+    if (!states) return;
+    for (int64_t t = rest; t < at.seqlen; t += static_cast<int64_t>(size) * kTile)
+      for (int64_t c = t; c < t + kTile && c < at.seqlen; c += kRecurChunk)
+#pragma unroll
+        for (int v = 0; v < V; ++v) states[c / kRecurChunk * p.dim + v] = x[v];
+  };
+  const auto of_tile = [&](int i) {
+    Map<V> all = Map<V>::none();
+#pragma unroll
+    for (int w = 0; w < W; ++w) all.then(maps[i % kFwdMaps][w][lane]);
+    return all;
+  };
   // folds the tile of round i and publishes its map
   const auto first_half = [&](Steps<V>& t, int i) {
     if (tile_of(i) < live && !bad && !ring.wait()) bad = true;
-    maps[i % 3][warp][lane] = fold<T, V>(t, ring.slot() + warp * kBox + lane * 4, W * kBox,
-                                         len - tile_of(i) * kTile - warp * kSteps, keep);
-    __syncthreads();
-    if (threadIdx.x == 0) load(i + kSlots, ring.at);
-    ring.next();
-    if (CLUSTER && warp < size) {
-      Map<V> all = Map<V>::none();
-#pragma unroll
-      for (int w = 0; w < W; ++w) all.then(maps[i % 3][w][lane]);
-      cluster.template send<W>(i, all);
-    }
-  };
-  Steps<V> now, next;
-  if (kAhead && rounds > 0) first_half(now, 0);
-  for (int i = 0; i < rounds; ++i) {
-    if (!kAhead) first_half(now, i);
-    if (kAhead && i + 1 < rounds) first_half(next, i + 1);
-    float in[V];
-    if (CLUSTER) {
-      if (!bad && !cluster.wait(i)) bad = true;
-      cluster.pass(i, x, in);
-#pragma unroll
-      for (int w = 0; w < W - 1; ++w)
-        if (w < warp) maps[i % 3][w][lane].through(in);
+    maps[i % kFwdMaps][warp][lane] =
+        fold<T, V>(t, ring.slot() + warp * kBox + lane * 4, W * kBox,
+                   len - tile_of(i) * kTile - warp * kSteps, keep);
+    if (kAhead) {
+      hand.map_given(i);
     } else {
-#pragma unroll
-      for (int w = 0; w < W; ++w) {
-        if (w == warp) {
-#pragma unroll
-          for (int v = 0; v < V; ++v) in[v] = x[v];
-        }
-        maps[i % 3][w][lane].through(x);
-      }
+      __syncthreads();
+      if (threadIdx.x == 0) load(i + kSlots, ring.at);
+      if (CLUSTER && warp < size) cluster.send(i, of_tile(i), warp, W);
     }
-    const int t0 = tile_of(i) * kTile + warp * kSteps, left = len - t0;
-    if (t0 < at.seqlen) {
-      if (states && at.on && t0 % kRecurChunk == 0) {
+    ring.next();
+  };
+  if (kAhead && warp == W) {
+    for (int i = 0; i < rounds; ++i) {
+      if (!bad && !hand.maps(i)) bad = true;
+      if (lane == 0) load(i + kSlots, i % kSlots);
+      cluster.send(i, of_tile(i), 0, 1);
+    }
+  } else if (kAhead && warp > W) {
+    for (int i = 0; i < rounds; ++i) {
+      float in[V];
+      if (!bad && !(hand.maps(i) && cluster.wait(i))) bad = true;
+      cluster.pass(i, x, in);
+      hand.publish(i, in);
+    }
+    ends();
+  } else {
+    Steps<V> now, next;
+    if (kAhead && rounds > 0) first_half(now, 0);
+    for (int i = 0; i < rounds; ++i) {
+      if (!kAhead) first_half(now, i);
+      if (kAhead && i + 1 < rounds) first_half(next, i + 1);
+      float in[V];
+      if (CLUSTER) {
+        if (kAhead) {
+          if (!bad && !hand.take(i, in)) bad = true;
+        } else {
+          if (!bad && !cluster.wait(i)) bad = true;
+          cluster.pass(i, x, in);
+        }
 #pragma unroll
-        for (int v = 0; v < V; ++v) states[t0 / kRecurChunk * p.dim + v] = in[v];
-      }
-      boxes_free();
-      if (left > 0) {
+        for (int w = 0; w < W - 1; ++w)
+          if (w < warp) maps[i % kFwdMaps][w][lane].through(in);
+      } else {
 #pragma unroll
-        for (int s = 0; s < kSteps; ++s) {
-          float o[V];
-          minus<V>(o, in, now.u[s]);
-          vfma<V>(in, now.g[s], o, in);
-          sts(out + s * kRow + lane * 4, pack(in));
+        for (int w = 0; w < W; ++w) {
+          if (w == warp) {
+#pragma unroll
+            for (int v = 0; v < V; ++v) in[v] = x[v];
+          }
+          maps[i % kFwdMaps][w][lane].through(x);
         }
       }
-      if (left < kSteps) {
-        for (int s = left < 0 ? 0 : left; s < kSteps; ++s) sts(out + s * kRow + lane * 4, 0u);
+      const int t0 = tile_of(i) * kTile + warp * kSteps, left = len - t0;
+      if (t0 < at.seqlen) {
+        if (states && at.on && t0 % kRecurChunk == 0) {
+#pragma unroll
+          for (int v = 0; v < V; ++v) states[t0 / kRecurChunk * p.dim + v] = in[v];
+        }
+        boxes_free();
+        if (left > 0) {
+#pragma unroll
+          for (int s = 0; s < kSteps; ++s) {
+            float o[V];
+            minus<V>(o, in, now.u[s]);
+            vfma<V>(in, now.g[s], o, in);
+            sts(out + s * kRow + lane * 4, pack(in));
+          }
+        }
+        if (left < kSteps) {
+          for (int s = left < 0 ? 0 : left; s < kSteps; ++s) sts(out + s * kRow + lane * 4, 0u);
+        }
+        umma::fence_smem_to_async();
+        __syncwarp();
+        if (lane == 0) {
+          store_box(&my, out, at.x0, t0, static_cast<int>(at.b));
+          commit_stores();
+        }
       }
+      if (kAhead) now = next;
+    }
+    if (!kAhead && warp == 0) ends();
+    if (rest < at.seqlen) {
+      boxes_free();
+      for (int s = 0; s < kSteps; ++s) sts(out + s * kRow + lane * 4, 0u);
       umma::fence_smem_to_async();
       __syncwarp();
       if (lane == 0) {
-        store_box(&my, out, at.x0, t0, static_cast<int>(at.b));
-        commit_stores();
+        for (int64_t t = rest + warp * kSteps; t < at.seqlen; t += static_cast<int64_t>(size) * kTile) {
+          store_box(&my, out, at.x0, static_cast<int>(t), static_cast<int>(at.b));
+          commit_stores();
+        }
       }
     }
-    if (kAhead) now = next;
-  }
-  if (p.out_final && at.rank == 0 && warp == 0 && at.on) {
-#pragma unroll
-    for (int v = 0; v < V; ++v) p.out_final[at.b * p.dim + at.d + v] = x[v];
-  }
-  // past the valid steps: tiles that no round has covered
-  const int64_t rest = static_cast<int64_t>(tile_of(rounds)) * kTile;
-  if (rest < at.seqlen) {
     boxes_free();
-    for (int s = 0; s < kSteps; ++s) sts(out + s * kRow + lane * 4, 0u);
-    umma::fence_smem_to_async();
-    __syncwarp();
-    for (int64_t t = rest + warp * kSteps; t < at.seqlen; t += static_cast<int64_t>(size) * kTile) {
-      if (lane == 0) {
-        store_box(&my, out, at.x0, static_cast<int>(t), static_cast<int>(at.b));
-        commit_stores();
-      }
-      if (states && at.on && t % kRecurChunk == 0) {
-#pragma unroll
-        for (int v = 0; v < V; ++v) states[t / kRecurChunk * p.dim + v] = x[v];
-      }
-    }
   }
-  boxes_free();
   if (bad) {
-    // copies that were not waited for land before the CTA ends
+    // tiles and maps that were not waited for land before the CTA ends
     for (int i = rounds > kSlots ? rounds - kSlots : 0; i < rounds; ++i)
       if (tile_of(i) < live) ring.drain(i);
+    if (CLUSTER)
+      for (int i = rounds > kBuffers ? rounds - kBuffers : 0; i < rounds; ++i) cluster.wait(i);
     atomicOr(a.err, kErrRecurWait);
   }
   if (CLUSTER) pair::cluster_sync();  // no map is on its way to a CTA that has ended
@@ -582,7 +671,7 @@ __global__ void __launch_bounds__(W * 32)
         Map<V> all = Map<V>::none();
 #pragma unroll
         for (int w = W - 1; w >= 0; --w) all.then(back(w));
-        cluster.template send<W>(i, all);
+        cluster.send(i, all, warp, W);
       }
       if (!bad && !cluster.wait(i)) bad = true;
       cluster.pass(i, m, mi);
@@ -781,21 +870,21 @@ cudaError_t allow(int sizes) {
 // CTAs that share the time of a channel group: doubled while all clusters run at
 // once and every CTA has a tile.  (bf16 2 x 32768 x 2048, 64 groups, forward: 2 CTAs
 // 195 us, 4 135 us, 8, half of them waiting for the others to end, 220 us.)
-template <auto KERNEL, typename MEM, int W>
+template <auto KERNEL, typename MEM, int W, int THREADS>
 int cluster_of(const RecurParams& p, int64_t units) {
   const int64_t tiles = (p.seqlen + W * kSteps - 1) / (W * kSteps);
   int i = 0;
-  while (i < 4 && (int64_t(2) << i) <= tiles && units <= resident<KERNEL, MEM, W * 32>(i + 1)) ++i;
+  while (i < 4 && (int64_t(2) << i) <= tiles && units <= resident<KERNEL, MEM, THREADS>(i + 1)) ++i;
   return 1 << i;
 }
 
-template <auto KERNEL, typename MEM, int W, typename... A>
+template <auto KERNEL, typename MEM, int THREADS, typename... A>
 cudaError_t go(const RecurParams& p, bool bf16, int size, cudaStream_t s, const A&... args) {
   const cudaError_t e = allow<KERNEL, MEM>(size > 1 ? kMaxCluster : 1);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr;
   const cudaLaunchConfig_t cfg =
-      config(units_of(p, bf16), size, W * 32, MEM::bytes(size), s, &attr);
+      config(units_of(p, bf16), size, THREADS, MEM::bytes(size), s, &attr);
   return cudaLaunchKernelEx(&cfg, KERNEL, args...);
 }
 
@@ -818,11 +907,12 @@ cudaError_t fwd(const RecurParams& p, unsigned* err, cudaStream_t s) {
     constexpr auto shared = recur_fwd_tma_kernel<T, W, true>;
     const cudaError_t e = allow<shared, M>(kMaxCluster);
     if (e != cudaSuccess) return e;
-    const int size = cluster_of<shared, M, W>(p, units_of(p, bf16));
+    constexpr int threads = (W + kHelpers<T, true>) * 32;
+    const int size = cluster_of<shared, M, W, threads>(p, units_of(p, bf16));
     a.size = static_cast<uint32_t>(size);
-    if (size > 1) return go<shared, M, W>(p, bf16, size, s, mg, mv, my, p, a);
+    if (size > 1) return go<shared, M, threads>(p, bf16, size, s, mg, mv, my, p, a);
   }
-  return go<recur_fwd_tma_kernel<T, W, false>, M, W>(p, bf16, 1, s, mg, mv, my, p, a);
+  return go<recur_fwd_tma_kernel<T, W, false>, M, W * 32>(p, bf16, 1, s, mg, mv, my, p, a);
 }
 
 template <typename T>
@@ -843,7 +933,7 @@ cudaError_t bwd(const RecurBwdParams& q, int size, unsigned* err, cudaStream_t s
       !map_of(&mdv, bf16, q.dvalue, p, dense(p), kSteps))
     return cudaErrorInvalidValue;
   const TmaArgs a = {static_cast<uint32_t>(size), g.time_last, v.time_last, err};
-  return go<recur_bwd_tma_kernel<T, W, CLUSTER>, BwdMem<T, W>, W>(p, bf16, size, s, mg, mv, my, mdg,
+  return go<recur_bwd_tma_kernel<T, W, CLUSTER>, BwdMem<T, W>, W * 32>(p, bf16, size, s, mg, mv, my, mdg,
                                                                   mdv, q, a);
 }
 
@@ -860,7 +950,7 @@ cudaError_t bwd_any(const RecurBwdParams& q, unsigned* err, int* size, cudaStrea
   // With two channels per lane one CTA per group from half of the SMs on (bf16 5 x 4096
   // x 1024, 80 groups: 55 us, in clusters of two 59 us; fp32 4 x 4096 x 1024, 128
   // groups: 68 and 56 us).
-  *size = bf16 && 2 * units >= kSms ? 1 : cluster_of<shared, BwdMem<T, 4>, 4>(q.fwd, units);
+  *size = bf16 && 2 * units >= kSms ? 1 : cluster_of<shared, BwdMem<T, 4>, 4, 128>(q.fwd, units);
   if (*size > 1) return bwd<T, 4, true>(q, *size, err, s);
   return bwd<T, bf16 ? 8 : 4, false>(q, 1, err, s);
 }
