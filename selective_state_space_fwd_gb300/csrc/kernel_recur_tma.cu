@@ -238,8 +238,7 @@ struct Exchange {
 };
 
 // What the warps of a CTA and the two beside them that deal with the cluster hand
-// over: every warp's map of a round, by `full`, and the state that enters the CTA's
-// tile, by `known`.  Two barriers of each are enough: a warp gives the map of round i + 2
+// over: every warp's map of a round, and the state that enters the CTA's tile.  Two barriers of each are enough: a warp gives the map of round i + 2
 // after it has taken the state of round i, which both helpers' parts in round i precede.
 template <int V>
 struct Handover {
