@@ -340,9 +340,7 @@ __device__ __forceinline__ Map<V> fold(Steps<V>& t, uint32_t at, uint32_t far, i
     float o[V];
     unpack(lds(at + s * kRow), g);
     unpack(lds(at + far + s * kRow), t.u[s]);
-    vscale<V>(g, g, kLog2e);
-#pragma unroll
-    for (int v = 0; v < V; ++v) g[v] = ex2(g[v]);
+    recur::exps<V>(g);
 #pragma unroll
     for (int v = 0; v < V; ++v) o[v] = 1.f;
     vadd<V>(g, g, o);
@@ -623,9 +621,7 @@ __global__ void __launch_bounds__(W * 32)
         unpack(lds(row + s * kRow), e);
         unpack(lds(row + W * kBox + s * kRow), u[s]);
         unpack(lds(row + 2 * W * kBox + s * kRow), l[s]);
-        vscale<V>(e, e, kLog2e);
-#pragma unroll
-        for (int v = 0; v < V; ++v) e[v] = ex2(e[v]);
+        recur::exps<V>(e);
 #pragma unroll
         for (int v = 0; v < V; ++v) o[v] = 1.f;
         vadd<V>(o, e, o);

@@ -9,6 +9,7 @@
 // (long memories) nor b near 1 (a reset) costs digits.
 #pragma once
 #include "common.cuh"
+#include "f32x2.cuh"
 #include "layers.h"
 
 namespace ssm {
@@ -49,14 +50,48 @@ __device__ __forceinline__ float rcp(float x) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
+// g <- e^g, within 7 2^-24 of itself whatever g: 2^t with t = g log2(e) rounded, times
+// what the rounding, and log2(e)'s own, took.  That is below 2^-16 where e^g is neither
+// infinite nor flushed to 0 (below 2^-126); beyond, where it may be infinite or none, it is
+// kept small.
+template <int V>
+__device__ __forceinline__ void exps(float (&g)[V]) {
+  constexpr float kFar = 0x1p-13f;
+  float down[V], r[V], k[V];
+  vscale<V>(down, g, -kLog2e);  // -t
+#pragma unroll
+  for (int v = 0; v < V; ++v) k[v] = kLog2e;
+  vfma<V>(r, g, k, down);
+#pragma unroll
+  for (int v = 0; v < V; ++v) k[v] = 1.92596299e-8f;  // log2(e) - kLog2e
+  vfma<V>(r, g, k, r);
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    r[v] = fmaxf(fminf(r[v], kFar), -kFar);
+    g[v] = ex2(-down[v]);
+  }
+  float ln2[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    ln2[v] = 0.693147181f;
+    k[v] = 1.f;
+  }
+  vfma<V>(r, r, ln2, k);
+  vmul<V>(g, g, r);
+}
+__device__ __forceinline__ float expg(float g) {
+  float e[1] = {g};
+  exps<1>(e);
+  return e[0];
+}
 // sigmoid(-g): 0 for a gate of +infinity, 1 for -infinity, NaN for NaN.
-__device__ __forceinline__ float opening(float g) { return rcp(1.f + ex2(g * kLog2e)); }
+__device__ __forceinline__ float opening(float g) { return rcp(1.f + expg(g)); }
 // e^g where it still has a reciprocal (its product with a reciprocal of 0 would be
 // NaN at infinity); NaN is left to the reciprocal.
 __device__ __forceinline__ float within(float e) { return fminf(e, 8.5e37f); }
-// The same, and hold = sigmoid(g), both with full relative precision.
+// The same, and hold = sigmoid(g), within 18 2^-24 of itself.
 __device__ __forceinline__ float opening(float g, float& hold) {
-  const float e = ex2(g * kLog2e), r = rcp(1.f + e);
+  const float e = expg(g), r = rcp(1.f + e);
   hold = within(e) * r;
   return r;
 }
