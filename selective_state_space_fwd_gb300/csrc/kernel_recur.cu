@@ -29,6 +29,7 @@
 //
 // A single step is bound by its launch: bf16 1024 x 2048 in 4.7 us, of which its bytes
 // take 4.3.
+#include "f32x2.cuh"
 #include "pdl.cuh"
 #include "recur.cuh"
 #include "umma_pair.cuh"
@@ -137,10 +138,11 @@ __global__ void __launch_bounds__(kThreads, 2) recur_fwd_kernel(const RecurParam
   float* states = p.states ? p.states + at.b * tiles * p.dim + d : nullptr;
   const int inside = at.warp * kSteps;
 
-  float keep[VEC], x[VEC];  // x: the state that enters the round
+  float floor[VEC], keep[VEC], x[VEC];  // keep: 1 - floor; x: the state that enters the round
 #pragma unroll
   for (int v = 0; v < VEC; ++v) {
-    keep[v] = p.floor ? 1.f - __ldg(p.floor + d + v) : 1.f;
+    floor[v] = p.floor ? __ldg(p.floor + d + v) : 0.f;
+    keep[v] = 1.f - floor[v];
     // before the first barrier, and not as a constant: out_final may be the same memory
     x[v] = p.state0 ? p.state0[at.b * p.dim + d + v] : 0.f;
   }
@@ -150,7 +152,7 @@ __global__ void __launch_bounds__(kThreads, 2) recur_fwd_kernel(const RecurParam
   load_rows<T, VEC>(vw, value, p.value_step, t0, len, at.on);
   if (size > 1) pair::cluster_sync();  // all of the cluster has started
   for (int64_t i = 0; i < rounds; ++i, t0 += static_cast<int64_t>(size) * kTile) {
-    float b[kSteps][VEC], u[kSteps][VEC];
+    float a[kSteps][VEC], u[kSteps][VEC];  // u: b v
     float hl[VEC], pl[VEC];
 #pragma unroll
     for (int v = 0; v < VEC; ++v) {
@@ -160,15 +162,19 @@ __global__ void __launch_bounds__(kThreads, 2) recur_fwd_kernel(const RecurParam
     const int64_t left = len - t0;
 #pragma unroll
     for (int s = 0; s < kSteps; ++s) {
-      float g[VEC];
+      float g[VEC], open[VEC], b[VEC];
       Cell<T, VEC>::get(gw[s], g);
       Cell<T, VEC>::get(vw[s], u[s]);
+      recur::gates<VEC>(g, keep, floor, open, b, a[s]);
 #pragma unroll
       for (int v = 0; v < VEC; ++v) {
-        const float o = keep[v] * recur::opening(g[v]);
-        b[s][v] = s < left ? o : 0.f;
-        hl[v] = fmaf(b[s][v], u[s][v] - hl[v], hl[v]);
-        pl[v] = fmaf(-b[s][v], pl[v], pl[v]);
+        u[s][v] *= b[v];
+        if (s >= left) {
+          a[s][v] = 1.f;
+          u[s][v] = 0.f;
+        }
+        hl[v] = fmaf(a[s][v], hl[v], u[s][v]);
+        pl[v] *= a[s][v];
       }
     }
     const int64_t next = t0 + static_cast<int64_t>(size) * kTile;
@@ -231,7 +237,7 @@ __global__ void __launch_bounds__(kThreads, 2) recur_fwd_kernel(const RecurParam
       float f[VEC];
 #pragma unroll
       for (int v = 0; v < VEC; ++v) {
-        in[v] = fmaf(b[s][v], u[s][v] - in[v], in[v]);
+        in[v] = fmaf(a[s][v], in[v], u[s][v]);
         f[v] = s < left ? in[v] : 0.f;
       }
       yw[s] = Cell<T, VEC>::put(f);
@@ -279,10 +285,11 @@ __global__ void __launch_bounds__(kThreads, 2)
   const float* states = q.states + at.b * tiles * p.dim + d;
   const int inside = at.warp * kSteps;
 
-  float keep[VEC], m[VEC], dfloor[VEC];  // m: a l of the step after the round's last
+  float floor[VEC], keep[VEC], m[VEC], dfloor[VEC];  // m: a l of the step after the round's last
 #pragma unroll
   for (int v = 0; v < VEC; ++v) {
-    keep[v] = p.floor ? 1.f - __ldg(p.floor + d + v) : 1.f;
+    floor[v] = p.floor ? __ldg(p.floor + d + v) : 0.f;
+    keep[v] = 1.f - floor[v];
     m[v] = q.dfinal ? __ldg(q.dfinal + at.b * p.dim + d + v) : 0.f;
     dfloor[v] = 0.f;
   }
@@ -299,7 +306,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     float h[VEC];
 #pragma unroll
     for (int v = 0; v < VEC; ++v) h[v] = tile < 0 ? 0.f : __ldg(states + tile * p.dim + v);
-    float open[kSteps][VEC], hold[kSteps][VEC], u[kSteps][VEC], l[kSteps][VEC];
+    float open[kSteps][VEC], hold[kSteps][VEC], a[kSteps][VEC], u[kSteps][VEC];
     float pl[VEC], hl[VEC], ml[VEC];
 #pragma unroll
     for (int v = 0; v < VEC; ++v) {
@@ -308,26 +315,28 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
 #pragma unroll
     for (int s = 0; s < kSteps; ++s) {
-      float g[VEC];
+      float g[VEC], b[VEC];
       Cell<T, VEC>::get(gw[s], g);
       Cell<T, VEC>::get(vw[s], u[s]);
-      Cell<T, VEC>::get(yw[s], l[s]);
+      recur::gates<VEC>(g, keep, floor, open[s], b, a[s]);
 #pragma unroll
       for (int v = 0; v < VEC; ++v) {
-        const float o = recur::opening(g[v], hold[s][v]);
-        open[s][v] = s < left ? o : 0.f;
-        const float b = keep[v] * open[s][v];
-        hl[v] = fmaf(b, u[s][v] - hl[v], hl[v]);
-        pl[v] = fmaf(-b, pl[v], pl[v]);
+        hold[s][v] = recur::holding(g[v], open[s][v]);
+        if (s >= left) {
+          open[s][v] = b[v] = 0.f;
+          a[s][v] = 1.f;
+        }
+        hl[v] = fmaf(a[s][v], hl[v], b[v] * u[s][v]);
+        pl[v] *= a[s][v];
       }
     }
 #pragma unroll
-    for (int s = kSteps - 1; s >= 0; --s)
+    for (int s = kSteps - 1; s >= 0; --s) {
+      float l[VEC];
+      Cell<T, VEC>::get(yw[s], l);
 #pragma unroll
-      for (int v = 0; v < VEC; ++v) {
-        const float lam = l[s][v] + ml[v];
-        ml[v] = fmaf(-(keep[v] * open[s][v]), lam, lam);
-      }
+      for (int v = 0; v < VEC; ++v) ml[v] = a[s][v] * (l[v] + ml[v]);
+    }
     const int k = i & 1;
 #pragma unroll
     for (int v = 0; v < VEC; ++v) {
@@ -385,19 +394,21 @@ __global__ void __launch_bounds__(kThreads, 2)
     for (int s = 0; s < kSteps; ++s)
 #pragma unroll
       for (int v = 0; v < VEC; ++v) {
+        const float in = keep[v] * open[s][v] * u[s][v];
         u[s][v] = h[v] - u[s][v];
-        h[v] = fmaf(-(keep[v] * open[s][v]), u[s][v], h[v]);
+        h[v] = fmaf(a[s][v], h[v], in);
       }
     float some[VEC];
 #pragma unroll
     for (int v = 0; v < VEC; ++v) some[v] = 0.f;
 #pragma unroll
     for (int s = kSteps - 1; s >= 0; --s) {
-      float dv[VEC], dg[VEC];
+      float dv[VEC], dg[VEC], l[VEC];
+      Cell<T, VEC>::get(yw[s], l);
 #pragma unroll
       for (int v = 0; v < VEC; ++v) {
-        const float b = keep[v] * open[s][v], lam = l[s][v] + mi[v];
-        mi[v] = fmaf(-b, lam, lam);
+        const float b = keep[v] * open[s][v], lam = l[v] + mi[v];
+        mi[v] = a[s][v] * lam;
         dv[v] = b * lam;
         const float w = lam * u[s][v];
         dg[v] = w * (b * hold[s][v]);
@@ -471,18 +482,21 @@ __global__ void __launch_bounds__(256) recur_step_kernel(const RecurParams p) {
   const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
   const int64_t b = i / vecs, d = (i - b * vecs) * VEC;
   if (b >= p.batch) return;
-  float g[VEC], u[VEC], h[VEC], f[VEC];
+  float g[VEC], u[VEC], h[VEC], floor[VEC], keep[VEC], open[VEC], add[VEC], a[VEC];
   load_f<T, VEC>(static_cast<const T*>(p.gate) + b * p.gate_batch + d, g);
   load_f<T, VEC>(static_cast<const T*>(p.value) + b * p.value_batch + d, u);
   widen<VEC>(raw_load_rw<float, VEC>(p.out_final + b * p.dim + d), h);
   if (p.floor) {
-    load_f<float, VEC>(p.floor + d, f);
+    load_f<float, VEC>(p.floor + d, floor);
   } else {
 #pragma unroll
-    for (int v = 0; v < VEC; ++v) f[v] = 0.f;
+    for (int v = 0; v < VEC; ++v) floor[v] = 0.f;
   }
 #pragma unroll
-  for (int v = 0; v < VEC; ++v) h[v] = fmaf((1.f - f[v]) * recur::opening(g[v]), u[v] - h[v], h[v]);
+  for (int v = 0; v < VEC; ++v) keep[v] = 1.f - floor[v];
+  recur::gates<VEC>(g, keep, floor, open, add, a);
+  vmul<VEC>(add, add, u);
+  vfma<VEC>(h, a, h, add);
   store_f<float, VEC>(p.out_final + b * p.dim + d, h);
   store_f<T, VEC>(static_cast<T*>(p.y) + b * p.dim + d, h);
 }

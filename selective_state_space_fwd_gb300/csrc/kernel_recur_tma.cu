@@ -318,13 +318,13 @@ constexpr int kFwdMaps = 4;  // rounds whose warps' maps are kept
 template <typename T, int W>
 using FwdMem = Mem<T, W, 2, 1, kFwdMaps * W * 32 * sizeof(Map<Of<T>::kVec>)>;
 
-// A warp's steps of a tile: -b (so that no factor is negated) and the values.
-template <int V> struct Steps { float g[kSteps][V], u[kSteps][V]; };
+// A warp's steps of a tile: a and b v.
+template <int V> struct Steps { float a[kSteps][V], u[kSteps][V]; };
 
 // Reads the rows at `at` (of the gate; the value's are `far` bytes on) and folds them.
 template <typename T, int V>
 __device__ __forceinline__ Map<V> fold(Steps<V>& t, uint32_t at, uint32_t far, int left,
-                                       const float (&keep)[V]) {
+                                       const float (&keep)[V], const float (&floor)[V]) {
   if (left <= 0) return Map<V>::none();
   if (left < kSteps) {  // closed gates past the valid steps
     for (int s = left; s < kSteps; ++s) {
@@ -336,20 +336,13 @@ __device__ __forceinline__ Map<V> fold(Steps<V>& t, uint32_t at, uint32_t far, i
   Map<V> m = Map<V>::none();
 #pragma unroll
   for (int s = 0; s < kSteps; ++s) {
-    float(&g)[V] = t.g[s];
-    float o[V];
+    float g[V], open[V], b[V];
     unpack(lds(at + s * kRow), g);
     unpack(lds(at + far + s * kRow), t.u[s]);
-    recur::exps<V>(g);
-#pragma unroll
-    for (int v = 0; v < V; ++v) o[v] = 1.f;
-    vadd<V>(g, g, o);
-#pragma unroll
-    for (int v = 0; v < V; ++v) g[v] = rcp(g[v]);
-    vmul<V>(g, g, keep);
-    minus<V>(o, m.e, t.u[s]);
-    vfma<V>(m.e, g, o, m.e);
-    vfma<V>(m.p, g, m.p, m.p);
+    recur::gates<V>(g, keep, floor, open, b, t.a[s]);
+    vmul<V>(t.u[s], b, t.u[s]);
+    vfma<V>(m.e, t.a[s], m.e, t.u[s]);
+    vmul<V>(m.p, t.a[s], m.p);
   }
   return m;
 }
@@ -395,10 +388,11 @@ __global__ void __launch_bounds__((W + kHelpers<T, CLUSTER>) * 32, W == 8 ? 2 : 
   __syncthreads();
   if (threadIdx.x == 0)
     for (int i = 0; i < kSlots; ++i) load(i, i);
-  float keep[V], x[V];  // -(1 - floor); the state that enters the round
+  float floor[V], keep[V], x[V];  // keep: 1 - floor; x: the state that enters the round
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    keep[v] = p.floor ? __ldg(p.floor + at.d + v) - 1.f : -1.f;
+    floor[v] = p.floor ? __ldg(p.floor + at.d + v) : 0.f;
+    keep[v] = 1.f - floor[v];
     // before the first barrier, and not as a constant: out_final may be the same memory
     x[v] = p.state0 && (!kAhead || warp > W) ? p.state0[at.b * p.dim + at.d + v] : 0.f;
   }
@@ -434,7 +428,7 @@ __global__ void __launch_bounds__((W + kHelpers<T, CLUSTER>) * 32, W == 8 ? 2 : 
     if (tile_of(i) < live && !bad && !ring.wait()) bad = true;
     maps[i % kFwdMaps][warp][lane] =
         fold<T, V>(t, ring.slot() + warp * kBox + lane * 4, W * kBox,
-                   len - tile_of(i) * kTile - warp * kSteps, keep);
+                   len - tile_of(i) * kTile - warp * kSteps, keep, floor);
     if (kAhead) {
       hand.map_given(i);
     } else {
@@ -495,9 +489,7 @@ __global__ void __launch_bounds__((W + kHelpers<T, CLUSTER>) * 32, W == 8 ? 2 : 
         if (left > 0) {
 #pragma unroll
           for (int s = 0; s < kSteps; ++s) {
-            float o[V];
-            minus<V>(o, in, now.u[s]);
-            vfma<V>(in, now.g[s], o, in);
+            vfma<V>(in, now.a[s], in, now.u[s]);
             sts(out + s * kRow + lane * 4, pack(in));
           }
         }
@@ -576,13 +568,12 @@ __global__ void __launch_bounds__(W * 32)
   __syncthreads();
   if (threadIdx.x == 0)
     for (int i = 0; i < kSlots; ++i) load(i, i);
-  // -(1 - floor); m: -a l of the step after the round's last.  With -b and -l no
-  // factor is negated on the way.
-  float keep[V], m[V], dfloor[V];
+  float floor[V], keep[V], m[V], dfloor[V];  // m: a l of the step after the round's last
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    keep[v] = p.floor ? __ldg(p.floor + at.d + v) - 1.f : -1.f;
-    m[v] = q.dfinal ? -__ldg(q.dfinal + at.b * p.dim + at.d + v) : 0.f;
+    floor[v] = p.floor ? __ldg(p.floor + at.d + v) : 0.f;
+    keep[v] = 1.f - floor[v];
+    m[v] = q.dfinal ? __ldg(q.dfinal + at.b * p.dim + at.d + v) : 0.f;
     dfloor[v] = 0.f;
   }
   const float* states =
@@ -609,7 +600,9 @@ __global__ void __launch_bounds__(W * 32)
       }
       umma::fence_smem_to_async();
     }
-    float open[kSteps][V], hold[kSteps][V], u[kSteps][V], l[kSteps][V];
+    // dy stays in its own words: with two channels per lane registers are short
+    float open[kSteps][V], hold[kSteps][V], decay[kSteps][V], u[kSteps][V];
+    uint32_t l[kSteps];
     Map<V> map = Map<V>::none();
     float ml[V];
 #pragma unroll
@@ -617,31 +610,23 @@ __global__ void __launch_bounds__(W * 32)
     if (left > 0) {
 #pragma unroll
       for (int s = 0; s < kSteps; ++s) {
-        float e[V], o[V], w[V], bs[V];
+        float e[V], b[V];
         unpack(lds(row + s * kRow), e);
         unpack(lds(row + W * kBox + s * kRow), u[s]);
-        unpack(lds(row + 2 * W * kBox + s * kRow), l[s]);
-        recur::exps<V>(e);
+        l[s] = lds(row + 2 * W * kBox + s * kRow);
+        recur::gates<V>(e, keep, floor, open[s], b, decay[s]);
 #pragma unroll
-        for (int v = 0; v < V; ++v) o[v] = 1.f;
-        vadd<V>(o, e, o);
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-          open[s][v] = rcp(o[v]);
-          e[v] = recur::within(e[v]);
-        }
-        vmul<V>(hold[s], e, open[s]);
-        vmul<V>(bs, keep, open[s]);  // -b
-        minus<V>(w, map.e, u[s]);
-        vfma<V>(map.e, bs, w, map.e);
-        vfma<V>(map.p, bs, map.p, map.p);
+        for (int v = 0; v < V; ++v) hold[s][v] = recur::holding(e[v], open[s][v]);
+        vmul<V>(b, b, u[s]);
+        vfma<V>(map.e, decay[s], map.e, b);
+        vmul<V>(map.p, decay[s], map.p);
       }
 #pragma unroll
       for (int s = kSteps - 1; s >= 0; --s) {
-        float lam[V], bs[V];
-        minus<V>(lam, ml, l[s]);
-        vmul<V>(bs, keep, open[s]);
-        vfma<V>(ml, bs, lam, lam);
+        float lam[V];
+        unpack(l[s], lam);
+        vadd<V>(lam, ml, lam);
+        vmul<V>(ml, decay[s], lam);
       }
     }
     const int k = i & 1;
@@ -688,33 +673,35 @@ __global__ void __launch_bounds__(W * 32)
       if (w < warp) past[k][w][lane].through(h);
     boxes_free();
     if (left > 0) {
-      // the distance of the value to the state before a step, in the value's place
+      // the distance of the state before a step to its value, in the value's place
 #pragma unroll
       for (int s = 0; s < kSteps; ++s) {
-        float bs[V];
-        vmul<V>(bs, keep, open[s]);
+        float b[V];
+        vmul<V>(b, keep, open[s]);
+        vmul<V>(b, b, u[s]);
         minus<V>(u[s], h, u[s]);
-        vfma<V>(h, bs, u[s], h);
+        vfma<V>(h, decay[s], h, b);
       }
       float some[V];
 #pragma unroll
       for (int v = 0; v < V; ++v) some[v] = 0.f;
 #pragma unroll
       for (int s = kSteps - 1; s >= 0; --s) {
-        float bs[V], lam[V], o[V];
-        vmul<V>(bs, keep, open[s]);
-        minus<V>(lam, mi, l[s]);
-        vfma<V>(mi, bs, lam, lam);
-        vmul<V>(o, bs, lam);
+        float b[V], lam[V], o[V];
+        unpack(l[s], lam);
+        vmul<V>(b, keep, open[s]);
+        vadd<V>(lam, mi, lam);
+        vmul<V>(mi, decay[s], lam);
+        vmul<V>(o, b, lam);
         sts(out + s * kRow + lane * 4, pack(o));
         vmul<V>(lam, lam, u[s]);
         vfma<V>(some, lam, open[s], some);
-        vmul<V>(bs, bs, hold[s]);
-        vmul<V>(o, lam, bs);
+        vmul<V>(b, b, hold[s]);
+        vmul<V>(o, lam, b);
         sts(out + kBox + s * kRow + lane * 4, pack(o));
       }
 #pragma unroll
-      for (int v = 0; v < V; ++v) dfloor[v] -= some[v];
+      for (int v = 0; v < V; ++v) dfloor[v] += some[v];
     }
     if (left < kSteps) {
       for (int s = left < 0 ? 0 : left; s < kSteps; ++s) {
@@ -732,7 +719,7 @@ __global__ void __launch_bounds__(W * 32)
   }
   if (q.dstate0 && at.rank == 0 && warp == 0 && at.on) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) q.dstate0[at.b * p.dim + at.d + v] = -m[v];
+    for (int v = 0; v < V; ++v) q.dstate0[at.b * p.dim + at.d + v] = m[v];
   }
   const int64_t rest = static_cast<int64_t>(live + static_cast<int>(at.rank)) * kTile;
   if (rest < at.seqlen) {

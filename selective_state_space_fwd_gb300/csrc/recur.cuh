@@ -1,12 +1,13 @@
 // recur.cuh -- the gated linear recurrence: shared device code.
 //
 // Per channel, with the gate g and the value v of a step,
-//   b = (1 - floor) sigmoid(-g),   a = 1 - b,   h <- a h + b v = h + b (v - h).
+//   b = (1 - floor) sigmoid(-g),   a = 1 - b,   h <- a h + b v.
+// b has its digits however small it is.  So has a: from b = 1/2 on it is formed from the
+// sigmoid's other side, floor + (1 - floor) sigmoid(g), so that a state that a gate throws
+// away (a reset) leaves nothing but a times itself.  (h + b (v - h) rounds v - h, at the size
+// of the state that goes: 1e8 before a value of 1 left 0.)
 // A stretch of steps maps the state that enters it to the one that leaves,
 //   h -> P h + e,   P = prod a,   e the state it leaves from h = 0.
-// P is formed as P <- P - b P, not from a rounded a, and the state as h + b (v - h):
-// each rounds once per step, at the size of what it is, so that neither small b
-// (long memories) nor b near 1 (a reset) costs digits.
 #pragma once
 #include "common.cuh"
 #include "f32x2.cuh"
@@ -84,17 +85,28 @@ __device__ __forceinline__ float expg(float g) {
   exps<1>(e);
   return e[0];
 }
-// sigmoid(-g): 0 for a gate of +infinity, 1 for -infinity, NaN for NaN.
-__device__ __forceinline__ float opening(float g) { return rcp(1.f + expg(g)); }
-// e^g where it still has a reciprocal (its product with a reciprocal of 0 would be
-// NaN at infinity); NaN is left to the reciprocal.
-__device__ __forceinline__ float within(float e) { return fminf(e, 8.5e37f); }
-// The same, and hold = sigmoid(g), within 18 2^-24 of itself.
-__device__ __forceinline__ float opening(float g, float& hold) {
-  const float e = expg(g), r = rcp(1.f + e);
-  hold = within(e) * r;
-  return r;
+// The gates of a step: open = sigmoid(-g) (0 for a gate of +infinity, 1 for -infinity, NaN
+// for NaN), b = keep open and a = 1 - b, with keep = 1 - floor.  g becomes e^g.
+template <int V>
+__device__ __forceinline__ void gates(float (&g)[V], const float (&keep)[V], const float (&floor)[V],
+                                      float (&open)[V], float (&b)[V], float (&a)[V]) {
+  float t[V], far[V];
+  exps<V>(g);
+#pragma unroll
+  for (int v = 0; v < V; ++v) t[v] = 1.f;
+  vadd<V>(t, g, t);
+#pragma unroll
+  for (int v = 0; v < V; ++v) open[v] = rcp(t[v]);
+  vmul<V>(b, keep, open);
+  vmul<V>(far, g, open);
+  vfma<V>(far, keep, far, floor);
+#pragma unroll
+  for (int v = 0; v < V; ++v) a[v] = b[v] > 0.5f ? far[v] : 1.f - b[v];  // e^g < 1 in the first
 }
+// sigmoid(g) from e^g and sigmoid(-g), within 18 2^-24 of itself; e^g where it still has a
+// reciprocal (its product with a reciprocal of 0 would be NaN at infinity).  NaN is left to
+// the reciprocal.
+__device__ __forceinline__ float holding(float e, float open) { return fminf(e, 8.5e37f) * open; }
 
 __device__ __forceinline__ int64_t valid_of(const int32_t* valid_len, int64_t b, int64_t seqlen) {
   if (!valid_len) return seqlen;
