@@ -102,6 +102,33 @@ __device__ __forceinline__ void store_rows(const typename Cell<T, VEC>::Word (&w
   }
 }
 
+// Stretches one after the other: (P, e) per channel in `all`, 1 - P in `rest`.
+template <int VEC>
+__device__ __forceinline__ void none(float (&all)[2 * VEC], float (&rest)[VEC]) {
+#pragma unroll
+  for (int v = 0; v < VEC; ++v) {
+    all[2 * v] = 1.f;
+    all[2 * v + 1] = rest[v] = 0.f;
+  }
+}
+// ... and then one of which c is kept, from which e comes; a channel's are so far apart.
+template <int VEC>
+__device__ __forceinline__ void then(float (&all)[2 * VEC], float (&rest)[VEC], const float* c,
+                                     int c_step, const float* e, int e_step) {
+#pragma unroll
+  for (int v = 0; v < VEC; ++v) {
+    const float P = recur::product(c[v * c_step]);
+    all[2 * v] *= P;
+    rest[v] = fmaf(P, rest[v], recur::remainder(c[v * c_step]));
+    all[2 * v + 1] = fmaf(P, all[2 * v + 1], e[v * e_step]);
+  }
+}
+template <int VEC>
+__device__ __forceinline__ void keep_all(float (&all)[2 * VEC], const float (&rest)[VEC]) {
+#pragma unroll
+  for (int v = 0; v < VEC; ++v) all[2 * v] = recur::kept(all[2 * v], rest[v]);
+}
+
 // The maps of the tiles that the cluster's CTAs hold in a round, sent to all of
 // them; `slots` alternates so that one barrier per round is enough.
 template <int N>
@@ -124,7 +151,7 @@ __device__ __forceinline__ void share(float (*slots)[32][N], const Place<N / 2>&
 template <typename T, int VEC>
 __global__ void __launch_bounds__(kThreads, 2) recur_fwd_kernel(const RecurParams p, uint32_t size) {
   using Word = typename Cell<T, VEC>::Word;
-  constexpr int N = 2 * VEC;  // floats of a map: (P, e) per channel
+  constexpr int N = 2 * VEC;  // floats of a map: P as it is kept, and e, per channel
   __shared__ __align__(16) float maps[2][kWarps][32][N];
   __shared__ __align__(16) float tiles_s[2][kMaxCluster][32][N];
   const Place<VEC> at(p.dim, size);
@@ -138,11 +165,11 @@ __global__ void __launch_bounds__(kThreads, 2) recur_fwd_kernel(const RecurParam
   float* states = p.states ? p.states + at.b * tiles * p.dim + d : nullptr;
   const int inside = at.warp * kSteps;
 
-  float floor[VEC], keep[VEC], x[VEC];  // keep: 1 - floor; x: the state that enters the round
+  recur::Floor<VEC> floor;
+  float x[VEC];  // the state that enters the round
 #pragma unroll
   for (int v = 0; v < VEC; ++v) {
-    floor[v] = p.floor ? __ldg(p.floor + d + v) : 0.f;
-    keep[v] = 1.f - floor[v];
+    floor.set(v, p.floor ? __ldg(p.floor + d + v) : 0.f);
     // before the first barrier, and not as a constant: out_final may be the same memory
     x[v] = p.state0 ? p.state0[at.b * p.dim + d + v] : 0.f;
   }
@@ -153,10 +180,10 @@ __global__ void __launch_bounds__(kThreads, 2) recur_fwd_kernel(const RecurParam
   if (size > 1) pair::cluster_sync();  // all of the cluster has started
   for (int64_t i = 0; i < rounds; ++i, t0 += static_cast<int64_t>(size) * kTile) {
     float a[kSteps][VEC], u[kSteps][VEC];  // u: b v
-    float hl[VEC], pl[VEC];
+    float hl[VEC], pl[VEC], ql[VEC];
 #pragma unroll
     for (int v = 0; v < VEC; ++v) {
-      hl[v] = 0.f;
+      hl[v] = ql[v] = 0.f;
       pl[v] = 1.f;
     }
     const int64_t left = len - t0;
@@ -165,15 +192,16 @@ __global__ void __launch_bounds__(kThreads, 2) recur_fwd_kernel(const RecurParam
       float g[VEC], open[VEC], b[VEC];
       Cell<T, VEC>::get(gw[s], g);
       Cell<T, VEC>::get(vw[s], u[s]);
-      recur::gates<VEC>(g, keep, floor, open, b, a[s]);
+      recur::gates<T>(g, floor, open, b, a[s]);
 #pragma unroll
       for (int v = 0; v < VEC; ++v) {
         u[s][v] *= b[v];
         if (s >= left) {
           a[s][v] = 1.f;
-          u[s][v] = 0.f;
+          b[v] = u[s][v] = 0.f;
         }
         hl[v] = fmaf(a[s][v], hl[v], u[s][v]);
+        ql[v] = fmaf(a[s][v], ql[v], b[v]);
         pl[v] *= a[s][v];
       }
     }
@@ -183,31 +211,26 @@ __global__ void __launch_bounds__(kThreads, 2) recur_fwd_kernel(const RecurParam
     const int k = i & 1;
 #pragma unroll
     for (int v = 0; v < VEC; ++v) {
-      maps[k][at.warp][at.lane][2 * v] = pl[v];
+      maps[k][at.warp][at.lane][2 * v] = recur::kept(pl[v], ql[v]);
       maps[k][at.warp][at.lane][2 * v + 1] = hl[v];
     }
     __syncthreads();
     float xt[VEC];  // the state that enters this CTA's tile
     if (size > 1) {
-      float all[N];
-#pragma unroll
-      for (int v = 0; v < N; ++v) all[v] = v & 1 ? 0.f : 1.f;
+      float all[N], rest[VEC];
+      none<VEC>(all, rest);
       if (at.warp == 0) {
 #pragma unroll
         for (int w = 0; w < kWarps; ++w)
-#pragma unroll
-          for (int v = 0; v < VEC; ++v) {
-            const float pw = maps[k][w][at.lane][2 * v];
-            all[2 * v] *= pw;
-            all[2 * v + 1] = fmaf(pw, all[2 * v + 1], maps[k][w][at.lane][2 * v + 1]);
-          }
+          then<VEC>(all, rest, maps[k][w][at.lane], 2, maps[k][w][at.lane] + 1, 2);
+        keep_all<VEC>(all, rest);
       }
       share<N>(tiles_s[k], at, all);
       for (uint32_t r = 0; r < size; ++r)
 #pragma unroll
         for (int v = 0; v < VEC; ++v) {
           if (r == at.rank) xt[v] = x[v];
-          x[v] = fmaf(tiles_s[k][r][at.lane][2 * v], x[v], tiles_s[k][r][at.lane][2 * v + 1]);
+          x[v] = recur::through(tiles_s[k][r][at.lane][2 * v], x[v], tiles_s[k][r][at.lane][2 * v + 1]);
         }
     } else {
 #pragma unroll
@@ -221,7 +244,7 @@ __global__ void __launch_bounds__(kThreads, 2) recur_fwd_kernel(const RecurParam
 #pragma unroll
       for (int v = 0; v < VEC; ++v) {
         if (w == at.warp) in[v] = out[v];
-        out[v] = fmaf(maps[k][w][at.lane][2 * v], out[v], maps[k][w][at.lane][2 * v + 1]);
+        out[v] = recur::through(maps[k][w][at.lane][2 * v], out[v], maps[k][w][at.lane][2 * v + 1]);
       }
     if (size == 1) {
 #pragma unroll
@@ -285,11 +308,11 @@ __global__ void __launch_bounds__(kThreads, 2)
   const float* states = q.states + at.b * tiles * p.dim + d;
   const int inside = at.warp * kSteps;
 
-  float floor[VEC], keep[VEC], m[VEC], dfloor[VEC];  // m: a l of the step after the round's last
+  recur::Floor<VEC> floor;
+  float m[VEC], dfloor[VEC];  // m: a l of the step after the round's last; half of dfloor
 #pragma unroll
   for (int v = 0; v < VEC; ++v) {
-    floor[v] = p.floor ? __ldg(p.floor + d + v) : 0.f;
-    keep[v] = 1.f - floor[v];
+    floor.set(v, p.floor ? __ldg(p.floor + d + v) : 0.f);
     m[v] = q.dfinal ? __ldg(q.dfinal + at.b * p.dim + d + v) : 0.f;
     dfloor[v] = 0.f;
   }
@@ -307,10 +330,10 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
     for (int v = 0; v < VEC; ++v) h[v] = tile < 0 ? 0.f : __ldg(states + tile * p.dim + v);
     float open[kSteps][VEC], hold[kSteps][VEC], a[kSteps][VEC], u[kSteps][VEC];
-    float pl[VEC], hl[VEC], ml[VEC];
+    float pl[VEC], ql[VEC], hl[VEC], ml[VEC];
 #pragma unroll
     for (int v = 0; v < VEC; ++v) {
-      hl[v] = ml[v] = 0.f;
+      ql[v] = hl[v] = ml[v] = 0.f;
       pl[v] = 1.f;
     }
 #pragma unroll
@@ -318,7 +341,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       float g[VEC], b[VEC];
       Cell<T, VEC>::get(gw[s], g);
       Cell<T, VEC>::get(vw[s], u[s]);
-      recur::gates<VEC>(g, keep, floor, open[s], b, a[s]);
+      recur::gates<T>(g, floor, open[s], b, a[s]);
 #pragma unroll
       for (int v = 0; v < VEC; ++v) {
         hold[s][v] = recur::holding(g[v], open[s][v]);
@@ -327,6 +350,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           a[s][v] = 1.f;
         }
         hl[v] = fmaf(a[s][v], hl[v], b[v] * u[s][v]);
+        ql[v] = fmaf(a[s][v], ql[v], b[v]);
         pl[v] *= a[s][v];
       }
     }
@@ -340,32 +364,27 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int k = i & 1;
 #pragma unroll
     for (int v = 0; v < VEC; ++v) {
-      past[k][at.warp][at.lane][2 * v] = pl[v];
+      past[k][at.warp][at.lane][2 * v] = recur::kept(pl[v], ql[v]);
       past[k][at.warp][at.lane][2 * v + 1] = hl[v];
       coming[k][at.warp][at.lane][v] = ml[v];
     }
     __syncthreads();
     float mt[VEC];  // what enters the tile from the steps after it
     if (size > 1) {
-      float all[N];
-#pragma unroll
-      for (int v = 0; v < N; ++v) all[v] = v & 1 ? 0.f : 1.f;
+      float all[N], rest[VEC];
+      none<VEC>(all, rest);
       if (at.warp == 0) {
 #pragma unroll
         for (int w = kWarps - 1; w >= 0; --w)
-#pragma unroll
-          for (int v = 0; v < VEC; ++v) {
-            const float pw = past[k][w][at.lane][2 * v];
-            all[2 * v] *= pw;
-            all[2 * v + 1] = fmaf(pw, all[2 * v + 1], coming[k][w][at.lane][v]);
-          }
+          then<VEC>(all, rest, past[k][w][at.lane], 2, coming[k][w][at.lane], 1);
+        keep_all<VEC>(all, rest);
       }
       share<N>(tiles_s[k], at, all);
       for (uint32_t r = 0; r < size; ++r)
 #pragma unroll
         for (int v = 0; v < VEC; ++v) {
           if (r == at.rank) mt[v] = m[v];
-          m[v] = fmaf(tiles_s[k][r][at.lane][2 * v], m[v], tiles_s[k][r][at.lane][2 * v + 1]);
+          m[v] = recur::through(tiles_s[k][r][at.lane][2 * v], m[v], tiles_s[k][r][at.lane][2 * v + 1]);
         }
     } else {
 #pragma unroll
@@ -377,13 +396,13 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
       for (int v = 0; v < VEC; ++v)
         if (w < at.warp)
-          h[v] = fmaf(past[k][w][at.lane][2 * v], h[v], past[k][w][at.lane][2 * v + 1]);
+          h[v] = recur::through(past[k][w][at.lane][2 * v], h[v], past[k][w][at.lane][2 * v + 1]);
 #pragma unroll
     for (int w = kWarps - 1; w >= 0; --w)
 #pragma unroll
       for (int v = 0; v < VEC; ++v) {
         if (w == at.warp) mi[v] = mt[v];
-        mt[v] = fmaf(past[k][w][at.lane][2 * v], mt[v], coming[k][w][at.lane][v]);
+        mt[v] = recur::through(past[k][w][at.lane][2 * v], mt[v], coming[k][w][at.lane][v]);
       }
     if (size == 1) {
 #pragma unroll
@@ -394,7 +413,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     for (int s = 0; s < kSteps; ++s)
 #pragma unroll
       for (int v = 0; v < VEC; ++v) {
-        const float in = keep[v] * open[s][v] * u[s][v];
+        const float in = floor.half[v] * open[s][v] * u[s][v];
         u[s][v] = h[v] - u[s][v];
         h[v] = fmaf(a[s][v], h[v], in);
       }
@@ -407,7 +426,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       Cell<T, VEC>::get(yw[s], l);
 #pragma unroll
       for (int v = 0; v < VEC; ++v) {
-        const float b = keep[v] * open[s][v], lam = l[v] + mi[v];
+        const float b = floor.half[v] * open[s][v], lam = l[v] + mi[v];
         mi[v] = a[s][v] * lam;
         dv[v] = b * lam;
         const float w = lam * u[s][v];
@@ -449,7 +468,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       for (int v = 0; v < VEC; ++v) {
         float t = 0.f;
         for (int w = 0; w < kWarps; ++w) t += sums[(w * 32 + at.lane) * VEC + v];
-        q.partial[(at.b * size + at.rank) * p.dim + d + v] = t;
+        q.partial[(at.b * size + at.rank) * p.dim + d + v] = 0.5f * t;
       }
     }
   }
@@ -482,21 +501,23 @@ __global__ void __launch_bounds__(256) recur_step_kernel(const RecurParams p) {
   const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
   const int64_t b = i / vecs, d = (i - b * vecs) * VEC;
   if (b >= p.batch) return;
-  float g[VEC], u[VEC], h[VEC], floor[VEC], keep[VEC], open[VEC], add[VEC], a[VEC];
+  float g[VEC], u[VEC], h[VEC], f[VEC], open[VEC], in[VEC], a[VEC];
+  recur::Floor<VEC> floor;
   load_f<T, VEC>(static_cast<const T*>(p.gate) + b * p.gate_batch + d, g);
   load_f<T, VEC>(static_cast<const T*>(p.value) + b * p.value_batch + d, u);
   widen<VEC>(raw_load_rw<float, VEC>(p.out_final + b * p.dim + d), h);
   if (p.floor) {
-    load_f<float, VEC>(p.floor + d, floor);
+    load_f<float, VEC>(p.floor + d, f);
   } else {
 #pragma unroll
-    for (int v = 0; v < VEC; ++v) floor[v] = 0.f;
+    for (int v = 0; v < VEC; ++v) f[v] = 0.f;
   }
 #pragma unroll
-  for (int v = 0; v < VEC; ++v) keep[v] = 1.f - floor[v];
-  recur::gates<VEC>(g, keep, floor, open, add, a);
-  vmul<VEC>(add, add, u);
-  vfma<VEC>(h, a, h, add);
+  for (int v = 0; v < VEC; ++v) floor.set(v, f[v]);
+  recur::gates<T>(g, floor, open, in, a);
+#pragma unroll
+  for (int v = 0; v < VEC; ++v)
+    h[v] = recur::through(recur::kept(a[v], in[v]), h[v], in[v] * u[v]);
   store_f<float, VEC>(p.out_final + b * p.dim + d, h);
   store_f<T, VEC>(static_cast<T*>(p.y) + b * p.dim + d, h);
 }

@@ -93,20 +93,52 @@ __device__ __forceinline__ bool wait_here(uint32_t bar, uint32_t parity) {
   }
 }
 
-// A lane's 2 V floats in shared memory: (P, e) of its channels.
+// A lane's 2 V floats in shared memory: P as it is kept, and e, of its channels.
 template <int V> struct alignas(8 * V) Map {
   float p[V], e[V];
   // The state (or what goes back) that leaves when x enters.
-  __device__ __forceinline__ void through(float (&x)[V]) const { vfma<V>(x, p, x, e); }
-  // This stretch and then `m`, as one.
-  __device__ __forceinline__ void then(const Map& m) {
-    vfma<V>(e, m.p, e, m.e);
-    vmul<V>(p, p, m.p);
-  }
-  static __device__ __forceinline__ Map none() {
-    Map m;
+  __device__ __forceinline__ void through(float (&x)[V]) const {
+    float d[V], k[V];
+    vfma<V>(d, x, p, e);
 #pragma unroll
-    for (int v = 0; v < V; ++v) { m.p[v] = 1.f; m.e[v] = 0.f; }
+    for (int v = 0; v < V; ++v) k[v] = recur::is_rest(p[v]);
+    vfma<V>(x, x, k, d);
+  }
+};
+// Steps or stretches, one after the other.
+template <int V> struct Fold {
+  float p[V], q[V], e[V];
+  __device__ __forceinline__ Fold() {
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      p[v] = 1.f;
+      q[v] = e[v] = 0.f;
+    }
+  }
+  __device__ __forceinline__ void then(const float (&a)[V], const float (&b)[V], const float (&add)[V]) {
+    vmul<V>(p, a, p);
+    vfma<V>(q, a, q, b);
+    vfma<V>(e, a, e, add);
+  }
+  __device__ __forceinline__ void then(const Map<V>& m) {
+    float a[V], b[V], k[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      k[v] = recur::is_rest(m.p[v]);
+      b[v] = 1.f;
+    }
+    vadd<V>(a, m.p, k);  // P
+    minus<V>(b, b, k);
+    minus<V>(b, b, m.p);  // 1 - P
+    then(a, b, m.e);
+  }
+  __device__ __forceinline__ Map<V> map() const {
+    Map<V> m;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      m.p[v] = recur::kept(p[v], q[v]);
+      m.e[v] = e[v];
+    }
     return m;
   }
 };
@@ -324,8 +356,9 @@ template <int V> struct Steps { float a[kSteps][V], u[kSteps][V]; };
 // Reads the rows at `at` (of the gate; the value's are `far` bytes on) and folds them.
 template <typename T, int V>
 __device__ __forceinline__ Map<V> fold(Steps<V>& t, uint32_t at, uint32_t far, int left,
-                                       const float (&keep)[V], const float (&floor)[V]) {
-  if (left <= 0) return Map<V>::none();
+                                       const recur::Floor<V>& floor) {
+  Fold<V> m;
+  if (left <= 0) return m.map();
   if (left < kSteps) {  // closed gates past the valid steps
     for (int s = left; s < kSteps; ++s) {
       sts(at + s * kRow, closed<T>());
@@ -333,18 +366,16 @@ __device__ __forceinline__ Map<V> fold(Steps<V>& t, uint32_t at, uint32_t far, i
     }
     umma::fence_smem_to_async();
   }
-  Map<V> m = Map<V>::none();
 #pragma unroll
   for (int s = 0; s < kSteps; ++s) {
     float g[V], open[V], b[V];
     unpack(lds(at + s * kRow), g);
     unpack(lds(at + far + s * kRow), t.u[s]);
-    recur::gates<V>(g, keep, floor, open, b, t.a[s]);
+    recur::gates<T>(g, floor, open, b, t.a[s]);
     vmul<V>(t.u[s], b, t.u[s]);
-    vfma<V>(m.e, t.a[s], m.e, t.u[s]);
-    vmul<V>(m.p, t.a[s], m.p);
+    m.then(t.a[s], b, t.u[s]);
   }
-  return m;
+  return m.map();
 }
 
 // CLUSTER: a cluster shares the time.  With one channel per lane the next round's tile
@@ -388,11 +419,11 @@ __global__ void __launch_bounds__((W + kHelpers<T, CLUSTER>) * 32, W == 8 ? 2 : 
   __syncthreads();
   if (threadIdx.x == 0)
     for (int i = 0; i < kSlots; ++i) load(i, i);
-  float floor[V], keep[V], x[V];  // keep: 1 - floor; x: the state that enters the round
+  recur::Floor<V> floor;
+  float x[V];  // the state that enters the round
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    floor[v] = p.floor ? __ldg(p.floor + at.d + v) : 0.f;
-    keep[v] = 1.f - floor[v];
+    floor.set(v, p.floor ? __ldg(p.floor + at.d + v) : 0.f);
     // before the first barrier, and not as a constant: out_final may be the same memory
     x[v] = p.state0 && (!kAhead || warp > W) ? p.state0[at.b * p.dim + at.d + v] : 0.f;
   }
@@ -418,17 +449,17 @@ __global__ void __launch_bounds__((W + kHelpers<T, CLUSTER>) * 32, W == 8 ? 2 : 
         for (int v = 0; v < V; ++v) states[c / kRecurChunk * p.dim + v] = x[v];
   };
   const auto of_tile = [&](int i) {
-    Map<V> all = Map<V>::none();
+    Fold<V> all;
 #pragma unroll
     for (int w = 0; w < W; ++w) all.then(maps[i % kFwdMaps][w][lane]);
-    return all;
+    return all.map();
   };
   // folds the tile of round i and publishes its map
   const auto first_half = [&](Steps<V>& t, int i) {
     if (tile_of(i) < live && !bad && !ring.wait()) bad = true;
     maps[i % kFwdMaps][warp][lane] =
         fold<T, V>(t, ring.slot() + warp * kBox + lane * 4, W * kBox,
-                   len - tile_of(i) * kTile - warp * kSteps, keep, floor);
+                   len - tile_of(i) * kTile - warp * kSteps, floor);
     if (kAhead) {
       hand.map_given(i);
     } else {
@@ -568,11 +599,11 @@ __global__ void __launch_bounds__(W * 32)
   __syncthreads();
   if (threadIdx.x == 0)
     for (int i = 0; i < kSlots; ++i) load(i, i);
-  float floor[V], keep[V], m[V], dfloor[V];  // m: a l of the step after the round's last
+  recur::Floor<V> floor;
+  float m[V], dfloor[V];  // m: a l of the step after the round's last; half of dfloor
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    floor[v] = p.floor ? __ldg(p.floor + at.d + v) : 0.f;
-    keep[v] = 1.f - floor[v];
+    floor.set(v, p.floor ? __ldg(p.floor + at.d + v) : 0.f);
     m[v] = q.dfinal ? __ldg(q.dfinal + at.b * p.dim + at.d + v) : 0.f;
     dfloor[v] = 0.f;
   }
@@ -603,7 +634,7 @@ __global__ void __launch_bounds__(W * 32)
     // dy stays in its own words: with two channels per lane registers are short
     float open[kSteps][V], hold[kSteps][V], decay[kSteps][V], u[kSteps][V];
     uint32_t l[kSteps];
-    Map<V> map = Map<V>::none();
+    Fold<V> fold;
     float ml[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) ml[v] = 0.f;
@@ -614,12 +645,12 @@ __global__ void __launch_bounds__(W * 32)
         unpack(lds(row + s * kRow), e);
         unpack(lds(row + W * kBox + s * kRow), u[s]);
         l[s] = lds(row + 2 * W * kBox + s * kRow);
-        recur::gates<V>(e, keep, floor, open[s], b, decay[s]);
+        recur::gates<T>(e, floor, open[s], b, decay[s]);
 #pragma unroll
         for (int v = 0; v < V; ++v) hold[s][v] = recur::holding(e[v], open[s][v]);
-        vmul<V>(b, b, u[s]);
-        vfma<V>(map.e, decay[s], map.e, b);
-        vmul<V>(map.p, decay[s], map.p);
+        float in[V];
+        vmul<V>(in, b, u[s]);
+        fold.then(decay[s], b, in);
       }
 #pragma unroll
       for (int s = kSteps - 1; s >= 0; --s) {
@@ -630,7 +661,7 @@ __global__ void __launch_bounds__(W * 32)
       }
     }
     const int k = i & 1;
-    past[k][warp][lane] = map;
+    past[k][warp][lane] = fold.map();
 #pragma unroll
     for (int v = 0; v < V; ++v) coming[k][warp][lane][v] = ml[v];
     __syncthreads();
@@ -648,10 +679,10 @@ __global__ void __launch_bounds__(W * 32)
     float mi[V];
     if (CLUSTER) {
       if (warp < size) {
-        Map<V> all = Map<V>::none();
+        Fold<V> all;
 #pragma unroll
         for (int w = W - 1; w >= 0; --w) all.then(back(w));
-        cluster.send(i, all, warp, W);
+        cluster.send(i, all.map(), warp, W);
       }
       if (!bad && !cluster.wait(i)) bad = true;
       cluster.pass(i, m, mi);
@@ -677,7 +708,7 @@ __global__ void __launch_bounds__(W * 32)
 #pragma unroll
       for (int s = 0; s < kSteps; ++s) {
         float b[V];
-        vmul<V>(b, keep, open[s]);
+        vmul<V>(b, floor.half, open[s]);
         vmul<V>(b, b, u[s]);
         minus<V>(u[s], h, u[s]);
         vfma<V>(h, decay[s], h, b);
@@ -689,7 +720,7 @@ __global__ void __launch_bounds__(W * 32)
       for (int s = kSteps - 1; s >= 0; --s) {
         float b[V], lam[V], o[V];
         unpack(l[s], lam);
-        vmul<V>(b, keep, open[s]);
+        vmul<V>(b, floor.half, open[s]);
         vadd<V>(lam, mi, lam);
         vmul<V>(mi, decay[s], lam);
         vmul<V>(o, b, lam);
@@ -747,7 +778,7 @@ __global__ void __launch_bounds__(W * 32)
       for (int v = 0; v < V; ++v) {
         float t = 0.f;
         for (int w = 0; w < W; ++w) t += sums[(w * 32 + lane) * V + v];
-        q.partial[(at.b * size + at.rank) * p.dim + at.d + v] = t;
+        q.partial[(at.b * size + at.rank) * p.dim + at.d + v] = 0.5f * t;
       }
     }
   }

@@ -8,7 +8,15 @@
 // of the state that goes: 1e8 before a value of 1 left 0.)
 // A stretch of steps maps the state that enters it to the one that leaves,
 //   h -> P h + e,   P = prod a,   e the state it leaves from h = 0.
+// Beside P, Q = 1 - P is formed as Q <- a Q + b, so that each has its digits where it is
+// small, and Q is kept where it is at most 1/2, as -Q in P's place: the state then moves
+// by e - Q h.  With a rounded P near 1 a long memory would be off by P's rounding times
+// all of the state, stretch after stretch and the same way (a state of 1 under steady
+// values of 1 was off by 4e-4 to 2e-3 after 65536 steps); as e and Q are formed alike,
+// what is steady stays.
 #pragma once
+#include <cuda_bf16.h>
+
 #include "common.cuh"
 #include "f32x2.cuh"
 #include "layers.h"
@@ -45,68 +53,95 @@ template <> struct Cell<__nv_bfloat16, 2> {
   }
 };
 
-// 1 / x for x >= 1 (0 past 2^126), within 1 ulp.
+// 1 / x for x >= 1/2 (0 past 2^126), within 1 ulp.
 __device__ __forceinline__ float rcp(float x) {
   float r;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
-// g <- e^g, within 7 2^-24 of itself whatever g: 2^t with t = g log2(e) rounded, times
-// what the rounding, and log2(e)'s own, took.  That is below 2^-16 where e^g is neither
-// infinite nor flushed to 0 (below 2^-126); beyond, where it may be infinite or none, it is
-// kept small.
+// g <- e^g / 2, within 7 2^-24 of itself whatever g: 2^t with t = g log2(e) rounded, times
+// half of what the rounding, and log2(e)'s own, took.  That is near 1/2 where e^g is neither
+// infinite nor flushed to 0 (below 2^-126), and kept within [0, 1] elsewhere.
 template <int V>
-__device__ __forceinline__ void exps(float (&g)[V]) {
-  constexpr float kFar = 0x1p-13f;
+__device__ __forceinline__ void half_exps(float (&g)[V], float) {
   float down[V], r[V], k[V];
-  vscale<V>(down, g, -kLog2e);  // -t
 #pragma unroll
-  for (int v = 0; v < V; ++v) k[v] = kLog2e;
+  for (int v = 0; v < V; ++v) {
+    // where 1 / (1 + e^g) is 0, and no infinity less infinity below
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(g[v]) : "f"(g[v]), "f"(88.f));
+    k[v] = kLog2e;
+  }
+  vscale<V>(down, g, -kLog2e);  // -t
   vfma<V>(r, g, k, down);
 #pragma unroll
   for (int v = 0; v < V; ++v) k[v] = 1.92596299e-8f;  // log2(e) - kLog2e
   vfma<V>(r, g, k, r);
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    r[v] = fmaxf(fminf(r[v], kFar), -kFar);
+    r[v] = __saturatef(fmaf(r[v], 0.346573590f, 0.5f));  // ln(2) / 2; NaN becomes 0
     g[v] = ex2(-down[v]);
   }
-  float ln2[V];
-#pragma unroll
-  for (int v = 0; v < V; ++v) {
-    ln2[v] = 0.693147181f;
-    k[v] = 1.f;
-  }
-  vfma<V>(r, r, ln2, k);
   vmul<V>(g, g, r);
 }
-__device__ __forceinline__ float expg(float g) {
-  float e[1] = {g};
-  exps<1>(e);
-  return e[0];
-}
-// The gates of a step: open = sigmoid(-g) (0 for a gate of +infinity, 1 for -infinity, NaN
-// for NaN), b = keep open and a = 1 - b, with keep = 1 - floor.  g becomes e^g.
+// The same for gates of 8 significant bits, whose product with 16 of log2(e) is exact.
 template <int V>
-__device__ __forceinline__ void gates(float (&g)[V], const float (&keep)[V], const float (&floor)[V],
-                                      float (&open)[V], float (&b)[V], float (&a)[V]) {
-  float t[V], far[V];
-  exps<V>(g);
+__device__ __forceinline__ void half_exps(float (&g)[V], __nv_bfloat16) {
+  float t[V];
+  vscale<V>(t, g, 1.44268798828125f);
 #pragma unroll
-  for (int v = 0; v < V; ++v) t[v] = 1.f;
+  for (int v = 0; v < V; ++v) {
+    g[v] = __saturatef(fmaf(g[v], 2.44427e-6f, 0.5f));  // (log2(e) - the above) ln(2) / 2
+    t[v] = ex2(t[v]);
+  }
+  vmul<V>(g, g, t);
+}
+
+// A channel's floor: 1 - floor, and half of it.
+template <int V> struct Floor {
+  float at[V], keep[V], half[V];
+  __device__ __forceinline__ void set(int v, float f) {
+    at[v] = f;
+    keep[v] = 1.f - f;
+    half[v] = 0.5f * keep[v];
+  }
+};
+
+// The gates of a step: open = 2 sigmoid(-g) (0 for a gate of +infinity, 2 for -infinity, NaN
+// for NaN), b = (1 - floor) sigmoid(-g) and a = 1 - b.  T: the gate's type; g becomes e^g / 2.
+template <typename T, int V>
+__device__ __forceinline__ void gates(float (&g)[V], const Floor<V>& floor, float (&open)[V],
+                                      float (&b)[V], float (&a)[V]) {
+  float t[V], far[V];
+  half_exps<V>(g, T());
+#pragma unroll
+  for (int v = 0; v < V; ++v) t[v] = 0.5f;
   vadd<V>(t, g, t);
 #pragma unroll
   for (int v = 0; v < V; ++v) open[v] = rcp(t[v]);
-  vmul<V>(b, keep, open);
+  vmul<V>(b, floor.half, open);
   vmul<V>(far, g, open);
-  vfma<V>(far, keep, far, floor);
+  vfma<V>(far, floor.keep, far, floor.at);
 #pragma unroll
   for (int v = 0; v < V; ++v) a[v] = b[v] > 0.5f ? far[v] : 1.f - b[v];  // e^g < 1 in the first
 }
-// sigmoid(g) from e^g and sigmoid(-g), within 18 2^-24 of itself; e^g where it still has a
-// reciprocal (its product with a reciprocal of 0 would be NaN at infinity).  NaN is left to
-// the reciprocal.
-__device__ __forceinline__ float holding(float e, float open) { return fminf(e, 8.5e37f) * open; }
+// sigmoid(g) from e^g / 2 and 2 sigmoid(-g), within 18 2^-24 of itself; where the latter is 0
+// it is 0 too.
+__device__ __forceinline__ float holding(float e, float open) { return fminf(e, 4e37f) * open; }
+
+// How P is kept (Q of 0: P is 1), and h through what is kept of a stretch.
+__device__ __forceinline__ float kept(float P, float Q) { return Q > 0.f && Q <= 0.5f ? -Q : P; }
+// 1 where Q is kept, 0 where P is.
+__device__ __forceinline__ float is_rest(float c) {
+  float k;
+  asm("set.lt.f32.f32 %0, %1, 0f00000000;" : "=f"(k) : "f"(c));
+  return k;
+}
+__device__ __forceinline__ float through(float c, float h, float e) {
+  return fmaf(is_rest(c), h, fmaf(c, h, e));
+}
+// P and Q from what is kept.
+__device__ __forceinline__ float product(float c) { return c + is_rest(c); }
+__device__ __forceinline__ float remainder(float c) { return (1.f - is_rest(c)) - c; }
 
 __device__ __forceinline__ int64_t valid_of(const int32_t* valid_len, int64_t b, int64_t seqlen) {
   if (!valid_len) return seqlen;

@@ -109,6 +109,47 @@ def test_an_open_gate_forgets(L, D, big, v):
     assert (out == value[:, 0]).all() and (state == value[:, 0]).all()
 
 
+STEADY = [(11.0, 0.0), (18.0, 0.0), (6.0, 0.99), (6.0, 0.999), (9.0, 0.5), (4.0, 0.0), (0.5, 0.0), (14.0, 0.9)]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("B,L,D", [
+    (1, 65536, 64), (1, 65536, 33),      # clusters
+    (8, 16384, 1024), (5, 16384, 1025),  # more CTAs than the GPU holds, or half of them
+])
+def test_steady_gates_hold_a_steady_state(dtype, B, L, D):
+    """A state equal to a steady value stays there, over all of a long sequence.
+
+    A stretch's e and Q = 1 - P are formed alike; e is off from Q v by 33 u (16 steps of two
+    roundings, the product b v), by 24 u more where 8 stretches are composed, P by 40 u:
+    a state that enters is moved towards a value within 97 u of v, never past it but for
+    its own rounding.  Within a stretch a step rounds twice: 26 u.  128 u in all.
+    Backward the same holds for l = dy / b, whose b is off by 12 u, and the share of l that
+    goes to the value is dy: 256 u with the products."""
+    dt = DTYPES[dtype]
+    pick = torch.arange(D, device="cuda") % len(STEADY)
+    steady = torch.tensor(STEADY, device="cuda")
+    gate = steady[pick, 0].to(dt).expand(B, L, D).contiguous()
+    floor = steady[pick, 1].contiguous()
+    v = torch.linspace(-2, 2, D, device="cuda").to(dt)
+    value = v.expand(B, L, D).contiguous()
+    state0 = v.float().expand(B, D).contiguous()
+    y, final, states = S.recur_fwd(gate, value, floor, state0=state0, want_final=True, want_states=True)
+    bound = 128 * U * state0.abs()
+    assert ((final - state0).abs() <= bound).all()
+    assert ((states - state0[:, None]).abs() <= bound[:, None]).all()
+    if dtype == "f32":
+        assert ((y - value).abs() <= 128 * U * value.abs()).all()
+    else:  # the value itself is the nearest
+        assert torch.equal(y, value)
+    b = (1 - floor.double()) * torch.sigmoid(-gate[:, 0].double())
+    dfinal = ((1 - b) / b).float()  # what goes back to a step when dy is 1 for ever
+    dy = torch.ones_like(gate)
+    g = S.recur_bwd(gate, value, floor, states=states, dy=dy, dfinal=dfinal, want_dstate0=True)
+    assert ((g["dstate0"].double() * b / (1 - b) - 1).abs() <= 256 * U).all()
+    assert ((g["dvalue"].double() - 1).abs() <= 256 * U).all()
+
+
 @pytest.mark.parametrize("D", [1024, 1023])
 def test_sigmoids_keep_their_digits_far_out(D):
     """b, a and a's derivative relative to themselves, for gates up to +-80."""
