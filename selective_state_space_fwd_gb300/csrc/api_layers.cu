@@ -405,8 +405,7 @@ ssm_status ssm_recur_fwd(const void* gate, const void* value, const float* floor
 
 size_t ssm_recur_bwd_workspace_bytes(const ssm_recur_shapes* shapes) {
   if (check_recur(shapes, SSM_F32) != SSM_OK) return 0;
-  return static_cast<size_t>(ssm::recur_bwd_partials(shapes->batch, shapes->seqlen)) *
-         shapes->dim * sizeof(float);
+  return static_cast<size_t>(ssm::recur_bwd_partials(shapes->batch)) * shapes->dim * sizeof(float);
 }
 
 int64_t ssm_recur_chunks(const ssm_recur_shapes* shapes) {

@@ -27,8 +27,7 @@
 // whole gradient, not 38.
 #include <cuda_bf16.h>
 
-#include <atomic>
-
+#include "cluster.cuh"
 #include "common.cuh"
 #include "f32x2.cuh"
 #include "layers.h"
@@ -77,7 +76,7 @@ __global__ void __launch_bounds__(kLookThreads) embed_fwd_kernel(const EmbedPara
 }
 
 // ---- sorting the tokens, and zeros ------------------------------------------------
-constexpr int kSortCtas = 16;                          // at most
+constexpr int kSortCtas = kMaxCluster;                 // at most
 constexpr int kSortThreads = 1024, kSortWarps = kSortThreads / 32;
 constexpr int kDigitBits = 9, kDigits = 1 << kDigitBits;
 constexpr int kRounds = 4;                             // keys per thread and tile
@@ -639,36 +638,18 @@ cudaError_t sum(SumArgs a, cudaStream_t s) {
 // Sorts with one thread per token, but in at most kSortCtas CTAs (8 where the GPU has
 // no room for a larger cluster).
 cudaError_t sort(SortArgs& a, cudaStream_t s) {
-  cudaError_t e =
-      cudaFuncSetAttribute(embed_sort_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-  if (e != cudaSuccess) return e;
   a.ctas = 1;
   while (a.ctas < kSortCtas && a.ctas * kSortThreads < a.tokens) a.ctas *= 2;
-  cudaLaunchAttribute attr = {};
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = a.ctas;
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(a.ctas);
-  cfg.blockDim = dim3(kSortThreads);
-  cfg.stream = s;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  static std::atomic<int> whole{-1};  // clusters of kSortCtas that the GPU holds
-  int n = whole.load(std::memory_order_relaxed);
-  if (a.ctas == kSortCtas && n < 0) {
-    if (cudaOccupancyMaxActiveClusters(&n, embed_sort_kernel, &cfg) != cudaSuccess) {
-      cudaGetLastError();
-      n = 0;
+  if (a.ctas > kPortableCluster) {
+    if (resident_clusters<embed_sort_kernel>(4, kSortThreads, 0) < 1) {
+      a.ctas = kPortableCluster;
+    } else {
+      const cudaError_t e = allow_large_clusters(reinterpret_cast<const void*>(embed_sort_kernel));
+      if (e != cudaSuccess) return e;
     }
-    whole.store(n, std::memory_order_relaxed);
   }
-  if (a.ctas == kSortCtas && n < 1) {
-    a.ctas = kSortCtas / 2;
-    attr.val.clusterDim.x = a.ctas;
-    cfg.gridDim = dim3(a.ctas);
-  }
-  return cudaLaunchKernelEx(&cfg, embed_sort_kernel, a);
+  const ClusterLaunch l(1, static_cast<int>(a.ctas), kSortThreads, 0, s);
+  return cudaLaunchKernelEx(&l.cfg, embed_sort_kernel, a);
 }
 
 }  // namespace

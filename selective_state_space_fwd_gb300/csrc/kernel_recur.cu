@@ -7,8 +7,8 @@
 // consecutive steps of the tile, lane by lane, into the stretch's map; the
 // maps meet in shared memory, every thread composes those before its own with
 // the carried state, and the warp's outputs follow from the state that enters it.
-// The next tile's rows are loaded while a tile is folded.  With fewer CTAs than
-// the GPU holds, a cluster of R of them shares the time of its channels, each
+// The next tile's rows are loaded while a tile is folded.  While the
+// GPU holds more, a cluster of R of them shares the time of its channels, each
 // taking every R-th tile: the tiles' maps then go to all of the cluster's shared
 // memories, one barrier of the cluster per round.  No step is read twice, and no
 // CTA waits for one that might not run.
@@ -29,6 +29,7 @@
 //
 // A single step is bound by its launch: bf16 1024 x 2048 in 4.7 us, of which its bytes
 // take 4.3.
+#include "cluster.cuh"
 #include "f32x2.cuh"
 #include "pdl.cuh"
 #include "recur.cuh"
@@ -40,13 +41,11 @@ namespace {
 
 using recur::Cell;
 
-constexpr int kSms = 152;
 constexpr int kWarps = 8;
 constexpr int kSteps = 8;                  // per warp and tile
 constexpr int kTile = kWarps * kSteps;     // steps of a tile, and between kept states
 static_assert(kTile == kRecurChunk, "the states that the backward starts from");
 constexpr int kThreads = kWarps * 32;
-constexpr int kMaxCluster = 16;
 
 // Where a thread stands.
 template <int VEC>
@@ -530,49 +529,41 @@ bool pairs(const RecurParams& p) {
           reinterpret_cast<uintptr_t>(p.y)) % 4 == 0;
 }
 
-template <typename... P, typename... A>
-cudaError_t launch_cluster(void (*kernel)(P...), int64_t units, int size, cudaStream_t s,
-                           A... args) {
-  cudaLaunchAttribute attr = {};
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = size;
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(units * size));
-  cfg.blockDim = dim3(kThreads);
-  cfg.stream = s;
-  cfg.attrs = &attr;
-  cfg.numAttrs = size > 1 ? 1 : 0;
-  if (size > 8) {
-    const cudaError_t e =
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+// CTAs that share the time of a channel group: a power of two, doubled while all clusters
+// run at once and every CTA has a tile (fp32 1 x 65536 x 601, 19 groups, forward: 8 CTAs
+// 269 us, 16, some of them after the others, 289 us).
+template <auto KERNEL>
+int cluster_of(const RecurParams& p, int64_t units) {
+  const int64_t tiles = (p.seqlen + kTile - 1) / kTile;
+  int i = 0;
+  while (i < 4 && (int64_t(2) << i) <= tiles && units <= resident_clusters<KERNEL>(i + 1, kThreads, 0))
+    ++i;
+  return 1 << i;
+}
+
+// `lanes`: channels of a CTA; *size: the CTAs of a cluster.
+template <auto KERNEL, typename A>
+cudaError_t launch(const RecurParams& p, int lanes, const A& args, int* size, cudaStream_t s) {
+  const int64_t units = p.batch * ((p.dim + lanes - 1) / lanes);
+  *size = cluster_of<KERNEL>(p, units);
+  if (*size > kPortableCluster) {
+    const cudaError_t e = allow_large_clusters(reinterpret_cast<const void*>(KERNEL));
     if (e != cudaSuccess) return e;
   }
-  return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+  const ClusterLaunch l(units, *size, kThreads, 0, s);
+  return cudaLaunchKernelEx(&l.cfg, KERNEL, args, static_cast<uint32_t>(*size));
 }
 
 }  // namespace
 
-// CTAs that share the time of a channel group: a power of two, while the grid
-// stays within two CTAs per SM and every CTA has tiles of its own.
-static int recur_cluster(int64_t batch, int64_t seqlen, int64_t units) {
-  const int64_t tiles = (seqlen + kTile - 1) / kTile;
-  int r = 1;
-  while (r < kMaxCluster && 2 * r * units <= 2 * kSms && 2 * r <= tiles) r *= 2;
-  return r;
-}
-
-int64_t recur_bwd_partials(int64_t batch, int64_t seqlen) { return batch * kMaxCluster; }
+int64_t recur_bwd_partials(int64_t batch) { return batch * kMaxCluster; }
 
 cudaError_t launch_recur_fwd(const RecurParams& p, bool bf16, unsigned* err, cudaStream_t s) {
   if (recur_tma_ok(p, bf16)) return launch_recur_fwd_tma(p, bf16, err, s);
-  const bool two = bf16 && pairs(p);
-  const int64_t lanes = two ? 64 : 32;
-  const int64_t units = p.batch * ((p.dim + lanes - 1) / lanes);
-  const int r = recur_cluster(p.batch, p.seqlen, units);
-  if (!bf16) return launch_cluster(recur_fwd_kernel<float, 1>, units, r, s, p, r);
-  return two ? launch_cluster(recur_fwd_kernel<__nv_bfloat16, 2>, units, r, s, p, r)
-             : launch_cluster(recur_fwd_kernel<__nv_bfloat16, 1>, units, r, s, p, r);
+  int size;
+  if (!bf16) return launch<recur_fwd_kernel<float, 1>>(p, 32, p, &size, s);
+  return pairs(p) ? launch<recur_fwd_kernel<__nv_bfloat16, 2>>(p, 64, p, &size, s)
+                  : launch<recur_fwd_kernel<__nv_bfloat16, 1>>(p, 32, p, &size, s);
 }
 
 cudaError_t launch_recur_bwd(const RecurBwdParams& q, bool bf16, unsigned* err, cudaStream_t s) {
@@ -580,20 +571,18 @@ cudaError_t launch_recur_bwd(const RecurBwdParams& q, bool bf16, unsigned* err, 
   const bool two = bf16 && pairs(p) &&
                    (reinterpret_cast<uintptr_t>(q.dy) | reinterpret_cast<uintptr_t>(q.dgate) |
                     reinterpret_cast<uintptr_t>(q.dvalue)) % 4 == 0;
-  const int64_t lanes = two ? 64 : 32;
-  const int64_t units = p.batch * ((p.dim + lanes - 1) / lanes);
-  int r = recur_cluster(p.batch, p.seqlen, units);
+  int size;
   cudaError_t e;
   if (recur_bwd_tma_ok(q, bf16))
-    e = launch_recur_bwd_tma(q, bf16, err, &r, s);
+    e = launch_recur_bwd_tma(q, bf16, err, &size, s);
   else if (!bf16)
-    e = launch_cluster(recur_bwd_kernel<float, 1>, units, r, s, q, r);
+    e = launch<recur_bwd_kernel<float, 1>>(p, 32, q, &size, s);
   else
-    e = two ? launch_cluster(recur_bwd_kernel<__nv_bfloat16, 2>, units, r, s, q, r)
-            : launch_cluster(recur_bwd_kernel<__nv_bfloat16, 1>, units, r, s, q, r);
+    e = two ? launch<recur_bwd_kernel<__nv_bfloat16, 2>>(p, 64, q, &size, s)
+            : launch<recur_bwd_kernel<__nv_bfloat16, 1>>(p, 32, q, &size, s);
   if (e != cudaSuccess || !q.dfloor) return e;
   return launch_after(recur_floor_kernel, static_cast<unsigned>((p.dim + 31) / 32), 256, 0, s,
-                      q.partial, p.batch * r, p.dim, q.dfloor);
+                      q.partial, p.batch * size, p.dim, q.dfloor);
 }
 
 cudaError_t launch_recur_step(const RecurParams& p, bool bf16, cudaStream_t s) {

@@ -26,8 +26,7 @@
 // us, and with all of a round's latency in the open 92 us forward.
 #include <cuda.h>
 
-#include <atomic>
-
+#include "cluster.cuh"
 #include "f32x2.cuh"
 #include "pdl.cuh"
 #include "recur.cuh"
@@ -43,7 +42,6 @@ constexpr int kSms = 152;
 constexpr int kSteps = 16;                       // per warp and tile
 constexpr uint32_t kRow = 128;                   // bytes of a step's channels
 constexpr uint32_t kBox = kSteps * kRow;         // of a warp's rows
-constexpr int kMaxCluster = 16;
 constexpr uint64_t kWaitNs = 2000000000ull;
 
 template <typename T> struct Of;
@@ -833,50 +831,17 @@ Axes dense(const RecurParams& p) { return {true, false, p.dim, p.seqlen * p.dim}
 
 bool fits(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
-cudaLaunchConfig_t config(int64_t units, int size, int threads, uint32_t smem, cudaStream_t s,
-                          cudaLaunchAttribute* attr) {
-  *attr = {};
-  attr->id = cudaLaunchAttributeClusterDimension;
-  attr->val.clusterDim.x = size;
-  attr->val.clusterDim.y = attr->val.clusterDim.z = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(units * size));
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cfg.attrs = attr;
-  cfg.numAttrs = size > 1 ? 1 : 0;
-  return cfg;
-}
-
 int64_t units_of(const RecurParams& p, bool bf16) {
   const int64_t lanes = bf16 ? 64 : 32;
   return p.batch * ((p.dim + lanes - 1) / lanes);
-}
-
-// How many clusters of 2^i CTAs the GPU holds at once, asked for once per kernel.
-template <auto KERNEL, typename MEM, int THREADS>
-int resident(int i) {
-  static std::atomic<int> known[5];  // 0: not asked yet; the number + 1
-  int n = known[i].load(std::memory_order_relaxed);
-  if (n > 0) return n - 1;
-  const int size = 1 << i;
-  cudaLaunchAttribute attr;
-  const cudaLaunchConfig_t cfg = config(1, size, THREADS, MEM::bytes(size), nullptr, &attr);
-  if (cudaOccupancyMaxActiveClusters(&n, KERNEL, &cfg) != cudaSuccess) {
-    cudaGetLastError();
-    n = 0;
-  }
-  known[i].store(n + 1, std::memory_order_relaxed);
-  return n;
 }
 
 template <auto KERNEL, typename MEM>
 cudaError_t allow(int sizes) {
   cudaError_t e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        static_cast<int>(MEM::bytes(sizes)));
-  if (e == cudaSuccess && sizes > 8)
-    e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e == cudaSuccess && sizes > kPortableCluster)
+    e = allow_large_clusters(reinterpret_cast<const void*>(KERNEL));
   return e;
 }
 
@@ -887,7 +852,9 @@ template <auto KERNEL, typename MEM, int W, int THREADS>
 int cluster_of(const RecurParams& p, int64_t units) {
   const int64_t tiles = (p.seqlen + W * kSteps - 1) / (W * kSteps);
   int i = 0;
-  while (i < 4 && (int64_t(2) << i) <= tiles && units <= resident<KERNEL, MEM, THREADS>(i + 1)) ++i;
+  while (i < 4 && (int64_t(2) << i) <= tiles &&
+         units <= resident_clusters<KERNEL>(i + 1, THREADS, MEM::bytes(2 << i)))
+    ++i;
   return 1 << i;
 }
 
@@ -895,10 +862,8 @@ template <auto KERNEL, typename MEM, int THREADS, typename... A>
 cudaError_t go(const RecurParams& p, bool bf16, int size, cudaStream_t s, const A&... args) {
   const cudaError_t e = allow<KERNEL, MEM>(size > 1 ? kMaxCluster : 1);
   if (e != cudaSuccess) return e;
-  cudaLaunchAttribute attr;
-  const cudaLaunchConfig_t cfg =
-      config(units_of(p, bf16), size, THREADS, MEM::bytes(size), s, &attr);
-  return cudaLaunchKernelEx(&cfg, KERNEL, args...);
+  const ClusterLaunch l(units_of(p, bf16), size, THREADS, MEM::bytes(size), s);
+  return cudaLaunchKernelEx(&l.cfg, KERNEL, args...);
 }
 
 // Warps per CTA.  Forward: 8 (fp32 8 x 4096 x 1024 62 us, with 4 68 us; bf16 40 and

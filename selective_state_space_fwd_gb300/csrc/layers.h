@@ -171,7 +171,7 @@ struct RecurBwdParams {
   float* partial;         // workspace: [recur_bwd_partials, dim]
 };
 
-int64_t recur_bwd_partials(int64_t batch, int64_t seqlen);
+int64_t recur_bwd_partials(int64_t batch);
 // `err`: the sticky error word of the bounded waits.
 cudaError_t launch_recur_fwd(const RecurParams& p, bool bf16, unsigned* err, cudaStream_t s);
 cudaError_t launch_recur_bwd(const RecurBwdParams& p, bool bf16, unsigned* err, cudaStream_t s);
