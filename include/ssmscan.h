@@ -621,7 +621,8 @@ ssm_status ssm_recur_fwd(const void* gate, const void* value, const float* floor
  *   workspace: with dfloor, device memory of at least
  *             ssm_recur_bwd_workspace_bytes() bytes, 16-byte aligned, unused by
  *             other work until `stream` passes the call; NULL without.
- * Sums are taken in a fixed order: equal inputs give equal bits.
+ * Sums are taken in a fixed order: equal inputs at equal strides and alignments (which
+ * choose the kernel) give equal bits.
  */
 ssm_status ssm_recur_bwd(const void* gate, const void* value, const float* floor,
                          const int32_t* valid_len, const float* states, const void* dy,
@@ -671,9 +672,9 @@ ssm_status ssm_embed_fwd(const int64_t* ids, const void* weight, void* out_y,
 /*
  * ssm_embed_bwd -- the gradient of sum(dy * y) in the weight:
  *   dweight[v] = scale sum_{t: ids[t] = v} dy[t],
- * summed in fp32 in an order fixed by the ids (equal inputs give equal bits) and
- * rounded to dtype once.  ids of ignore_index, and ids outside [0, vocab), take no
- * part, whatever their rows of dy hold.
+ * summed in fp32 in an order fixed by the ids (equal inputs give equal bits, whatever
+ * their alignment) and rounded to dtype once.  ids of ignore_index, and ids outside
+ * [0, vocab), take no part, whatever their rows of dy hold.
  *   dy        : device, [tokens, dim], io_dtype.
  *   dweight   : device, [vocab, dim], dtype.  With `add` 0 it is written as a
  *               whole; with `add` 1 the sums are added to what it holds, and rows

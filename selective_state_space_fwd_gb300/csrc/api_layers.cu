@@ -478,7 +478,7 @@ ssm_status ssm_embed_fwd(const int64_t* ids, const void* weight, void* out_y,
 
 size_t ssm_embed_bwd_workspace_bytes(const ssm_embed_shapes* shapes) {
   if (check_embed(shapes) != SSM_OK) return 0;
-  return ssm::embed_bwd_workspace_bytes(shapes->tokens, shapes->dim);
+  return ssm::embed_bwd_workspace_bytes(shapes->tokens, shapes->dim, shapes->dtype == SSM_BF16);
 }
 
 ssm_status ssm_embed_bwd(const int64_t* ids, const void* dy, void* dweight, int add,

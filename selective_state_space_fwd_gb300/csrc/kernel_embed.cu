@@ -592,9 +592,12 @@ struct Layout {
 };
 
 // Tokens per warp: the most, up to 32, that leave 16 warps per SM (long windows
-// leave fewer partial sums).
-Layout layout_of(int64_t tokens, int64_t dim, int width) {
+// leave fewer partial sums).  They are counted by the slabs of tensors on a boundary, even
+// where a call's are not: the windows fix the order of the sums.
+Layout layout_of(int64_t tokens, int64_t dim, bool bf16) {
   Layout l;
+  const int vec = bf16 ? 8 : 4;
+  const int width = dim % vec != 0 ? Slab<1>::kWidth : bf16 ? Slab<8>::kWidth : Slab<4>::kWidth;
   const int64_t slabs = (dim + width - 1) / width;
   l.window = 8;
   while (l.window < 32 && tokens / (2 * l.window) * slabs >= 16 * kSms) l.window *= 2;
@@ -654,14 +657,8 @@ cudaError_t sort(SortArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-// The slabs' width depends on the tensors' alignment; the workspace holds for both.
-size_t embed_bwd_workspace_bytes(int64_t tokens, int64_t dim) {
-  size_t most = 0;
-  for (int width : {Slab<1>::kWidth, Slab<4>::kWidth, Slab<8>::kWidth}) {
-    const size_t n = layout_of(tokens, dim, width).total;
-    most = n > most ? n : most;
-  }
-  return most;
+size_t embed_bwd_workspace_bytes(int64_t tokens, int64_t dim, bool bf16) {
+  return layout_of(tokens, dim, bf16).total;
 }
 
 cudaError_t launch_embed_fwd(const EmbedParams& p, bool bf16, bool io_bf16, cudaStream_t s) {
@@ -679,7 +676,7 @@ cudaError_t launch_embed_bwd(const EmbedBwdParams& p, bool bf16, bool io_bf16, c
   const int most = bf16 ? 8 : 4;
   const bool wide = rows_of(p.dweight, p.dim, bf16 ? 2 : 4, most) &&
                     rows_of(p.dy, p.dim, io_bf16 ? 2 : 4, most);
-  const Layout l = layout_of(p.tokens, p.dim, !wide ? Slab<1>::kWidth : bf16 ? Slab<8>::kWidth : Slab<4>::kWidth);
+  const Layout l = layout_of(p.tokens, p.dim, bf16);
   char* ws = static_cast<char*>(p.workspace);
   SortArgs a = {};
   a.ids = p.ids;

@@ -203,7 +203,7 @@ struct EmbedBwdParams {
   void* workspace;
 };
 
-size_t embed_bwd_workspace_bytes(int64_t tokens, int64_t dim);
+size_t embed_bwd_workspace_bytes(int64_t tokens, int64_t dim, bool bf16);  // of the weight
 cudaError_t launch_embed_fwd(const EmbedParams& p, bool bf16, bool io_bf16, cudaStream_t s);
 cudaError_t launch_embed_bwd(const EmbedBwdParams& p, bool bf16, bool io_bf16, cudaStream_t s);
 
