@@ -245,6 +245,10 @@ struct Exchange {
   __device__ __forceinline__ bool wait(int i) const {
     return pair::mbar_wait(bars + 8 * (i % kBuffers), (i / kBuffers) & 1, kWaitNs);
   }
+  // The maps of the last rounds, which nothing may have waited for, have landed.
+  __device__ __forceinline__ void drain(int rounds) const {
+    for (int i = rounds > kBuffers ? rounds - kBuffers : 0; i < rounds; ++i) wait(i);
+  }
   // x through the tiles of round i; `in` is what enters this CTA's.
   template <int N>
   __device__ __forceinline__ void some(const Map<V> (*at)[32], uint32_t r, float (&x)[V],
@@ -553,8 +557,7 @@ __global__ void __launch_bounds__((W + kHelpers<T, CLUSTER>) * 32, W == 8 ? 2 : 
     // tiles and maps that were not waited for land before the CTA ends
     for (int i = rounds > kSlots ? rounds - kSlots : 0; i < rounds; ++i)
       if (tile_of(i) < live) ring.drain(i);
-    if (CLUSTER)
-      for (int i = rounds > kBuffers ? rounds - kBuffers : 0; i < rounds; ++i) cluster.wait(i);
+    if (CLUSTER) cluster.drain(rounds);
     atomicOr(a.err, kErrRecurWait);
   }
   if (CLUSTER) pair::cluster_sync();  // no map is on its way to a CTA that has ended
@@ -781,8 +784,10 @@ __global__ void __launch_bounds__(W * 32)
     }
   }
   if (bad) {
+    // as in the forward
     for (int i = rounds > kSlots ? rounds - kSlots : 0; i < rounds; ++i)
       if (tile_of(i) >= 0) ring.drain(i);
+    if (CLUSTER) cluster.drain(rounds);
     atomicOr(a.err, kErrRecurWait);
   }
   if (CLUSTER) pair::cluster_sync();  // no map is on its way to a CTA that has ended
