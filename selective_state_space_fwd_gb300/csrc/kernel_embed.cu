@@ -308,7 +308,9 @@ __global__ void __launch_bounds__(kRankWarps * 32) embed_rank_kernel(const SortA
 }
 
 // Zeros over `bytes` bytes at `begin`.  It runs beside the sort, which it does not
-// depend on, but ends after it, so that what follows has both.  (Filling only the rows
+// depend on, but ends after it, so that what follows has both.  It writes before it waits:
+// the sort (or embed_rank_kernel) is launched in plain stream order, so that all work before
+// it, which may still use those bytes, is done.  (Filling only the rows
 // without tokens, beside the sums, gained nothing: the sums' few dependent loads wait
 // behind its stores.)
 constexpr int kFillThreads = 256;
@@ -638,6 +640,7 @@ cudaError_t sum(SumArgs a, cudaStream_t s) {
   return launch_after(embed_join_kernel<W, VEC, ADD>, static_cast<unsigned>(units), kSumThreads, 0, s, a);
 }
 
+// Launched in plain stream order: embed_fill_kernel counts on it.
 // Sorts with one thread per token, but in at most kSortCtas CTAs (8 where the GPU has
 // no room for a larger cluster).
 cudaError_t sort(SortArgs& a, cudaStream_t s) {
@@ -691,6 +694,7 @@ cudaError_t launch_embed_bwd(const EmbedBwdParams& p, bool bf16, bool io_bf16, c
   if (p.tokens <= kRankMost) {
     a.passes = 1;
     const int64_t ctas = (p.tokens + kRankTokens - 1) / kRankTokens;
+    // in plain stream order too
     embed_rank_kernel<<<static_cast<unsigned>(ctas), kRankWarps * 32, 0, s>>>(a);
     e = cudaGetLastError();
   } else {

@@ -4,7 +4,8 @@
 // ended), and wait_previous() holds them until the earlier grid is complete and
 // its writes are visible.  Every kernel launched this way calls
 // wait_previous() before it touches memory, so completion stays in order along
-// a chain of such launches.
+// a chain of such launches; one that touches memory before it (embed_fill_kernel) says which
+// launch without this attribute, just before, makes that safe, and still calls it.
 #pragma once
 #include <cuda_runtime.h>
 
