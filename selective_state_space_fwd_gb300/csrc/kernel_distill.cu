@@ -255,7 +255,8 @@ cudaError_t launch_distill_fwd(const DistillParams& d, cudaStream_t s) {
     a.count = nullptr;
   else if ((e = gather(g, true, s)) != cudaSuccess)
     return e;
-  if ((e = gemm<kSoftLse>(maps, a, s)) != cudaSuccess) return e;
+  e = z.dim > kRange * kBk ? gemm<kRangeLse>(maps, a, s) : gemm<kSoftLse>(maps, a, s);
+  if (e != cudaSuccess) return e;
   return launch_after(distill_join_kernel, static_cast<unsigned>((z.tokens + 31) / 32), 1024, 0, s,
                       a, ceil_div(z.vocab, kTile), p.loss, p.lse);
 }

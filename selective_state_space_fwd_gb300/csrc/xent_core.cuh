@@ -45,11 +45,25 @@ struct Common {
 
 // Values, G and the products against one target per token (kLse, kGrad, kProducts) or
 // against a few entries with probabilities.
-enum Mode { kLse = 0, kGrad = 1, kProducts = 2, kSoftLse = 3, kSoftGrad = 4, kSoftProducts = 5 };
-constexpr bool is_lse(int mode) { return mode == kLse || mode == kSoftLse; }
+// (kRangeLse: kSoftLse with the logits summed in ranges.)
+enum Mode { kLse = 0, kGrad = 1, kProducts = 2, kSoftLse = 3, kSoftGrad = 4, kSoftProducts = 5, kRangeLse = 6 };
+constexpr bool is_lse(int mode) { return mode == kLse || mode == kSoftLse || mode == kRangeLse; }
 constexpr bool is_grad(int mode) { return mode == kGrad || mode == kSoftGrad; }
 constexpr bool is_products(int mode) { return mode == kProducts || mode == kSoftProducts; }
 constexpr bool is_soft(int mode) { return mode >= kSoftLse; }
+
+// The tensor cores cut an accumulator off, and do not round it, after every 16 products: a
+// logit of dense operands is too small by about 2^-26 of what it has grown to each time,
+// which the divergence from a teacher, a difference of two logarithms, shows.  From more
+// than kRange stages (768 products) on its values are therefore formed in ranges that are added in
+// fp32, in registers, by 8 warps instead of 4: a thread holds half of a row of the tile.
+// 4096 tokens x 50257 x 1536: loss 6.4e-7 off in 403 to 424 us, 1.4e-6 off in 372 us without;
+// ranges of 8 stages 4.0e-7 and 456 us, of 16 7.3e-7 and 422 us.  Below, ranges cost more
+// and give less (1000 x 32001 x 768, two of 6 stages: 1.8e-7 in 75 us, 3.1e-7 in 65 us without).
+constexpr int kRange = 12;
+constexpr bool in_ranges(int mode) { return mode == kRangeLse; }
+constexpr int epilogue_warps(int mode) { return in_ranges(mode) ? 2 * kEpilogueWarps : kEpilogueWarps; }
+constexpr int threads_of(int mode) { return 64 + 32 * epilogue_warps(mode); }
 
 // Against entries no part of G is nearly exact in bf16 as p - 1 at a target is.  Up to
 // kHalfTile tokens leave half of the one row of tiles empty: there G's lower half is
@@ -83,7 +97,7 @@ struct GemmArgs {
   const uint2* entries;   // soft modes: [tokens][top + kEntryPad] (id, probability), by id
   int top;
   float inv_temp;         // soft modes: the logits' factor in the softmax
-  float* entry_logit;     // kSoftLse: [tokens][top]
+  float* entry_logit;     // kSoftLse, kRangeLse: [tokens][top]
   unsigned* err;
 };
 
@@ -308,6 +322,38 @@ __device__ __forceinline__ void exponentials(float (&v)[32], float from, float i
   for (int j = 0; j < 32; ++j) v[j] = ex2(v[j]);
 }
 
+// (m, l), a maximum and a sum of exponentials of the distances to it, joined with the
+// values of 32 columns.
+__device__ __forceinline__ void join_columns(float& m, float& l, float (&v)[32], float inv_temp = 1.f) {
+  float top[4] = {v[0], v[1], v[2], v[3]};
+#pragma unroll
+  for (int j = 4; j < 32; ++j) top[j & 3] = fmaxf(top[j & 3], v[j]);
+  const float nm = fmaxf(m, fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])));
+  const float from = origin(nm);
+  exponentials(v, from, inv_temp);
+  float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int j = 0; j < 32; ++j) s[j & 3] += v[j];
+  l = fmaf(l, ex2((m - from) * (kLog2e * inv_temp)), (s[0] + s[1]) + (s[2] + s[3]));
+  m = nm;
+}
+
+// The logits of the entries in 32 columns of the vocabulary, from column `base` on.
+__device__ __forceinline__ void keep_entries(const GemmArgs& p, const float (&v)[32], uint32_t base,
+                                             Cursor& cur) {
+  for (;;) {
+    const uint32_t at = cur.now.x - base;
+    if (!__any_sync(0xffffffffu, at < 32u)) break;
+    float t = 0.f;
+#pragma unroll
+    for (uint32_t j = 0; j < 32; ++j) t = j == at ? v[j] : t;
+    if (at < 32u) {
+      p.entry_logit[cur.token * p.top + cur.e] = t;
+      cur.step();
+    }
+  }
+}
+
 // The epilogue of one thread: row `row` of the tile, whose 256 columns are the
 // TMEM columns from `acc`.
 template <bool SOFT>
@@ -329,39 +375,63 @@ __device__ __forceinline__ void epilogue_lse(const GemmArgs& p, uint32_t acc, in
 #pragma unroll
       for (int j = 0; j < 32; ++j) v[j] = c + j < cols ? v[j] : -INFINITY;
     }
-    if constexpr (SOFT) {  // the logits of the entries in these columns
-      const uint32_t base = static_cast<uint32_t>(c0 + c);
-      for (;;) {
-        const uint32_t at = cur.now.x - base;
-        if (!__any_sync(0xffffffffu, at < 32u)) break;
-        float t = 0.f;
-#pragma unroll
-        for (uint32_t j = 0; j < 32; ++j) t = j == at ? v[j] : t;
-        if (at < 32u) {
-          p.entry_logit[cur.token * p.top + cur.e] = t;
-          cur.step();
-        }
-      }
+    if constexpr (SOFT) {
+      keep_entries(p, v, static_cast<uint32_t>(c0 + c), cur);
     } else if (static_cast<unsigned>(rel - c) < 32u) {
       float t = 0.f;
 #pragma unroll
       for (int j = 0; j < 32; ++j) t = c + j == rel ? v[j] : t;
       p.target_logit[row] = t;
     }
-    float top[4] = {v[0], v[1], v[2], v[3]};
-#pragma unroll
-    for (int j = 4; j < 32; ++j) top[j & 3] = fmaxf(top[j & 3], v[j]);
-    const float nm = fmaxf(m, fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])));
-    const float from = origin(nm);
-    exponentials(v, from, SOFT ? p.inv_temp : 1.f);
-    float s[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int j = 0; j < 32; ++j) s[j & 3] += v[j];
-    l = fmaf(l, ex2((m - from) * (SOFT ? kLog2e * p.inv_temp : kLog2e)),
-             (s[0] + s[1]) + (s[2] + s[3]));
-    m = nm;
+    join_columns(m, l, v, SOFT ? p.inv_temp : 1.f);
   }
   p.part[static_cast<int64_t>(n) * p.part_pitch + row] = make_float2(m, l);
+}
+
+// Half a row of a tile, in registers.
+struct HalfRow {
+  float v[kHalfTile / 32][32];
+  __device__ __forceinline__ HalfRow() {
+#pragma unroll
+    for (int q = 0; q < kHalfTile / 32; ++q)
+#pragma unroll
+      for (int j = 0; j < 32; ++j) v[q][j] = 0.f;
+  }
+  // A range of products, in the TMEM columns from `acc` on.
+  __device__ __forceinline__ void add(uint32_t acc) {
+#pragma unroll
+    for (int q = 0; q < kHalfTile / 32; ++q) {
+      uint32_t r[32];
+      __syncwarp();
+      umma::tmem_ld32_async(acc + 32 * q, r);
+      umma::tmem_wait_ld(r);
+      float f[32];
+#pragma unroll
+      for (int j = 0; j < 32; ++j) f[j] = __uint_as_float(r[j]);
+      vadd<32>(v[q], v[q], f);
+    }
+  }
+};
+
+// The epilogue of one thread against entries: the row's maximum and sum in half tile `n` of the
+// vocabulary, whose entries `cur` meets.
+__device__ __forceinline__ float2 epilogue_entries(const GemmArgs& p, HalfRow& h, int n,
+                                                   Cursor& cur) {
+  const int c0 = n * kHalfTile, cols = p.vp - c0;
+  float m = -INFINITY, l = 0.f;
+#pragma unroll
+  for (int q = 0; q < kHalfTile / 32; ++q) {
+    float(&v)[32] = h.v[q];
+    const int c = 32 * q;
+    if (c >= cols) break;
+    if (c + 32 > cols) {  // columns past the vocabulary
+#pragma unroll
+      for (int j = 0; j < 32; ++j) v[j] = c + j < cols ? v[j] : -INFINITY;
+    }
+    keep_entries(p, v, static_cast<uint32_t>(c0 + c), cur);
+    join_columns(m, l, v, p.inv_temp);
+  }
+  return make_float2(m, l);
 }
 
 template <bool SOFT>
@@ -497,8 +567,33 @@ __device__ __forceinline__ void epilogue_products(const GemmArgs& p, const Maps&
   }
 }
 
+// (maximum, sum) pairs of a softmax's denominator joined with (m, l): the maximum
+// of all first, then the sums, each scaled to it once.  `unit` is log2(e) over the
+// softmax's temperature.
+template <int N>
+__device__ __forceinline__ void join(float& m, float& l, const float2 (&v)[N], float unit = kLog2e) {
+  float top = m;
+#pragma unroll
+  for (int i = 0; i < N; ++i) top = fmaxf(top, v[i].x);
+  const float from = origin(top);
+  l *= ex2((m - from) * unit);
+#pragma unroll
+  for (int i = 0; i < N; ++i) l = fmaf(v[i].y, ex2((v[i].x - from) * unit), l);
+  m = top;
+}
+// The pairs of a warp's lanes, joined in every lane.
+__device__ __forceinline__ void join_lanes(float& m, float& l, float unit = kLog2e) {
+  float top = m;
+#pragma unroll
+  for (int o = 16; o >= 1; o /= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  l *= ex2((m - origin(top)) * unit);
+#pragma unroll
+  for (int o = 16; o >= 1; o /= 2) l += __shfl_xor_sync(0xffffffffu, l, o);
+  m = top;
+}
+
 template <int MODE>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(MODE), 1)
     xent_gemm_kernel(const __grid_constant__ Maps maps, const GemmArgs p) {
   extern __shared__ unsigned char sm_raw[];
   const uint32_t base = (umma::smem_u32(sm_raw) + 1023u) & ~1023u;
@@ -508,6 +603,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const auto acc_full = [&](int b) { return bars + 8 * (2 * kStages + b); };
   const auto acc_empty = [&](int b) { return bars + 8 * (2 * kStages + 2 + b); };
   const uint32_t slot = bars + 8 * (2 * kStages + 4);
+  // in_ranges: the halves of the rows meet where the others have their boxes
+  float2* halves = reinterpret_cast<float2*>(sm_raw + (base - umma::smem_u32(sm_raw)) + kOut);
+  const uint32_t meets = base + kOut + 4 * kEpilogueWarps * 32 * sizeof(float2);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = pair::cluster_rank();
 
@@ -518,8 +616,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     for (int b = 0; b < 2; ++b) {
       umma::mbar_init(acc_full(b), 1);
-      umma::mbar_init(acc_empty(b), 2 * kEpilogueWarps);
+      umma::mbar_init(acc_empty(b), 2 * epilogue_warps(MODE));
     }
+    if (in_ranges(MODE))
+      for (int i = 0; i < 4 * kEpilogueWarps; ++i) umma::mbar_init(meets + 8 * i, 1);
   }
   if (warp == 1) pair::tmem_alloc(slot, 512);
   umma::fence_before_sync();
@@ -531,6 +631,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   wait_previous();
   release_next();
   const Work<MODE> work(p, blockIdx.x >> 1, gridDim.x >> 1);
+  // equal ranges, in stages
+  const int ranges = ceil_div(work.kt, kRange);
+  const int range = in_ranges(MODE) ? ceil_div(work.kt, ranges) : 0;
 
   bool bad = false;
   if (warp == 0 && lane == 0) {
@@ -588,77 +691,123 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 1 && lane == 0 && rank == 0) {
     // ---- products
-    int s = 0, n = 0;
+    int s = 0, n = 0;  // n: accumulators filled
     uint32_t ph = 0;
     Unit t;
-    for (; !bad && work.at(n, &t); ++n) {
-      const int b = n & 1;
+    for (int i = 0; !bad && work.at(i, &t); ++i) {
       const bool a_mn = t.dw, b_mn = is_products(MODE);
       const uint32_t id = umma::idesc_bf16(kTile, kTile, a_mn, b_mn);
-      if (!pair::mbar_wait(acc_empty(b), ((n >> 1) & 1) ^ 1, kWaitNs)) {
-        bad = true;
-        break;
-      }
-      umma::fence_after_sync();
-      for (int k = t.k0; k < t.k1; ++k) {
-        if (!pair::mbar_wait(full(s), ph, kWaitNs)) {
+      int k = t.k0;
+      do {  // once, or once per range
+        const int b = n & 1, from = k;
+        const int to = in_ranges(MODE) && t.k1 - k > range ? k + range : t.k1;
+        if (!pair::mbar_wait(acc_empty(b), ((n >> 1) & 1) ^ 1, kWaitNs)) {
           bad = true;
           break;
         }
         umma::fence_after_sync();
-        const uint32_t at = base + s * kStage, bt = at + kOperand;
+        for (; k < to; ++k) {
+          if (!pair::mbar_wait(full(s), ph, kWaitNs)) {
+            bad = true;
+            break;
+          }
+          umma::fence_after_sync();
+          const uint32_t at = base + s * kStage, bt = at + kOperand;
 #pragma unroll
-        for (int j = 0; j < kBk / 16; ++j)
-          pair::mma_bf16(tm + b * kTile, desc(at, j, a_mn), desc(bt, j, b_mn), id,
-                         k > t.k0 || j > 0);
-        pair::mma_commit(empty(s));
-        if (++s == kStages) { s = 0; ph ^= 1; }
-      }
-      if (!bad) pair::mma_commit(acc_full(b));
+          for (int j = 0; j < kBk / 16; ++j)
+            pair::mma_bf16(tm + b * kTile, desc(at, j, a_mn), desc(bt, j, b_mn), id,
+                           k > from || j > 0);
+          pair::mma_commit(empty(s));
+          if (++s == kStages) { s = 0; ph ^= 1; }
+        }
+        if (bad) break;
+        pair::mma_commit(acc_full(b));
+        ++n;
+      } while (k < t.k1);
     }
   } else if (warp >= 2) {
     // ---- epilogue: warp w reads TMEM lanes 32 (w mod 4) ..
     const int q = warp & 3;
     const int row = static_cast<int>(rank) * kHalfTile + q * 32 + lane;
-    OutBox out = {base + kOut + (warp - 2) * 2 * kBox, 0};
-    const float common = is_products(MODE) ? p.common->dloss * p.gain : 1.f;
-    const bool shared = is_grad(MODE) && p.common->shared;
-    Unit t;
-    for (int n = 0; !bad && work.at(n, &t); ++n) {
-      const int b = n & 1;
-      const int64_t r = static_cast<int64_t>(t.m) * kTile + row;
-      int tgt = -1;
-      float lse = 0.f, scale = 0.f;
-      if (!is_products(MODE)) tgt = target_of(p, r);
-      if (is_grad(MODE)) {
-        lse = p.lse[r];
-        scale = shared ? 1.f : p.scale[r];
-      }
-      Cursor cur = {};
-      if (is_soft(MODE))
-        cur.seek(p, r, work.rows, p.v0 + static_cast<int64_t>(t.n) * kTile);
-      if (!pair::mbar_wait(acc_full(b), (n >> 1) & 1, kWaitNs)) bad = true;
-      if (__any_sync(0xffffffffu, bad)) {
-        bad = true;
-        break;
-      }
-      umma::fence_after_sync();
-      const uint32_t acc = tm + b * kTile + (static_cast<uint32_t>(q * 32) << 16);
-      if (is_lse(MODE)) epilogue_lse<is_soft(MODE)>(p, acc, r, t.n, tgt, cur);
-      // rows of G past the last kept one are read up to a whole stage of dW's products
-      if (is_grad(MODE) && r - lane < (work.rows + kBk - 1) / kBk * kBk)
-        epilogue_grad<is_soft(MODE)>(p, maps, out, acc, r, t.n, tgt, lse, scale, r < work.rows,
-                                     is_soft(MODE) && two_halves(work.rows), cur);
-      if (is_products(MODE))
-        epilogue_products(p, maps, out, acc, t, row - lane,
-                          MODE == kSoftProducts && two_halves(work.rows) ? kHalfTile + work.rows : work.rows,
-                          work.mt, t.k1 <= t.k0, common);
+    const uint32_t lanes = static_cast<uint32_t>(q * 32) << 16;
+    // waits for the n-th accumulator; gives it back
+    const auto take = [&](int n) {
+      if (!pair::mbar_wait(acc_full(n & 1), (n >> 1) & 1, kWaitNs)) bad = true;
+      bad = __any_sync(0xffffffffu, bad);
+      if (!bad) umma::fence_after_sync();
+      return !bad;
+    };
+    const auto give = [&](int n) {
       __syncwarp();
       umma::fence_before_sync();
       __syncwarp();
-      if (lane == 0) pair::mbar_arrive(pair::map_to(acc_empty(b), 0));
+      if (lane == 0) pair::mbar_arrive(pair::map_to(acc_empty(n & 1), 0));
+    };
+    Unit t;
+    if constexpr (in_ranges(MODE)) {
+      const int half = (warp - 2) / kEpilogueWarps;
+      const auto meet = [&](int i) { return meets + 8 * (4 * q + (i & 3)); };
+      int n = 0;
+      for (int i = 0; !bad && work.at(i, &t); ++i) {
+        const int64_t r = static_cast<int64_t>(t.m) * kTile + row;
+        const int at = 2 * t.n + half;
+        Cursor cur = {};
+        HalfRow h;
+        for (int k = t.k0; k < t.k1 && take(n); k += range, ++n) {
+          h.add(tm + (n & 1) * kTile + half * kHalfTile + lanes);
+          give(n);
+          // its loads run beside the next range's products
+          if (k == t.k0) cur.seek(p, r, work.rows, p.v0 + static_cast<int64_t>(at) * kHalfTile);
+        }
+        if (bad) break;
+        const float2 own = epilogue_entries(p, h, at, cur);
+        // the second half's to the first.  It is no further ahead than the accumulators that
+        // the first half has given back: two units, so that four places are enough
+        float2* place = halves + ((i & 3) * kEpilogueWarps + q) * 32 + lane;
+        if (half == 1) {
+          *place = own;
+          __syncwarp();
+          if (lane == 0) umma::mbar_arrive(meet(i));
+        } else {
+          if (!pair::mbar_wait(meet(i), (i >> 2) & 1, kWaitNs)) bad = true;
+          bad = __any_sync(0xffffffffu, bad);
+          const float2 other[1] = {*place};
+          float m = own.x, l = own.y;
+          join(m, l, other, kLog2e * p.inv_temp);
+          if (!bad) p.part[static_cast<int64_t>(t.n) * p.part_pitch + r] = make_float2(m, l);
+        }
+      }
+    } else {
+      OutBox out = {base + kOut + (warp - 2) * 2 * kBox, 0};
+      const float common = is_products(MODE) ? p.common->dloss * p.gain : 1.f;
+      const bool shared = is_grad(MODE) && p.common->shared;
+      for (int n = 0; !bad && work.at(n, &t); ++n) {
+        const int64_t r = static_cast<int64_t>(t.m) * kTile + row;
+        int tgt = -1;
+        float lse = 0.f, scale = 0.f;
+        if (!is_products(MODE)) tgt = target_of(p, r);
+        if (is_grad(MODE)) {
+          lse = p.lse[r];
+          scale = shared ? 1.f : p.scale[r];
+        }
+        Cursor cur = {};
+        if (is_soft(MODE))
+          cur.seek(p, r, work.rows, p.v0 + static_cast<int64_t>(t.n) * kTile);
+        if (!take(n)) break;
+        const uint32_t acc = tm + (n & 1) * kTile + lanes;
+        if (is_lse(MODE)) epilogue_lse<is_soft(MODE)>(p, acc, r, t.n, tgt, cur);
+        // rows of G past the last kept one are read up to a whole stage of dW's products
+        if (is_grad(MODE) && r - lane < (work.rows + kBk - 1) / kBk * kBk)
+          epilogue_grad<is_soft(MODE)>(p, maps, out, acc, r, t.n, tgt, lse, scale, r < work.rows,
+                                       is_soft(MODE) && two_halves(work.rows), cur);
+        if (is_products(MODE))
+          epilogue_products(p, maps, out, acc, t, row - lane,
+                            MODE == kSoftProducts && two_halves(work.rows) ? kHalfTile + work.rows : work.rows,
+                            work.mt, t.k1 <= t.k0, common);
+        give(n);
+      }
+      out.drain();
     }
-    out.drain();
   }
   if (bad) atomicOr(p.err, kErrXentWait);
   __syncwarp();
@@ -667,31 +816,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   pair::cluster_sync();  // the peer's barriers and operands stay until both are done
   umma::fence_after_sync();
   if (warp == 1) pair::tmem_dealloc(tm, 512);
-}
-
-// (maximum, sum) pairs of a softmax's denominator joined with (m, l): the maximum
-// of all first, then the sums, each scaled to it once.  `unit` is log2(e) over the
-// softmax's temperature.
-template <int N>
-__device__ __forceinline__ void join(float& m, float& l, const float2 (&v)[N], float unit = kLog2e) {
-  float top = m;
-#pragma unroll
-  for (int i = 0; i < N; ++i) top = fmaxf(top, v[i].x);
-  const float from = origin(top);
-  l *= ex2((m - from) * unit);
-#pragma unroll
-  for (int i = 0; i < N; ++i) l = fmaf(v[i].y, ex2((v[i].x - from) * unit), l);
-  m = top;
-}
-// The pairs of a warp's lanes, joined in every lane.
-__device__ __forceinline__ void join_lanes(float& m, float& l, float unit = kLog2e) {
-  float top = m;
-#pragma unroll
-  for (int o = 16; o >= 1; o /= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-  l *= ex2((m - origin(top)) * unit);
-#pragma unroll
-  for (int o = 16; o >= 1; o /= 2) l += __shfl_xor_sync(0xffffffffu, l, o);
-  m = top;
 }
 
 // ---- gathering the kept tokens --------------------------------------------------
@@ -951,7 +1075,7 @@ cudaError_t gemm(const Maps& maps, const GemmArgs& a, cudaStream_t s) {
   const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              static_cast<int>(kSmem));
   if (e != cudaSuccess) return e;
-  return launch_after(k, 2 * kClusters, kThreads, kSmem, s, maps, a);
+  return launch_after(k, 2 * kClusters, threads_of(MODE), kSmem, s, maps, a);
 }
 
 cudaError_t gather(const GatherArgs& g, bool after, cudaStream_t s) {
