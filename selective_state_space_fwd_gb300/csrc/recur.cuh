@@ -67,8 +67,8 @@ __device__ __forceinline__ void half_exps(float (&g)[V], float) {
   float down[V], r[V], k[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    // where 1 / (1 + e^g) is 0, and no infinity less infinity below
-    asm("min.NaN.f32 %0, %1, %2;" : "=f"(g[v]) : "f"(g[v]), "f"(88.f));
+    // e^89 is infinite, 1 / (1 + e^g) 0; no infinity less infinity below
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(g[v]) : "f"(g[v]), "f"(89.f));
     k[v] = kLog2e;
   }
   vscale<V>(down, g, -kLog2e);  // -t

@@ -38,7 +38,8 @@ def reference(t):
     Mb = torch.cat([start.abs()[:, None], M[:, :-1]], 1)
     E = _walk(a, 28 * U * M + TINY * (Mb + v.abs() + 1), torch.zeros_like(start))
     Eb = torch.cat([torch.zeros_like(start)[:, None], E[:, :-1]], 1)
-    r = {"y": h, "y_bound": E, "final": h[:, -1], "final_bound": E[:, -1]}
+    r = {"y": h, "y_bound": E, "final": h[:, -1], "final_bound": E[:, -1],
+         "states": before[:, ::64], "states_bound": Eb[:, ::64]}
     dy, size = t["dy"].double(), t["dy"].double().abs()
     dy[:, -1] += t["dfinal"].double()
     size[:, -1] += t["dfinal"].double().abs()
@@ -83,7 +84,7 @@ def test_resets_from_large_states(dtype, B, L, D, floor):
     if floor:  # some channels without
         t["floor"] = torch.where(torch.arange(D, device="cuda") % 2 == 0, t["floor"], 0.0)
     ref, got = reference(t), run(t)
-    for name in ("y", "final", "dvalue", "dgate", "dstate0"):
+    for name in ("y", "final", "states", "dvalue", "dgate", "dstate0"):
         assert_close(got[name], ref, name)
     state = t["state0"].clone()
     y = S.recur_step(t["gate"][:, 0], t["value"][:, 0], t["floor"], state=state)
@@ -107,6 +108,23 @@ def test_an_open_gate_forgets(L, D, big, v):
         assert torch.equal(g["dvalue"], dy) and (g["dgate"] == 0).all() and (g["dstate0"] == 0).all()
     out = S.recur_step(gate[:, 0], value[:, 0], state=state)
     assert (out == value[:, 0]).all() and (state == value[:, 0]).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("L,D", [(1, 64), (20, 33), (3000, 64)])
+def test_a_closed_gate_takes_nothing(dtype, L, D):
+    """With gates of infinity, or far out, every state is the first, whatever the values."""
+    dt = DTYPES[dtype]
+    top = torch.finfo(dt).max
+    gate = torch.tensor([float("inf"), top, 1e4, 100.0], device="cuda").to(dt).repeat(D)[:D].expand(2, L, D).contiguous()
+    value = torch.full((2, L, D), -top, device="cuda", dtype=dt)
+    state = torch.linspace(-1, 1, D, device="cuda").to(dt).float().expand(2, D).contiguous()
+    y, final, states = S.recur_fwd(gate, value, state0=state, want_final=True, want_states=True)
+    assert (y.float() == state[:, None]).all() and torch.equal(final, state)
+    g = S.recur_bwd(gate, value.sign(), states=states, dy=torch.ones_like(y), want_dstate0=True)
+    assert (g["dvalue"] == 0).all() and (g["dgate"] == 0).all() and (g["dstate0"] == L).all()
+    S.recur_step(gate[:, 0], value[:, 0], state=state)
+    assert torch.equal(state, final)
 
 
 STEADY = [(11.0, 0.0), (18.0, 0.0), (6.0, 0.99), (6.0, 0.999), (9.0, 0.5), (4.0, 0.0), (0.5, 0.0), (14.0, 0.9)]
