@@ -14,9 +14,9 @@
 // that p - q keeps its digits where the student has come close.  The rest of the
 // loss is formed by the kernel that joins the tiles.
 //
-// Measured on GB300: values of 4096 tokens x 50257 x 1536, 64 entries, 377 us in a loop
-// (1.68 PFLOP/s; the cross entropy of the same sizes 367), with gradients 8192 x 65536 x
-// 2048, 32 entries, 5.15 ms (1.71 PFLOP/s), both at the power limit; 1000 tokens, half of
+// Measured on GB300: values of 4096 tokens x 50257 x 1536, 64 entries, 385 us in a graph
+// (1.64 PFLOP/s; the cross entropy of the same sizes 367), with gradients 8192 x 65536 x
+// 2048, 32 entries, 5.13 ms (1.71 PFLOP/s), both at the power limit; 1000 tokens, half of
 // them without entries, x 32001 x 768, 16 entries, 128 us: uneven last tiles and the
 // ends of nine short launches.
 #include "xent_core.cuh"

@@ -24,10 +24,10 @@
 // Tensors whose rows start on 16-byte boundaries take kernel_recur_tma.cu; the kernels
 // here read rows directly, two bf16 channels per lane where both lie on 4 bytes and one
 // otherwise.  Bound by the latency of the loads that 16 warps per SM have in flight:
-// fp32 8 x 4096 x 1025 forward 82 us (4.9 TB/s), backward 158 us (4.2 TB/s), bf16
-// 8 x 4096 x 1026 82 and 138 us; with 1024 channels staged by TMA 62 and 101, 39 and 59.
+// fp32 8 x 4096 x 1025 forward 91 us (4.4 TB/s), backward 180 us (3.7 TB/s), bf16
+// 8 x 4096 x 1026 91 and 155 us; with 1024 channels staged by TMA 63 and 103, 47 and 65.
 //
-// A single step is bound by its launch: bf16 1024 x 2048 in 4.7 us, of which its bytes
+// A single step is bound by its launch: bf16 1024 x 2048 in 4.4 us, of which its bytes
 // take 4.3.
 #include "cluster.cuh"
 #include "f32x2.cuh"

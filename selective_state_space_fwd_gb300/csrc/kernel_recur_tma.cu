@@ -16,14 +16,17 @@
 // and where a channel forgets within a stretch it leaves an error of the size of the
 // state before it.
 //
-// Measured on GB300, forward and backward: fp32 8 x 4096 x 1024 62 and 101 us (6.4 and
-// 6.6 TB/s), bf16 39 and 59 us (5.2 and 5.7), both bound by HBM; bf16 2 x 32768 x 2048
-// in clusters of 4 132 and 233 us (6.1 and 5.8); bf16 prompts 32 x 2048 x 1536 with
-// valid lengths 68 us forward (in index order of the rows 74); fp32 1 x 65536 x 256 in
-// clusters of 16, 128 CTAs in all, 49 and 107 us (4.1 and 3.1 TB/s): a round of a
-// cluster takes 1.5 us (backward 1.7), the latency of its dependent steps.
-// With the cluster's own barrier in place of the exchange these last took 106 and 219
-// us, and with all of a round's latency in the open 92 us forward.
+// Measured on GB300, forward and backward: fp32 8 x 4096 x 1024 63 and 103 us (6.4 and
+// 6.5 TB/s), bound by HBM; bf16 47 and 65 us (4.3 and 5.1) and 2 x 32768 x 2048 in clusters
+// of 4 167 and 264 us (4.8 and 5.1): 53 and 49 % of the issue slots with four and two
+// warps per scheduler, which wait for their own dependent steps; bf16 prompts 32 x 2048 x 1536
+// with valid lengths 70 us forward; fp32 1 x 65536 x 256 in clusters of 16, 128 CTAs in all,
+// 59 and 116 us (3.4 and 2.9 TB/s): a round of a cluster takes 1.8 us, the latency of its
+// dependent steps.  With h + b (v - h) for a h + b v and a product P alone, which loses a
+// small a and a long memory's digits, these took 62 and 101, 39 and 59, 132 and 233, 68, 49 and 107
+// us; the choices of shapes below were measured with that.  With the cluster's own barrier in
+// place of the exchange the last took 106 and 219 us, and with all of a round's latency in the
+// open 92 us forward.
 #include <cuda.h>
 
 #include "cluster.cuh"

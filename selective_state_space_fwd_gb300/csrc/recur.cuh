@@ -151,7 +151,7 @@ __device__ __forceinline__ int64_t valid_of(const int32_t* valid_len, int64_t b,
 
 // Rows of a batch with valid lengths go to the CTAs longest first (CTAs start in
 // index order, so that the short ones fill the end): the row of rank r among up to
-// 32, a lane per row, ties by index.  All lanes of the warp call it.
+// 32, a lane per row, ties by index; larger batches stay in index order.  All lanes of the warp call it.
 __device__ __forceinline__ int64_t by_length(const int32_t* valid_len, int64_t batch,
                                              int64_t seqlen, int64_t r) {
   const int lane = threadIdx.x & 31, n = static_cast<int>(batch);
