@@ -545,7 +545,8 @@ typedef struct {
  *   out_loss, out_lse : device fp32 [tokens].
  *   workspace : at least ssm_distill_workspace_bytes(shapes, 0) bytes, 256-byte
  *             aligned, unused by other work until `stream` passes the call.
- * Arithmetic, dtype (of h and weight) and errors as in ssm_xent_fwd.
+ * Arithmetic, dtype (of h and weight) and errors as in ssm_xent_fwd; logits of more than
+ * 768 dimensions are summed in ranges of at most 768 products, added in fp32.
  */
 ssm_status ssm_distill_fwd(const void* h, const void* weight, const int64_t* ids,
                            const void* logits, float* out_loss, float* out_lse, void* workspace,
