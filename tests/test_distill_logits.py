@@ -10,6 +10,7 @@ import pytest
 import torch
 
 import selective_state_space_fwd_gb300 as S
+from test_distill import assert_close, make, reference
 
 pytestmark = pytest.mark.gpu
 U = 2.0 ** -24
@@ -65,3 +66,33 @@ def test_long_products_are_summed_in_ranges(tokens):
     _, whole = S.xent_fwd(h, w, ids[:, 0].contiguous())
     _, lse = S.distill_fwd(h, w, ids, torch.zeros(tokens, 3, device="cuda"))
     assert (lse.double() - want).abs().mean() <= 0.6 * (whole.double() - want).abs().mean()
+
+
+SEAMS = [
+    # tokens, vocab, dim, top, and what differs: around 768 dimensions, half tiles and tiles of the vocabulary
+    (1, 1, 776, 1, {}),
+    (3, 127, 776, 127, {}),
+    (129, 128, 784, 100, dict(ragged=True)),
+    (128, 129, 768, 129, {}),
+    (257, 257, 1000, 16, dict(ignored=0.4)),
+    (40, 385, 832, 300, dict(temp=0.5)),
+    (300, 600, 2056, 64, dict(teacher=torch.bfloat16)),
+    (100, 700, 4104, 5, dict(temp=3.0)),
+    (600, 5000, 1536, 120, dict(low=True)),                  # all entries in the first tile
+    (2500, 9001, 776, 9, dict(ragged=True, ignored=0.2)),    # many tiles per cluster
+]
+
+
+@pytest.mark.parametrize("T,V,D,K,more", SEAMS)
+def test_values_around_the_seams(T, V, D, K, more):
+    t = make(T, V, D, K, seed=T + V, **more)
+    ref = reference(t)
+    a = (t["h"], t["w"], t["ids"], t["logits"])
+    loss, lse = S.distill_fwd(*a, temperature=t["temp"])
+    assert_close(loss, ref, "loss")
+    assert_close(lse, ref, "lse")
+    for fill in (0, 255):  # whatever a workspace holds
+        ws = torch.full((64 << 20,), fill, dtype=torch.uint8, device="cuda")
+        again = S.distill_fwd(*a, temperature=t["temp"], workspace=ws)
+        assert torch.equal(again[0], loss) and torch.equal(again[1], lse)
+    S.check_device_errors()
